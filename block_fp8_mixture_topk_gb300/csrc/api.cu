@@ -43,7 +43,7 @@ int device_state(DeviceState** out) {
             void* p = nullptr;
             if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess || route_init_device() != cudaSuccess ||
                 permute_init_device() != cudaSuccess || gemm_init_device() != cudaSuccess ||
-                decode_init_device() != cudaSuccess) {
+                decode_init_device() != cudaSuccess || tokens_init_device() != cudaSuccess) {
                 cudaGetLastError();
                 return MOE_ERR_CUDA;
             }
@@ -233,6 +233,10 @@ int device_status_word(uint32_t** status) {
     const int rc = device_state(&s);
     if (rc == MOE_OK) *status = s->status;
     return rc;
+}
+int device_sms() {
+    DeviceState* s = nullptr;
+    return device_state(&s) == MOE_OK ? s->num_sms : 1;
 }
 }  // namespace mfp8
 

@@ -1,0 +1,499 @@
+// Token rows sorted by expert and back, with their gradients (the training form of the "sorted
+// token" pattern and of the router-weighted gather, page "Quantization and MoE Optimizations",
+// sections Triton Fused MoE Kernel and Modular Kernel Architecture).
+//
+//   dispatch            rows[pos[t, j]] = x[t]            (stable sort of the pairs by expert)
+//   combine             out[t] = sum_j w[t, j] * y[pos[t, j]]
+//   combine, backward   dy[pos[t, j]] = w[t, j] * dout[t],  dw[t, j] = <dout[t], y[pos[t, j]]>
+//   dispatch, backward  dx[t] = sum_j drows[pos[t, j]]
+//
+// All four are bound by memory: every row is read or written once and the arithmetic is one fused
+// multiply-add per element.  Sums are fp32, in j order, rounded once to the rows' type; there are
+// no atomics on values, so results do not depend on the schedule.
+#include "train.cuh"
+
+namespace mfp8 {
+namespace {
+
+constexpr int kSortThreads = 1024;   // one thread per expert in the scan (MOE_MAX_EXPERTS)
+constexpr int64_t kDirectPairs = 16384;
+
+// Counts of one chunk's pairs per expert.
+__global__ void __launch_bounds__(kSortThreads) pair_count_kernel(const int32_t* __restrict__ ids, int64_t P,
+                                                                  int chunk, int E, int32_t* __restrict__ counts) {
+    grid_dependency_wait();
+    __shared__ int hist[MOE_MAX_EXPERTS];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * chunk;
+    const int64_t p1 = p0 + chunk < P ? p0 + chunk : P;
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += blockDim.x) {
+        const int id = ids[p];
+        if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+}
+
+struct DispatchArgs {
+    const char* x;
+    int64_t ld_bytes;
+    const int32_t* ids;
+    int64_t P;
+    int topk, E;
+    int chunk;                 // pairs per chunk (blockIdx.x), a multiple of topk
+    int nch;
+    const int32_t* counts;     // [nch][E], or null: every CTA counts the ids itself
+    int vecs, slab;            // vectors per row, vectors per column slab (blockIdx.y)
+    char* rows;
+    int32_t* expert_offsets;
+    int32_t* pair_ids;
+    int32_t* pos;
+    uint32_t* status;
+};
+
+// The sort and the copies of one chunk of tokens and one slab of columns.  Every CTA derives the
+// first row of its chunk for each expert from the pair counts (a scan over experts of the totals,
+// plus the pairs of earlier chunks), ranks its pairs with a warp match, and copies its tokens: a
+// row is read once and written topk times.  The slab-0 CTAs also write the tables.
+template <class R>
+__global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchArgs a) {
+    extern __shared__ int smem[];
+    int* before = smem;                    // [E] pairs of earlier chunks, then the next row of each expert
+    int* after = smem + a.E;               // [E] pairs of this and later chunks
+    int* pos_s = smem + 2 * a.E;           // [kSortThreads] rows of the current round's pairs
+    int16_t* warp_count = reinterpret_cast<int16_t*>(pos_s + kSortThreads);   // [32][E]
+    __shared__ int warp_sums[32];
+    __shared__ int total_s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int e = tid; e < 2 * a.E; e += kSortThreads) smem[e] = 0;
+    __syncthreads();
+    grid_dependency_wait();
+    const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+    const int64_t p1 = p0 + a.chunk < a.P ? p0 + a.chunk : a.P;
+    if (a.counts) {
+        const int G = kSortThreads / a.E;
+        const int e = tid % a.E, g = tid / a.E;
+        if (g < G) {
+            int b = 0, t = 0;
+#pragma unroll 8
+            for (int c = g; c < a.nch; c += G) {
+                const int v = a.counts[static_cast<int64_t>(c) * a.E + e];
+                if (c < static_cast<int>(blockIdx.x)) b += v;
+                else t += v;
+            }
+            atomicAdd(&before[e], b);
+            atomicAdd(&after[e], t);
+        }
+    } else {
+#pragma unroll 4
+        for (int64_t p = tid; p < a.P; p += kSortThreads) {
+            const int id = __ldg(a.ids + p);
+            if (id >= 0 && id < a.E) atomicAdd(p < p0 ? &before[id] : &after[id], 1);
+        }
+    }
+    __syncthreads();
+    const int mine = tid < a.E ? before[tid] + after[tid] : 0;
+    const int off = block_exclusive_scan(mine, warp_sums);
+    if (tid < a.E) {
+        before[tid] += off;
+        if (blockIdx.x == 0 && blockIdx.y == 0) a.expert_offsets[tid] = off;
+        if (tid == a.E - 1) {
+            total_s = off + mine;
+            if (blockIdx.x == 0 && blockIdx.y == 0) a.expert_offsets[a.E] = off + mine;
+        }
+    }
+    __syncthreads();
+    const int64_t total = total_s;
+    const int v0 = blockIdx.y * a.slab;
+    const int nv = a.vecs - v0 < a.slab ? a.vecs - v0 : a.slab;
+    const bool tables = blockIdx.y == 0;
+    const int round = kSortThreads / a.topk * a.topk;
+    R* rows = reinterpret_cast<R*>(a.rows);
+    for (int64_t r0 = p0; r0 < p1; r0 += round) {
+        for (int i = tid; i < 32 * a.E / 2; i += kSortThreads) reinterpret_cast<int*>(warp_count)[i] = 0;
+        __syncthreads();
+        const int n = static_cast<int>(p1 - r0 < round ? p1 - r0 : round);
+        int id = -1;
+        if (tid < n) {
+            id = a.ids[r0 + tid];
+            if (id >= a.E) {
+                if (tables) status_set(a.status, MOE_STATUS_BAD_EXPERT_ID);
+                id = -1;
+            }
+            if (id < 0) id = -1;
+        }
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        if (id >= 0 && rank == 0) warp_count[warp * a.E + id] = static_cast<int16_t>(__popc(same));
+        __syncthreads();
+        int at = -1;
+        if (id >= 0) {
+            int b = before[id];
+            for (int w = 0; w < warp; ++w) b += warp_count[w * a.E + id];
+            at = b + rank;
+        }
+        pos_s[tid] = at;
+        if (tables && tid < n) {
+            a.pos[r0 + tid] = at;
+            if (at >= 0) a.pair_ids[at] = static_cast<int32_t>(r0 + tid);
+        }
+        __syncthreads();
+        if (tid < a.E) {
+            int c = 0;
+#pragma unroll 8
+            for (int w = 0; w < 32; ++w) c += warp_count[w * a.E + tid];
+            before[tid] += c;
+        }
+        const int tokens = n / a.topk;
+        const int64_t t0 = r0 / a.topk;
+        const int items = tokens * nv;
+        constexpr int U = 4;
+        for (int i = tid; i < items; i += U * kSortThreads) {
+            R val[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = i + u * kSortThreads;
+                if (k < items)
+                    val[u] = __ldg(reinterpret_cast<const R*>(a.x + (t0 + k / nv) * a.ld_bytes) + v0 + k % nv);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = i + u * kSortThreads;
+                if (k >= items) break;
+                const int t = k / nv, v = v0 + k % nv;
+                for (int j = 0; j < a.topk; ++j) {
+                    const int r = pos_s[t * a.topk + j];
+                    if (r >= 0) rows[static_cast<int64_t>(r) * a.vecs + v] = val[u];
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // rows of no pair (as many as there are pairs without an expert): zero, at the end
+    const int64_t left = (a.P - total) * nv;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < left;
+         i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+        rows[(total + i / nv) * a.vecs + v0 + i % nv] = R{};
+    if (tables)
+        for (int64_t r = total + static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; r < a.P;
+             r += static_cast<int64_t>(gridDim.x) * kSortThreads)
+            a.pair_ids[r] = -1;
+}
+
+// out[t] = sum_j w[t, j] * y[pos[t, j]] (w null: 1), one thread per vector of V elements.
+template <class T, int V>
+__global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y, int64_t ld,
+                                                      const int32_t* __restrict__ pos,
+                                                      const float* __restrict__ w, int64_t n_tokens, int topk,
+                                                      int vecs, int64_t num_rows, T* __restrict__ out,
+                                                      uint32_t* status) {
+    grid_dependency_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= n_tokens * vecs) return;
+    const int64_t t = i / vecs;
+    const int v = static_cast<int>(i - t * vecs);
+    const int32_t* tp = pos + t * topk;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+    constexpr int U = 8;
+    for (int j0 = 0; j0 < topk; j0 += U) {
+        Pack<T, V> val[U];
+        float wj[U];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int64_t r = j0 + u < topk ? tp[j0 + u] : -1;
+            if (r >= num_rows) {
+                if (v == 0) status_set(status, MOE_STATUS_BAD_EXPERT_ID);
+                r = -1;
+            }
+            live[u] = r >= 0;
+            if (live[u]) {
+                val[u].load(y + r * ld + static_cast<int64_t>(v) * V);
+                wj[u] = w ? w[t * topk + j0 + u] : 1.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!live[u]) continue;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(wj[u], val[u].get(e), acc[e]);
+        }
+    }
+    Pack<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.set(e, acc[e]);
+    o.store(out + (t * vecs + v) * V);
+}
+
+// One warp per pair: dy[pos] = w * dout[t] and dw = <dout[t], y[pos]>.  The pairs of one token are
+// neighbouring warps, so that dout comes from DRAM once.  The warps past the pairs zero the rows
+// that belong to no pair, 32 rows each.
+template <class T, int V>
+__global__ void __launch_bounds__(256)
+    combine_backward_kernel(const T* __restrict__ dout, int64_t ldo, const T* __restrict__ y, int64_t ldy,
+                            const int32_t* __restrict__ pos, const int32_t* __restrict__ pair_ids,
+                            const float* __restrict__ w, int64_t P, int topk, int vecs, int64_t num_rows,
+                            T* __restrict__ dy, float* __restrict__ dw, uint32_t* status) {
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t p = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    if (p >= P) {
+        const int64_t r0 = (p - P) * 32;
+        if (r0 >= num_rows) return;
+        uint32_t empty = __ballot_sync(0xffffffffu, r0 + lane < num_rows && pair_ids[r0 + lane] < 0);
+        Pack<T, V> z;
+        z.zero();
+        while (empty) {
+            const int64_t r = r0 + __ffs(empty) - 1;
+            empty &= empty - 1;
+            for (int v = lane; v < vecs; v += 32) z.store(dy + (r * vecs + v) * V);
+        }
+        return;
+    }
+    const int64_t r = pos[p];
+    if (r < 0 || r >= num_rows) {
+        if (lane == 0) {
+            dw[p] = 0.0f;
+            if (r >= num_rows) status_set(status, MOE_STATUS_BAD_EXPERT_ID);
+        }
+        return;
+    }
+    const float wp = w ? w[p] : 1.0f;
+    const T* o = dout + p / topk * ldo;
+    const T* yr = y + r * ldy;
+    T* dr = dy + r * vecs * V;
+    float dot = 0.0f;
+    constexpr int U = 4;
+    for (int v0 = lane; v0 < vecs; v0 += 32 * U) {
+        Pack<T, V> a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * 32;
+            if (v < vecs) {
+                a[u].load(o + static_cast<int64_t>(v) * V);
+                b[u].load(yr + static_cast<int64_t>(v) * V);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * 32;
+            if (v >= vecs) break;
+            Pack<T, V> d;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float g = a[u].get(e);
+                dot = fmaf(g, b[u].get(e), dot);
+                d.set(e, wp * g);
+            }
+            d.store(dr + static_cast<int64_t>(v) * V);
+        }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+    if (lane == 0) dw[p] = dot;
+}
+
+// Widest vector, in bytes, that divides the row, the row strides and the addresses.
+int vector_bytes(int64_t row_bytes, uintptr_t bits, int element) {
+    const uintptr_t all = bits | static_cast<uintptr_t>(row_bytes);
+    for (int b = 16; b > element; b >>= 1)
+        if (all % b == 0) return b;
+    return element;
+}
+
+struct DispatchPlan {
+    int chunk, nch;
+    bool direct;
+};
+// Chunks of whole tokens, about one per SM, so that every SM copies; few pairs: no counting launch.
+DispatchPlan dispatch_plan(int64_t P, int topk) {
+    DispatchPlan d;
+    const int64_t T = P / topk;
+    const int64_t per = (T + kPlanSms - 1) / kPlanSms;
+    d.chunk = static_cast<int>(per * topk);
+    d.nch = static_cast<int>((P + d.chunk - 1) / d.chunk);
+    d.direct = P <= kDirectPairs;
+    return d;
+}
+
+size_t dispatch_smem(int E) { return (2 * E + kSortThreads) * 4 + 32 * static_cast<size_t>(E) * 2 + 4; }
+
+template <class R>
+cudaError_t launch_dispatch(const DispatchArgs& a, dim3 grid, cudaStream_t stream) {
+    return launch_pdl(dispatch_kernel<R>, grid, dim3(kSortThreads), dispatch_smem(a.E), stream, a);
+}
+
+template <class T, int V>
+cudaError_t launch_combine(const void* y, int64_t ld, const int32_t* pos, const float* w, int64_t T_, int topk, int H,
+                           int64_t num_rows, void* out, uint32_t* status, cudaStream_t stream) {
+    const int64_t n = T_ * (H / V);
+    return launch_pdl(combine_kernel<T, V>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
+                      static_cast<const T*>(y), ld, pos, w, T_, topk, H / V, num_rows, static_cast<T*>(out), status);
+}
+
+template <class T, int V>
+cudaError_t launch_combine_backward(const void* dout, int64_t ldo, const void* y, int64_t ldy, const int32_t* pos,
+                                    const int32_t* pair_ids, const float* w, int64_t P, int topk, int H,
+                                    int64_t num_rows, void* dy, float* dw, uint32_t* status, cudaStream_t stream) {
+    const int64_t warps = P + (num_rows + 31) / 32;
+    return launch_pdl(combine_backward_kernel<T, V>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
+                      stream, static_cast<const T*>(dout), ldo, static_cast<const T*>(y), ldy, pos, pair_ids, w, P,
+                      topk, H / V, num_rows, static_cast<T*>(dy), dw, status);
+}
+
+// F<T, V> for the type and the vector width
+#define MOE_BY_TYPE(F, dtype, vb, ...)                                             \
+    ((dtype) == MOE_DTYPE_FP32   ? ((vb) == 16  ? F<float, 4>(__VA_ARGS__)         \
+                                    : (vb) == 8 ? F<float, 2>(__VA_ARGS__)         \
+                                                : F<float, 1>(__VA_ARGS__))        \
+     : (dtype) == MOE_DTYPE_FP16 ? ((vb) == 16  ? F<__half, 8>(__VA_ARGS__)        \
+                                    : (vb) == 8 ? F<__half, 4>(__VA_ARGS__)        \
+                                    : (vb) == 4 ? F<__half, 2>(__VA_ARGS__)        \
+                                                : F<__half, 1>(__VA_ARGS__))       \
+                                 : ((vb) == 16  ? F<__nv_bfloat16, 8>(__VA_ARGS__) \
+                                    : (vb) == 8 ? F<__nv_bfloat16, 4>(__VA_ARGS__) \
+                                    : (vb) == 4 ? F<__nv_bfloat16, 2>(__VA_ARGS__) \
+                                                : F<__nv_bfloat16, 1>(__VA_ARGS__)))
+
+int check_rows(int T, int topk, int H, int64_t ld, int64_t num_rows, int dtype) {
+    if (T < 0 || topk < 1 || H < 1 || ld < H || num_rows < 0 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    if (topk > MOE_MAX_TOPK || H > MOE_MAX_HIDDEN || static_cast<int64_t>(T) * topk >= (int64_t(1) << 31) ||
+        num_rows >= (int64_t(1) << 31) || static_cast<int64_t>(T) * H / 256 >= (int64_t(1) << 31))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+
+cudaError_t tokens_init_device() {
+    const int bytes = static_cast<int>(dispatch_smem(MOE_MAX_EXPERTS));
+    cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<uint4>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dispatch_kernel<uint2>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dispatch_kernel<uint32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dispatch_kernel<uint16_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e;
+}
+
+}  // namespace mfp8
+
+using namespace mfp8;
+
+extern "C" {
+
+size_t moe_dispatch_workspace_size(int T, int topk, int E) {
+    if (T < 0 || topk < 1 || E < 1) return 0;
+    const int64_t P = static_cast<int64_t>(T) * topk;
+    if (P == 0) return 0;
+    const DispatchPlan d = dispatch_plan(P, topk);
+    return d.direct ? 0 : static_cast<size_t>(d.nch) * E * 4;
+}
+
+int moe_dispatch(const void* x, int64_t ldx, int dtype, const int32_t* topk_ids, int T, int topk, int E, int H,
+                 void* rows, int32_t* expert_offsets, int32_t* pair_ids, int32_t* pos, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+    int rc = check_rows(T, topk, H, ldx, 0, dtype);
+    if (rc != MOE_OK) return rc;
+    if (E < 1) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int64_t P = static_cast<int64_t>(T) * topk;
+    if (!expert_offsets || (P > 0 && (!x || !topk_ids || !rows || !pair_ids || !pos))) return MOE_ERR_INVALID_ARG;
+    if (!on_element(address(x) | address(rows), dtype_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    const size_t need = moe_dispatch_workspace_size(T, topk, E);
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (need > 0 && !workspace) return MOE_ERR_INVALID_ARG;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (P == 0) return cuda_status(cudaMemsetAsync(expert_offsets, 0, (static_cast<size_t>(E) + 1) * 4, s));
+    const DispatchPlan d = dispatch_plan(P, topk);
+    const int es = static_cast<int>(dtype_bytes(dtype));
+    const int64_t row_bytes = static_cast<int64_t>(H) * es;
+    const int vb = vector_bytes(row_bytes, address(x) | address(rows) | static_cast<uintptr_t>(ldx * es), es);
+    DispatchArgs a;
+    a.x = static_cast<const char*>(x);
+    a.ld_bytes = ldx * es;
+    a.ids = topk_ids;
+    a.P = P;
+    a.topk = topk;
+    a.E = E;
+    a.chunk = d.chunk;
+    a.nch = d.nch;
+    a.counts = d.direct ? nullptr : static_cast<const int32_t*>(workspace);
+    a.vecs = static_cast<int>(row_bytes / vb);
+    // few tokens: several CTAs share a chunk, each with a slab of at least 128 vectors of the columns
+    int slabs = kPlanSms / d.nch;
+    if (slabs > (a.vecs + 127) / 128) slabs = (a.vecs + 127) / 128;
+    if (slabs < 1) slabs = 1;
+    a.slab = (a.vecs + slabs - 1) / slabs;
+    slabs = (a.vecs + a.slab - 1) / a.slab;
+    a.rows = static_cast<char*>(rows);
+    a.expert_offsets = expert_offsets;
+    a.pair_ids = pair_ids;
+    a.pos = pos;
+    a.status = status;
+    cudaError_t e = cudaSuccess;
+    if (!d.direct)
+        e = launch_pdl(pair_count_kernel, dim3(static_cast<unsigned>(d.nch)), dim3(kSortThreads), 0, s, topk_ids, P,
+                       d.chunk, E, static_cast<int32_t*>(workspace));
+    const dim3 grid(static_cast<unsigned>(d.nch), static_cast<unsigned>(slabs));
+    if (e == cudaSuccess) {
+        switch (vb) {
+            case 16: e = launch_dispatch<uint4>(a, grid, s); break;
+            case 8: e = launch_dispatch<uint2>(a, grid, s); break;
+            case 4: e = launch_dispatch<uint32_t>(a, grid, s); break;
+            default: e = launch_dispatch<uint16_t>(a, grid, s); break;
+        }
+    }
+    return cuda_status(e);
+}
+
+int moe_combine(const void* y, int64_t ldy, int dtype, const int32_t* pos, const float* weights, int T, int topk,
+                int H, int64_t num_rows, void* out, void* stream) {
+    int rc = check_rows(T, topk, H, ldy, num_rows, dtype);
+    if (rc != MOE_OK) return rc;
+    if (T == 0) return MOE_OK;
+    if (!pos || !out || (num_rows > 0 && !y)) return MOE_ERR_INVALID_ARG;
+    if (!on_element(address(y) | address(out), dtype_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
+    const int es = static_cast<int>(dtype_bytes(dtype));
+    const int vb = vector_bytes(static_cast<int64_t>(H) * es,
+                                address(y) | address(out) | static_cast<uintptr_t>(ldy * es), es);
+    return cuda_status(MOE_BY_TYPE(launch_combine, dtype, vb, y, ldy, pos, weights, T, topk, H, num_rows, out, status,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+int moe_dispatch_backward(const void* drows, int64_t lddrows, int dtype, const int32_t* pos, int T, int topk, int H,
+                          int64_t num_rows, void* dx, void* stream) {
+    return moe_combine(drows, lddrows, dtype, pos, nullptr, T, topk, H, num_rows, dx, stream);
+}
+
+int moe_combine_backward(const void* dout, int64_t lddout, const void* y, int64_t ldy, int dtype, const int32_t* pos,
+                         const int32_t* pair_ids, const float* weights, int T, int topk, int H, int64_t num_rows,
+                         void* dy, float* dweights, void* stream) {
+    int rc = check_rows(T, topk, H, ldy, num_rows, dtype);
+    if (rc != MOE_OK) return rc;
+    if (lddout < H) return MOE_ERR_INVALID_ARG;
+    const int64_t P = static_cast<int64_t>(T) * topk;
+    if (P == 0 && num_rows == 0) return MOE_OK;
+    if (P > 0 && (!dout || !pos || !dweights)) return MOE_ERR_INVALID_ARG;
+    if (num_rows > 0 && (!y || !dy || !pair_ids)) return MOE_ERR_INVALID_ARG;
+    if (!on_element(address(dout) | address(y) | address(dy), dtype_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
+    const int es = static_cast<int>(dtype_bytes(dtype));
+    const int vb = vector_bytes(static_cast<int64_t>(H) * es,
+                                address(dout) | address(y) | address(dy) | static_cast<uintptr_t>(lddout * es) |
+                                    static_cast<uintptr_t>(ldy * es),
+                                es);
+    return cuda_status(MOE_BY_TYPE(launch_combine_backward, dtype, vb, dout, lddout, y, ldy, pos, pair_ids, weights, P,
+                                   topk, H, num_rows, dy, dweights, status, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -123,6 +123,11 @@ def lib():
                 "moe_fp8_block_forward_masked": ([P, P, P, P, P, P, I, I, I, I, P, P, SZ, P, P], I),
                 "moe_unpermute_sum": ([P, I64, P, I, I, I, P, P], I),
                 "moe_combine_pairs": ([P, P, I, I, I, P, P], I),
+                "moe_dispatch_workspace_size": ([I, I, I], SZ),
+                "moe_dispatch": ([P, I64, I, P, I, I, I, I, P, P, P, P, P, SZ, P], I),
+                "moe_dispatch_backward": ([P, I64, I, P, I, I, I, I64, P, P], I),
+                "moe_combine": ([P, I64, I, P, P, I, I, I, I64, P, P], I),
+                "moe_combine_backward": ([P, I64, P, I64, I, P, P, P, I, I, I, I64, P, P, P], I),
                 "moe_get_device_status": ([P, I], I),
                 "moe_selftest_bounded_wait": ([I, P], I),
                 "moe_error_string": ([I], ctypes.c_char_p),
@@ -519,6 +524,129 @@ def moe_fp8_block_forward_masked(hidden, counts, w13, w13_scale, w2, w2_scale, o
                                             _ptr(out), _stream())
     _check("moe_fp8_block_forward_masked", rc)
     return out
+
+
+# ---- training operators (C ABI section "training") ------------------------------------------
+
+DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _typed(t, name, like=None):
+    """Code of t's element type; with `like`, t must have that tensor's type."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    code = DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _rows(t, name, like=None, shape=None):
+    """A matrix whose columns are adjacent: (type code, row stride)."""
+    code = _typed(t, name, like)
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {list(shape) if shape is not None else 'a matrix'}, got {list(t.shape)}")
+    n, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name} must have adjacent columns")
+    if n <= 1:
+        return code, cols
+    if s0 < cols:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return code, s0
+
+
+def _dense(t, name, dtype, shape):
+    _cuda(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+@dataclasses.dataclass
+class Dispatch:
+    """Token rows sorted by expert (moe_dispatch)."""
+    rows: torch.Tensor             # [T*topk, H]; rows of no pair are zero
+    expert_offsets: torch.Tensor   # int32 [E+1]
+    pair_ids: torch.Tensor         # int32 [T*topk], -1 for a row of no pair
+    pos: torch.Tensor              # int32 [T, topk], -1 for a dropped pair
+
+
+def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
+    """Rows of x [T, H] (bf16, fp16 or fp32) sorted by expert: rows[pos[t, j]] = x[t], the pairs of an
+    expert in ascending order, nothing padded.  topk_ids int32 [T, topk]; a negative id drops its pair."""
+    code, ld = _rows(x, "x")
+    _cuda(topk_ids, torch.int32, "topk_ids")
+    T, H = x.shape
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must be [{T}, topk], got {list(topk_ids.shape)}")
+    k = topk_ids.shape[1]
+    P = T * k
+    L = lib()
+    wsb = L.moe_dispatch_workspace_size(T, k, num_experts)
+    # one buffer: the tables, then the scratch
+    n = num_experts + 1
+    tables = torch.empty(max(n, 1) + 2 * P + (wsb + 3) // 4, dtype=torch.int32, device=x.device)
+    offsets, pair_ids, pos = tables[:n], tables[n:n + P], tables[n + P:n + 2 * P].view(T, k)
+    rows = torch.empty(P, H, dtype=x.dtype, device=x.device)
+    base = tables.data_ptr()
+    rc = L.moe_dispatch(x.data_ptr(), ld, code, topk_ids.data_ptr(), T, k, num_experts, H, rows.data_ptr(), base,
+                        base + 4 * n, base + 4 * (n + P), base + 4 * (n + 2 * P), wsb, _stream())
+    _check("moe_dispatch", rc)
+    return Dispatch(rows, offsets, pair_ids, pos)
+
+
+def _pos(pos):
+    _cuda(pos, torch.int32, "pos")
+    if pos.dim() != 2:
+        raise ValueError(f"pos must be [T, topk], got {list(pos.shape)}")
+    return pos.shape
+
+
+def moe_dispatch_backward(drows, pos):
+    """Gradient of x: dx[t] = sum_j drows[pos[t, j]], [T, H] in drows' type."""
+    code, ld = _rows(drows, "drows")
+    T, k = _pos(pos)
+    n, H = drows.shape
+    dx = torch.empty(T, H, dtype=drows.dtype, device=drows.device)
+    _check("moe_dispatch_backward", lib().moe_dispatch_backward(drows.data_ptr(), ld, code, pos.data_ptr(), T, k, H, n,
+                                                                dx.data_ptr(), _stream()))
+    return dx
+
+
+def moe_combine(y, pos, weights=None):
+    """The experts' rows back to their tokens: out[t] = sum_j weights[t, j] * y[pos[t, j]] over the
+    pairs with a row (weights fp32 [T, topk]; None: 1), [T, H] in y's type."""
+    code, ld = _rows(y, "y")
+    T, k = _pos(pos)
+    if weights is not None:
+        _dense(weights, "weights", torch.float32, (T, k))
+    n, H = y.shape
+    out = torch.empty(T, H, dtype=y.dtype, device=y.device)
+    _check("moe_combine", lib().moe_combine(y.data_ptr(), ld, code, pos.data_ptr(),
+                                            None if weights is None else weights.data_ptr(), T, k, H, n,
+                                            out.data_ptr(), _stream()))
+    return out
+
+
+def moe_combine_backward(dout, y, pos, pair_ids, weights=None):
+    """Gradients of moe_combine: (dy [rows, H] in y's type, zero in rows of no pair; dweights fp32 [T, topk])."""
+    code, ldy = _rows(y, "y")
+    T, k = _pos(pos)
+    n, H = y.shape
+    _, ldo = _rows(dout, "dout", y, (T, H))
+    _dense(pair_ids, "pair_ids", torch.int32, (n,))
+    if weights is not None:
+        _dense(weights, "weights", torch.float32, (T, k))
+    dy = torch.empty(n, H, dtype=y.dtype, device=y.device)
+    dw = torch.empty(T, k, dtype=torch.float32, device=y.device)
+    rc = lib().moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, pos.data_ptr(), pair_ids.data_ptr(),
+                                    None if weights is None else weights.data_ptr(), T, k, H, n, dy.data_ptr(),
+                                    dw.data_ptr(), _stream())
+    _check("moe_combine_backward", rc)
+    return dy, dw
 
 
 def moe_selftest_bounded_wait(expire=True):

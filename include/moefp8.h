@@ -494,6 +494,51 @@ int moe_fp8_block_forward_masked(const uint16_t* hidden, const int32_t* counts,
                                  int E, int max_tokens, int H, int I, const moe_forward_options* opts,
                                  void* workspace, size_t workspace_bytes, uint16_t* out, void* stream);
 
+/* ---- training: the operators around and inside the experts, in 16 or 32 bits -------------
+ * What a training step of the layer (or a 16-bit forward pass) needs next to the FP8 layer,
+ * each with its gradient.  The pages describe the sorted-token pattern, the gather and the
+ * weights' layout for inference (page "Quantization and MoE Optimizations", sections Triton Fused
+ * MoE Kernel, Modular Kernel Architecture and FusedMoE Class); the gradients are those of these
+ * formulas.
+ *
+ * Common to them: element types are MOE_DTYPE_*; matrices are row-major with the row stride in
+ * elements where a `ld` argument follows the pointer, dense otherwise; addresses need the
+ * alignment of one element (16 bytes for the products), and rows whose addresses and strides are
+ * multiples of 16 bytes run fastest; sums are held in fp32 or more and rounded once; outputs may not
+ * overlap inputs unless said; no result depends on the schedule (no atomics on values). */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP16 1
+#define MOE_DTYPE_FP32 2
+
+/* Token rows sorted by expert.  Pair p = t*topk + j goes to expert topk_ids[p]; a negative id drops the
+ * pair, an id >= E drops it and sets MOE_STATUS_BAD_EXPERT_ID.  The pairs of an expert are in
+ * ascending p and nothing is padded:
+ *   expert_offsets int32 [E+1]      expert e owns rows [expert_offsets[e], expert_offsets[e+1])
+ *   pair_ids       int32 [T*topk]   pair of each row, -1 past the last row of an expert
+ *   pos            int32 [T, topk]  row of each pair, -1 for a dropped pair
+ *   rows           [T*topk, H]      rows[pos[t, j]] = x[t]; rows of no pair are zero
+ * workspace: device scratch of moe_dispatch_workspace_size(T, topk, E) bytes (4-byte aligned).
+ * H <= MOE_MAX_HIDDEN. */
+#define MOE_MAX_HIDDEN 65536
+size_t moe_dispatch_workspace_size(int T, int topk, int E);
+int moe_dispatch(const void* x, int64_t ldx, int dtype, const int32_t* topk_ids, int T, int topk, int E, int H,
+                 void* rows, int32_t* expert_offsets, int32_t* pair_ids, int32_t* pos, void* workspace,
+                 size_t workspace_bytes, void* stream);
+/* Its gradient: dx[t] = sum_j drows[pos[t, j]] over the pairs with a row, in j order. */
+int moe_dispatch_backward(const void* drows, int64_t lddrows, int dtype, const int32_t* pos, int T, int topk, int H,
+                          int64_t num_rows, void* dx, void* stream);
+/* The experts' rows back to their tokens: out[t] = sum_j weights[t, j] * y[pos[t, j]] over the pairs
+ * with a row, in j order, fp32, rounded once (weights fp32 [T, topk], NULL = 1; a token without
+ * rows gets zeros; a pos >= num_rows is skipped and sets MOE_STATUS_BAD_EXPERT_ID). */
+int moe_combine(const void* y, int64_t ldy, int dtype, const int32_t* pos, const float* weights, int T, int topk,
+                int H, int64_t num_rows, void* out, void* stream);
+/* Its gradients: dy[pos[t, j]] = weights[t, j] * dout[t] (rows of no pair, pair_ids < 0: zero) and
+ * dweights[t, j] = <dout[t], y[pos[t, j]]> (fp32; 0 for a dropped pair).  dy [num_rows, H];
+ * pair_ids [num_rows]. */
+int moe_combine_backward(const void* dout, int64_t lddout, const void* y, int64_t ldy, int dtype, const int32_t* pos,
+                         const int32_t* pair_ids, const float* weights, int T, int topk, int H, int64_t num_rows,
+                         void* dy, float* dweights, void* stream);
+
 /* ---- status -------------------------------------------------------------------- */
 /* Reads (and with clear != 0, resets) the device status word of the current
  * device into *status (host).  Synchronises the device. */
