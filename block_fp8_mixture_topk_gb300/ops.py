@@ -90,6 +90,7 @@ def lib():
                 _build.build()
             L = ctypes.CDLL(_build.LIB_PATH)
             P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+            F = ctypes.c_float
             sig = {
                 "moe_route_topk": ([P, I, I, I, I, P, P, P, P], I),
                 "moe_max_padded_rows": ([I, I, I, I], I64),
@@ -128,6 +129,11 @@ def lib():
                 "moe_dispatch_backward": ([P, I64, I, P, I, I, I, I64, P, P], I),
                 "moe_combine": ([P, I64, I, P, P, I, I, I, I64, P, P], I),
                 "moe_combine_backward": ([P, I64, P, I64, I, P, P, P, I, I, I, I64, P, P, P], I),
+                "moe_pre_norm": ([P, I64, I, P, I, F, F, I, I, P, P, P], I),
+                "moe_norm_backward_workspace_size": ([I, I], SZ),
+                "moe_pre_norm_backward": ([P, I64, P, I64, I, P, I, F, P, P, I64, I, I, P, P, P, SZ, P], I),
+                "moe_post_norm": ([P, I64, P, I64, I, P, I, I, P, P, P, P, P], I),
+                "moe_post_norm_backward": ([P, I64, P, I64, I, P, P, I, I, P, P, P, P, P, SZ, P], I),
                 "moe_get_device_status": ([P, I], I),
                 "moe_selftest_bounded_wait": ([I, P], I),
                 "moe_error_string": ([I], ctypes.c_char_p),
@@ -647,6 +653,159 @@ def moe_combine_backward(dout, y, pos, pair_ids, weights=None):
                                     dw.data_ptr(), _stream())
     _check("moe_combine_backward", rc)
     return dy, dw
+
+
+GATE_KIND = {"none": 0, "token": 1, "channel": 2, "full": 3}
+
+
+class _PostNormParams(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("next_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("weight_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("gate_sigmoid", ctypes.c_int32), ("weight_offset", ctypes.c_float), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float)]
+
+
+def _norm_weight(w, H, name):
+    code = _typed(w, name)
+    if w.dim() != 1 or w.shape[0] != H or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{H}], got {list(w.shape)}")
+    return code
+
+
+def moe_pre_norm(x, weight, eps=1e-6, weight_offset=0.0):
+    """RMS norm before a block: h = x * rstd * (weight + weight_offset).  Returns (h in x's type,
+    rstd fp32 [T])."""
+    code, ld = _rows(x, "x")
+    T, H = x.shape
+    wcode = _norm_weight(weight, H, "weight")
+    h = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check("moe_pre_norm", lib().moe_pre_norm(x.data_ptr(), ld, code, weight.data_ptr(), wcode, weight_offset, eps, T,
+                                              H, h.data_ptr(), rstd.data_ptr(), _stream()))
+    return h, rstd
+
+
+def _norm_sums(T, H, device, vectors=1):
+    """`vectors` fp32 [H] outputs and the scratch of a norm's gradient behind them, in one allocation:
+    the outputs and the scratch's address and size."""
+    wsb = lib().moe_norm_backward_workspace_size(T, H)
+    buf = torch.empty(vectors * H + wsb // 4, dtype=torch.float32, device=device)
+    out = tuple(buf[i * H:(i + 1) * H] for i in range(vectors))
+    return (*out, buf.data_ptr() + 4 * vectors * H, wsb)
+
+
+def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0):
+    """Gradients of moe_pre_norm: (dx in x's type, dresidual included; dweight fp32 [H])."""
+    code, ldx = _rows(x, "x")
+    T, H = x.shape
+    _, ldd = _rows(dh, "dh", x, (T, H))
+    wcode = _norm_weight(weight, H, "weight")
+    _dense(rstd, "rstd", torch.float32, (T,))
+    dres, ldr = None, 0
+    if dresidual is not None:
+        _, ldr = _rows(dresidual, "dresidual", x, (T, H))
+        dres = dresidual.data_ptr()
+    L = lib()
+    dx = torch.empty(T, H, dtype=x.dtype, device=x.device)
+    dw, ws, wsb = _norm_sums(T, H, x.device)
+    rc = L.moe_pre_norm_backward(dh.data_ptr(), ldd, x.data_ptr(), ldx, code, weight.data_ptr(), wcode, weight_offset,
+                                 rstd.data_ptr(), dres, ldr, T, H, dx.data_ptr(), dw.data_ptr(), ws, wsb, _stream())
+    _check("moe_pre_norm_backward", rc)
+    return dx, dw
+
+
+@dataclasses.dataclass
+class PostNorm:
+    """moe_post_norm: out and rstd, and the next block's norm of out (or None)."""
+    out: torch.Tensor
+    rstd: torch.Tensor
+    next_h: torch.Tensor | None = None
+    next_rstd: torch.Tensor | None = None
+
+
+@dataclasses.dataclass
+class PostNormGrads:
+    """moe_post_norm_backward: dresidual and dgate are None where not wanted."""
+    dy: torch.Tensor
+    dweight: torch.Tensor               # fp32 [H]
+    dresidual: torch.Tensor | None = None
+    dgate: torch.Tensor | None = None   # token, full: the gate's type and shape; channel: fp32 [H]
+
+
+def _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, eps, weight_offset,
+                      next_weight=None):
+    T, H = y.shape
+    wcode = _norm_weight(weight, H, "weight")
+    if next_weight is not None and _norm_weight(next_weight, H, "next_weight") != wcode:
+        raise TypeError("next_weight must have weight's type")
+    if gate_kind not in GATE_KIND:
+        raise ValueError(f"gate_kind must be one of {list(GATE_KIND)}, got {gate_kind!r}")
+    if (gate is None) != (gate_kind == "none"):
+        raise ValueError(f"gate_kind {gate_kind!r} and gate do not go together")
+    gp, gs = None, 0
+    if gate is not None:
+        _typed(gate, "gate", y)
+        if gate_kind == "full":
+            _, gs = _rows(gate, "gate", y, (T, H))
+        else:
+            n = T if gate_kind == "token" else H
+            if tuple(gate.shape) not in ((n,), (n, 1) if gate_kind == "token" else (1, n)):
+                raise ValueError(f"a {gate_kind} gate must hold {n} values, got {list(gate.shape)}")
+            gs = gate.stride(0 if gate_kind == "token" else -1) if n > 1 else 1
+            if gs < 1 or (gate_kind == "channel" and gs != 1):
+                raise ValueError(f"a {gate_kind} gate must not be broadcast"
+                                 + (" or strided" if gate_kind == "channel" else ""))
+        gp = gate.data_ptr()
+    return _PostNormParams(weight.data_ptr(), None if next_weight is None else next_weight.data_ptr(), gp, gs, wcode,
+                           GATE_KIND[gate_kind], int(bool(gate_sigmoid)), weight_offset, eps, residual_scale,
+                           block_scale)
+
+
+def moe_post_norm(y, residual, weight, gate=None, gate_kind="none", gate_sigmoid=False, residual_scale=1.0,
+                  block_scale=1.0, eps=1e-6, weight_offset=0.0, next_weight=None) -> PostNorm:
+    """RMS norm after a block with its gate and residual:
+    out = residual_scale * residual + block_scale * g * (y * rstd * (weight + weight_offset)), g the gate
+    (gate_kind "token": [T] or [T, 1], "channel": [H] or [1, H], "full": [T, H], in y's type) or its sigmoid.
+    next_weight: also the next block's norm of out, as stored."""
+    code, ldy = _rows(y, "y")
+    T, H = y.shape
+    _, ldr = _rows(residual, "residual", y, (T, H))
+    prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, eps, weight_offset,
+                            next_weight)
+    r = PostNorm(torch.empty(T, H, dtype=y.dtype, device=y.device),
+                 torch.empty(T, dtype=torch.float32, device=y.device))
+    h2 = r2 = None
+    if next_weight is not None:
+        r.next_h, r.next_rstd = torch.empty_like(r.out), torch.empty_like(r.rstd)
+        h2, r2 = r.next_h.data_ptr(), r.next_rstd.data_ptr()
+    _check("moe_post_norm", lib().moe_post_norm(y.data_ptr(), ldy, residual.data_ptr(), ldr, code, ctypes.byref(prm), T,
+                                                H, r.out.data_ptr(), r.rstd.data_ptr(), h2, r2, _stream()))
+    return r
+
+
+def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", gate_sigmoid=False,
+                           residual_scale=1.0, block_scale=1.0, weight_offset=0.0, residual_grad=True) -> PostNormGrads:
+    """Gradients of moe_post_norm for dout (with a next_weight: the gradient of out, the part that
+    next_h sends there included).  residual_grad=False: dresidual = residual_scale * dout is not written."""
+    code, ldy = _rows(y, "y")
+    T, H = y.shape
+    _, ldo = _rows(dout, "dout", y, (T, H))
+    _dense(rstd, "rstd", torch.float32, (T,))
+    prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, 0.0, weight_offset)
+    dy = torch.empty(T, H, dtype=y.dtype, device=y.device)
+    dres = torch.empty_like(dy) if residual_grad else None
+    if gate_kind == "channel":
+        dw, dg, ws, wsb = _norm_sums(T, H, y.device, 2)
+    else:
+        dw, ws, wsb = _norm_sums(T, H, y.device)
+        dg = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    rc = lib().moe_post_norm_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, ctypes.byref(prm),
+                                      rstd.data_ptr(), T, H, dy.data_ptr(), None if dres is None else dres.data_ptr(),
+                                      None if dg is None else dg.data_ptr(), dw.data_ptr(), ws, wsb, _stream())
+    _check("moe_post_norm_backward", rc)
+    if gate_kind == "channel":
+        dg = dg.view(gate.shape)
+    return PostNormGrads(dy, dw, dres, dg)
 
 
 def moe_selftest_bounded_wait(expire=True):

@@ -539,6 +539,57 @@ int moe_combine_backward(const void* dout, int64_t lddout, const void* y, int64_
                          const int32_t* pair_ids, const float* weights, int T, int topk, int H, int64_t num_rows,
                          void* dy, float* dweights, void* stream);
 
+/* The RMS norm before a block: h = x * rstd * (weight + weight_offset), rstd = 1/sqrt(mean(x^2) +
+ * eps) per row (fp32 [T]; kept for the gradient).  weight [H] of type weight_dtype.
+ * H <= MOE_MAX_HIDDEN_NORM. */
+#define MOE_MAX_HIDDEN_NORM 16384
+int moe_pre_norm(const void* x, int64_t ldx, int dtype, const void* weight, int weight_dtype, float weight_offset,
+                 float eps, int T, int H, void* h, float* rstd, void* stream);
+/* Its gradients: dx = rstd * (t - n * mean(t * n)) + dresidual with n = x * rstd and
+ * t = dh * (weight + weight_offset) (dresidual NULL = none: the gradient that reaches x by the
+ * residual), dweight fp32 [H] = sum over rows of dh * n.  workspace: device scratch of
+ * moe_norm_backward_workspace_size(T, H) bytes (4-byte aligned). */
+size_t moe_norm_backward_workspace_size(int T, int H);
+int moe_pre_norm_backward(const void* dh, int64_t lddh, const void* x, int64_t ldx, int dtype, const void* weight,
+                          int weight_dtype, float weight_offset, const float* rstd, const void* dresidual,
+                          int64_t lddres, int T, int H, void* dx, float* dweight, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The norm after a block, with the block's gate and the scaled residual:
+ *   out = residual_scale * residual + block_scale * g * (y * rstd * (weight + weight_offset))
+ * g: 1 (MOE_GATE_NONE), one value per row (MOE_GATE_TOKEN, element t at gate[t * gate_stride]), per
+ * column (MOE_GATE_CHANNEL, [H]) or per element (MOE_GATE_FULL, row stride gate_stride), of the rows'
+ * type; with gate_sigmoid its sigmoid.  With next_weight (of weight_dtype), the next block's norm
+ * of the stored out follows in the same pass: next_h = out * next_rstd * (next_weight +
+ * weight_offset), with the same eps. */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_TOKEN 1
+#define MOE_GATE_CHANNEL 2
+#define MOE_GATE_FULL 3
+typedef struct moe_post_norm_params {
+    const void* weight;
+    const void* next_weight;     /* or NULL (ignored by the gradient) */
+    const void* gate;            /* NULL with MOE_GATE_NONE */
+    int64_t gate_stride;
+    int32_t weight_dtype;
+    int32_t gate_kind;
+    int32_t gate_sigmoid;
+    float weight_offset;
+    float eps;
+    float residual_scale;
+    float block_scale;
+} moe_post_norm_params;
+int moe_post_norm(const void* y, int64_t ldy, const void* residual, int64_t ldr, int dtype,
+                  const moe_post_norm_params* params, int T, int H, void* out, float* rstd, void* next_h,
+                  float* next_rstd, void* stream);
+/* Its gradients for dout: dy; dresidual = residual_scale * dout (NULL = not wanted); dweight fp32 [H]; dgate
+ * (NULL = not wanted): token [T] and full [T, H] in the rows' type, channel fp32 [H].  The gradient
+ * that next_h sends to out is part of dout (moe_pre_norm_backward adds it).  workspace as above. */
+int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int64_t ldy, int dtype,
+                           const moe_post_norm_params* params, const float* rstd, int T, int H, void* dy,
+                           void* dresidual, void* dgate, float* dweight, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 /* ---- status -------------------------------------------------------------------- */
 /* Reads (and with clear != 0, resets) the device status word of the current
  * device into *status (host).  Synchronises the device. */

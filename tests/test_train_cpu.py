@@ -81,3 +81,89 @@ def test_token_binding_refuses():
               lambda: moe.moe_dispatch_backward(x, ids), lambda: moe.moe_combine_backward(x, x, ids, ids[:, 0])):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def pre_norm(**change):
+    good = dict(x=P, ldx=64, dtype=0, w=P, wt=2, off=0.0, eps=1e-6, T=8, H=64, h=P, rstd=P, stream=NULL)
+    return call("moe_pre_norm", good, **change)
+
+
+def pre_norm_backward(**change):
+    good = dict(dh=P, ldd=64, x=P, ldx=64, dtype=0, w=P, wt=2, off=0.0, rstd=P, dres=P, ldr=64, T=8, H=64, dx=P, dw=P,
+                ws=P, wsb=BIG, stream=NULL)
+    return call("moe_pre_norm_backward", good, **change)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(ldx=63), INVALID), (dict(dtype=3), INVALID), (dict(wt=3), INVALID),
+    (dict(x=NULL), INVALID), (dict(w=NULL), INVALID), (dict(rstd=NULL), INVALID), (dict(x=ODD), INVALID),
+    (dict(w=TWO), INVALID), (dict(H=16385, ldx=16385), SHAPE),
+])
+def test_pre_norm_refuses(change, code):
+    assert pre_norm(**change) == code
+    assert pre_norm_backward(**change) == code
+
+
+def test_pre_norm_refuses_its_outputs():
+    assert pre_norm(h=NULL) == INVALID and pre_norm(h=ODD) == INVALID
+    for change in (dict(dx=NULL), dict(dw=NULL), dict(dh=NULL), dict(ldd=63), dict(ldr=63), dict(dx=ODD), dict(ws=NULL)):
+        assert pre_norm_backward(**change) == INVALID
+    assert pre_norm_backward(wsb=0) == WORKSPACE
+    assert ops.lib().moe_norm_backward_workspace_size(0, 64) == 0
+    assert ops.lib().moe_norm_backward_workspace_size(4096, 64) > 0
+
+
+def params(**change):
+    good = dict(weight=0x10000, next_weight=0, gate=0x10000, gate_stride=64, weight_dtype=2, gate_kind=3, gate_sigmoid=0,
+                weight_offset=0.0, eps=1e-6, residual_scale=1.0, block_scale=1.0)
+    return ctypes.byref(ops._PostNormParams(*{**good, **change}.values()))
+
+
+def post_norm(prm=None, **change):
+    good = dict(y=P, ldy=64, r=P, ldr=64, dtype=0, prm=params(**(prm or {})), T=8, H=64, out=P, rstd=P, h2=P, r2=P,
+                stream=NULL)
+    return call("moe_post_norm", good, **change)
+
+
+def post_norm_backward(prm=None, **change):
+    good = dict(dout=P, ldo=64, y=P, ldy=64, dtype=0, prm=params(**(prm or {})), rstd=P, T=8, H=64, dy=P, dres=P, dgate=P,
+                dw=P, ws=P, wsb=BIG, stream=NULL)
+    return call("moe_post_norm_backward", good, **change)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(T=-1), INVALID), (dict(H=0), INVALID), (dict(ldy=63), INVALID), (dict(dtype=3), INVALID), (dict(y=NULL), INVALID),
+    (dict(rstd=NULL), INVALID), (dict(y=ODD), INVALID), (dict(H=16385, ldy=16385), SHAPE),
+])
+def test_post_norm_refuses(change, code):
+    assert post_norm(**change) == code
+    assert post_norm_backward(**change) == code
+
+
+@pytest.mark.parametrize("prm", [
+    dict(weight=0), dict(weight=0x10002), dict(weight_dtype=5), dict(gate_kind=4), dict(gate_kind=-1), dict(gate_kind=0),
+    dict(gate=0), dict(gate_stride=63), dict(gate_kind=1, gate_stride=0), dict(gate=0x10001),
+])
+def test_post_norm_refuses_parameters(prm):
+    assert post_norm(prm) == INVALID
+    assert post_norm_backward(prm) == INVALID
+
+
+def test_post_norm_refuses_its_outputs():
+    nxt = dict(next_weight=0x10000)
+    assert call("moe_post_norm", dict(y=P, ldy=64, r=P, ldr=64, dtype=0, prm=NULL, T=8, H=64, out=P, rstd=P, h2=P, r2=P,
+                                      stream=NULL)) == INVALID
+    assert post_norm(out=NULL) == INVALID and post_norm(r=NULL) == INVALID and post_norm(ldr=63) == INVALID
+    assert post_norm(nxt, h2=NULL) == INVALID and post_norm(nxt, r2=NULL) == INVALID
+    for change in (dict(dy=NULL), dict(dw=NULL), dict(dout=NULL), dict(ldo=63), dict(dres=ODD), dict(ws=NULL)):
+        assert post_norm_backward(**change) == INVALID
+    assert post_norm_backward(dict(gate=0, gate_kind=0)) == INVALID      # a gradient for no gate
+    assert post_norm_backward(wsb=8) == WORKSPACE
+
+
+def test_norm_binding_refuses():
+    x = torch.zeros(4, 8)
+    for f in (lambda: moe.moe_pre_norm(x, x[0]), lambda: moe.moe_post_norm(x, x, x[0]),
+              lambda: moe.moe_pre_norm_backward(x, x, x[0], x[:, 0]), lambda: moe.moe_post_norm_backward(x, x, x[0], x[:, 0])):
+        with pytest.raises(ValueError, match="CUDA"):
+            f()
