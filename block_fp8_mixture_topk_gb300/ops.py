@@ -134,6 +134,8 @@ def lib():
                 "moe_pre_norm_backward": ([P, I64, P, I64, I, P, I, F, P, P, I64, I, I, P, P, P, SZ, P], I),
                 "moe_post_norm": ([P, I64, P, I64, I, P, I, I, P, P, P, P, P], I),
                 "moe_post_norm_backward": ([P, I64, P, I64, I, P, P, I, I, P, P, P, P, P, SZ, P], I),
+                "moe_clip_grads_workspace_size": ([I], SZ),
+                "moe_clip_grads": ([P, P, P, P, I, I, F, F, P, P, SZ, P], I),
                 "moe_get_device_status": ([P, I], I),
                 "moe_selftest_bounded_wait": ([I, P], I),
                 "moe_error_string": ([I], ctypes.c_char_p),
@@ -806,6 +808,37 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     if gate_kind == "channel":
         dg = dg.view(gate.shape)
     return PostNormGrads(dy, dw, dres, dg)
+
+
+def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
+    """Global norm of a list of contiguous gradient tensors (bf16, fp16, fp32, in any mix) and their
+    clipping by min(1, max_norm / (norm + eps)): in place, or into the list `out` (same shapes and
+    types).  norm_type 2 or inf.  Returns the norm before clipping, fp32, on the device."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    kind = {2.0: 0, float("inf"): 1}.get(float(norm_type))
+    if kind is None:
+        raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
+    if len(out) != len(grads):
+        raise ValueError("out must hold one tensor per gradient")
+    n = len(grads)
+    codes = []
+    for i, (g, o) in enumerate(zip(grads, out)):
+        codes.append(_typed(g, f"grads[{i}]"))
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be contiguous")
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous()):
+            raise ValueError(f"out[{i}] must be a contiguous CUDA tensor like grads[{i}]")
+    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    L = lib()
+    wsb = L.moe_clip_grads_workspace_size(n)
+    buf = torch.empty(wsb // 4 + 1, dtype=torch.float32, device=device)   # the scratch, then the norm
+    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    outs = ptrs if out is grads else (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    rc = L.moe_clip_grads(ptrs, outs, (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*codes),
+                          n, kind, float(max_norm), float(eps), buf.data_ptr() + wsb, buf.data_ptr(), wsb, _stream())
+    _check("moe_clip_grads", rc)
+    return buf[wsb // 4]
 
 
 def moe_selftest_bounded_wait(expire=True):

@@ -590,6 +590,20 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
                            void* dresidual, void* dgate, float* dweight, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* Global norm of n gradient tensors and their clipping:
+ *   total = sqrt(sum of squares) (MOE_NORM_L2) or the largest magnitude (MOE_NORM_INF) over all,
+ *   out[i] = grads[i] * min(1, max_norm / (total + eps))
+ * grads, out, numel, dtype: host arrays of n (device addresses, elements, MOE_DTYPE_*); out[i] ==
+ * grads[i] clips in place (otherwise they may not overlap).  total_norm: device fp32.  A NaN total
+ * makes every gradient NaN, as the formula does.  Nothing is read after the call returns but the
+ * tensors.  workspace: device scratch of moe_clip_grads_workspace_size(n) bytes, 8-byte aligned. */
+#define MOE_NORM_L2 0
+#define MOE_NORM_INF 1
+size_t moe_clip_grads_workspace_size(int n);
+int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dtype, int n,
+                   int norm_kind, float max_norm, float eps, float* total_norm, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
 /* ---- status -------------------------------------------------------------------- */
 /* Reads (and with clear != 0, resets) the device status word of the current
  * device into *status (host).  Synchronises the device. */

@@ -167,3 +167,30 @@ def test_norm_binding_refuses():
               lambda: moe.moe_pre_norm_backward(x, x, x[0], x[:, 0]), lambda: moe.moe_post_norm_backward(x, x, x[0], x[:, 0])):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def clip(n=2, grads=(0x10000, 0x20000), out=None, numel=(4, 5), dtype=(0, 2), kind=0, limit=1.0, eps=1e-6, total=P, ws=P,
+         wsb=BIG):
+    a = (ctypes.c_void_p * 2)(*grads)
+    o = (ctypes.c_void_p * 2)(*(out or grads))
+    return ops.lib().moe_clip_grads(a, o, (ctypes.c_int64 * 2)(*numel), (ctypes.c_int32 * 2)(*dtype), n, kind, limit, eps,
+                                    total, ws, wsb, None)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(n=-1), INVALID), (dict(kind=2), INVALID), (dict(limit=-1.0), INVALID), (dict(limit=float("nan")), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(total=NULL), INVALID), (dict(numel=(4, -1)), INVALID), (dict(dtype=(0, 3)), INVALID),
+    (dict(grads=(0x10000, 0)), INVALID), (dict(grads=(0x10001, 0x20000)), INVALID), (dict(out=(0x10000, 0x20002)), INVALID),
+    (dict(numel=(1 << 51, 1)), SHAPE), (dict(wsb=0), WORKSPACE), (dict(ws=NULL), INVALID),
+])
+def test_clip_refuses(change, code):
+    assert clip(**change) == code
+
+
+def test_clip_binding_refuses():
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_clip_grads([torch.zeros(3)], 1.0)
+    with pytest.raises(ValueError, match="norm_type"):
+        moe.moe_clip_grads([], 1.0, norm_type=1)
+    with pytest.raises(ValueError, match="one tensor per gradient"):
+        moe.moe_clip_grads([torch.zeros(3)], 1.0, out=[])
