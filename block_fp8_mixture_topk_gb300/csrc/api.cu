@@ -43,7 +43,8 @@ int device_state(DeviceState** out) {
             void* p = nullptr;
             if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess || route_init_device() != cudaSuccess ||
                 permute_init_device() != cudaSuccess || gemm_init_device() != cudaSuccess ||
-                decode_init_device() != cudaSuccess || tokens_init_device() != cudaSuccess) {
+                decode_init_device() != cudaSuccess || tokens_init_device() != cudaSuccess ||
+                experts_init_device() != cudaSuccess) {
                 cudaGetLastError();
                 return MOE_ERR_CUDA;
             }

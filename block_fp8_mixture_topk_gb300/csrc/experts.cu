@@ -1,0 +1,634 @@
+// The experts' products over rows sorted by expert, in bf16 or fp16 with fp32 accumulation, and
+// their gradients ("w13 [num_experts, N, K]", page "Quantization and MoE Optimizations", section
+// FusedMoE Class):
+//
+//   product            c[r]  = a[r] @ w[e]^T              a [rows, K], w [E, N, K], c [rows, N]
+//   ... SiLU(gate)*up  h[r]  = silu(c[r, :N/2]) * c[r, N/2:]
+//   rows' gradient     da[r] = dc[r] @ w[e]               dc [rows, N], da [rows, K]
+//   ... through SiLU(gate)*up (gate, up [rows, 2K]):
+//                      dgate = da * up * s * (1 + gate * (1 - s)),  dup = da * gate * s,  s = sigmoid(gate)
+//   weights' gradient  dw[e] = dc[rows of e]^T @ a[rows of e]
+// where expert e owns rows [offsets[e], offsets[e+1]).
+//
+// One persistent kernel, one CTA per SM: a TMA thread fills a ring of 64-wide K blocks, one thread
+// issues tcgen05.mma (128 x 256 x 16, two accumulators in tensor memory), eight warps drain an
+// accumulator while the next one fills.  The operands keep the caller's layout; where the
+// reduction runs along the slow axis (w of the rows' gradient, both operands of the weights'
+// gradient) the 128-byte rows of a TMA box run along the other axis and the MMA reads the tile
+// transposed (MN-major).  Rows need no padding: a tile that ends inside an expert computes rows of
+// the next and does not store them, and the weights' gradient zeroes the rows past its expert's end in
+// shared memory, for both operands, so that nothing a neighbour holds (a NaN, say) reaches it.
+#include <type_traits>
+
+#include "train.cuh"
+
+namespace mfp8 {
+namespace {
+
+enum Mode { kForward = 0, kForwardSilu = 1, kRows = 2, kRowsSilu = 3, kWeights = 4 };
+
+constexpr int XM = 128, XN = 256, XK = 64;         // tile; XK elements are one 128-byte swizzled row
+constexpr int X_STAGES = 4;
+constexpr int XA_TILE = XM * XK * 2, XB_TILE = XN * XK * 2;
+constexpr int X_BOX = 64 * 128;                    // bytes of a transposed operand's box: 64 rows of 64 elements
+constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: tile table, 3: idle
+constexpr int X_THREADS = (X_FIRST_EPI + X_EPI_WARPS) * 32;
+constexpr uint32_t X_TMEM = 512;
+constexpr int X_PITCH = 80;                        // bytes of a staged row of 32 elements (64 B and a pad: conflict-free)
+constexpr int X_WARP_STAGE = 32 * X_PITCH;
+
+struct ExpertArgs {
+    const int32_t* offsets;
+    int E;
+    int64_t rows;
+    int N, K;                  // w is [E, N, K]
+    void* out;                 // c, h, da, dgate|dup or dw
+    void* gate_up;             // kForwardSilu: written [rows, N] (null: not); kRowsSilu: read [rows, 2K]
+    int64_t ld_gu;
+    uint32_t* status;
+};
+
+struct XCtl {
+    uint64_t full[X_STAGES], empty[X_STAGES], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
+    int tile0[MOE_MAX_EXPERTS + 1];   // first 128-row tile of each expert
+};
+constexpr size_t X_SMEM = 1024 + X_STAGES * (XA_TILE + XB_TILE) + X_EPI_WARPS * X_WARP_STAGE + sizeof(XCtl);
+static_assert(X_SMEM <= 232448, "more shared memory than a CTA has");
+
+// One output tile: rows [r0, r0 + nrow) of column tile n of expert e; kblocks of the reduction
+// (length red).
+struct XItem {
+    int e, n, kblocks, red;
+    int64_t r0;
+    int nrow;
+};
+
+template <int MODE>
+__device__ __forceinline__ int64_t item_count(const ExpertArgs& a, const XCtl* ctl, int NT) {
+    if (MODE == kWeights) return static_cast<int64_t>(a.E) * ((a.N + XM - 1) / XM) * NT;
+    return static_cast<int64_t>(ctl->tile0[a.E]) * NT;
+}
+
+template <int MODE>
+__device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, int64_t w, int NT) {
+    XItem t;
+    if (MODE == kWeights) {
+        const int MT = (a.N + XM - 1) / XM, per = MT * NT;
+        t.e = static_cast<int>(w / per);
+        const int local = static_cast<int>(w - static_cast<int64_t>(t.e) * per);
+        const int m = local % MT;
+        t.n = local / MT;
+        t.r0 = m * XM;
+        t.nrow = a.N - m * XM < XM ? a.N - m * XM : XM;
+        t.red = ctl->row0[t.e + 1] - ctl->row0[t.e];
+    } else {
+        // the expert whose tiles hold tile w / NT; its row tiles run fastest, so that neighbouring
+        // CTAs read the same columns of its weights
+        const int g = static_cast<int>(w / NT);
+        int lo = 0, hi = a.E - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (ctl->tile0[mid] <= g) lo = mid;
+            else hi = mid - 1;
+        }
+        t.e = lo;
+        const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo];
+        const int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
+        const int m = local % mt;
+        t.n = local / mt;
+        const int cnt = ctl->row0[lo + 1] - ctl->row0[lo];
+        t.r0 = ctl->row0[lo] + m * XM;
+        t.nrow = cnt - m * XM < XM ? cnt - m * XM : XM;
+        t.red = MODE == kRows || MODE == kRowsSilu ? a.N : a.K;
+    }
+    t.kblocks = t.red > 0 ? (t.red + XK - 1) / XK : 0;
+    return t;
+}
+
+// Descriptor of a tile read transposed: 64-element rows of 128 bytes along M or N (swizzled, as
+// TMA writes them), one per reduction index; 8 of them (1024 bytes) to a group, the next 64
+// elements of M or N one box further.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(X_BOX >> 4) << 16;         // leading byte offset: next 64 of M or N
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;          // stride byte offset: next 8 of K
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+template <class T>
+__host__ __device__ constexpr uint32_t idesc_16bit(int n, bool a_mn, bool b_mn) {
+    const uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return (1u << 4)                                       // D format: f32
+           | (fmt << 7) | (fmt << 10)                      // A, B format: bf16 or f16
+           | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16)   // transposed
+           | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(XM >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, 128 x N x 16, 16-bit operands, fp32 accumulation.
+__device__ __forceinline__ void mma_16bit(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (std::is_same<T, __nv_bfloat16>::value) return bf16x2(lo, hi);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if (std::is_same<T, __nv_bfloat16>::value)
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+// 32 columns (v: this lane's row) to rows [r0, r0 + nrow) of a matrix of `cols` columns at column c,
+// through the warp's staging area so that each row leaves as 64 contiguous bytes.  nrow: rows of
+// this warp that exist.
+template <class T>
+__device__ __forceinline__ void store_columns(const float* v, uint8_t* stage, int lane, T* out, int64_t ld, int64_t r0,
+                                              int nrow, int c, int cols) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint4 u;
+        u.x = pack2<T>(v[q * 8 + 0], v[q * 8 + 1]);
+        u.y = pack2<T>(v[q * 8 + 2], v[q * 8 + 3]);
+        u.z = pack2<T>(v[q * 8 + 4], v[q * 8 + 5]);
+        u.w = pack2<T>(v[q * 8 + 6], v[q * 8 + 7]);
+        *reinterpret_cast<uint4*>(stage + lane * X_PITCH + q * 16) = u;
+    }
+    __syncwarp();
+    const int q = lane & 3;
+    if (c + q * 8 < cols) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r < nrow)
+                *reinterpret_cast<uint4*>(out + (r0 + r) * ld + c + q * 8) =
+                    *reinterpret_cast<const uint4*>(stage + r * X_PITCH + q * 16);
+        }
+    }
+    __syncwarp();
+}
+// The reverse: this lane's row of 32 columns.
+template <class T>
+__device__ __forceinline__ void load_columns(float* v, uint8_t* stage, int lane, const T* in, int64_t ld, int64_t r0,
+                                             int nrow, int c, int cols) {
+    const int q = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (r < nrow && c + q * 8 < cols) u = __ldg(reinterpret_cast<const uint4*>(in + (r0 + r) * ld + c + q * 8));
+        *reinterpret_cast<uint4*>(stage + r * X_PITCH + q * 16) = u;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint4 u = *reinterpret_cast<const uint4*>(stage + lane * X_PITCH + k * 16);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2<T>(w[i]);
+            v[k * 8 + 2 * i] = f.x;
+            v[k * 8 + 2 * i + 1] = f.y;
+        }
+    }
+    __syncwarp();
+}
+
+template <class T, int MODE>
+__global__ void __launch_bounds__(X_THREADS, 1)
+    expert_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const ExpertArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    uint8_t* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    uint8_t* smA = base;
+    uint8_t* smB = base + X_STAGES * XA_TILE;
+    uint8_t* smE = smB + X_STAGES * XB_TILE;
+    XCtl* ctl = reinterpret_cast<XCtl*>(smE + X_EPI_WARPS * X_WARP_STAGE);
+    constexpr bool A_MN = MODE == kWeights;
+    constexpr bool B_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
+    constexpr bool SILU = MODE == kForwardSilu;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int OC = MODE == kForward ? a.N : SILU ? a.N / 2 : a.K;   // output columns (of h, for kForwardSilu)
+    const int NT = SILU ? (OC + 127) / 128 : (OC + XN - 1) / XN;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < X_STAGES; ++s) {
+            mbar_init(smem_addr(&ctl->full[s]), 1);
+            mbar_init(smem_addr(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&ctl->tfull[b]), 1);
+            mbar_init(smem_addr(&ctl->tempty[b]), X_EPI_WARPS);
+        }
+        mbar_init(smem_addr(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&ctl->tmem_base), X_TMEM);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    // the experts' rows: offsets that leave [0, rows] or run backwards are clamped and reported
+    for (int e = threadIdx.x; e <= a.E; e += X_THREADS) {
+        int64_t o = a.offsets[e];
+        const int64_t prev = e > 0 ? a.offsets[e - 1] : 0;
+        if (o < 0 || o > a.rows || prev > o || (e == 0 && o != 0)) {
+            status_set(a.status, MOE_STATUS_BAD_COUNT);
+            o = o < 0 ? 0 : o > a.rows ? a.rows : o;
+        }
+        ctl->row0[e] = static_cast<int>(o);
+    }
+    __syncthreads();
+    if (warp == 2) {
+        int carry = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int cnt = e < a.E ? ctl->row0[e + 1] - ctl->row0[e] : 0;
+            const int own = cnt > 0 ? (cnt + XM - 1) / XM : 0;
+            int v = own;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, s);
+                if (lane >= s) v += u;
+            }
+            if (e < a.E) ctl->tile0[e] = carry + v - own;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) ctl->tile0[a.E] = carry;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    const int64_t total = item_count<MODE>(a, ctl, NT);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ TMA
+            int stage = 0;
+            uint32_t phase = 0, issued = 0;
+            bool ok = true;
+            for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+                const XItem t = item_at<MODE>(a, ctl, w, NT);
+                const int c0 = SILU ? t.n * 128 : t.n * XN;
+                for (int kb = 0; kb < t.kblocks; ++kb) {
+                    if (!mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_addr(&ctl->full[stage]);
+                    const uint32_t sa = smem_addr(smA + stage * XA_TILE), sb = smem_addr(smB + stage * XB_TILE);
+                    mbar_arrive_expect_tx(fb, XA_TILE + XB_TILE);
+                    if (MODE == kWeights) {
+                        // 64 rows of the expert: 128 columns of dc, 256 of a, in boxes of 64
+                        const int32_t r = ctl->row0[t.e] + kb * XK;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            tma_load_2d(sa + i * X_BOX, &tmA, (static_cast<int32_t>(t.r0) + i * 64) * 2, r, fb);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) tma_load_2d(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, r, fb);
+                    } else {
+                        tma_load_2d(sa, &tmA, kb * XK * 2, static_cast<int32_t>(t.r0), fb);
+                        if (B_MN) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                tma_load_3d(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, kb * XK, t.e, fb);
+                        } else {
+                            tma_load_3d(sb, &tmB, kb * XK * 2, c0, t.e, fb);
+                            tma_load_3d(sb + XB_TILE / 2, &tmB, kb * XK * 2, SILU ? OC + c0 : c0 + 128, t.e, fb);
+                        }
+                    }
+                    ++issued;
+                    if (++stage == X_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                // let every load already issued land before the CTA exits
+                for (int s = 0; s < X_STAGES; ++s) {
+                    const uint32_t n_s = (issued + X_STAGES - 1 - s) / X_STAGES;
+                    if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA
+        const uint32_t idesc = idesc_16bit<T>(XN, A_MN, B_MN);
+        int stage = 0;
+        uint32_t phase = 0, buf = 0, bphase = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            const XItem t = item_at<MODE>(a, ctl, w, NT);
+            if (t.kblocks == 0) continue;
+            const uint32_t d = tmem + buf * XN;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
+            for (int kb = 0; kb < t.kblocks && ok; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
+                if (!ok) break;
+                tc_fence_after();
+                int steps = XK / 16;
+                if (MODE == kWeights && t.red - kb * XK < XK) {
+                    // the expert ends in this block: only the 16-row steps that hold its rows, the
+                    // rest of the last step zeroed
+                    const int live = t.red - kb * XK;
+                    steps = (live + 15) / 16;
+                    const int pieces = (steps * 16 - live) * 8;   // 16-byte pieces of one box
+                    for (int i = lane; i < pieces * 6; i += 32) {
+                        const int box = i / pieces, p = i - box * pieces;
+                        uint8_t* at = box < 2 ? smA + stage * XA_TILE + box * X_BOX
+                                              : smB + stage * XB_TILE + (box - 2) * X_BOX;
+                        *reinterpret_cast<uint4*>(at + live * 128 + p * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_proxy();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    const uint32_t a0 = smem_addr(smA + stage * XA_TILE);
+                    const uint32_t b0 = smem_addr(smB + stage * XB_TILE);
+                    for (int k = 0; k < steps; ++k) {
+                        const uint64_t ad = A_MN ? smem_desc_mn_sw128(a0 + k * 2048) : smem_desc_k128_sw128(a0 + k * 32);
+                        const uint64_t bd = B_MN ? smem_desc_mn_sw128(b0 + k * 2048) : smem_desc_k128_sw128(b0 + k * 32);
+                        mma_16bit(d, ad, bd, idesc, (kb | k) > 0 ? 1u : 0u);
+                    }
+                    mma_commit(smem_addr(&ctl->empty[stage]));
+                    if (kb + 1 == t.kblocks) mma_commit(smem_addr(&ctl->tfull[buf]));
+                }
+                __syncwarp();
+                if (++stage == X_STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            buf ^= 1u;
+            if (buf == 0) bphase ^= 1u;
+        }
+        if (!ok && lane == 0) {
+            mma_commit(smem_addr(&ctl->drain));
+            mbar_wait(smem_addr(&ctl->drain), 0, nullptr, a.status);
+        }
+    } else if (warp >= X_FIRST_EPI) {
+        // ---------------------------------------------------------------- epilogue
+        const int g = (warp - X_FIRST_EPI) >> 2;   // column half
+        const int sp = warp & 3;                   // tensor-memory lane quarter
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+        uint8_t* stage = smE + (warp - X_FIRST_EPI) * X_WARP_STAGE;
+        T* out = static_cast<T*>(a.out);
+        uint32_t buf = 0, bphase = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+            const XItem t = item_at<MODE>(a, ctl, w, NT);
+            const int64_t r0 = t.r0 + sp * 32 + (MODE == kWeights ? static_cast<int64_t>(t.e) * a.N : 0);
+            const int nrow = t.nrow - sp * 32;
+            const int c0 = SILU ? t.n * 128 : t.n * XN;
+            if (MODE == kWeights && t.kblocks == 0) {   // an expert without rows: zero
+                float z[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+                for (int j = 0; j < 4; ++j)
+                    store_columns<T>(z, stage, lane, out, OC, r0, nrow, c0 + g * 128 + j * 32, OC);
+                continue;
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t acc = lane_base + buf * XN;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float va[32], vb[32];
+                if (SILU) {
+                    const int c = g * 64 + j * 32;
+                    tmem_ld32x2(acc + c, acc + 128 + c, va, vb);
+                } else {
+                    const int c = g * 128 + j * 64;
+                    tmem_ld32x2(acc + c, acc + c + 32, va, vb);
+                }
+                if (j == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ctl->tempty[buf]));
+                }
+                if (nrow <= 0) continue;
+                if (SILU) {
+                    const int c = c0 + g * 64 + j * 32;
+                    T* gu = static_cast<T*>(a.gate_up);
+                    if (gu) {
+                        store_columns<T>(va, stage, lane, gu, 2 * OC, r0, nrow, c, OC);
+                        store_columns<T>(vb, stage, lane, gu + OC, 2 * OC, r0, nrow, c, OC);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) va[i] = va[i] / (1.0f + __expf(-va[i])) * vb[i];
+                    store_columns<T>(va, stage, lane, out, OC, r0, nrow, c, OC);
+                } else if (MODE == kRowsSilu) {
+                    const T* gu = static_cast<const T*>(a.gate_up);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float* v = h ? vb : va;
+                        const int c = c0 + g * 128 + j * 64 + h * 32;
+                        float gt[32], up[32];
+                        load_columns<T>(gt, stage, lane, gu, a.ld_gu, r0, nrow, c, OC);
+                        load_columns<T>(up, stage, lane, gu + OC, a.ld_gu, r0, nrow, c, OC);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float s = 1.0f / (1.0f + __expf(-gt[i]));
+                            const float dup = v[i] * gt[i] * s;
+                            v[i] = v[i] * up[i] * s * (1.0f + gt[i] * (1.0f - s));
+                            up[i] = dup;
+                        }
+                        store_columns<T>(v, stage, lane, out, 2 * OC, r0, nrow, c, OC);
+                        store_columns<T>(up, stage, lane, out + OC, 2 * OC, r0, nrow, c, OC);
+                    }
+                } else {
+                    const int c = c0 + g * 128 + j * 64;
+                    store_columns<T>(va, stage, lane, out, OC, r0, nrow, c, OC);
+                    store_columns<T>(vb, stage, lane, out, OC, r0, nrow, c + 32, OC);
+                }
+            }
+            buf ^= 1u;
+            if (buf == 0) bphase ^= 1u;
+        }
+        if (MODE != kWeights && ok) {
+            // rows of no expert: zero
+            const int64_t cols = MODE == kRowsSilu ? 2 * OC : OC, first = ctl->row0[a.E], left = a.rows - first;
+            const int64_t n = left * cols / 8, n2 = SILU && a.gate_up ? left * a.N / 8 : 0;
+            const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (X_EPI_WARPS * 32) + threadIdx.x - X_FIRST_EPI * 32;
+            const int64_t step = static_cast<int64_t>(gridDim.x) * (X_EPI_WARPS * 32);
+            for (int64_t i = i0; i < n; i += step)
+                reinterpret_cast<uint4*>(out + first * cols)[i] = make_uint4(0, 0, 0, 0);
+            for (int64_t i = i0; i < n2; i += step)
+                reinterpret_cast<uint4*>(static_cast<T*>(a.gate_up) + first * a.N)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, X_TMEM);
+    }
+}
+
+// Tensor map of 16-bit rows [n1, n0] (n2 of them; 0: two dimensions), boxes of 64 elements by box1
+// rows, as bytes.
+cudaError_t map_16bit(CUtensorMap* map, const void* p, int64_t n0, int64_t ld, int64_t n1, int64_t n2, int box1) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(n0) * 2, static_cast<uint64_t>(n1), static_cast<uint64_t>(n2)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(ld) * 2 * n1};
+    const uint32_t box[3] = {128, static_cast<uint32_t>(box1), 1};
+    return encode_u8_map_nd(map, static_cast<const uint8_t*>(p), n2 > 0 ? 3 : 2, dims, strides, box, true);
+}
+
+template <class T, int MODE>
+cudaError_t launch_experts(const ExpertArgs& a, const CUtensorMap& tmA, const CUtensorMap& tmB, int64_t most_items,
+                           cudaStream_t stream) {
+    const int sms = device_sms();
+    const unsigned grid = static_cast<unsigned>(most_items < sms ? most_items : sms);
+    return launch_pdl(expert_gemm_kernel<T, MODE>, dim3(grid), dim3(X_THREADS), X_SMEM, stream, tmA, tmB, a);
+}
+
+template <int MODE>
+cudaError_t launch_experts_type(int dtype, const ExpertArgs& a, const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                int64_t most_items, cudaStream_t stream) {
+    return dtype == MOE_DTYPE_BF16 ? launch_experts<__nv_bfloat16, MODE>(a, tmA, tmB, most_items, stream)
+                                   : launch_experts<__half, MODE>(a, tmA, tmB, most_items, stream);
+}
+
+template <class T, int MODE>
+cudaError_t set_smem() {
+    return cudaFuncSetAttribute(expert_gemm_kernel<T, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(X_SMEM));
+}
+template <class T>
+cudaError_t set_smem_all() {
+    cudaError_t e = set_smem<T, kForward>();
+    if (e == cudaSuccess) e = set_smem<T, kForwardSilu>();
+    if (e == cudaSuccess) e = set_smem<T, kRows>();
+    if (e == cudaSuccess) e = set_smem<T, kRowsSilu>();
+    if (e == cudaSuccess) e = set_smem<T, kWeights>();
+    return e;
+}
+
+int64_t most_row_tiles(int64_t rows, int E) { return rows / XM + (rows < E ? rows : E) + 1; }
+
+// Checks that all three products share.
+int check_experts(int dtype, int64_t rows, int E, int N, int K) {
+    if (rows < 0 || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || N % 8 != 0 || K % 8 != 0 || rows >= (int64_t(1) << 31) || N >= (1 << 29) ||
+        K >= (1 << 29))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+bool on_16(const void* p) { return (address(p) & 15) == 0; }
+
+}  // namespace
+
+cudaError_t experts_init_device() {
+    const cudaError_t e = set_smem_all<__nv_bfloat16>();
+    return e == cudaSuccess ? set_smem_all<__half>() : e;
+}
+
+}  // namespace mfp8
+
+using namespace mfp8;
+
+extern "C" {
+
+int moe_expert_gemm(const void* rows_a, int64_t lda, int dtype, const void* w, const int32_t* expert_offsets,
+                    int64_t num_rows, int E, int N, int K, int epilogue, void* out, void* gate_up, void* stream) {
+    int rc = check_experts(dtype, num_rows, E, N, K);
+    if (rc != MOE_OK) return rc;
+    if (epilogue != MOE_EXPERT_STORE && epilogue != MOE_EXPERT_SILU_MUL) return MOE_ERR_INVALID_ARG;
+    if (lda < K || (gate_up && epilogue == MOE_EXPERT_STORE)) return MOE_ERR_INVALID_ARG;
+    if (lda % 8 != 0 || (epilogue == MOE_EXPERT_SILU_MUL && N % 16 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!w || !expert_offsets || (num_rows > 0 && (!rows_a || !out))) return MOE_ERR_INVALID_ARG;
+    if (!on_16(rows_a) || !on_16(w) || !on_16(out) || !on_16(gate_up)) return MOE_ERR_INVALID_ARG;
+    if (num_rows == 0) return MOE_OK;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
+    CUtensorMap tmA, tmB;
+    if (map_16bit(&tmA, rows_a, K, lda, num_rows, 0, XM) != cudaSuccess ||
+        map_16bit(&tmB, w, K, K, N, E, 128) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, gate_up, 0, status};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t tiles = most_row_tiles(num_rows, E);
+    if (epilogue == MOE_EXPERT_STORE)
+        return cuda_status(launch_experts_type<kForward>(dtype, a, tmA, tmB, tiles * ((N + XN - 1) / XN), s));
+    return cuda_status(launch_experts_type<kForwardSilu>(dtype, a, tmA, tmB, tiles * ((N / 2 + 127) / 128), s));
+}
+
+int moe_expert_gemm_dgrad(const void* dc, int64_t lddc, int dtype, const void* w, const int32_t* expert_offsets,
+                          int64_t num_rows, int E, int N, int K, const void* gate_up, int64_t ldgu, void* out,
+                          void* stream) {
+    int rc = check_experts(dtype, num_rows, E, N, K);
+    if (rc != MOE_OK) return rc;
+    if (lddc < N || (gate_up && ldgu < 2 * static_cast<int64_t>(K))) return MOE_ERR_INVALID_ARG;
+    if (lddc % 8 != 0 || (gate_up && ldgu % 8 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!w || !expert_offsets || (num_rows > 0 && (!dc || !out))) return MOE_ERR_INVALID_ARG;
+    if (!on_16(dc) || !on_16(w) || !on_16(out) || !on_16(gate_up)) return MOE_ERR_INVALID_ARG;
+    if (num_rows == 0) return MOE_OK;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
+    CUtensorMap tmA, tmB;
+    if (map_16bit(&tmA, dc, N, lddc, num_rows, 0, XM) != cudaSuccess ||
+        map_16bit(&tmB, w, K, K, N, E, XK) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, const_cast<void*>(gate_up), ldgu, status};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t items = most_row_tiles(num_rows, E) * ((K + XN - 1) / XN);
+    if (gate_up) return cuda_status(launch_experts_type<kRowsSilu>(dtype, a, tmA, tmB, items, s));
+    return cuda_status(launch_experts_type<kRows>(dtype, a, tmA, tmB, items, s));
+}
+
+int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* rows_a, int64_t lda, int dtype,
+                          const int32_t* expert_offsets, int64_t num_rows, int E, int N, int K, void* dw,
+                          void* stream) {
+    int rc = check_experts(dtype, num_rows, E, N, K);
+    if (rc != MOE_OK) return rc;
+    if (lddc < N || lda < K) return MOE_ERR_INVALID_ARG;
+    if (lddc % 8 != 0 || lda % 8 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!dw || !expert_offsets || (num_rows > 0 && (!dc || !rows_a))) return MOE_ERR_INVALID_ARG;
+    if (!on_16(dc) || !on_16(rows_a) || !on_16(dw)) return MOE_ERR_INVALID_ARG;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * N * K * 2, s));
+    CUtensorMap tmA, tmB;
+    if (map_16bit(&tmA, dc, N, lddc, num_rows, 0, XK) != cudaSuccess ||
+        map_16bit(&tmB, rows_a, K, lda, num_rows, 0, XK) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, dw, nullptr, 0, status};
+    const int64_t items = static_cast<int64_t>(E) * ((N + XM - 1) / XM) * ((K + XN - 1) / XN);
+    return cuda_status(launch_experts_type<kWeights>(dtype, a, tmA, tmB, items, s));
+}
+
+}  // extern "C"

@@ -134,6 +134,9 @@ def lib():
                 "moe_pre_norm_backward": ([P, I64, P, I64, I, P, I, F, P, P, I64, I, I, P, P, P, SZ, P], I),
                 "moe_post_norm": ([P, I64, P, I64, I, P, I, I, P, P, P, P, P], I),
                 "moe_post_norm_backward": ([P, I64, P, I64, I, P, P, I, I, P, P, P, P, P, SZ, P], I),
+                "moe_expert_gemm": ([P, I64, I, P, P, I64, I, I, I, I, P, P, P], I),
+                "moe_expert_gemm_dgrad": ([P, I64, I, P, P, I64, I, I, I, P, I64, P, P], I),
+                "moe_expert_gemm_wgrad": ([P, I64, P, I64, I, P, I64, I, I, I, P, P], I),
                 "moe_clip_grads_workspace_size": ([I], SZ),
                 "moe_clip_grads": ([P, P, P, P, I, I, F, F, P, P, SZ, P], I),
                 "moe_get_device_status": ([P, I], I),
@@ -808,6 +811,88 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     if gate_kind == "channel":
         dg = dg.view(gate.shape)
     return PostNormGrads(dy, dw, dres, dg)
+
+
+def _expert_operands(t, E, offsets, name):
+    code, ld = _rows(t, name)
+    if t.dtype == torch.float32:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    _dense(offsets, "expert_offsets", torch.int32, (E + 1,))
+    return code, ld
+
+
+def _expert_weights(w, like):
+    if w.dim() != 3:
+        raise ValueError(f"w must be [E, N, K], got {list(w.shape)}")
+    _cuda(w, like.dtype, "w")
+    return w.shape
+
+
+def _expert_gemm(a, w, expert_offsets, epilogue, out, gate_up):
+    E, N, K = w.shape
+    code, ld = _expert_operands(a, E, expert_offsets, "a")
+    if a.shape[1] != K:
+        raise ValueError(f"a must have {K} columns, got {a.shape[1]}")
+    rc = lib().moe_expert_gemm(a.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), a.shape[0], E, N, K,
+                               epilogue, out.data_ptr(), None if gate_up is None else gate_up.data_ptr(), _stream())
+    _check("moe_expert_gemm", rc)
+
+
+def moe_expert_gemm(a, w, expert_offsets):
+    """The experts' product over rows sorted by expert: out[r] = a[r] @ w[e]^T for the rows
+    [expert_offsets[e], expert_offsets[e+1]) of a [rows, K]; w [E, N, K]; bf16 or fp16.  Rows of no expert are zero."""
+    _, N, _ = _expert_weights(w, a)
+    out = torch.empty(a.shape[0], N, dtype=a.dtype, device=a.device)
+    _expert_gemm(a, w, expert_offsets, 0, out, None)
+    return out
+
+
+def moe_expert_gemm_silu_mul(a, w, expert_offsets, save_gate_up=True):
+    """The first product with its activation: (h [rows, N/2] = silu(gate) * up, gate_up [rows, N] = the
+    product itself, which the gradient needs; None with save_gate_up=False).  w [E, N, K]: gate rows, then up."""
+    _, N, _ = _expert_weights(w, a)
+    h = torch.empty(a.shape[0], N // 2, dtype=a.dtype, device=a.device)
+    gu = torch.empty(a.shape[0], N, dtype=a.dtype, device=a.device) if save_gate_up else None
+    _expert_gemm(a, w, expert_offsets, 1, h, gu)
+    return h, gu
+
+
+def moe_expert_gemm_dgrad(dc, w, expert_offsets, gate_up=None):
+    """The rows' gradient da[r] = dc[r] @ w[e], [rows, K]; with gate_up [rows, 2K], where a was
+    silu(gate) * up, the gradient of gate_up instead."""
+    E, N, K = _expert_weights(w, dc)
+    code, ld = _expert_operands(dc, E, expert_offsets, "dc")
+    n = dc.shape[0]
+    if dc.shape[1] != N:
+        raise ValueError(f"dc must have {N} columns, got {dc.shape[1]}")
+    gp, ldgu = None, 0
+    if gate_up is not None:
+        _, ldgu = _rows(gate_up, "gate_up", dc, (n, 2 * K))
+        gp = gate_up.data_ptr()
+    out = torch.empty(n, K if gate_up is None else 2 * K, dtype=dc.dtype, device=dc.device)
+    rc = lib().moe_expert_gemm_dgrad(dc.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), n, E, N, K, gp,
+                                     ldgu, out.data_ptr(), _stream())
+    _check("moe_expert_gemm_dgrad", rc)
+    return out
+
+
+def moe_expert_gemm_wgrad(dc, a, expert_offsets):
+    """The weights' gradient dw[e] = dc[rows of e]^T @ a[rows of e], [E, N, K] in dc's type (zero for
+    an expert without rows)."""
+    if expert_offsets.dim() != 1 or expert_offsets.shape[0] < 2:
+        raise ValueError(f"expert_offsets must be [E+1], got {list(expert_offsets.shape)}")
+    E = expert_offsets.shape[0] - 1
+    code, ldd = _expert_operands(dc, E, expert_offsets, "dc")
+    _, lda = _rows(a, "a", dc)
+    if a.shape[0] != dc.shape[0]:
+        raise ValueError("dc and a must have the same rows")
+    n, N = dc.shape
+    K = a.shape[1]
+    dw = torch.empty(E, N, K, dtype=dc.dtype, device=dc.device)
+    rc = lib().moe_expert_gemm_wgrad(dc.data_ptr(), ldd, a.data_ptr(), lda, code, expert_offsets.data_ptr(), n, E, N, K,
+                                     dw.data_ptr(), _stream())
+    _check("moe_expert_gemm_wgrad", rc)
+    return dw
 
 
 def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):

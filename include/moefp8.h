@@ -50,7 +50,7 @@ extern "C" {
 /* device status bits (moe_get_device_status) */
 #define MOE_STATUS_WAIT_TIMEOUT 0x1u      /* a pipeline wait gave up; outputs invalid */
 #define MOE_STATUS_BAD_EXPERT_ID 0x2u     /* a routed id was outside [0, E); pair dropped */
-#define MOE_STATUS_BAD_COUNT 0x4u         /* a masked-layout count was outside [0, max_tokens]; clamped */
+#define MOE_STATUS_BAD_COUNT 0x4u         /* a masked-layout count or an expert's row offset was out of range; clamped */
 #define MOE_STATUS_BAD_SCALE 0x8u         /* a scale packed as UE8M0 was not a positive power of two */
 
 /* Limits of this implementation. */
@@ -589,6 +589,30 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
                            const moe_post_norm_params* params, const float* rstd, int T, int H, void* dy,
                            void* dresidual, void* dgate, float* dweight, void* workspace, size_t workspace_bytes,
                            void* stream);
+
+/* The experts' products over rows sorted by expert (moe_dispatch), bf16 or fp16 with fp32
+ * accumulation: expert e's rows [expert_offsets[e], expert_offsets[e+1]) against w [E, N, K].
+ *   MOE_EXPERT_STORE:    out [num_rows, N] = a @ w^T
+ *   MOE_EXPERT_SILU_MUL: out [num_rows, N/2] = silu(c[:, :N/2]) * c[:, N/2:] of the fp32 products
+ *                        (w13's rows: gate, then up), and, where gate_up is not NULL, c itself rounded,
+ *                        [num_rows, N], which the gradient needs
+ * Rows past expert_offsets[E] are zero.  expert_offsets that leave [0, num_rows], start above 0 or run
+ * backwards are clamped and set MOE_STATUS_BAD_COUNT.  N and K multiples of 8 (N of 16 with
+ * SILU_MUL), row strides multiples of 8, all addresses 16-byte aligned. */
+#define MOE_EXPERT_STORE 0
+#define MOE_EXPERT_SILU_MUL 1
+int moe_expert_gemm(const void* a, int64_t lda, int dtype, const void* w, const int32_t* expert_offsets,
+                    int64_t num_rows, int E, int N, int K, int epilogue, void* out, void* gate_up, void* stream);
+/* The gradient of the rows: da [num_rows, K] = dc @ w[e].  With gate_up [num_rows, 2K] (row stride ldgu),
+ * where a was silu(gate) * up: out [num_rows, 2K] = the gradients of gate and of up instead. */
+int moe_expert_gemm_dgrad(const void* dc, int64_t lddc, int dtype, const void* w, const int32_t* expert_offsets,
+                          int64_t num_rows, int E, int N, int K, const void* gate_up, int64_t ldgu, void* out,
+                          void* stream);
+/* The gradient of the weights: dw [E, N, K] = dc[rows of e]^T @ a[rows of e], zero for an expert
+ * without rows. */
+int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* a, int64_t lda, int dtype,
+                          const int32_t* expert_offsets, int64_t num_rows, int E, int N, int K, void* dw,
+                          void* stream);
 
 /* Global norm of n gradient tensors and their clipping:
  *   total = sqrt(sum of squares) (MOE_NORM_L2) or the largest magnitude (MOE_NORM_INF) over all,

@@ -194,3 +194,50 @@ def test_clip_binding_refuses():
         moe.moe_clip_grads([], 1.0, norm_type=1)
     with pytest.raises(ValueError, match="one tensor per gradient"):
         moe.moe_clip_grads([torch.zeros(3)], 1.0, out=[])
+
+
+def product(**change):
+    good = dict(a=P, lda=64, dtype=0, w=P, off=P, rows=16, E=4, N=32, K=64, epilogue=1, out=P, gu=P, stream=NULL)
+    return call("moe_expert_gemm", good, **change)
+
+
+def dgrad(**change):
+    good = dict(dc=P, ldd=32, dtype=0, w=P, off=P, rows=16, E=4, N=32, K=64, gu=P, ldgu=128, out=P, stream=NULL)
+    return call("moe_expert_gemm_dgrad", good, **change)
+
+
+def wgrad(**change):
+    good = dict(dc=P, ldd=32, a=P, lda=64, dtype=0, off=P, rows=16, E=4, N=32, K=64, dw=P, stream=NULL)
+    return call("moe_expert_gemm_wgrad", good, **change)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=-1), INVALID), (dict(E=0), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(dtype=2), INVALID),
+    (dict(dtype=-1), INVALID), (dict(off=NULL), INVALID), (dict(E=1025), SHAPE), (dict(N=12), SHAPE), (dict(K=60), SHAPE),
+    (dict(rows=2 ** 31), SHAPE),
+])
+def test_products_refuse(change, code):
+    for f in (product, dgrad, wgrad):
+        assert f(**change) == code
+
+
+def test_products_refuse_operands():
+    for change, code in ((dict(a=NULL), INVALID), (dict(w=NULL), INVALID), (dict(out=NULL), INVALID), (dict(lda=56), INVALID),
+                         (dict(lda=65), SHAPE), (dict(a=TWO), INVALID), (dict(w=TWO), INVALID), (dict(out=TWO), INVALID),
+                         (dict(gu=TWO), INVALID), (dict(epilogue=2), INVALID), (dict(epilogue=0), INVALID), (dict(N=40), SHAPE)):
+        assert product(**change) == code, change
+    for change, code in ((dict(dc=NULL), INVALID), (dict(w=NULL), INVALID), (dict(out=NULL), INVALID), (dict(ldd=24), INVALID),
+                         (dict(ldd=33), SHAPE), (dict(ldgu=120), INVALID), (dict(ldgu=129), SHAPE), (dict(gu=TWO), INVALID)):
+        assert dgrad(**change) == code, change
+    for change, code in ((dict(dc=NULL), INVALID), (dict(a=NULL), INVALID), (dict(dw=NULL), INVALID), (dict(ldd=24), INVALID),
+                         (dict(lda=56), INVALID), (dict(lda=65), SHAPE), (dict(ldd=33), SHAPE), (dict(dw=TWO), INVALID)):
+        assert wgrad(**change) == code, change
+
+
+def test_expert_binding_refuses():
+    x, off = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    w = torch.zeros(2, 8, 8, dtype=torch.bfloat16)
+    for f in (lambda: moe.moe_expert_gemm(x, w, off), lambda: moe.moe_expert_gemm_silu_mul(x, w, off),
+              lambda: moe.moe_expert_gemm_dgrad(x, w, off), lambda: moe.moe_expert_gemm_wgrad(x, x, off)):
+        with pytest.raises(ValueError, match="CUDA"):
+            f()
