@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const FinalArgs 
     }
     float g = weight_at(a.gate, a.g_dtype, c), slope = 1.0f;
     if (a.sigmoid) {
-        g = sigmoid_f32(g);
+        g = sigmoid_as<float>(g);
         slope = g * (1.0f - g);
     }
     a.dw[c] = a.b * g * v;
@@ -103,6 +103,7 @@ int moe_pre_norm(const void* x, int64_t ldx, int dtype, const void* weight, int 
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     NormArgs a = {};
+    a.status = status;
     a.T = T;
     a.H = H;
     a.x = x;
@@ -143,6 +144,7 @@ int moe_pre_norm_backward(const void* dh, int64_t lddh, const void* x, int64_t l
     int ctas = 0;
     if (T > 0) {
         NormArgs a = {};
+        a.status = status;
         a.T = T;
         a.H = H;
         a.x = x;
@@ -187,6 +189,7 @@ int moe_post_norm(const void* y, int64_t ldy, const void* residual, int64_t ldr,
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     NormArgs a = {};
+    a.status = status;
     a.T = T;
     a.H = H;
     a.x = y;
@@ -236,6 +239,7 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
     int ctas = 0;
     if (T > 0) {
         NormArgs a = {};
+        a.status = status;
         a.T = T;
         a.H = H;
         a.x = y;

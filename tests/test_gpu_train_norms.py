@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 # and five products; a row's dot product 53 more
 ROW = 53 / 2 + 8
 SHAPES = [(1, 1), (1, 7168), (3, 8), (5, 33), (64, 256), (7, 1000), (301, 520), (2, 16384), (3, 16383), (400, 2880),
-          (160, 4104), (19, 4097)]
+          (160, 4104), (19, 4097), (1000, 64), (2100, 1032), (700, 7168), (310, 16384), (320, 8448)]
 
 
 def norm64(x, w, off, eps):
@@ -64,7 +64,7 @@ def test_pre_norm_and_gradient(T, H, dtype, wtype):
 @pytest.mark.parametrize("kind", ["none", "token", "channel", "full"])
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 7168), (5, 33), (64, 256), (301, 520), (2, 16384), (3, 16383), (400, 2880),
-                                 (19, 4097)])
+                                 (19, 4097), (2100, 1032), (700, 7168), (310, 16384), (320, 8448)])
 def test_post_norm_and_gradient(T, H, dtype, kind, sigmoid):
     if kind == "none" and sigmoid:
         pytest.skip("no gate to take the sigmoid of")
