@@ -73,7 +73,10 @@ int check_gate(const moe_post_norm_params* p, int H, int* gate) {
     if ((p->gate_kind == MOE_GATE_NONE) != (p->gate == nullptr)) return MOE_ERR_INVALID_ARG;
     if (p->gate_kind == MOE_GATE_TOKEN && p->gate_stride < 1) return MOE_ERR_INVALID_ARG;
     if (p->gate_kind == MOE_GATE_FULL && p->gate_stride < H) return MOE_ERR_INVALID_ARG;
-    *gate = p->gate_kind == MOE_GATE_CHANNEL ? kGateChannel : p->gate_kind == MOE_GATE_FULL ? kGateFull : kGateRow;
+    *gate = p->gate_kind == MOE_GATE_CHANNEL ? kGateChannel
+            : p->gate_kind != MOE_GATE_FULL  ? kGateRow
+            : p->gate_sigmoid                ? kGateFullSigmoid
+                                             : kGateFull;
     return MOE_OK;
 }
 // Addresses and strides of the gate that decide on 16-byte vectors (a row gate is read by element).
@@ -261,7 +264,7 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
         a.partial = static_cast<float*>(workspace);
         uintptr_t bits = address(dout) | address(y) | address(dy) | static_cast<uintptr_t>((lddout | ldy) * es) |
                          address(dresidual) | gate_bits(p, es);
-        if (gate == kGateFull) bits |= address(dgate);
+        if (full_gate(gate)) bits |= address(dgate);
         const cudaError_t e = launch_norm_dtype(a, dtype, kPostBackward, gate, wide_rows(bits, H, es), s, &ctas);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }

@@ -10,8 +10,8 @@
 //
 // All are bound by memory: every element is read once from DRAM and held between the row's reduction
 // and its use (at most 32 elements per thread, G threads per row).  A CTA holds R groups of G
-// threads, each with its own named barrier, and walks over rows with the weights in registers.  Two
-// sources of rows: registers (RowRegs: any alignment, and few rows), or a ring in shared memory
+// threads, each with its own named barrier, and walks over rows with the weights at hand.  Two
+// sources of rows and weights: registers (RowRegs: any alignment, and few rows), or shared memory
 // (RowRing: 16-byte rows; one thread of a group keeps up to four rows of bulk copies in flight
 // ahead of the group, so that the reduction's latency does not stop the loads).  The weights'
 // gradient is summed over a CTA's rows in fp32 registers, over its groups in shared memory, written once
@@ -25,8 +25,12 @@
 
 namespace mfp8 {
 
-constexpr int kNormThreads = 512;   // most threads of a CTA
-enum GateShape { kGateRow = 0, kGateChannel = 1, kGateFull = 2 };   // kGateRow also stands for no gate
+// Most threads of a CTA (128 registers); forward with rows in the ring and no next norm (64 registers)
+constexpr int kNormThreads = 512, kNormWideThreads = 1024;
+constexpr int kNormGroups = 15;     // groups of a CTA with a named barrier each
+// kGateRow also stands for no gate; kGateFullSigmoid: the sigmoid of a full gate
+enum GateShape { kGateRow = 0, kGateChannel = 1, kGateFull = 2, kGateFullSigmoid = 3 };
+constexpr bool full_gate(int g) { return g == kGateFull || g == kGateFullSigmoid; }
 
 struct NormArgs {
     int64_t T;
@@ -51,12 +55,20 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i) 
     if (dtype == MOE_DTYPE_FP16) return __half2float(static_cast<const __half*>(w)[i]);
     return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
-// sigmoid(v): for 16-bit results with the fast exponential and division (a few 2^-23 relative, far
-// below their rounding of 2^-9 and 2^-12)
+// sigmoid(v): for 16-bit results with the approximate exponential and reciprocal instructions (a few
+// 2^-23 relative, far below their rounding of 2^-9 and 2^-12; the division form costs three times
+// the instructions and made the gated backward pass instruction-bound)
 template <class T>
 __device__ __forceinline__ float sigmoid_as(float v) {
-    if (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-v));
-    return 1.0f / (1.0f + expf(-v));
+    if (sizeof(T) != 2) return 1.0f / (1.0f + expf(-v));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+template <class T>
+__device__ __forceinline__ float2 sigmoid_as(float2 v) {
+    return make_float2(sigmoid_as<T>(v.x), sigmoid_as<T>(v.y));
 }
 
 struct Group {
@@ -70,9 +82,10 @@ struct Group {
         parity ^= 1;
         if ((tid & 31) == 0) slot[tid >> 5] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(G) : "memory");
-        float t = 0.0f;
-        for (int i = 0; i < G / 32; ++i) t += slot[i];
-        return t;
+        const float4* q = reinterpret_cast<const float4*>(slot);   // (slots past the group's warps hold zero)
+        const float4 a = q[0], b = q[1], c = q[2], d = q[3];
+        return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + (((c.x + c.y) + (c.z + c.w)) +
+                                                                           ((d.x + d.y) + (d.z + d.w)));
     }
 };
 
@@ -83,20 +96,11 @@ __device__ __forceinline__ Group make_group(float* red, int G) {
     g.tid = threadIdx.x % G;
     g.parity = 0;
     g.red = red + g.id * 32;
+    if (G > 32 && g.tid < 32) g.red[g.tid] = 0.0f;
+    __syncthreads();
     return g;
 }
 
-template <class T, int V, int NV>
-__device__ __forceinline__ void load_weights(float (&w)[NV * V], const void* p, int dtype, float offset, int tid,
-                                             int G, int nvec) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int v = tid + i * G;
-            w[i * V + e] = v < nvec ? weight_at(p, dtype, static_cast<int64_t>(v) * V + e) + offset : 0.0f;
-        }
-}
 template <class T, int V, int NV>
 __device__ __forceinline__ void load_row(Pack<T, V> (&r)[NV], const T* p, int tid, int G, int nvec) {
 #pragma unroll
@@ -108,11 +112,19 @@ __device__ __forceinline__ void load_row(Pack<T, V> (&r)[NV], const T* p, int ti
 }
 
 // ---------------------------------------------------------------- sources of rows
-// A source hands out a group's rows of NIN matrices: start() once, then for each row fetch(t),
-// get(n, i) = vector i of this thread in matrix n (any number of times) and, after the group's
-// barrier in that row, next() (the row before is done with).  finish() at the end.
+// A source hands out a group's rows of NIN matrices and a row of weights (fp32): start() and weights()
+// once, then for each row fetch(t), get(n, i) = vector i of this thread in matrix n (any number of
+// times) and, after the group's barrier in that row, next() (the row before is done with); finish()
+// at the end.  weight(i) = the weights of vector i.
+template <int V>
+struct Weights {
+    float2 v[(V + 1) / 2];
+};
+
 template <class T, int V, int NV, int NIN>
 struct RowRegs {
+    static constexpr bool kWide = false;
+    Weights<V> w[NV];
     Pack<T, V> r[NIN][NV];
     const T* src[NIN];
     int64_t ld[NIN];
@@ -122,6 +134,21 @@ struct RowRegs {
         tid = g.tid;
         nvec = a.H / V;
     }
+    // f(column) = its weight
+    template <class F>
+    __device__ __forceinline__ void weights(F f) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int v = tid + i * G;
+                const float x = v < nvec ? f(v * V + e) : 0.0f;
+                if (e & 1) w[i].v[e / 2].y = x;
+                else w[i].v[e / 2] = make_float2(x, 0.0f);
+            }
+    }
+    __device__ __forceinline__ void weights_done() {}
+    __device__ __forceinline__ Weights<V> weight(int i) const { return w[i]; }
     __device__ __forceinline__ void fetch(int64_t t) {
 #pragma unroll
         for (int n = 0; n < NIN; ++n) load_row<T, V, NV>(r[n], src[n] + t * ld[n], tid, G, nvec);
@@ -133,6 +160,9 @@ struct RowRegs {
 
 template <class T, int V, int NV, int NIN>
 struct RowRing {
+    static constexpr bool kWide = true;
+    static constexpr int Q = V / 4;   // the weights of a vector: Q planes of float4, so that a warp reads 512 bytes in a row
+    float4* wsm;                      // [Q][nvec], the CTA's
     const T* src[NIN];
     int64_t ld[NIN];
     uint8_t* ring;              // this group's rows: [depth][NIN][row_bytes]
@@ -159,7 +189,26 @@ struct RowRing {
             if (++load_slot == depth) load_slot = 0;
         }
     }
-    // smem: [R][depth][NIN][row_bytes], then the barriers and the abort flag
+    template <class F>
+    __device__ __forceinline__ void weights(F f) {
+        for (int q = threadIdx.x; q < nvec * Q; q += blockDim.x) {
+            const int v = q / Q, p = q - v * Q, c = v * V + p * 4;
+            wsm[p * nvec + v] = make_float4(f(c), f(c + 1), f(c + 2), f(c + 3));
+        }
+    }
+    __device__ __forceinline__ void weights_done() { __syncthreads(); }
+    __device__ __forceinline__ Weights<V> weight(int i) const {
+        Weights<V> r;
+        const int v = tid + i * G;
+#pragma unroll
+        for (int p = 0; p < Q; ++p) {
+            const float4 f = v < nvec ? wsm[p * nvec + v] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            r.v[p * 2] = make_float2(f.x, f.y);
+            r.v[p * 2 + 1] = make_float2(f.z, f.w);
+        }
+        return r;
+    }
+    // smem: [H] weights, [R][depth][NIN][row_bytes], then the barriers and the abort flag
     __device__ __forceinline__ void start(const NormArgs& a, const Group& g, int64_t t0, int64_t step, int R,
                                           uint8_t* smem) {
         G = a.G;
@@ -168,6 +217,8 @@ struct RowRing {
         depth = a.depth;
         status = a.status;
         row_bytes = static_cast<uint32_t>(a.H) * sizeof(T);
+        wsm = reinterpret_cast<float4*>(smem);
+        smem += static_cast<size_t>(a.H) * 4;
         ring = smem + static_cast<size_t>(g.id) * depth * NIN * row_bytes;
         uint64_t* bars = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(R) * depth * NIN * row_bytes);
         bar = bars + g.id * depth;
@@ -219,34 +270,45 @@ struct RowRing {
     }
 };
 
+// The weight of column c, times the channel gate.
+template <class T, int GATE>
+__device__ __forceinline__ float gated_weight(const NormArgs& a, int c) {
+    const float w = weight_at(a.w, a.w_dtype, c) + a.w_offset;
+    if constexpr (GATE != kGateChannel) return w;
+    const float v = to_f32(static_cast<const T*>(a.gate)[c]);
+    return w * (a.sigmoid ? sigmoid_as<T>(v) : v);
+}
+
 #define MOE_NORM_PROLOGUE                                                             \
     extern __shared__ __align__(128) uint8_t norm_smem[];                             \
-    __shared__ float red[16 * 32];                                                    \
+    __shared__ __align__(16) float red[kNormGroups * 32];                                                    \
     Group g = make_group(red, a.G);                                                   \
+    constexpr int NP = (V + 1) / 2;                                                   \
     const int nvec = a.H / V, R = blockDim.x / a.G;                                   \
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * R + g.id, step = static_cast<int64_t>(gridDim.x) * R; \
     grid_dependency_wait();
 
 // h = x * rstd * w
 template <class T, int V, int NV, template <class, int, int, int> class Rows>
-__global__ void __launch_bounds__(kNormThreads) pre_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(Rows<T, V, NV, 1>::kWide ? kNormWideThreads : kNormThreads)
+    pre_norm_kernel(const NormArgs a) {
     MOE_NORM_PROLOGUE
     Rows<T, V, NV, 1> in;
     in.src[0] = static_cast<const T*>(a.x);
     in.ld[0] = a.ldx;
     in.start(a, g, t0, step, R, norm_smem);
-    float w[NV * V];
-    load_weights<T, V, NV>(w, a.w, a.w_dtype, a.w_offset, g.tid, a.G, nvec);
+    in.weights([&](int c) { return weight_at(a.w, a.w_dtype, c) + a.w_offset; });
+    in.weights_done();
     for (int64_t t = t0; t < a.T; t += step) {
         in.fetch(t);
-        float ss = 0.0f;
+        float2 ss = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Pack<T, V> x = in.get(0, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(x.get(e), x.get(e), ss);
+            for (int e = 0; e < NP; ++e) ss = fma2(x.pair(e), x.pair(e), ss);
         }
-        const float r = __frsqrt_rn(g.sum(ss) / static_cast<float>(a.H) + a.eps);
+        const float r = __frsqrt_rn(g.sum(ss.x + ss.y) / static_cast<float>(a.H) + a.eps);
         in.next();
         if (g.tid == 0) a.rstd[t] = r;
         T* out = static_cast<T*>(a.out) + t * a.H;
@@ -255,9 +317,10 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_kernel(const NormArgs a
             const int v = g.tid + i * a.G;
             if (v >= nvec) continue;
             const Pack<T, V> x = in.get(0, i);
+            const Weights<V> w = in.weight(i);
             Pack<T, V> o;
 #pragma unroll
-            for (int e = 0; e < V; ++e) o.set(e, x.get(e) * r * w[i * V + e]);
+            for (int e = 0; e < NP; ++e) o.set_pair(e, mul2(mul2(x.pair(e), both(r)), w.v[e]));
             o.store(out + static_cast<int64_t>(v) * V);
         }
     }
@@ -266,28 +329,31 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_kernel(const NormArgs a
 
 // out = a * res + b * g * (y * rstd * w); NEXT: h2 = out * rstd2 * w2 of the stored out
 template <class T, int V, int NV, int GATE, bool NEXT, template <class, int, int, int> class Rows>
-__global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThreads : kNormWideThreads)
+    post_norm_kernel(const NormArgs a) {
     MOE_NORM_PROLOGUE
-    Rows<T, V, NV, GATE == kGateFull ? 3 : 2> in;
+    Rows<T, V, NV, full_gate(GATE) ? 3 : 2> in;
     in.src[0] = static_cast<const T*>(a.x);
     in.ld[0] = a.ldx;
     in.src[1] = static_cast<const T*>(a.res);
     in.ld[1] = a.ldr;
-    if constexpr (GATE == kGateFull) {
+    if constexpr (full_gate(GATE)) {
         in.src[2] = static_cast<const T*>(a.gate);
         in.ld[2] = a.ldg;
     }
     in.start(a, g, t0, step, R, norm_smem);
-    float w[NV * V], w2[NEXT ? NV * V : 1];
-    load_weights<T, V, NV>(w, a.w, a.w_dtype, a.w_offset, g.tid, a.G, nvec);
-    if constexpr (NEXT) load_weights<T, V, NV>(w2, a.w2, a.w_dtype, a.w_offset, g.tid, a.G, nvec);
-    if constexpr (GATE == kGateChannel) {   // the gate scales the weight, for every row alike
-        Pack<T, V> gt[NV];
-        load_row<T, V, NV>(gt, static_cast<const T*>(a.gate), g.tid, a.G, nvec);
+    in.weights([&](int c) { return gated_weight<T, GATE>(a, c); });
+    in.weights_done();
+    float2 w2[NEXT ? NV * NP : 1];
+    if constexpr (NEXT) {
 #pragma unroll
-        for (int i = 0; i < NV * V; ++i) {
-            const float v = gt[i / V].get(i % V);
-            w[i] *= a.sigmoid ? sigmoid_as<T>(v) : v;
+        for (int i = 0; i < NV * NP; ++i) {
+            const int v = g.tid + (i / NP) * a.G, c = v * V + (i % NP) * 2;
+            w2[i] = both(0.0f);
+            if (v < nvec) {
+                w2[i].x = weight_at(a.w2, a.w_dtype, c) + a.w_offset;
+                if (V > 1) w2[i].y = weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset;
+            }
         }
     }
     for (int64_t t = t0; t < a.T; t += step) {
@@ -299,39 +365,38 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const NormArgs 
                 b *= a.sigmoid ? sigmoid_as<T>(v) : v;
             }
         }
-        float ss = 0.0f;
+        float2 ss = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Pack<T, V> y = in.get(0, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(y.get(e), y.get(e), ss);
+            for (int e = 0; e < NP; ++e) ss = fma2(y.pair(e), y.pair(e), ss);
         }
-        const float r = __frsqrt_rn(g.sum(ss) / static_cast<float>(a.H) + a.eps);
+        const float r = __frsqrt_rn(g.sum(ss.x + ss.y) / static_cast<float>(a.H) + a.eps);
         in.next();
         if (g.tid == 0) a.rstd[t] = r;
         T* out = static_cast<T*>(a.out) + t * a.H;
-        float s2 = 0.0f;
+        float2 s2 = both(0.0f);
         Pack<T, V> s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = g.tid + i * a.G;
             const Pack<T, V> y = in.get(0, i), res = in.get(1, i);
+            const Weights<V> w = in.weight(i);
             Pack<T, V> gt;
-            if constexpr (GATE == kGateFull) gt = in.get(2, i);
+            if constexpr (full_gate(GATE)) gt = in.get(2, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float z = y.get(e) * r * w[i * V + e] * b;
-                if constexpr (GATE == kGateFull) {
-                    const float gv = gt.get(e);
-                    z *= a.sigmoid ? sigmoid_as<T>(gv) : gv;
-                }
-                s[i].set(e, fmaf(a.a, res.get(e), z));
-                if constexpr (NEXT) s2 = fmaf(s[i].get(e), s[i].get(e), s2);
+            for (int e = 0; e < NP; ++e) {
+                float2 z = mul2(mul2(mul2(y.pair(e), both(r)), w.v[e]), both(b));
+                if constexpr (GATE == kGateFull) z = mul2(z, gt.pair(e));
+                if constexpr (GATE == kGateFullSigmoid) z = mul2(z, sigmoid_as<T>(gt.pair(e)));
+                s[i].set_pair(e, fma2(both(a.a), res.pair(e), z));
+                if constexpr (NEXT) s2 = fma2(s[i].pair(e), s[i].pair(e), s2);
             }
             if (v < nvec) s[i].store(out + static_cast<int64_t>(v) * V);
         }
         if constexpr (NEXT) {
-            const float r2 = __frsqrt_rn(g.sum(s2) / static_cast<float>(a.H) + a.eps);
+            const float r2 = __frsqrt_rn(g.sum(s2.x + s2.y) / static_cast<float>(a.H) + a.eps);
             if (g.tid == 0) a.rstd2[t] = r2;
             T* h2 = static_cast<T*>(a.h2) + t * a.H;
 #pragma unroll
@@ -340,7 +405,7 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const NormArgs 
                 if (v >= nvec) continue;
                 Pack<T, V> o;
 #pragma unroll
-                for (int e = 0; e < V; ++e) o.set(e, s[i].get(e) * r2 * w2[i * V + e]);
+                for (int e = 0; e < NP; ++e) o.set_pair(e, mul2(mul2(s[i].pair(e), both(r2)), w2[i * NP + e]));
                 o.store(h2 + static_cast<int64_t>(v) * V);
             }
         }
@@ -348,10 +413,11 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const NormArgs 
     in.finish();
 }
 
-// The CTA's sums over rows, group after group, into its row of the partials.
+// The CTA's sums over rows (times scale), group after group, into its row of the partials.
 template <int V, int NV>
-__device__ __forceinline__ void write_partial(const float (&acc)[NV * V], float* sum_s, const Group& g, int R,
-                                              int nvec, float* partial) {
+__device__ __forceinline__ void write_partial(const float2 (&acc)[NV * ((V + 1) / 2)], float scale, float* sum_s,
+                                              const Group& g, int R, int nvec, float* partial) {
+    constexpr int NP = (V + 1) / 2;
     __syncthreads();   // sum_s is the ring's memory
     for (int k = 0; k < R; ++k) {
         if (g.id == k) {
@@ -361,9 +427,10 @@ __device__ __forceinline__ void write_partial(const float (&acc)[NV * V], float*
                 if (v >= nvec) continue;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float u = acc[i * V + e] + (k > 0 ? sum_s[v * V + e] : 0.0f);
+                    const float2 p = acc[i * NP + e / 2];
+                    const float u = (e & 1 ? p.y : p.x) + (k > 0 ? sum_s[v * V + e] : 0.0f);
                     if (k + 1 < R) sum_s[v * V + e] = u;
-                    else partial[v * V + e] = u;
+                    else partial[v * V + e] = u * scale;
                 }
             }
         }
@@ -385,25 +452,27 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
         in.ld[2] = a.ldr;
     }
     in.start(a, g, t0, step, R, norm_smem);
-    float w[NV * V], acc[NV * V];
-    load_weights<T, V, NV>(w, a.w, a.w_dtype, a.w_offset, g.tid, a.G, nvec);
+    in.weights([&](int c) { return weight_at(a.w, a.w_dtype, c) + a.w_offset; });
+    in.weights_done();
+    float2 acc[NV * NP];
 #pragma unroll
-    for (int i = 0; i < NV * V; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < NV * NP; ++i) acc[i] = both(0.0f);
     for (int64_t t = t0; t < a.T; t += step) {
         const float r = a.rstd[t];
         in.fetch(t);
-        float m = 0.0f;
+        float2 m2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Pack<T, V> x = in.get(0, i), d = in.get(1, i);
+            const Weights<V> w = in.weight(i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float p = d.get(e) * (x.get(e) * r);
-                m = fmaf(p, w[i * V + e], m);
-                acc[i * V + e] += p;
+            for (int e = 0; e < NP; ++e) {
+                const float2 p = mul2(d.pair(e), mul2(x.pair(e), both(r)));
+                m2 = fma2(p, w.v[e], m2);
+                acc[i * NP + e] = add2(acc[i * NP + e], p);
             }
         }
-        m = g.sum(m) / static_cast<float>(a.H);
+        const float m = g.sum(m2.x + m2.y) / static_cast<float>(a.H);
         in.next();
         T* out = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
@@ -411,19 +480,20 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
             const int v = g.tid + i * a.G;
             if (v >= nvec) continue;
             const Pack<T, V> x = in.get(0, i), d = in.get(1, i);
+            const Weights<V> w = in.weight(i);
             Pack<T, V> o, s;
             if constexpr (RES) s = in.get(2, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float u = r * fmaf(-(x.get(e) * r), m, d.get(e) * w[i * V + e]);
-                if constexpr (RES) u += s.get(e);
-                o.set(e, u);
+            for (int e = 0; e < NP; ++e) {
+                const float2 u = fma2(mul2(x.pair(e), both(r)), both(-m), mul2(d.pair(e), w.v[e]));
+                if constexpr (RES) o.set_pair(e, fma2(u, both(r), s.pair(e)));
+                else o.set_pair(e, mul2(u, both(r)));
             }
             o.store(out + static_cast<int64_t>(v) * V);
         }
     }
     in.finish();
-    write_partial<V, NV>(acc, reinterpret_cast<float*>(norm_smem), g, R, nvec,
+    write_partial<V, NV>(acc, 1.0f, reinterpret_cast<float*>(norm_smem), g, R, nvec,
                          a.partial + static_cast<int64_t>(blockIdx.x) * a.H);
 }
 
@@ -434,29 +504,22 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
 template <class T, int V, int NV, int GATE, template <class, int, int, int> class Rows>
 __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const NormArgs a) {
     MOE_NORM_PROLOGUE
-    Rows<T, V, NV, GATE == kGateFull ? 3 : 2> in;
+    constexpr bool FULL = full_gate(GATE), KEEP = GATE == kGateFullSigmoid;   // KEEP: sigmoids, from pass to pass
+    Rows<T, V, NV, FULL ? 3 : 2> in;
     in.src[0] = static_cast<const T*>(a.x);
     in.ld[0] = a.ldx;
     in.src[1] = static_cast<const T*>(a.dout);
     in.ld[1] = a.ldo;
-    if constexpr (GATE == kGateFull) {
+    if constexpr (FULL) {
         in.src[2] = static_cast<const T*>(a.gate);
         in.ld[2] = a.ldg;
     }
     in.start(a, g, t0, step, R, norm_smem);
-    float w[NV * V], acc[NV * V];   // w: weight (channel: times the gate)
-    load_weights<T, V, NV>(w, a.w, a.w_dtype, a.w_offset, g.tid, a.G, nvec);
-    if constexpr (GATE == kGateChannel) {
-        Pack<T, V> gt[NV];
-        load_row<T, V, NV>(gt, static_cast<const T*>(a.gate), g.tid, a.G, nvec);
+    in.weights([&](int c) { return gated_weight<T, GATE>(a, c); });
+    in.weights_done();
+    float2 acc[NV * NP], kept[KEEP ? NV * NP : 1];
 #pragma unroll
-        for (int i = 0; i < NV * V; ++i) {
-            const float v = gt[i / V].get(i % V);
-            w[i] *= a.sigmoid ? sigmoid_as<T>(v) : v;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NV * V; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < NV * NP; ++i) acc[i] = both(0.0f);
     for (int64_t t = t0; t < a.T; t += step) {
         const float r = a.rstd[t];
         float gr = 1.0f, slope = 1.0f;   // the row's gate and the gate's slope
@@ -470,63 +533,65 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
             }
         }
         in.fetch(t);
-        float m = 0.0f;   // sum of dout (* full gate) * n * w
+        float2 m2 = both(0.0f);   // sum of dout (* full gate) * n * w
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const Pack<T, V> y = in.get(0, i), d = in.get(1, i);
+            const Weights<V> w = in.weight(i);
             Pack<T, V> gt;
-            if constexpr (GATE == kGateFull) gt = in.get(2, i);
+            if constexpr (FULL) gt = in.get(2, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float p = d.get(e) * (y.get(e) * r);
-                if constexpr (GATE == kGateFull) {
-                    const float gv = gt.get(e);
-                    p *= a.sigmoid ? sigmoid_as<T>(gv) : gv;
+            for (int e = 0; e < NP; ++e) {
+                float2 p = mul2(d.pair(e), mul2(y.pair(e), both(r)));
+                if constexpr (KEEP) {
+                    kept[i * NP + e] = sigmoid_as<T>(gt.pair(e));
+                    p = mul2(p, kept[i * NP + e]);
+                } else if constexpr (FULL) {
+                    p = mul2(p, gt.pair(e));
                 }
-                m = fmaf(p, w[i * V + e], m);
-                if constexpr (GATE == kGateChannel) acc[i * V + e] += p;
-                else acc[i * V + e] = fmaf(p, gr * a.b, acc[i * V + e]);
+                m2 = fma2(p, w.v[e], m2);
+                if constexpr (GATE == kGateRow) acc[i * NP + e] = fma2(p, both(gr), acc[i * NP + e]);
+                else acc[i * NP + e] = add2(acc[i * NP + e], p);
             }
         }
-        m = g.sum(m);
+        const float sum = g.sum(m2.x + m2.y);
         in.next();
         if constexpr (GATE == kGateRow)
-            if (a.dgate && g.tid == 0) static_cast<T*>(a.dgate)[t] = from_f32<T>(slope * a.b * m);
-        const float scale = a.b * gr * r;      // of t / w
-        m /= static_cast<float>(a.H);
+            if (a.dgate && g.tid == 0) static_cast<T*>(a.dgate)[t] = from_f32<T>(slope * a.b * sum);
+        const float2 scale = both(a.b * gr * r), m = both(-(sum / static_cast<float>(a.H)));   // scale: of t / w
         T* dy = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = g.tid + i * a.G;
             if (v >= nvec) continue;
             const Pack<T, V> y = in.get(0, i), d = in.get(1, i);
+            const Weights<V> w = in.weight(i);
             Pack<T, V> o, p, q, gt;
-            if constexpr (GATE == kGateFull) gt = in.get(2, i);
+            if constexpr (FULL && !KEEP) gt = in.get(2, i);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float n = y.get(e) * r, dw = d.get(e) * w[i * V + e];
-                float gv = 1.0f;
-                if constexpr (GATE == kGateFull) {
-                    gv = gt.get(e);
-                    float sl = a.b;
-                    if (a.sigmoid) {
-                        gv = sigmoid_as<T>(gv);
-                        sl *= gv * (1.0f - gv);
-                    }
-                    q.set(e, sl * dw * n);
+            for (int e = 0; e < NP; ++e) {
+                const float2 n = mul2(y.pair(e), both(r));
+                float2 dw = mul2(d.pair(e), w.v[e]);
+                if constexpr (KEEP) {
+                    const float2 s = kept[i * NP + e], sl = mul2(s, make_float2(1.0f - s.x, 1.0f - s.y));
+                    q.set_pair(e, mul2(mul2(sl, mul2(dw, n)), both(a.b)));
+                    dw = mul2(dw, s);
+                } else if constexpr (FULL) {
+                    q.set_pair(e, mul2(mul2(dw, n), both(a.b)));
+                    dw = mul2(dw, gt.pair(e));
                 }
-                o.set(e, scale * fmaf(-n, m, dw * gv));
-                p.set(e, a.a * d.get(e));
+                o.set_pair(e, mul2(scale, fma2(n, m, dw)));
+                p.set_pair(e, mul2(both(a.a), d.pair(e)));
             }
             const int64_t at = static_cast<int64_t>(v) * V;
             o.store(dy + at);
             if (a.dres) p.store(static_cast<T*>(a.dres) + t * a.H + at);
-            if constexpr (GATE == kGateFull)
+            if constexpr (FULL)
                 if (a.dgate) q.store(static_cast<T*>(a.dgate) + t * a.H + at);
         }
     }
     in.finish();
-    write_partial<V, NV>(acc, reinterpret_cast<float*>(norm_smem), g, R, nvec,
+    write_partial<V, NV>(acc, GATE == kGateChannel ? 1.0f : a.b, reinterpret_cast<float*>(norm_smem), g, R, nvec,
                          a.partial + static_cast<int64_t>(blockIdx.x) * a.H);
 }
 #undef MOE_NORM_PROLOGUE
@@ -540,7 +605,7 @@ inline int norm_group(int nvec, int NV) {
     return (need + 31) / 32 * 32;
 }
 
-constexpr int kRingBytes = 196 * 1024;   // of a CTA's rings (one CTA per SM)
+constexpr int kRingBytes = 222 * 1024;   // of a CTA's weights and rings (one CTA per SM)
 constexpr int kRingMostDepth = 4;
 
 // What an instance remembers per device: that its shared-memory limit is set, and the CTAs per SM by
@@ -550,24 +615,25 @@ struct NormInstance {
     std::atomic<int> occupancy[kNormThreads / 32 + 1] = {};
 };
 
-// One kernel instance.  Rows in registers: CTAs of R row groups (about 256 threads forward, as many
-// as fit backward, so that few partial sums leave the SM), as many CTAs as are resident at
-// once.  Rows in a ring: one CTA of up to kNormThreads per SM.  *ctas: partial rows.
+// One kernel instance, with CTAs of as many row groups as `threads` holds.  Rows in registers: as many
+// CTAs as are resident at once, backward one per SM (few partial sums).  Rows in a ring: one
+// CTA per SM.  *ctas: partial rows.
 template <class K>
-cudaError_t launch_norm(K kernel, NormArgs a, bool backward, int ring_inputs, int esize, int sms, cudaStream_t stream,
-                        int* ctas, NormInstance* inst) {
-    int R = (backward || ring_inputs ? kNormThreads : 256) / a.G;
+cudaError_t launch_norm(K kernel, NormArgs a, int threads, bool backward, int ring_inputs, int esize, int sms,
+                        cudaStream_t stream, int* ctas, NormInstance* inst) {
+    int R = threads / a.G;
     if (R < 1) R = 1;
-    if (R > 8) R = 8;
+    if (R > kNormGroups) R = kNormGroups;
     // sums over groups (two or more: at most 256 threads and 8192 columns each, so at most 32 KB)
     size_t smem = backward && R > 1 ? static_cast<size_t>(a.H) * 4 : 0;
     int occ = 1;
     if (ring_inputs) {
-        const int row = ring_inputs * a.H * esize;
-        while (R > 1 && 2 * R * row > kRingBytes) --R;
-        a.depth = kRingBytes / (R * row);
+        const int row = ring_inputs * a.H * esize, rings = kRingBytes - a.H * 4;
+        while (R > 1 && 2 * R * row > rings) --R;
+        a.depth = rings / (R * row);
         if (a.depth > kRingMostDepth) a.depth = kRingMostDepth;
-        const size_t ring = static_cast<size_t>(R) * a.depth * row + (R * a.depth + 1) * 8;
+        const size_t ring = static_cast<size_t>(a.H) * 4 + static_cast<size_t>(R) * a.depth * row +
+                            (R * a.depth + 1) * 8;
         if (ring > smem) smem = ring;
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
@@ -601,8 +667,9 @@ cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_
 #define MOE_NORM(INPUTS, BACKWARD, ...)                                                                          \
     do {                                                                                                         \
         static NormInstance inst;                                                                                \
-        return launch_norm(__VA_ARGS__, a, BACKWARD, RING ? INPUTS : 0, static_cast<int>(sizeof(T)), sms, stream, \
-                           ctas, &inst);                                                                         \
+        return launch_norm(__VA_ARGS__, a,                                                                       \
+                           BACKWARD ? kNormThreads : !RING ? 256 : next ? kNormThreads : kNormWideThreads,       \
+                           BACKWARD, RING ? INPUTS : 0, static_cast<int>(sizeof(T)), sms, stream, ctas, &inst);  \
     } while (0)
     switch (which) {
         case kPreForward: MOE_NORM(1, false, pre_norm_kernel<T, V, NV, Rows>);
@@ -618,11 +685,16 @@ cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_
                 if (next) MOE_NORM(3, false, post_norm_kernel<T, V, NV, kGateFull, true, Rows>);
                 MOE_NORM(3, false, post_norm_kernel<T, V, NV, kGateFull, false, Rows>);
             }
+            if (gate == kGateFullSigmoid) {
+                if (next) MOE_NORM(3, false, post_norm_kernel<T, V, NV, kGateFullSigmoid, true, Rows>);
+                MOE_NORM(3, false, post_norm_kernel<T, V, NV, kGateFullSigmoid, false, Rows>);
+            }
             if (next) MOE_NORM(2, false, post_norm_kernel<T, V, NV, kGateRow, true, Rows>);
             MOE_NORM(2, false, post_norm_kernel<T, V, NV, kGateRow, false, Rows>);
         default:
             if (gate == kGateChannel) MOE_NORM(2, true, post_norm_backward_kernel<T, V, NV, kGateChannel, Rows>);
             if (gate == kGateFull) MOE_NORM(3, true, post_norm_backward_kernel<T, V, NV, kGateFull, Rows>);
+            if (gate == kGateFullSigmoid) MOE_NORM(3, true, post_norm_backward_kernel<T, V, NV, kGateFullSigmoid, Rows>);
             MOE_NORM(2, true, post_norm_backward_kernel<T, V, NV, kGateRow, Rows>);
     }
 #undef MOE_NORM
@@ -631,7 +703,8 @@ cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_
 // V elements per vector: 16 bytes where rows and addresses allow it, else one element.
 //   16 bytes, fewer rows than twice the SMs: registers, 16 elements per thread where the row then
 //     fits a CTA's threads (more threads on each row)
-//   16 bytes: the ring, 32 elements per thread (registers where two rows do not fit the ring: fp32)
+//   16 bytes: the ring, 32 elements per thread (registers where the weights and two rows do not
+//     fit a CTA's shared memory)
 //   one element: registers, 8 or 32 elements per thread
 template <class T>
 cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, int sms, cudaStream_t stream,
@@ -643,11 +716,10 @@ cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, 
     }
     if (a.T < 2 * sms && a.H <= 16 * kNormThreads)
         return launch_norm_nv<T, W, 16 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
-    if constexpr (sizeof(T) == 4) {
-        const int inputs = which == kPreForward ? 1 : which == kPreBackward ? (a.res ? 3 : 2) : gate == kGateFull ? 3 : 2;
-        if (2 * inputs * a.H * 4 > kRingBytes)
-            return launch_norm_nv<T, W, 32 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
-    }
+    const int inputs = which == kPreForward ? 1 : which == kPreBackward ? (a.res ? 3 : 2) : full_gate(gate) ? 3 : 2;
+    const int column = 4 + 2 * inputs * static_cast<int>(sizeof(T));   // bytes: the weights, two rows
+    if (static_cast<int64_t>(column) * a.H > kRingBytes)
+        return launch_norm_nv<T, W, 32 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
     return launch_norm_nv<T, W, 32 / W, RowRing, true>(a, which, gate, sms, stream, ctas);
 }
 

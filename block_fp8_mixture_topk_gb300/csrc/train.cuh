@@ -65,7 +65,21 @@ struct Pack {
     __device__ __forceinline__ void zero() { raw = Raw{}; }
     __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
     __device__ __forceinline__ void set(int i, float v) { e[i] = from_f32<T>(v); }
+    // elements 2i and 2i + 1 (V == 1: the element and zero), for the packed fp32 arithmetic
+    static constexpr int kPairs = (V + 1) / 2;
+    __device__ __forceinline__ float2 pair(int i) const {
+        return make_float2(to_f32(e[2 * i]), V > 1 ? to_f32(e[V > 1 ? 2 * i + 1 : 0]) : 0.0f);
+    }
+    __device__ __forceinline__ void set_pair(int i, float2 v) {
+        e[2 * i] = from_f32<T>(v.x);
+        if (V > 1) e[V > 1 ? 2 * i + 1 : 0] = from_f32<T>(v.y);
+    }
 };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // ---------------------------------------------------------------- host helpers
 inline size_t dtype_bytes(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
