@@ -10,14 +10,22 @@
 //   weights' gradient  dw[e] = dc[rows of e]^T @ a[rows of e]
 // where expert e owns rows [offsets[e], offsets[e+1]).
 //
-// One persistent kernel, one CTA per SM: a TMA thread fills a ring of 64-wide K blocks, one thread
-// issues tcgen05.mma (128 x 256 x 16, two accumulators in tensor memory), eight warps drain an
-// accumulator while the next one fills.  The operands keep the caller's layout; where the
-// reduction runs along the slow axis (w of the rows' gradient, both operands of the weights'
-// gradient) the 128-byte rows of a TMA box run along the other axis and the MMA reads the tile
-// transposed (MN-major).  Rows need no padding: a tile that ends inside an expert computes rows of
-// the next and does not store them, and the weights' gradient zeroes the rows past its expert's end in
-// shared memory, for both operands, so that nothing a neighbour holds (a NaN, say) reaches it.
+// One persistent kernel on clusters of two CTAs, one CTA per SM.  An item is a 256 x 256 output tile:
+// each CTA holds 128 of its rows and stages 128 of its columns, and one thread of CTA 0 issues
+// tcgen05.mma.cta_group::2 (256 x 256 x 16), which reads both CTAs' operands and leaves each CTA its
+// 128 rows x 256 columns in its own tensor memory (two accumulators).  A 64-wide K block then
+// brings 32 KB into an SM for 512 cycles of its tensor pipe; with one CTA per 128 x 256 tile it
+// brought 48 KB and the L2-to-SM feed (about 15 TB/s over the GPU) was the bound.  A TMA thread per
+// CTA fills a ring of three 128-wide stages (one barrier wait and commit per eight MMAs), eight
+// warps per CTA drain an accumulator while the next one fills.
+//
+// The operands keep the caller's layout; where the reduction runs along the slow axis (w of the
+// rows' gradient, both operands of the weights' gradient) the 128-byte rows of a TMA box run along the
+// other axis and the MMA reads the tile transposed (MN-major).  Rows need no padding: a tile that
+// ends inside an expert computes rows of the next and does not store them.  In the weights'
+// gradient the rows are the reduction: the stage in which an expert ends is finished by a warp of each
+// CTA that zeroes the rows past the end, for both operands, so that nothing a neighbour holds (a
+// NaN, say) reaches the sum.
 #include <type_traits>
 
 #include "train.cuh"
@@ -27,15 +35,16 @@ namespace {
 
 enum Mode { kForward = 0, kForwardSilu = 1, kRows = 2, kRowsSilu = 3, kWeights = 4 };
 
-constexpr int XM = 128, XN = 256, XK = 64;         // tile; XK elements are one 128-byte swizzled row
-constexpr int X_STAGES = 4;
-constexpr int XA_TILE = XM * XK * 2, XB_TILE = XN * XK * 2;
+constexpr int XM = 256, XN = 256, XK = 64;         // item; XK elements are one 128-byte swizzled row
+constexpr int X_SUB = 2, X_SUPER = 3;              // K blocks per stage, stages
+constexpr int X_TILE = 128 * XK * 2;               // one operand's K block in one CTA
 constexpr int X_BOX = 64 * 128;                    // bytes of a transposed operand's box: 64 rows of 64 elements
-constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: tile table, 3: idle
+constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: tile table, 3: ends of experts
 constexpr int X_THREADS = (X_FIRST_EPI + X_EPI_WARPS) * 32;
 constexpr uint32_t X_TMEM = 512;
 constexpr int X_PITCH = 80;                        // bytes of a staged row of 32 elements (64 B and a pad: conflict-free)
 constexpr int X_WARP_STAGE = 32 * X_PITCH;
+constexpr int X_GROUP = 16;                        // row tiles visited together (see item_at)
 
 struct ExpertArgs {
     const int32_t* offsets;
@@ -49,13 +58,18 @@ struct ExpertArgs {
 };
 
 struct XCtl {
-    uint64_t full[X_STAGES], empty[X_STAGES], tfull[2], tempty[2], drain;
+    uint64_t full[X_SUPER];     // (CTA 0) both CTAs' operands of the stage are in place
+    uint64_t empty[X_SUPER];    // the stage's MMAs completed
+    uint64_t tail[X_SUPER];     // this CTA's loads of an expert's last stage landed (weights' gradient)
+    uint64_t tfull[2];          // the accumulators are complete
+    uint64_t tempty[2];         // (CTA 0) both CTAs' epilogue warps moved them out
+    uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
     int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
-    int tile0[MOE_MAX_EXPERTS + 1];   // first 128-row tile of each expert
+    int tile0[MOE_MAX_EXPERTS + 1];   // first 256-row tile of each expert; weights' gradient: experts by falling rows
 };
-constexpr size_t X_SMEM = 1024 + X_STAGES * (XA_TILE + XB_TILE) + X_EPI_WARPS * X_WARP_STAGE + sizeof(XCtl);
+constexpr size_t X_SMEM = 1024 + X_SUPER * X_SUB * 2 * X_TILE + X_EPI_WARPS * X_WARP_STAGE + sizeof(XCtl);
 static_assert(X_SMEM <= 232448, "more shared memory than a CTA has");
 
 // One output tile: rows [r0, r0 + nrow) of column tile n of expert e; kblocks of the reduction
@@ -72,21 +86,31 @@ __device__ __forceinline__ int64_t item_count(const ExpertArgs& a, const XCtl* c
     return static_cast<int64_t>(ctl->tile0[a.E]) * NT;
 }
 
+// The round-th item of this cluster.  Rows' products: cluster c takes items c, c + clusters, ...
+// (equal work).  Weights' gradient: the experts come by falling rows and every other round runs
+// backwards, so that no cluster always gets the longer items.
+template <int MODE>
+__device__ __forceinline__ int64_t item_of_round(int64_t round) {
+    const int64_t c = blockIdx.x >> 1, n = gridDim.x >> 1;
+    return round * n + (MODE == kWeights && (round & 1) ? n - 1 - c : c);
+}
+
 template <int MODE>
 __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, int64_t w, int NT) {
     XItem t;
     if (MODE == kWeights) {
         const int MT = (a.N + XM - 1) / XM, per = MT * NT;
-        t.e = static_cast<int>(w / per);
-        const int local = static_cast<int>(w - static_cast<int64_t>(t.e) * per);
+        const int k = static_cast<int>(w / per);
+        t.e = ctl->tile0[k];
+        const int local = static_cast<int>(w - static_cast<int64_t>(k) * per);
         const int m = local % MT;
         t.n = local / MT;
         t.r0 = m * XM;
         t.nrow = a.N - m * XM < XM ? a.N - m * XM : XM;
         t.red = ctl->row0[t.e + 1] - ctl->row0[t.e];
     } else {
-        // the expert whose tiles hold tile w / NT; its row tiles run fastest, so that neighbouring
-        // CTAs read the same columns of its weights
+        // the expert whose tiles hold tile w / NT; within it X_GROUP row tiles by all column tiles, row
+        // tiles fastest, so that the items under way at one time share rows and weights in L2
         const int g = static_cast<int>(w / NT);
         int lo = 0, hi = a.E - 1;
         while (lo < hi) {
@@ -96,9 +120,12 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
         }
         t.e = lo;
         const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo];
-        const int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
-        const int m = local % mt;
-        t.n = local / mt;
+        int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
+        const int grp = local / (X_GROUP * NT);
+        local -= grp * X_GROUP * NT;
+        const int gm = mt - grp * X_GROUP < X_GROUP ? mt - grp * X_GROUP : X_GROUP;
+        const int m = grp * X_GROUP + local % gm;
+        t.n = local / gm;
         const int cnt = ctl->row0[lo + 1] - ctl->row0[lo];
         t.r0 = ctl->row0[lo] + m * XM;
         t.nrow = cnt - m * XM < XM ? cnt - m * XM : XM;
@@ -130,18 +157,90 @@ __host__ __device__ constexpr uint32_t idesc_16bit(int n, bool a_mn, bool b_mn) 
            | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(XM >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 128 x N x 16, 16-bit operands, fp32 accumulation.
-__device__ __forceinline__ void mma_16bit(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// TMA tile loads into this CTA's shared memory whose bytes complete on `bar`, a shared::cluster
+// address that may be the other CTA's barrier (the .cta_group::2 form).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                                 int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Arrive on a barrier of either CTA of the pair (shared::cluster address).  CTA-scope release, like
+// the waits (mbar_wait): the arrivals hand over tensor memory (ordered by the tcgen05 fences around
+// the barrier) and shared-memory stages (written by TMA, completion counted on the barrier), never
+// data the arriving thread wrote itself; a cluster-scope release made every arrival of the
+// epilogue warps wait for their earlier global stores.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// All threads of both CTAs.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrive once on the barrier at this offset in each CTA of `mask` when the MMAs issued so far complete.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
+}
+
+// D (256 x N over both CTAs) (+)= A * B^T, K = 16, 16-bit operands, fp32 accumulation; issued by one
+// thread of CTA 0.
+__device__ __forceinline__ void mma_16bit_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Arrive on a barrier of either CTA, releasing this thread's writes to the cluster.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Acquire at cluster scope what the arrivals on a completed phase released.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(parity)
+        : "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -219,26 +318,28 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint8_t* smA = base;
-    uint8_t* smB = base + X_STAGES * XA_TILE;
-    uint8_t* smE = smB + X_STAGES * XB_TILE;
+    uint8_t* smA = base;                                   // [X_SUPER][X_SUB][X_TILE]
+    uint8_t* smB = base + X_SUPER * X_SUB * X_TILE;        // likewise
+    uint8_t* smE = smB + X_SUPER * X_SUB * X_TILE;
     XCtl* ctl = reinterpret_cast<XCtl*>(smE + X_EPI_WARPS * X_WARP_STAGE);
     constexpr bool A_MN = MODE == kWeights;
     constexpr bool B_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
     constexpr bool SILU = MODE == kForwardSilu;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_rank());
     const int OC = MODE == kForward ? a.N : SILU ? a.N / 2 : a.K;   // output columns (of h, for kForwardSilu)
     const int NT = SILU ? (OC + 127) / 128 : (OC + XN - 1) / XN;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < X_STAGES; ++s) {
-            mbar_init(smem_addr(&ctl->full[s]), 1);
+        for (int s = 0; s < X_SUPER; ++s) {
+            mbar_init(smem_addr(&ctl->full[s]), MODE == kWeights ? 2 : 1);
             mbar_init(smem_addr(&ctl->empty[s]), 1);
+            mbar_init(smem_addr(&ctl->tail[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&ctl->tfull[b]), 1);
-            mbar_init(smem_addr(&ctl->tempty[b]), X_EPI_WARPS);
+            mbar_init(smem_addr(&ctl->tempty[b]), 2 * X_EPI_WARPS);
         }
         mbar_init(smem_addr(&ctl->drain), 1);
         ctl->abort_flag = 0;
@@ -249,8 +350,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         tma_prefetch_map(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc(smem_addr(&ctl->tmem_base), X_TMEM);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_addr(&ctl->tmem_base), X_TMEM);
+        tmem_relinquish_pair();
     }
     grid_dependency_wait();
     // the experts' rows: offsets that leave [0, rows] or run backwards are clamped and reported
@@ -264,7 +365,17 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         ctl->row0[e] = static_cast<int>(o);
     }
     __syncthreads();
-    if (warp == 2) {
+    if (MODE == kWeights) {
+        for (int e = threadIdx.x; e < a.E; e += X_THREADS) {
+            const int n = ctl->row0[e + 1] - ctl->row0[e];
+            int place = 0;   // experts with more rows, or as many and a lower index
+            for (int o = 0; o < a.E; ++o) {
+                const int m = ctl->row0[o + 1] - ctl->row0[o];
+                place += m > n || (m == n && o < e);
+            }
+            ctl->tile0[place] = e;
+        }
+    } else if (warp == 2) {
         int carry = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
@@ -283,117 +394,164 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    cluster_barrier();   // both CTAs' barriers are initialised before any arrival from the other
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort_flag = &ctl->abort_flag;
     const int64_t total = item_count<MODE>(a, ctl, NT);
+    const int64_t rounds = (total + (gridDim.x >> 1) - 1) / (gridDim.x >> 1);
 
     if (warp == 0) {
         if (lane == 0) {
-            // ------------------------------------------------------------ TMA
+            // ------------------------------------------------------------ TMA (both CTAs)
             int stage = 0;
             uint32_t phase = 0, issued = 0;
             bool ok = true;
-            for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
+            for (int64_t round = 0; round < rounds && ok; ++round) {
+                const int64_t w = item_of_round<MODE>(round);
+                if (w >= total) continue;
                 const XItem t = item_at<MODE>(a, ctl, w, NT);
-                const int c0 = SILU ? t.n * 128 : t.n * XN;
-                for (int kb = 0; kb < t.kblocks; ++kb) {
+                const int c0 = SILU ? t.n * 128 + rank * OC : t.n * XN + rank * 128;   // this CTA's columns
+                const int32_t r0 = static_cast<int32_t>(t.r0) + rank * 128;            // and rows
+                // a CTA without rows computes on whatever its stage holds, and stores nothing
+                const bool second = MODE == kWeights || t.nrow > 128;
+                const bool load_a = rank == 0 || second;
+                for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
+                    const int nsub = t.kblocks - kb0 < X_SUB ? t.kblocks - kb0 : X_SUB;
                     if (!mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = smem_addr(&ctl->full[stage]);
-                    const uint32_t sa = smem_addr(smA + stage * XA_TILE), sb = smem_addr(smB + stage * XB_TILE);
-                    mbar_arrive_expect_tx(fb, XA_TILE + XB_TILE);
-                    if (MODE == kWeights) {
-                        // 64 rows of the expert: 128 columns of dc, 256 of a, in boxes of 64
-                        const int32_t r = ctl->row0[t.e] + kb * XK;
+                    const bool tail = MODE == kWeights && t.red - kb0 * XK < X_SUB * XK;
+                    const uint32_t full0 = cluster_map(smem_addr(&ctl->full[stage]), 0);
+                    const uint32_t bar = tail ? smem_addr(&ctl->tail[stage]) : full0;
+                    if (tail) mbar_arrive_expect_tx(bar, nsub * 2 * X_TILE);
+                    else if (rank == 0) mbar_arrive_expect_tx(smem_addr(&ctl->full[stage]), nsub * (second ? 4 : 3) * X_TILE);
+                    else if (MODE == kWeights) mbar_arrive_cluster(full0);
+                    for (int j = 0; j < nsub; ++j) {
+                        const int kb = kb0 + j;
+                        const uint32_t sa = smem_addr(smA + (stage * X_SUB + j) * X_TILE);
+                        const uint32_t sb = smem_addr(smB + (stage * X_SUB + j) * X_TILE);
+                        if (MODE == kWeights) {
+                            // 64 rows of the expert, 128 columns of dc and of a
+                            const int32_t r = ctl->row0[t.e] + kb * XK;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            tma_load_2d(sa + i * X_BOX, &tmA, (static_cast<int32_t>(t.r0) + i * 64) * 2, r, fb);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) tma_load_2d(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, r, fb);
-                    } else {
-                        tma_load_2d(sa, &tmA, kb * XK * 2, static_cast<int32_t>(t.r0), fb);
-                        if (B_MN) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                tma_load_3d(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, kb * XK, t.e, fb);
+                            for (int i = 0; i < 2; ++i) {
+                                if (tail) {
+                                    tma_load_2d(sa + i * X_BOX, &tmA, (r0 + i * 64) * 2, r, bar);
+                                    tma_load_2d(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, r, bar);
+                                } else {
+                                    tma_load_2d_pair(sa + i * X_BOX, &tmA, (r0 + i * 64) * 2, r, bar);
+                                    tma_load_2d_pair(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, r, bar);
+                                }
+                            }
                         } else {
-                            tma_load_3d(sb, &tmB, kb * XK * 2, c0, t.e, fb);
-                            tma_load_3d(sb + XB_TILE / 2, &tmB, kb * XK * 2, SILU ? OC + c0 : c0 + 128, t.e, fb);
+                            if (load_a) tma_load_2d_pair(sa, &tmA, kb * XK * 2, r0, bar);
+                            if (B_MN) {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    tma_load_3d_pair(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, kb * XK, t.e, bar);
+                            } else {
+                                tma_load_3d_pair(sb, &tmB, kb * XK * 2, c0, t.e, bar);
+                            }
                         }
                     }
                     ++issued;
-                    if (++stage == X_STAGES) {
+                    if (++stage == X_SUPER) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok) {
-                // let every load already issued land before the CTA exits
-                for (int s = 0; s < X_STAGES; ++s) {
-                    const uint32_t n_s = (issued + X_STAGES - 1 - s) / X_STAGES;
+            // after an abort CTA 0 lets the loads of the stages it armed land, both CTAs' bytes; CTA 1,
+            // which cannot see its loads' completion, waits for CTA 0 at the closing cluster barrier
+            if (!ok && rank == 0) {
+                for (int s = 0; s < X_SUPER; ++s) {
+                    const uint32_t n_s = (issued + X_SUPER - 1 - s) / X_SUPER;
                     if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
                 }
             }
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------------------- MMA
-        const uint32_t idesc = idesc_16bit<T>(XN, A_MN, B_MN);
-        int stage = 0;
-        uint32_t phase = 0, buf = 0, bphase = 0;
-        bool ok = true;
-        for (int64_t w = blockIdx.x; w < total && ok; w += gridDim.x) {
-            const XItem t = item_at<MODE>(a, ctl, w, NT);
-            if (t.kblocks == 0) continue;
-            const uint32_t d = tmem + buf * XN;
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
-            for (int kb = 0; kb < t.kblocks && ok; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
-                if (!ok) break;
-                tc_fence_after();
-                int steps = XK / 16;
-                if (MODE == kWeights && t.red - kb * XK < XK) {
-                    // the expert ends in this block: only the 16-row steps that hold its rows, the
-                    // rest of the last step zeroed
-                    const int live = t.red - kb * XK;
-                    steps = (live + 15) / 16;
-                    const int pieces = (steps * 16 - live) * 8;   // 16-byte pieces of one box
-                    for (int i = lane; i < pieces * 6; i += 32) {
-                        const int box = i / pieces, p = i - box * pieces;
-                        uint8_t* at = box < 2 ? smA + stage * XA_TILE + box * X_BOX
-                                              : smB + stage * XB_TILE + (box - 2) * X_BOX;
-                        *reinterpret_cast<uint4*>(at + live * 128 + p * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_proxy();
-                    __syncwarp();
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------------------ MMA (CTA 0)
+            const uint32_t idesc = idesc_16bit<T>(XN, A_MN, B_MN);
+            int stage = 0;
+            uint32_t phase = 0, buf = 0, bphase = 0;
+            bool ok = true;
+            for (int64_t round = 0; round < rounds && ok; ++round) {
+                const int64_t w = item_of_round<MODE>(round);
+                if (w >= total) continue;
+                const XItem t = item_at<MODE>(a, ctl, w, NT);
+                if (t.kblocks == 0) continue;
+                if (!mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status)) {
+                    ok = false;
+                    break;
                 }
-                if (lane == 0) {
-                    const uint32_t a0 = smem_addr(smA + stage * XA_TILE);
-                    const uint32_t b0 = smem_addr(smB + stage * XB_TILE);
+                const uint32_t d = tmem + buf * XN;
+                for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
+                    if (!mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status)) {
+                        ok = false;
+                        break;
+                    }
+                    const int left = t.red - kb0 * XK;
+                    int steps = left >= X_SUB * XK ? X_SUB * XK / 16 : (left + 15) / 16;
+                    if (MODE == kWeights && left < X_SUB * XK) mbar_acquire_cluster(smem_addr(&ctl->full[stage]), phase);
+                    tc_fence_after();
+                    const uint32_t a0 = smem_addr(smA + stage * X_SUB * X_TILE);
+                    const uint32_t b0 = smem_addr(smB + stage * X_SUB * X_TILE);
                     for (int k = 0; k < steps; ++k) {
-                        const uint64_t ad = A_MN ? smem_desc_mn_sw128(a0 + k * 2048) : smem_desc_k128_sw128(a0 + k * 32);
-                        const uint64_t bd = B_MN ? smem_desc_mn_sw128(b0 + k * 2048) : smem_desc_k128_sw128(b0 + k * 32);
-                        mma_16bit(d, ad, bd, idesc, (kb | k) > 0 ? 1u : 0u);
+                        const uint32_t sub = (k >> 2) * X_TILE, kk = k & 3;
+                        const uint64_t ad = A_MN ? smem_desc_mn_sw128(a0 + sub + kk * 2048)
+                                                 : smem_desc_k128_sw128(a0 + sub + kk * 32);
+                        const uint64_t bd = B_MN ? smem_desc_mn_sw128(b0 + sub + kk * 2048)
+                                                 : smem_desc_k128_sw128(b0 + sub + kk * 32);
+                        mma_16bit_pair(d, ad, bd, idesc, (kb0 | k) > 0 ? 1u : 0u);
                     }
-                    mma_commit(smem_addr(&ctl->empty[stage]));
-                    if (kb + 1 == t.kblocks) mma_commit(smem_addr(&ctl->tfull[buf]));
+                    mma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
+                    if (++stage == X_SUPER) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                __syncwarp();
-                if (++stage == X_STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (!ok) break;
+                mma_commit_pair(smem_addr(&ctl->tfull[buf]), 3);
+                buf ^= 1u;
+                if (buf == 0) bphase ^= 1u;
             }
-            buf ^= 1u;
-            if (buf == 0) bphase ^= 1u;
-        }
-        if (!ok && lane == 0) {
-            mma_commit(smem_addr(&ctl->drain));
+            // every MMA complete before the CTAs can leave (they read both CTAs' shared memory)
+            mma_commit_pair(smem_addr(&ctl->drain), 1);
             mbar_wait(smem_addr(&ctl->drain), 0, nullptr, a.status);
+        }
+    } else if (warp == 3 && MODE == kWeights) {
+        // ---------------------------------------------------------------- ends of experts (both CTAs)
+        int stage = 0;
+        uint32_t tails = 0;   // bit s: parity of stage s's tail barrier
+        bool ok = true;
+        for (int64_t round = 0; round < rounds && ok; ++round) {
+            const int64_t w = item_of_round<MODE>(round);
+            if (w >= total) continue;
+            const XItem t = item_at<MODE>(a, ctl, w, NT);
+            const int stages = (t.kblocks + X_SUB - 1) / X_SUB;
+            if (stages == 0) continue;
+            const int live = t.red - (stages - 1) * X_SUB * XK;   // rows of the last stage, 1 .. 128
+            const int last = (stage + stages - 1) % X_SUPER;
+            stage = (last + 1) % X_SUPER;
+            if (live == X_SUB * XK) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tail[last]), (tails >> last) & 1u, abort_flag, a.status));
+            if (!ok) break;
+            tails ^= 1u << last;
+            // the MMAs run in steps of 16 rows: the rest of the last step's rows, in this CTA's four boxes
+            const int sub = (live - 1) / XK, row = live - sub * XK;
+            const int pieces = ((row + 15) / 16 * 16 - row) * 8;   // 16-byte pieces of a box
+            uint8_t* at = smA + (last * X_SUB + sub) * X_TILE + row * 128;
+            for (int i = lane; i < pieces * 4; i += 32) {
+                const int box = i / pieces, p = i - box * pieces;
+                *reinterpret_cast<uint4*>(at + (box & 1) * X_BOX + (box >> 1) * (smB - smA) + p * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release_cluster(cluster_map(smem_addr(&ctl->full[last]), 0));
         }
     } else if (warp >= X_FIRST_EPI) {
         // ---------------------------------------------------------------- epilogue
@@ -404,10 +562,13 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         T* out = static_cast<T*>(a.out);
         uint32_t buf = 0, bphase = 0;
         bool ok = true;
-        for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+        const uint32_t tempty0 = cluster_map(smem_addr(&ctl->tempty[0]), 0), tempty1 = cluster_map(smem_addr(&ctl->tempty[1]), 0);
+        for (int64_t round = 0; round < rounds; ++round) {
+            const int64_t w = item_of_round<MODE>(round);
+            if (w >= total) continue;
             const XItem t = item_at<MODE>(a, ctl, w, NT);
-            const int64_t r0 = t.r0 + sp * 32 + (MODE == kWeights ? static_cast<int64_t>(t.e) * a.N : 0);
-            const int nrow = t.nrow - sp * 32;
+            const int64_t r0 = t.r0 + rank * 128 + sp * 32 + (MODE == kWeights ? static_cast<int64_t>(t.e) * a.N : 0);
+            const int nrow = t.nrow - rank * 128 - sp * 32;   // this warp's rows (none: <= 0)
             const int c0 = SILU ? t.n * 128 : t.n * XN;
             if (MODE == kWeights && t.kblocks == 0) {   // an expert without rows: zero
                 float z[32];
@@ -434,7 +595,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                 if (j == 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&ctl->tempty[buf]));
+                    if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
                 }
                 if (nrow <= 0) continue;
                 if (SILU) {
@@ -488,13 +649,12 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         }
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_barrier();   // no CTA leaves while the other's MMAs, loads or arrivals may still reach it
     tc_fence_after();
-    if (warp == 1) {
-        __syncwarp();
-        tmem_dealloc(tmem, X_TMEM);
-    }
+    if (warp == 1) tmem_dealloc_pair(tmem, X_TMEM);
 }
 
 // Tensor map of 16-bit rows [n1, n0] (n2 of them; 0: two dimensions), boxes of 64 elements by box1
@@ -506,12 +666,32 @@ cudaError_t map_16bit(CUtensorMap* map, const void* p, int64_t n0, int64_t ld, i
     return encode_u8_map_nd(map, static_cast<const uint8_t*>(p), n2 > 0 ? 3 : 2, dims, strides, box, true);
 }
 
+int g_clusters = 0;   // clusters of two CTAs resident at once (the same for every instance: one CTA per SM)
+
+void pair_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned clusters, cudaStream_t stream) {
+    *cfg = {};
+    cfg->gridDim = dim3(2 * clusters);
+    cfg->blockDim = dim3(X_THREADS);
+    cfg->dynamicSmemBytes = X_SMEM;
+    cfg->stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+}
+
 template <class T, int MODE>
 cudaError_t launch_experts(const ExpertArgs& a, const CUtensorMap& tmA, const CUtensorMap& tmB, int64_t most_items,
                            cudaStream_t stream) {
-    const int sms = device_sms();
-    const unsigned grid = static_cast<unsigned>(most_items < sms ? most_items : sms);
-    return launch_pdl(expert_gemm_kernel<T, MODE>, dim3(grid), dim3(X_THREADS), X_SMEM, stream, tmA, tmB, a);
+    if (g_clusters < 1) return cudaErrorNotSupported;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    pair_config(&cfg, attr, static_cast<unsigned>(most_items < g_clusters ? most_items : g_clusters), stream);
+    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<T, MODE>, tmA, tmB, a);
 }
 
 template <int MODE>
@@ -552,8 +732,20 @@ bool on_16(const void* p) { return (address(p) & 15) == 0; }
 }  // namespace
 
 cudaError_t experts_init_device() {
-    const cudaError_t e = set_smem_all<__nv_bfloat16>();
-    return e == cudaSuccess ? set_smem_all<__half>() : e;
+    cudaError_t e = set_smem_all<__nv_bfloat16>();
+    if (e == cudaSuccess) e = set_smem_all<__half>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    pair_config(&cfg, attr, 1, nullptr);
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, expert_gemm_kernel<__nv_bfloat16, kForward>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+    }
+    g_clusters = n;
+    return cudaSuccess;
 }
 
 }  // namespace mfp8
@@ -575,7 +767,7 @@ int moe_expert_gemm(const void* rows_a, int64_t lda, int dtype, const void* w, c
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     CUtensorMap tmA, tmB;
-    if (map_16bit(&tmA, rows_a, K, lda, num_rows, 0, XM) != cudaSuccess ||
+    if (map_16bit(&tmA, rows_a, K, lda, num_rows, 0, 128) != cudaSuccess ||
         map_16bit(&tmB, w, K, K, N, E, 128) != cudaSuccess)
         return MOE_ERR_CUDA;
     const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, gate_up, 0, status};
@@ -599,7 +791,7 @@ int moe_expert_gemm_dgrad(const void* dc, int64_t lddc, int dtype, const void* w
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     CUtensorMap tmA, tmB;
-    if (map_16bit(&tmA, dc, N, lddc, num_rows, 0, XM) != cudaSuccess ||
+    if (map_16bit(&tmA, dc, N, lddc, num_rows, 0, 128) != cudaSuccess ||
         map_16bit(&tmB, w, K, K, N, E, XK) != cudaSuccess)
         return MOE_ERR_CUDA;
     const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, const_cast<void*>(gate_up), ldgu, status};
