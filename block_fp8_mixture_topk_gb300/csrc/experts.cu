@@ -135,6 +135,18 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
     return t;
 }
 
+// The same item, in values the compiler knows to be the same in every lane.
+__device__ __forceinline__ XItem uniform(const XItem& t) {
+    XItem u;
+    u.e = __shfl_sync(0xffffffffu, t.e, 0);
+    u.n = __shfl_sync(0xffffffffu, t.n, 0);
+    u.kblocks = __shfl_sync(0xffffffffu, t.kblocks, 0);
+    u.red = __shfl_sync(0xffffffffu, t.red, 0);
+    u.r0 = __shfl_sync(0xffffffffu, t.r0, 0);
+    u.nrow = __shfl_sync(0xffffffffu, t.nrow, 0);
+    return u;
+}
+
 // Descriptor of a tile read transposed: 64-element rows of 128 bytes along M or N (swizzled, as
 // TMA writes them), one per reduction index; 8 of them (1024 bytes) to a group, the next 64
 // elements of M or N one box further.
@@ -232,6 +244,14 @@ __device__ __forceinline__ void mma_16bit_pair(uint32_t d_tmem, uint64_t adesc, 
 __device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// One lane of a converged warp, the same every time.  The TMA and MMA warps run their loops as whole
+// warps on warp-uniform values and elect the issuing lane, so that the tensor instructions' operands stay
+// in uniform registers (with one thread in the loop each MMA cost it about 70 cycles).
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
 // Acquire at cluster scope what the arrivals on a completed phase released.
 __device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
     asm volatile(
@@ -326,7 +346,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     constexpr bool B_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
     constexpr bool SILU = MODE == kForwardSilu;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
     const int OC = MODE == kForward ? a.N : SILU ? a.N / 2 : a.K;   // output columns (of h, for kForwardSilu)
     const int NT = SILU ? (OC + 127) / 128 : (OC + XN - 1) / XN;
@@ -402,39 +422,39 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     const int64_t rounds = (total + (gridDim.x >> 1) - 1) / (gridDim.x >> 1);
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ TMA (both CTAs)
-            int stage = 0;
-            uint32_t phase = 0, issued = 0;
-            bool ok = true;
-            for (int64_t round = 0; round < rounds && ok; ++round) {
-                const int64_t w = item_of_round<MODE>(round);
-                if (w >= total) continue;
-                const XItem t = item_at<MODE>(a, ctl, w, NT);
-                const int c0 = SILU ? t.n * 128 + rank * OC : t.n * XN + rank * 128;   // this CTA's columns
-                const int32_t r0 = static_cast<int32_t>(t.r0) + rank * 128;            // and rows
-                // a CTA without rows computes on whatever its stage holds, and stores nothing
-                const bool second = MODE == kWeights || t.nrow > 128;
-                const bool load_a = rank == 0 || second;
-                for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
-                    const int nsub = t.kblocks - kb0 < X_SUB ? t.kblocks - kb0 : X_SUB;
-                    if (!mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool tail = MODE == kWeights && t.red - kb0 * XK < X_SUB * XK;
-                    const uint32_t full0 = cluster_map(smem_addr(&ctl->full[stage]), 0);
-                    const uint32_t bar = tail ? smem_addr(&ctl->tail[stage]) : full0;
+        // ---------------------------------------------------------------- TMA (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true;
+        const uint32_t smA0 = smem_addr(smA), smB0 = smem_addr(smB);
+        const uint32_t full = smem_addr(&ctl->full[0]), full0 = cluster_map(full, 0);
+        for (int64_t round = 0; round < rounds && ok; ++round) {
+            const int64_t w = item_of_round<MODE>(round);
+            if (w >= total) continue;
+            const XItem t = uniform(item_at<MODE>(a, ctl, w, NT));
+            const int c0 = SILU ? t.n * 128 + rank * OC : t.n * XN + rank * 128;   // this CTA's columns
+            const int32_t r0 = static_cast<int32_t>(t.r0) + rank * 128;            // and rows
+            // a CTA without rows computes on whatever its stage holds, and stores nothing
+            const bool second = MODE == kWeights || t.nrow > 128;
+            const bool load_a = rank == 0 || second;
+            const int32_t first = MODE == kWeights ? ctl->row0[t.e] : 0;
+            for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
+                const int nsub = t.kblocks - kb0 < X_SUB ? t.kblocks - kb0 : X_SUB;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status));
+                if (!ok) break;
+                const bool tail = MODE == kWeights && t.red - kb0 * XK < X_SUB * XK;
+                const uint32_t bar = tail ? smem_addr(&ctl->tail[stage]) : full0 + stage * 8;
+                if (elect_lane()) {
                     if (tail) mbar_arrive_expect_tx(bar, nsub * 2 * X_TILE);
-                    else if (rank == 0) mbar_arrive_expect_tx(smem_addr(&ctl->full[stage]), nsub * (second ? 4 : 3) * X_TILE);
-                    else if (MODE == kWeights) mbar_arrive_cluster(full0);
+                    else if (rank == 0) mbar_arrive_expect_tx(full + stage * 8, nsub * (second ? 4 : 3) * X_TILE);
+                    else if (MODE == kWeights) mbar_arrive_cluster(bar);
                     for (int j = 0; j < nsub; ++j) {
                         const int kb = kb0 + j;
-                        const uint32_t sa = smem_addr(smA + (stage * X_SUB + j) * X_TILE);
-                        const uint32_t sb = smem_addr(smB + (stage * X_SUB + j) * X_TILE);
+                        const uint32_t sa = smA0 + (stage * X_SUB + j) * X_TILE;
+                        const uint32_t sb = smB0 + (stage * X_SUB + j) * X_TILE;
                         if (MODE == kWeights) {
                             // 64 rows of the expert, 128 columns of dc and of a
-                            const int32_t r = ctl->row0[t.e] + kb * XK;
+                            const int32_t r = first + kb * XK;
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 if (tail) {
@@ -456,72 +476,81 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                             }
                         }
                     }
-                    ++issued;
-                    if (++stage == X_SUPER) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
-            }
-            // after an abort CTA 0 lets the loads of the stages it armed land, both CTAs' bytes; CTA 1,
-            // which cannot see its loads' completion, waits for CTA 0 at the closing cluster barrier
-            if (!ok && rank == 0) {
-                for (int s = 0; s < X_SUPER; ++s) {
-                    const uint32_t n_s = (issued + X_SUPER - 1 - s) / X_SUPER;
-                    if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
+                __syncwarp();
+                ++issued;
+                if (++stage == X_SUPER) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
         }
+        // after an abort CTA 0 lets the loads of the stages it armed land, both CTAs' bytes; CTA 1, which
+        // cannot see its loads' completion, waits for CTA 0 at the closing cluster barrier
+        if (!ok && rank == 0 && lane == 0) {
+            for (int s = 0; s < X_SUPER; ++s) {
+                const uint32_t n_s = (issued + X_SUPER - 1 - s) / X_SUPER;
+                if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
+            }
+        }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ------------------------------------------------------------ MMA (CTA 0)
-            const uint32_t idesc = idesc_16bit<T>(XN, A_MN, B_MN);
+            constexpr uint32_t idesc = idesc_16bit<T>(XN, A_MN, B_MN);
+            const uint64_t ad0 = A_MN ? smem_desc_mn_sw128(smem_addr(smA)) : smem_desc_k128_sw128(smem_addr(smA));
+            const uint64_t bd0 = B_MN ? smem_desc_mn_sw128(smem_addr(smB)) : smem_desc_k128_sw128(smem_addr(smB));
+            constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
+            constexpr uint32_t sub_step = X_TILE >> 4, stage_step = X_SUB * X_TILE >> 4;
             int stage = 0;
             uint32_t phase = 0, buf = 0, bphase = 0;
             bool ok = true;
             for (int64_t round = 0; round < rounds && ok; ++round) {
                 const int64_t w = item_of_round<MODE>(round);
                 if (w >= total) continue;
-                const XItem t = item_at<MODE>(a, ctl, w, NT);
+                const XItem t = uniform(item_at<MODE>(a, ctl, w, NT));
                 if (t.kblocks == 0) continue;
-                if (!mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
+                if (!ok) break;
                 const uint32_t d = tmem + buf * XN;
                 for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
-                    if (!mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
+                    if (!ok) break;
                     const int left = t.red - kb0 * XK;
-                    int steps = left >= X_SUB * XK ? X_SUB * XK / 16 : (left + 15) / 16;
                     if (MODE == kWeights && left < X_SUB * XK) mbar_acquire_cluster(smem_addr(&ctl->full[stage]), phase);
                     tc_fence_after();
-                    const uint32_t a0 = smem_addr(smA + stage * X_SUB * X_TILE);
-                    const uint32_t b0 = smem_addr(smB + stage * X_SUB * X_TILE);
-                    for (int k = 0; k < steps; ++k) {
-                        const uint32_t sub = (k >> 2) * X_TILE, kk = k & 3;
-                        const uint64_t ad = A_MN ? smem_desc_mn_sw128(a0 + sub + kk * 2048)
-                                                 : smem_desc_k128_sw128(a0 + sub + kk * 32);
-                        const uint64_t bd = B_MN ? smem_desc_mn_sw128(b0 + sub + kk * 2048)
-                                                 : smem_desc_k128_sw128(b0 + sub + kk * 32);
-                        mma_16bit_pair(d, ad, bd, idesc, (kb0 | k) > 0 ? 1u : 0u);
+                    const uint64_t ad = ad0 + stage * stage_step, bd = bd0 + stage * stage_step;
+                    if (elect_lane()) {
+                        if (left >= X_SUB * XK) {
+                            mma_16bit_pair(d, ad, bd, idesc, kb0 > 0 ? 1u : 0u);
+#pragma unroll
+                            for (int k = 1; k < X_SUB * XK / 16; ++k)
+                                mma_16bit_pair(d, ad + (k >> 2) * sub_step + (k & 3) * a_step,
+                                               bd + (k >> 2) * sub_step + (k & 3) * b_step, idesc, 1u);
+                        } else {
+                            const int steps = (left + 15) / 16;
+                            for (int k = 0; k < steps; ++k)
+                                mma_16bit_pair(d, ad + (k >> 2) * sub_step + (k & 3) * a_step,
+                                               bd + (k >> 2) * sub_step + (k & 3) * b_step, idesc,
+                                               (kb0 | k) > 0 ? 1u : 0u);
+                        }
+                        mma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
+                        if (kb0 + X_SUB >= t.kblocks) mma_commit_pair(smem_addr(&ctl->tfull[buf]), 3);
                     }
-                    mma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
+                    __syncwarp();
                     if (++stage == X_SUPER) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                mma_commit_pair(smem_addr(&ctl->tfull[buf]), 3);
                 buf ^= 1u;
                 if (buf == 0) bphase ^= 1u;
             }
             // every MMA complete before the CTAs can leave (they read both CTAs' shared memory)
-            mma_commit_pair(smem_addr(&ctl->drain), 1);
-            mbar_wait(smem_addr(&ctl->drain), 0, nullptr, a.status);
+            if (elect_lane()) {
+                mma_commit_pair(smem_addr(&ctl->drain), 1);
+                mbar_wait(smem_addr(&ctl->drain), 0, nullptr, a.status);
+            }
         }
     } else if (warp == 3 && MODE == kWeights) {
         // ---------------------------------------------------------------- ends of experts (both CTAs)
