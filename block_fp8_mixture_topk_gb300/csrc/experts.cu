@@ -10,22 +10,26 @@
 //   weights' gradient  dw[e] = dc[rows of e]^T @ a[rows of e]
 // where expert e owns rows [offsets[e], offsets[e+1]).
 //
-// One persistent kernel on clusters of two CTAs, one CTA per SM.  An item is a 256 x 256 output tile:
-// each CTA holds 128 of its rows and stages 128 of its columns, and one thread of CTA 0 issues
-// tcgen05.mma.cta_group::2 (256 x 256 x 16), which reads both CTAs' operands and leaves each CTA its
-// 128 rows x 256 columns in its own tensor memory (two accumulators).  A 64-wide K block then
-// brings 32 KB into an SM for 512 cycles of its tensor pipe; with one CTA per 128 x 256 tile it
-// brought 48 KB and the L2-to-SM feed (about 15 TB/s over the GPU) was the bound.  A TMA thread per
-// CTA fills a ring of three 128-wide stages (one barrier wait and commit per eight MMAs), eight
-// warps per CTA drain an accumulator while the next one fills.
+// One persistent kernel on clusters of two CTAs, one CTA per SM.  An item is a tile of 256 x up to 256
+// outputs: one thread of CTA 0 issues tcgen05.mma.cta_group::2 (256 x N x 16), which reads both CTAs'
+// operands (128 of the 256, half of the N each) and leaves each CTA its 128 x N in its own tensor
+// memory (two accumulators).  A 64-wide K block then brings 32 KB into an SM for 512 cycles of its
+// tensor pipe.  A TMA warp per CTA fills a ring of three 128-wide stages (one barrier wait and
+// commit per eight MMAs), eight warps per CTA drain an accumulator while the next one fills.
+//
+// Products and rows' gradient: the 256 run along the output columns (the weights) and N along the
+// rows, so that the tile in which an expert ends costs its rows rounded up to 32, not to 256 (a
+// skewed router leaves most experts few rows: with rows along the 256, 19% of the multiply-adds of
+// the Qwen3-shaped batch were padding).  The accumulators then hold one output column per lane,
+// and the epilogue turns them over through shared memory.  Weights' gradient: 256 columns of dc by
+// 256 of a, the rows are the reduction.
 //
 // The operands keep the caller's layout; where the reduction runs along the slow axis (w of the
 // rows' gradient, both operands of the weights' gradient) the 128-byte rows of a TMA box run along the
 // other axis and the MMA reads the tile transposed (MN-major).  Rows need no padding: a tile that
-// ends inside an expert computes rows of the next and does not store them.  In the weights'
-// gradient the rows are the reduction: the stage in which an expert ends is finished by a warp of each
-// CTA that zeroes the rows past the end, for both operands, so that nothing a neighbour holds (a
-// NaN, say) reaches the sum.
+// ends inside an expert computes rows of the next and does not store them; in the weights' gradient
+// the stage in which an expert ends is finished by a warp of each CTA that zeroes the rows past the
+// end, for both operands, so that nothing a neighbour holds (a NaN, say) reaches the sum.
 #include <type_traits>
 
 #include "train.cuh"
@@ -43,6 +47,7 @@ constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: t
 constexpr int X_THREADS = (X_FIRST_EPI + X_EPI_WARPS) * 32;
 constexpr uint32_t X_TMEM = 512;
 constexpr int X_PITCH = 80;                        // bytes of a staged row of 32 elements (64 B and a pad: conflict-free)
+constexpr int X_HPITCH = 48;                       // of 16 elements
 constexpr int X_WARP_STAGE = 32 * X_PITCH;
 constexpr int X_GROUP = 16;                        // row tiles visited together (see item_at)
 
@@ -54,6 +59,7 @@ struct ExpertArgs {
     void* out;                 // c, h, da, dgate|dup or dw
     void* gate_up;             // kForwardSilu: written [rows, N] (null: not); kRowsSilu: read [rows, 2K]
     int64_t ld_gu;
+    int turn;                  // kForwardSilu: gate and up columns alternate in the tile by this many (8 or 16)
     uint32_t* status;
 };
 
@@ -86,13 +92,17 @@ __device__ __forceinline__ int64_t item_count(const ExpertArgs& a, const XCtl* c
     return static_cast<int64_t>(ctl->tile0[a.E]) * NT;
 }
 
-// The round-th item of this cluster.  Rows' products: cluster c takes items c, c + clusters, ...
-// (equal work).  Weights' gradient: the experts come by falling rows and every other round runs
-// backwards, so that no cluster always gets the longer items.
+// The item this cluster takes in its v-th round.  Rows' products: cluster c takes items c, c + clusters,
+// ... (about equal work).  Weights' gradient: items are sorted by falling work; every other round
+// of items is dealt backwards, so that no cluster always gets the longer ones, and rounds are taken
+// from both ends in turn, so that the short items (whose cost is their stores) run beside the
+// multiply-adds of the long ones.
 template <int MODE>
-__device__ __forceinline__ int64_t item_of_round(int64_t round) {
+__device__ __forceinline__ int64_t item_of_round(int64_t v, int64_t rounds) {
     const int64_t c = blockIdx.x >> 1, n = gridDim.x >> 1;
-    return round * n + (MODE == kWeights && (round & 1) ? n - 1 - c : c);
+    if (MODE != kWeights) return v * n + c;
+    const int64_t r = (v & 1) ? rounds - 1 - (v >> 1) : v >> 1;
+    return r * n + ((r & 1) ? n - 1 - c : c);
 }
 
 template <int MODE>
@@ -134,6 +144,9 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
     t.kblocks = t.red > 0 ? (t.red + XK - 1) / XK : 0;
     return t;
 }
+
+// Rows that the MMAs of a tile with nrow rows take (N: a multiple of 32 for a pair of CTAs).
+__device__ __forceinline__ int rows_mma(int nrow) { return (nrow + 31) / 32 * 32; }
 
 // The same item, in values the compiler knows to be the same in every lane.
 __device__ __forceinline__ XItem uniform(const XItem& t) {
@@ -196,6 +209,14 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const CUtens
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
         "%4}], [%5];" ::"r"(smem_dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                                 int32_t z, int32_t w, int32_t v, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+        "%4, %5, %6}], [%7];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
         : "memory");
 }
 // Arrive on a barrier of either CTA of the pair (shared::cluster address).  CTA-scope release, like
@@ -276,12 +297,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-// 32 columns (v: this lane's row) to rows [r0, r0 + nrow) of a matrix of `cols` columns at column c,
-// through the warp's staging area so that each row leaves as 64 contiguous bytes.  nrow: rows of
-// this warp that exist.
+// A warp's 32 x 32 block of outputs through its staging area ([32] rows of X_PITCH bytes), so that each
+// row of the result leaves as 64 contiguous bytes.
+//   put_row:    this lane's row (32 columns)
+//   put_column: this lane's column, row i from v[i]
 template <class T>
-__device__ __forceinline__ void store_columns(const float* v, uint8_t* stage, int lane, T* out, int64_t ld, int64_t r0,
-                                              int nrow, int c, int cols) {
+__device__ __forceinline__ void put_row(const float* v, uint8_t* stage, int lane) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint4 u;
@@ -291,6 +312,20 @@ __device__ __forceinline__ void store_columns(const float* v, uint8_t* stage, in
         u.w = pack2<T>(v[q * 8 + 6], v[q * 8 + 7]);
         *reinterpret_cast<uint4*>(stage + lane * X_PITCH + q * 16) = u;
     }
+}
+template <class T>
+__device__ __forceinline__ void put_column(const float* v, uint8_t* stage, int lane) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const uint32_t u = pack2<T>(v[i], v[i + 1]);
+        *reinterpret_cast<uint16_t*>(stage + i * X_PITCH + lane * 2) = static_cast<uint16_t>(u);
+        *reinterpret_cast<uint16_t*>(stage + (i + 1) * X_PITCH + lane * 2) = static_cast<uint16_t>(u >> 16);
+    }
+}
+// The staged block to rows [r0, r0 + nrow) of a matrix of `cols` columns at column c.
+template <class T>
+__device__ __forceinline__ void store_block(const uint8_t* stage, int lane, T* out, int64_t ld, int64_t r0, int nrow,
+                                            int c, int cols) {
     __syncwarp();
     const int q = lane & 3;
     if (c + q * 8 < cols) {
@@ -304,37 +339,52 @@ __device__ __forceinline__ void store_columns(const float* v, uint8_t* stage, in
     }
     __syncwarp();
 }
-// The reverse: this lane's row of 32 columns.
+// The reverse: u holds the 16-byte pieces of the block this lane loads; then this lane's column.
 template <class T>
-__device__ __forceinline__ void load_columns(float* v, uint8_t* stage, int lane, const T* in, int64_t ld, int64_t r0,
-                                             int nrow, int c, int cols) {
+__device__ __forceinline__ void load_block(uint4 (&u)[4], int lane, const T* in, int64_t ld, int64_t r0, int nrow, int c,
+                                           int cols) {
     const int q = lane & 3;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (r < nrow && c + q * 8 < cols) u = __ldg(reinterpret_cast<const uint4*>(in + (r0 + r) * ld + c + q * 8));
-        *reinterpret_cast<uint4*>(stage + r * X_PITCH + q * 16) = u;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (r < nrow && c + q * 8 < cols) u[i] = __ldg(reinterpret_cast<const uint4*>(in + (r0 + r) * ld + c + q * 8));
     }
+}
+template <class T>
+__device__ __forceinline__ void get_column(float* v, const uint4 (&u)[4], uint8_t* stage, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(stage + (i * 8 + (lane >> 2)) * X_PITCH + (lane & 3) * 16) = u[i];
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint4 u = *reinterpret_cast<const uint4*>(stage + lane * X_PITCH + k * 16);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2<T>(w[i]);
-            v[k * 8 + 2 * i] = f.x;
-            v[k * 8 + 2 * i + 1] = f.y;
-        }
-    }
+    for (int i = 0; i < 32; ++i)
+        v[i] = to_f32(*reinterpret_cast<const T*>(stage + i * X_PITCH + lane * 2));
     __syncwarp();
+}
+
+// 32 columns of the warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+    uint32_t a[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+          "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]),
+          "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]),
+          "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
 }
 
 template <class T, int MODE>
 __global__ void __launch_bounds__(X_THREADS, 1)
     expert_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const ExpertArgs a) {
+                       const __grid_constant__ CUtensorMap tmB16, const ExpertArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -342,8 +392,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     uint8_t* smB = base + X_SUPER * X_SUB * X_TILE;        // likewise
     uint8_t* smE = smB + X_SUPER * X_SUB * X_TILE;
     XCtl* ctl = reinterpret_cast<XCtl*>(smE + X_EPI_WARPS * X_WARP_STAGE);
-    constexpr bool A_MN = MODE == kWeights;
-    constexpr bool B_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
+    constexpr bool A_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
+    constexpr bool B_MN = MODE == kWeights;
     constexpr bool SILU = MODE == kForwardSilu;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -429,14 +479,15 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         const uint32_t smA0 = smem_addr(smA), smB0 = smem_addr(smB);
         const uint32_t full = smem_addr(&ctl->full[0]), full0 = cluster_map(full, 0);
         for (int64_t round = 0; round < rounds && ok; ++round) {
-            const int64_t w = item_of_round<MODE>(round);
+            const int64_t w = item_of_round<MODE>(round, rounds);
             if (w >= total) continue;
             const XItem t = uniform(item_at<MODE>(a, ctl, w, NT));
-            const int c0 = SILU ? t.n * 128 + rank * OC : t.n * XN + rank * 128;   // this CTA's columns
-            const int32_t r0 = static_cast<int32_t>(t.r0) + rank * 128;            // and rows
-            // a CTA without rows computes on whatever its stage holds, and stores nothing
-            const bool second = MODE == kWeights || t.nrow > 128;
-            const bool load_a = rank == 0 || second;
+            const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's output columns
+            const int nn = rows_mma(t.nrow);                                      // rows the MMAs take
+            const int32_t r0 = static_cast<int32_t>(t.r0) + rank * (MODE == kWeights ? 128 : nn / 2);
+            // few rows: in boxes of 16, only as many as the MMAs read
+            const int small = MODE != kWeights && nn <= 64 ? nn / 32 : 0;
+            const int n_bytes = small ? small * 2048 : X_TILE;
             const int32_t first = MODE == kWeights ? ctl->row0[t.e] : 0;
             for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
                 const int nsub = t.kblocks - kb0 < X_SUB ? t.kblocks - kb0 : X_SUB;
@@ -446,7 +497,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                 const uint32_t bar = tail ? smem_addr(&ctl->tail[stage]) : full0 + stage * 8;
                 if (elect_lane()) {
                     if (tail) mbar_arrive_expect_tx(bar, nsub * 2 * X_TILE);
-                    else if (rank == 0) mbar_arrive_expect_tx(full + stage * 8, nsub * (second ? 4 : 3) * X_TILE);
+                    else if (rank == 0) mbar_arrive_expect_tx(full + stage * 8, nsub * 2 * (X_TILE + n_bytes));
                     else if (MODE == kWeights) mbar_arrive_cluster(bar);
                     for (int j = 0; j < nsub; ++j) {
                         const int kb = kb0 + j;
@@ -466,14 +517,18 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                                 }
                             }
                         } else {
-                            if (load_a) tma_load_2d_pair(sa, &tmA, kb * XK * 2, r0, bar);
-                            if (B_MN) {
+                            if (MODE == kForwardSilu) {   // gate and up columns in turn, a.turn of each
+                                tma_load_5d_pair(sa, &tmA, kb * XK * 2, 0, 0, c0 / a.turn, t.e, bar);
+                            } else if (MODE == kForward) {
+                                tma_load_3d_pair(sa, &tmA, kb * XK * 2, c0, t.e, bar);
+                            } else {
 #pragma unroll
                                 for (int i = 0; i < 2; ++i)
-                                    tma_load_3d_pair(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, kb * XK, t.e, bar);
-                            } else {
-                                tma_load_3d_pair(sb, &tmB, kb * XK * 2, c0, t.e, bar);
+                                    tma_load_3d_pair(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, kb * XK, t.e, bar);
                             }
+                            if (small == 0) tma_load_2d_pair(sb, &tmB, kb * XK * 2, r0, bar);
+                            for (int i = 0; i < small; ++i)
+                                tma_load_2d_pair(sb + i * 2048, &tmB16, kb * XK * 2, r0 + i * 16, bar);
                         }
                     }
                 }
@@ -496,7 +551,6 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     } else if (warp == 1) {
         if (rank == 0) {
             // ------------------------------------------------------------ MMA (CTA 0)
-            constexpr uint32_t idesc = idesc_16bit<T>(XN, A_MN, B_MN);
             const uint64_t ad0 = A_MN ? smem_desc_mn_sw128(smem_addr(smA)) : smem_desc_k128_sw128(smem_addr(smA));
             const uint64_t bd0 = B_MN ? smem_desc_mn_sw128(smem_addr(smB)) : smem_desc_k128_sw128(smem_addr(smB));
             constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
@@ -505,13 +559,14 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             uint32_t phase = 0, buf = 0, bphase = 0;
             bool ok = true;
             for (int64_t round = 0; round < rounds && ok; ++round) {
-                const int64_t w = item_of_round<MODE>(round);
+                const int64_t w = item_of_round<MODE>(round, rounds);
                 if (w >= total) continue;
                 const XItem t = uniform(item_at<MODE>(a, ctl, w, NT));
                 if (t.kblocks == 0) continue;
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
                 if (!ok) break;
                 const uint32_t d = tmem + buf * XN;
+                const uint32_t idesc = idesc_16bit<T>(MODE == kWeights ? XN : rows_mma(t.nrow), A_MN, B_MN);
                 for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
                     ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
                     if (!ok) break;
@@ -558,7 +613,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         uint32_t tails = 0;   // bit s: parity of stage s's tail barrier
         bool ok = true;
         for (int64_t round = 0; round < rounds && ok; ++round) {
-            const int64_t w = item_of_round<MODE>(round);
+            const int64_t w = item_of_round<MODE>(round, rounds);
             if (w >= total) continue;
             const XItem t = item_at<MODE>(a, ctl, w, NT);
             const int stages = (t.kblocks + X_SUB - 1) / X_SUB;
@@ -584,83 +639,140 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         }
     } else if (warp >= X_FIRST_EPI) {
         // ---------------------------------------------------------------- epilogue
-        const int g = (warp - X_FIRST_EPI) >> 2;   // column half
+        const int g = (warp - X_FIRST_EPI) >> 2;
         const int sp = warp & 3;                   // tensor-memory lane quarter
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
         uint8_t* stage = smE + (warp - X_FIRST_EPI) * X_WARP_STAGE;
         T* out = static_cast<T*>(a.out);
+        const T* gu_in = static_cast<const T*>(a.gate_up);   // kRowsSilu
         uint32_t buf = 0, bphase = 0;
         bool ok = true;
         const uint32_t tempty0 = cluster_map(smem_addr(&ctl->tempty[0]), 0), tempty1 = cluster_map(smem_addr(&ctl->tempty[1]), 0);
         for (int64_t round = 0; round < rounds; ++round) {
-            const int64_t w = item_of_round<MODE>(round);
+            const int64_t w = item_of_round<MODE>(round, rounds);
             if (w >= total) continue;
             const XItem t = item_at<MODE>(a, ctl, w, NT);
-            const int64_t r0 = t.r0 + rank * 128 + sp * 32 + (MODE == kWeights ? static_cast<int64_t>(t.e) * a.N : 0);
-            const int nrow = t.nrow - rank * 128 - sp * 32;   // this warp's rows (none: <= 0)
-            const int c0 = SILU ? t.n * 128 : t.n * XN;
-            if (MODE == kWeights && t.kblocks == 0) {   // an expert without rows: zero
-                float z[32];
+            if (MODE == kWeights) {
+                // rows of dw[e] (columns of dc) in the lanes; warps g take 128 of the 256 columns each
+                const int64_t r0 = static_cast<int64_t>(t.e) * a.N + t.r0 + rank * 128 + sp * 32;
+                const int nrow = t.nrow - rank * 128 - sp * 32, c0 = t.n * XN + g * 128;
+                if (t.kblocks == 0) {   // an expert without rows: zero
+                    float z[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = 0.0f;
-                for (int j = 0; j < 4; ++j)
-                    store_columns<T>(z, stage, lane, out, OC, r0, nrow, c0 + g * 128 + j * 32, OC);
-                continue;
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t acc = lane_base + buf * XN;
+                    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+                    put_row<T>(z, stage, lane);
+                    for (int j = 0; j < 4; ++j) store_block<T>(stage, lane, out, OC, r0, nrow, c0 + j * 32, OC);
+                    continue;
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float va[32], vb[32];
-                if (SILU) {
-                    const int c = g * 64 + j * 32;
-                    tmem_ld32x2(acc + c, acc + 128 + c, va, vb);
-                } else {
-                    const int c = g * 128 + j * 64;
-                    tmem_ld32x2(acc + c, acc + c + 32, va, vb);
-                }
-                if (j == 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
-                }
-                if (nrow <= 0) continue;
-                if (SILU) {
-                    const int c = c0 + g * 64 + j * 32;
-                    T* gu = static_cast<T*>(a.gate_up);
-                    if (gu) {
-                        store_columns<T>(va, stage, lane, gu, 2 * OC, r0, nrow, c, OC);
-                        store_columns<T>(vb, stage, lane, gu + OC, 2 * OC, r0, nrow, c, OC);
+                for (int j = 0; j < 2; ++j) {
+                    float va[32], vb[32];
+                    const uint32_t acc = lane_base + buf * XN + g * 128 + j * 64;
+                    tmem_ld32x2(acc, acc + 32, va, vb);
+                    if (j == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
                     }
+                    put_row<T>(va, stage, lane);
+                    store_block<T>(stage, lane, out, OC, r0, nrow, c0 + j * 64, OC);
+                    put_row<T>(vb, stage, lane);
+                    store_block<T>(stage, lane, out, OC, r0, nrow, c0 + j * 64 + 32, OC);
+                }
+            } else {
+                // output columns in the lanes; the tile's rows in blocks of 32, dealt to the warps g in turn
+                const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128) + sp * (SILU ? 16 : 32);
+                const int blocks = (t.nrow + 31) / 32;
+                uint4 gq[4], uq[4];
+                if (MODE == kRowsSilu && g < blocks) {   // gate and up of the first block, ahead of the products
+                    load_block<T>(gq, lane, gu_in, a.ld_gu, t.r0 + g * 32, t.nrow - g * 32, c0, OC);
+                    load_block<T>(uq, lane, gu_in + OC, a.ld_gu, t.r0 + g * 32, t.nrow - g * 32, c0, OC);
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
+                if (!ok) break;
+                tc_fence_after();
+                for (int blk = g; blk < blocks; blk += 2) {
+                    float v[32];
+                    tmem_ld32(lane_base + buf * XN + blk * 32, v);
+                    const int64_t r0 = t.r0 + blk * 32;
+                    const int nrow = t.nrow - blk * 32;
+                    if (SILU) {
+                        // lanes: a.turn gate columns, then the up columns of the same, and so on
+                        const bool up = (lane & a.turn) != 0;
+                        T* gu = static_cast<T*>(a.gate_up);
+                        if (gu) {
+                            put_column<T>(v, stage, lane);
+                            __syncwarp();
+                            // 16-byte piece q of a staged row: columns 8q .. 8q + 7 of the lanes
+                            const int q = lane & 3, l = q * 8;
+                            const int col = c0 + (a.turn == 16 ? l & 15 : (l >> 4) * 8);
+                            if (col < OC) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) va[i] = va[i] / (1.0f + __expf(-va[i])) * vb[i];
-                    store_columns<T>(va, stage, lane, out, OC, r0, nrow, c, OC);
-                } else if (MODE == kRowsSilu) {
-                    const T* gu = static_cast<const T*>(a.gate_up);
+                                for (int i = 0; i < 4; ++i) {
+                                    const int r = i * 8 + (lane >> 2);
+                                    if (r < nrow)
+                                        *reinterpret_cast<uint4*>(gu + (r0 + r) * (2 * OC) + col + ((l & a.turn) ? OC : 0)) =
+                                            *reinterpret_cast<const uint4*>(stage + r * X_PITCH + q * 16);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        // a gate lane gives the up lane beside it its rows 16 .. 31 for that lane's up of rows
+                        // 0 .. 15: each then holds 16 rows of one column of h
+                        float h[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float* v = h ? vb : va;
-                        const int c = c0 + g * 128 + j * 64 + h * 32;
+                        for (int i = 0; i < 16; ++i) {
+                            const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[16 + i], a.turn);
+                            const float gate = up ? o : v[i], u = up ? v[16 + i] : o;
+                            h[i] = gate / (1.0f + __expf(-gate)) * u;
+                        }
+                        // staged as [32 rows][16 columns]
+                        const int hc = a.turn == 16 ? lane & 15 : ((lane >> 4) * 8) + (lane & 7);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            *reinterpret_cast<T*>(stage + ((up ? 16 : 0) + i) * X_HPITCH + hc * 2) = from_f32<T>(h[i]);
+                        __syncwarp();
+                        const int hq = lane & 1;
+                        if (c0 + hq * 8 < OC) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int r = i * 16 + (lane >> 1);
+                                if (r < nrow)
+                                    *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + hq * 8) =
+                                        *reinterpret_cast<const uint4*>(stage + r * X_HPITCH + hq * 16);
+                            }
+                        }
+                        __syncwarp();
+                    } else if (MODE == kRowsSilu) {
                         float gt[32], up[32];
-                        load_columns<T>(gt, stage, lane, gu, a.ld_gu, r0, nrow, c, OC);
-                        load_columns<T>(up, stage, lane, gu + OC, a.ld_gu, r0, nrow, c, OC);
+                        get_column<T>(gt, gq, stage, lane);
+                        get_column<T>(up, uq, stage, lane);
+                        if (blk + 2 < blocks) {
+                            load_block<T>(gq, lane, gu_in, a.ld_gu, r0 + 64, nrow - 64, c0, OC);
+                            load_block<T>(uq, lane, gu_in + OC, a.ld_gu, r0 + 64, nrow - 64, c0, OC);
+                        }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float s = 1.0f / (1.0f + __expf(-gt[i]));
+                            const float s = __fdividef(1.0f, 1.0f + __expf(-gt[i]));
                             const float dup = v[i] * gt[i] * s;
                             v[i] = v[i] * up[i] * s * (1.0f + gt[i] * (1.0f - s));
                             up[i] = dup;
                         }
-                        store_columns<T>(v, stage, lane, out, 2 * OC, r0, nrow, c, OC);
-                        store_columns<T>(up, stage, lane, out + OC, 2 * OC, r0, nrow, c, OC);
+                        put_column<T>(v, stage, lane);
+                        store_block<T>(stage, lane, out, 2 * OC, r0, nrow, c0, OC);
+                        put_column<T>(up, stage, lane);
+                        store_block<T>(stage, lane, out + OC, 2 * OC, r0, nrow, c0, OC);
+                    } else {
+                        put_column<T>(v, stage, lane);
+                        store_block<T>(stage, lane, out, OC, r0, nrow, c0, OC);
                     }
-                } else {
-                    const int c = c0 + g * 128 + j * 64;
-                    store_columns<T>(va, stage, lane, out, OC, r0, nrow, c, OC);
-                    store_columns<T>(vb, stage, lane, out, OC, r0, nrow, c + 32, OC);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
             }
             buf ^= 1u;
             if (buf == 0) bphase ^= 1u;
@@ -695,6 +807,22 @@ cudaError_t map_16bit(CUtensorMap* map, const void* p, int64_t n0, int64_t ld, i
     return encode_u8_map_nd(map, static_cast<const uint8_t*>(p), n2 > 0 ? 3 : 2, dims, strides, box, true);
 }
 
+// The rows of a product in boxes of 128 and of 16 (tm[1], tm[2]).
+cudaError_t map_rows(CUtensorMap (&tm)[3], const void* p, int64_t cols, int64_t ld, int64_t rows) {
+    const cudaError_t e = map_16bit(&tm[1], p, cols, ld, rows, 0, 128);
+    return e == cudaSuccess ? map_16bit(&tm[2], p, cols, ld, rows, 0, 16) : e;
+}
+
+// w [E, 2I, K] as [E][I / turn][gate, up][turn][K]: one box brings 128 rows, turn gate columns and
+// the up columns of the same in turn (I a multiple of turn).
+cudaError_t map_gate_up(CUtensorMap* map, const void* w, int64_t K, int64_t I, int64_t E, int turn) {
+    const uint64_t row = static_cast<uint64_t>(K) * 2, n = static_cast<uint64_t>(I);
+    const uint64_t dims[5] = {row, static_cast<uint64_t>(turn), 2, n / turn, static_cast<uint64_t>(E)};
+    const uint64_t strides[4] = {row, n * row, turn * row, 2 * n * row};
+    const uint32_t box[5] = {128, static_cast<uint32_t>(turn), 2, static_cast<uint32_t>(64 / turn), 1};
+    return encode_u8_map_nd(map, static_cast<const uint8_t*>(w), 5, dims, strides, box, true);
+}
+
 int g_clusters = 0;   // clusters of two CTAs resident at once (the same for every instance: one CTA per SM)
 
 void pair_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned clusters, cudaStream_t stream) {
@@ -714,20 +842,19 @@ void pair_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned cl
 }
 
 template <class T, int MODE>
-cudaError_t launch_experts(const ExpertArgs& a, const CUtensorMap& tmA, const CUtensorMap& tmB, int64_t most_items,
-                           cudaStream_t stream) {
+cudaError_t launch_experts(const ExpertArgs& a, const CUtensorMap (&tm)[3], int64_t most_items, cudaStream_t stream) {
     if (g_clusters < 1) return cudaErrorNotSupported;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     pair_config(&cfg, attr, static_cast<unsigned>(most_items < g_clusters ? most_items : g_clusters), stream);
-    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<T, MODE>, tmA, tmB, a);
+    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<T, MODE>, tm[0], tm[1], tm[2], a);
 }
 
 template <int MODE>
-cudaError_t launch_experts_type(int dtype, const ExpertArgs& a, const CUtensorMap& tmA, const CUtensorMap& tmB,
-                                int64_t most_items, cudaStream_t stream) {
-    return dtype == MOE_DTYPE_BF16 ? launch_experts<__nv_bfloat16, MODE>(a, tmA, tmB, most_items, stream)
-                                   : launch_experts<__half, MODE>(a, tmA, tmB, most_items, stream);
+cudaError_t launch_experts_type(int dtype, const ExpertArgs& a, const CUtensorMap (&tm)[3], int64_t most_items,
+                                cudaStream_t stream) {
+    return dtype == MOE_DTYPE_BF16 ? launch_experts<__nv_bfloat16, MODE>(a, tm, most_items, stream)
+                                   : launch_experts<__half, MODE>(a, tm, most_items, stream);
 }
 
 template <class T, int MODE>
@@ -795,16 +922,17 @@ int moe_expert_gemm(const void* rows_a, int64_t lda, int dtype, const void* w, c
     if (num_rows == 0) return MOE_OK;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
-    CUtensorMap tmA, tmB;
-    if (map_16bit(&tmA, rows_a, K, lda, num_rows, 0, 128) != cudaSuccess ||
-        map_16bit(&tmB, w, K, K, N, E, 128) != cudaSuccess)
+    const int I = N / 2, turn = I % 16 == 0 ? 16 : 8;
+    const bool silu = epilogue == MOE_EXPERT_SILU_MUL;
+    CUtensorMap tm[3];   // weights, rows, rows in small boxes
+    if ((silu ? map_gate_up(&tm[0], w, K, I, E, turn) : map_16bit(&tm[0], w, K, K, N, E, 128)) != cudaSuccess ||
+        map_rows(tm, rows_a, K, lda, num_rows) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, gate_up, 0, status};
+    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, gate_up, 0, turn, status};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t tiles = most_row_tiles(num_rows, E);
-    if (epilogue == MOE_EXPERT_STORE)
-        return cuda_status(launch_experts_type<kForward>(dtype, a, tmA, tmB, tiles * ((N + XN - 1) / XN), s));
-    return cuda_status(launch_experts_type<kForwardSilu>(dtype, a, tmA, tmB, tiles * ((N / 2 + 127) / 128), s));
+    if (silu) return cuda_status(launch_experts_type<kForwardSilu>(dtype, a, tm, tiles * ((I + 127) / 128), s));
+    return cuda_status(launch_experts_type<kForward>(dtype, a, tm, tiles * ((N + XN - 1) / XN), s));
 }
 
 int moe_expert_gemm_dgrad(const void* dc, int64_t lddc, int dtype, const void* w, const int32_t* expert_offsets,
@@ -819,15 +947,14 @@ int moe_expert_gemm_dgrad(const void* dc, int64_t lddc, int dtype, const void* w
     if (num_rows == 0) return MOE_OK;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
-    CUtensorMap tmA, tmB;
-    if (map_16bit(&tmA, dc, N, lddc, num_rows, 0, 128) != cudaSuccess ||
-        map_16bit(&tmB, w, K, K, N, E, XK) != cudaSuccess)
+    CUtensorMap tm[3];
+    if (map_16bit(&tm[0], w, K, K, N, E, XK) != cudaSuccess || map_rows(tm, dc, N, lddc, num_rows) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, const_cast<void*>(gate_up), ldgu, status};
+    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, out, const_cast<void*>(gate_up), ldgu, 0, status};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t items = most_row_tiles(num_rows, E) * ((K + XN - 1) / XN);
-    if (gate_up) return cuda_status(launch_experts_type<kRowsSilu>(dtype, a, tmA, tmB, items, s));
-    return cuda_status(launch_experts_type<kRows>(dtype, a, tmA, tmB, items, s));
+    if (gate_up) return cuda_status(launch_experts_type<kRowsSilu>(dtype, a, tm, items, s));
+    return cuda_status(launch_experts_type<kRows>(dtype, a, tm, items, s));
 }
 
 int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* rows_a, int64_t lda, int dtype,
@@ -843,13 +970,14 @@ int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* rows_a, int6
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (num_rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * N * K * 2, s));
-    CUtensorMap tmA, tmB;
-    if (map_16bit(&tmA, dc, N, lddc, num_rows, 0, XK) != cudaSuccess ||
-        map_16bit(&tmB, rows_a, K, lda, num_rows, 0, XK) != cudaSuccess)
+    CUtensorMap tm[3];
+    if (map_16bit(&tm[0], dc, N, lddc, num_rows, 0, XK) != cudaSuccess ||
+        map_16bit(&tm[1], rows_a, K, lda, num_rows, 0, XK) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, dw, nullptr, 0, status};
+    tm[2] = tm[1];   // not read
+    const ExpertArgs a = {expert_offsets, E, num_rows, N, K, dw, nullptr, 0, 0, status};
     const int64_t items = static_cast<int64_t>(E) * ((N + XM - 1) / XM) * ((K + XN - 1) / XN);
-    return cuda_status(launch_experts_type<kWeights>(dtype, a, tmA, tmB, items, s));
+    return cuda_status(launch_experts_type<kWeights>(dtype, a, tm, items, s));
 }
 
 }  // extern "C"
