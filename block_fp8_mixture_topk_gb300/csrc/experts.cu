@@ -14,15 +14,14 @@
 // outputs: one thread of CTA 0 issues tcgen05.mma.cta_group::2 (256 x N x 16), which reads both CTAs'
 // operands (128 of the 256, half of the N each) and leaves each CTA its 128 x N in its own tensor
 // memory (two accumulators).  A 64-wide K block then brings 32 KB into an SM for 512 cycles of its
-// tensor pipe.  A TMA warp per CTA fills a ring of three 128-wide stages (one barrier wait and
-// commit per eight MMAs), eight warps per CTA drain an accumulator while the next one fills.
+// tensor pipe.  A TMA warp per CTA fills a ring of six 64-wide stages, eight warps per CTA drain an accumulator while the next one fills.
 //
 // Products and rows' gradient: the 256 run along the output columns (the weights) and N along the
 // rows, so that the tile in which an expert ends costs its rows rounded up to 32, not to 256 (a
 // skewed router leaves most experts few rows: with rows along the 256, 19% of the multiply-adds of
 // the Qwen3-shaped batch were padding).  The accumulators then hold one output column per lane,
-// and the epilogue turns them over through shared memory.  Weights' gradient: 256 columns of dc by
-// 256 of a, the rows are the reduction.
+// and the epilogue stores row by row.  Weights' gradient: 256 columns of a by 256 of dc, the rows are
+// the reduction.
 //
 // The operands keep the caller's layout; where the reduction runs along the slow axis (w of the
 // rows' gradient, both operands of the weights' gradient) the 128-byte rows of a TMA box run along the
@@ -40,16 +39,13 @@ namespace {
 enum Mode { kForward = 0, kForwardSilu = 1, kRows = 2, kRowsSilu = 3, kWeights = 4 };
 
 constexpr int XM = 256, XN = 256, XK = 64;         // item; XK elements are one 128-byte swizzled row
-constexpr int X_SUB = 2, X_SUPER = 3;              // K blocks per stage, stages
+constexpr int X_SUB = 1, X_SUPER = 6;              // K blocks per stage, stages
 constexpr int X_TILE = 128 * XK * 2;               // one operand's K block in one CTA
 constexpr int X_BOX = 64 * 128;                    // bytes of a transposed operand's box: 64 rows of 64 elements
 constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: tile table, 3: ends of experts
 constexpr int X_THREADS = (X_FIRST_EPI + X_EPI_WARPS) * 32;
 constexpr uint32_t X_TMEM = 512;
-constexpr int X_PITCH = 80;                        // bytes of a staged row of 32 elements (64 B and a pad: conflict-free)
-constexpr int X_HPITCH = 48;                       // of 16 elements
-constexpr int X_WARP_STAGE = 32 * X_PITCH;
-constexpr int X_GROUP = 16;                        // row tiles visited together (see item_at)
+constexpr int X_GROUP = 4;                        // row tiles visited together (see item_at)
 
 struct ExpertArgs {
     const int32_t* offsets;
@@ -73,9 +69,10 @@ struct XCtl {
     uint32_t tmem_base;
     int abort_flag;
     int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
-    int tile0[MOE_MAX_EXPERTS + 1];   // first 256-row tile of each expert; weights' gradient: experts by falling rows
+    int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each place (not for the weights' gradient)
+    int16_t order[MOE_MAX_EXPERTS];   // experts by falling rows: the expert at each place
 };
-constexpr size_t X_SMEM = 1024 + X_SUPER * X_SUB * 2 * X_TILE + X_EPI_WARPS * X_WARP_STAGE + sizeof(XCtl);
+constexpr size_t X_SMEM = 1024 + X_SUPER * X_SUB * 2 * X_TILE + sizeof(XCtl);
 static_assert(X_SMEM <= 232448, "more shared memory than a CTA has");
 
 // One output tile: rows [r0, r0 + nrow) of column tile n of expert e; kblocks of the reduction
@@ -92,17 +89,17 @@ __device__ __forceinline__ int64_t item_count(const ExpertArgs& a, const XCtl* c
     return static_cast<int64_t>(ctl->tile0[a.E]) * NT;
 }
 
-// The item this cluster takes in its v-th round.  Rows' products: cluster c takes items c, c + clusters,
-// ... (about equal work).  Weights' gradient: items are sorted by falling work; every other round
-// of items is dealt backwards, so that no cluster always gets the longer ones, and rounds are taken
-// from both ends in turn, so that the short items (whose cost is their stores) run beside the
-// multiply-adds of the long ones.
+// The item this cluster takes in its v-th round.  Items are sorted by their experts' falling rows.  Rounds
+// are taken from both ends in turn, the odd clusters one step behind the even ones, so that at any
+// time half of the clusters run items bound by their loads or stores (experts with few rows) beside
+// the multiply-adds of the other half; in the weights' gradient, whose items take as long as their
+// experts have rows, every other round of items is dealt backwards, so that no cluster always gets
+// the longer ones.
 template <int MODE>
 __device__ __forceinline__ int64_t item_of_round(int64_t v, int64_t rounds) {
     const int64_t c = blockIdx.x >> 1, n = gridDim.x >> 1;
-    if (MODE != kWeights) return v * n + c;
-    const int64_t r = (v & 1) ? rounds - 1 - (v >> 1) : v >> 1;
-    return r * n + ((r & 1) ? n - 1 - c : c);
+    const int64_t r = ((v + c) & 1) ? rounds - 1 - (v >> 1) : v >> 1;
+    return r * n + (MODE == kWeights && (r & 1) ? n - 1 - c : c);
 }
 
 template <int MODE>
@@ -111,7 +108,7 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
     if (MODE == kWeights) {
         const int MT = (a.N + XM - 1) / XM, per = MT * NT;
         const int k = static_cast<int>(w / per);
-        t.e = ctl->tile0[k];
+        t.e = ctl->order[k];
         const int local = static_cast<int>(w - static_cast<int64_t>(k) * per);
         const int m = local % MT;
         t.n = local / MT;
@@ -128,7 +125,7 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
             if (ctl->tile0[mid] <= g) lo = mid;
             else hi = mid - 1;
         }
-        t.e = lo;
+        t.e = ctl->order[lo];
         const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo];
         int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
         const int grp = local / (X_GROUP * NT);
@@ -136,9 +133,9 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
         const int gm = mt - grp * X_GROUP < X_GROUP ? mt - grp * X_GROUP : X_GROUP;
         const int m = grp * X_GROUP + local % gm;
         t.n = local / gm;
-        const int cnt = ctl->row0[lo + 1] - ctl->row0[lo];
-        t.r0 = ctl->row0[lo] + m * XM;
-        t.nrow = cnt - m * XM < XM ? cnt - m * XM : XM;
+        const int cnt = ctl->row0[t.e + 1] - ctl->row0[t.e];
+        t.r0 = ctl->row0[t.e] + m * XN;
+        t.nrow = cnt - m * XN < XN ? cnt - m * XN : XN;
         t.red = MODE == kRows || MODE == kRowsSilu ? a.N : a.K;
     }
     t.kblocks = t.red > 0 ? (t.red + XK - 1) / XK : 0;
@@ -284,83 +281,39 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t pari
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 template <class T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    if (std::is_same<T, __nv_bfloat16>::value) return bf16x2(lo, hi);
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-template <class T>
 __device__ __forceinline__ float2 unpack2(uint32_t v) {
     if (std::is_same<T, __nv_bfloat16>::value)
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-// A warp's 32 x 32 block of outputs through its staging area ([32] rows of X_PITCH bytes), so that each
-// row of the result leaves as 64 contiguous bytes.
-//   put_row:    this lane's row (32 columns)
-//   put_column: this lane's column, row i from v[i]
+// An accumulator lane is an output column, so the warp stores one row of a 32 x 32 block at a time, 64
+// contiguous bytes.  (Through shared memory each lane could store 16 bytes, but the staging took a
+// tenth of the shared-memory cycles, which the tensor cores' operand reads and the TMA writes
+// fill: 546 against 475 us for the skewed batch's product without any epilogue.)
+//   store_column: rows i < nrow of this lane's column from v[i];  load_column: the reverse, two rows
+//   per register
 template <class T>
-__device__ __forceinline__ void put_row(const float* v, uint8_t* stage, int lane) {
+__device__ __forceinline__ void store_column(const float* v, T* out, int64_t ld, int nrow, bool live) {
+    if (!live) return;
+    if (nrow >= 32) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint4 u;
-        u.x = pack2<T>(v[q * 8 + 0], v[q * 8 + 1]);
-        u.y = pack2<T>(v[q * 8 + 2], v[q * 8 + 3]);
-        u.z = pack2<T>(v[q * 8 + 4], v[q * 8 + 5]);
-        u.w = pack2<T>(v[q * 8 + 6], v[q * 8 + 7]);
-        *reinterpret_cast<uint4*>(stage + lane * X_PITCH + q * 16) = u;
+        for (int i = 0; i < 32; ++i) out[i * ld] = from_f32<T>(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < nrow) out[i * ld] = from_f32<T>(v[i]);
     }
 }
 template <class T>
-__device__ __forceinline__ void put_column(const float* v, uint8_t* stage, int lane) {
+__device__ __forceinline__ void load_column(uint32_t (&u)[16], const T* in, int64_t ld, int nrow, bool live) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-        const uint32_t u = pack2<T>(v[i], v[i + 1]);
-        *reinterpret_cast<uint16_t*>(stage + i * X_PITCH + lane * 2) = static_cast<uint16_t>(u);
-        *reinterpret_cast<uint16_t*>(stage + (i + 1) * X_PITCH + lane * 2) = static_cast<uint16_t>(u >> 16);
+    for (int i = 0; i < 16; ++i) {
+        const uint16_t lo = live && 2 * i < nrow ? __ldg(reinterpret_cast<const uint16_t*>(in + (2 * i) * ld)) : uint16_t(0);
+        const uint16_t hi =
+            live && 2 * i + 1 < nrow ? __ldg(reinterpret_cast<const uint16_t*>(in + (2 * i + 1) * ld)) : uint16_t(0);
+        u[i] = lo | (static_cast<uint32_t>(hi) << 16);
     }
-}
-// The staged block to rows [r0, r0 + nrow) of a matrix of `cols` columns at column c.
-template <class T>
-__device__ __forceinline__ void store_block(const uint8_t* stage, int lane, T* out, int64_t ld, int64_t r0, int nrow,
-                                            int c, int cols) {
-    __syncwarp();
-    const int q = lane & 3;
-    if (c + q * 8 < cols) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + (lane >> 2);
-            if (r < nrow)
-                *reinterpret_cast<uint4*>(out + (r0 + r) * ld + c + q * 8) =
-                    *reinterpret_cast<const uint4*>(stage + r * X_PITCH + q * 16);
-        }
-    }
-    __syncwarp();
-}
-// The reverse: u holds the 16-byte pieces of the block this lane loads; then this lane's column.
-template <class T>
-__device__ __forceinline__ void load_block(uint4 (&u)[4], int lane, const T* in, int64_t ld, int64_t r0, int nrow, int c,
-                                           int cols) {
-    const int q = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2);
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (r < nrow && c + q * 8 < cols) u[i] = __ldg(reinterpret_cast<const uint4*>(in + (r0 + r) * ld + c + q * 8));
-    }
-}
-template <class T>
-__device__ __forceinline__ void get_column(float* v, const uint4 (&u)[4], uint8_t* stage, int lane) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(stage + (i * 8 + (lane >> 2)) * X_PITCH + (lane & 3) * 16) = u[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = to_f32(*reinterpret_cast<const T*>(stage + i * X_PITCH + lane * 2));
-    __syncwarp();
 }
 
 // 32 columns of the warp's 32 tensor-memory lanes.
@@ -390,8 +343,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     uint8_t* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint8_t* smA = base;                                   // [X_SUPER][X_SUB][X_TILE]
     uint8_t* smB = base + X_SUPER * X_SUB * X_TILE;        // likewise
-    uint8_t* smE = smB + X_SUPER * X_SUB * X_TILE;
-    XCtl* ctl = reinterpret_cast<XCtl*>(smE + X_EPI_WARPS * X_WARP_STAGE);
+    XCtl* ctl = reinterpret_cast<XCtl*>(smB + X_SUPER * X_SUB * X_TILE);
     constexpr bool A_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
     constexpr bool B_MN = MODE == kWeights;
     constexpr bool SILU = MODE == kForwardSilu;
@@ -435,32 +387,35 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         ctl->row0[e] = static_cast<int>(o);
     }
     __syncthreads();
-    if (MODE == kWeights) {
-        for (int e = threadIdx.x; e < a.E; e += X_THREADS) {
-            const int n = ctl->row0[e + 1] - ctl->row0[e];
-            int place = 0;   // experts with more rows, or as many and a lower index
-            for (int o = 0; o < a.E; ++o) {
-                const int m = ctl->row0[o + 1] - ctl->row0[o];
-                place += m > n || (m == n && o < e);
-            }
-            ctl->tile0[place] = e;
+    for (int e = threadIdx.x; e < a.E; e += X_THREADS) {
+        const int n = ctl->row0[e + 1] - ctl->row0[e];
+        int place = 0;   // experts with more rows, or as many and a lower index
+#pragma unroll 8
+        for (int o = 0; o < a.E; ++o) {
+            const int m = ctl->row0[o + 1] - ctl->row0[o];
+            place += m > n || (m == n && o < e);
         }
-    } else if (warp == 2) {
-        int carry = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int cnt = e < a.E ? ctl->row0[e + 1] - ctl->row0[e] : 0;
-            const int own = cnt > 0 ? (cnt + XM - 1) / XM : 0;
-            int v = own;
+        ctl->order[place] = static_cast<int16_t>(e);
+    }
+    if (MODE != kWeights) {
+        __syncthreads();
+        if (warp == 2) {
+            int carry = 0;
+            for (int k0 = 0; k0 < a.E; k0 += 32) {
+                const int k = k0 + lane, e = k < a.E ? ctl->order[k] : 0;
+                const int cnt = k < a.E ? ctl->row0[e + 1] - ctl->row0[e] : 0;
+                const int own = cnt > 0 ? (cnt + XN - 1) / XN : 0;
+                int v = own;
 #pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, s);
-                if (lane >= s) v += u;
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, v, s);
+                    if (lane >= s) v += u;
+                }
+                if (k < a.E) ctl->tile0[k] = carry + v - own;
+                carry += __shfl_sync(0xffffffffu, v, 31);
             }
-            if (e < a.E) ctl->tile0[e] = carry + v - own;
-            carry += __shfl_sync(0xffffffffu, v, 31);
+            if (lane == 0) ctl->tile0[a.E] = carry;
         }
-        if (lane == 0) ctl->tile0[a.E] = carry;
     }
     tc_fence_before();
     __syncthreads();
@@ -504,16 +459,16 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                         const uint32_t sa = smA0 + (stage * X_SUB + j) * X_TILE;
                         const uint32_t sb = smB0 + (stage * X_SUB + j) * X_TILE;
                         if (MODE == kWeights) {
-                            // 64 rows of the expert, 128 columns of dc and of a
+                            // 64 rows of the expert, 128 columns of a and of dc
                             const int32_t r = first + kb * XK;
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 if (tail) {
-                                    tma_load_2d(sa + i * X_BOX, &tmA, (r0 + i * 64) * 2, r, bar);
-                                    tma_load_2d(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, r, bar);
+                                    tma_load_2d(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, r, bar);
+                                    tma_load_2d(sb + i * X_BOX, &tmB, (r0 + i * 64) * 2, r, bar);
                                 } else {
-                                    tma_load_2d_pair(sa + i * X_BOX, &tmA, (r0 + i * 64) * 2, r, bar);
-                                    tma_load_2d_pair(sb + i * X_BOX, &tmB, (c0 + i * 64) * 2, r, bar);
+                                    tma_load_2d_pair(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, r, bar);
+                                    tma_load_2d_pair(sb + i * X_BOX, &tmB, (r0 + i * 64) * 2, r, bar);
                                 }
                             }
                         } else {
@@ -642,7 +597,6 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         const int g = (warp - X_FIRST_EPI) >> 2;
         const int sp = warp & 3;                   // tensor-memory lane quarter
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
-        uint8_t* stage = smE + (warp - X_FIRST_EPI) * X_WARP_STAGE;
         T* out = static_cast<T*>(a.out);
         const T* gu_in = static_cast<const T*>(a.gate_up);   // kRowsSilu
         uint32_t buf = 0, bphase = 0;
@@ -652,128 +606,75 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             const int64_t w = item_of_round<MODE>(round, rounds);
             if (w >= total) continue;
             const XItem t = item_at<MODE>(a, ctl, w, NT);
-            if (MODE == kWeights) {
-                // rows of dw[e] (columns of dc) in the lanes; warps g take 128 of the 256 columns each
-                const int64_t r0 = static_cast<int64_t>(t.e) * a.N + t.r0 + rank * 128 + sp * 32;
-                const int nrow = t.nrow - rank * 128 - sp * 32, c0 = t.n * XN + g * 128;
-                if (t.kblocks == 0) {   // an expert without rows: zero
-                    float z[32];
+            // output columns in the lanes; the tile's rows in blocks of 32, dealt to the warps g in turn
+            const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128) + sp * (SILU ? 16 : 32);
+            const int col = SILU ? c0 + (a.turn == 16 ? lane & 15 : ((lane >> 4) * 8) + (lane & 7)) : c0 + lane;
+            const bool live = col < OC;
+            const int blocks = (t.nrow + 31) / 32;
+            const int64_t row = t.r0 + (MODE == kWeights ? static_cast<int64_t>(t.e) * a.N : 0);
+            if (MODE == kWeights && t.kblocks == 0) {   // an expert without rows: zero
+                float z[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = 0.0f;
-                    put_row<T>(z, stage, lane);
-                    for (int j = 0; j < 4; ++j) store_block<T>(stage, lane, out, OC, r0, nrow, c0 + j * 32, OC);
-                    continue;
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float va[32], vb[32];
-                    const uint32_t acc = lane_base + buf * XN + g * 128 + j * 64;
-                    tmem_ld32x2(acc, acc + 32, va, vb);
-                    if (j == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
-                    }
-                    put_row<T>(va, stage, lane);
-                    store_block<T>(stage, lane, out, OC, r0, nrow, c0 + j * 64, OC);
-                    put_row<T>(vb, stage, lane);
-                    store_block<T>(stage, lane, out, OC, r0, nrow, c0 + j * 64 + 32, OC);
-                }
-            } else {
-                // output columns in the lanes; the tile's rows in blocks of 32, dealt to the warps g in turn
-                const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128) + sp * (SILU ? 16 : 32);
-                const int blocks = (t.nrow + 31) / 32;
-                uint4 gq[4], uq[4];
-                if (MODE == kRowsSilu && g < blocks) {   // gate and up of the first block, ahead of the products
-                    load_block<T>(gq, lane, gu_in, a.ld_gu, t.r0 + g * 32, t.nrow - g * 32, c0, OC);
-                    load_block<T>(uq, lane, gu_in + OC, a.ld_gu, t.r0 + g * 32, t.nrow - g * 32, c0, OC);
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
-                if (!ok) break;
-                tc_fence_after();
-                for (int blk = g; blk < blocks; blk += 2) {
-                    float v[32];
-                    tmem_ld32(lane_base + buf * XN + blk * 32, v);
-                    const int64_t r0 = t.r0 + blk * 32;
-                    const int nrow = t.nrow - blk * 32;
-                    if (SILU) {
-                        // lanes: a.turn gate columns, then the up columns of the same, and so on
-                        const bool up = (lane & a.turn) != 0;
-                        T* gu = static_cast<T*>(a.gate_up);
-                        if (gu) {
-                            put_column<T>(v, stage, lane);
-                            __syncwarp();
-                            // 16-byte piece q of a staged row: columns 8q .. 8q + 7 of the lanes
-                            const int q = lane & 3, l = q * 8;
-                            const int col = c0 + (a.turn == 16 ? l & 15 : (l >> 4) * 8);
-                            if (col < OC) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int r = i * 8 + (lane >> 2);
-                                    if (r < nrow)
-                                        *reinterpret_cast<uint4*>(gu + (r0 + r) * (2 * OC) + col + ((l & a.turn) ? OC : 0)) =
-                                            *reinterpret_cast<const uint4*>(stage + r * X_PITCH + q * 16);
-                                }
-                            }
-                            __syncwarp();
-                        }
-                        // a gate lane gives the up lane beside it its rows 16 .. 31 for that lane's up of rows
-                        // 0 .. 15: each then holds 16 rows of one column of h
-                        float h[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[16 + i], a.turn);
-                            const float gate = up ? o : v[i], u = up ? v[16 + i] : o;
-                            h[i] = gate / (1.0f + __expf(-gate)) * u;
-                        }
-                        // staged as [32 rows][16 columns]
-                        const int hc = a.turn == 16 ? lane & 15 : ((lane >> 4) * 8) + (lane & 7);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            *reinterpret_cast<T*>(stage + ((up ? 16 : 0) + i) * X_HPITCH + hc * 2) = from_f32<T>(h[i]);
-                        __syncwarp();
-                        const int hq = lane & 1;
-                        if (c0 + hq * 8 < OC) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int r = i * 16 + (lane >> 1);
-                                if (r < nrow)
-                                    *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + hq * 8) =
-                                        *reinterpret_cast<const uint4*>(stage + r * X_HPITCH + hq * 16);
-                            }
-                        }
-                        __syncwarp();
-                    } else if (MODE == kRowsSilu) {
-                        float gt[32], up[32];
-                        get_column<T>(gt, gq, stage, lane);
-                        get_column<T>(up, uq, stage, lane);
-                        if (blk + 2 < blocks) {
-                            load_block<T>(gq, lane, gu_in, a.ld_gu, r0 + 64, nrow - 64, c0, OC);
-                            load_block<T>(uq, lane, gu_in + OC, a.ld_gu, r0 + 64, nrow - 64, c0, OC);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float s = __fdividef(1.0f, 1.0f + __expf(-gt[i]));
-                            const float dup = v[i] * gt[i] * s;
-                            v[i] = v[i] * up[i] * s * (1.0f + gt[i] * (1.0f - s));
-                            up[i] = dup;
-                        }
-                        put_column<T>(v, stage, lane);
-                        store_block<T>(stage, lane, out, 2 * OC, r0, nrow, c0, OC);
-                        put_column<T>(up, stage, lane);
-                        store_block<T>(stage, lane, out + OC, 2 * OC, r0, nrow, c0, OC);
-                    } else {
-                        put_column<T>(v, stage, lane);
-                        store_block<T>(stage, lane, out, OC, r0, nrow, c0, OC);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
+                for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+                for (int blk = g; blk < blocks; blk += 2)
+                    store_column<T>(z, out + (row + blk * 32) * OC + col, OC, t.nrow - blk * 32, live);
+                continue;
             }
+            uint32_t gq[MODE == kRowsSilu ? 16 : 1], uq[MODE == kRowsSilu ? 16 : 1];
+            if constexpr (MODE == kRowsSilu) {   // gate and up of the first block, ahead of the products
+                load_column<T>(gq, gu_in + (row + g * 32) * a.ld_gu + col, a.ld_gu, t.nrow - g * 32, live);
+                load_column<T>(uq, gu_in + (row + g * 32) * a.ld_gu + OC + col, a.ld_gu, t.nrow - g * 32, live);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
+            if (!ok) break;
+            tc_fence_after();
+            for (int blk = g; blk < blocks; blk += 2) {
+                float v[32];
+                tmem_ld32(lane_base + buf * XN + blk * 32, v);
+                const int64_t r0 = row + blk * 32;
+                const int nrow = t.nrow - blk * 32;
+                if constexpr (SILU) {
+                    // lanes: a.turn gate columns, then the up columns of the same, and so on
+                    const bool up = (lane & a.turn) != 0;
+                    T* gu = static_cast<T*>(a.gate_up);
+                    if (gu) store_column<T>(v, gu + r0 * (2 * OC) + col + (up ? OC : 0), 2 * OC, nrow, live);
+                    // a gate lane gives the up lane beside it its rows 16 .. 31 for that lane's up of rows
+                    // 0 .. 15: each then holds 16 rows of one column of h
+                    const int first = up ? 16 : 0;
+                    T* h = out + (r0 + first) * OC + col;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[16 + i], a.turn);
+                        const float gate = up ? o : v[i], u = up ? v[16 + i] : o;
+                        if (live && first + i < nrow)
+                            h[static_cast<int64_t>(i) * OC] = from_f32<T>(__fdividef(gate, 1.0f + __expf(-gate)) * u);
+                    }
+                } else if constexpr (MODE == kRowsSilu) {
+                    float dup[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 gt = unpack2<T>(gq[i]), up = unpack2<T>(uq[i]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float gv = k ? gt.y : gt.x, uv = k ? up.y : up.x, d = v[2 * i + k];
+                            const float s = __fdividef(1.0f, 1.0f + __expf(-gv));
+                            dup[2 * i + k] = d * gv * s;
+                            v[2 * i + k] = d * uv * s * (1.0f + gv * (1.0f - s));
+                        }
+                    }
+                    if (blk + 2 < blocks) {
+                        load_column<T>(gq, gu_in + (r0 + 64) * a.ld_gu + col, a.ld_gu, nrow - 64, live);
+                        load_column<T>(uq, gu_in + (r0 + 64) * a.ld_gu + OC + col, a.ld_gu, nrow - 64, live);
+                    }
+                    store_column<T>(v, out + r0 * (2 * OC) + col, 2 * OC, nrow, live);
+                    store_column<T>(dup, out + r0 * (2 * OC) + OC + col, 2 * OC, nrow, live);
+                } else {
+                    store_column<T>(v, out + r0 * OC + col, OC, nrow, live);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
             buf ^= 1u;
             if (buf == 0) bphase ^= 1u;
         }
@@ -971,8 +872,8 @@ int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* rows_a, int6
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (num_rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(E) * N * K * 2, s));
     CUtensorMap tm[3];
-    if (map_16bit(&tm[0], dc, N, lddc, num_rows, 0, XK) != cudaSuccess ||
-        map_16bit(&tm[1], rows_a, K, lda, num_rows, 0, XK) != cudaSuccess)
+    if (map_16bit(&tm[0], rows_a, K, lda, num_rows, 0, XK) != cudaSuccess ||
+        map_16bit(&tm[1], dc, N, lddc, num_rows, 0, XK) != cudaSuccess)
         return MOE_ERR_CUDA;
     tm[2] = tm[1];   // not read
     const ExpertArgs a = {expert_offsets, E, num_rows, N, K, dw, nullptr, 0, 0, status};
