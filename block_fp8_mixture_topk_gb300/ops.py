@@ -6,6 +6,7 @@ torch.float8_e4m3fn), launched on torch's current stream.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import dataclasses
 import os
@@ -596,16 +597,16 @@ def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
         raise ValueError(f"topk_ids must be [{T}, topk], got {list(topk_ids.shape)}")
     k = topk_ids.shape[1]
     P = T * k
-    L = lib()
+    L, dev = lib(), x.device
     wsb = L.moe_dispatch_workspace_size(T, k, num_experts)
-    # one buffer: the tables, then the scratch
-    n = num_experts + 1
-    tables = torch.empty(max(n, 1) + 2 * P + (wsb + 3) // 4, dtype=torch.int32, device=x.device)
-    offsets, pair_ids, pos = tables[:n], tables[n:n + P], tables[n + P:n + 2 * P].view(T, k)
-    rows = torch.empty(P, H, dtype=x.dtype, device=x.device)
-    base = tables.data_ptr()
-    rc = L.moe_dispatch(x.data_ptr(), ld, code, topk_ids.data_ptr(), T, k, num_experts, H, rows.data_ptr(), base,
-                        base + 4 * n, base + 4 * (n + P), base + 4 * (n + 2 * P), wsb, _stream())
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    rows = torch.empty(P, H, dtype=x.dtype, device=dev)
+    offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int32, device=dev)
+    pair_ids = torch.empty(P, dtype=torch.int32, device=dev)
+    pos = torch.empty(T, k, dtype=torch.int32, device=dev)
+    rc = L.moe_dispatch(x.data_ptr(), ld, code, topk_ids.data_ptr(), T, k, num_experts, H, rows.data_ptr(),
+                        offsets.data_ptr(), pair_ids.data_ptr(), pos.data_ptr(), None if ws is None else ws.data_ptr(),
+                        wsb, _stream())
     _check("moe_dispatch", rc)
     return Dispatch(rows, offsets, pair_ids, pos)
 
@@ -691,13 +692,10 @@ def moe_pre_norm(x, weight, eps=1e-6, weight_offset=0.0):
     return h, rstd
 
 
-def _norm_sums(T, H, device, vectors=1):
-    """`vectors` fp32 [H] outputs and the scratch of a norm's gradient behind them, in one allocation:
-    the outputs and the scratch's address and size."""
+def _norm_workspace(T, H, device):
+    """Scratch of a norm's gradient and its size in bytes."""
     wsb = lib().moe_norm_backward_workspace_size(T, H)
-    buf = torch.empty(vectors * H + wsb // 4, dtype=torch.float32, device=device)
-    out = tuple(buf[i * H:(i + 1) * H] for i in range(vectors))
-    return (*out, buf.data_ptr() + 4 * vectors * H, wsb)
+    return torch.empty(wsb, dtype=torch.uint8, device=device), wsb
 
 
 def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0):
@@ -711,11 +709,12 @@ def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0
     if dresidual is not None:
         _, ldr = _rows(dresidual, "dresidual", x, (T, H))
         dres = dresidual.data_ptr()
-    L = lib()
     dx = torch.empty(T, H, dtype=x.dtype, device=x.device)
-    dw, ws, wsb = _norm_sums(T, H, x.device)
-    rc = L.moe_pre_norm_backward(dh.data_ptr(), ldd, x.data_ptr(), ldx, code, weight.data_ptr(), wcode, weight_offset,
-                                 rstd.data_ptr(), dres, ldr, T, H, dx.data_ptr(), dw.data_ptr(), ws, wsb, _stream())
+    dw = torch.empty(H, dtype=torch.float32, device=x.device)
+    ws, wsb = _norm_workspace(T, H, x.device)
+    rc = lib().moe_pre_norm_backward(dh.data_ptr(), ldd, x.data_ptr(), ldx, code, weight.data_ptr(), wcode, weight_offset,
+                                     rstd.data_ptr(), dres, ldr, T, H, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb,
+                                     _stream())
     _check("moe_pre_norm_backward", rc)
     return dx, dw
 
@@ -800,17 +799,15 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, 0.0, weight_offset)
     dy = torch.empty(T, H, dtype=y.dtype, device=y.device)
     dres = torch.empty_like(dy) if residual_grad else None
-    if gate_kind == "channel":
-        dw, dg, ws, wsb = _norm_sums(T, H, y.device, 2)
-    else:
-        dw, ws, wsb = _norm_sums(T, H, y.device)
-        dg = None if gate is None else torch.empty(gate.shape, dtype=gate.dtype, device=gate.device)
+    dw = torch.empty(H, dtype=torch.float32, device=y.device)
+    dg = None
+    if gate is not None:
+        dg = torch.empty(gate.shape, dtype=torch.float32 if gate_kind == "channel" else gate.dtype, device=gate.device)
+    ws, wsb = _norm_workspace(T, H, y.device)
     rc = lib().moe_post_norm_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, ctypes.byref(prm),
                                       rstd.data_ptr(), T, H, dy.data_ptr(), None if dres is None else dres.data_ptr(),
-                                      None if dg is None else dg.data_ptr(), dw.data_ptr(), ws, wsb, _stream())
+                                      None if dg is None else dg.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb, _stream())
     _check("moe_post_norm_backward", rc)
-    if gate_kind == "channel":
-        dg = dg.view(gate.shape)
     return PostNormGrads(dy, dw, dres, dg)
 
 
@@ -908,23 +905,33 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     if len(out) != len(grads):
         raise ValueError("out must hold one tensor per gradient")
     n = len(grads)
-    codes = []
-    for i, (g, o) in enumerate(zip(grads, out)):
-        codes.append(_typed(g, f"grads[{i}]"))
-        if not g.is_contiguous():
+    ptrs, sizes, codes = [], [], []
+    for i, g in enumerate(grads):
+        code = DTYPE.get(g.dtype)
+        if code is None or not g.is_cuda or not g.is_contiguous():
+            _typed(g, f"grads[{i}]")
             raise ValueError(f"grads[{i}] must be contiguous")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous()):
-            raise ValueError(f"out[{i}] must be a contiguous CUDA tensor like grads[{i}]")
+        ptrs.append(g.data_ptr())
+        sizes.append(g.numel())
+        codes.append(code)
+    outs = ptrs
+    if out is not grads:
+        outs = []
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be a contiguous CUDA tensor like grads[{i}]")
+            outs.append(o.data_ptr())
     device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
     L = lib()
     wsb = L.moe_clip_grads_workspace_size(n)
-    buf = torch.empty(wsb // 4 + 1, dtype=torch.float32, device=device)   # the scratch, then the norm
-    ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    outs = ptrs if out is grads else (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
-    rc = L.moe_clip_grads(ptrs, outs, (ctypes.c_int64 * n)(*[g.numel() for g in grads]), (ctypes.c_int32 * n)(*codes),
-                          n, kind, float(max_norm), float(eps), buf.data_ptr() + wsb, buf.data_ptr(), wsb, _stream())
+    ws = torch.empty(wsb, dtype=torch.uint8, device=device)
+    total = torch.empty((), dtype=torch.float32, device=device)
+    table, kinds = array.array("q", ptrs + outs + sizes), array.array("i", codes)   # host arrays of the C call
+    at = table.buffer_info()[0]
+    rc = L.moe_clip_grads(at, at + 8 * n, at + 16 * n, kinds.buffer_info()[0], n, kind, float(max_norm), float(eps),
+                          total.data_ptr(), ws.data_ptr(), wsb, _stream())
     _check("moe_clip_grads", rc)
-    return buf[wsb // 4]
+    return total
 
 
 def moe_selftest_bounded_wait(expire=True):
