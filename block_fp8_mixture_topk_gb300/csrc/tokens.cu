@@ -8,8 +8,11 @@
 //   dispatch, backward  dx[t] = sum_j drows[pos[t, j]]
 //
 // All four are bound by memory: every row is read or written once and the arithmetic is one fused
-// multiply-add per element.  Sums are fp32, in j order, rounded once to the rows' type; there are
-// no atomics on values, so results do not depend on the schedule.
+// multiply-add per element.  Rows of 16-byte addresses and strides move by bulk copies through
+// shared memory, with more than 100 KB in flight per SM: the dispatch copies a row in once and out topk
+// times without touching a register, the sums read a slab of columns of a token's topk rows at a time.
+// Sums are fp32, in j order, rounded once to the rows' type; there are no atomics on values, so
+// results do not depend on the schedule.
 #include "train.cuh"
 
 namespace mfp8 {
@@ -49,23 +52,93 @@ struct DispatchArgs {
     int32_t* expert_offsets;
     int32_t* pair_ids;
     int32_t* pos;
+    int piece, slots, ring;    // bulk copies: bytes of a piece of a row, slots of a warp's ring, their offset in shared memory
     uint32_t* status;
 };
+
+constexpr int kCopyWarps = 8;              // warps that issue bulk copies
+constexpr int kMostPiece = 8192;           // bytes of a piece of a row
+constexpr int kMostSlots = 8;
+constexpr int kSmemLimit = 232448, kStaticSmem = 2048;   // a CTA's shared memory; upper bound of what is declared statically
+
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t smem_src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// All but the last N of this thread's groups of bulk stores have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// One warp's share of a round's copies: pieces warp, warp + kCopyWarps, ... of the round's tokens (token
+// by token).  A ring of slots: lane 0 loads a piece, lanes j < topk store it to the pair's row; a slot
+// is loaded again some pieces after its stores were issued, once every lane has seen its store's read of
+// the slot finish.
+__device__ __forceinline__ void copy_round(const DispatchArgs& a, const int* pos_s, int64_t t0, int tokens, uint8_t* ring,
+                                           uint64_t* bars, uint32_t* phases, volatile int* abort_flag) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row_bytes = a.vecs * 16, pieces = (row_bytes + a.piece - 1) / a.piece, items = tokens * pieces;
+    auto load = [&](int i, int slot) {
+        const int t = i / pieces, c = (i - t * pieces) * a.piece;
+        const uint32_t bytes = row_bytes - c < a.piece ? row_bytes - c : a.piece;
+        const uint32_t b = smem_addr(bars + slot);
+        mbar_arrive_expect_tx(b, bytes);
+        bulk_load(smem_addr(ring + slot * a.piece), a.x + (t0 + t) * a.ld_bytes + c, bytes, b);
+    };
+    const int n = items > warp ? (items - warp + kCopyWarps - 1) / kCopyWarps : 0;   // this warp's pieces
+    if (lane == 0)
+        for (int k = 0; k < a.slots && k < n; ++k) load(warp + k * kCopyWarps, k);
+    const int lag = a.slots >= 4 ? 2 : a.slots >= 2 ? 1 : 0;   // pieces between a store and its slot's next load
+    int slot = 0;
+    for (int k = 0; k < n; ++k) {
+        mbar_wait(smem_addr(bars + slot), (*phases >> slot) & 1u, abort_flag, a.status);
+        *phases ^= 1u << slot;
+        const int i = warp + k * kCopyWarps, t = i / pieces, c = (i - t * pieces) * a.piece;
+        const uint32_t bytes = row_bytes - c < a.piece ? row_bytes - c : a.piece;
+        if (lane < a.topk) {
+            const int r = pos_s[t * a.topk + lane];
+            if (r >= 0) bulk_store(a.rows + static_cast<int64_t>(r) * row_bytes + c, smem_addr(ring + slot * a.piece), bytes);
+        }
+        bulk_commit();
+        if (k >= lag) {
+            if (lag == 2) bulk_wait_read<2>();
+            else if (lag == 1) bulk_wait_read<1>();
+            else bulk_wait_read<0>();
+            __syncwarp();
+            const int next = k - lag + a.slots;   // the slot of piece k - lag takes it
+            if (lane == 0 && next < n) load(warp + next * kCopyWarps, (k - lag) % a.slots);
+        }
+        if (++slot == a.slots) slot = 0;
+    }
+    bulk_wait_read<0>();
+    __syncwarp();
+}
 
 // The sort and the copies of one chunk of tokens and one slab of columns.  Every CTA derives the
 // first row of its chunk for each expert from the pair counts (a scan over experts of the totals,
 // plus the pairs of earlier chunks), ranks its pairs with a warp match, and copies its tokens: a
 // row is read once and written topk times.  The slab-0 CTAs also write the tables.
-template <class R>
+template <class R, bool BULK>
 __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchArgs a) {
-    extern __shared__ int smem[];
+    extern __shared__ __align__(128) int smem[];
     int* before = smem;                    // [E] pairs of earlier chunks, then the next row of each expert
     int* after = smem + a.E;               // [E] pairs of this and later chunks
     int* pos_s = smem + 2 * a.E;           // [kSortThreads] rows of the current round's pairs
     int16_t* warp_count = reinterpret_cast<int16_t*>(pos_s + kSortThreads);   // [32][E]
     __shared__ int warp_sums[32];
     __shared__ int total_s;
+    __shared__ uint64_t bars[kCopyWarps * kMostSlots];
+    __shared__ int abort_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t phases = 0;
+    if (BULK && tid < kCopyWarps * kMostSlots) mbar_init(smem_addr(bars + tid), 1);
+    if (tid == 0) {
+        abort_s = 0;
+        fence_barrier_init();
+    }
     for (int e = tid; e < 2 * a.E; e += kSortThreads) smem[e] = 0;
     __syncthreads();
     grid_dependency_wait();
@@ -147,6 +220,13 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
         }
         const int tokens = n / a.topk;
         const int64_t t0 = r0 / a.topk;
+        if constexpr (BULK) {
+            if (warp < kCopyWarps)
+                copy_round(a, pos_s, t0, tokens, reinterpret_cast<uint8_t*>(smem) + a.ring + warp * a.slots * a.piece,
+                           bars + warp * kMostSlots, &phases, &abort_s);
+            __syncthreads();
+            continue;
+        }
         const int items = tokens * nv;
         constexpr int U = 4;
         for (int i = tid; i < items; i += U * kSortThreads) {
@@ -170,6 +250,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
         }
         __syncthreads();
     }
+    if constexpr (BULK) bulk_wait_all();
     // rows of no pair (as many as there are pairs without an expert): zero, at the end
     const int64_t left = (a.P - total) * nv;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < left;
@@ -226,6 +307,129 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y, i
 #pragma unroll
     for (int e = 0; e < V; ++e) o.set(e, acc[e]);
     o.store(out + (t * vecs + v) * V);
+}
+
+// The same for rows of 16-byte addresses and strides and many tokens.  A CTA holds groups of G threads; a
+// group walks over items (token, slab of G vectors), its first warp keeping `depth` items of bulk
+// copies ahead: lane j < topk brings pair j's piece of the slab, the pairs without a row left out.
+// Each thread then sums one vector over the token's rows from shared memory.
+struct CombineArgs {
+    const char* y;
+    int64_t ld_bytes;
+    const int32_t* pos;
+    const float* w;
+    int64_t tokens;
+    int topk, vecs, slabs, G, depth;
+    int64_t num_rows;
+    char* out;
+    uint32_t* status;
+};
+constexpr int kCombineThreads = 512, kCombineGroups = 15, kCombineDepth = 8;
+constexpr int kCombineMeta = (MOE_MAX_TOPK + 4) * 4;   // of a slot: the weights of its pieces, then their number
+
+// A place in the items of a group: token and slab, moved on by a fixed number of items.
+struct CombineAt {
+    int64_t t;
+    int s;
+    __device__ __forceinline__ void next(int64_t step_t, int step_s, int slabs) {
+        t += step_t;
+        s += step_s;
+        if (s >= slabs) {
+            s -= slabs;
+            ++t;
+        }
+    }
+};
+
+template <class T>
+__global__ void __launch_bounds__(kCombineThreads) combine_ring_kernel(const CombineArgs a) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    extern __shared__ __align__(128) uint8_t ring_smem[];
+    __shared__ uint64_t bars[kCombineGroups * kCombineDepth];
+    __shared__ int abort_s;
+    const int G = a.G, R = blockDim.x / G, g = threadIdx.x / G, tid = threadIdx.x - g * G, lane = threadIdx.x & 31;
+    const int slot_bytes = a.topk * G * 16 + kCombineMeta, piece = G * 16;
+    uint8_t* ring = ring_smem + static_cast<size_t>(g) * a.depth * slot_bytes;
+    uint64_t* bar = bars + g * kCombineDepth;
+    if (threadIdx.x < kCombineGroups * kCombineDepth) mbar_init(smem_addr(bars + threadIdx.x), 1);
+    if (threadIdx.x == 0) {
+        abort_s = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R, first = static_cast<int64_t>(blockIdx.x) * R + g;
+    const int64_t step_t = step / a.slabs;
+    const int step_s = static_cast<int>(step - step_t * a.slabs);
+    CombineAt now = {first / a.slabs, static_cast<int>(first % a.slabs)}, load = now;
+    // first warp: row and weight of this lane's pair in the item to load next, fetched one item early
+    int64_t row = -1;
+    float weight = 1.0f;
+    auto fetch = [&] {
+        row = -1;
+        if (lane < a.topk && load.t < a.tokens) {
+            row = a.pos[load.t * a.topk + lane];
+            if (a.w) weight = a.w[load.t * a.topk + lane];
+        }
+    };
+    auto issue = [&](int slot) {
+        if (load.t >= a.tokens) return;
+        const int v0 = load.s * G, nv = a.vecs - v0 < G ? a.vecs - v0 : G;
+        if (row >= a.num_rows) {
+            if (v0 == 0) status_set(a.status, MOE_STATUS_BAD_EXPERT_ID);
+            row = -1;
+        }
+        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+        const int at = __popc(live & ((1u << lane) - 1)), n = __popc(live);
+        uint8_t* s = ring + static_cast<size_t>(slot) * slot_bytes;
+        float* meta = reinterpret_cast<float*>(s + a.topk * piece);
+        if (row >= 0) meta[at] = weight;
+        if (lane == 0) reinterpret_cast<int*>(meta)[MOE_MAX_TOPK] = n;
+        __syncwarp();
+        const uint32_t b = smem_addr(bar + slot);
+        if (lane == 0) mbar_arrive_expect_tx(b, n * nv * 16);
+        __syncwarp();
+        if (row >= 0) bulk_load(smem_addr(s + at * piece), a.y + row * a.ld_bytes + static_cast<int64_t>(v0) * 16, nv * 16, b);
+        load.next(step_t, step_s, a.slabs);
+        fetch();
+    };
+    if (tid < 32) {
+        fetch();
+        for (int d = 0; d < a.depth; ++d) issue(d);
+    }
+    int slot = 0;
+    uint32_t phase = 0;
+    for (; now.t < a.tokens; now.next(step_t, step_s, a.slabs)) {
+        mbar_wait(smem_addr(bar + slot), phase, &abort_s, a.status);
+        const int v = now.s * G + tid;
+        const uint8_t* s = ring + static_cast<size_t>(slot) * slot_bytes;
+        const float* meta = reinterpret_cast<const float*>(s + a.topk * piece);
+        const int n = reinterpret_cast<const int*>(meta)[MOE_MAX_TOPK];
+        if (v < a.vecs) {
+            float2 acc[V / 2];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) acc[e] = both(0.0f);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                Pack<T, V> x;
+                x.raw = *reinterpret_cast<const uint4*>(s + j * piece + tid * 16);
+                const float2 w = both(meta[j]);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) acc[e] = fma2(w, x.pair(e), acc[e]);
+            }
+            Pack<T, V> o;
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) o.set_pair(e, acc[e]);
+            *reinterpret_cast<uint4*>(a.out + (now.t * a.vecs + v) * 16) = o.raw;
+        }
+        if (G == 32) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(G) : "memory");
+        if (tid < 32) issue(slot);
+        if (++slot == a.depth) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
 }
 
 // One warp per pair: dy[pos] = w * dout[t] and dw = <dout[t], y[pos]>.  The pairs of one token are
@@ -323,7 +527,18 @@ size_t dispatch_smem(int E) { return (2 * E + kSortThreads) * 4 + 32 * static_ca
 
 template <class R>
 cudaError_t launch_dispatch(const DispatchArgs& a, dim3 grid, cudaStream_t stream) {
-    return launch_pdl(dispatch_kernel<R>, grid, dim3(kSortThreads), dispatch_smem(a.E), stream, a);
+    return launch_pdl(dispatch_kernel<R, false>, grid, dim3(kSortThreads), dispatch_smem(a.E), stream, a);
+}
+// With bulk copies: one CTA per SM, what the sort leaves of its shared memory divided among the
+// copying warps.
+cudaError_t launch_dispatch_bulk(DispatchArgs a, dim3 grid, cudaStream_t stream) {
+    const int row_bytes = a.vecs * 16, pieces = (row_bytes + kMostPiece - 1) / kMostPiece;
+    a.piece = ((row_bytes + pieces - 1) / pieces + 15) / 16 * 16;
+    a.ring = static_cast<int>((dispatch_smem(a.E) + 127) / 128 * 128);
+    a.slots = (kSmemLimit - kStaticSmem - a.ring) / (kCopyWarps * a.piece);
+    if (a.slots > kMostSlots) a.slots = kMostSlots;
+    return launch_pdl(dispatch_kernel<uint4, true>, grid, dim3(kSortThreads),
+                      static_cast<size_t>(a.ring) + static_cast<size_t>(kCopyWarps) * a.slots * a.piece, stream, a);
 }
 
 template <class T, int V>
@@ -332,6 +547,26 @@ cudaError_t launch_combine(const void* y, int64_t ld, const int32_t* pos, const 
     const int64_t n = T_ * (H / V);
     return launch_pdl(combine_kernel<T, V>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
                       static_cast<const T*>(y), ld, pos, w, T_, topk, H / V, num_rows, static_cast<T*>(out), status);
+}
+
+// Whether the ring takes a combine: enough items to fill every group's ring; and its launch.
+bool combine_ring_shape(int64_t T_, int topk, int vecs, CombineArgs* a, int* groups) {
+    int G = topk <= 8 ? 128 : topk <= 16 ? 64 : 32;
+    while (G > 32 && G / 2 >= vecs) G /= 2;
+    const int slot = topk * G * 16 + kCombineMeta;
+    int R = kCombineThreads / G < kCombineGroups ? kCombineThreads / G : kCombineGroups;
+    const int room = kSmemLimit - kStaticSmem;
+    while (R > 1 && 2 * R * slot > room) --R;
+    a->G = G;
+    a->slabs = (vecs + G - 1) / G;
+    a->depth = room / (R * slot) < kCombineDepth ? room / (R * slot) : kCombineDepth;
+    *groups = R;
+    return T_ * a->slabs >= 2ll * R * kPlanSms;
+}
+template <class T>
+cudaError_t launch_combine_ring(const CombineArgs& a, int groups, cudaStream_t stream) {
+    const size_t smem = static_cast<size_t>(groups) * a.depth * (a.topk * a.G * 16 + kCombineMeta);
+    return launch_pdl(combine_ring_kernel<T>, dim3(kPlanSms), dim3(groups * a.G), smem, stream, a);
 }
 
 template <class T, int V>
@@ -366,17 +601,29 @@ int check_rows(int T, int topk, int H, int64_t ld, int64_t num_rows, int dtype) 
     return MOE_OK;
 }
 
+template <class T>
+cudaError_t combine_ring_init() {
+    return cudaFuncSetAttribute(combine_ring_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmemLimit - kStaticSmem);
+}
+
 }  // namespace
 
 cudaError_t tokens_init_device() {
     const int bytes = static_cast<int>(dispatch_smem(MOE_MAX_EXPERTS));
-    cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<uint4>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<uint4, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dispatch_kernel<uint2>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(dispatch_kernel<uint2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dispatch_kernel<uint32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(dispatch_kernel<uint32_t, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dispatch_kernel<uint16_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(dispatch_kernel<uint16_t, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(dispatch_kernel<uint4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemLimit - kStaticSmem);
+    if (e == cudaSuccess) e = combine_ring_init<float>();
+    if (e == cudaSuccess) e = combine_ring_init<__half>();
+    if (e == cudaSuccess) e = combine_ring_init<__nv_bfloat16>();
     return e;
 }
 
@@ -444,7 +691,7 @@ int moe_dispatch(const void* x, int64_t ldx, int dtype, const int32_t* topk_ids,
     const dim3 grid(static_cast<unsigned>(d.nch), static_cast<unsigned>(slabs));
     if (e == cudaSuccess) {
         switch (vb) {
-            case 16: e = launch_dispatch<uint4>(a, grid, s); break;
+            case 16: e = slabs > 1 ? launch_dispatch<uint4>(a, grid, s) : launch_dispatch_bulk(a, grid, s); break;
             case 8: e = launch_dispatch<uint2>(a, grid, s); break;
             case 4: e = launch_dispatch<uint32_t>(a, grid, s); break;
             default: e = launch_dispatch<uint16_t>(a, grid, s); break;
@@ -465,6 +712,26 @@ int moe_combine(const void* y, int64_t ldy, int dtype, const int32_t* pos, const
     const int es = static_cast<int>(dtype_bytes(dtype));
     const int vb = vector_bytes(static_cast<int64_t>(H) * es,
                                 address(y) | address(out) | static_cast<uintptr_t>(ldy * es), es);
+    if (vb == 16) {
+        CombineArgs a = {};
+        int groups = 0;
+        a.vecs = H * es / 16;
+        if (combine_ring_shape(T, topk, a.vecs, &a, &groups)) {
+            a.y = static_cast<const char*>(y);
+            a.ld_bytes = ldy * es;
+            a.pos = pos;
+            a.w = weights;
+            a.tokens = T;
+            a.topk = topk;
+            a.num_rows = num_rows;
+            a.out = static_cast<char*>(out);
+            a.status = status;
+            cudaStream_t s = static_cast<cudaStream_t>(stream);
+            return cuda_status(dtype == MOE_DTYPE_FP32   ? launch_combine_ring<float>(a, groups, s)
+                               : dtype == MOE_DTYPE_FP16 ? launch_combine_ring<__half>(a, groups, s)
+                                                         : launch_combine_ring<__nv_bfloat16>(a, groups, s));
+        }
+    }
     return cuda_status(MOE_BY_TYPE(launch_combine, dtype, vb, y, ldy, pos, weights, T, topk, H, num_rows, out, status,
                                    static_cast<cudaStream_t>(stream)));
 }

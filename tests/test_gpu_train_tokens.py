@@ -62,6 +62,10 @@ CASES = [  # T, k, E, H, drop, skew
     (2049, 8, 257, 40, 0.02, False),      # more pairs than one launch counts
     (5000, 7, 1024, 9, 0.02, True),
     (9001, 4, 3, 16, 0.0, True),
+    (700, 3, 16, 7168, 0.1, False),       # rows in several pieces; many slabs of columns
+    (3000, 8, 1024, 1032, 0.1, True),
+    (1500, 20, 64, 264, 0.05, True),
+    (400, 32, 40, 4096, 0.3, False),
 ]
 
 
@@ -225,6 +229,27 @@ def test_infinities_and_nan_stay_in_their_rows():
     dy, dw = moe.moe_combine_backward(torch.ones(3, 8, device="cuda"), y, d.pos, d.pair_ids, one)
     assert torch.isfinite(dy).all() and torch.equal(dy[5], torch.zeros(8, device="cuda"))
     assert torch.isinf(dw[0, 0]) and dw[1, 1].item() == 0
+
+
+def test_many_rows_of_no_pair_are_not_read():
+    """The same in the kernel that many tokens take."""
+    g = gen(41)
+    T, k, H = 4000, 4, 512
+    ids = make_ids(g, T, k, 8, 0.3).cuda()
+    x, w = rand(g, T, H, dtype=torch.bfloat16), rand(g, T, k)
+    d = moe.moe_dispatch(x, ids, 8)
+    n = d.expert_offsets[8].item()
+    y = d.rows.clone()
+    y[n:] = float("nan")
+    out, size = combine_ref(d.rows, d.pos, w)
+    check(moe.moe_combine(y, d.pos, w), out, size, k + 1, "out")
+    pos = d.pos.clone()
+    pos[7, 2], pos[3999, 0] = T * k, 2 ** 31 - 1
+    status_clear()
+    got = moe.moe_combine(y, pos, w)
+    assert status() == 2
+    pos[7, 2], pos[3999, 0] = -1, -1
+    assert torch.equal(got, moe.moe_combine(y, pos, w)) and status() == 0
 
 
 def test_rows_past_the_matrix_are_reported():
