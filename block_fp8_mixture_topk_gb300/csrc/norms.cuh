@@ -74,6 +74,10 @@ __device__ __forceinline__ float2 sigmoid_as(float2 v) {
 struct Group {
     float* red;       // [2][16] of this group
     int G, tid, id, parity;
+    __device__ __forceinline__ void sync() const {
+        if (G == 32) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(G) : "memory");
+    }
     __device__ __forceinline__ float sum(float v) {
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
@@ -114,8 +118,7 @@ __device__ __forceinline__ void load_row(Pack<T, V> (&r)[NV], const T* p, int ti
 // ---------------------------------------------------------------- sources of rows
 // A source hands out a group's rows of NIN matrices and a row of weights (fp32): start() and weights()
 // once, then for each row fetch(t), get(n, i) = vector i of this thread in matrix n (any number of
-// times) and, after the group's barrier in that row, next() (the row before is done with); finish()
-// at the end.  weight(i) = the weights of vector i.
+// times) and next() (the row is done with); finish() at the end.  weight(i) = the weights of vector i.
 template <int V>
 struct Weights {
     float2 v[(V + 1) / 2];
@@ -154,7 +157,7 @@ struct RowRegs {
         for (int n = 0; n < NIN; ++n) load_row<T, V, NV>(r[n], src[n] + t * ld[n], tid, G, nvec);
     }
     __device__ __forceinline__ Pack<T, V> get(int n, int i) const { return r[n][i]; }
-    __device__ __forceinline__ void next() {}
+    __device__ __forceinline__ void next(const Group&) {}
     __device__ __forceinline__ void finish() {}
 };
 
@@ -173,7 +176,6 @@ struct RowRing {
     uint32_t row_bytes;
     int depth, slot, load_slot, G, tid, nvec;
     uint32_t phase, issued;
-    bool first;
 
     __device__ __forceinline__ void issue() {
         if (t_load < t_end) {
@@ -236,7 +238,6 @@ struct RowRing {
         load_slot = 0;
         phase = 1;
         issued = 0;
-        first = true;
         for (int i = 0; i < depth; ++i) issue();
     }
     // (a wait that gave up leaves its status bit and wrong values, and all later waits return at
@@ -256,10 +257,10 @@ struct RowRing {
         else p.zero();
         return p;
     }
-    // every thread of the group has finished the row before this one: its slot takes the next row
-    __device__ __forceinline__ void next() {
-        if (!first) issue();
-        first = false;
+    // the group is done with the row: its slot takes the next one
+    __device__ __forceinline__ void next(const Group& g) {
+        g.sync();
+        issue();
     }
     __device__ __forceinline__ void finish() {
         if (*abort_flag && tid == 0)   // loads may be under way: let them land
@@ -309,7 +310,6 @@ __global__ void __launch_bounds__(Rows<T, V, NV, 1>::kWide ? kNormWideThreads : 
             for (int e = 0; e < NP; ++e) ss = fma2(x.pair(e), x.pair(e), ss);
         }
         const float r = __frsqrt_rn(g.sum(ss.x + ss.y) / static_cast<float>(a.H) + a.eps);
-        in.next();
         if (g.tid == 0) a.rstd[t] = r;
         T* out = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(Rows<T, V, NV, 1>::kWide ? kNormWideThreads : 
             for (int e = 0; e < NP; ++e) o.set_pair(e, mul2(mul2(x.pair(e), both(r)), w.v[e]));
             o.store(out + static_cast<int64_t>(v) * V);
         }
+        in.next(g);
     }
     in.finish();
 }
@@ -373,7 +374,6 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
             for (int e = 0; e < NP; ++e) ss = fma2(y.pair(e), y.pair(e), ss);
         }
         const float r = __frsqrt_rn(g.sum(ss.x + ss.y) / static_cast<float>(a.H) + a.eps);
-        in.next();
         if (g.tid == 0) a.rstd[t] = r;
         T* out = static_cast<T*>(a.out) + t * a.H;
         float2 s2 = both(0.0f);
@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
             }
             if (v < nvec) s[i].store(out + static_cast<int64_t>(v) * V);
         }
+        in.next(g);
         if constexpr (NEXT) {
             const float r2 = __frsqrt_rn(g.sum(s2.x + s2.y) / static_cast<float>(a.H) + a.eps);
             if (g.tid == 0) a.rstd2[t] = r2;
@@ -473,7 +474,6 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
             }
         }
         const float m = g.sum(m2.x + m2.y) / static_cast<float>(a.H);
-        in.next();
         T* out = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
             }
             o.store(out + static_cast<int64_t>(v) * V);
         }
+        in.next(g);
     }
     in.finish();
     write_partial<V, NV>(acc, 1.0f, reinterpret_cast<float*>(norm_smem), g, R, nvec,
@@ -555,7 +556,6 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
             }
         }
         const float sum = g.sum(m2.x + m2.y);
-        in.next();
         if constexpr (GATE == kGateRow)
             if (a.dgate && g.tid == 0) static_cast<T*>(a.dgate)[t] = from_f32<T>(slope * a.b * sum);
         const float2 scale = both(a.b * gr * r), m = both(-(sum / static_cast<float>(a.H)));   // scale: of t / w
@@ -589,6 +589,7 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
             if constexpr (FULL)
                 if (a.dgate) q.store(static_cast<T*>(a.dgate) + t * a.H + at);
         }
+        in.next(g);
     }
     in.finish();
     write_partial<V, NV>(acc, GATE == kGateChannel ? 1.0f : a.b, reinterpret_cast<float*>(norm_smem), g, R, nvec,
