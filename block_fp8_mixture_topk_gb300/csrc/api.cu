@@ -44,7 +44,7 @@ int device_state(DeviceState** out) {
             if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess || route_init_device() != cudaSuccess ||
                 permute_init_device() != cudaSuccess || gemm_init_device() != cudaSuccess ||
                 decode_init_device() != cudaSuccess || tokens_init_device() != cudaSuccess ||
-                experts_init_device() != cudaSuccess) {
+                experts_init_device() != cudaSuccess || clip_init_device() != cudaSuccess) {
                 cudaGetLastError();
                 return MOE_ERR_CUDA;
             }

@@ -5,11 +5,12 @@
 // Bound by memory: one pass reads the gradients for the norm, a second reads and writes them.  The
 // tensors' addresses travel in the kernels' parameters (up to kMostTensors per launch), so nothing
 // is copied to the device and a captured graph holds its own copy.  The tensors are cut into
-// chunks; CTA c takes chunks c, c + CTAs, ... and leaves one partial result, and every CTA of the
-// scaling kernel joins all partials in one order: the result does not depend on the schedule.
-// Squares are summed in fp32 within a thread's share of a chunk and in fp64 beyond it; a share
-// whose largest magnitude lies outside 1e-18 .. 1e18, where fp32 squares overflow or vanish, is
-// summed again in fp64.
+// chunks of 8 KB; warp w of all warps takes chunks w, w + warps, ... through a ring of 2 KB bulk copies
+// of its own (192 KB in flight per SM, no barrier between warps).  Every CTA leaves one partial
+// result, and every CTA of the scaling kernel joins all partials in one order: the result does not
+// depend on the schedule.  Squares are summed in fp32 within a lane's share of a chunk and in fp64
+// beyond it; a share whose largest magnitude lies outside 1e-18 .. 1e18, where fp32 squares
+// overflow or vanish, is summed again in fp64.
 #include <math.h>
 
 #include "train.cuh"
@@ -18,11 +19,12 @@ namespace mfp8 {
 namespace {
 
 constexpr int kClipThreads = 512;
-constexpr int kVecs = 4;                  // 16-byte vectors of a thread's share
-constexpr int kChunkBytes = kClipThreads * kVecs * 16;
+constexpr int kClipWarps = kClipThreads / 32;
+constexpr int kChunkBytes = 8192, kPiece = 2048;
+constexpr int kSlots = 6;                 // pieces of a warp's ring
+constexpr int kRingBytes = kClipWarps * kSlots * kPiece;
 constexpr int kMostTensors = 960;         // per launch: their table fits the 32,764 bytes of kernel parameters
-constexpr int kClipCtasPerSm = 3;
-constexpr int kMostCtas = kPlanSms * kClipCtasPerSm;   // partial results
+constexpr int kMostCtas = kPlanSms;       // partial results of a launch
 
 template <int N>
 struct ClipTable {
@@ -61,108 +63,199 @@ __device__ __forceinline__ double join_cta(double acc, int inf, double* warp_s) 
     if ((threadIdx.x & 31) == 0) warp_s[threadIdx.x >> 5] = acc;
     __syncthreads();
     acc = warp_s[0];
-    for (int w = 1; w < kClipThreads / 32; ++w) acc = join(acc, warp_s[w], inf);
+    for (int w = 1; w < kClipWarps; ++w) acc = join(acc, warp_s[w], inf);
     return acc;
 }
 
-// One thread's elements of a chunk: the vectors tid, tid + threads, ... of an aligned tensor, single
-// elements otherwise and past the last whole vector.  f(value) is called for each.
-template <class T, class F>
-__device__ __forceinline__ void each_element(const T* p, int64_t n, bool wide, F f) {
-    constexpr int V = 16 / static_cast<int>(sizeof(T));
-    int64_t tail = 0;
-    if (wide) {
-        const int64_t nv = n / V;
-        Pack<T, V> x[kVecs];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int64_t v = threadIdx.x + i * kClipThreads;
-            if (v < nv) x[i].load(p + v * V);
-            else x[i].zero();
-        }
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-            for (int e = 0; e < V; ++e) f(x[i].get(e));
-        tail = nv * V;
-    }
-    for (int64_t i = tail + threadIdx.x; i < n; i += kClipThreads) f(to_f32(p[i]));
+// A chunk: n elements of tensor k from element e0; bytes of it that come by bulk copies (none where an
+// address of the tensor is not a multiple of 16).
+struct Chunk {
+    int k;
+    int64_t e0;
+    int n, bulk;
+};
+template <int N>
+__device__ __forceinline__ Chunk chunk_at(const ClipTable<N>& t, int64_t c) {
+    Chunk u;
+    u.k = tensor_of(t, c);
+    const int es = t.dtype[u.k] == MOE_DTYPE_FP32 ? 4 : 2, per = kChunkBytes / es;
+    u.e0 = (c - t.chunk0[u.k]) * per;
+    const int64_t left = t.numel[u.k] - u.e0;
+    u.n = left < per ? static_cast<int>(left) : per;
+    u.bulk = (reinterpret_cast<uintptr_t>(t.src[u.k]) | reinterpret_cast<uintptr_t>(t.dst[u.k])) & 15 ? 0 : u.n * es / 16 * 16;
+    return u;
 }
 
-template <class T>
-__device__ __forceinline__ double share_norm(const T* p, int64_t n, bool wide, bool inf) {
+// A warp's ring of pieces.  The chunks are index(0), index(1), ... of this warp; issue() brings the
+// next piece of the next chunk that has one.
+template <int N, bool REVERSE>
+struct ClipRing {
+    const ClipTable<N>& t;
+    uint8_t* ring;
+    uint64_t* bars;
+    volatile int* abort_flag;
+    uint32_t* status;
+    int64_t chunks, next;      // next: chunk after the one being loaded (in this warp's order)
+    int stride, slot, load_slot, left;
+    uint32_t phase, issued;
+    const char* src;
+
+    __device__ __forceinline__ ClipRing(const ClipTable<N>& table, uint8_t* smem, uint64_t* barriers, volatile int* flag,
+                                        uint32_t* st)
+        : t(table), abort_flag(flag), status(st) {
+        const int warp = threadIdx.x >> 5;
+        ring = smem + warp * kSlots * kPiece;
+        bars = barriers + warp * kSlots;
+        chunks = t.chunk0[t.n];
+        next = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+        stride = gridDim.x * kClipWarps;
+        slot = load_slot = left = 0;
+        phase = issued = 0;
+        for (int i = 0; i < kSlots; ++i) issue();
+    }
+    __device__ __forceinline__ int64_t index(int64_t c) const { return REVERSE ? chunks - 1 - c : c; }
+    __device__ __forceinline__ void issue() {
+        while (left == 0 && next < chunks) {
+            const Chunk u = chunk_at(t, index(next));
+            src = static_cast<const char*>(t.src[u.k]) + u.e0 * (t.dtype[u.k] == MOE_DTYPE_FP32 ? 4 : 2);
+            left = u.bulk;
+            next += stride;
+        }
+        if (left == 0) return;
+        const int bytes = left < kPiece ? left : kPiece;
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t b = smem_addr(bars + load_slot);
+            mbar_arrive_expect_tx(b, bytes);
+            bulk_load(smem_addr(ring + load_slot * kPiece), src, bytes, b);
+        }
+        ++issued;
+        src += bytes;
+        left -= bytes;
+        if (++load_slot == kSlots) load_slot = 0;
+    }
+    // After a wait that gave up (its status bit is set, values are wrong): let the loads under way land.
+    __device__ __forceinline__ void finish() const {
+        if (*abort_flag && (threadIdx.x & 31) == 0)
+            for (int i = 0; i < kSlots; ++i) {
+                const uint32_t n = (issued + kSlots - 1 - i) / kSlots;
+                if (n > 0) mbar_wait(smem_addr(bars + i), (n - 1) & 1u, nullptr, status);
+            }
+    }
+    // This lane's vectors of a piece of nv, f(vector index, vector) each; then the slot takes the next piece.
+    template <class T, class F>
+    __device__ __forceinline__ void piece(int nv, F f) {
+        constexpr int V = 16 / static_cast<int>(sizeof(T));
+        mbar_wait(smem_addr(bars + slot), phase, abort_flag, status);
+        Pack<T, V> x[kPiece / 512];
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < kPiece / 512; ++i)
+            if (lane + i * 32 < nv) x[i].raw = *reinterpret_cast<const uint4*>(ring + slot * kPiece + (lane + i * 32) * 16);
+        __syncwarp();
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+        issue();
+#pragma unroll
+        for (int i = 0; i < kPiece / 512; ++i)
+            if (lane + i * 32 < nv) f(lane + i * 32, x[i]);
+    }
+};
+
+// This lane's share of a chunk: sum of squares, or the largest magnitude.
+template <class T, class R>
+__device__ __forceinline__ double share_norm(R& ring, const T* p, const Chunk& u, int inf) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const int lane = threadIdx.x & 31, nv = u.bulk / 16;
     float ss = 0.0f, top = 0.0f;
-    each_element<T>(p, n, wide, [&](float v) {
+    for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
+        ring.template piece<T>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int, const Pack<T, V>& x) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const float v = x.get(e);
+                ss = fmaf(v, v, ss);
+                top = max_nan(top, fabsf(v));
+            }
+        });
+    for (int i = nv * V + lane; i < u.n; i += 32) {
+        const float v = to_f32(p[i]);
         ss = fmaf(v, v, ss);
         top = max_nan(top, fabsf(v));
-    });
+    }
     if (inf) return top;
     if (top > 1e18f || (top < 1e-18f && top > 0.0f)) {
         double sd = 0.0;
-        each_element<T>(p, n, wide, [&](float v) { sd = fma(static_cast<double>(v), static_cast<double>(v), sd); });
+        for (int v = lane; v < nv; v += 32)
+            for (int e = 0; e < V; ++e) {
+                const double x = to_f32(p[v * V + e]);
+                sd = fma(x, x, sd);
+            }
+        for (int i = nv * V + lane; i < u.n; i += 32) {
+            const double x = to_f32(p[i]);
+            sd = fma(x, x, sd);
+        }
         return sd;
     }
     return ss;
 }
 
-// The partial result of CTA b: sum of squares (or largest magnitude) of chunks b, b + CTAs, ...
-template <int N>
-__global__ void __launch_bounds__(kClipThreads)
-    grad_norm_kernel(const __grid_constant__ ClipTable<N> t, int inf, double* __restrict__ partial) {
-    __shared__ double warp_s[kClipThreads / 32];
+#define MOE_CLIP_PROLOGUE                                                       \
+    extern __shared__ __align__(128) uint8_t clip_smem[];                       \
+    __shared__ double warp_s[kClipWarps];                                       \
+    __shared__ uint64_t bars[kClipWarps * kSlots];                              \
+    __shared__ int abort_s;                                                     \
+    if (threadIdx.x < kClipWarps * kSlots) mbar_init(smem_addr(bars + threadIdx.x), 1); \
+    if (threadIdx.x == 0) {                                                     \
+        abort_s = 0;                                                            \
+        fence_barrier_init();                                                   \
+    }                                                                           \
+    __syncthreads();                                                            \
     grid_dependency_wait();
+
+// The partial result of a CTA: sum of squares (or largest magnitude) of its warps' chunks.
+template <int N>
+__global__ void __launch_bounds__(kClipThreads, 1)
+    grad_norm_kernel(const __grid_constant__ ClipTable<N> t, int inf, double* __restrict__ partial, uint32_t* status) {
+    MOE_CLIP_PROLOGUE
+    ClipRing<N, false> ring(t, clip_smem, bars, &abort_s, status);
     double acc = 0.0;
-    const int64_t chunks = t.chunk0[t.n];
-    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int k = tensor_of(t, c);
-        const int64_t per = t.dtype[k] == MOE_DTYPE_FP32 ? kChunkBytes / 4 : kChunkBytes / 2;
-        const int64_t e0 = (c - t.chunk0[k]) * per;
-        const int64_t n = t.numel[k] - e0 < per ? t.numel[k] - e0 : per;
-        const bool wide = (reinterpret_cast<uintptr_t>(t.src[k]) & 15) == 0;
+    for (int64_t c = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; c < ring.chunks; c += ring.stride) {
+        const Chunk u = chunk_at(t, c);
         double v;
-        if (t.dtype[k] == MOE_DTYPE_FP32) v = share_norm(static_cast<const float*>(t.src[k]) + e0, n, wide, inf);
-        else if (t.dtype[k] == MOE_DTYPE_FP16) v = share_norm(static_cast<const __half*>(t.src[k]) + e0, n, wide, inf);
-        else v = share_norm(static_cast<const __nv_bfloat16*>(t.src[k]) + e0, n, wide, inf);
+        if (t.dtype[u.k] == MOE_DTYPE_FP32) v = share_norm(ring, static_cast<const float*>(t.src[u.k]) + u.e0, u, inf);
+        else if (t.dtype[u.k] == MOE_DTYPE_FP16) v = share_norm(ring, static_cast<const __half*>(t.src[u.k]) + u.e0, u, inf);
+        else v = share_norm(ring, static_cast<const __nv_bfloat16*>(t.src[u.k]) + u.e0, u, inf);
         acc = join(acc, v, inf);
     }
+    ring.finish();
     acc = join_cta(acc, inf, warp_s);
     if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
-template <class T>
-__device__ __forceinline__ void scale_share(const T* p, T* q, int64_t n, bool wide, float scale) {
+template <class T, class R>
+__device__ __forceinline__ void scale_share(R& ring, const T* p, T* q, const Chunk& u, float scale) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    int64_t tail = 0;
-    if (wide) {
-        const int64_t nv = n / V;
-        Pack<T, V> x[kVecs];
+    const int nv = u.bulk / 16;
+    for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
+        ring.template piece<T>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
+            Pack<T, V> o;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int64_t v = threadIdx.x + i * kClipThreads;
-            if (v < nv) x[i].raw = *reinterpret_cast<const typename Pack<T, V>::Raw*>(p + v * V);
-        }
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int64_t v = threadIdx.x + i * kClipThreads;
-            if (v >= nv) continue;
-#pragma unroll
-            for (int e = 0; e < V; ++e) x[i].set(e, x[i].get(e) * scale);
-            x[i].store(q + v * V);
-        }
-        tail = nv * V;
-    }
-    for (int64_t i = tail + threadIdx.x; i < n; i += kClipThreads) q[i] = from_f32<T>(to_f32(p[i]) * scale);
+            for (int e = 0; e < V; ++e) o.set(e, x.get(e) * scale);
+            o.store(q + (v0 + v) * V);
+        });
+    for (int i = nv * V + (threadIdx.x & 31); i < u.n; i += 32) q[i] = from_f32<T>(to_f32(p[i]) * scale);
 }
 
 // Every CTA joins the partial results (np of them) and scales its chunks, the last first: they are
-// the ones the norm read last, so they are still in L2.  A scale of one leaves gradients that stay
-// in place alone.
+// the ones the norm read last, so they are still in L2.  A scale of one where every gradient stays in
+// place leaves them alone.
 template <int N>
-__global__ void __launch_bounds__(kClipThreads)
+__global__ void __launch_bounds__(kClipThreads, 1)
     grad_scale_kernel(const __grid_constant__ ClipTable<N> t, int inf, const double* __restrict__ partial, int np,
-                      float max_norm, float eps, int write_total, float* __restrict__ total) {
-    __shared__ double warp_s[kClipThreads / 32];
-    grid_dependency_wait();
+                      float max_norm, float eps, int write_total, int all_in_place, float* __restrict__ total,
+                      uint32_t* status) {
+    MOE_CLIP_PROLOGUE
     double acc = 0.0;
     for (int i = threadIdx.x; i < np; i += kClipThreads) acc = join(acc, partial[i], inf);
     acc = join_cta(acc, inf, warp_s);
@@ -170,24 +263,21 @@ __global__ void __launch_bounds__(kClipThreads)
     if (write_total && blockIdx.x == 0 && threadIdx.x == 0) *total = static_cast<float>(norm);
     const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
     const float scale = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);   // a NaN stays
-    const int64_t chunks = t.chunk0[t.n];
-    for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-        const int64_t c = chunks - 1 - i;
-        const int k = tensor_of(t, c);
-        if (scale == 1.0f && t.src[k] == t.dst[k]) continue;
-        const int64_t per = t.dtype[k] == MOE_DTYPE_FP32 ? kChunkBytes / 4 : kChunkBytes / 2;
-        const int64_t e0 = (c - t.chunk0[k]) * per;
-        const int64_t n = t.numel[k] - e0 < per ? t.numel[k] - e0 : per;
-        const bool wide = ((reinterpret_cast<uintptr_t>(t.src[k]) | reinterpret_cast<uintptr_t>(t.dst[k])) & 15) == 0;
-        if (t.dtype[k] == MOE_DTYPE_FP32)
-            scale_share(static_cast<const float*>(t.src[k]) + e0, static_cast<float*>(t.dst[k]) + e0, n, wide, scale);
-        else if (t.dtype[k] == MOE_DTYPE_FP16)
-            scale_share(static_cast<const __half*>(t.src[k]) + e0, static_cast<__half*>(t.dst[k]) + e0, n, wide, scale);
+    if (scale == 1.0f && all_in_place) return;
+    ClipRing<N, true> ring(t, clip_smem, bars, &abort_s, status);
+    for (int64_t c = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; c < ring.chunks; c += ring.stride) {
+        const Chunk u = chunk_at(t, ring.index(c));
+        if (t.dtype[u.k] == MOE_DTYPE_FP32)
+            scale_share(ring, static_cast<const float*>(t.src[u.k]) + u.e0, static_cast<float*>(t.dst[u.k]) + u.e0, u, scale);
+        else if (t.dtype[u.k] == MOE_DTYPE_FP16)
+            scale_share(ring, static_cast<const __half*>(t.src[u.k]) + u.e0, static_cast<__half*>(t.dst[u.k]) + u.e0, u, scale);
         else
-            scale_share(static_cast<const __nv_bfloat16*>(t.src[k]) + e0, static_cast<__nv_bfloat16*>(t.dst[k]) + e0, n,
-                        wide, scale);
+            scale_share(ring, static_cast<const __nv_bfloat16*>(t.src[u.k]) + u.e0,
+                        static_cast<__nv_bfloat16*>(t.dst[u.k]) + u.e0, u, scale);
     }
+    ring.finish();
 }
+#undef MOE_CLIP_PROLOGUE
 
 int64_t chunks_of(int64_t numel, int dtype) {
     const int64_t per = kChunkBytes / static_cast<int64_t>(dtype_bytes(dtype));
@@ -203,6 +293,8 @@ struct ClipCall {
     float max_norm, eps;
     float* total;
     double* partial;
+    int all_in_place;
+    uint32_t* status;
     cudaStream_t stream;
 };
 
@@ -235,18 +327,36 @@ cudaError_t clip_launches(const ClipCall& c) {
     for (int b = 0; b < batches && e == cudaSuccess; ++b) {
         fill_table(&t, c, b * N, c.n < (b + 1) * N ? c.n : (b + 1) * N);
         const unsigned grid = clip_grid(t.chunk0[t.n]);
-        e = launch_pdl(grad_norm_kernel<N>, dim3(grid), dim3(kClipThreads), 0, c.stream, t, c.inf, c.partial + np);
+        e = launch_pdl(grad_norm_kernel<N>, dim3(grid), dim3(kClipThreads), kRingBytes, c.stream, t, c.inf, c.partial + np,
+                       c.status);
         np += static_cast<int>(grid);
     }
     for (int b = 0; b < batches && e == cudaSuccess; ++b) {
         if (batches > 1) fill_table(&t, c, b * N, c.n < (b + 1) * N ? c.n : (b + 1) * N);
-        e = launch_pdl(grad_scale_kernel<N>, dim3(clip_grid(t.chunk0[t.n])), dim3(kClipThreads), 0, c.stream, t, c.inf,
-                       static_cast<const double*>(c.partial), np, c.max_norm, c.eps, b == 0 ? 1 : 0, c.total);
+        e = launch_pdl(grad_scale_kernel<N>, dim3(clip_grid(t.chunk0[t.n])), dim3(kClipThreads), kRingBytes, c.stream, t,
+                       c.inf, static_cast<const double*>(c.partial), np, c.max_norm, c.eps, b == 0 ? 1 : 0, c.all_in_place,
+                       c.total, c.status);
     }
     return e;
 }
 
+template <int N>
+cudaError_t clip_init() {
+    const cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    return e == cudaSuccess
+               ? cudaFuncSetAttribute(grad_scale_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)
+               : e;
+}
+
 }  // namespace
+
+cudaError_t clip_init_device() {
+    cudaError_t e = clip_init<32>();
+    if (e == cudaSuccess) e = clip_init<128>();
+    if (e == cudaSuccess) e = clip_init<kMostTensors>();
+    return e;
+}
+
 }  // namespace mfp8
 
 using namespace mfp8;
@@ -265,11 +375,13 @@ int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* nu
     if (n < 0 || (norm_kind != MOE_NORM_L2 && norm_kind != MOE_NORM_INF)) return MOE_ERR_INVALID_ARG;
     if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || !total_norm) return MOE_ERR_INVALID_ARG;
     if (n > 0 && (!grads || !out || !numel || !dtype)) return MOE_ERR_INVALID_ARG;
+    int all_in_place = 1;
     for (int i = 0; i < n; ++i) {
         if (numel[i] < 0 || !known_dtype(dtype[i])) return MOE_ERR_INVALID_ARG;
         if (numel[i] > 0 && (!grads[i] || !out[i])) return MOE_ERR_INVALID_ARG;
         if (!on_element(address(grads[i]) | address(out[i]), dtype_bytes(dtype[i]))) return MOE_ERR_INVALID_ARG;
         if (numel[i] > (int64_t(1) << 50)) return MOE_ERR_UNSUPPORTED_SHAPE;
+        if (numel[i] > 0 && grads[i] != out[i]) all_in_place = 0;
     }
     if (workspace_bytes < moe_clip_grads_workspace_size(n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace || !on_element(address(workspace), 8)) return MOE_ERR_INVALID_ARG;
@@ -277,7 +389,7 @@ int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* nu
     const int rc = device_status_word(&status);
     if (rc != MOE_OK) return rc;
     const ClipCall c = {grads, out, numel, dtype, n, norm_kind == MOE_NORM_INF ? 1 : 0, max_norm, eps, total_norm,
-                        static_cast<double*>(workspace), static_cast<cudaStream_t>(stream)};
+                        static_cast<double*>(workspace), all_in_place, status, static_cast<cudaStream_t>(stream)};
     return cuda_status(n <= 32 ? clip_launches<32>(c) : n <= 128 ? clip_launches<128>(c)
                                                                  : clip_launches<kMostTensors>(c));
 }

@@ -20,7 +20,7 @@
 // rows, so that the tile in which an expert ends costs its rows rounded up to 32, not to 256 (a
 // skewed router leaves most experts few rows: with rows along the 256, 19% of the multiply-adds of
 // the Qwen3-shaped batch were padding).  The accumulators then hold one output column per lane,
-// and the epilogue stores row by row.  Weights' gradient: 256 columns of a by 256 of dc, the rows are
+// and the epilogue turns them over.  Weights' gradient: 256 columns of a by 256 of dc, the rows are
 // the reduction.
 //
 // The operands keep the caller's layout; where the reduction runs along the slow axis (w of the
@@ -45,7 +45,9 @@ constexpr int X_BOX = 64 * 128;                    // bytes of a transposed oper
 constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: tile table, 3: ends of experts
 constexpr int X_THREADS = (X_FIRST_EPI + X_EPI_WARPS) * 32;
 constexpr uint32_t X_TMEM = 512;
-constexpr int X_GROUP = 4;                        // row tiles visited together (see item_at)
+constexpr int X_PITCH = 256 + 16;                  // bytes of a staged row of 128 outputs
+constexpr int X_STAGED = 32 * X_PITCH;             // of a block of 32 rows
+constexpr int X_GROUP = 4;                         // row tiles visited together (see item_at)
 
 struct ExpertArgs {
     const int32_t* offsets;
@@ -68,11 +70,12 @@ struct XCtl {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    int half_bad[2];            // a warp of the epilogue's half gave up
     int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
     int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each place (not for the weights' gradient)
     int16_t order[MOE_MAX_EXPERTS];   // experts by falling rows: the expert at each place
 };
-constexpr size_t X_SMEM = 1024 + X_SUPER * X_SUB * 2 * X_TILE + sizeof(XCtl);
+constexpr size_t X_SMEM = 1024 + X_SUPER * X_SUB * 2 * X_TILE + 2 * X_STAGED + sizeof(XCtl);
 static_assert(X_SMEM <= 232448, "more shared memory than a CTA has");
 
 // One output tile: rows [r0, r0 + nrow) of column tile n of expert e; kblocks of the reduction
@@ -287,33 +290,69 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-// An accumulator lane is an output column, so the warp stores one row of a 32 x 32 block at a time, 64
-// contiguous bytes.  (Through shared memory each lane could store 16 bytes, but the staging took a
-// tenth of the shared-memory cycles, which the tensor cores' operand reads and the TMA writes
-// fill: 546 against 475 us for the skewed batch's product without any epilogue.)
-//   store_column: rows i < nrow of this lane's column from v[i];  load_column: the reverse, two rows
-//   per register
-template <class T>
-__device__ __forceinline__ void store_column(const float* v, T* out, int64_t ld, int nrow, bool live) {
-    if (!live) return;
-    if (nrow >= 32) {
+// An accumulator lane is an output column: the four warps that hold a CTA's 128 columns turn a block of 32
+// rows over in shared memory, so that it is stored (and gate and up are loaded) by whole 128-byte
+// lines.  (Stored by each warp from registers, 32 or 64 bytes of a row at a time, the writes were a
+// quarter of the L2's requests.)
+struct Block {
+    uint8_t* stage;            // [32] rows of X_PITCH bytes
+    int bar, et;               // named barrier of the 128 threads, this thread among them
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
+    // this thread's 16-byte pieces of a block whose rows have `pieces` of them (16 or 8): f(row, piece, address)
+    template <int PIECES, class F>
+    __device__ __forceinline__ void each_piece(F f) const {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) out[i * ld] = from_f32<T>(v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < nrow) out[i * ld] = from_f32<T>(v[i]);
+        for (int i = 0; i < PIECES / 4; ++i) {
+            const int k = i * 128 + et, r = k / PIECES, q = k % PIECES;
+            f(i, r, q, stage + r * X_PITCH + q * 16);
+        }
     }
-}
-template <class T>
-__device__ __forceinline__ void load_column(uint32_t (&u)[16], const T* in, int64_t ld, int nrow, bool live) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const uint16_t lo = live && 2 * i < nrow ? __ldg(reinterpret_cast<const uint16_t*>(in + (2 * i) * ld)) : uint16_t(0);
-        const uint16_t hi =
-            live && 2 * i + 1 < nrow ? __ldg(reinterpret_cast<const uint16_t*>(in + (2 * i + 1) * ld)) : uint16_t(0);
-        u[i] = lo | (static_cast<uint32_t>(hi) << 16);
+    template <class T>
+    __device__ __forceinline__ void put(int row, int col, float v) const {
+        *reinterpret_cast<T*>(stage + row * X_PITCH + col * 2) = from_f32<T>(v);
     }
+    template <class T>
+    __device__ __forceinline__ float get(int row, int col) const {
+        return to_f32(*reinterpret_cast<const T*>(stage + row * X_PITCH + col * 2));
+    }
+    // column `col` of 32 staged rows from v, then the block to rows [0, nrow) of out, from column c
+    template <class T>
+    __device__ __forceinline__ void store(const float* v, int col, T* out, int64_t ld, int nrow, int c, int cols) const {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) put<T>(i, col, v[i]);
+        sync();
+        each_piece<16>([&](int, int r, int q, uint8_t* p) {
+            if (r < nrow && c + q * 8 < cols)
+                *reinterpret_cast<uint4*>(out + r * ld + c + q * 8) = *reinterpret_cast<const uint4*>(p);
+        });
+        sync();
+    }
+    // the reverse, in two steps: this thread's pieces of the block; column `col` of them all
+    template <class T>
+    __device__ __forceinline__ void fetch(uint4 (&u)[4], const T* in, int64_t ld, int nrow, int c, int cols) const {
+        each_piece<16>([&](int i, int r, int q, uint8_t*) {
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (r < nrow && c + q * 8 < cols) u[i] = __ldg(reinterpret_cast<const uint4*>(in + r * ld + c + q * 8));
+        });
+    }
+    template <class T>
+    __device__ __forceinline__ void turn(const uint4 (&u)[4], float* v, int col) const {
+        each_piece<16>([&](int i, int, int, uint8_t* p) { *reinterpret_cast<uint4*>(p) = u[i]; });
+        sync();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = get<T>(i, col);
+        sync();
+    }
+};
+
+// Whether all four warps of an epilogue half got through their wait: the same answer in all of them (the
+// second barrier keeps a later item's answer away from this one's readers).
+__device__ __forceinline__ bool half_ok(bool ok, const Block& block, volatile int* bad) {
+    if (!ok) *bad = 1;
+    block.sync();
+    const bool fine = *bad == 0;
+    block.sync();
+    return fine;
 }
 
 // 32 columns of the warp's 32 tensor-memory lanes.
@@ -343,7 +382,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     uint8_t* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     uint8_t* smA = base;                                   // [X_SUPER][X_SUB][X_TILE]
     uint8_t* smB = base + X_SUPER * X_SUB * X_TILE;        // likewise
-    XCtl* ctl = reinterpret_cast<XCtl*>(smB + X_SUPER * X_SUB * X_TILE);
+    uint8_t* smE = smB + X_SUPER * X_SUB * X_TILE;         // [2][X_STAGED]
+    XCtl* ctl = reinterpret_cast<XCtl*>(smE + 2 * X_STAGED);
     constexpr bool A_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
     constexpr bool B_MN = MODE == kWeights;
     constexpr bool SILU = MODE == kForwardSilu;
@@ -365,6 +405,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         }
         mbar_init(smem_addr(&ctl->drain), 1);
         ctl->abort_flag = 0;
+        ctl->half_bad[0] = ctl->half_bad[1] = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -599,6 +640,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
         T* out = static_cast<T*>(a.out);
         const T* gu_in = static_cast<const T*>(a.gate_up);   // kRowsSilu
+        const Block block = {smE + g * X_STAGED, 1 + g, sp * 32 + lane};
         uint32_t buf = 0, bphase = 0;
         bool ok = true;
         const uint32_t tempty0 = cluster_map(smem_addr(&ctl->tempty[0]), 0), tempty1 = cluster_map(smem_addr(&ctl->tempty[1]), 0);
@@ -606,27 +648,26 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             const int64_t w = item_of_round<MODE>(round, rounds);
             if (w >= total) continue;
             const XItem t = item_at<MODE>(a, ctl, w, NT);
-            // output columns in the lanes; the tile's rows in blocks of 32, dealt to the warps g in turn
-            const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128) + sp * (SILU ? 16 : 32);
-            const int col = SILU ? c0 + (a.turn == 16 ? lane & 15 : ((lane >> 4) * 8) + (lane & 7)) : c0 + lane;
-            const bool live = col < OC;
+            // output columns in the lanes; the tile's rows in blocks of 32, dealt to the halves g in turn
+            const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's columns
+            const int col = sp * 32 + lane;
             const int blocks = (t.nrow + 31) / 32;
             const int64_t row = t.r0 + (MODE == kWeights ? static_cast<int64_t>(t.e) * a.N : 0);
             if (MODE == kWeights && t.kblocks == 0) {   // an expert without rows: zero
-                float z[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = 0.0f;
                 for (int blk = g; blk < blocks; blk += 2)
-                    store_column<T>(z, out + (row + blk * 32) * OC + col, OC, t.nrow - blk * 32, live);
+                    block.each_piece<16>([&](int, int r, int q, uint8_t*) {
+                        if (r < t.nrow - blk * 32 && c0 + q * 8 < OC)
+                            *reinterpret_cast<uint4*>(out + (row + blk * 32 + r) * OC + c0 + q * 8) = make_uint4(0, 0, 0, 0);
+                    });
                 continue;
             }
-            uint32_t gq[MODE == kRowsSilu ? 16 : 1], uq[MODE == kRowsSilu ? 16 : 1];
+            uint4 gq[4], uq[4];
             if constexpr (MODE == kRowsSilu) {   // gate and up of the first block, ahead of the products
-                load_column<T>(gq, gu_in + (row + g * 32) * a.ld_gu + col, a.ld_gu, t.nrow - g * 32, live);
-                load_column<T>(uq, gu_in + (row + g * 32) * a.ld_gu + OC + col, a.ld_gu, t.nrow - g * 32, live);
+                block.fetch<T>(gq, gu_in + (row + g * 32) * a.ld_gu, a.ld_gu, t.nrow - g * 32, c0, OC);
+                block.fetch<T>(uq, gu_in + (row + g * 32) * a.ld_gu + OC, a.ld_gu, t.nrow - g * 32, c0, OC);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
-            if (!ok) break;
+            if (!half_ok(ok, block, &ctl->half_bad[g])) break;
             tc_fence_after();
             for (int blk = g; blk < blocks; blk += 2) {
                 float v[32];
@@ -634,42 +675,55 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                 const int64_t r0 = row + blk * 32;
                 const int nrow = t.nrow - blk * 32;
                 if constexpr (SILU) {
-                    // lanes: a.turn gate columns, then the up columns of the same, and so on
+                    // lanes: a.turn gate columns, then the up columns of the same, and so on; hc: the column of h
                     const bool up = (lane & a.turn) != 0;
+                    const int hc = sp * 16 + (a.turn == 16 ? lane & 15 : ((lane >> 4) * 8) + (lane & 7));
                     T* gu = static_cast<T*>(a.gate_up);
-                    if (gu) store_column<T>(v, gu + r0 * (2 * OC) + col + (up ? OC : 0), 2 * OC, nrow, live);
+                    if (gu) {   // staged as 64 gate and 64 up columns
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) block.put<T>(i, hc + (up ? 64 : 0), v[i]);
+                        block.sync();
+                        block.each_piece<16>([&](int, int r, int q, uint8_t* p) {
+                            const int c = c0 + (q & 7) * 8;
+                            if (r < nrow && c < OC)
+                                *reinterpret_cast<uint4*>(gu + (r0 + r) * (2 * OC) + c + (q & 8 ? OC : 0)) =
+                                    *reinterpret_cast<const uint4*>(p);
+                        });
+                        block.sync();
+                    }
                     // a gate lane gives the up lane beside it its rows 16 .. 31 for that lane's up of rows
                     // 0 .. 15: each then holds 16 rows of one column of h
                     const int first = up ? 16 : 0;
-                    T* h = out + (r0 + first) * OC + col;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[16 + i], a.turn);
                         const float gate = up ? o : v[i], u = up ? v[16 + i] : o;
-                        if (live && first + i < nrow)
-                            h[static_cast<int64_t>(i) * OC] = from_f32<T>(__fdividef(gate, 1.0f + __expf(-gate)) * u);
+                        block.put<T>(first + i, hc, __fdividef(gate, 1.0f + __expf(-gate)) * u);
                     }
+                    block.sync();
+                    block.each_piece<8>([&](int, int r, int q, uint8_t* p) {
+                        if (r < nrow && c0 + q * 8 < OC)
+                            *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) = *reinterpret_cast<const uint4*>(p);
+                    });
+                    block.sync();
                 } else if constexpr (MODE == kRowsSilu) {
-                    float dup[32];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 gt = unpack2<T>(gq[i]), up = unpack2<T>(uq[i]);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float gv = k ? gt.y : gt.x, uv = k ? up.y : up.x, d = v[2 * i + k];
-                            const float s = __fdividef(1.0f, 1.0f + __expf(-gv));
-                            dup[2 * i + k] = d * gv * s;
-                            v[2 * i + k] = d * uv * s * (1.0f + gv * (1.0f - s));
-                        }
-                    }
+                    float gt[32], up[32];
+                    block.turn<T>(gq, gt, col);
+                    block.turn<T>(uq, up, col);
                     if (blk + 2 < blocks) {
-                        load_column<T>(gq, gu_in + (r0 + 64) * a.ld_gu + col, a.ld_gu, nrow - 64, live);
-                        load_column<T>(uq, gu_in + (r0 + 64) * a.ld_gu + OC + col, a.ld_gu, nrow - 64, live);
+                        block.fetch<T>(gq, gu_in + (r0 + 64) * a.ld_gu, a.ld_gu, nrow - 64, c0, OC);
+                        block.fetch<T>(uq, gu_in + (r0 + 64) * a.ld_gu + OC, a.ld_gu, nrow - 64, c0, OC);
                     }
-                    store_column<T>(v, out + r0 * (2 * OC) + col, 2 * OC, nrow, live);
-                    store_column<T>(dup, out + r0 * (2 * OC) + OC + col, 2 * OC, nrow, live);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float s = __fdividef(1.0f, 1.0f + __expf(-gt[i])), d = v[i];
+                        v[i] = d * up[i] * s * (1.0f + gt[i] * (1.0f - s));
+                        up[i] = d * gt[i] * s;
+                    }
+                    block.store<T>(v, col, out + r0 * (2 * OC), 2 * OC, nrow, c0, OC);
+                    block.store<T>(up, col, out + r0 * (2 * OC) + OC, 2 * OC, nrow, c0, OC);
                 } else {
-                    store_column<T>(v, out + r0 * OC + col, OC, nrow, live);
+                    block.store<T>(v, col, out + r0 * OC, OC, nrow, c0, OC);
                 }
             }
             tc_fence_before();

@@ -220,9 +220,10 @@ int64_t decode_counters(int max_tiles, int I);
 cudaError_t decode_init_device();
 cudaError_t launch_decode_mlp(const DecodeMlpArgs& args, int num_sms, cudaStream_t stream);
 
-// tokens.cu, experts.cu: once-per-device set-up
+// tokens.cu, experts.cu, clip.cu: once-per-device set-up
 cudaError_t tokens_init_device();
 cudaError_t experts_init_device();
+cudaError_t clip_init_device();
 
 // api.cu: once-per-device set-up; on MOE_OK, *status = the device status word's address
 int device_status_word(uint32_t** status);

@@ -115,6 +115,8 @@ __device__ __forceinline__ void copy_round(const DispatchArgs& a, const int* pos
     }
     bulk_wait_read<0>();
     __syncwarp();
+    if (*abort_flag && lane == 0)   // a wait gave up (its status bit is set): let the loads under way land
+        for (int i = 0; i < a.slots; ++i) mbar_wait(smem_addr(bars + i), ((*phases >> i) & 1u) ^ 1u, nullptr, a.status);
 }
 
 // The sort and the copies of one chunk of tokens and one slab of columns.  Every CTA derives the
@@ -365,6 +367,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_ring_kernel(const Com
     // first warp: row and weight of this lane's pair in the item to load next, fetched one item early
     int64_t row = -1;
     float weight = 1.0f;
+    uint32_t issued = 0;
     auto fetch = [&] {
         row = -1;
         if (lane < a.topk && load.t < a.tokens) {
@@ -390,6 +393,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_ring_kernel(const Com
         if (lane == 0) mbar_arrive_expect_tx(b, n * nv * 16);
         __syncwarp();
         if (row >= 0) bulk_load(smem_addr(s + at * piece), a.y + row * a.ld_bytes + static_cast<int64_t>(v0) * 16, nv * 16, b);
+        ++issued;
         load.next(step_t, step_s, a.slabs);
         fetch();
     };
@@ -430,6 +434,11 @@ __global__ void __launch_bounds__(kCombineThreads) combine_ring_kernel(const Com
             phase ^= 1u;
         }
     }
+    if (*static_cast<volatile int*>(&abort_s) && tid == 0)   // a wait gave up: let the loads under way land
+        for (int d = 0; d < a.depth; ++d) {
+            const uint32_t n = (issued + a.depth - 1 - d) / a.depth;
+            if (n > 0) mbar_wait(smem_addr(bar + d), (n - 1) & 1u, nullptr, a.status);
+        }
 }
 
 // One warp per pair: dy[pos] = w * dout[t] and dw = <dout[t], y[pos]>.  The pairs of one token are
