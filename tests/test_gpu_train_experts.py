@@ -49,6 +49,9 @@ CASES = [  # rows per expert, rows of no expert, N, K
     ([0, 0, 0], 7, 32, 64),
     ([2] * 300, 0, 64, 64),
     ([1, 0] * 512, 1, 16, 16),
+    ([513, 1500, 0, 40, 1025], 9, 336, 328),      # several tiles of rows
+    ([1030], 0, 1040, 72),
+    ([257, 2000, 700], 0, 272, 16),
 ]
 
 
@@ -107,12 +110,13 @@ def test_weights_gradient(case, dtype):
     check(dw, ref, size, steps(max(case[0])), "dw")
 
 
+@pytest.mark.parametrize("long", [False, True])
 @pytest.mark.parametrize("dtype", TYPES, ids=ids_of)
-def test_large_tiles_many_items(dtype):
+def test_large_tiles_many_items(dtype, long):
     """Every SM takes several tiles of each product (accumulators alternate, the ring wraps), K and
     N past several blocks."""
     g = torch.Generator(device="cuda").manual_seed(6)
-    counts = [1500, 0, 4000, 129, 900, 1, 2000, 640]
+    counts = [500, 0, 1400, 129, 300, 1, 700, 640] if not long else [3000, 0, 700, 257, 9000, 1, 2000, 640, 513]
     off, rows, N, K = offsets_of(counts), sum(counts), 1552, 1096
     ends = off.tolist()
     a = torch.randn(rows, K, generator=g, device="cuda").to(dtype)
