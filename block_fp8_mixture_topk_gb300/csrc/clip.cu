@@ -205,11 +205,11 @@ __device__ __forceinline__ double share_norm(R& ring, const T* p, const Chunk& u
     __shared__ double warp_s[kClipWarps];                                       \
     __shared__ uint64_t bars[kClipWarps * kSlots];                              \
     __shared__ int abort_s;                                                     \
-    if (threadIdx.x < kClipWarps * kSlots) mbar_init(smem_addr(bars + threadIdx.x), 1); \
-    if (threadIdx.x == 0) {                                                     \
-        abort_s = 0;                                                            \
+    if (threadIdx.x < kClipWarps * kSlots) {                                    \
+        mbar_init(smem_addr(bars + threadIdx.x), 1);                            \
         fence_barrier_init();                                                   \
     }                                                                           \
+    if (threadIdx.x == 0) abort_s = 0;                                          \
     __syncthreads();                                                            \
     grid_dependency_wait();
 

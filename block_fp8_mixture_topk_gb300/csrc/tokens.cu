@@ -136,11 +136,11 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     __shared__ int abort_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t phases = 0;
-    if (BULK && tid < kCopyWarps * kMostSlots) mbar_init(smem_addr(bars + tid), 1);
-    if (tid == 0) {
-        abort_s = 0;
+    if (BULK && tid < kCopyWarps * kMostSlots) {
+        mbar_init(smem_addr(bars + tid), 1);
         fence_barrier_init();
     }
+    if (tid == 0) abort_s = 0;
     for (int e = tid; e < 2 * a.E; e += kSortThreads) smem[e] = 0;
     __syncthreads();
     grid_dependency_wait();
@@ -353,11 +353,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_ring_kernel(const Com
     const int slot_bytes = a.topk * G * 16 + kCombineMeta, piece = G * 16;
     uint8_t* ring = ring_smem + static_cast<size_t>(g) * a.depth * slot_bytes;
     uint64_t* bar = bars + g * kCombineDepth;
-    if (threadIdx.x < kCombineGroups * kCombineDepth) mbar_init(smem_addr(bars + threadIdx.x), 1);
-    if (threadIdx.x == 0) {
-        abort_s = 0;
-        fence_barrier_init();
-    }
+    for (int i = threadIdx.x; i < kCombineGroups * kCombineDepth; i += blockDim.x) mbar_init(smem_addr(bars + i), 1);
+    fence_barrier_init();
+    if (threadIdx.x == 0) abort_s = 0;
     __syncthreads();
     grid_dependency_wait();
     const int64_t step = static_cast<int64_t>(gridDim.x) * R, first = static_cast<int64_t>(blockIdx.x) * R + g;
