@@ -85,6 +85,8 @@ def library_path() -> str:
 def lib():
     """The loaded libmoefp8 (built on first use if absent; raises if that fails)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_build.LIB_PATH):
@@ -543,6 +545,21 @@ def moe_fp8_block_forward_masked(hidden, counts, w13, w13_scale, w2, w2_scale, o
 
 DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
+try:   # half the time of torch.empty, which counts in a step of one token
+    _empty_strided = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    def _empty_strided(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+def _vector(n, dtype):
+    """A new [n] on the current device, where the kernels run."""
+    return _empty_strided((n,), (1,), dtype)
+
+
+def _matrix(n, m, dtype):
+    return _empty_strided((n, m), (m, 1), dtype)
+
 
 def _typed(t, name, like=None):
     """Code of t's element type; with `like`, t must have that tensor's type."""
@@ -597,13 +614,13 @@ def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
         raise ValueError(f"topk_ids must be [{T}, topk], got {list(topk_ids.shape)}")
     k = topk_ids.shape[1]
     P = T * k
-    L, dev = lib(), x.device
+    L = lib()
     wsb = L.moe_dispatch_workspace_size(T, k, num_experts)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    rows = torch.empty(P, H, dtype=x.dtype, device=dev)
-    offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int32, device=dev)
-    pair_ids = torch.empty(P, dtype=torch.int32, device=dev)
-    pos = torch.empty(T, k, dtype=torch.int32, device=dev)
+    ws = _vector(wsb, torch.uint8) if wsb else None
+    rows = _matrix(P, H, x.dtype)
+    offsets = _vector(max(num_experts, 0) + 1, torch.int32)
+    pair_ids = _vector(P, torch.int32)
+    pos = _matrix(T, k, torch.int32)
     rc = L.moe_dispatch(x.data_ptr(), ld, code, topk_ids.data_ptr(), T, k, num_experts, H, rows.data_ptr(),
                         offsets.data_ptr(), pair_ids.data_ptr(), pos.data_ptr(), None if ws is None else ws.data_ptr(),
                         wsb, _stream())
@@ -623,7 +640,7 @@ def moe_dispatch_backward(drows, pos):
     code, ld = _rows(drows, "drows")
     T, k = _pos(pos)
     n, H = drows.shape
-    dx = torch.empty(T, H, dtype=drows.dtype, device=drows.device)
+    dx = _matrix(T, H, drows.dtype)
     _check("moe_dispatch_backward", lib().moe_dispatch_backward(drows.data_ptr(), ld, code, pos.data_ptr(), T, k, H, n,
                                                                 dx.data_ptr(), _stream()))
     return dx
@@ -637,7 +654,7 @@ def moe_combine(y, pos, weights=None):
     if weights is not None:
         _dense(weights, "weights", torch.float32, (T, k))
     n, H = y.shape
-    out = torch.empty(T, H, dtype=y.dtype, device=y.device)
+    out = _matrix(T, H, y.dtype)
     _check("moe_combine", lib().moe_combine(y.data_ptr(), ld, code, pos.data_ptr(),
                                             None if weights is None else weights.data_ptr(), T, k, H, n,
                                             out.data_ptr(), _stream()))
@@ -653,8 +670,8 @@ def moe_combine_backward(dout, y, pos, pair_ids, weights=None):
     _dense(pair_ids, "pair_ids", torch.int32, (n,))
     if weights is not None:
         _dense(weights, "weights", torch.float32, (T, k))
-    dy = torch.empty(n, H, dtype=y.dtype, device=y.device)
-    dw = torch.empty(T, k, dtype=torch.float32, device=y.device)
+    dy = _matrix(n, H, y.dtype)
+    dw = _matrix(T, k, torch.float32)
     rc = lib().moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, pos.data_ptr(), pair_ids.data_ptr(),
                                     None if weights is None else weights.data_ptr(), T, k, H, n, dy.data_ptr(),
                                     dw.data_ptr(), _stream())
@@ -685,17 +702,17 @@ def moe_pre_norm(x, weight, eps=1e-6, weight_offset=0.0):
     code, ld = _rows(x, "x")
     T, H = x.shape
     wcode = _norm_weight(weight, H, "weight")
-    h = torch.empty(T, H, dtype=x.dtype, device=x.device)
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    h = _matrix(T, H, x.dtype)
+    rstd = _vector(T, torch.float32)
     _check("moe_pre_norm", lib().moe_pre_norm(x.data_ptr(), ld, code, weight.data_ptr(), wcode, weight_offset, eps, T,
                                               H, h.data_ptr(), rstd.data_ptr(), _stream()))
     return h, rstd
 
 
-def _norm_workspace(T, H, device):
+def _norm_workspace(T, H):
     """Scratch of a norm's gradient and its size in bytes."""
     wsb = lib().moe_norm_backward_workspace_size(T, H)
-    return torch.empty(wsb, dtype=torch.uint8, device=device), wsb
+    return _vector(wsb, torch.uint8), wsb
 
 
 def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0):
@@ -709,9 +726,9 @@ def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0
     if dresidual is not None:
         _, ldr = _rows(dresidual, "dresidual", x, (T, H))
         dres = dresidual.data_ptr()
-    dx = torch.empty(T, H, dtype=x.dtype, device=x.device)
-    dw = torch.empty(H, dtype=torch.float32, device=x.device)
-    ws, wsb = _norm_workspace(T, H, x.device)
+    dx = _matrix(T, H, x.dtype)
+    dw = _vector(H, torch.float32)
+    ws, wsb = _norm_workspace(T, H)
     rc = lib().moe_pre_norm_backward(dh.data_ptr(), ldd, x.data_ptr(), ldx, code, weight.data_ptr(), wcode, weight_offset,
                                      rstd.data_ptr(), dres, ldr, T, H, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb,
                                      _stream())
@@ -777,11 +794,11 @@ def moe_post_norm(y, residual, weight, gate=None, gate_kind="none", gate_sigmoid
     _, ldr = _rows(residual, "residual", y, (T, H))
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, eps, weight_offset,
                             next_weight)
-    r = PostNorm(torch.empty(T, H, dtype=y.dtype, device=y.device),
-                 torch.empty(T, dtype=torch.float32, device=y.device))
+    r = PostNorm(_matrix(T, H, y.dtype),
+                 _vector(T, torch.float32))
     h2 = r2 = None
     if next_weight is not None:
-        r.next_h, r.next_rstd = torch.empty_like(r.out), torch.empty_like(r.rstd)
+        r.next_h, r.next_rstd = _matrix(T, H, y.dtype), _vector(T, torch.float32)
         h2, r2 = r.next_h.data_ptr(), r.next_rstd.data_ptr()
     _check("moe_post_norm", lib().moe_post_norm(y.data_ptr(), ldy, residual.data_ptr(), ldr, code, ctypes.byref(prm), T,
                                                 H, r.out.data_ptr(), r.rstd.data_ptr(), h2, r2, _stream()))
@@ -797,13 +814,13 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     _, ldo = _rows(dout, "dout", y, (T, H))
     _dense(rstd, "rstd", torch.float32, (T,))
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, 0.0, weight_offset)
-    dy = torch.empty(T, H, dtype=y.dtype, device=y.device)
-    dres = torch.empty_like(dy) if residual_grad else None
-    dw = torch.empty(H, dtype=torch.float32, device=y.device)
+    dy = _matrix(T, H, y.dtype)
+    dres = _matrix(T, H, y.dtype) if residual_grad else None
+    dw = _vector(H, torch.float32)
     dg = None
     if gate is not None:
         dg = torch.empty(gate.shape, dtype=torch.float32 if gate_kind == "channel" else gate.dtype, device=gate.device)
-    ws, wsb = _norm_workspace(T, H, y.device)
+    ws, wsb = _norm_workspace(T, H)
     rc = lib().moe_post_norm_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, ctypes.byref(prm),
                                       rstd.data_ptr(), T, H, dy.data_ptr(), None if dres is None else dres.data_ptr(),
                                       None if dg is None else dg.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb, _stream())
@@ -840,7 +857,7 @@ def moe_expert_gemm(a, w, expert_offsets):
     """The experts' product over rows sorted by expert: out[r] = a[r] @ w[e]^T for the rows
     [expert_offsets[e], expert_offsets[e+1]) of a [rows, K]; w [E, N, K]; bf16 or fp16.  Rows of no expert are zero."""
     _, N, _ = _expert_weights(w, a)
-    out = torch.empty(a.shape[0], N, dtype=a.dtype, device=a.device)
+    out = _matrix(a.shape[0], N, a.dtype)
     _expert_gemm(a, w, expert_offsets, 0, out, None)
     return out
 
@@ -849,8 +866,8 @@ def moe_expert_gemm_silu_mul(a, w, expert_offsets, save_gate_up=True):
     """The first product with its activation: (h [rows, N/2] = silu(gate) * up, gate_up [rows, N] = the
     product itself, which the gradient needs; None with save_gate_up=False).  w [E, N, K]: gate rows, then up."""
     _, N, _ = _expert_weights(w, a)
-    h = torch.empty(a.shape[0], N // 2, dtype=a.dtype, device=a.device)
-    gu = torch.empty(a.shape[0], N, dtype=a.dtype, device=a.device) if save_gate_up else None
+    h = _matrix(a.shape[0], N // 2, a.dtype)
+    gu = _matrix(a.shape[0], N, a.dtype) if save_gate_up else None
     _expert_gemm(a, w, expert_offsets, 1, h, gu)
     return h, gu
 
@@ -867,7 +884,7 @@ def moe_expert_gemm_dgrad(dc, w, expert_offsets, gate_up=None):
     if gate_up is not None:
         _, ldgu = _rows(gate_up, "gate_up", dc, (n, 2 * K))
         gp = gate_up.data_ptr()
-    out = torch.empty(n, K if gate_up is None else 2 * K, dtype=dc.dtype, device=dc.device)
+    out = _matrix(n, K if gate_up is None else 2 * K, dc.dtype)
     rc = lib().moe_expert_gemm_dgrad(dc.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), n, E, N, K, gp,
                                      ldgu, out.data_ptr(), _stream())
     _check("moe_expert_gemm_dgrad", rc)
@@ -886,7 +903,7 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
         raise ValueError("dc and a must have the same rows")
     n, N = dc.shape
     K = a.shape[1]
-    dw = torch.empty(E, N, K, dtype=dc.dtype, device=dc.device)
+    dw = _empty_strided((E, N, K), (N * K, K, 1), dc.dtype)
     rc = lib().moe_expert_gemm_wgrad(dc.data_ptr(), ldd, a.data_ptr(), lda, code, expert_offsets.data_ptr(), n, E, N, K,
                                      dw.data_ptr(), _stream())
     _check("moe_expert_gemm_wgrad", rc)
@@ -921,11 +938,10 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
             if o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
                 raise ValueError(f"out[{i}] must be a contiguous CUDA tensor like grads[{i}]")
             outs.append(o.data_ptr())
-    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
     L = lib()
     wsb = L.moe_clip_grads_workspace_size(n)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=device)
-    total = torch.empty((), dtype=torch.float32, device=device)
+    ws = _vector(wsb, torch.uint8)
+    total = _empty_strided((), (), torch.float32)
     table, kinds = array.array("q", ptrs + outs + sizes), array.array("i", codes)   # host arrays of the C call
     at = table.buffer_info()[0]
     rc = L.moe_clip_grads(at, at + 8 * n, at + 16 * n, kinds.buffer_info()[0], n, kind, float(max_norm), float(eps),
