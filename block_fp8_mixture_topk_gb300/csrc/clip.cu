@@ -56,14 +56,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ double join(double a, double b, int inf) {
     return inf ? static_cast<double>(max_nan(static_cast<float>(a), static_cast<float>(b))) : a + b;
 }
-// Over the CTA's threads; the result in every thread.
-__device__ __forceinline__ double join_cta(double acc, int inf, double* warp_s) {
+// Over the lanes of a warp.
+__device__ __forceinline__ double join_warp(double acc, int inf) {
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) acc = join(acc, __shfl_xor_sync(0xffffffffu, acc, s), inf);
-    if ((threadIdx.x & 31) == 0) warp_s[threadIdx.x >> 5] = acc;
-    __syncthreads();
-    acc = warp_s[0];
-    for (int w = 1; w < kClipWarps; ++w) acc = join(acc, warp_s[w], inf);
     return acc;
 }
 
@@ -135,7 +131,10 @@ struct ClipRing {
     }
     // After a wait that gave up (its status bit is set, values are wrong): let the loads under way land.
     __device__ __forceinline__ void finish() const {
-        if (*abort_flag && (threadIdx.x & 31) == 0)
+        if (*abort_flag) drain();
+    }
+    __device__ __forceinline__ void drain() const {
+        if ((threadIdx.x & 31) == 0)
             for (int i = 0; i < kSlots; ++i) {
                 const uint32_t n = (issued + kSlots - 1 - i) / kSlots;
                 if (n > 0) mbar_wait(smem_addr(bars + i), (n - 1) & 1u, nullptr, status);
@@ -202,7 +201,6 @@ __device__ __forceinline__ double share_norm(R& ring, const T* p, const Chunk& u
 
 #define MOE_CLIP_PROLOGUE                                                       \
     extern __shared__ __align__(128) uint8_t clip_smem[];                       \
-    __shared__ double warp_s[kClipWarps];                                       \
     __shared__ uint64_t bars[kClipWarps * kSlots];                              \
     __shared__ int abort_s;                                                     \
     if (threadIdx.x < kClipWarps * kSlots) {                                    \
@@ -229,7 +227,15 @@ __global__ void __launch_bounds__(kClipThreads, 1)
         acc = join(acc, v, inf);
     }
     ring.finish();
-    acc = join_cta(acc, inf, warp_s);
+    // the threads' results through shared memory to one warp (fp64 runs at a 64th of the fp32 rate: joined
+    // by all warps they took as long as the loads of a small call)
+    __syncthreads();
+    double* all = reinterpret_cast<double*>(clip_smem);
+    all[threadIdx.x] = acc;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    for (int i = 1; i < kClipWarps; ++i) acc = join(acc, all[threadIdx.x + i * 32], inf);
+    acc = join_warp(acc, inf);
     if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
@@ -256,15 +262,25 @@ __global__ void __launch_bounds__(kClipThreads, 1)
                       float max_norm, float eps, int write_total, int all_in_place, float* __restrict__ total,
                       uint32_t* status) {
     MOE_CLIP_PROLOGUE
-    double acc = 0.0;
-    for (int i = threadIdx.x; i < np; i += kClipThreads) acc = join(acc, partial[i], inf);
-    acc = join_cta(acc, inf, warp_s);
-    const double norm = inf ? acc : sqrt(acc);
-    if (write_total && blockIdx.x == 0 && threadIdx.x == 0) *total = static_cast<float>(norm);
-    const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
-    const float scale = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);   // a NaN stays
-    if (scale == 1.0f && all_in_place) return;
-    ClipRing<N, true> ring(t, clip_smem, bars, &abort_s, status);
+    __shared__ float scale_s;
+    ClipRing<N, true> ring(t, clip_smem, bars, &abort_s, status);   // the first loads run while the norm is joined
+    if (threadIdx.x < 32) {
+        double acc = 0.0;
+        for (int i = threadIdx.x; i < np; i += 32) acc = join(acc, partial[i], inf);
+        acc = join_warp(acc, inf);
+        if (threadIdx.x == 0) {
+            const double norm = inf ? acc : sqrt(acc);
+            if (write_total && blockIdx.x == 0) *total = static_cast<float>(norm);
+            const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
+            scale_s = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);   // a NaN stays
+        }
+    }
+    __syncthreads();
+    const float scale = scale_s;
+    if (scale == 1.0f && all_in_place) {
+        ring.drain();
+        return;
+    }
     for (int64_t c = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; c < ring.chunks; c += ring.stride) {
         const Chunk u = chunk_at(t, ring.index(c));
         if (t.dtype[u.k] == MOE_DTYPE_FP32)
