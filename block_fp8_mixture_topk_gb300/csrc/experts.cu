@@ -39,7 +39,7 @@ namespace {
 enum Mode { kForward = 0, kForwardSilu = 1, kRows = 2, kRowsSilu = 3, kWeights = 4 };
 
 constexpr int XM = 256, XN = 256, XK = 64;         // item; XK elements are one 128-byte swizzled row
-constexpr int X_SUB = 1, X_SUPER = 6;              // K blocks per stage, stages
+constexpr int X_STAGES = 6;                        // of the ring, one K block each
 constexpr int X_TILE = 128 * XK * 2;               // one operand's K block in one CTA
 constexpr int X_BOX = 64 * 128;                    // bytes of a transposed operand's box: 64 rows of 64 elements
 constexpr int X_EPI_WARPS = 8, X_FIRST_EPI = 4;    // warps 0: TMA, 1: MMA, 2: tile table, 3: ends of experts
@@ -62,9 +62,9 @@ struct ExpertArgs {
 };
 
 struct XCtl {
-    uint64_t full[X_SUPER];     // (CTA 0) both CTAs' operands of the stage are in place
-    uint64_t empty[X_SUPER];    // the stage's MMAs completed
-    uint64_t tail[X_SUPER];     // this CTA's loads of an expert's last stage landed (weights' gradient)
+    uint64_t full[X_STAGES];     // (CTA 0) both CTAs' operands of the stage are in place
+    uint64_t empty[X_STAGES];    // the stage's MMAs completed
+    uint64_t tail[X_STAGES];     // this CTA's loads of an expert's last stage landed (weights' gradient)
     uint64_t tfull[2];          // the accumulators are complete
     uint64_t tempty[2];         // (CTA 0) both CTAs' epilogue warps moved them out
     uint64_t drain;
@@ -72,10 +72,9 @@ struct XCtl {
     int abort_flag;
     int half_bad[2];            // a warp of the epilogue's half gave up
     int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
-    int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each place (not for the weights' gradient)
-    int16_t order[MOE_MAX_EXPERTS];   // experts by falling rows: the expert at each place
+    int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each expert; weights' gradient: experts by falling rows
 };
-constexpr size_t X_SMEM = 1024 + X_SUPER * X_SUB * 2 * X_TILE + 2 * X_STAGED + sizeof(XCtl);
+constexpr size_t X_SMEM = 1024 + X_STAGES * 2 * X_TILE + 2 * X_STAGED + sizeof(XCtl);
 static_assert(X_SMEM <= 232448, "more shared memory than a CTA has");
 
 // One output tile: rows [r0, r0 + nrow) of column tile n of expert e; kblocks of the reduction
@@ -92,17 +91,17 @@ __device__ __forceinline__ int64_t item_count(const ExpertArgs& a, const XCtl* c
     return static_cast<int64_t>(ctl->tile0[a.E]) * NT;
 }
 
-// The item this cluster takes in its v-th round.  Items are sorted by their experts' falling rows.  Rounds
-// are taken from both ends in turn, the odd clusters one step behind the even ones, so that at any
-// time half of the clusters run items bound by their loads or stores (experts with few rows) beside
-// the multiply-adds of the other half; in the weights' gradient, whose items take as long as their
-// experts have rows, every other round of items is dealt backwards, so that no cluster always gets
-// the longer ones.
+// The item this cluster takes in its v-th round.  Rows' products: cluster c takes items c, c + clusters,
+// ... (about equal work).  Weights' gradient: an item takes as long as its expert has rows, so the
+// experts come by falling rows, every other round is dealt backwards (no cluster always gets the
+// longer ones), and rounds are taken from both ends in turn, the odd clusters one step behind, so that
+// items bound by their stores run beside the multiply-adds of the others.
 template <int MODE>
 __device__ __forceinline__ int64_t item_of_round(int64_t v, int64_t rounds) {
     const int64_t c = blockIdx.x >> 1, n = gridDim.x >> 1;
+    if (MODE != kWeights) return v * n + c;
     const int64_t r = ((v + c) & 1) ? rounds - 1 - (v >> 1) : v >> 1;
-    return r * n + (MODE == kWeights && (r & 1) ? n - 1 - c : c);
+    return r * n + ((r & 1) ? n - 1 - c : c);
 }
 
 template <int MODE>
@@ -111,7 +110,7 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
     if (MODE == kWeights) {
         const int MT = (a.N + XM - 1) / XM, per = MT * NT;
         const int k = static_cast<int>(w / per);
-        t.e = ctl->order[k];
+        t.e = ctl->tile0[k];
         const int local = static_cast<int>(w - static_cast<int64_t>(k) * per);
         const int m = local % MT;
         t.n = local / MT;
@@ -128,7 +127,7 @@ __device__ __forceinline__ XItem item_at(const ExpertArgs& a, const XCtl* ctl, i
             if (ctl->tile0[mid] <= g) lo = mid;
             else hi = mid - 1;
         }
-        t.e = ctl->order[lo];
+        t.e = lo;
         const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo];
         int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
         const int grp = local / (X_GROUP * NT);
@@ -380,9 +379,9 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t* base = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    uint8_t* smA = base;                                   // [X_SUPER][X_SUB][X_TILE]
-    uint8_t* smB = base + X_SUPER * X_SUB * X_TILE;        // likewise
-    uint8_t* smE = smB + X_SUPER * X_SUB * X_TILE;         // [2][X_STAGED]
+    uint8_t* smA = base;                                   // [X_STAGES][X_TILE]
+    uint8_t* smB = base + X_STAGES * X_TILE;        // likewise
+    uint8_t* smE = smB + X_STAGES * X_TILE;         // [2][X_STAGED]
     XCtl* ctl = reinterpret_cast<XCtl*>(smE + 2 * X_STAGED);
     constexpr bool A_MN = MODE == kWeights || MODE == kRows || MODE == kRowsSilu;
     constexpr bool B_MN = MODE == kWeights;
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     const int NT = SILU ? (OC + 127) / 128 : (OC + XN - 1) / XN;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < X_SUPER; ++s) {
+        for (int s = 0; s < X_STAGES; ++s) {
             mbar_init(smem_addr(&ctl->full[s]), MODE == kWeights ? 2 : 1);
             mbar_init(smem_addr(&ctl->empty[s]), 1);
             mbar_init(smem_addr(&ctl->tail[s]), 1);
@@ -428,35 +427,33 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         ctl->row0[e] = static_cast<int>(o);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += X_THREADS) {
-        const int n = ctl->row0[e + 1] - ctl->row0[e];
-        int place = 0;   // experts with more rows, or as many and a lower index
+    if (MODE == kWeights) {
+        for (int e = threadIdx.x; e < a.E; e += X_THREADS) {
+            const int n = ctl->row0[e + 1] - ctl->row0[e];
+            int place = 0;   // experts with more rows, or as many and a lower index
 #pragma unroll 8
-        for (int o = 0; o < a.E; ++o) {
-            const int m = ctl->row0[o + 1] - ctl->row0[o];
-            place += m > n || (m == n && o < e);
-        }
-        ctl->order[place] = static_cast<int16_t>(e);
-    }
-    if (MODE != kWeights) {
-        __syncthreads();
-        if (warp == 2) {
-            int carry = 0;
-            for (int k0 = 0; k0 < a.E; k0 += 32) {
-                const int k = k0 + lane, e = k < a.E ? ctl->order[k] : 0;
-                const int cnt = k < a.E ? ctl->row0[e + 1] - ctl->row0[e] : 0;
-                const int own = cnt > 0 ? (cnt + XN - 1) / XN : 0;
-                int v = own;
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) {
-                    const int u = __shfl_up_sync(0xffffffffu, v, s);
-                    if (lane >= s) v += u;
-                }
-                if (k < a.E) ctl->tile0[k] = carry + v - own;
-                carry += __shfl_sync(0xffffffffu, v, 31);
+            for (int o = 0; o < a.E; ++o) {
+                const int m = ctl->row0[o + 1] - ctl->row0[o];
+                place += m > n || (m == n && o < e);
             }
-            if (lane == 0) ctl->tile0[a.E] = carry;
+            ctl->tile0[place] = e;
         }
+    } else if (warp == 2) {
+        int carry = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int cnt = e < a.E ? ctl->row0[e + 1] - ctl->row0[e] : 0;
+            const int own = cnt > 0 ? (cnt + XN - 1) / XN : 0;
+            int v = own;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, s);
+                if (lane >= s) v += u;
+            }
+            if (e < a.E) ctl->tile0[e] = carry + v - own;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) ctl->tile0[a.E] = carry;
     }
     tc_fence_before();
     __syncthreads();
@@ -485,52 +482,47 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             const int small = MODE != kWeights && nn <= 64 ? nn / 32 : 0;
             const int n_bytes = small ? small * 2048 : X_TILE;
             const int32_t first = MODE == kWeights ? ctl->row0[t.e] : 0;
-            for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
-                const int nsub = t.kblocks - kb0 < X_SUB ? t.kblocks - kb0 : X_SUB;
+            for (int kb = 0; kb < t.kblocks; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status));
                 if (!ok) break;
-                const bool tail = MODE == kWeights && t.red - kb0 * XK < X_SUB * XK;
+                const bool tail = MODE == kWeights && t.red - kb * XK < XK;
                 const uint32_t bar = tail ? smem_addr(&ctl->tail[stage]) : full0 + stage * 8;
                 if (elect_lane()) {
-                    if (tail) mbar_arrive_expect_tx(bar, nsub * 2 * X_TILE);
-                    else if (rank == 0) mbar_arrive_expect_tx(full + stage * 8, nsub * 2 * (X_TILE + n_bytes));
+                    if (tail) mbar_arrive_expect_tx(bar, 2 * X_TILE);
+                    else if (rank == 0) mbar_arrive_expect_tx(full + stage * 8, 2 * (X_TILE + n_bytes));
                     else if (MODE == kWeights) mbar_arrive_cluster(bar);
-                    for (int j = 0; j < nsub; ++j) {
-                        const int kb = kb0 + j;
-                        const uint32_t sa = smA0 + (stage * X_SUB + j) * X_TILE;
-                        const uint32_t sb = smB0 + (stage * X_SUB + j) * X_TILE;
-                        if (MODE == kWeights) {
-                            // 64 rows of the expert, 128 columns of a and of dc
-                            const int32_t r = first + kb * XK;
+                    const uint32_t sa = smA0 + stage * X_TILE, sb = smB0 + stage * X_TILE;
+                    if (MODE == kWeights) {
+                        // 64 rows of the expert, 128 columns of a and of dc
+                        const int32_t r = first + kb * XK;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                if (tail) {
-                                    tma_load_2d(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, r, bar);
-                                    tma_load_2d(sb + i * X_BOX, &tmB, (r0 + i * 64) * 2, r, bar);
-                                } else {
-                                    tma_load_2d_pair(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, r, bar);
-                                    tma_load_2d_pair(sb + i * X_BOX, &tmB, (r0 + i * 64) * 2, r, bar);
-                                }
-                            }
-                        } else {
-                            if (MODE == kForwardSilu) {   // gate and up columns in turn, a.turn of each
-                                tma_load_5d_pair(sa, &tmA, kb * XK * 2, 0, 0, c0 / a.turn, t.e, bar);
-                            } else if (MODE == kForward) {
-                                tma_load_3d_pair(sa, &tmA, kb * XK * 2, c0, t.e, bar);
+                        for (int i = 0; i < 2; ++i) {
+                            if (tail) {
+                                tma_load_2d(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, r, bar);
+                                tma_load_2d(sb + i * X_BOX, &tmB, (r0 + i * 64) * 2, r, bar);
                             } else {
-#pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    tma_load_3d_pair(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, kb * XK, t.e, bar);
+                                tma_load_2d_pair(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, r, bar);
+                                tma_load_2d_pair(sb + i * X_BOX, &tmB, (r0 + i * 64) * 2, r, bar);
                             }
-                            if (small == 0) tma_load_2d_pair(sb, &tmB, kb * XK * 2, r0, bar);
-                            for (int i = 0; i < small; ++i)
-                                tma_load_2d_pair(sb + i * 2048, &tmB16, kb * XK * 2, r0 + i * 16, bar);
                         }
+                    } else {
+                        if (MODE == kForwardSilu) {   // gate and up columns in turn, a.turn of each
+                            tma_load_5d_pair(sa, &tmA, kb * XK * 2, 0, 0, c0 / a.turn, t.e, bar);
+                        } else if (MODE == kForward) {
+                            tma_load_3d_pair(sa, &tmA, kb * XK * 2, c0, t.e, bar);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                tma_load_3d_pair(sa + i * X_BOX, &tmA, (c0 + i * 64) * 2, kb * XK, t.e, bar);
+                        }
+                        if (small == 0) tma_load_2d_pair(sb, &tmB, kb * XK * 2, r0, bar);
+                        for (int i = 0; i < small; ++i)
+                            tma_load_2d_pair(sb + i * 2048, &tmB16, kb * XK * 2, r0 + i * 16, bar);
                     }
                 }
                 __syncwarp();
                 ++issued;
-                if (++stage == X_SUPER) {
+                if (++stage == X_STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -539,8 +531,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         // after an abort CTA 0 lets the loads of the stages it armed land, both CTAs' bytes; CTA 1, which
         // cannot see its loads' completion, waits for CTA 0 at the closing cluster barrier
         if (!ok && rank == 0 && lane == 0) {
-            for (int s = 0; s < X_SUPER; ++s) {
-                const uint32_t n_s = (issued + X_SUPER - 1 - s) / X_SUPER;
+            for (int s = 0; s < X_STAGES; ++s) {
+                const uint32_t n_s = (issued + X_STAGES - 1 - s) / X_STAGES;
                 if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
             }
         }
@@ -550,7 +542,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             const uint64_t ad0 = A_MN ? smem_desc_mn_sw128(smem_addr(smA)) : smem_desc_k128_sw128(smem_addr(smA));
             const uint64_t bd0 = B_MN ? smem_desc_mn_sw128(smem_addr(smB)) : smem_desc_k128_sw128(smem_addr(smB));
             constexpr uint32_t a_step = (A_MN ? 2048 : 32) >> 4, b_step = (B_MN ? 2048 : 32) >> 4;
-            constexpr uint32_t sub_step = X_TILE >> 4, stage_step = X_SUB * X_TILE >> 4;
+            constexpr uint32_t stage_step = X_TILE >> 4;
             int stage = 0;
             uint32_t phase = 0, buf = 0, bphase = 0;
             bool ok = true;
@@ -563,32 +555,29 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                 if (!ok) break;
                 const uint32_t d = tmem + buf * XN;
                 const uint32_t idesc = idesc_16bit<T>(MODE == kWeights ? XN : rows_mma(t.nrow), A_MN, B_MN);
-                for (int kb0 = 0; kb0 < t.kblocks; kb0 += X_SUB) {
+                for (int kb = 0; kb < t.kblocks; ++kb) {
                     ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
                     if (!ok) break;
-                    const int left = t.red - kb0 * XK;
-                    if (MODE == kWeights && left < X_SUB * XK) mbar_acquire_cluster(smem_addr(&ctl->full[stage]), phase);
+                    const int left = t.red - kb * XK;
+                    if (MODE == kWeights && left < XK) mbar_acquire_cluster(smem_addr(&ctl->full[stage]), phase);
                     tc_fence_after();
                     const uint64_t ad = ad0 + stage * stage_step, bd = bd0 + stage * stage_step;
                     if (elect_lane()) {
-                        if (left >= X_SUB * XK) {
-                            mma_16bit_pair(d, ad, bd, idesc, kb0 > 0 ? 1u : 0u);
+                        if (left >= XK) {
+                            mma_16bit_pair(d, ad, bd, idesc, kb > 0 ? 1u : 0u);
 #pragma unroll
-                            for (int k = 1; k < X_SUB * XK / 16; ++k)
-                                mma_16bit_pair(d, ad + (k >> 2) * sub_step + (k & 3) * a_step,
-                                               bd + (k >> 2) * sub_step + (k & 3) * b_step, idesc, 1u);
+                            for (int k = 1; k < XK / 16; ++k)
+                                mma_16bit_pair(d, ad + k * a_step, bd + k * b_step, idesc, 1u);
                         } else {
                             const int steps = (left + 15) / 16;
                             for (int k = 0; k < steps; ++k)
-                                mma_16bit_pair(d, ad + (k >> 2) * sub_step + (k & 3) * a_step,
-                                               bd + (k >> 2) * sub_step + (k & 3) * b_step, idesc,
-                                               (kb0 | k) > 0 ? 1u : 0u);
+                                mma_16bit_pair(d, ad + k * a_step, bd + k * b_step, idesc, (kb | k) > 0 ? 1u : 0u);
                         }
                         mma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
-                        if (kb0 + X_SUB >= t.kblocks) mma_commit_pair(smem_addr(&ctl->tfull[buf]), 3);
+                        if (kb + 1 == t.kblocks) mma_commit_pair(smem_addr(&ctl->tfull[buf]), 3);
                     }
                     __syncwarp();
-                    if (++stage == X_SUPER) {
+                    if (++stage == X_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -612,19 +601,17 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             const int64_t w = item_of_round<MODE>(round, rounds);
             if (w >= total) continue;
             const XItem t = item_at<MODE>(a, ctl, w, NT);
-            const int stages = (t.kblocks + X_SUB - 1) / X_SUB;
-            if (stages == 0) continue;
-            const int live = t.red - (stages - 1) * X_SUB * XK;   // rows of the last stage, 1 .. 128
-            const int last = (stage + stages - 1) % X_SUPER;
-            stage = (last + 1) % X_SUPER;
-            if (live == X_SUB * XK) continue;
+            if (t.kblocks == 0) continue;
+            const int live = t.red - (t.kblocks - 1) * XK;   // rows of the last stage, 1 .. 64
+            const int last = (stage + t.kblocks - 1) % X_STAGES;
+            stage = (last + 1) % X_STAGES;
+            if (live == XK) continue;
             ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tail[last]), (tails >> last) & 1u, abort_flag, a.status));
             if (!ok) break;
             tails ^= 1u << last;
             // the MMAs run in steps of 16 rows: the rest of the last step's rows, in this CTA's four boxes
-            const int sub = (live - 1) / XK, row = live - sub * XK;
-            const int pieces = ((row + 15) / 16 * 16 - row) * 8;   // 16-byte pieces of a box
-            uint8_t* at = smA + (last * X_SUB + sub) * X_TILE + row * 128;
+            const int pieces = ((live + 15) / 16 * 16 - live) * 8;   // 16-byte pieces of a box
+            uint8_t* at = smA + last * X_TILE + live * 128;
             for (int i = lane; i < pieces * 4; i += 32) {
                 const int box = i / pieces, p = i - box * pieces;
                 *reinterpret_cast<uint4*>(at + (box & 1) * X_BOX + (box >> 1) * (smB - smA) + p * 16) = make_uint4(0, 0, 0, 0);
