@@ -63,22 +63,30 @@ __device__ __forceinline__ double join_warp(double acc, int inf) {
     return acc;
 }
 
-// A chunk: n elements of tensor k from element e0; bytes of it that come by bulk copies (none where an
-// address of the tensor is not a multiple of 16).
+// A chunk: n elements of tensor k from element e0, between two 8 KB boundaries from the 16-byte one at
+// or before the tensor's start.  `bulk` bytes from element `head` come by bulk copies, what is before and
+// after them (a tensor that starts or ends inside 16 bytes) element by element.
 struct Chunk {
     int k;
     int64_t e0;
-    int n, bulk;
+    int n, head, bulk;
 };
+__host__ __device__ __forceinline__ int lead_elements(const void* p, int es) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / es);
+}
 template <int N>
 __device__ __forceinline__ Chunk chunk_at(const ClipTable<N>& t, int64_t c) {
     Chunk u;
     u.k = tensor_of(t, c);
     const int es = t.dtype[u.k] == MOE_DTYPE_FP32 ? 4 : 2, per = kChunkBytes / es;
-    u.e0 = (c - t.chunk0[u.k]) * per;
+    const int lead = lead_elements(t.src[u.k], es), V = 16 / es;
+    const bool first = c == t.chunk0[u.k];
+    u.e0 = first ? 0 : (c - t.chunk0[u.k]) * per - lead;
+    const int room = first ? per - lead : per;
     const int64_t left = t.numel[u.k] - u.e0;
-    u.n = left < per ? static_cast<int>(left) : per;
-    u.bulk = (reinterpret_cast<uintptr_t>(t.src[u.k]) | reinterpret_cast<uintptr_t>(t.dst[u.k])) & 15 ? 0 : u.n * es / 16 * 16;
+    u.n = left < room ? static_cast<int>(left) : room;
+    u.head = first && lead ? (V - lead < u.n ? V - lead : u.n) : 0;
+    u.bulk = (u.n - u.head) * es / 16 * 16;
     return u;
 }
 
@@ -113,7 +121,7 @@ struct ClipRing {
     __device__ __forceinline__ void issue() {
         while (left == 0 && next < chunks) {
             const Chunk u = chunk_at(t, index(next));
-            src = static_cast<const char*>(t.src[u.k]) + u.e0 * (t.dtype[u.k] == MOE_DTYPE_FP32 ? 4 : 2);
+            src = static_cast<const char*>(t.src[u.k]) + (u.e0 + u.head) * (t.dtype[u.k] == MOE_DTYPE_FP32 ? 4 : 2);
             left = u.bulk;
             next += stride;
         }
@@ -140,8 +148,9 @@ struct ClipRing {
                 if (n > 0) mbar_wait(smem_addr(bars + i), (n - 1) & 1u, nullptr, status);
             }
     }
-    // This lane's vectors of a piece of nv, f(vector index, vector) each; then the slot takes the next piece.
-    template <class T, class F>
+    // This lane's vectors of a piece of nv, f(vector index, vector) each; then the slot takes the next
+    // piece.  ALL: f is called by whole warps, on the lanes past nv too (with no data).
+    template <class T, bool ALL, class F>
     __device__ __forceinline__ void piece(int nv, F f) {
         constexpr int V = 16 / static_cast<int>(sizeof(T));
         mbar_wait(smem_addr(bars + slot), phase, abort_flag, status);
@@ -158,7 +167,7 @@ struct ClipRing {
         issue();
 #pragma unroll
         for (int i = 0; i < kPiece / 512; ++i)
-            if (lane + i * 32 < nv) f(lane + i * 32, x[i]);
+            if (ALL ? i * 32 < nv : lane + i * 32 < nv) f(lane + i * 32, x[i]);
     }
 };
 
@@ -169,7 +178,7 @@ __device__ __forceinline__ double share_norm(R& ring, const T* p, const Chunk& u
     const int lane = threadIdx.x & 31, nv = u.bulk / 16;
     float ss = 0.0f, top = 0.0f;
     for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
-        ring.template piece<T>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int, const Pack<T, V>& x) {
+        ring.template piece<T, false>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int, const Pack<T, V>& x) {
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float v = x.get(e);
@@ -177,23 +186,23 @@ __device__ __forceinline__ double share_norm(R& ring, const T* p, const Chunk& u
                 top = max_nan(top, fabsf(v));
             }
         });
-    for (int i = nv * V + lane; i < u.n; i += 32) {
-        const float v = to_f32(p[i]);
+    const auto loose = [&](auto f) {   // (less than a vector on either side)
+        if (lane < u.head) f(to_f32(p[lane]));
+        if (u.head + nv * V + lane < u.n) f(to_f32(p[u.head + nv * V + lane]));
+    };
+    loose([&](float v) {
         ss = fmaf(v, v, ss);
         top = max_nan(top, fabsf(v));
-    }
+    });
     if (inf) return top;
     if (top > 1e18f || (top < 1e-18f && top > 0.0f)) {
         double sd = 0.0;
         for (int v = lane; v < nv; v += 32)
             for (int e = 0; e < V; ++e) {
-                const double x = to_f32(p[v * V + e]);
+                const double x = to_f32(p[u.head + v * V + e]);
                 sd = fma(x, x, sd);
             }
-        for (int i = nv * V + lane; i < u.n; i += 32) {
-            const double x = to_f32(p[i]);
-            sd = fma(x, x, sd);
-        }
+        loose([&](float v) { sd = fma(static_cast<double>(v), static_cast<double>(v), sd); });
         return sd;
     }
     return ss;
@@ -242,15 +251,28 @@ __global__ void __launch_bounds__(kClipThreads, 1)
 template <class T, class R>
 __device__ __forceinline__ void scale_share(R& ring, const T* p, T* q, const Chunk& u, float scale) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    const int nv = u.bulk / 16;
-    for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
-        ring.template piece<T>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
-            Pack<T, V> o;
+    const int nv = u.bulk / 16, lane = threadIdx.x & 31;
+    T* qb = q + u.head;
+    const auto scaled = [&](const Pack<T, V>& x) {
+        Pack<T, V> o;
 #pragma unroll
-            for (int e = 0; e < V; ++e) o.set(e, x.get(e) * scale);
-            o.store(q + (v0 + v) * V);
-        });
-    for (int i = nv * V + (threadIdx.x & 31); i < u.n; i += 32) q[i] = from_f32<T>(to_f32(p[i]) * scale);
+        for (int e = 0; e < V; ++e) o.set(e, x.get(e) * scale);
+        return o;
+    };
+    if ((reinterpret_cast<uintptr_t>(qb) & 15) == 0) {
+        for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
+            ring.template piece<T, false>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
+                scaled(x).store(qb + (v0 + v) * V);
+            });
+    } else {   // the result's vectors lie elsewhere than the gradient's
+        for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
+            ring.template piece<T, true>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
+                store_any(qb, nv * V, v0 + v, scaled(x).raw);
+            });
+    }
+    if (lane < u.head) q[lane] = from_f32<T>(to_f32(p[lane]) * scale);
+    const int tail = u.head + nv * V + lane;
+    if (tail < u.n) q[tail] = from_f32<T>(to_f32(p[tail]) * scale);
 }
 
 // Every CTA joins the partial results (np of them) and scales its chunks, the last first: they are
@@ -295,9 +317,10 @@ __global__ void __launch_bounds__(kClipThreads, 1)
 }
 #undef MOE_CLIP_PROLOGUE
 
-int64_t chunks_of(int64_t numel, int dtype) {
-    const int64_t per = kChunkBytes / static_cast<int64_t>(dtype_bytes(dtype));
-    return (numel + per - 1) / per;
+int64_t chunks_of(const void* src, int64_t numel, int dtype) {
+    const int es = static_cast<int>(dtype_bytes(dtype));
+    const int64_t per = kChunkBytes / es;
+    return numel == 0 ? 0 : (lead_elements(src, es) + numel + per - 1) / per;
 }
 
 struct ClipCall {
@@ -324,7 +347,7 @@ void fill_table(ClipTable<N>* t, const ClipCall& c, int k0, int k1) {
         t->dst[i] = c.dst[k];
         t->numel[i] = c.numel[k];
         t->dtype[i] = static_cast<uint8_t>(c.dtype[k]);
-        t->chunk0[i + 1] = t->chunk0[i] + chunks_of(c.numel[k], c.dtype[k]);
+        t->chunk0[i + 1] = t->chunk0[i] + chunks_of(c.src[k], c.numel[k], c.dtype[k]);
     }
 }
 

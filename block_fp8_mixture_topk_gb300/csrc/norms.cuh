@@ -11,7 +11,7 @@
 // All are bound by memory: every element is read once from DRAM and held between the row's reduction
 // and its use (at most 32 elements per thread, G threads per row).  A CTA holds R groups of G
 // threads, each with its own named barrier, and walks over rows with the weights at hand.  Two
-// sources of rows and weights: registers (RowRegs: any alignment, and few rows), or shared memory
+// sources of rows and weights: registers (RowRegs: few rows; RowAny: rows at any address), or shared memory
 // (RowRing: 16-byte rows; one thread of a group keeps up to four rows of bulk copies in flight
 // ahead of the group, so that the reduction's latency does not stop the loads).  The weights'
 // gradient is summed over a CTA's rows in fp32 registers, over its groups in shared memory, written once
@@ -105,36 +105,31 @@ __device__ __forceinline__ Group make_group(float* red, int G) {
     return g;
 }
 
-template <class T, int V, int NV>
-__device__ __forceinline__ void load_row(Pack<T, V> (&r)[NV], const T* p, int tid, int G, int nvec) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * G;
-        if (v < nvec) r[i].load(p + static_cast<int64_t>(v) * V);
-        else r[i].zero();
-    }
-}
-
 // ---------------------------------------------------------------- sources of rows
 // A source hands out a group's rows of NIN matrices and a row of weights (fp32): start() and weights()
 // once, then for each row fetch(t), get(n, i) = vector i of this thread in matrix n (any number of
-// times) and next() (the row is done with); finish() at the end.  weight(i) = the weights of vector i.
+// times) and next() (the row is done with); finish() at the end.  weight(i) = the weights of vector i;
+// store(row, i, o) writes it, skip(i) tells that there is nothing of it to write.  Vectors and elements
+// past the row read as zero.
 template <int V>
 struct Weights {
-    float2 v[(V + 1) / 2];
+    float2 v[V / 2];
 };
 
-template <class T, int V, int NV, int NIN>
-struct RowRegs {
+template <class T, int V, int NV, int NIN, bool ANY>
+struct RowInRegs {
     static constexpr bool kWide = false;
     Weights<V> w[NV];
     Pack<T, V> r[NIN][NV];
     const T* src[NIN];
     int64_t ld[NIN];
-    int G, tid, nvec;
+    int G, tid, H, nvec;
+    int64_t T_;
     __device__ __forceinline__ void start(const NormArgs& a, const Group& g, int64_t, int64_t, int, uint8_t*) {
         G = a.G;
         tid = g.tid;
+        H = a.H;
+        T_ = a.T;
         nvec = a.H / V;
     }
     // f(column) = its weight
@@ -144,22 +139,70 @@ struct RowRegs {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const int v = tid + i * G;
-                const float x = v < nvec ? f(v * V + e) : 0.0f;
+                const int c = vec(i) * V + e;
+                const float x = c < H ? f(c) : 0.0f;
                 if (e & 1) w[i].v[e / 2].y = x;
-                else w[i].v[e / 2] = make_float2(x, 0.0f);
+                else w[i].v[e / 2].x = x;
             }
     }
     __device__ __forceinline__ void weights_done() {}
     __device__ __forceinline__ Weights<V> weight(int i) const { return w[i]; }
     __device__ __forceinline__ void fetch(int64_t t) {
+        if constexpr (ANY) {
+            const int lane = threadIdx.x & 31;
+            if (!inner_row(t, T_)) {
 #pragma unroll
-        for (int n = 0; n < NIN; ++n) load_row<T, V, NV>(r[n], src[n] + t * ld[n], tid, G, nvec);
+                for (int n = 0; n < NIN; ++n)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) r[n][i].raw = load_elements(src[n] + t * ld[n], H, vec(i) * V);
+                return;
+            }
+            // the warp's NV * 32 vectors and the next one, which the first lane holds: the next lane of the last is
+            // the first, one vector on
+            uint4 beyond[NIN];
+#pragma unroll
+            for (int n = 0; n < NIN; ++n) {
+                const T* row = src[n] + t * ld[n];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) r[n][i].raw = load_around(row, H, vec(i) * V);
+                beyond[n] = load_around(row, H, vec(NV) * V, lane == 0);
+            }
+#pragma unroll
+            for (int n = 0; n < NIN; ++n) {
+                const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src[n] + t * ld[n])) & 15u;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const uint4 w = r[n][i].raw, on = i + 1 < NV ? r[n][i + 1 < NV ? i + 1 : 0].raw : beyond[n];
+                    const uint4 hi = shuffle(lane == 0 ? on : w, (lane + 1) & 31);
+                    r[n][i].raw = inside_row<T>(bytes_from(w, hi, s), H, vec(i) * V);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int n = 0; n < NIN; ++n)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = tid + i * G;
+                if (v < nvec) r[n][i].load(src[n] + t * ld[n] + v * V);
+                else r[n][i].zero();
+            }
     }
+    // this thread's i-th vector of a row; at any address the vectors of a warp are neighbours
+    __device__ __forceinline__ int vec(int i) const { return ANY ? ((tid >> 5) * NV + i) * 32 + (tid & 31) : tid + i * G; }
     __device__ __forceinline__ Pack<T, V> get(int n, int i) const { return r[n][i]; }
+    __device__ __forceinline__ bool skip(int i) const { return !ANY && tid + i * G >= nvec; }
+    __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const {
+        if constexpr (ANY) store_any(row, H, vec(i), o.raw);
+        else o.store(row + vec(i) * V);
+    }
     __device__ __forceinline__ void next(const Group&) {}
     __device__ __forceinline__ void finish() {}
 };
+template <class T, int V, int NV, int NIN>
+struct RowRegs : RowInRegs<T, V, NV, NIN, false> {};
+template <class T, int V, int NV, int NIN>
+struct RowAny : RowInRegs<T, V, NV, NIN, true> {};
 
 template <class T, int V, int NV, int NIN>
 struct RowRing {
@@ -257,6 +300,9 @@ struct RowRing {
         else p.zero();
         return p;
     }
+    __device__ __forceinline__ int vec(int i) const { return tid + i * G; }
+    __device__ __forceinline__ bool skip(int i) const { return vec(i) >= nvec; }
+    __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const { o.store(row + vec(i) * V); }
     // the group is done with the row: its slot takes the next one
     __device__ __forceinline__ void next(const Group& g) {
         g.sync();
@@ -284,8 +330,8 @@ __device__ __forceinline__ float gated_weight(const NormArgs& a, int c) {
     extern __shared__ __align__(128) uint8_t norm_smem[];                             \
     __shared__ __align__(16) float red[kNormGroups * 32];                                                    \
     Group g = make_group(red, a.G);                                                   \
-    constexpr int NP = (V + 1) / 2;                                                   \
-    const int nvec = a.H / V, R = blockDim.x / a.G;                                   \
+    constexpr int NP = V / 2;                                                   \
+    const int R = blockDim.x / a.G;                                   \
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * R + g.id, step = static_cast<int64_t>(gridDim.x) * R; \
     grid_dependency_wait();
 
@@ -314,14 +360,13 @@ __global__ void __launch_bounds__(Rows<T, V, NV, 1>::kWide ? kNormWideThreads : 
         T* out = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = g.tid + i * a.G;
-            if (v >= nvec) continue;
+            if (in.skip(i)) continue;
             const Pack<T, V> x = in.get(0, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o;
 #pragma unroll
             for (int e = 0; e < NP; ++e) o.set_pair(e, mul2(mul2(x.pair(e), both(r)), w.v[e]));
-            o.store(out + static_cast<int64_t>(v) * V);
+            in.store(out, i, o);
         }
         in.next(g);
     }
@@ -349,12 +394,9 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
     if constexpr (NEXT) {
 #pragma unroll
         for (int i = 0; i < NV * NP; ++i) {
-            const int v = g.tid + (i / NP) * a.G, c = v * V + (i % NP) * 2;
-            w2[i] = both(0.0f);
-            if (v < nvec) {
-                w2[i].x = weight_at(a.w2, a.w_dtype, c) + a.w_offset;
-                if (V > 1) w2[i].y = weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset;
-            }
+            const int c = in.vec(i / NP) * V + (i % NP) * 2;
+            w2[i].x = c < a.H ? weight_at(a.w2, a.w_dtype, c) + a.w_offset : 0.0f;
+            w2[i].y = c + 1 < a.H ? weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset : 0.0f;
         }
     }
     for (int64_t t = t0; t < a.T; t += step) {
@@ -380,7 +422,6 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
         Pack<T, V> s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = g.tid + i * a.G;
             const Pack<T, V> y = in.get(0, i), res = in.get(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> gt;
@@ -393,7 +434,7 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
                 s[i].set_pair(e, fma2(both(a.a), res.pair(e), z));
                 if constexpr (NEXT) s2 = fma2(s[i].pair(e), s[i].pair(e), s2);
             }
-            if (v < nvec) s[i].store(out + static_cast<int64_t>(v) * V);
+            if (!in.skip(i)) in.store(out, i, s[i]);
         }
         in.next(g);
         if constexpr (NEXT) {
@@ -402,12 +443,11 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
             T* h2 = static_cast<T*>(a.h2) + t * a.H;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int v = g.tid + i * a.G;
-                if (v >= nvec) continue;
+                if (in.skip(i)) continue;
                 Pack<T, V> o;
 #pragma unroll
                 for (int e = 0; e < NP; ++e) o.set_pair(e, mul2(mul2(s[i].pair(e), both(r2)), w2[i * NP + e]));
-                o.store(h2 + static_cast<int64_t>(v) * V);
+                in.store(h2, i, o);
             }
         }
     }
@@ -415,23 +455,23 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
 }
 
 // The CTA's sums over rows (times scale), group after group, into its row of the partials.
-template <int V, int NV>
-__device__ __forceinline__ void write_partial(const float2 (&acc)[NV * ((V + 1) / 2)], float scale, float* sum_s,
-                                              const Group& g, int R, int nvec, float* partial) {
-    constexpr int NP = (V + 1) / 2;
+template <int V, int NV, class Rows>
+__device__ __forceinline__ void write_partial(const float2 (&acc)[NV * (V / 2)], float scale, float* sum_s,
+                                              const Rows& in, const Group& g, int R, int H, float* partial) {
+    constexpr int NP = V / 2;
     __syncthreads();   // sum_s is the ring's memory
     for (int k = 0; k < R; ++k) {
         if (g.id == k) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int v = g.tid + i * g.G;
-                if (v >= nvec) continue;
+                const int c0 = in.vec(i) * V;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
+                    if (c0 + e >= H) break;
                     const float2 p = acc[i * NP + e / 2];
-                    const float u = (e & 1 ? p.y : p.x) + (k > 0 ? sum_s[v * V + e] : 0.0f);
-                    if (k + 1 < R) sum_s[v * V + e] = u;
-                    else partial[v * V + e] = u * scale;
+                    const float u = (e & 1 ? p.y : p.x) + (k > 0 ? sum_s[c0 + e] : 0.0f);
+                    if (k + 1 < R) sum_s[c0 + e] = u;
+                    else partial[c0 + e] = u * scale;
                 }
             }
         }
@@ -477,8 +517,7 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
         T* out = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = g.tid + i * a.G;
-            if (v >= nvec) continue;
+            if (in.skip(i)) continue;
             const Pack<T, V> x = in.get(0, i), d = in.get(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o, s;
@@ -489,12 +528,12 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
                 if constexpr (RES) o.set_pair(e, fma2(u, both(r), s.pair(e)));
                 else o.set_pair(e, mul2(u, both(r)));
             }
-            o.store(out + static_cast<int64_t>(v) * V);
+            in.store(out, i, o);
         }
         in.next(g);
     }
     in.finish();
-    write_partial<V, NV>(acc, 1.0f, reinterpret_cast<float*>(norm_smem), g, R, nvec,
+    write_partial<V, NV>(acc, 1.0f, reinterpret_cast<float*>(norm_smem), in, g, R, a.H,
                          a.partial + static_cast<int64_t>(blockIdx.x) * a.H);
 }
 
@@ -562,8 +601,7 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
         T* dy = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = g.tid + i * a.G;
-            if (v >= nvec) continue;
+            if (in.skip(i)) continue;
             const Pack<T, V> y = in.get(0, i), d = in.get(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o, p, q, gt;
@@ -583,16 +621,15 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
                 o.set_pair(e, mul2(scale, fma2(n, m, dw)));
                 p.set_pair(e, mul2(both(a.a), d.pair(e)));
             }
-            const int64_t at = static_cast<int64_t>(v) * V;
-            o.store(dy + at);
-            if (a.dres) p.store(static_cast<T*>(a.dres) + t * a.H + at);
+            in.store(dy, i, o);
+            if (a.dres) in.store(static_cast<T*>(a.dres) + t * a.H, i, p);
             if constexpr (FULL)
-                if (a.dgate) q.store(static_cast<T*>(a.dgate) + t * a.H + at);
+                if (a.dgate) in.store(static_cast<T*>(a.dgate) + t * a.H, i, q);
         }
         in.next(g);
     }
     in.finish();
-    write_partial<V, NV>(acc, GATE == kGateChannel ? 1.0f : a.b, reinterpret_cast<float*>(norm_smem), g, R, nvec,
+    write_partial<V, NV>(acc, GATE == kGateChannel ? 1.0f : a.b, reinterpret_cast<float*>(norm_smem), in, g, R, a.H,
                          a.partial + static_cast<int64_t>(blockIdx.x) * a.H);
 }
 #undef MOE_NORM_PROLOGUE
@@ -663,7 +700,7 @@ cudaError_t launch_norm(K kernel, NormArgs a, int threads, bool backward, int ri
 
 template <class T, int V, int NV, template <class, int, int, int> class Rows, bool RING>
 cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_t stream, int* ctas) {
-    a.G = norm_group(a.H / V, NV);
+    a.G = norm_group((a.H + V - 1) / V, NV);
     const bool next = a.w2 != nullptr;
 #define MOE_NORM(INPUTS, BACKWARD, ...)                                                                          \
     do {                                                                                                         \
@@ -701,19 +738,20 @@ cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_
 #undef MOE_NORM
 }
 
-// V elements per vector: 16 bytes where rows and addresses allow it, else one element.
-//   16 bytes, fewer rows than twice the SMs: registers, 16 elements per thread where the row then
-//     fits a CTA's threads (more threads on each row)
-//   16 bytes: the ring, 32 elements per thread (registers where the weights and two rows do not
+// Where the rows come from, by their alignment (wide: 16-byte addresses and strides), number and width:
+//   fewer rows than twice the SMs: registers, 16 elements per thread where the row then fits a CTA's
+//     threads (more threads on each row)
+//   else wide rows: the ring, 32 elements per thread (registers where the weights and two rows do not
 //     fit a CTA's shared memory)
-//   one element: registers, 8 or 32 elements per thread
+//   rows at any address: registers, 16 elements per thread where the row then fits, else 32
 template <class T>
 cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, int sms, cudaStream_t stream,
                              int* ctas) {
     constexpr int W = 16 / static_cast<int>(sizeof(T));
     if (!wide) {
-        if (a.H <= 8 * kNormThreads) return launch_norm_nv<T, 1, 8, RowRegs, false>(a, which, gate, sms, stream, ctas);
-        return launch_norm_nv<T, 1, 32, RowRegs, false>(a, which, gate, sms, stream, ctas);
+        if (a.H <= 16 * kNormThreads)
+            return launch_norm_nv<T, W, 16 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
+        return launch_norm_nv<T, W, 32 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
     }
     if (a.T < 2 * sms && a.H <= 16 * kNormThreads)
         return launch_norm_nv<T, W, 16 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);

@@ -47,7 +47,8 @@ struct DispatchArgs {
     int chunk;                 // pairs per chunk (blockIdx.x), a multiple of topk
     int nch;
     const int32_t* counts;     // [nch][E], or null: every CTA counts the ids itself
-    int vecs, slab;            // vectors per row, vectors per column slab (blockIdx.y)
+    int H;
+    int vecs, slab;            // most vectors of a row, vectors per column slab (blockIdx.y)
     char* rows;
     int32_t* expert_offsets;
     int32_t* pair_ids;
@@ -119,10 +120,57 @@ __device__ __forceinline__ void copy_round(const DispatchArgs& a, const int* pos
         for (int i = 0; i < a.slots; ++i) mbar_wait(smem_addr(bars + i), ((*phases >> i) & 1u) ^ 1u, nullptr, a.status);
 }
 
+// Vectors that a row of H elements of E touches at most: it may start and end inside one.
+template <class E>
+constexpr int vectors_any(int H) {
+    return (H + 2 * (16 / static_cast<int>(sizeof(E))) - 2) / (16 / static_cast<int>(sizeof(E)));
+}
+// First element of the row's v-th aligned vector (negative for the first one of a row that starts inside it).
+template <class E>
+__device__ __forceinline__ int vector_any(const E* row, int v) {
+    constexpr int V = 16 / static_cast<int>(sizeof(E));
+    return v * V - static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(E));
+}
+
+// A round's copies for rows at any address: a warp to a pair, vectors v0 .. v0 + nv - 1 of its row in parts of
+// kAnyLanes.
+template <class E>
+__device__ __forceinline__ void copy_round_any(const DispatchArgs& a, const int* pos_s, int64_t t0, int pairs, int v0,
+                                               int nv) {
+    constexpr int V = 16 / static_cast<int>(sizeof(E)), U = 4;
+    const int64_t ld = a.ld_bytes / static_cast<int64_t>(sizeof(E)), T_ = a.P / a.topk;
+    const int lane = threadIdx.x & 31;
+    for (int p = threadIdx.x >> 5; p < pairs; p += kSortThreads / 32) {
+        const int r = pos_s[p];
+        if (r < 0) continue;
+        const int64_t t = t0 + p / a.topk;
+        const E* src = reinterpret_cast<const E*>(a.x) + t * ld;
+        E* dst = reinterpret_cast<E*>(a.rows) + static_cast<int64_t>(r) * a.H;
+        const int e0 = vector_any(dst, v0), e1 = min(a.H, e0 + nv * V);   // (whole vectors from e0 on)
+        if (!inner_row(t, T_)) {
+            for (int e = e0 + lane * V; e < e1; e += 32 * V) store_whole(dst, a.H, e, load_elements(src, a.H, e));
+            continue;
+        }
+        for (int e = e0 + lane * V; e - lane * V < e1; e += U * kAnyLanes * V) {
+            uint4 w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u] = load_around(src, a.H, e + u * kAnyLanes * V);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = e + u * kAnyLanes * V;
+                if (at - lane * V >= e1) break;
+                w[u] = join_lanes(w[u], src + at);
+                if (lane < kAnyLanes && at < e1) store_whole(dst, a.H, at, w[u]);
+            }
+        }
+    }
+}
+
 // The sort and the copies of one chunk of tokens and one slab of columns.  Every CTA derives the
 // first row of its chunk for each expert from the pair counts (a scan over experts of the totals,
 // plus the pairs of earlier chunks), ranks its pairs with a warp match, and copies its tokens: a
-// row is read once and written topk times.  The slab-0 CTAs also write the tables.
+// row is read once and written topk times.  The slab-0 CTAs also write the tables.  R: the vector, or the
+// element of rows at any address.
 template <class R, bool BULK>
 __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchArgs a) {
     extern __shared__ __align__(128) int smem[];
@@ -184,7 +232,6 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     const int nv = a.vecs - v0 < a.slab ? a.vecs - v0 : a.slab;
     const bool tables = blockIdx.y == 0;
     const int round = kSortThreads / a.topk * a.topk;
-    R* rows = reinterpret_cast<R*>(a.rows);
     for (int64_t r0 = p0; r0 < p1; r0 += round) {
         for (int i = tid; i < 32 * a.E / 2; i += kSortThreads) reinterpret_cast<int*>(warp_count)[i] = 0;
         __syncthreads();
@@ -228,7 +275,12 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
                            bars + warp * kMostSlots, &phases, &abort_s);
             __syncthreads();
             continue;
+        } else if constexpr (sizeof(R) < 16) {
+            copy_round_any<R>(a, pos_s, t0, n, v0, nv);
+            __syncthreads();
+            continue;
         }
+        R* rows = reinterpret_cast<R*>(a.rows);
         const int items = tokens * nv;
         constexpr int U = 4;
         for (int i = tid; i < items; i += U * kSortThreads) {
@@ -256,21 +308,27 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     // rows of no pair (as many as there are pairs without an expert): zero, at the end
     const int64_t left = (a.P - total) * nv;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; i < left;
-         i += static_cast<int64_t>(gridDim.x) * kSortThreads)
-        rows[(total + i / nv) * a.vecs + v0 + i % nv] = R{};
+         i += static_cast<int64_t>(gridDim.x) * kSortThreads) {
+        const int64_t r = total + i / nv;
+        const int v = v0 + static_cast<int>(i % nv);
+        R* rows = reinterpret_cast<R*>(a.rows);
+        if constexpr (sizeof(R) < 16) store_whole(rows + r * a.H, a.H, vector_any(rows + r * a.H, v), make_uint4(0u, 0u, 0u, 0u));
+        else rows[r * a.vecs + v] = R{};
+    }
     if (tables)
         for (int64_t r = total + static_cast<int64_t>(blockIdx.x) * kSortThreads + tid; r < a.P;
              r += static_cast<int64_t>(gridDim.x) * kSortThreads)
             a.pair_ids[r] = -1;
 }
 
-// out[t] = sum_j w[t, j] * y[pos[t, j]] (w null: 1), one thread per vector of V elements.
-template <class T, int V>
+// out[t] = sum_j w[t, j] * y[pos[t, j]] (w null: 1), one thread per 16-byte vector of the result.
+template <class T>
 __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y, int64_t ld,
                                                       const int32_t* __restrict__ pos,
                                                       const float* __restrict__ w, int64_t n_tokens, int topk,
                                                       int vecs, int64_t num_rows, T* __restrict__ out,
                                                       uint32_t* status) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
     grid_dependency_wait();
     const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= n_tokens * vecs) return;
@@ -309,6 +367,66 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y, i
 #pragma unroll
     for (int e = 0; e < V; ++e) o.set(e, acc[e]);
     o.store(out + (t * vecs + v) * V);
+}
+
+// The same for rows at any address: a warp to a token and a part of kAnyLanes vectors of the result; lane j
+// holds the row and the weight of pair j.
+template <class T>
+__global__ void __launch_bounds__(256) combine_any_kernel(const T* __restrict__ y, int64_t ld,
+                                                          const int32_t* __restrict__ pos,
+                                                          const float* __restrict__ w, int n_tokens, int topk, int H,
+                                                          int parts, int num_rows, T* __restrict__ out,
+                                                          uint32_t* status) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T)), U = 4;
+    grid_dependency_wait();
+    const uint32_t i = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, t = i / parts, part = i - t * parts;
+    if (t >= n_tokens) return;
+    const int lane = threadIdx.x & 31;
+    int mine = -1;
+    float weight = 1.0f;
+    if (lane < topk) {
+        mine = pos[static_cast<int64_t>(t) * topk + lane];
+        if (w) weight = w[static_cast<int64_t>(t) * topk + lane];
+        if (mine >= num_rows) {
+            if (part == 0) status_set(status, MOE_STATUS_BAD_EXPERT_ID);
+            mine = -1;
+        }
+    }
+    T* row = out + static_cast<int64_t>(t) * H;
+    const int e0 = vector_any(row, static_cast<int>(part) * kAnyLanes + lane);
+    float2 acc[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) acc[e] = both(0.0f);
+    for (uint32_t live = __ballot_sync(0xffffffffu, mine >= 0); live;) {
+        uint4 x[U];
+        const T* src[U];
+        float wj[U];
+        uint32_t inner = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            src[u] = nullptr;
+            if (!live) continue;
+            const int j = __ffs(live) - 1, r = __shfl_sync(0xffffffffu, mine, j);
+            live &= live - 1;
+            wj[u] = __shfl_sync(0xffffffffu, weight, j);
+            src[u] = y + r * ld;
+            if (!inner_row(r, num_rows)) continue;
+            inner |= 1u << u;
+            x[u] = load_around(src[u], H, e0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!src[u]) break;
+            Pack<T, V> p;
+            p.raw = inner >> u & 1 ? join_lanes(x[u], src[u] + e0) : load_elements(src[u], H, e0);
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) acc[e] = fma2(both(wj[u]), p.pair(e), acc[e]);
+        }
+    }
+    Pack<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) o.set_pair(e, acc[e]);
+    if (lane < kAnyLanes) store_whole(row, H, e0, o.raw);
 }
 
 // The same for rows of 16-byte addresses and strides and many tokens.  A CTA holds groups of G threads; a
@@ -442,12 +560,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_ring_kernel(const Com
 // One warp per pair: dy[pos] = w * dout[t] and dw = <dout[t], y[pos]>.  The pairs of one token are
 // neighbouring warps, so that dout comes from DRAM once.  The warps past the pairs zero the rows
 // that belong to no pair, 32 rows each.
-template <class T, int V>
+template <class T, bool ANY>
 __global__ void __launch_bounds__(256)
     combine_backward_kernel(const T* __restrict__ dout, int64_t ldo, const T* __restrict__ y, int64_t ldy,
                             const int32_t* __restrict__ pos, const int32_t* __restrict__ pair_ids,
-                            const float* __restrict__ w, int64_t P, int topk, int vecs, int64_t num_rows,
+                            const float* __restrict__ w, int64_t P, int topk, int H, int vecs, int64_t num_rows,
                             T* __restrict__ dy, float* __restrict__ dw, uint32_t* status) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const int64_t p = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -460,7 +579,11 @@ __global__ void __launch_bounds__(256)
         while (empty) {
             const int64_t r = r0 + __ffs(empty) - 1;
             empty &= empty - 1;
-            for (int v = lane; v < vecs; v += 32) z.store(dy + (r * vecs + v) * V);
+            T* dr = dy + r * H;
+            for (int v = lane; v < vecs; v += 32) {
+                if constexpr (ANY) store_whole(dr, H, vector_any(dr, v), z.raw);
+                else z.store(dr + v * V);
+            }
         }
         return;
     }
@@ -475,23 +598,50 @@ __global__ void __launch_bounds__(256)
     const float wp = w ? w[p] : 1.0f;
     const T* o = dout + p / topk * ldo;
     const T* yr = y + r * ldy;
-    T* dr = dy + r * vecs * V;
+    T* dr = dy + r * H;
     float dot = 0.0f;
-    constexpr int U = 4;
-    for (int v0 = lane; v0 < vecs; v0 += 32 * U) {
+    if constexpr (ANY)
+        if (!inner_row(p / topk, P / topk) || !inner_row(r, num_rows)) {
+            for (int v = lane; v < vecs; v += 32) {
+                const int e0 = vector_any(dr, v);
+                Pack<T, V> a, b, d;
+                a.raw = load_elements(o, H, e0);
+                b.raw = load_elements(yr, H, e0);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    dot = fmaf(a.get(e), b.get(e), dot);
+                    d.set(e, wp * a.get(e));
+                }
+                store_whole(dr, H, e0, d.raw);
+            }
+            vecs = 0;
+        }
+    constexpr int U = 4, LANES = ANY ? kAnyLanes : 32;
+    for (int v0 = 0; v0 < vecs; v0 += LANES * U) {
         Pack<T, V> a[U], b[U];
+        const int first = ANY ? vector_any(dr, v0 + lane) : (v0 + lane) * V;   // element
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int v = v0 + u * 32;
-            if (v < vecs) {
-                a[u].load(o + static_cast<int64_t>(v) * V);
-                b[u].load(yr + static_cast<int64_t>(v) * V);
+            const int e0 = first + u * LANES * V;
+            if constexpr (ANY) {
+                a[u].raw = load_around(o, H, e0);
+                b[u].raw = load_around(yr, H, e0);
+            } else if (e0 < H) {
+                a[u].load(o + e0);
+                b[u].load(yr + e0);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int v = v0 + u * 32;
-            if (v >= vecs) break;
+            const int e0 = first + u * LANES * V;
+            if constexpr (ANY) {
+                if (v0 + u * LANES >= vecs) break;
+                const int n = lane < kAnyLanes ? H : 0;
+                a[u].raw = inside_row<T>(join_lanes(a[u].raw, o + e0), n, e0);
+                b[u].raw = inside_row<T>(join_lanes(b[u].raw, yr + e0), n, e0);
+            } else if (e0 >= H) {
+                break;
+            }
             Pack<T, V> d;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
@@ -499,7 +649,8 @@ __global__ void __launch_bounds__(256)
                 dot = fmaf(g, b[u].get(e), dot);
                 d.set(e, wp * g);
             }
-            d.store(dr + static_cast<int64_t>(v) * V);
+            if constexpr (!ANY) d.store(dr + e0);
+            else if (lane < kAnyLanes) store_whole(dr, H, e0, d.raw);
         }
     }
 #pragma unroll
@@ -507,13 +658,8 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) dw[p] = dot;
 }
 
-// Widest vector, in bytes, that divides the row, the row strides and the addresses.
-int vector_bytes(int64_t row_bytes, uintptr_t bits, int element) {
-    const uintptr_t all = bits | static_cast<uintptr_t>(row_bytes);
-    for (int b = 16; b > element; b >>= 1)
-        if (all % b == 0) return b;
-    return element;
-}
+// Whether rows of these addresses (bits: addresses and strides in bytes, or-ed) go in whole 16-byte vectors.
+bool whole_rows(int64_t row_bytes, uintptr_t bits) { return ((bits | static_cast<uintptr_t>(row_bytes)) & 15) == 0; }
 
 struct DispatchPlan {
     int chunk, nch;
@@ -548,12 +694,19 @@ cudaError_t launch_dispatch_bulk(DispatchArgs a, dim3 grid, cudaStream_t stream)
                       static_cast<size_t>(a.ring) + static_cast<size_t>(kCopyWarps) * a.slots * a.piece, stream, a);
 }
 
-template <class T, int V>
+template <class T, bool ANY>
 cudaError_t launch_combine(const void* y, int64_t ld, const int32_t* pos, const float* w, int64_t T_, int topk, int H,
                            int64_t num_rows, void* out, uint32_t* status, cudaStream_t stream) {
-    const int64_t n = T_ * (H / V);
-    return launch_pdl(combine_kernel<T, V>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
-                      static_cast<const T*>(y), ld, pos, w, T_, topk, H / V, num_rows, static_cast<T*>(out), status);
+    if constexpr (ANY) {
+        const int parts = (vectors_any<T>(H) + kAnyLanes - 1) / kAnyLanes;
+        return launch_pdl(combine_any_kernel<T>, dim3(static_cast<unsigned>((T_ * parts + 7) / 8)), dim3(256), 0, stream,
+                          static_cast<const T*>(y), ld, pos, w, static_cast<int>(T_), topk, H, parts,
+                          static_cast<int>(num_rows), static_cast<T*>(out), status);
+    }
+    const int vecs = H / (16 / static_cast<int>(sizeof(T)));
+    const int64_t n = T_ * vecs;
+    return launch_pdl(combine_kernel<T>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream,
+                      static_cast<const T*>(y), ld, pos, w, T_, topk, vecs, num_rows, static_cast<T*>(out), status);
 }
 
 // Whether the ring takes a combine: enough items to fill every group's ring; and its launch.
@@ -576,29 +729,22 @@ cudaError_t launch_combine_ring(const CombineArgs& a, int groups, cudaStream_t s
     return launch_pdl(combine_ring_kernel<T>, dim3(kPlanSms), dim3(groups * a.G), smem, stream, a);
 }
 
-template <class T, int V>
+template <class T, bool ANY>
 cudaError_t launch_combine_backward(const void* dout, int64_t ldo, const void* y, int64_t ldy, const int32_t* pos,
                                     const int32_t* pair_ids, const float* w, int64_t P, int topk, int H,
                                     int64_t num_rows, void* dy, float* dw, uint32_t* status, cudaStream_t stream) {
     const int64_t warps = P + (num_rows + 31) / 32;
-    return launch_pdl(combine_backward_kernel<T, V>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
+    return launch_pdl(combine_backward_kernel<T, ANY>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0,
                       stream, static_cast<const T*>(dout), ldo, static_cast<const T*>(y), ldy, pos, pair_ids, w, P,
-                      topk, H / V, num_rows, static_cast<T*>(dy), dw, status);
+                      topk, H, ANY ? vectors_any<T>(H) : H / (16 / static_cast<int>(sizeof(T))), num_rows,
+                      static_cast<T*>(dy), dw, status);
 }
 
-// F<T, V> for the type and the vector width
-#define MOE_BY_TYPE(F, dtype, vb, ...)                                             \
-    ((dtype) == MOE_DTYPE_FP32   ? ((vb) == 16  ? F<float, 4>(__VA_ARGS__)         \
-                                    : (vb) == 8 ? F<float, 2>(__VA_ARGS__)         \
-                                                : F<float, 1>(__VA_ARGS__))        \
-     : (dtype) == MOE_DTYPE_FP16 ? ((vb) == 16  ? F<__half, 8>(__VA_ARGS__)        \
-                                    : (vb) == 8 ? F<__half, 4>(__VA_ARGS__)        \
-                                    : (vb) == 4 ? F<__half, 2>(__VA_ARGS__)        \
-                                                : F<__half, 1>(__VA_ARGS__))       \
-                                 : ((vb) == 16  ? F<__nv_bfloat16, 8>(__VA_ARGS__) \
-                                    : (vb) == 8 ? F<__nv_bfloat16, 4>(__VA_ARGS__) \
-                                    : (vb) == 4 ? F<__nv_bfloat16, 2>(__VA_ARGS__) \
-                                                : F<__nv_bfloat16, 1>(__VA_ARGS__)))
+// F<T, ANY> for the type and the rows' alignment
+#define MOE_BY_TYPE(F, dtype, whole, ...)                                                                 \
+    ((dtype) == MOE_DTYPE_FP32   ? ((whole) ? F<float, false>(__VA_ARGS__) : F<float, true>(__VA_ARGS__)) \
+     : (dtype) == MOE_DTYPE_FP16 ? ((whole) ? F<__half, false>(__VA_ARGS__) : F<__half, true>(__VA_ARGS__)) \
+                                 : ((whole) ? F<__nv_bfloat16, false>(__VA_ARGS__) : F<__nv_bfloat16, true>(__VA_ARGS__)))
 
 int check_rows(int T, int topk, int H, int64_t ld, int64_t num_rows, int dtype) {
     if (T < 0 || topk < 1 || H < 1 || ld < H || num_rows < 0 || !known_dtype(dtype)) return MOE_ERR_INVALID_ARG;
@@ -619,8 +765,6 @@ cudaError_t combine_ring_init() {
 cudaError_t tokens_init_device() {
     const int bytes = static_cast<int>(dispatch_smem(MOE_MAX_EXPERTS));
     cudaError_t e = cudaFuncSetAttribute(dispatch_kernel<uint4, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(dispatch_kernel<uint2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(dispatch_kernel<uint32_t, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess)
@@ -668,7 +812,7 @@ int moe_dispatch(const void* x, int64_t ldx, int dtype, const int32_t* topk_ids,
     const DispatchPlan d = dispatch_plan(P, topk);
     const int es = static_cast<int>(dtype_bytes(dtype));
     const int64_t row_bytes = static_cast<int64_t>(H) * es;
-    const int vb = vector_bytes(row_bytes, address(x) | address(rows) | static_cast<uintptr_t>(ldx * es), es);
+    const bool whole = whole_rows(row_bytes, address(x) | address(rows) | static_cast<uintptr_t>(ldx * es));
     DispatchArgs a;
     a.x = static_cast<const char*>(x);
     a.ld_bytes = ldx * es;
@@ -679,7 +823,8 @@ int moe_dispatch(const void* x, int64_t ldx, int dtype, const int32_t* topk_ids,
     a.chunk = d.chunk;
     a.nch = d.nch;
     a.counts = d.direct ? nullptr : static_cast<const int32_t*>(workspace);
-    a.vecs = static_cast<int>(row_bytes / vb);
+    a.H = H;
+    a.vecs = whole ? static_cast<int>(row_bytes / 16) : es == 4 ? vectors_any<uint32_t>(H) : vectors_any<uint16_t>(H);
     // few tokens: several CTAs share a chunk, each with a slab of at least 128 vectors of the columns
     int slabs = kPlanSms / d.nch;
     if (slabs > (a.vecs + 127) / 128) slabs = (a.vecs + 127) / 128;
@@ -697,12 +842,9 @@ int moe_dispatch(const void* x, int64_t ldx, int dtype, const int32_t* topk_ids,
                        d.chunk, E, static_cast<int32_t*>(workspace));
     const dim3 grid(static_cast<unsigned>(d.nch), static_cast<unsigned>(slabs));
     if (e == cudaSuccess) {
-        switch (vb) {
-            case 16: e = slabs > 1 ? launch_dispatch<uint4>(a, grid, s) : launch_dispatch_bulk(a, grid, s); break;
-            case 8: e = launch_dispatch<uint2>(a, grid, s); break;
-            case 4: e = launch_dispatch<uint32_t>(a, grid, s); break;
-            default: e = launch_dispatch<uint16_t>(a, grid, s); break;
-        }
+        e = !whole      ? es == 4 ? launch_dispatch<uint32_t>(a, grid, s) : launch_dispatch<uint16_t>(a, grid, s)
+            : slabs > 1 ? launch_dispatch<uint4>(a, grid, s)
+                        : launch_dispatch_bulk(a, grid, s);
     }
     return cuda_status(e);
 }
@@ -717,9 +859,9 @@ int moe_combine(const void* y, int64_t ldy, int dtype, const int32_t* pos, const
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     const int es = static_cast<int>(dtype_bytes(dtype));
-    const int vb = vector_bytes(static_cast<int64_t>(H) * es,
-                                address(y) | address(out) | static_cast<uintptr_t>(ldy * es), es);
-    if (vb == 16) {
+    const bool whole = whole_rows(static_cast<int64_t>(H) * es,
+                                  address(y) | address(out) | static_cast<uintptr_t>(ldy * es));
+    if (whole) {
         CombineArgs a = {};
         int groups = 0;
         a.vecs = H * es / 16;
@@ -739,7 +881,7 @@ int moe_combine(const void* y, int64_t ldy, int dtype, const int32_t* pos, const
                                                          : launch_combine_ring<__nv_bfloat16>(a, groups, s));
         }
     }
-    return cuda_status(MOE_BY_TYPE(launch_combine, dtype, vb, y, ldy, pos, weights, T, topk, H, num_rows, out, status,
+    return cuda_status(MOE_BY_TYPE(launch_combine, dtype, whole, y, ldy, pos, weights, T, topk, H, num_rows, out, status,
                                    static_cast<cudaStream_t>(stream)));
 }
 
@@ -762,11 +904,10 @@ int moe_combine_backward(const void* dout, int64_t lddout, const void* y, int64_
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     const int es = static_cast<int>(dtype_bytes(dtype));
-    const int vb = vector_bytes(static_cast<int64_t>(H) * es,
-                                address(dout) | address(y) | address(dy) | static_cast<uintptr_t>(lddout * es) |
-                                    static_cast<uintptr_t>(ldy * es),
-                                es);
-    return cuda_status(MOE_BY_TYPE(launch_combine_backward, dtype, vb, dout, lddout, y, ldy, pos, pair_ids, weights, P,
+    const bool whole = whole_rows(static_cast<int64_t>(H) * es,
+                                  address(dout) | address(y) | address(dy) | static_cast<uintptr_t>(lddout * es) |
+                                      static_cast<uintptr_t>(ldy * es));
+    return cuda_status(MOE_BY_TYPE(launch_combine_backward, dtype, whole, dout, lddout, y, ldy, pos, pair_ids, weights, P,
                                    topk, H, num_rows, dy, dweights, status, static_cast<cudaStream_t>(stream)));
 }
 
