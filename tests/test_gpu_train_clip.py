@@ -131,3 +131,20 @@ def test_large_tensor_repeats_and_graph():
     check(n, torch.tensor(norm64([t, small], 2), dtype=torch.float64), roundings=NORM, name="norm of the replay")
     again = moe.moe_clip_grads([t, small], 5.0, out=outs[1])
     assert torch.equal(n, again) and torch.equal(outs[0][0], outs[1][0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("src,dst", [(0, 1), (1, 0), (3, 2), (5, 5), (7, 4)])
+def test_results_elsewhere_between_boundaries(src, dst, dtype):
+    """Gradients and results at addresses of their own; nothing beside the results is written."""
+    g = gen(src * 8 + dst)
+    sizes = [1, 2, 7, 8, 9, 31, 1023, 4093, 4096, 4099, 8200, 70001]
+    grads = [offset_copy(rand(g, n, dtype=dtype), src) for n in sizes]
+    around = [torch.full((n + dst + 9,), 5.0, dtype=dtype, device="cuda") for n in sizes]
+    out = [b[dst:dst + n] for b, n in zip(around, sizes)]
+    total = norm64(grads, 2)
+    got = moe.moe_clip_grads(grads, total / 2, out=out)
+    check(got, torch.tensor(total, dtype=torch.float64), roundings=NORM, name="norm")
+    for t, o, b, n in zip(grads, out, around, sizes):
+        check(o, t.double() * (total / 2 / (total + 1e-6)), roundings=NORM + 4, name="clipped")
+        assert (b[:dst] == 5).all() and (b[dst + n:] == 5).all()

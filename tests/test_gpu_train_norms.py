@@ -230,3 +230,30 @@ def test_repeats_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, step()))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("T,H", [(40, 1), (40, 7), (60, 249), (60, 250), (40, 1753), (200, 4811), (30, 9001)])
+def test_rows_between_sixteen_byte_boundaries(T, H, dtype):
+    """Rows that share 16 bytes with their neighbours."""
+    test_pre_norm_and_gradient(T, H, dtype, "same")
+    for kind, sigmoid in (("token", False), ("channel", True), ("full", False), ("full", True)):
+        test_post_norm_and_gradient(T, H, dtype, kind, sigmoid)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+def test_neighbours_that_are_not_finite(dtype):
+    g = gen(5)
+    T, H = 40, 251
+    x, w, d = rand(g, T, H, dtype=dtype), rand(g, H), rand(g, T, H, dtype=dtype)
+    x[20] = float("nan")
+    x[22, 3] = float("inf")
+    h, rstd = moe.moe_pre_norm(x, w, eps=1e-5)
+    want, _ = norm64(x, w, 0, 1e-5)
+    keep = [t for t in range(T) if t not in (20, 22)]
+    check(h[keep], want[keep], roundings=ROW, name="h")
+    assert h[20].isnan().all()
+    p = moe.moe_post_norm(x, d, w, eps=1e-5, next_weight=w)
+    assert torch.isfinite(p.next_h[keep]).all() and torch.isfinite(p.out[keep]).all()
+    dx, _ = moe.moe_pre_norm_backward(d, x, w, rstd)
+    assert torch.isfinite(dx[keep]).all() and dx[20].isnan().all()

@@ -309,3 +309,30 @@ def test_rows_past_two_to_the_31_elements():
     del dx
     dy, dw = moe.moe_combine_backward(x, d.rows, d.pos, d.pair_ids)
     assert torch.equal(dy[at], want[:, None].expand(5, H))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("T,H", [(60, 1), (60, 7), (60, 17), (40, 249), (30, 250), (24, 2375), (18, 4097)])
+def test_rows_between_sixteen_byte_boundaries(T, H, dtype):
+    """Neighbours of a row share 16 bytes with it: what they hold (NaN here, or the gap between rows) stays theirs."""
+    g = gen(T * H)
+    k, E = 3, 5
+    ids = make_ids(g, T, k, E, 0.1).cuda()
+    x, y, dout, w = rand(g, T, H, dtype=dtype), rand(g, T * k, H, dtype=dtype), rand(g, T, H, dtype=dtype), rand(g, T, k)
+    x[T // 2] = dout[T // 2] = float("nan")
+    for lay in (lambda t: t, lambda t: offset_copy(t, 3), lambda t: strided_copy(t, 3, 1)):
+        d = moe.moe_dispatch(lay(x), ids, E)
+        offsets, pair_ids, pos = sort_ref(ids.cpu(), E)
+        live = pair_ids[:int(offsets[-1])] // k
+        assert torch.equal(d.rows[:len(live)].cpu().isnan(), x.cpu()[live].isnan())
+        assert torch.equal(d.rows[:len(live)].cpu().nan_to_num(7.0), x.cpu()[live].nan_to_num(7.0))
+        assert not d.rows[len(live):].any()
+        bad = y.clone()
+        r = int(torch.nonzero(pos[T // 2] >= 0)[0])
+        bad[pos[T // 2, r]] = float("nan")
+        out, size = combine_ref(bad, d.pos, w)
+        check(moe.moe_combine(lay(bad), d.pos, w), out, size, k + 1, "out")
+        dy, dw = moe.moe_combine_backward(lay(dout), lay(bad), d.pos, d.pair_ids, w)
+        want, (ww, size) = combine_backward_ref(dout, bad, d.pos, w)
+        check(dy, want, name="dy")
+        check(dw, ww, size, H, "dweights")
