@@ -71,22 +71,23 @@ struct Chunk {
     int64_t e0;
     int n, head, bulk;
 };
-__host__ __device__ __forceinline__ int lead_elements(const void* p, int es) {
-    return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / es);
+// (sh: elements of 1 << sh bytes; divisions by the size made the chunks' arithmetic 40 us of 620 at 1.2 GB)
+__host__ __device__ __forceinline__ int lead_elements(const void* p, int sh) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15) >> sh;
 }
 template <int N>
 __device__ __forceinline__ Chunk chunk_at(const ClipTable<N>& t, int64_t c) {
     Chunk u;
     u.k = tensor_of(t, c);
-    const int es = t.dtype[u.k] == MOE_DTYPE_FP32 ? 4 : 2, per = kChunkBytes / es;
-    const int lead = lead_elements(t.src[u.k], es), V = 16 / es;
+    const int sh = t.dtype[u.k] == MOE_DTYPE_FP32 ? 2 : 1, per = kChunkBytes >> sh, V = 16 >> sh;
+    const int lead = lead_elements(t.src[u.k], sh);
     const bool first = c == t.chunk0[u.k];
     u.e0 = first ? 0 : (c - t.chunk0[u.k]) * per - lead;
     const int room = first ? per - lead : per;
     const int64_t left = t.numel[u.k] - u.e0;
     u.n = left < room ? static_cast<int>(left) : room;
     u.head = first && lead ? (V - lead < u.n ? V - lead : u.n) : 0;
-    u.bulk = (u.n - u.head) * es / 16 * 16;
+    u.bulk = ((u.n - u.head) << sh) & ~15;
     return u;
 }
 
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kClipThreads, 1)
     if (threadIdx.x == 0) partial[blockIdx.x] = acc;
 }
 
-template <class T, class R>
+// ANY: the result's 16-byte boundaries lie elsewhere than the gradient's.
+template <class T, bool ANY, class R>
 __device__ __forceinline__ void scale_share(R& ring, const T* p, T* q, const Chunk& u, float scale) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     const int nv = u.bulk / 16, lane = threadIdx.x & 31;
@@ -259,17 +261,11 @@ __device__ __forceinline__ void scale_share(R& ring, const T* p, T* q, const Chu
         for (int e = 0; e < V; ++e) o.set(e, x.get(e) * scale);
         return o;
     };
-    if ((reinterpret_cast<uintptr_t>(qb) & 15) == 0) {
-        for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
-            ring.template piece<T, false>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
-                scaled(x).store(qb + (v0 + v) * V);
-            });
-    } else {   // the result's vectors lie elsewhere than the gradient's
-        for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
-            ring.template piece<T, true>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
-                store_any(qb, nv * V, v0 + v, scaled(x).raw);
-            });
-    }
+    for (int v0 = 0; v0 < nv; v0 += kPiece / 16)
+        ring.template piece<T, ANY>(nv - v0 < kPiece / 16 ? nv - v0 : kPiece / 16, [&](int v, const Pack<T, V>& x) {
+            if constexpr (ANY) store_any(qb, nv * V, v0 + v, scaled(x).raw);
+            else scaled(x).store(qb + (v0 + v) * V);
+        });
     if (lane < u.head) q[lane] = from_f32<T>(to_f32(p[lane]) * scale);
     const int tail = u.head + nv * V + lane;
     if (tail < u.n) q[tail] = from_f32<T>(to_f32(p[tail]) * scale);
@@ -278,7 +274,7 @@ __device__ __forceinline__ void scale_share(R& ring, const T* p, T* q, const Chu
 // Every CTA joins the partial results (np of them) and scales its chunks, the last first: they are
 // the ones the norm read last, so they are still in L2.  A scale of one where every gradient stays in
 // place leaves them alone.
-template <int N>
+template <int N, bool ANY>
 __global__ void __launch_bounds__(kClipThreads, 1)
     grad_scale_kernel(const __grid_constant__ ClipTable<N> t, int inf, const double* __restrict__ partial, int np,
                       float max_norm, float eps, int write_total, int all_in_place, float* __restrict__ total,
@@ -306,11 +302,11 @@ __global__ void __launch_bounds__(kClipThreads, 1)
     for (int64_t c = static_cast<int64_t>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; c < ring.chunks; c += ring.stride) {
         const Chunk u = chunk_at(t, ring.index(c));
         if (t.dtype[u.k] == MOE_DTYPE_FP32)
-            scale_share(ring, static_cast<const float*>(t.src[u.k]) + u.e0, static_cast<float*>(t.dst[u.k]) + u.e0, u, scale);
+            scale_share<float, ANY>(ring, static_cast<const float*>(t.src[u.k]) + u.e0, static_cast<float*>(t.dst[u.k]) + u.e0, u, scale);
         else if (t.dtype[u.k] == MOE_DTYPE_FP16)
-            scale_share(ring, static_cast<const __half*>(t.src[u.k]) + u.e0, static_cast<__half*>(t.dst[u.k]) + u.e0, u, scale);
+            scale_share<__half, ANY>(ring, static_cast<const __half*>(t.src[u.k]) + u.e0, static_cast<__half*>(t.dst[u.k]) + u.e0, u, scale);
         else
-            scale_share(ring, static_cast<const __nv_bfloat16*>(t.src[u.k]) + u.e0,
+            scale_share<__nv_bfloat16, ANY>(ring, static_cast<const __nv_bfloat16*>(t.src[u.k]) + u.e0,
                         static_cast<__nv_bfloat16*>(t.dst[u.k]) + u.e0, u, scale);
     }
     ring.finish();
@@ -318,9 +314,9 @@ __global__ void __launch_bounds__(kClipThreads, 1)
 #undef MOE_CLIP_PROLOGUE
 
 int64_t chunks_of(const void* src, int64_t numel, int dtype) {
-    const int es = static_cast<int>(dtype_bytes(dtype));
-    const int64_t per = kChunkBytes / es;
-    return numel == 0 ? 0 : (lead_elements(src, es) + numel + per - 1) / per;
+    const int sh = dtype == MOE_DTYPE_FP32 ? 2 : 1;
+    const int64_t per = kChunkBytes >> sh;
+    return numel == 0 ? 0 : (lead_elements(src, sh) + numel + per - 1) / per;
 }
 
 struct ClipCall {
@@ -333,6 +329,7 @@ struct ClipCall {
     float* total;
     double* partial;
     int all_in_place;
+    bool apart;      // some result's 16-byte boundaries lie elsewhere than its gradient's
     uint32_t* status;
     cudaStream_t stream;
 };
@@ -372,7 +369,7 @@ cudaError_t clip_launches(const ClipCall& c) {
     }
     for (int b = 0; b < batches && e == cudaSuccess; ++b) {
         if (batches > 1) fill_table(&t, c, b * N, c.n < (b + 1) * N ? c.n : (b + 1) * N);
-        e = launch_pdl(grad_scale_kernel<N>, dim3(clip_grid(t.chunk0[t.n])), dim3(kClipThreads), kRingBytes, c.stream, t,
+        e = launch_pdl(c.apart ? grad_scale_kernel<N, true> : grad_scale_kernel<N, false>, dim3(clip_grid(t.chunk0[t.n])), dim3(kClipThreads), kRingBytes, c.stream, t,
                        c.inf, static_cast<const double*>(c.partial), np, c.max_norm, c.eps, b == 0 ? 1 : 0, c.all_in_place,
                        c.total, c.status);
     }
@@ -381,10 +378,12 @@ cudaError_t clip_launches(const ClipCall& c) {
 
 template <int N>
 cudaError_t clip_init() {
-    const cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    return e == cudaSuccess
-               ? cudaFuncSetAttribute(grad_scale_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)
-               : e;
+    cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(grad_scale_kernel<N, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(grad_scale_kernel<N, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    return e;
 }
 
 }  // namespace
@@ -415,12 +414,14 @@ int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* nu
     if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || !total_norm) return MOE_ERR_INVALID_ARG;
     if (n > 0 && (!grads || !out || !numel || !dtype)) return MOE_ERR_INVALID_ARG;
     int all_in_place = 1;
+    bool apart = false;
     for (int i = 0; i < n; ++i) {
         if (numel[i] < 0 || !known_dtype(dtype[i])) return MOE_ERR_INVALID_ARG;
         if (numel[i] > 0 && (!grads[i] || !out[i])) return MOE_ERR_INVALID_ARG;
         if (!on_element(address(grads[i]) | address(out[i]), dtype_bytes(dtype[i]))) return MOE_ERR_INVALID_ARG;
         if (numel[i] > (int64_t(1) << 50)) return MOE_ERR_UNSUPPORTED_SHAPE;
         if (numel[i] > 0 && grads[i] != out[i]) all_in_place = 0;
+        if (numel[i] > 0 && ((address(grads[i]) ^ address(out[i])) & 15)) apart = true;
     }
     if (workspace_bytes < moe_clip_grads_workspace_size(n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace || !on_element(address(workspace), 8)) return MOE_ERR_INVALID_ARG;
@@ -428,7 +429,7 @@ int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* nu
     const int rc = device_status_word(&status);
     if (rc != MOE_OK) return rc;
     const ClipCall c = {grads, out, numel, dtype, n, norm_kind == MOE_NORM_INF ? 1 : 0, max_norm, eps, total_norm,
-                        static_cast<double*>(workspace), all_in_place, status, static_cast<cudaStream_t>(stream)};
+                        static_cast<double*>(workspace), all_in_place, apart, status, static_cast<cudaStream_t>(stream)};
     return cuda_status(n <= 32 ? clip_launches<32>(c) : n <= 128 ? clip_launches<128>(c)
                                                                  : clip_launches<kMostTensors>(c));
 }

@@ -118,7 +118,7 @@ struct Weights {
 
 template <class T, int V, int NV, int NIN, bool ANY>
 struct RowInRegs {
-    static constexpr bool kWide = false;
+    static constexpr bool kWide = false, kAny = ANY;
     Weights<V> w[NV];
     Pack<T, V> r[NIN][NV];
     const T* src[NIN];
@@ -194,7 +194,7 @@ struct RowInRegs {
     __device__ __forceinline__ bool skip(int i) const { return !ANY && tid + i * G >= nvec; }
     __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const {
         if constexpr (ANY) store_any(row, H, vec(i), o.raw);
-        else o.store(row + vec(i) * V);
+        else o.store(row + static_cast<int64_t>(vec(i)) * V);
     }
     __device__ __forceinline__ void next(const Group&) {}
     __device__ __forceinline__ void finish() {}
@@ -206,7 +206,7 @@ struct RowAny : RowInRegs<T, V, NV, NIN, true> {};
 
 template <class T, int V, int NV, int NIN>
 struct RowRing {
-    static constexpr bool kWide = true;
+    static constexpr bool kWide = true, kAny = false;
     static constexpr int Q = V / 4;   // the weights of a vector: Q planes of float4, so that a warp reads 512 bytes in a row
     float4* wsm;                      // [Q][nvec], the CTA's
     const T* src[NIN];
@@ -302,7 +302,7 @@ struct RowRing {
     }
     __device__ __forceinline__ int vec(int i) const { return tid + i * G; }
     __device__ __forceinline__ bool skip(int i) const { return vec(i) >= nvec; }
-    __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const { o.store(row + vec(i) * V); }
+    __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const { o.store(row + static_cast<int64_t>(vec(i)) * V); }
     // the group is done with the row: its slot takes the next one
     __device__ __forceinline__ void next(const Group& g) {
         g.sync();
@@ -395,8 +395,11 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
 #pragma unroll
         for (int i = 0; i < NV * NP; ++i) {
             const int c = in.vec(i / NP) * V + (i % NP) * 2;
-            w2[i].x = c < a.H ? weight_at(a.w2, a.w_dtype, c) + a.w_offset : 0.0f;
-            w2[i].y = c + 1 < a.H ? weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset : 0.0f;
+            w2[i] = both(0.0f);
+            if (c < a.H) {
+                w2[i].x = weight_at(a.w2, a.w_dtype, c) + a.w_offset;
+                if (!in.kAny || c + 1 < a.H) w2[i].y = weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset;
+            }
         }
     }
     for (int64_t t = t0; t < a.T; t += step) {
@@ -465,9 +468,10 @@ __device__ __forceinline__ void write_partial(const float2 (&acc)[NV * (V / 2)],
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c0 = in.vec(i) * V;
+                if (c0 >= H) continue;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    if (c0 + e >= H) break;
+                    if (in.kAny && c0 + e >= H) break;
                     const float2 p = acc[i * NP + e / 2];
                     const float u = (e & 1 ? p.y : p.x) + (k > 0 ? sum_s[c0 + e] : 0.0f);
                     if (k + 1 < R) sum_s[c0 + e] = u;
@@ -743,13 +747,14 @@ cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_
 //     threads (more threads on each row)
 //   else wide rows: the ring, 32 elements per thread (registers where the weights and two rows do not
 //     fit a CTA's shared memory)
-//   rows at any address: registers, 16 elements per thread where the row then fits, else 32
+//   rows at any address: registers, 16 elements per thread up to 4096 columns, else 32 (8000 rows of 4811: 212
+//     and 164 us; of 1569: 57 and 67)
 template <class T>
 cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, int sms, cudaStream_t stream,
                              int* ctas) {
     constexpr int W = 16 / static_cast<int>(sizeof(T));
     if (!wide) {
-        if (a.H <= 16 * kNormThreads)
+        if (a.H <= 8 * kNormThreads || (a.T < 2 * sms && a.H <= 16 * kNormThreads))
             return launch_norm_nv<T, W, 16 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
         return launch_norm_nv<T, W, 32 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
     }
