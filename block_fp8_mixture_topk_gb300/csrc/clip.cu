@@ -11,6 +11,11 @@
 // depend on the schedule.  Squares are summed in fp32 within a lane's share of a chunk and in fp64
 // beyond it; a share whose largest magnitude lies outside 1e-18 .. 1e18, where fp32 squares
 // overflow or vanish, is summed again in fp64.
+//
+// Measured: 1.21 GB of bf16 gradients into other tensors 581 us (norm 178 us = 6.8 TB/s; scaling 377 us = 6.3 TB/s;
+// the second read cannot be saved beyond what L2 keeps: 537 us at copy bandwidth); one small layer's 8
+// tensors 9.5 us on the device, both launches' latency.  With vectors through registers the large case took
+// 662 us; more CTAs per SM or more vectors per thread did not change that.
 #include <math.h>
 
 #include "train.cuh"

@@ -14,7 +14,8 @@
 // outputs: one thread of CTA 0 issues tcgen05.mma.cta_group::2 (256 x N x 16), which reads both CTAs'
 // operands (128 of the 256, half of the N each) and leaves each CTA its 128 x N in its own tensor
 // memory (two accumulators).  A 64-wide K block then brings 32 KB into an SM for 512 cycles of its
-// tensor pipe.  A TMA warp per CTA fills a ring of six 64-wide stages, eight warps per CTA drain an accumulator while the next one fills.
+// tensor pipe.  A TMA warp per CTA fills a ring of six 64-wide stages, eight warps per CTA drain an
+// accumulator while the next one fills.
 //
 // Products and rows' gradient: the 256 run along the output columns (the weights) and N along the
 // rows, so that the tile in which an expert ends costs its rows rounded up to 32, not to 256 (a
@@ -29,6 +30,13 @@
 // ends inside an expert computes rows of the next and does not store them; in the weights' gradient
 // the stage in which an expert ends is finished by a warp of each CTA that zeroes the rows past the
 // end, for both operands, so that nothing a neighbour holds (a NaN, say) reaches the sum.
+//
+// Measured: 131072 rows of bf16 over 128 skewed experts, K 2048, N 1536 with SiLU: 520 us at full clocks (1586
+// TFLOP/s, tensor pipe 79% busy), 600 us in a long loop, where the power limit lowers them (cuBLAS's dense
+// product falls from 2030 to 1720 TFLOP/s the same way).  Bound by the operands' way from L2 into the SMs:
+// the loads alone take 465 us (15.5 TB/s), without the epilogue 475 us.  Weights' gradient of the
+// same rows 562 us (637 us in a loop).  Decode, 64 rows over 128 experts: 54 us for 321 MB (0.88 of a copy); rows'
+// gradient of 1024 rows, 8 experts of 14336 x 4096: 166 us (0.95 of a copy).
 #include <type_traits>
 
 #include "train.cuh"

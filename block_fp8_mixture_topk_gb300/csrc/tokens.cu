@@ -13,6 +13,13 @@
 // times without touching a register, the sums read a slab of columns of a token's topk rows at a time.
 // Sums are fp32, in j order, rounded once to the rows' type; there are no atomics on values, so
 // results do not depend on the schedule.
+//
+// Measured (bf16): dispatch and combine of 4096 tokens x 7168, top-8 of 256, 185 us for 1.06 GB (5.7 TB/s,
+// 0.85 of a copy); the dispatch takes half, about 10 us of it the sort before its first store.  Both
+// gradients for 16384 x 2048, top-8 of 128, skewed: 292 us for 1.75 GB (0.88 of a copy).  Eight tokens:
+// 6.2 us on the device for both.  With vectors through registers the first shape took 211 us.  Rows at any
+// address are bound by instructions (joining the vectors): 8000 x 4070 fp16, top-2 of 64, 108 us, 1.9 times
+// the bytes' time.
 #include "train.cuh"
 
 namespace mfp8 {

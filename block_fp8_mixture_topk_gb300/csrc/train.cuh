@@ -20,10 +20,6 @@ struct RawOf<16> {
     using type = uint4;
 };
 template <>
-struct RawOf<8> {
-    using type = uint2;
-};
-template <>
 struct RawOf<4> {
     using type = uint32_t;
 };
@@ -50,8 +46,7 @@ __device__ __forceinline__ __half from_f32<__half>(float v) {
     return __float2half_rn(v);
 }
 
-// V elements of type T in one register vector (V * sizeof(T) is 2, 4, 8 or 16 bytes; addresses
-// aligned to it).
+// V elements of type T in one register vector of 16 bytes (addresses aligned to it).
 template <class T, int V>
 struct Pack {
     using Raw = typename RawOf<static_cast<int>(sizeof(T)) * V>::type;
@@ -65,14 +60,11 @@ struct Pack {
     __device__ __forceinline__ void zero() { raw = Raw{}; }
     __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
     __device__ __forceinline__ void set(int i, float v) { e[i] = from_f32<T>(v); }
-    // elements 2i and 2i + 1 (V == 1: the element and zero), for the packed fp32 arithmetic
-    static constexpr int kPairs = (V + 1) / 2;
-    __device__ __forceinline__ float2 pair(int i) const {
-        return make_float2(to_f32(e[2 * i]), V > 1 ? to_f32(e[V > 1 ? 2 * i + 1 : 0]) : 0.0f);
-    }
+    // elements 2i and 2i + 1, for the packed fp32 arithmetic
+    __device__ __forceinline__ float2 pair(int i) const { return make_float2(to_f32(e[2 * i]), to_f32(e[2 * i + 1])); }
     __device__ __forceinline__ void set_pair(int i, float2 v) {
         e[2 * i] = from_f32<T>(v.x);
-        if (V > 1) e[V > 1 ? 2 * i + 1 : 0] = from_f32<T>(v.y);
+        e[2 * i + 1] = from_f32<T>(v.y);
     }
 };
 
