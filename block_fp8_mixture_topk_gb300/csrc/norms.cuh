@@ -126,7 +126,7 @@ struct Weights {
 
 template <class T, int V, int NV, int NIN, bool ANY>
 struct RowInRegs {
-    static constexpr bool kWide = false, kAny = ANY;
+    static constexpr bool kWide = false, kAny = ANY, kShift = false;
     Weights<V> w[NV];
     Pack<T, V> r[NIN][NV];
     const T* src[NIN];
@@ -197,6 +197,7 @@ struct RowInRegs {
             }
     }
     // this thread's i-th vector of a row; at any address the vectors of a warp are neighbours
+    __device__ __forceinline__ int column(int i) const { return vec(i) * V; }
     __device__ __forceinline__ int vec(int i) const { return ANY ? ((tid >> 5) * NV + i) * 32 + (tid & 31) : tid + i * G; }
     __device__ __forceinline__ Pack<T, V> get(int n, int i) const { return r[n][i]; }
     __device__ __forceinline__ bool skip(int i) const { return !ANY && tid + i * G >= nvec; }
@@ -212,9 +213,23 @@ struct RowRegs : RowInRegs<T, V, NV, NIN, false> {};
 template <class T, int V, int NV, int NIN>
 struct RowAny : RowInRegs<T, V, NV, NIN, true> {};
 
-template <class T, int V, int NV, int NIN>
-struct RowRing {
-    static constexpr bool kWide = true, kAny = false;
+// Bytes of a row in the ring, and vectors that a row touches at most; SHIFT: it may start inside a vector.
+template <class T, bool SHIFT>
+__host__ __device__ __forceinline__ int ring_row_bytes(int H) {
+    const int bytes = H * static_cast<int>(sizeof(T));
+    return SHIFT ? (bytes + 15) / 16 * 16 + 16 : bytes;
+}
+template <bool SHIFT>
+__host__ __device__ __forceinline__ int ring_vectors(int H, int V) {
+    return SHIFT ? (H + 2 * V - 2) / V : H / V;
+}
+// SHIFT: rows of any width whose matrices all lie alike between two 16-byte boundaries.  A row starts there
+// by its number modulo 8, and so does every row of a CTA, whose rows are a multiple of 8 apart: its
+// vectors are the memory's, its weights and sums are kept by those, and only a row's first and last vector
+// hold columns that are not the row's.
+template <class T, int V, int NV, int NIN, bool SHIFT>
+struct RowInRing {
+    static constexpr bool kWide = true, kAny = SHIFT, kShift = SHIFT;
     static constexpr int Q = V / 4;   // the weights of a vector: Q planes of float4, so that a warp reads 512 bytes in a row
     float4* wsm;                      // [Q][nvec], the CTA's
     const T* src[NIN];
@@ -225,28 +240,60 @@ struct RowRing {
     uint32_t* status;
     int64_t t_load, t_end, stride;
     uint32_t row_bytes;
-    int depth, slot, load_slot, G, tid, nvec;
+    int depth, slot, load_slot, G, tid, H, nvec;
+    int lead;                   // SHIFT: elements of a row's start past a 16-byte boundary
     uint32_t phase, issued;
 
     __device__ __forceinline__ void issue() {
         if (t_load < t_end) {
             if (tid == 0) {
                 const uint32_t b = smem_addr(bar + load_slot);
-                mbar_arrive_expect_tx(b, NIN * row_bytes);
+                if constexpr (SHIFT) {
+                    issue_shifted(b);
+                } else {
+                    mbar_arrive_expect_tx(b, NIN * row_bytes);
 #pragma unroll
-                for (int n = 0; n < NIN; ++n)
-                    bulk_load(smem_addr(ring + (load_slot * NIN + n) * row_bytes), src[n] + t_load * ld[n], row_bytes, b);
+                    for (int n = 0; n < NIN; ++n)
+                        bulk_load(smem_addr(ring + (load_slot * NIN + n) * row_bytes), src[n] + t_load * ld[n], row_bytes, b);
+                }
             }
             ++issued;
             t_load += stride;
             if (++load_slot == depth) load_slot = 0;
         }
     }
+    // Row t_load, by one thread: whole aligned vectors, which reach into the neighbouring rows; of the
+    // matrix's first and last rows only what is in them, the elements at their ends one by one.
+    __device__ __forceinline__ void issue_shifted(uint32_t b) {
+        const bool inner = inner_row(t_load, t_end);
+        const int before = lead * static_cast<int>(sizeof(T)), after = before + H * static_cast<int>(sizeof(T));
+        const int from = inner || lead == 0 ? 0 : 16, to = inner ? (after + 15) & ~15 : after & ~15;
+        const int bytes = to > from ? to - from : 0;
+#pragma unroll
+        for (int n = 0; n < NIN; ++n) {
+            uint8_t* s = ring + (load_slot * NIN + n) * row_bytes;
+            const uint8_t* g = reinterpret_cast<const uint8_t*>(src[n] + t_load * ld[n]) - before;
+            if (!inner)
+#pragma unroll 1
+                for (int a = before; a < after; a += sizeof(T)) {
+                    if (bytes && a == from) a = to;
+                    if (a < after) *reinterpret_cast<T*>(s + a) = *reinterpret_cast<const T*>(g + a);
+                }
+        }
+        if (!inner) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // later copies land in the same bytes
+        mbar_arrive_expect_tx(b, NIN * bytes);
+        if (bytes)
+#pragma unroll
+            for (int n = 0; n < NIN; ++n)
+                bulk_load(smem_addr(ring + (load_slot * NIN + n) * row_bytes + from),
+                          reinterpret_cast<const uint8_t*>(src[n] + t_load * ld[n]) - before + from, bytes, b);
+    }
     template <class F>
     __device__ __forceinline__ void weights(F f) {
         for (int q = threadIdx.x; q < nvec * Q; q += blockDim.x) {
-            const int v = q / Q, p = q - v * Q, c = v * V + p * 4;
-            wsm[p * nvec + v] = make_float4(f(c), f(c + 1), f(c + 2), f(c + 3));
+            const int v = q / Q, p = q - v * Q, c = v * V + p * 4 - lead;
+            const auto at = [&](int k) { return !SHIFT || (c + k >= 0 && c + k < H) ? f(c + k) : 0.0f; };
+            wsm[p * nvec + v] = make_float4(at(0), at(1), at(2), at(3));
         }
     }
     __device__ __forceinline__ void weights_done() { __syncthreads(); }
@@ -261,17 +308,19 @@ struct RowRing {
         }
         return r;
     }
-    // smem: [H] weights, [R][depth][NIN][row_bytes], then the barriers and the abort flag
+    // smem: [vectors * V] weights, [R][depth][NIN][row_bytes], then the barriers and the abort flag
     __device__ __forceinline__ void start(const NormArgs& a, const Group& g, int64_t t0, int64_t step, int R,
                                           uint8_t* smem) {
         G = a.G;
         tid = g.tid;
-        nvec = a.H / V;
+        H = a.H;
+        nvec = ring_vectors<SHIFT>(a.H, V);
+        lead = SHIFT ? static_cast<int>((reinterpret_cast<uintptr_t>(src[0] + t0 * ld[0]) & 15) / sizeof(T)) : 0;
         depth = a.depth;
         status = a.status;
-        row_bytes = static_cast<uint32_t>(a.H) * sizeof(T);
+        row_bytes = static_cast<uint32_t>(ring_row_bytes<T, SHIFT>(a.H));
         wsm = reinterpret_cast<float4*>(smem);
-        smem += static_cast<size_t>(a.H) * 4;
+        smem += static_cast<size_t>(nvec) * V * 4;
         ring = smem + static_cast<size_t>(g.id) * depth * NIN * row_bytes;
         uint64_t* bars = reinterpret_cast<uint64_t*>(smem + static_cast<size_t>(R) * depth * NIN * row_bytes);
         bar = bars + g.id * depth;
@@ -306,11 +355,16 @@ struct RowRing {
         if (v < nvec)
             p.raw = *reinterpret_cast<const typename Pack<T, V>::Raw*>(ring + (slot * NIN + n) * row_bytes + v * 16);
         else p.zero();
+        if constexpr (SHIFT) p.raw = inside_row<T>(p.raw, H, v * V - lead);
         return p;
     }
     __device__ __forceinline__ int vec(int i) const { return tid + i * G; }
+    __device__ __forceinline__ int column(int i) const { return vec(i) * V - (SHIFT ? lead : 0); }
     __device__ __forceinline__ bool skip(int i) const { return vec(i) >= nvec; }
-    __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const { o.store(row + static_cast<int64_t>(vec(i)) * V); }
+    __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const {
+        if constexpr (SHIFT) store_whole(row, H, column(i), o.raw);
+        else o.store(row + static_cast<int64_t>(vec(i)) * V);
+    }
     // the group is done with the row: its slot takes the next one
     __device__ __forceinline__ void next(const Group& g) {
         g.sync();
@@ -324,6 +378,11 @@ struct RowRing {
             }
     }
 };
+
+template <class T, int V, int NV, int NIN>
+struct RowRing : RowInRing<T, V, NV, NIN, false> {};
+template <class T, int V, int NV, int NIN>
+struct RowShift : RowInRing<T, V, NV, NIN, true> {};
 
 // The weight of column c, times the channel gate.
 template <class T, int GATE>
@@ -340,7 +399,9 @@ __device__ __forceinline__ float gated_weight(const NormArgs& a, int c) {
     Group g = make_group(red, a.G);                                                   \
     constexpr int NP = V / 2;                                                   \
     const int R = blockDim.x / a.G;                                   \
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * R + g.id, step = static_cast<int64_t>(gridDim.x) * R; \
+    const int64_t step = static_cast<int64_t>(gridDim.x) * R;                         \
+    const int64_t t0 = Rows<T, V, NV, 1>::kShift ? static_cast<int64_t>(g.id) * gridDim.x + blockIdx.x \
+                                                 : static_cast<int64_t>(blockIdx.x) * R + g.id; \
     grid_dependency_wait();
 
 // h = x * rstd * w
@@ -402,11 +463,11 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
     if constexpr (NEXT) {
 #pragma unroll
         for (int i = 0; i < NV * NP; ++i) {
-            const int c = in.vec(i / NP) * V + (i % NP) * 2;
+            const int c = in.column(i / NP) + (i % NP) * 2;
             w2[i] = both(0.0f);
             if (c < a.H) {
-                w2[i].x = weight_at(a.w2, a.w_dtype, c) + a.w_offset;
-                if (!in.kAny || c + 1 < a.H) w2[i].y = weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset;
+                if (!in.kShift || c >= 0) w2[i].x = weight_at(a.w2, a.w_dtype, c) + a.w_offset;
+                if (!in.kAny || (c + 1 >= 0 && c + 1 < a.H)) w2[i].y = weight_at(a.w2, a.w_dtype, c + 1) + a.w_offset;
             }
         }
     }
@@ -475,11 +536,11 @@ __device__ __forceinline__ void write_partial(const float2 (&acc)[NV * (V / 2)],
         if (g.id == k) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c0 = in.vec(i) * V;
+                const int c0 = in.column(i);
                 if (c0 >= H) continue;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    if (in.kAny && c0 + e >= H) break;
+                    if (in.kAny && (c0 + e < 0 || c0 + e >= H)) continue;
                     const float2 p = acc[i * NP + e / 2];
                     const float u = (e & 1 ? p.y : p.x) + (k > 0 ? sum_s[c0 + e] : 0.0f);
                     if (k + 1 < R) sum_s[c0 + e] = u;
@@ -658,6 +719,9 @@ inline int norm_group(int nvec, int NV) {
 constexpr int kRingBytes = 222 * 1024;   // of a CTA's weights and rings (one CTA per SM)
 constexpr int kRingMostDepth = 4;
 
+// At most: vectors are 8 or 4 elements.
+inline int ring_weight_bytes(int H, bool shift) { return shift ? ring_vectors<true>(H, 8) * 32 : H * 4; }
+
 // What an instance remembers per device: that its shared-memory limit is set, and the CTAs per SM by
 // the warps of a CTA.
 struct NormInstance {
@@ -666,10 +730,11 @@ struct NormInstance {
 };
 
 // One kernel instance, with CTAs of as many row groups as `threads` holds.  Rows in registers: as many
-// CTAs as are resident at once, backward one per SM (few partial sums).  Rows in a ring: one
-// CTA per SM.  *ctas: partial rows.
+// CTAs as are resident at once, backward one per SM (few partial sums).  Rows in a ring (ring_row bytes of
+// it for a row of every matrix): one CTA per SM; shifted, a multiple of 8 of them, so that the rows of
+// each start alike.  *ctas: partial rows.
 template <class K>
-cudaError_t launch_norm(K kernel, NormArgs a, int threads, bool backward, int ring_inputs, int esize, int sms,
+cudaError_t launch_norm(K kernel, NormArgs a, int threads, bool backward, int ring_row, bool shift, int sms,
                         cudaStream_t stream, int* ctas, NormInstance* inst) {
     int R = threads / a.G;
     if (R < 1) R = 1;
@@ -677,12 +742,12 @@ cudaError_t launch_norm(K kernel, NormArgs a, int threads, bool backward, int ri
     // sums over groups (two or more: at most 256 threads and 8192 columns each, so at most 32 KB)
     size_t smem = backward && R > 1 ? static_cast<size_t>(a.H) * 4 : 0;
     int occ = 1;
-    if (ring_inputs) {
-        const int row = ring_inputs * a.H * esize, rings = kRingBytes - a.H * 4;
+    if (ring_row) {
+        const int row = ring_row, weights = ring_weight_bytes(a.H, shift), rings = kRingBytes - weights;
         while (R > 1 && 2 * R * row > rings) --R;
         a.depth = rings / (R * row);
         if (a.depth > kRingMostDepth) a.depth = kRingMostDepth;
-        const size_t ring = static_cast<size_t>(a.H) * 4 + static_cast<size_t>(R) * a.depth * row +
+        const size_t ring = static_cast<size_t>(weights) + static_cast<size_t>(R) * a.depth * row +
                             (R * a.depth + 1) * 8;
         if (ring > smem) smem = ring;
         int dev = 0;
@@ -705,21 +770,23 @@ cudaError_t launch_norm(K kernel, NormArgs a, int threads, bool backward, int ri
         }
     }
     const int64_t need = (a.T + R - 1) / R;
-    const int64_t grid = need < static_cast<int64_t>(occ) * sms ? need : static_cast<int64_t>(occ) * sms;
+    int64_t grid = need < static_cast<int64_t>(occ) * sms ? need : static_cast<int64_t>(occ) * sms;
+    if (shift) grid = grid / 8 * 8;
     *ctas = static_cast<int>(grid);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(R * a.G)), smem, stream, a);
 }
 
 template <class T, int V, int NV, template <class, int, int, int> class Rows, bool RING>
 cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_t stream, int* ctas) {
-    a.G = norm_group((a.H + V - 1) / V, NV);
+    constexpr bool SHIFT = Rows<T, V, NV, 1>::kShift;
+    a.G = norm_group(SHIFT ? ring_vectors<true>(a.H, V) : (a.H + V - 1) / V, NV);
     const bool next = a.w2 != nullptr;
 #define MOE_NORM(INPUTS, BACKWARD, ...)                                                                          \
     do {                                                                                                         \
         static NormInstance inst;                                                                                \
         return launch_norm(__VA_ARGS__, a,                                                                       \
                            BACKWARD ? kNormThreads : !RING ? 256 : next ? kNormThreads : kNormWideThreads,       \
-                           BACKWARD, RING ? INPUTS : 0, static_cast<int>(sizeof(T)), sms, stream, ctas, &inst);  \
+                           BACKWARD, RING ? INPUTS * ring_row_bytes<T, SHIFT>(a.H) : 0, SHIFT, sms, stream, ctas, &inst); \
     } while (0)
     switch (which) {
         case kPreForward: MOE_NORM(1, false, pre_norm_kernel<T, V, NV, Rows>);
@@ -750,29 +817,41 @@ cudaError_t launch_norm_nv(NormArgs a, int which, int gate, int sms, cudaStream_
 #undef MOE_NORM
 }
 
+// Whether all matrices of a call lie alike between 16-byte boundaries, row by row.
+inline bool alike(const NormArgs& a, int gate, int es) {
+    const auto one = [&](const void* p, int64_t ld) {
+        return !p || (((address(p) ^ address(a.out)) & 15) == 0 && (ld - a.H) * es % 16 == 0);
+    };
+    return one(a.x, a.ldx) && one(a.res, a.ldr) && one(a.dout, a.ldo) && one(a.h2, a.H) && one(a.dres, a.H) &&
+           (!full_gate(gate) || (one(a.gate, a.ldg) && one(a.dgate, a.H)));
+}
+
 // Where the rows come from, by their alignment (wide: 16-byte addresses and strides), number and width:
 //   fewer rows than twice the SMs: registers, 16 elements per thread where the row then fits a CTA's
 //     threads (more threads on each row)
-//   else wide rows: the ring, 32 elements per thread (registers where the weights and two rows do not
-//     fit a CTA's shared memory)
-//   rows at any address: registers, 16 elements per thread up to 4096 columns, else 32 (8000 rows of 4811: 212
-//     and 164 us; of 1569: 57 and 67)
+//   else wide rows, and others whose matrices lie alike: the ring, 32 elements per thread (8000 bf16 rows
+//     of 4811 before and after with the next norm: 106 against 165 us from registers); registers where
+//     the weights and two rows do not fit a CTA's shared memory
+//   else registers, 16 elements per thread up to 4096 columns, else 32 (8000 rows of 4811: 212 and 165 us;
+//     of 1569: 57 and 67)
 template <class T>
 cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, int sms, cudaStream_t stream,
                              int* ctas) {
     constexpr int W = 16 / static_cast<int>(sizeof(T));
-    if (!wide) {
-        if (a.H <= 8 * kNormThreads || (a.T < 2 * sms && a.H <= 16 * kNormThreads))
-            return launch_norm_nv<T, W, 16 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
-        return launch_norm_nv<T, W, 32 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
-    }
-    if (a.T < 2 * sms && a.H <= 16 * kNormThreads)
-        return launch_norm_nv<T, W, 16 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
     const int inputs = which == kPreForward ? 1 : which == kPreBackward ? (a.res ? 3 : 2) : full_gate(gate) ? 3 : 2;
-    const int column = 4 + 2 * inputs * static_cast<int>(sizeof(T));   // bytes: the weights, two rows
-    if (static_cast<int64_t>(column) * a.H > kRingBytes)
+    const bool few = a.T < 2 * sms && a.H <= 16 * kNormThreads;
+    const int row = wide ? ring_row_bytes<T, false>(a.H) : ring_row_bytes<T, true>(a.H);
+    const bool ring = !few && ring_weight_bytes(a.H, !wide) + 2 * inputs * row <= kRingBytes;
+    if (wide) {
+        if (few) return launch_norm_nv<T, W, 16 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
+        if (ring) return launch_norm_nv<T, W, 32 / W, RowRing, true>(a, which, gate, sms, stream, ctas);
         return launch_norm_nv<T, W, 32 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
-    return launch_norm_nv<T, W, 32 / W, RowRing, true>(a, which, gate, sms, stream, ctas);
+    }
+    if (ring && ring_vectors<true>(a.H, W) <= 32 / W * kNormThreads && alike(a, gate, static_cast<int>(sizeof(T))))
+        return launch_norm_nv<T, W, 32 / W, RowShift, true>(a, which, gate, sms, stream, ctas);
+    if (few || a.H <= 8 * kNormThreads)
+        return launch_norm_nv<T, W, 16 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
+    return launch_norm_nv<T, W, 32 / W, RowAny, false>(a, which, gate, sms, stream, ctas);
 }
 
 // norms_bf16.cu, norms_fp16.cu, norms_fp32.cu

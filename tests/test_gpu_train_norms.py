@@ -257,3 +257,34 @@ def test_neighbours_that_are_not_finite(dtype):
     assert torch.isfinite(p.next_h[keep]).all() and torch.isfinite(p.out[keep]).all()
     dx, _ = moe.moe_pre_norm_backward(d, x, w, rstd)
     assert torch.isfinite(dx[keep]).all() and dx[20].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("T,H", [(310, 1), (311, 3), (333, 249), (2101, 250), (700, 1753), (400, 4811), (320, 9001)])
+def test_many_rows_between_sixteen_byte_boundaries(T, H, dtype):
+    """Enough rows for the ring, whose rows start by their number modulo 8."""
+    test_pre_norm_and_gradient(T, H, dtype, "fp32")
+    for kind, sigmoid in (("none", False), ("token", True), ("channel", True), ("full", False), ("full", True)):
+        test_post_norm_and_gradient(T, H, dtype, kind, sigmoid)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("pad,lead", [(16, 0), (16, 8), (7, 3)])
+def test_many_strided_rows_and_their_neighbours(pad, lead, dtype):
+    """Rows of wider matrices (NaN between them), some of them not finite: the others are as without."""
+    g = gen(pad + lead)
+    T, H = 330, 251
+    lay = lambda t: strided_copy(t, pad, lead)
+    x, w, d = rand(g, T, H, dtype=dtype), rand(g, H), rand(g, T, H, dtype=dtype)
+    x[100], x[329], x[200, 7] = float("nan"), float("nan"), float("inf")
+    keep = torch.tensor([t for t in range(T) if t not in (100, 200, 329)])
+    h, rstd = moe.moe_pre_norm(lay(x), w, eps=1e-5)
+    want, _ = norm64(x, w, 0, 1e-5)
+    check(h.cpu()[keep], want[keep], roundings=ROW, name="h")
+    assert h[100].isnan().all() and h[329].isnan().all()
+    p = moe.moe_post_norm(lay(x), lay(d), w, eps=1e-5, next_weight=w)
+    z = d.double().cpu() + want
+    check(p.out.cpu()[keep], z[keep], (d.double().cpu().abs() + want.abs())[keep], ROW + 12, "out")
+    check(p.next_h.cpu()[keep], norm64(p.out, w, 0, 1e-5)[0][keep], roundings=ROW, name="next_h")
+    dx, _ = moe.moe_pre_norm_backward(lay(d), lay(x), w, rstd, dresidual=lay(d))
+    assert torch.isfinite(dx.cpu()[keep]).all() and dx[100].isnan().all()
