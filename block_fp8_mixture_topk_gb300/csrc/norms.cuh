@@ -12,7 +12,7 @@
 // and its use (at most 32 elements per thread, G threads per row).  A CTA holds R groups of G
 // threads, each with its own named barrier, and walks over rows with the weights at hand.  Two
 // sources of rows and weights: registers (RowRegs: few rows; RowAny: rows at any address), or shared memory
-// (RowRing: 16-byte rows; one thread of a group keeps up to four rows of bulk copies in flight
+// (RowShift: rows of any width whose matrices lie alike; RowRing: 16-byte rows; one thread of a group keeps up to four rows of bulk copies in flight
 // ahead of the group, so that the reduction's latency does not stop the loads).  The weights'
 // gradient is summed over a CTA's rows in fp32 registers, over its groups in shared memory, written once
 // per CTA and summed by a second kernel in a fixed order: no atomics, so the result does not
@@ -23,8 +23,8 @@
 // 4.7 us among them that sum the weights' partials.  One row: 6.7 us on the device.  About 4 us of
 // each launch are its first loads and last stores; the after-norm with a next norm holds its weights and the
 // stored row in registers (111, so 448 threads per SM) and is then bound by the two reductions' latency.
-// Rows at any address are bound by instructions (joining the vectors): 8000 x 4811 before and after with
-// the next norm 165 us, 2.9 times the floor.
+// Rows of odd widths: 8000 x 4811 before and after with the next norm 102 us, 1.8 times the bytes' time; where
+// the matrices do not lie alike the vectors are joined, bound by instructions: 165 us.
 #pragma once
 
 #include <atomic>
@@ -118,7 +118,7 @@ __device__ __forceinline__ Group make_group(float* red, int G) {
 // once, then for each row fetch(t), get(n, i) = vector i of this thread in matrix n (any number of
 // times) and next() (the row is done with); finish() at the end.  weight(i) = the weights of vector i;
 // store(row, i, o) writes it, skip(i) tells that there is nothing of it to write.  Vectors and elements
-// past the row read as zero.
+// past the row read as zero; again(n, i) is get for values that are only stored (anything past the row).
 template <int V>
 struct Weights {
     float2 v[V / 2];
@@ -200,6 +200,7 @@ struct RowInRegs {
     __device__ __forceinline__ int column(int i) const { return vec(i) * V; }
     __device__ __forceinline__ int vec(int i) const { return ANY ? ((tid >> 5) * NV + i) * 32 + (tid & 31) : tid + i * G; }
     __device__ __forceinline__ Pack<T, V> get(int n, int i) const { return r[n][i]; }
+    __device__ __forceinline__ Pack<T, V> again(int n, int i) const { return r[n][i]; }
     __device__ __forceinline__ bool skip(int i) const { return !ANY && tid + i * G >= nvec; }
     __device__ __forceinline__ void store(T* row, int i, const Pack<T, V>& o) const {
         if constexpr (ANY) store_any(row, H, vec(i), o.raw);
@@ -350,12 +351,16 @@ struct RowInRing {
         mbar_wait(smem_addr(bar + slot), phase, abort_flag, status);
     }
     __device__ __forceinline__ Pack<T, V> get(int n, int i) const {
+        Pack<T, V> p = again(n, i);
+        if constexpr (SHIFT) p.raw = inside_row<T>(p.raw, H, column(i));
+        return p;
+    }
+    __device__ __forceinline__ Pack<T, V> again(int n, int i) const {
         Pack<T, V> p;
         const int v = tid + i * G;
         if (v < nvec)
             p.raw = *reinterpret_cast<const typename Pack<T, V>::Raw*>(ring + (slot * NIN + n) * row_bytes + v * 16);
         else p.zero();
-        if constexpr (SHIFT) p.raw = inside_row<T>(p.raw, H, v * V - lead);
         return p;
     }
     __device__ __forceinline__ int vec(int i) const { return tid + i * G; }
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(Rows<T, V, NV, 1>::kWide ? kNormWideThreads : 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (in.skip(i)) continue;
-            const Pack<T, V> x = in.get(0, i);
+            const Pack<T, V> x = in.again(0, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o;
 #pragma unroll
@@ -494,10 +499,10 @@ __global__ void __launch_bounds__(!Rows<T, V, NV, 1>::kWide || NEXT ? kNormThrea
         Pack<T, V> s[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const Pack<T, V> y = in.get(0, i), res = in.get(1, i);
+            const Pack<T, V> y = NEXT ? in.get(0, i) : in.again(0, i), res = NEXT ? in.get(1, i) : in.again(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> gt;
-            if constexpr (full_gate(GATE)) gt = in.get(2, i);
+            if constexpr (full_gate(GATE)) gt = NEXT ? in.get(2, i) : in.again(2, i);
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 float2 z = mul2(mul2(mul2(y.pair(e), both(r)), w.v[e]), both(b));
@@ -591,10 +596,10 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (in.skip(i)) continue;
-            const Pack<T, V> x = in.get(0, i), d = in.get(1, i);
+            const Pack<T, V> x = in.again(0, i), d = in.again(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o, s;
-            if constexpr (RES) s = in.get(2, i);
+            if constexpr (RES) s = in.again(2, i);
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 const float2 u = fma2(mul2(x.pair(e), both(r)), both(-m), mul2(d.pair(e), w.v[e]));
@@ -675,10 +680,10 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (in.skip(i)) continue;
-            const Pack<T, V> y = in.get(0, i), d = in.get(1, i);
+            const Pack<T, V> y = in.again(0, i), d = in.again(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o, p, q, gt;
-            if constexpr (FULL && !KEEP) gt = in.get(2, i);
+            if constexpr (FULL && !KEEP) gt = in.again(2, i);
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 const float2 n = mul2(y.pair(e), both(r));
@@ -830,7 +835,7 @@ inline bool alike(const NormArgs& a, int gate, int es) {
 //   fewer rows than twice the SMs: registers, 16 elements per thread where the row then fits a CTA's
 //     threads (more threads on each row)
 //   else wide rows, and others whose matrices lie alike: the ring, 32 elements per thread (8000 bf16 rows
-//     of 4811 before and after with the next norm: 106 against 165 us from registers); registers where
+//     of 4811 before and after with the next norm: 102 against 165 us from registers); registers where
 //     the weights and two rows do not fit a CTA's shared memory
 //   else registers, 16 elements per thread up to 4096 columns, else 32 (8000 rows of 4811: 212 and 165 us;
 //     of 1569: 57 and 67)
