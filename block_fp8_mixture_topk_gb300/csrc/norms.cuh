@@ -834,7 +834,7 @@ inline bool alike(const NormArgs& a, int gate, int es) {
 // Where the rows come from, by their alignment (wide: 16-byte addresses and strides), number and width:
 //   fewer rows than twice the SMs: registers, 16 elements per thread where the row then fits a CTA's
 //     threads (more threads on each row)
-//   else wide rows, and others whose matrices lie alike: the ring, 32 elements per thread (8000 bf16 rows
+//   else wide rows, and others whose matrices lie alike (not few: 8 CTAs need rows): the ring, 32 elements per thread (8000 bf16 rows
 //     of 4811 before and after with the next norm: 102 against 165 us from registers); registers where
 //     the weights and two rows do not fit a CTA's shared memory
 //   else registers, 16 elements per thread up to 4096 columns, else 32 (8000 rows of 4811: 212 and 165 us;
@@ -852,7 +852,7 @@ cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, 
         if (ring) return launch_norm_nv<T, W, 32 / W, RowRing, true>(a, which, gate, sms, stream, ctas);
         return launch_norm_nv<T, W, 32 / W, RowRegs, false>(a, which, gate, sms, stream, ctas);
     }
-    if (ring && ring_vectors<true>(a.H, W) <= 32 / W * kNormThreads && alike(a, gate, static_cast<int>(sizeof(T))))
+    if (ring && a.T >= 2 * sms && ring_vectors<true>(a.H, W) <= 32 / W * kNormThreads && alike(a, gate, static_cast<int>(sizeof(T))))
         return launch_norm_nv<T, W, 32 / W, RowShift, true>(a, which, gate, sms, stream, ctas);
     if (few || a.H <= 8 * kNormThreads)
         return launch_norm_nv<T, W, 16 / W, RowAny, false>(a, which, gate, sms, stream, ctas);

@@ -288,3 +288,11 @@ def test_many_strided_rows_and_their_neighbours(pad, lead, dtype):
     check(p.next_h.cpu()[keep], norm64(p.out, w, 0, 1e-5)[0][keep], roundings=ROW, name="next_h")
     dx, _ = moe.moe_pre_norm_backward(lay(d), lay(x), w, rstd, dresidual=lay(d))
     assert torch.isfinite(dx.cpu()[keep]).all() and dx[100].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("T,H", [(1, 9001), (5, 8193), (7, 12001), (100, 16381), (303, 10003), (304, 8199)])
+def test_few_wide_rows_between_sixteen_byte_boundaries(T, H, dtype):
+    test_pre_norm_and_gradient(T, H, dtype, "fp32")
+    for kind, sigmoid in (("none", False), ("full", True)):
+        test_post_norm_and_gradient(T, H, dtype, kind, sigmoid)
