@@ -424,17 +424,23 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         tmem_relinquish_pair();
     }
     grid_dependency_wait();
-    // the experts' rows: offsets that leave [0, rows] or run backwards are clamped and reported
+    // the experts' rows: every row up to the last offset belongs to exactly one expert.  Offsets that leave
+    // [0, rows], start above 0 or run backwards are reported, and replaced by 0 for the first and the running
+    // maximum of the clamped ones for the others.
+    int bad = 0;
     for (int e = threadIdx.x; e <= a.E; e += X_THREADS) {
-        int64_t o = a.offsets[e];
-        const int64_t prev = e > 0 ? a.offsets[e - 1] : 0;
-        if (o < 0 || o > a.rows || prev > o || (e == 0 && o != 0)) {
-            status_set(a.status, MOE_STATUS_BAD_COUNT);
-            o = o < 0 ? 0 : o > a.rows ? a.rows : o;
-        }
-        ctl->row0[e] = static_cast<int>(o);
+        const int64_t o = a.offsets[e], prev = e > 0 ? a.offsets[e - 1] : 0;
+        bad |= o < 0 || o > a.rows || prev > o || (e == 0 && o != 0);
+        ctl->row0[e] = static_cast<int>(e == 0 || o < 0 ? 0 : o > a.rows ? a.rows : o);
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            status_set(a.status, MOE_STATUS_BAD_COUNT);
+            for (int e = 1; e <= a.E; ++e)
+                if (ctl->row0[e] < ctl->row0[e - 1]) ctl->row0[e] = ctl->row0[e - 1];
+        }
+        __syncthreads();
+    }
     if (MODE == kWeights) {
         for (int e = threadIdx.x; e < a.E; e += X_THREADS) {
             const int n = ctl->row0[e + 1] - ctl->row0[e];

@@ -597,7 +597,8 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
  *                        (w13's rows: gate, then up), and, where gate_up is not NULL, c itself rounded,
  *                        [num_rows, N], which the gradient needs
  * Rows past expert_offsets[E] are zero.  expert_offsets that leave [0, num_rows], start above 0 or run
- * backwards are clamped and set MOE_STATUS_BAD_COUNT.  N and K multiples of 8 (N of 16 with
+ * backwards set MOE_STATUS_BAD_COUNT, and the products are those of 0 in place of the first and the
+ * running maximum of the others, each clamped to [0, num_rows].  N and K multiples of 8 (N of 16 with
  * SILU_MUL), row strides multiples of 8, all addresses 16-byte aligned. */
 #define MOE_EXPERT_STORE 0
 #define MOE_EXPERT_SILU_MUL 1

@@ -245,3 +245,33 @@ def test_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(held, step()))
+
+
+@pytest.mark.parametrize("bad", [[0, 12, 5, 20], [5, 8, 13, 20], [3, 3, 3, 3], [-7, 4, 4, 20], [0, 400, -1, 20],
+                                 [20, 10, 5, 0], [2 ** 31 - 1, -2 ** 31, 7, 19], [9, 0, 20, 20]],
+                         ids=lambda b: "-".join(map(str, b)))
+def test_offsets_out_of_order_are_repaired(bad):
+    """Every row up to the last offset has one expert: 0 in place of the first offset, the running maximum of the
+    others.  All forms equal those of the repaired offsets, in the rows of no expert too."""
+    g = gen(15)
+    rows, N, K = 20, 32, 16
+    a, w = rand(g, rows, K, dtype=torch.bfloat16), rand(g, 3, N, K, dtype=torch.bfloat16)
+    dc, gu = rand(g, rows, N, dtype=torch.bfloat16), rand(g, rows, 2 * K, dtype=torch.bfloat16)
+    good = [0]
+    for o in bad[1:]:
+        good.append(max(good[-1], min(max(o, 0), rows)))
+    bad, good = (torch.tensor(o, dtype=torch.int32, device="cuda") for o in (bad, good))
+
+    def forms(off):
+        h, c = moe.moe_expert_gemm_silu_mul(a, w, off)
+        return (moe.moe_expert_gemm(a, w, off), h, c, moe.moe_expert_gemm_dgrad(dc, w, off),
+                moe.moe_expert_gemm_dgrad(dc, w, off, gate_up=gu), moe.moe_expert_gemm_wgrad(dc, a, off))
+    status_clear()
+    want = forms(good)
+    assert status() == 0
+    for n in (N, N // 2, K, 2 * K):   # memory that the results take next holds NaN
+        torch.full((rows, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    got = forms(bad)
+    assert status() == 4
+    for name, x, y in zip(("c", "h", "gate_up", "da", "dgate_up", "dw"), got, want):
+        assert torch.equal(x, y), name
