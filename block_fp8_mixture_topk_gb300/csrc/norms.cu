@@ -67,10 +67,13 @@ cudaError_t launch_final(const FinalArgs& f, cudaStream_t stream) {
     return launch_pdl(norm_weight_grad_kernel, dim3(static_cast<unsigned>((f.H + 31) / 32)), dim3(1024), 0, stream, f);
 }
 
-// The gate's part of the arguments: MOE_OK, *gate = its shape (row for none).
-int check_gate(const moe_post_norm_params* p, int H, int* gate) {
+// The gate's part of the arguments: MOE_OK, *gate = its shape (row for none).  A gate with a value per row or
+// element holds none where there are no rows, and then needs no address.
+int check_gate(const moe_post_norm_params* p, int T, int H, int* gate) {
     if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_FULL) return MOE_ERR_INVALID_ARG;
-    if ((p->gate_kind == MOE_GATE_NONE) != (p->gate == nullptr)) return MOE_ERR_INVALID_ARG;
+    const bool by_row = p->gate_kind == MOE_GATE_TOKEN || p->gate_kind == MOE_GATE_FULL;
+    if (p->gate_kind == MOE_GATE_NONE ? p->gate != nullptr : p->gate == nullptr && !(by_row && T == 0))
+        return MOE_ERR_INVALID_ARG;
     if (p->gate_kind == MOE_GATE_TOKEN && p->gate_stride < 1) return MOE_ERR_INVALID_ARG;
     if (p->gate_kind == MOE_GATE_FULL && p->gate_stride < H) return MOE_ERR_INVALID_ARG;
     *gate = p->gate_kind == MOE_GATE_CHANNEL ? kGateChannel
@@ -180,7 +183,7 @@ int moe_post_norm(const void* y, int64_t ldy, const void* residual, int64_t ldr,
                   void* stream) {
     if (!p) return MOE_ERR_INVALID_ARG;
     int gate = 0, rc = check_norm(T, H, dtype, p->weight_dtype);
-    if (rc != MOE_OK || (rc = check_gate(p, H, &gate)) != MOE_OK) return rc;
+    if (rc != MOE_OK || (rc = check_gate(p, T, H, &gate)) != MOE_OK) return rc;
     if (ldy < H || ldr < H) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
     const size_t es = dtype_bytes(dtype), ws = dtype_bytes(p->weight_dtype);
@@ -226,8 +229,8 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
                            void* dgate, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
     if (!p) return MOE_ERR_INVALID_ARG;
     int gate = 0, rc = check_norm(T, H, dtype, p->weight_dtype);
-    if (rc != MOE_OK || (rc = check_gate(p, H, &gate)) != MOE_OK) return rc;
-    if (lddout < H || ldy < H || !p->weight || !dweight || (dgate && !p->gate)) return MOE_ERR_INVALID_ARG;
+    if (rc != MOE_OK || (rc = check_gate(p, T, H, &gate)) != MOE_OK) return rc;
+    if (lddout < H || ldy < H || !p->weight || !dweight || (dgate && p->gate_kind == MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
     const size_t es = dtype_bytes(dtype), ws = dtype_bytes(p->weight_dtype);
     if (T > 0 && (!dout || !y || !rstd || !dy)) return MOE_ERR_INVALID_ARG;
     const size_t gs = gate == kGateChannel ? 4 : es;   // a channel gate's gradient is fp32

@@ -569,7 +569,7 @@ int moe_pre_norm_backward(const void* dh, int64_t lddh, const void* x, int64_t l
 typedef struct moe_post_norm_params {
     const void* weight;
     const void* next_weight;     /* or NULL (ignored by the gradient) */
-    const void* gate;            /* NULL with MOE_GATE_NONE */
+    const void* gate;            /* NULL with MOE_GATE_NONE; may be NULL where T = 0 with MOE_GATE_TOKEN and _FULL */
     int64_t gate_stride;
     int32_t weight_dtype;
     int32_t gate_kind;

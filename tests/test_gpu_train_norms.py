@@ -296,3 +296,23 @@ def test_few_wide_rows_between_sixteen_byte_boundaries(T, H, dtype):
     test_pre_norm_and_gradient(T, H, dtype, "fp32")
     for kind, sigmoid in (("none", False), ("full", True)):
         test_post_norm_and_gradient(T, H, dtype, kind, sigmoid)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("kind", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+def test_no_rows_with_each_gate(kind, sigmoid, dtype):
+    H = 96
+    x, w = torch.zeros(0, H, device="cuda", dtype=dtype), torch.ones(H, device="cuda")
+    gate = make_gate(gen(1), kind, 0, H, dtype)
+    kw = dict(gate=gate, gate_kind=kind, gate_sigmoid=sigmoid and kind != "none")
+    p = moe.moe_post_norm(x, x, w, next_weight=w, **kw)
+    assert p.out.shape == p.next_h.shape == (0, H) and p.rstd.shape == p.next_rstd.shape == (0,)
+    torch.full((H,), float("nan"), device="cuda")   # memory that the sums take next
+    d = moe.moe_post_norm_backward(x, x, w, p.rstd, **kw)
+    assert d.dy.shape == d.dresidual.shape == (0, H) and torch.equal(d.dweight, torch.zeros(H, device="cuda"))
+    assert (d.dgate is None) == (kind == "none")
+    if kind == "channel":
+        assert torch.equal(d.dgate, torch.zeros(H, device="cuda"))
+    elif gate is not None:
+        assert d.dgate.shape == gate.shape and d.dgate.dtype == dtype

@@ -241,3 +241,14 @@ def test_expert_binding_refuses():
               lambda: moe.moe_expert_gemm_dgrad(x, w, off), lambda: moe.moe_expert_gemm_wgrad(x, x, off)):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+@pytest.mark.parametrize("kind", [1, 3])
+def test_post_norm_of_no_rows_needs_no_gate(kind):
+    """An empty tensor's address is 0: a gate of no values has none.  (A row or a channel gate still needs one.)"""
+    empty = dict(gate=0, gate_kind=kind)
+    assert post_norm(empty, T=0, y=NULL, r=NULL, out=NULL, rstd=NULL) == 0
+    assert post_norm(empty, T=1) == INVALID and post_norm_backward(empty, T=1) == INVALID
+    assert post_norm(dict(gate=0, gate_kind=2), T=0) == INVALID
+    assert post_norm_backward(dict(gate=0, gate_kind=2), T=0) == INVALID
+    assert post_norm_backward(dict(gate=0, gate_kind=0), T=0) == INVALID    # a gradient for no gate
