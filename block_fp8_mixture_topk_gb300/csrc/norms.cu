@@ -39,8 +39,9 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const FinalArgs 
     }
     float g = weight_at(a.gate, a.g_dtype, c), slope = 1.0f;
     if (a.sigmoid) {
-        g = sigmoid_as<float>(g);
-        slope = g * (1.0f - g);
+        const float e = exp_minus<float>(g);
+        g = sigmoid_of<float>(e);
+        slope = slope_of(e, g);
     }
     a.dw[c] = a.b * g * v;
     if (a.dgate) a.dgate[c] = slope * a.b * (weight_at(a.w, a.w_dtype, c) + a.w_offset) * v;

@@ -63,21 +63,41 @@ __device__ __forceinline__ float weight_at(const void* w, int dtype, int64_t i) 
     if (dtype == MOE_DTYPE_FP16) return __half2float(static_cast<const __half*>(w)[i]);
     return __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
-// sigmoid(v): for 16-bit results with the approximate exponential and reciprocal instructions (a few
-// 2^-23 relative, far below their rounding of 2^-9 and 2^-12; the division form costs three times
-// the instructions and made the gated backward pass instruction-bound)
+// exp(-v) and 1 / v: for 16-bit results by the approximate instructions, whose product with log2(e) and
+// results are off by (2 |v| + 4) 2^-24 and 2^-23 of themselves, far below the results' rounding of 2^-9 and
+// 2^-12 (the division form costs three times the instructions and made the gated backward pass
+// instruction-bound)
+template <class T>
+__device__ __forceinline__ float exp_minus(float v) {
+    if (sizeof(T) != 2) return expf(-v);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+    return e;
+}
+template <class T>
+__device__ __forceinline__ float reciprocal(float v) {
+    if (sizeof(T) != 2) return 1.0f / v;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 template <class T>
 __device__ __forceinline__ float sigmoid_as(float v) {
-    if (sizeof(T) != 2) return 1.0f / (1.0f + expf(-v));
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
+    return reciprocal<T>(1.0f + exp_minus<T>(v));
 }
 template <class T>
 __device__ __forceinline__ float2 sigmoid_as(float2 v) {
     return make_float2(sigmoid_as<T>(v.x), sigmoid_as<T>(v.y));
 }
+// The sigmoid and its slope for gradients, of e = exp(-v): s = 1 / (1 + e), and s (1 - s) with 1 - s = e s
+// (1 where an infinite e leaves s = 0: fminf passes over what is no number).  The slope then keeps
+// its digits where the gate saturates; 1 - s of a rounded s is off by 5e-4 of itself at v = 10 and
+// is 0 from 17 on.
+template <class T>
+__device__ __forceinline__ float sigmoid_of(float e) {
+    return reciprocal<T>(1.0f + e);
+}
+__device__ __forceinline__ float slope_of(float e, float s) { return s * fminf(e * s, 1.0f); }
 
 struct Group {
     float* red;       // [2][16] of this group
@@ -622,7 +642,9 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_backward_kernel(const N
 template <class T, int V, int NV, int GATE, template <class, int, int, int> class Rows>
 __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const NormArgs a) {
     MOE_NORM_PROLOGUE
-    constexpr bool FULL = full_gate(GATE), KEEP = GATE == kGateFullSigmoid;   // KEEP: sigmoids, from pass to pass
+    // the gate's sigmoids: fp32 ones stay in registers from pass to pass (their division costs more), the slope
+    // needs the exponential again either way
+    constexpr bool FULL = full_gate(GATE), SIGMOID = GATE == kGateFullSigmoid, KEEP = SIGMOID && sizeof(T) == 4;
     Rows<T, V, NV, FULL ? 3 : 2> in;
     in.src[0] = static_cast<const T*>(a.x);
     in.ld[0] = a.ldx;
@@ -645,8 +667,9 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
             if (a.gate) {
                 gr = to_f32(static_cast<const T*>(a.gate)[t * a.ldg]);
                 if (a.sigmoid) {
-                    gr = sigmoid_as<T>(gr);
-                    slope = gr * (1.0f - gr);
+                    const float e = exp_minus<T>(gr);
+                    gr = sigmoid_of<T>(e);
+                    slope = slope_of(e, gr);
                 }
             }
         }
@@ -661,9 +684,10 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 float2 p = mul2(d.pair(e), mul2(y.pair(e), both(r)));
-                if constexpr (KEEP) {
-                    kept[i * NP + e] = sigmoid_as<T>(gt.pair(e));
-                    p = mul2(p, kept[i * NP + e]);
+                if constexpr (SIGMOID) {
+                    const float2 s = sigmoid_as<T>(gt.pair(e));
+                    if constexpr (KEEP) kept[i * NP + e] = s;
+                    p = mul2(p, s);
                 } else if constexpr (FULL) {
                     p = mul2(p, gt.pair(e));
                 }
@@ -676,6 +700,7 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
         if constexpr (GATE == kGateRow)
             if (a.dgate && g.tid == 0) static_cast<T*>(a.dgate)[t] = from_f32<T>(slope * a.b * sum);
         const float2 scale = both(a.b * gr * r), m = both(-(sum / static_cast<float>(a.H)));   // scale: of t / w
+        const float2 mr = both(m.x * r), rb = both(r * a.b);   // sigmoid of a full gate: n without its own product
         T* dy = static_cast<T*>(a.out) + t * a.H;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -683,20 +708,25 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
             const Pack<T, V> y = in.again(0, i), d = in.again(1, i);
             const Weights<V> w = in.weight(i);
             Pack<T, V> o, p, q, gt;
-            if constexpr (FULL && !KEEP) gt = in.again(2, i);
+            if constexpr (FULL) gt = in.again(2, i);
 #pragma unroll
             for (int e = 0; e < NP; ++e) {
                 const float2 n = mul2(y.pair(e), both(r));
                 float2 dw = mul2(d.pair(e), w.v[e]);
-                if constexpr (KEEP) {
-                    const float2 s = kept[i * NP + e], sl = mul2(s, make_float2(1.0f - s.x, 1.0f - s.y));
-                    q.set_pair(e, mul2(mul2(sl, mul2(dw, n)), both(a.b)));
+                if constexpr (SIGMOID) {
+                    const float2 v = gt.pair(e), x = make_float2(exp_minus<T>(v.x), exp_minus<T>(v.y));
+                    float2 s;
+                    if constexpr (KEEP) s = kept[i * NP + e];
+                    else s = make_float2(sigmoid_of<T>(x.x), sigmoid_of<T>(x.y));
+                    const float2 slope = make_float2(slope_of(x.x, s.x), slope_of(x.y, s.y));
+                    q.set_pair(e, mul2(slope, mul2(dw, mul2(y.pair(e), rb))));
                     dw = mul2(dw, s);
                 } else if constexpr (FULL) {
                     q.set_pair(e, mul2(mul2(dw, n), both(a.b)));
                     dw = mul2(dw, gt.pair(e));
                 }
-                o.set_pair(e, mul2(scale, fma2(n, m, dw)));
+                if constexpr (SIGMOID) o.set_pair(e, mul2(scale, fma2(y.pair(e), mr, dw)));
+                else o.set_pair(e, mul2(scale, fma2(n, m, dw)));
                 p.set_pair(e, mul2(both(a.a), d.pair(e)));
             }
             in.store(dy, i, o);

@@ -316,3 +316,38 @@ def test_no_rows_with_each_gate(kind, sigmoid, dtype):
         assert torch.equal(d.dgate, torch.zeros(H, device="cuda"))
     elif gate is not None:
         assert d.dgate.shape == gate.shape and d.dgate.dtype == dtype
+
+
+@pytest.mark.parametrize("kind", ["token", "channel", "full"])
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("T,H", [(1, 8), (7, 264), (40, 97), (700, 1032), (333, 249)])
+def test_gradients_of_saturated_gates(T, H, dtype, kind):
+    """Gates from -30 to 30, where s * (1 - s) of a rounded sigmoid s has no digits left: errors count against the
+    slope itself, d/dg sigmoid = e / (1 + e)^2 with e = exp(-|g|).  An fp32 exponential of an argument |g| is off
+    by at most 2 |g| + 4 half-steps, the quotient and the products by 12 more."""
+    g = gen(T + H)
+    b = 1024.0   # the slopes in fp16's normal range
+    y, dout, w = rand(g, T, H, dtype=dtype), rand(g, T, H, dtype=dtype), rand(g, H)
+    gate = make_gate(g, kind, T, H, dtype)
+    big = torch.tensor([8.0, -8, 10, -10, 12, -12, 16, -16, 17, -17, 20, -20, 30, -30], dtype=dtype, device="cuda")
+    gate.view(-1).copy_(big[torch.arange(gate.numel(), device="cuda") % len(big)])
+    rstd = norm64(y, w, 0, 1e-6)[1].float().cuda()
+    d = moe.moe_post_norm_backward(dout, y, w, rstd, gate=gate, gate_kind=kind, gate_sigmoid=True, block_scale=b)
+    g64 = gate.double().cpu()
+    g64 = g64.reshape(-1, 1) if kind == "token" else g64.reshape(1, -1) if kind == "channel" else g64
+    e = torch.exp(-g64.abs())
+    slope, sig = e / (1 + e) ** 2, torch.where(g64 < 0, e, torch.ones_like(e)) / (1 + e)
+    n, dd, ww = y.double().cpu() * rstd.double().cpu()[:, None], dout.double().cpu(), w.double().cpu()
+    s = slope * b * dd * n * ww
+    exp_error = 2 * 30 + 4 + 12
+    if kind == "full":
+        check(d.dgate, s, roundings=exp_error, name="dgate")
+    else:
+        check(d.dgate, s.sum(0 if kind == "channel" else 1), s.abs().sum(0 if kind == "channel" else 1),
+              exp_error + (T + 60 if kind == "channel" else 53 + 20), "dgate")
+    t = b * sig * dd * ww
+    m, ma = (t * n).mean(1, keepdim=True), (t * n).abs().mean(1, keepdim=True)
+    rs = rstd.double().cpu()[:, None]
+    check(d.dy, rs * (t - n * m), rs * (t.abs() + n.abs() * ma), exp_error + 53 + 20, "dy")
+    s = b * sig * dd * n
+    check(d.dweight, s.sum(0), s.abs().sum(0), exp_error + T + 60, "dweight")
