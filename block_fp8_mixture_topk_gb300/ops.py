@@ -2,7 +2,7 @@
 
 Function names and argument order follow the C ABI; tensors are torch CUDA
 tensors (bf16 as torch.bfloat16, e4m3 codes as torch.uint8 or
-torch.float8_e4m3fn), launched on torch's current stream.
+torch.float8_e4m3fn) of the current device, launched on torch's current stream.
 """
 from __future__ import annotations
 
@@ -161,9 +161,25 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream():
-    """The current stream of the current device, as the C ABI takes it."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+try:   # a third of the time of the public ones, which counts in a step of one token
+    _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    _device = torch.cuda.current_device
+
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _stream(names="", *operands):
+    """The current stream of the current device, as the C ABI takes it.  An operand of another device (`names` in
+    their order, None for one that is not given) is refused: the kernel would run beside the stream that
+    orders it, on memory that its GPU may not reach."""
+    device = _device()
+    for t in operands:
+        if t is not None and t.get_device() != device:
+            at = [x is t for x in operands].index(True)
+            raise ValueError(f"{names.split()[at]} is on {t.device}, but the current device is cuda:{device}")
+    return _raw_stream(device)
 
 
 def _check(name, rc):
@@ -209,7 +225,7 @@ def moe_route_topk(logits, topk, renormalize=True, routing: RoutingParams | None
     w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
     rp = routing.to_c() if routing else None
     rc = lib().moe_route_topk(_ptr(logits), T, E, topk, int(bool(renormalize)),
-                              ctypes.byref(rp) if rp else None, _ptr(ids), _ptr(w), _stream())
+                              ctypes.byref(rp) if rp else None, _ptr(ids), _ptr(w), _stream("logits", logits))
     _check("moe_route_topk", rc)
     return ids, w
 
@@ -232,7 +248,7 @@ def moe_align_permute(topk_ids, num_experts, block_m=MOE_BLOCK_M):
     rc = lib().moe_align_permute(_ptr(topk_ids), T, k, num_experts, block_m, _ptr(out["expert_offsets"]),
                                  _ptr(out["padded_offsets"]), _ptr(out["sorted_pair_ids"]), _ptr(out["pos"]),
                                  _ptr(out["tile_expert"]), _ptr(out["tile_row0"]), _ptr(out["num_tiles"]),
-                                 _ptr(ws), wsb, _stream())
+                                 _ptr(ws), wsb, _stream("topk_ids", topk_ids))
     _check("moe_align_permute", rc)
     out["max_rows"], out["max_tiles"] = rows, tiles
     return out
@@ -257,7 +273,7 @@ def fp8_group_quant(x, scale_fmt="f32"):
         s = torch.empty(rows, max(cols // 32, 1), dtype=torch.uint8, device=x.device)
     else:
         s = torch.empty(rows, max(cols // 128, 1), dtype=torch.float32, device=x.device)
-    rc = lib().fp8_group_quant_ex(_ptr(x), rows, cols, cols, _ptr(q), _ptr(s), SCALE_FMT[scale_fmt], _stream())
+    rc = lib().fp8_group_quant_ex(_ptr(x), rows, cols, cols, _ptr(q), _ptr(s), SCALE_FMT[scale_fmt], _stream("x", x))
     _check("fp8_group_quant", rc)
     return q, s
 
@@ -268,7 +284,7 @@ def fp8_block_quant_weight(w, scale_fmt="f32"):
     E, N, K = w.shape
     q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
     s = torch.empty(E, max(N // 128, 1), max(K // 128, 1), dtype=torch.float32, device=w.device)
-    rc = lib().fp8_block_quant_weight_ex(_ptr(w), E, N, K, _ptr(q), _ptr(s), SCALE_FMT[scale_fmt], _stream())
+    rc = lib().fp8_block_quant_weight_ex(_ptr(w), E, N, K, _ptr(q), _ptr(s), SCALE_FMT[scale_fmt], _stream("w", w))
     _check("fp8_block_quant_weight", rc)
     return q, s
 
@@ -280,7 +296,7 @@ def moe_fp8_block_pack_scales(s):
     E, NB, KB = s.shape
     out = torch.empty(E, NB, (KB + 3) // 4, 512, dtype=torch.uint8, device=s.device)
     _check("moe_fp8_block_pack_scales", lib().moe_fp8_block_pack_scales(_ptr(s), E, NB * 128, KB * 128, _ptr(out),
-                                                                          _stream()))
+                                                                          _stream("s", s)))
     return out
 
 
@@ -291,7 +307,7 @@ def moe_mxfp8_quant_weight(w):
     E, N, K = w.shape
     q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
     s = torch.empty(E, N, max(K // 32, 1), dtype=torch.uint8, device=w.device)
-    _check("moe_mxfp8_quant_weight", lib().moe_mxfp8_quant_weight(_ptr(w), E, N, K, _ptr(q), _ptr(s), _stream()))
+    _check("moe_mxfp8_quant_weight", lib().moe_mxfp8_quant_weight(_ptr(w), E, N, K, _ptr(q), _ptr(s), _stream("w", w)))
     return q, s
 
 
@@ -306,7 +322,7 @@ def moe_mxfp8_pack_scales(s):
     K = s.shape[-1] * 32
     rows = s.numel() // s.shape[-1]
     out = torch.empty(max(moe_mxfp8_packed_scale_bytes(rows, K), 16), dtype=torch.uint8, device=s.device)
-    _check("moe_mxfp8_pack_scales", lib().moe_mxfp8_pack_scales(_ptr(s), rows, K, _ptr(out), _stream()))
+    _check("moe_mxfp8_pack_scales", lib().moe_mxfp8_pack_scales(_ptr(s), rows, K, _ptr(out), _stream("s", s)))
     return out
 
 
@@ -316,7 +332,8 @@ def moe_fp8_block_pack_weights(w):
     w = _codes(_cuda(w, None, "w"))
     E, N, K = w.shape
     packed = torch.empty(E, N // 128, K // 128, 128, 128, dtype=torch.uint8, device=w.device)
-    _check("moe_fp8_block_pack_weights", lib().moe_fp8_block_pack_weights(_ptr(w), E, N, K, _ptr(packed), _stream()))
+    _check("moe_fp8_block_pack_weights",
+           lib().moe_fp8_block_pack_weights(_ptr(w), E, N, K, _ptr(packed), _stream("w", w)))
     return packed
 
 
@@ -331,7 +348,7 @@ def moe_nvfp4_quant_weight(w):
     sf = torch.empty(E, N, K // 16, dtype=torch.uint8, device=w.device)
     gs = torch.empty(E, dtype=torch.float32, device=w.device)
     _check("moe_nvfp4_quant_weight",
-           lib().moe_nvfp4_quant_weight(_ptr(w), E, N, K, _ptr(q), _ptr(sf), _ptr(gs), _stream()))
+           lib().moe_nvfp4_quant_weight(_ptr(w), E, N, K, _ptr(q), _ptr(sf), _ptr(gs), _stream("w", w)))
     return q, sf, gs
 
 
@@ -346,7 +363,8 @@ def moe_nvfp4_pack_weights(q, block_scale):
         raise ValueError("block_scale must be [E, N, K/16]")
     packed = torch.empty(E, N // 16, K // 128, NVFP4_UNIT_BYTES, dtype=torch.uint8, device=q.device)
     _check("moe_nvfp4_pack_weights",
-           lib().moe_nvfp4_pack_weights(_ptr(q), _ptr(block_scale), E, N, K, _ptr(packed), _stream()))
+           lib().moe_nvfp4_pack_weights(_ptr(q), _ptr(block_scale), E, N, K, _ptr(packed),
+                                        _stream("q block_scale", q, block_scale)))
     return packed
 
 
@@ -377,7 +395,7 @@ def fp8_block_grouped_gemm(A, a_scale, a_scale_strides, B, b_scale, tile_expert,
     rc = lib().fp8_block_grouped_gemm(_ptr(A), _ptr(a_scale), int(a_scale_strides[0]), int(a_scale_strides[1]),
                                       A.shape[0], _ptr(B), _ptr(b_scale), N, K, E, _ptr(tile_expert),
                                       _ptr(tile_row0), _ptr(num_tiles), tile_expert.numel(), ctypes.byref(ep),
-                                      _stream())
+                                      _stream("A B", A, B))
     _check("fp8_block_grouped_gemm", rc)
 
 
@@ -388,7 +406,7 @@ def moe_unpermute_sum(y, pos, T, topk, out=None):
     H = y.shape[1]
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=y.device)
-    rc = lib().moe_unpermute_sum(_ptr(y), y.shape[0], _ptr(pos), T, topk, H, _ptr(out), _stream())
+    rc = lib().moe_unpermute_sum(_ptr(y), y.shape[0], _ptr(pos), T, topk, H, _ptr(out), _stream("y pos", y, pos))
     _check("moe_unpermute_sum", rc)
     return out
 
@@ -400,7 +418,7 @@ def moe_combine_pairs(y, pos, T, topk, out=None):
     H = y.shape[1]
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=y.device)
-    rc = lib().moe_combine_pairs(_ptr(y), _ptr(pos), T, topk, H, _ptr(out), _stream())
+    rc = lib().moe_combine_pairs(_ptr(y), _ptr(pos), T, topk, H, _ptr(out), _stream("y pos", y, pos))
     _check("moe_combine_pairs", rc)
     return out
 
@@ -494,7 +512,9 @@ def moe_fp8_block_forward(hidden, router_logits, w13, w13_scale, w2, w2_scale, t
     rc = lib().moe_fp8_block_forward_ex(_ptr(hidden), _ptr(router_logits), _ptr(w13), _ptr(w13_scale), _ptr(w2),
                                         _ptr(w2_scale), T, H, I, E, topk, int(bool(renormalize)),
                                         ctypes.byref(rp) if rp else None, ctypes.byref(opts), _ptr(workspace),
-                                        workspace.numel(), _ptr(out), _stream(), arr)
+                                        workspace.numel(), _ptr(out),
+                                        _stream("hidden router_logits w13 w13_scale w2 w2_scale", hidden,
+                                                router_logits, w13, w13_scale, w2, w2_scale), arr)
     _check("moe_fp8_block_forward", rc)
     return out
 
@@ -536,7 +556,8 @@ def moe_fp8_block_forward_masked(hidden, counts, w13, w13_scale, w2, w2_scale, o
     rc = lib().moe_fp8_block_forward_masked(_ptr(hidden), _ptr(counts), _ptr(w13), _ptr(w13_scale), _ptr(w2),
                                             _ptr(w2_scale), E, M, H, I, ctypes.byref(_ForwardOptions(layout,
                                             SCALE_FMT[scale_fmt], 0)), _ptr(workspace), workspace.numel(),
-                                            _ptr(out), _stream())
+                                            _ptr(out), _stream("hidden counts w13 w13_scale w2 w2_scale", hidden,
+                                                               counts, w13, w13_scale, w2, w2_scale))
     _check("moe_fp8_block_forward_masked", rc)
     return out
 
@@ -616,6 +637,7 @@ def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
     P = T * k
     L = lib()
     wsb = L.moe_dispatch_workspace_size(T, k, num_experts)
+    stream = _stream("x topk_ids", x, topk_ids)
     ws = _vector(wsb, torch.uint8) if wsb else None
     rows = _matrix(P, H, x.dtype)
     offsets = _vector(max(num_experts, 0) + 1, torch.int32)
@@ -623,7 +645,7 @@ def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
     pos = _matrix(T, k, torch.int32)
     rc = L.moe_dispatch(x.data_ptr(), ld, code, topk_ids.data_ptr(), T, k, num_experts, H, rows.data_ptr(),
                         offsets.data_ptr(), pair_ids.data_ptr(), pos.data_ptr(), None if ws is None else ws.data_ptr(),
-                        wsb, _stream())
+                        wsb, stream)
     _check("moe_dispatch", rc)
     return Dispatch(rows, offsets, pair_ids, pos)
 
@@ -640,9 +662,10 @@ def moe_dispatch_backward(drows, pos):
     code, ld = _rows(drows, "drows")
     T, k = _pos(pos)
     n, H = drows.shape
+    stream = _stream("drows pos", drows, pos)
     dx = _matrix(T, H, drows.dtype)
     _check("moe_dispatch_backward", lib().moe_dispatch_backward(drows.data_ptr(), ld, code, pos.data_ptr(), T, k, H, n,
-                                                                dx.data_ptr(), _stream()))
+                                                                dx.data_ptr(), stream))
     return dx
 
 
@@ -654,10 +677,11 @@ def moe_combine(y, pos, weights=None):
     if weights is not None:
         _dense(weights, "weights", torch.float32, (T, k))
     n, H = y.shape
+    stream = _stream("y pos weights", y, pos, weights)
     out = _matrix(T, H, y.dtype)
     _check("moe_combine", lib().moe_combine(y.data_ptr(), ld, code, pos.data_ptr(),
                                             None if weights is None else weights.data_ptr(), T, k, H, n,
-                                            out.data_ptr(), _stream()))
+                                            out.data_ptr(), stream))
     return out
 
 
@@ -670,11 +694,12 @@ def moe_combine_backward(dout, y, pos, pair_ids, weights=None):
     _dense(pair_ids, "pair_ids", torch.int32, (n,))
     if weights is not None:
         _dense(weights, "weights", torch.float32, (T, k))
+    stream = _stream("dout y pos pair_ids weights", dout, y, pos, pair_ids, weights)
     dy = _matrix(n, H, y.dtype)
     dw = _matrix(T, k, torch.float32)
     rc = lib().moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, pos.data_ptr(), pair_ids.data_ptr(),
                                     None if weights is None else weights.data_ptr(), T, k, H, n, dy.data_ptr(),
-                                    dw.data_ptr(), _stream())
+                                    dw.data_ptr(), stream)
     _check("moe_combine_backward", rc)
     return dy, dw
 
@@ -702,10 +727,11 @@ def moe_pre_norm(x, weight, eps=1e-6, weight_offset=0.0):
     code, ld = _rows(x, "x")
     T, H = x.shape
     wcode = _norm_weight(weight, H, "weight")
+    stream = _stream("x weight", x, weight)
     h = _matrix(T, H, x.dtype)
     rstd = _vector(T, torch.float32)
     _check("moe_pre_norm", lib().moe_pre_norm(x.data_ptr(), ld, code, weight.data_ptr(), wcode, weight_offset, eps, T,
-                                              H, h.data_ptr(), rstd.data_ptr(), _stream()))
+                                              H, h.data_ptr(), rstd.data_ptr(), stream))
     return h, rstd
 
 
@@ -726,12 +752,13 @@ def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0
     if dresidual is not None:
         _, ldr = _rows(dresidual, "dresidual", x, (T, H))
         dres = dresidual.data_ptr()
+    stream = _stream("dh x weight rstd dresidual", dh, x, weight, rstd, dresidual)
     dx = _matrix(T, H, x.dtype)
     dw = _vector(H, torch.float32)
     ws, wsb = _norm_workspace(T, H)
     rc = lib().moe_pre_norm_backward(dh.data_ptr(), ldd, x.data_ptr(), ldx, code, weight.data_ptr(), wcode, weight_offset,
                                      rstd.data_ptr(), dres, ldr, T, H, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb,
-                                     _stream())
+                                     stream)
     _check("moe_pre_norm_backward", rc)
     return dx, dw
 
@@ -794,6 +821,7 @@ def moe_post_norm(y, residual, weight, gate=None, gate_kind="none", gate_sigmoid
     _, ldr = _rows(residual, "residual", y, (T, H))
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, eps, weight_offset,
                             next_weight)
+    stream = _stream("y residual weight gate next_weight", y, residual, weight, gate, next_weight)
     r = PostNorm(_matrix(T, H, y.dtype),
                  _vector(T, torch.float32))
     h2 = r2 = None
@@ -801,7 +829,7 @@ def moe_post_norm(y, residual, weight, gate=None, gate_kind="none", gate_sigmoid
         r.next_h, r.next_rstd = _matrix(T, H, y.dtype), _vector(T, torch.float32)
         h2, r2 = r.next_h.data_ptr(), r.next_rstd.data_ptr()
     _check("moe_post_norm", lib().moe_post_norm(y.data_ptr(), ldy, residual.data_ptr(), ldr, code, ctypes.byref(prm), T,
-                                                H, r.out.data_ptr(), r.rstd.data_ptr(), h2, r2, _stream()))
+                                                H, r.out.data_ptr(), r.rstd.data_ptr(), h2, r2, stream))
     return r
 
 
@@ -814,6 +842,7 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     _, ldo = _rows(dout, "dout", y, (T, H))
     _dense(rstd, "rstd", torch.float32, (T,))
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, 0.0, weight_offset)
+    stream = _stream("dout y weight rstd gate", dout, y, weight, rstd, gate)
     dy = _matrix(T, H, y.dtype)
     dres = _matrix(T, H, y.dtype) if residual_grad else None
     dw = _vector(H, torch.float32)
@@ -823,7 +852,7 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     ws, wsb = _norm_workspace(T, H)
     rc = lib().moe_post_norm_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, ctypes.byref(prm),
                                       rstd.data_ptr(), T, H, dy.data_ptr(), None if dres is None else dres.data_ptr(),
-                                      None if dg is None else dg.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb, _stream())
+                                      None if dg is None else dg.data_ptr(), dw.data_ptr(), ws.data_ptr(), wsb, stream)
     _check("moe_post_norm_backward", rc)
     return PostNormGrads(dy, dw, dres, dg)
 
@@ -843,33 +872,30 @@ def _expert_weights(w, like):
     return w.shape
 
 
-def _expert_gemm(a, w, expert_offsets, epilogue, out, gate_up):
-    E, N, K = w.shape
+def _expert_gemm(a, w, expert_offsets, epilogue, save_gate_up=False):
+    E, N, K = _expert_weights(w, a)
     code, ld = _expert_operands(a, E, expert_offsets, "a")
     if a.shape[1] != K:
         raise ValueError(f"a must have {K} columns, got {a.shape[1]}")
+    stream = _stream("a w expert_offsets", a, w, expert_offsets)
+    out = _matrix(a.shape[0], N // 2 if epilogue else N, a.dtype)
+    gate_up = _matrix(a.shape[0], N, a.dtype) if save_gate_up else None
     rc = lib().moe_expert_gemm(a.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), a.shape[0], E, N, K,
-                               epilogue, out.data_ptr(), None if gate_up is None else gate_up.data_ptr(), _stream())
+                               epilogue, out.data_ptr(), None if gate_up is None else gate_up.data_ptr(), stream)
     _check("moe_expert_gemm", rc)
+    return out, gate_up
 
 
 def moe_expert_gemm(a, w, expert_offsets):
     """The experts' product over rows sorted by expert: out[r] = a[r] @ w[e]^T for the rows
     [expert_offsets[e], expert_offsets[e+1]) of a [rows, K]; w [E, N, K]; bf16 or fp16.  Rows of no expert are zero."""
-    _, N, _ = _expert_weights(w, a)
-    out = _matrix(a.shape[0], N, a.dtype)
-    _expert_gemm(a, w, expert_offsets, 0, out, None)
-    return out
+    return _expert_gemm(a, w, expert_offsets, 0)[0]
 
 
 def moe_expert_gemm_silu_mul(a, w, expert_offsets, save_gate_up=True):
     """The first product with its activation: (h [rows, N/2] = silu(gate) * up, gate_up [rows, N] = the
     product itself, which the gradient needs; None with save_gate_up=False).  w [E, N, K]: gate rows, then up."""
-    _, N, _ = _expert_weights(w, a)
-    h = _matrix(a.shape[0], N // 2, a.dtype)
-    gu = _matrix(a.shape[0], N, a.dtype) if save_gate_up else None
-    _expert_gemm(a, w, expert_offsets, 1, h, gu)
-    return h, gu
+    return _expert_gemm(a, w, expert_offsets, 1, save_gate_up)
 
 
 def moe_expert_gemm_dgrad(dc, w, expert_offsets, gate_up=None):
@@ -884,9 +910,10 @@ def moe_expert_gemm_dgrad(dc, w, expert_offsets, gate_up=None):
     if gate_up is not None:
         _, ldgu = _rows(gate_up, "gate_up", dc, (n, 2 * K))
         gp = gate_up.data_ptr()
+    stream = _stream("dc w expert_offsets gate_up", dc, w, expert_offsets, gate_up)
     out = _matrix(n, K if gate_up is None else 2 * K, dc.dtype)
     rc = lib().moe_expert_gemm_dgrad(dc.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), n, E, N, K, gp,
-                                     ldgu, out.data_ptr(), _stream())
+                                     ldgu, out.data_ptr(), stream)
     _check("moe_expert_gemm_dgrad", rc)
     return out
 
@@ -903,9 +930,10 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
         raise ValueError("dc and a must have the same rows")
     n, N = dc.shape
     K = a.shape[1]
+    stream = _stream("dc a expert_offsets", dc, a, expert_offsets)
     dw = _empty_strided((E, N, K), (N * K, K, 1), dc.dtype)
     rc = lib().moe_expert_gemm_wgrad(dc.data_ptr(), ldd, a.data_ptr(), lda, code, expert_offsets.data_ptr(), n, E, N, K,
-                                     dw.data_ptr(), _stream())
+                                     dw.data_ptr(), stream)
     _check("moe_expert_gemm_wgrad", rc)
     return dw
 
@@ -922,12 +950,16 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     if len(out) != len(grads):
         raise ValueError("out must hold one tensor per gradient")
     n = len(grads)
-    ptrs, sizes, codes = [], [], []
+    ptrs, sizes, codes, device = [], [], [], None
     for i, g in enumerate(grads):
         code = DTYPE.get(g.dtype)
         if code is None or not g.is_cuda or not g.is_contiguous():
             _typed(g, f"grads[{i}]")
             raise ValueError(f"grads[{i}] must be contiguous")
+        if device is None:
+            device = _device()
+        if g.get_device() != device:
+            raise ValueError(f"grads[{i}] is on {g.device}, but the current device is cuda:{device}")
         ptrs.append(g.data_ptr())
         sizes.append(g.numel())
         codes.append(code)
@@ -935,8 +967,8 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     if out is not grads:
         outs = []
         for i, (g, o) in enumerate(zip(grads, out)):
-            if o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
-                raise ValueError(f"out[{i}] must be a contiguous CUDA tensor like grads[{i}]")
+            if o.dtype != g.dtype or o.shape != g.shape or o.get_device() != device or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be a contiguous CUDA tensor like grads[{i}], on its device")
             outs.append(o.data_ptr())
     L = lib()
     wsb = L.moe_clip_grads_workspace_size(n)

@@ -336,3 +336,11 @@ def test_rows_between_sixteen_byte_boundaries(T, H, dtype):
         want, (ww, size) = combine_backward_ref(dout, bad, d.pos, w)
         check(dy, want, name="dy")
         check(dw, ww, size, H, "dweights")
+
+
+def test_the_current_stream_is_torchs():
+    from block_fp8_mixture_topk_gb300 import ops
+    x = torch.zeros(1, device="cuda")
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            assert ops._stream("x", x) == torch.cuda.current_stream().cuda_stream == s.cuda_stream

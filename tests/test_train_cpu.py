@@ -1,5 +1,7 @@
 """The training operators' refusals: argument errors are found on the host, before any device call."""
 import ctypes
+import importlib.util
+import sys
 
 import pytest
 import torch
@@ -252,3 +254,113 @@ def test_post_norm_of_no_rows_needs_no_gate(kind):
     assert post_norm(dict(gate=0, gate_kind=2), T=0) == INVALID
     assert post_norm_backward(dict(gate=0, gate_kind=2), T=0) == INVALID
     assert post_norm_backward(dict(gate=0, gate_kind=0), T=0) == INVALID    # a gradient for no gate
+
+
+class OnDevice:
+    """What the binding asks of a dense CUDA tensor before it launches."""
+    is_cuda = True
+    requires_grad = False
+
+    def __init__(self, dtype, *shape, device=0):
+        self.dtype, self.shape, self.device = dtype, shape, torch.device("cuda", device)
+
+    def get_device(self):
+        return self.device.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        s = [1]
+        for n in self.shape[:0:-1]:
+            s.insert(0, s[0] * n)
+        return tuple(s) if i is None else s[i]
+
+    def numel(self):
+        return int(torch.Size(self.shape).numel())
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+
+def device_calls():
+    """(function, keyword operands) of every training operator, each operand in order of shape and type."""
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    x, rows, vec, t = (bf, 4, 16), (bf, 8, 16), (f32, 16), (f32, 4)
+    pos, offs, w, dc, gu = (i32, 4, 2), (i32, 4), (bf, 3, 32, 16), (bf, 8, 32), (bf, 8, 32)
+    return [
+        (moe.moe_dispatch, dict(x=x, topk_ids=pos), dict(num_experts=3)),
+        (moe.moe_dispatch_backward, dict(drows=rows, pos=pos), {}),
+        (moe.moe_combine, dict(y=rows, pos=pos, weights=(f32, 4, 2)), {}),
+        (moe.moe_combine_backward, dict(dout=x, y=rows, pos=pos, pair_ids=(i32, 8), weights=(f32, 4, 2)), {}),
+        (moe.moe_pre_norm, dict(x=x, weight=vec), {}),
+        (moe.moe_pre_norm_backward, dict(dh=x, x=x, weight=vec, rstd=t, dresidual=x), {}),
+        (moe.moe_post_norm, dict(y=x, residual=x, weight=vec, gate=(bf, 4), next_weight=vec), dict(gate_kind="token")),
+        (moe.moe_post_norm_backward, dict(dout=x, y=x, weight=vec, rstd=t, gate=x), dict(gate_kind="full")),
+        (moe.moe_expert_gemm, dict(a=rows, w=w, expert_offsets=offs), {}),
+        (moe.moe_expert_gemm_silu_mul, dict(a=rows, w=w, expert_offsets=offs), {}),
+        (moe.moe_expert_gemm_dgrad, dict(dc=dc, w=(bf, 3, 32, 16), expert_offsets=offs, gate_up=gu), {}),
+        (moe.moe_expert_gemm_wgrad, dict(dc=dc, a=rows, expert_offsets=offs), {}),
+    ]
+
+
+class Launched(Exception):
+    pass
+
+
+@pytest.fixture
+def no_launch(monkeypatch):
+    """Device 0 is current; a call that gets as far as its results' memory stops there."""
+    def stop(*_):
+        raise Launched
+    monkeypatch.setattr(ops, "_device", lambda: 0)
+    monkeypatch.setattr(ops, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(ops, "_empty_strided", stop)
+
+
+@pytest.mark.parametrize("f,operands,other", device_calls(), ids=lambda v: getattr(v, "__name__", ""))
+def test_operands_on_another_device_are_refused(f, operands, other, no_launch):
+    make = lambda bad=None: {k: OnDevice(*v, device=int(k == bad)) for k, v in operands.items()}  # noqa: E731
+    with pytest.raises(Launched):
+        f(**make(), **other)
+    for name in operands:
+        with pytest.raises(ValueError, match=f"{name}.* is on cuda:1, but the current device is cuda:0"):
+            f(**make(name), **other)
+
+
+def test_gradients_on_another_device_are_refused(no_launch):
+    at = lambda d: OnDevice(torch.float32, 5, device=d)  # noqa: E731
+    with pytest.raises(Launched):
+        moe.moe_clip_grads([at(0), at(0)], 1.0, out=[at(0), at(0)])
+    with pytest.raises(ValueError, match=r"grads\[1\] is on cuda:1"):
+        moe.moe_clip_grads([at(0), at(1)], 1.0)
+    with pytest.raises(ValueError, match=r"grads\[0\] is on cuda:1"):
+        moe.moe_clip_grads([at(1), at(1)], 1.0)
+    with pytest.raises(ValueError, match=r"out\[1\] .* on its device"):
+        moe.moe_clip_grads([at(0), at(0)], 1.0, out=[at(0), at(1)])
+
+
+def test_layer_operands_on_another_device_are_refused(no_launch):
+    y, pos = (torch.float32, 8, 16), (torch.int32, 8)
+    out = OnDevice(torch.bfloat16, 4, 16)
+    for bad in "y", "pos":
+        with pytest.raises(ValueError, match=f"{bad} is on cuda:1"):
+            moe.moe_unpermute_sum(OnDevice(*y, device=int(bad == "y")), OnDevice(*pos, device=int(bad == "pos")), 4, 2, out)
+
+
+def test_binding_without_torchs_private_functions(monkeypatch):
+    """Where torch lacks the quick forms, the public ones stand in."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location(ops.__name__ + "_public", ops.__file__)
+    public = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(sys.modules, spec.name, public)
+    spec.loader.exec_module(public)
+
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
+    assert public._device is torch.cuda.current_device and public._raw_stream(0) == 77
