@@ -17,6 +17,9 @@
 // tensors 9.5 us on the device, both launches' latency.  With vectors through registers the large case took
 // 662 us; more CTAs per SM or more vectors per thread did not change that.
 #include <math.h>
+#include <stdlib.h>
+
+#include <algorithm>
 
 #include "train.cuh"
 
@@ -381,6 +384,37 @@ cudaError_t clip_launches(const ClipCall& c) {
     return e;
 }
 
+// Whether no result shares memory with another result or with another tensor's gradient (their chunks run side by
+// side, in no order).  MOE_OK, MOE_ERR_INVALID_ARG, or MOE_ERR_CUDA where the host has no memory for the check.
+int check_apart(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* dtype, int n) {
+    struct Span {
+        uintptr_t begin, end;
+        bool written;
+    };
+    constexpr int kOnStack = 256;
+    Span few[kOnStack];
+    Span* all = n <= kOnStack / 2 ? few : static_cast<Span*>(malloc(sizeof(Span) * 2 * static_cast<size_t>(n)));
+    if (!all) return MOE_ERR_CUDA;
+    int m = 0;
+    for (int i = 0; i < n; ++i) {
+        const uintptr_t bytes = static_cast<uintptr_t>(numel[i]) * dtype_bytes(dtype[i]);
+        if (bytes == 0) continue;
+        all[m++] = {address(out[i]), address(out[i]) + bytes, true};
+        if (grads[i] != out[i]) all[m++] = {address(grads[i]), address(grads[i]) + bytes, false};
+    }
+    const auto before = [](const Span& a, const Span& b) { return a.begin < b.begin; };
+    if (!std::is_sorted(all, all + m, before)) std::sort(all, all + m, before);
+    uintptr_t any = 0, written = 0;   // where the spans so far, and those of results, end
+    bool apart = true;
+    for (int i = 0; i < m && apart; ++i) {
+        apart = all[i].begin >= (all[i].written ? any : written);
+        any = std::max(any, all[i].end);
+        if (all[i].written) written = std::max(written, all[i].end);
+    }
+    if (all != few) free(all);
+    return apart ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
 template <int N>
 cudaError_t clip_init() {
     cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
@@ -428,11 +462,12 @@ int moe_clip_grads(const void* const* grads, void* const* out, const int64_t* nu
         if (numel[i] > 0 && grads[i] != out[i]) all_in_place = 0;
         if (numel[i] > 0 && ((address(grads[i]) ^ address(out[i])) & 15)) apart = true;
     }
+    int rc = check_apart(grads, out, numel, dtype, n);
+    if (rc != MOE_OK) return rc;
     if (workspace_bytes < moe_clip_grads_workspace_size(n)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!workspace || !on_element(address(workspace), 8)) return MOE_ERR_INVALID_ARG;
     uint32_t* status = nullptr;
-    const int rc = device_status_word(&status);
-    if (rc != MOE_OK) return rc;
+    if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     const ClipCall c = {grads, out, numel, dtype, n, norm_kind == MOE_NORM_INF ? 1 : 0, max_norm, eps, total_norm,
                         static_cast<double*>(workspace), all_in_place, apart, status, static_cast<cudaStream_t>(stream)};
     return cuda_status(n <= 32 ? clip_launches<32>(c) : n <= 128 ? clip_launches<128>(c)

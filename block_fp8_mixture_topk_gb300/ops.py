@@ -941,7 +941,7 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
 def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     """Global norm of a list of contiguous gradient tensors (bf16, fp16, fp32, in any mix) and their
     clipping by min(1, max_norm / (norm + eps)): in place, or into the list `out` (same shapes and
-    types).  norm_type 2 or inf.  Returns the norm before clipping, fp32, on the device."""
+    types), none of which may share memory with another result or gradient.  norm_type 2 or inf.  Returns the norm before clipping, fp32, on the device."""
     grads = list(grads)
     out = grads if out is None else list(out)
     kind = {2.0: 0, float("inf"): 1}.get(float(norm_type))
@@ -950,16 +950,14 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     if len(out) != len(grads):
         raise ValueError("out must hold one tensor per gradient")
     n = len(grads)
-    ptrs, sizes, codes, device = [], [], [], None
+    ptrs, sizes, codes = [], [], []
+    device = _device() if n and grads[0].is_cuda else None
     for i, g in enumerate(grads):
         code = DTYPE.get(g.dtype)
-        if code is None or not g.is_cuda or not g.is_contiguous():
+        if code is None or g.get_device() != device or not g.is_contiguous():
             _typed(g, f"grads[{i}]")
+            _stream(f"grads[{i}]", g)
             raise ValueError(f"grads[{i}] must be contiguous")
-        if device is None:
-            device = _device()
-        if g.get_device() != device:
-            raise ValueError(f"grads[{i}] is on {g.device}, but the current device is cuda:{device}")
         ptrs.append(g.data_ptr())
         sizes.append(g.numel())
         codes.append(code)

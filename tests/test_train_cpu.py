@@ -364,3 +364,27 @@ def test_binding_without_torchs_private_functions(monkeypatch):
         cuda_stream = 77
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
     assert public._device is torch.cuda.current_device and public._raw_stream(0) == 77
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(grads=(0x10000, 0x10000)), INVALID),                                 # a tensor given twice, in place
+    (dict(grads=(0x10000, 0x10004), dtype=(0, 0)), INVALID),                   # its second half beside it
+    (dict(grads=(0x10004, 0x10000), dtype=(0, 0), numel=(9, 3)), INVALID),
+    (dict(out=(0x20000, 0x10000)), INVALID),                                   # results in each other's gradients
+    (dict(out=(0x30000, 0x30000)), INVALID),
+    (dict(out=(0x10004, 0x40000)), INVALID),                                   # a result in its own, moved
+    (dict(grads=(0x10000, 0x10000), out=(0x10000, 0x30000), dtype=(0, 0)), INVALID),   # read and written in place
+    (dict(grads=(0x10000, 0x10000), out=(0x30000, 0x40000)), WORKSPACE),       # the same gradient read twice
+    (dict(grads=(0x10000, 0x10008), dtype=(0, 0)), WORKSPACE),                 # neighbours
+    (dict(grads=(0x10000, 0x10000), numel=(4, 0)), WORKSPACE),                 # nothing in the second
+])
+def test_clip_refuses_results_that_overlap(change, code):
+    assert clip(wsb=0, **change) == code
+
+
+def test_clip_refuses_overlaps_among_many():
+    n = 1000
+    for at, code in ((0x10000 + 64 * 500, INVALID), (0x10000 + 64 * n, WORKSPACE)):
+        g = (ctypes.c_void_p * n)(*[0x10000 + 64 * ((i * 7) % n) for i in range(n - 1)], at)
+        args = ((ctypes.c_int64 * n)(*[16] * n), (ctypes.c_int32 * n)(*[2] * n), n, 0, 1.0, 1e-6, P, P, 0, None)
+        assert ops.lib().moe_clip_grads(g, g, *args) == code
