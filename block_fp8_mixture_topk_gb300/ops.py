@@ -582,6 +582,13 @@ def _matrix(n, m, dtype):
     return _empty_strided((n, m), (m, 1), dtype)
 
 
+_INT_MAX = 2 ** 31 - 1   # sizes are C ints, to which ctypes cuts without a word
+
+
+def _too_large(name):
+    return ValueError(f"{name} has a size past 2^31 - 1")
+
+
 def _typed(t, name, like=None):
     """Code of t's element type; with `like`, t must have that tensor's type."""
     if not t.is_cuda:
@@ -600,6 +607,8 @@ def _rows(t, name, like=None, shape=None):
     if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
         raise ValueError(f"{name} must be {list(shape) if shape is not None else 'a matrix'}, got {list(t.shape)}")
     n, cols = t.shape
+    if n > _INT_MAX or cols > _INT_MAX:
+        raise _too_large(name)
     s0, s1 = t.stride()
     if cols > 1 and s1 != 1:
         raise ValueError(f"{name} must have adjacent columns")
@@ -634,6 +643,10 @@ def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError(f"topk_ids must be [{T}, topk], got {list(topk_ids.shape)}")
     k = topk_ids.shape[1]
+    if k > _INT_MAX:
+        raise _too_large("topk_ids")
+    if abs(num_experts) > _INT_MAX:
+        raise ValueError(f"num_experts must be an int below 2^31, got {num_experts}")
     P = T * k
     L = lib()
     wsb = L.moe_dispatch_workspace_size(T, k, num_experts)
@@ -654,7 +667,10 @@ def _pos(pos):
     _cuda(pos, torch.int32, "pos")
     if pos.dim() != 2:
         raise ValueError(f"pos must be [T, topk], got {list(pos.shape)}")
-    return pos.shape
+    T, k = pos.shape
+    if T > _INT_MAX or k > _INT_MAX:
+        raise _too_large("pos")
+    return T, k
 
 
 def moe_dispatch_backward(drows, pos):
@@ -869,7 +885,10 @@ def _expert_weights(w, like):
     if w.dim() != 3:
         raise ValueError(f"w must be [E, N, K], got {list(w.shape)}")
     _cuda(w, like.dtype, "w")
-    return w.shape
+    E, N, K = w.shape
+    if max(E, N, K) > _INT_MAX:
+        raise _too_large("w")
+    return E, N, K
 
 
 def _expert_gemm(a, w, expert_offsets, epilogue, save_gate_up=False):

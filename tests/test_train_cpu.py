@@ -388,3 +388,25 @@ def test_clip_refuses_overlaps_among_many():
         g = (ctypes.c_void_p * n)(*[0x10000 + 64 * ((i * 7) % n) for i in range(n - 1)], at)
         args = ((ctypes.c_int64 * n)(*[16] * n), (ctypes.c_int32 * n)(*[2] * n), n, 0, 1.0, 1e-6, P, P, 0, None)
         assert ops.lib().moe_clip_grads(g, g, *args) == code
+
+
+@pytest.mark.parametrize("f,operands,other", [
+    (moe.moe_dispatch, dict(x=(torch.bfloat16, 2 ** 32 + 4, 8), topk_ids=(torch.int32, 2 ** 32 + 4, 2)), dict(num_experts=3)),
+    (moe.moe_dispatch, dict(x=(torch.bfloat16, 4, 2 ** 32 + 8), topk_ids=(torch.int32, 4, 2)), dict(num_experts=3)),
+    (moe.moe_dispatch, dict(x=(torch.bfloat16, 4, 8), topk_ids=(torch.int32, 4, 2 ** 32 + 2)), dict(num_experts=3)),
+    (moe.moe_dispatch, dict(x=(torch.bfloat16, 4, 8), topk_ids=(torch.int32, 4, 2)), dict(num_experts=2 ** 32 + 3)),
+    (moe.moe_dispatch, dict(x=(torch.bfloat16, 4, 8), topk_ids=(torch.int32, 4, 2)), dict(num_experts=3 - 2 ** 32)),
+    (moe.moe_dispatch_backward, dict(drows=(torch.bfloat16, 8, 8), pos=(torch.int32, 2 ** 32 + 4, 2)), {}),
+    (moe.moe_combine, dict(y=(torch.bfloat16, 8, 8), pos=(torch.int32, 4, 2 ** 32 + 2)), {}),
+    (moe.moe_pre_norm, dict(x=(torch.bfloat16, 2 ** 32 + 4, 8), weight=(torch.float32, 8)), {}),
+    (moe.moe_post_norm, dict(y=(torch.bfloat16, 2 ** 32 + 4, 8), residual=(torch.bfloat16, 2 ** 32 + 4, 8),
+                             weight=(torch.float32, 8)), {}),
+    (moe.moe_expert_gemm, dict(a=(torch.bfloat16, 8, 16), w=(torch.bfloat16, 3, 2 ** 32 + 8, 16),
+                               expert_offsets=(torch.int32, 4)), {}),
+    (moe.moe_expert_gemm_dgrad, dict(dc=(torch.bfloat16, 8, 16), w=(torch.bfloat16, 3, 16, 2 ** 32 + 8),
+                                     expert_offsets=(torch.int32, 4)), {}),
+], ids=lambda v: getattr(v, "__name__", ""))
+def test_sizes_past_32_bits_are_refused(f, operands, other, no_launch):
+    """The C ABI takes int sizes, to which ctypes cuts silently."""
+    with pytest.raises(ValueError, match=r"2\^31"):
+        f(**{k: OnDevice(*v) for k, v in operands.items()}, **other)
