@@ -960,7 +960,8 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
 def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     """Global norm of a list of contiguous gradient tensors (bf16, fp16, fp32, in any mix) and their
     clipping by min(1, max_norm / (norm + eps)): in place, or into the list `out` (same shapes and
-    types), none of which may share memory with another result or gradient.  norm_type 2 or inf.  Returns the norm before clipping, fp32, on the device."""
+    types), none of which may share memory with another result or gradient.  norm_type 2 or inf.
+    Returns the norm before clipping, fp32, on the device."""
     grads = list(grads)
     out = grads if out is None else list(out)
     kind = {2.0: 0, float("inf"): 1}.get(float(norm_type))
@@ -969,18 +970,15 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     if len(out) != len(grads):
         raise ValueError("out must hold one tensor per gradient")
     n = len(grads)
-    ptrs, sizes, codes = [], [], []
     device = _device() if n and grads[0].is_cuda else None
-    for i, g in enumerate(grads):
-        code = DTYPE.get(g.dtype)
-        if code is None or g.get_device() != device or not g.is_contiguous():
+    codes = [DTYPE.get(g.dtype, -1) for g in grads]
+    if n and (-1 in codes or {g.get_device() for g in grads} != {device} or not all([g.is_contiguous() for g in grads])):
+        for i, g in enumerate(grads):
             _typed(g, f"grads[{i}]")
             _stream(f"grads[{i}]", g)
-            raise ValueError(f"grads[{i}] must be contiguous")
-        ptrs.append(g.data_ptr())
-        sizes.append(g.numel())
-        codes.append(code)
-    outs = ptrs
+            if not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be contiguous")
+    outs = ptrs = [g.data_ptr() for g in grads]
     if out is not grads:
         outs = []
         for i, (g, o) in enumerate(zip(grads, out)):
@@ -991,11 +989,13 @@ def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):
     wsb = L.moe_clip_grads_workspace_size(n)
     ws = _vector(wsb, torch.uint8)
     total = _empty_strided((), (), torch.float32)
+    sizes = list(map(torch.Tensor.numel, grads))   # (half the time of as many method calls)
     table, kinds = array.array("q", ptrs + outs + sizes), array.array("i", codes)   # host arrays of the C call
     at = table.buffer_info()[0]
     rc = L.moe_clip_grads(at, at + 8 * n, at + 16 * n, kinds.buffer_info()[0], n, kind, float(max_norm), float(eps),
                           total.data_ptr(), ws.data_ptr(), wsb, _stream())
     _check("moe_clip_grads", rc)
+    torch.autograd.graph.increment_version(out)   # autograd then knows what it may have saved of them as changed
     return total
 
 

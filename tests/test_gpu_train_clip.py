@@ -148,3 +148,22 @@ def test_results_elsewhere_between_boundaries(src, dst, dtype):
     for t, o, b, n in zip(grads, out, around, sizes):
         check(o, t.double() * (total / 2 / (total + 1e-6)), roundings=NORM + 4, name="clipped")
         assert (b[:dst] == 5).all() and (b[dst + n:] == 5).all()
+
+
+def test_autograd_sees_that_the_results_changed():
+    """What autograd saved of a clipped tensor is no longer what it saved: backward() refuses, as after torch's own
+    in-place operations, in place of a wrong gradient."""
+    other = torch.ones(7, device="cuda")
+    for out in (None, "out"):
+        w = torch.ones(7, device="cuda", requires_grad=True)
+        saved = w.exp()
+        grads = [other.clone(), saved.detach()] if out is None else [other.clone(), other.clone()]
+        before = [g._version for g in grads]
+        moe.moe_clip_grads(grads, 0.5, out=None if out is None else [torch.empty_like(other), saved.detach()])
+        assert [g._version > b for g, b in zip(grads, before)] == [out is None] * 2
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.sum().backward()
+    with torch.inference_mode():
+        g = torch.ones(7, device="cuda")
+    assert moe.moe_clip_grads([g], 1.0) > 1 and g[0] < 1
+    assert moe.moe_clip_grads([], 1.0) == 0
