@@ -11,6 +11,7 @@ import ctypes
 import dataclasses
 import os
 import threading
+import warnings
 
 import torch
 
@@ -563,6 +564,8 @@ def moe_fp8_block_forward_masked(hidden, counts, w13, w13_scale, w2, w2_scale, o
 
 
 # ---- training operators (C ABI section "training") ------------------------------------------
+# They record nothing for autograd: results have no grad_fn, and the gradients are the functions named
+# *_backward, *_dgrad and *_wgrad, which the caller runs.
 
 DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -571,6 +574,20 @@ try:   # half the time of torch.empty, which counts in a step of one token
 except AttributeError:
     def _empty_strided(size, stride, dtype):
         return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
+
+def _training_stream(function, names, *operands, stacklevel=3):
+    """_stream of a training operator, with a warning where autograd would have recorded it."""
+    device = _device()
+    for t in operands:
+        if t is not None and (t.requires_grad or t.get_device() != device):
+            stream = _stream(names, *operands)
+            if torch.is_grad_enabled():
+                warnings.warn(f"{function} records nothing for autograd, so no gradient reaches its operands through "
+                              "backward(): run the gradient functions, and this one under torch.no_grad()",
+                              stacklevel=stacklevel)
+            return stream
+    return _raw_stream(device)
 
 
 def _vector(n, dtype):
@@ -650,7 +667,7 @@ def moe_dispatch(x, topk_ids, num_experts) -> Dispatch:
     P = T * k
     L = lib()
     wsb = L.moe_dispatch_workspace_size(T, k, num_experts)
-    stream = _stream("x topk_ids", x, topk_ids)
+    stream = _training_stream("moe_dispatch", "x topk_ids", x, topk_ids)
     ws = _vector(wsb, torch.uint8) if wsb else None
     rows = _matrix(P, H, x.dtype)
     offsets = _vector(max(num_experts, 0) + 1, torch.int32)
@@ -678,7 +695,7 @@ def moe_dispatch_backward(drows, pos):
     code, ld = _rows(drows, "drows")
     T, k = _pos(pos)
     n, H = drows.shape
-    stream = _stream("drows pos", drows, pos)
+    stream = _training_stream("moe_dispatch_backward", "drows pos", drows, pos)
     dx = _matrix(T, H, drows.dtype)
     _check("moe_dispatch_backward", lib().moe_dispatch_backward(drows.data_ptr(), ld, code, pos.data_ptr(), T, k, H, n,
                                                                 dx.data_ptr(), stream))
@@ -693,7 +710,7 @@ def moe_combine(y, pos, weights=None):
     if weights is not None:
         _dense(weights, "weights", torch.float32, (T, k))
     n, H = y.shape
-    stream = _stream("y pos weights", y, pos, weights)
+    stream = _training_stream("moe_combine", "y pos weights", y, pos, weights)
     out = _matrix(T, H, y.dtype)
     _check("moe_combine", lib().moe_combine(y.data_ptr(), ld, code, pos.data_ptr(),
                                             None if weights is None else weights.data_ptr(), T, k, H, n,
@@ -710,7 +727,7 @@ def moe_combine_backward(dout, y, pos, pair_ids, weights=None):
     _dense(pair_ids, "pair_ids", torch.int32, (n,))
     if weights is not None:
         _dense(weights, "weights", torch.float32, (T, k))
-    stream = _stream("dout y pos pair_ids weights", dout, y, pos, pair_ids, weights)
+    stream = _training_stream("moe_combine_backward", "dout y pos pair_ids weights", dout, y, pos, pair_ids, weights)
     dy = _matrix(n, H, y.dtype)
     dw = _matrix(T, k, torch.float32)
     rc = lib().moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, code, pos.data_ptr(), pair_ids.data_ptr(),
@@ -743,7 +760,7 @@ def moe_pre_norm(x, weight, eps=1e-6, weight_offset=0.0):
     code, ld = _rows(x, "x")
     T, H = x.shape
     wcode = _norm_weight(weight, H, "weight")
-    stream = _stream("x weight", x, weight)
+    stream = _training_stream("moe_pre_norm", "x weight", x, weight)
     h = _matrix(T, H, x.dtype)
     rstd = _vector(T, torch.float32)
     _check("moe_pre_norm", lib().moe_pre_norm(x.data_ptr(), ld, code, weight.data_ptr(), wcode, weight_offset, eps, T,
@@ -768,7 +785,7 @@ def moe_pre_norm_backward(dh, x, weight, rstd, dresidual=None, weight_offset=0.0
     if dresidual is not None:
         _, ldr = _rows(dresidual, "dresidual", x, (T, H))
         dres = dresidual.data_ptr()
-    stream = _stream("dh x weight rstd dresidual", dh, x, weight, rstd, dresidual)
+    stream = _training_stream("moe_pre_norm_backward", "dh x weight rstd dresidual", dh, x, weight, rstd, dresidual)
     dx = _matrix(T, H, x.dtype)
     dw = _vector(H, torch.float32)
     ws, wsb = _norm_workspace(T, H)
@@ -837,7 +854,7 @@ def moe_post_norm(y, residual, weight, gate=None, gate_kind="none", gate_sigmoid
     _, ldr = _rows(residual, "residual", y, (T, H))
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, eps, weight_offset,
                             next_weight)
-    stream = _stream("y residual weight gate next_weight", y, residual, weight, gate, next_weight)
+    stream = _training_stream("moe_post_norm", "y residual weight gate next_weight", y, residual, weight, gate, next_weight)
     r = PostNorm(_matrix(T, H, y.dtype),
                  _vector(T, torch.float32))
     h2 = r2 = None
@@ -858,7 +875,7 @@ def moe_post_norm_backward(dout, y, weight, rstd, gate=None, gate_kind="none", g
     _, ldo = _rows(dout, "dout", y, (T, H))
     _dense(rstd, "rstd", torch.float32, (T,))
     prm = _post_norm_params(y, weight, gate, gate_kind, gate_sigmoid, residual_scale, block_scale, 0.0, weight_offset)
-    stream = _stream("dout y weight rstd gate", dout, y, weight, rstd, gate)
+    stream = _training_stream("moe_post_norm_backward", "dout y weight rstd gate", dout, y, weight, rstd, gate)
     dy = _matrix(T, H, y.dtype)
     dres = _matrix(T, H, y.dtype) if residual_grad else None
     dw = _vector(H, torch.float32)
@@ -896,7 +913,8 @@ def _expert_gemm(a, w, expert_offsets, epilogue, save_gate_up=False):
     code, ld = _expert_operands(a, E, expert_offsets, "a")
     if a.shape[1] != K:
         raise ValueError(f"a must have {K} columns, got {a.shape[1]}")
-    stream = _stream("a w expert_offsets", a, w, expert_offsets)
+    stream = _training_stream("moe_expert_gemm_silu_mul" if epilogue else "moe_expert_gemm", "a w expert_offsets", a, w,
+                              expert_offsets, stacklevel=4)
     out = _matrix(a.shape[0], N // 2 if epilogue else N, a.dtype)
     gate_up = _matrix(a.shape[0], N, a.dtype) if save_gate_up else None
     rc = lib().moe_expert_gemm(a.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), a.shape[0], E, N, K,
@@ -929,7 +947,7 @@ def moe_expert_gemm_dgrad(dc, w, expert_offsets, gate_up=None):
     if gate_up is not None:
         _, ldgu = _rows(gate_up, "gate_up", dc, (n, 2 * K))
         gp = gate_up.data_ptr()
-    stream = _stream("dc w expert_offsets gate_up", dc, w, expert_offsets, gate_up)
+    stream = _training_stream("moe_expert_gemm_dgrad", "dc w expert_offsets gate_up", dc, w, expert_offsets, gate_up)
     out = _matrix(n, K if gate_up is None else 2 * K, dc.dtype)
     rc = lib().moe_expert_gemm_dgrad(dc.data_ptr(), ld, code, w.data_ptr(), expert_offsets.data_ptr(), n, E, N, K, gp,
                                      ldgu, out.data_ptr(), stream)
@@ -949,7 +967,7 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
         raise ValueError("dc and a must have the same rows")
     n, N = dc.shape
     K = a.shape[1]
-    stream = _stream("dc a expert_offsets", dc, a, expert_offsets)
+    stream = _training_stream("moe_expert_gemm_wgrad", "dc a expert_offsets", dc, a, expert_offsets)
     dw = _empty_strided((E, N, K), (N * K, K, 1), dc.dtype)
     rc = lib().moe_expert_gemm_wgrad(dc.data_ptr(), ldd, a.data_ptr(), lda, code, expert_offsets.data_ptr(), n, E, N, K,
                                      dw.data_ptr(), stream)

@@ -2,6 +2,7 @@
 import ctypes
 import importlib.util
 import sys
+import warnings
 
 import pytest
 import torch
@@ -409,4 +410,23 @@ def test_clip_refuses_overlaps_among_many():
 def test_sizes_past_32_bits_are_refused(f, operands, other, no_launch):
     """The C ABI takes int sizes, to which ctypes cuts silently."""
     with pytest.raises(ValueError, match=r"2\^31"):
+        f(**{k: OnDevice(*v) for k, v in operands.items()}, **other)
+
+
+@pytest.mark.parametrize("f,operands,other", device_calls(), ids=lambda v: getattr(v, "__name__", ""))
+def test_operands_that_autograd_follows_draw_a_warning(f, operands, other, no_launch):
+    """The results have no grad_fn, so backward() would pass these operands by in silence."""
+    for name, (dtype, *_) in operands.items():
+        if not dtype.is_floating_point:
+            continue
+        made = {k: OnDevice(*v) for k, v in operands.items()}
+        made[name].requires_grad = True
+        with pytest.warns(UserWarning, match=f"^{f.__name__} records nothing for autograd") as seen, pytest.raises(Launched):
+            f(**made, **other)
+        assert len(seen) == 1 and seen[0].filename == __file__
+        with warnings.catch_warnings(), torch.no_grad(), pytest.raises(Launched):
+            warnings.simplefilter("error")
+            f(**made, **other)
+    with warnings.catch_warnings(), pytest.raises(Launched):
+        warnings.simplefilter("error")
         f(**{k: OnDevice(*v) for k, v in operands.items()}, **other)
