@@ -189,35 +189,7 @@ __host__ __device__ constexpr uint32_t idesc_16bit(int n, bool a_mn, bool b_mn) 
            | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(XM >> 4) << 24);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// Address of the same shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-// TMA tile loads into this CTA's shared memory whose bytes complete on `bar`, a shared::cluster
-// address that may be the other CTA's barrier (the .cta_group::2 form).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                                 uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                                 int32_t z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
+// As tma_load_2d_pair, in five dimensions.
 __device__ __forceinline__ void tma_load_5d_pair(uint32_t smem_dst, const CUtensorMap* map, int32_t x, int32_t y,
                                                  int32_t z, int32_t w, int32_t v, uint32_t bar) {
     asm volatile(
@@ -226,36 +198,6 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t smem_dst, const CUtens
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
         : "memory");
 }
-// Arrive on a barrier of either CTA of the pair (shared::cluster address).  CTA-scope release, like
-// the waits (mbar_wait): the arrivals hand over tensor memory (ordered by the tcgen05 fences around
-// the barrier) and shared-memory stages (written by TMA, completion counted on the barrier), never
-// data the arriving thread wrote itself; a cluster-scope release made every arrival of the
-// epilogue warps wait for their earlier global stores.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// All threads of both CTAs.
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// Arrive once on the barrier at this offset in each CTA of `mask` when the MMAs issued so far complete.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
-        : "memory");
-}
-
 // D (256 x N over both CTAs) (+)= A * B^T, K = 16, 16-bit operands, fp32 accumulation; issued by one
 // thread of CTA 0.
 __device__ __forceinline__ void mma_16bit_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
