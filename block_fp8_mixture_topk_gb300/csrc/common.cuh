@@ -63,17 +63,34 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The same without an acquire, for a barrier on which the other CTA of a pair arrives: what such an arrival
+// hands over is ordered by the tcgen05 fences on both sides, or is written by copies that complete on
+// the barrier.
+__device__ __forceinline__ bool mbar_test_pair(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Wait until the phase with the given parity has completed.  Returns false
 // (after setting the timeout status bit and the CTA-wide abort flag) if it did
 // not complete within kWaitLimitNs, or if another thread of the CTA already
-// aborted.  `abort_flag` points to a shared int (may be null).
+// aborted.  `abort_flag` points to a shared int (may be null).  PAIR: by mbar_test_pair.
+template <bool PAIR = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t* status) {
-    if (mbar_test(bar, parity)) return true;
+    const auto done = [&] { return PAIR ? mbar_test_pair(bar, parity) : mbar_test(bar, parity); };
+    if (done()) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t outer = 0; outer < (1u << 26); ++outer) {
         for (int i = 0; i < 32; ++i)
-            if (mbar_test(bar, parity)) return true;
+            if (done()) return true;
         if (abort_flag && *abort_flag) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) break;
     }
@@ -297,13 +314,13 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t smem_dst, const CUtens
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// Arrive on a barrier of either CTA of the pair (shared::cluster address).  CTA-scope release, like
-// the waits (mbar_wait): the arrivals hand over tensor memory (ordered by the tcgen05 fences around
-// the barrier) and shared-memory stages (written by TMA, completion counted on the barrier), never
-// data the arriving thread wrote itself; a cluster-scope release made every arrival of the
-// epilogue warps wait for their earlier global stores.
+// Arrive on a barrier of either CTA of the pair (shared::cluster address).  At cluster scope, like the waits
+// on such a barrier (mbar_wait<true>), but relaxed: the arrivals hand over tensor memory (ordered by the
+// tcgen05 fences around the barrier) and shared-memory stages (written by TMA, completion counted on the
+// barrier), never data the arriving thread wrote itself; a release at cluster scope made every
+// arrival of the epilogue warps wait for their earlier global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // All threads of both CTAs.
 __device__ __forceinline__ void cluster_barrier() {

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             const int n_bytes = small ? small * 2048 : X_TILE;
             const int32_t first = MODE == kWeights ? ctl->row0[t.e] : 0;
             for (int kb = 0; kb < t.kblocks; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status));
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status));
                 if (!ok) break;
                 const bool tail = MODE == kWeights && t.red - kb * XK < XK;
                 const uint32_t bar = tail ? smem_addr(&ctl->tail[stage]) : full0 + stage * 8;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         if (!ok && rank == 0 && lane == 0) {
             for (int s = 0; s < X_STAGES; ++s) {
                 const uint32_t n_s = (issued + X_STAGES - 1 - s) / X_STAGES;
-                if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
+                if (n_s > 0) mbar_wait<true>(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
             }
         }
     } else if (warp == 1) {
@@ -507,12 +507,12 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                 if (w >= total) continue;
                 const XItem t = uniform(item_at<MODE>(a, ctl, w, NT));
                 if (t.kblocks == 0) continue;
-                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
                 if (!ok) break;
                 const uint32_t d = tmem + buf * XN;
                 const uint32_t idesc = idesc_16bit<T>(MODE == kWeights ? XN : rows_mma(t.nrow), A_MN, B_MN);
                 for (int kb = 0; kb < t.kblocks; ++kb) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
+                    ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
                     if (!ok) break;
                     const int left = t.red - kb * XK;
                     if (MODE == kWeights && left < XK) mbar_acquire_cluster(smem_addr(&ctl->full[stage]), phase);
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                 block.fetch<T>(gq, gu_in + (row + g * 32) * a.ld_gu, a.ld_gu, t.nrow - g * 32, c0, OC);
                 block.fetch<T>(uq, gu_in + (row + g * 32) * a.ld_gu + OC, a.ld_gu, t.nrow - g * 32, c0, OC);
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
+            ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
             if (!half_ok(ok, block, &ctl->half_bad[g])) break;
             tc_fence_after();
             for (int blk = g; blk < blocks; blk += 2) {

@@ -1228,7 +1228,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int32_t sfb1 = (p.e * NBn + bcol1 / 128) * KB4;
                 for (int kb0 = 0; kb0 < KB; kb0 += P_SUB) {
                     const int nsub = KB - kb0 < P_SUB ? KB - kb0 : P_SUB;
-                    if (!mbar_wait(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status)) {
+                    if (!mbar_wait<true>(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status)) {
                         ok = false;
                         break;
                     }
@@ -1264,7 +1264,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (!ok && rank == 0) {
                 for (int s = 0; s < P_SUPER; ++s) {
                     const uint32_t n_s = (issued + P_SUPER - 1 - s) / P_SUPER;
-                    if (n_s > 0) mbar_wait(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
+                    if (n_s > 0) mbar_wait<true>(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
                 }
             }
         }
@@ -1285,7 +1285,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 bool any = false;
                 for (int j = 0; j < nsub; ++j) any = any || mx || ((kb0 + j) & 3) == 0;
                 if (any) {
-                    if (!mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status)) {
+                    if (!mbar_wait<true>(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status)) {
                         ok = false;
                         break;
                     }
@@ -1319,7 +1319,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int64_t w = cid; w < total && ok; w += ncl, ++k) {
             const PairItem p = pair_item(a, ctl, k, w, NT, rank, ntiles);
             if (!p.take || !p.ok) continue;
-            if (!mbar_wait(smem_addr(&ctl->tempty), (items & 1u) ^ 1u, abort_flag, a.status)) {
+            if (!mbar_wait<true>(smem_addr(&ctl->tempty), (items & 1u) ^ 1u, abort_flag, a.status)) {
                 ok = false;
                 break;
             }
@@ -1327,7 +1327,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t sfa_t = 0, sfb_t = 0;
             for (int kb0 = 0; kb0 < KB && ok; kb0 += P_SUB) {
                 const int nsub = KB - kb0 < P_SUB ? KB - kb0 : P_SUB;
-                if (!mbar_wait(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status)) {
+                if (!mbar_wait<true>(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
@@ -1397,7 +1397,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const bool row_real = p.live && (a.sorted_pair_ids == nullptr || a.sorted_pair_ids[grow] >= 0);
             const bool active = __any_sync(0xffffffffu, row_real);
             float acc[128];
-            if (!mbar_wait(smem_addr(&ctl->tfull), acc_iter & 1u, abort_flag, a.status)) {
+            if (!mbar_wait<true>(smem_addr(&ctl->tfull), acc_iter & 1u, abort_flag, a.status)) {
                 ok = false;
                 break;
             }
