@@ -792,9 +792,9 @@ using namespace mfp8;
 extern "C" {
 
 size_t moe_dispatch_workspace_size(int T, int topk, int E) {
-    if (T < 0 || topk < 1 || E < 1) return 0;
+    if (T < 0 || topk < 1 || topk > MOE_MAX_TOPK || E < 1 || E > MOE_MAX_EXPERTS) return 0;
     const int64_t P = static_cast<int64_t>(T) * topk;
-    if (P == 0) return 0;
+    if (P == 0 || P >= (int64_t(1) << 31)) return 0;   // (the plan counts pairs in ints)
     const DispatchPlan d = dispatch_plan(P, topk);
     return d.direct ? 0 : static_cast<size_t>(d.nch) * E * 4;
 }

@@ -517,7 +517,8 @@ int moe_fp8_block_forward_masked(const uint16_t* hidden, const int32_t* counts,
  *   pair_ids       int32 [T*topk]   pair of each row, -1 past the last row of an expert
  *   pos            int32 [T, topk]  row of each pair, -1 for a dropped pair
  *   rows           [T*topk, H]      rows[pos[t, j]] = x[t]; rows of no pair are zero
- * workspace: device scratch of moe_dispatch_workspace_size(T, topk, E) bytes (4-byte aligned).
+ * workspace: device scratch of moe_dispatch_workspace_size(T, topk, E) bytes (4-byte aligned; 0 for sizes that
+ * moe_dispatch refuses).
  * H <= MOE_MAX_HIDDEN. */
 #define MOE_MAX_HIDDEN 65536
 size_t moe_dispatch_workspace_size(int T, int topk, int E);

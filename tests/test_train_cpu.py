@@ -430,3 +430,11 @@ def test_operands_that_autograd_follows_draw_a_warning(f, operands, other, no_la
     with warnings.catch_warnings(), pytest.raises(Launched):
         warnings.simplefilter("error")
         f(**{k: OnDevice(*v) for k, v in operands.items()}, **other)
+
+
+@pytest.mark.parametrize("T,topk,E", [(152 * 65536, 65536, 8), (2 ** 31 - 1, 2 ** 31 - 1, 8), (16384, 2 ** 30, 8),
+                                      (2 ** 30, 2, 8), (300000, 33, 8), (300000, 2, 1025)])
+def test_dispatch_workspace_size_of_refused_sizes(T, topk, E):
+    """The chunks of so many pairs have no int size: it must not divide by what is left of one."""
+    assert ops.lib().moe_dispatch_workspace_size(T, topk, E) == 0
+    assert dispatch(T=T, topk=topk, E=E) == SHAPE
