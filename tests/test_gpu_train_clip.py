@@ -167,3 +167,16 @@ def test_autograd_sees_that_the_results_changed():
         g = torch.ones(7, device="cuda")
     assert moe.moe_clip_grads([g], 1.0) > 1 and g[0] < 1
     assert moe.moe_clip_grads([], 1.0) == 0
+
+
+def test_a_tensor_past_two_to_the_31_elements():
+    g = torch.Generator(device="cuda").manual_seed(9)
+    n = 2 ** 31 + 4099
+    t = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+    t[-9000:] = torch.randn(9000, generator=g, device="cuda").bfloat16()
+    end = t[-9000:].double()
+    total = math.sqrt(n - 9000 + end.square().sum().item())
+    got = moe.moe_clip_grads([t], total / 4)
+    check(got, torch.tensor(total, dtype=torch.float64), roundings=NORM, name="norm")
+    check(t[-9000:], end * (total / 4 / (total + 1e-6)), roundings=NORM + 4, name="the end")
+    assert (t[:-9000] == 0.25).all()

@@ -275,3 +275,41 @@ def test_offsets_out_of_order_are_repaired(bad):
     assert status() == 4
     for name, x, y in zip(("c", "h", "gate_up", "da", "dgate_up", "dw"), got, want):
         assert torch.equal(x, y), name
+
+
+def test_results_past_two_to_the_31_elements():
+    """Offsets that pass 32 bits in rows, weights and results: the last rows and the last expert equal those of a
+    call of their own."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rows, N, K, last = 540000, 4096, 16, 1000
+    off = torch.tensor([0, 300000, rows - last, rows], dtype=torch.int32, device="cuda")
+    end = torch.tensor([0, 0, 0, last], dtype=torch.int32, device="cuda")
+    a = torch.randn(rows, K, generator=g, device="cuda").bfloat16()
+    w = torch.randn(3, N, K, generator=g, device="cuda").bfloat16()
+    c = moe.moe_expert_gemm(a, w, off)
+    assert c.numel() > 2 ** 31 and torch.equal(c[-last:], moe.moe_expert_gemm(a[-last:], w, end))
+    da = moe.moe_expert_gemm_dgrad(c, w, off)
+    assert torch.equal(da[-last:], moe.moe_expert_gemm_dgrad(c[-last:], w, end))
+    w2 = torch.randn(3, K, N, generator=g, device="cuda").bfloat16()
+    dc = torch.randn(rows, K, generator=g, device="cuda").bfloat16()
+    gu = torch.cat([c, c.flip(0)], 1)                                    # 2^32 elements
+    dgu = moe.moe_expert_gemm_dgrad(dc, w2, off, gate_up=gu)
+    assert torch.equal(dgu[-last:], moe.moe_expert_gemm_dgrad(dc[-last:], w2, end, gate_up=gu[-last:]))
+    del c, gu, dgu
+    h, gu = moe.moe_expert_gemm_silu_mul(a, w, off)
+    h1, gu1 = moe.moe_expert_gemm_silu_mul(a[-last:], w, end)
+    assert torch.equal(h[-last:], h1) and torch.equal(gu[-last:], gu1)
+    del h, gu
+    E, N, K, n = 40, 8192, 7176, 70                                      # 2.4e9 weights
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * n
+    a, dc = (torch.randn(E * n, m, generator=g, device="cuda").bfloat16() for m in (K, N))
+    dw = moe.moe_expert_gemm_wgrad(dc, a, off)
+    one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for e in (0, E - 1):
+        at = slice(e * n, e * n + n)
+        assert torch.equal(dw[e:e + 1], moe.moe_expert_gemm_wgrad(dc[at], a[at], one))
+    b = torch.randn(E * 4, K, generator=g, device="cuda").bfloat16()     # weights that are read so far out
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * 4
+    c = moe.moe_expert_gemm(b, dw, off)
+    one = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    assert torch.equal(c[-4:], moe.moe_expert_gemm(b[-4:], dw[-1:].contiguous(), one))

@@ -351,3 +351,31 @@ def test_gradients_of_saturated_gates(T, H, dtype, kind):
     check(d.dy, rs * (t - n * m), rs * (t.abs() + n.abs() * ma), exp_error + 53 + 20, "dy")
     s = b * sig * dd * n
     check(d.dweight, s.sum(0), s.abs().sum(0), exp_error + T + 60, "dweight")
+
+
+def test_rows_past_two_to_the_31_elements():
+    """Row offsets that pass 32 bits: the last rows equal the same rows in a matrix of their own."""
+    T, H = 264000, 8200
+    g = torch.Generator(device="cuda").manual_seed(3)
+    some = [torch.randn(64, H, generator=g, device="cuda").bfloat16() for _ in range(3)]
+    x, y, gate = (s.repeat(T // 64, 1) for s in some)
+    w = torch.randn(H, generator=g, device="cuda")
+    kw = dict(gate_kind="full", gate_sigmoid=True, block_scale=0.5)
+    h, rstd = moe.moe_pre_norm(x, w)
+    h1, rstd1 = moe.moe_pre_norm(some[0].repeat(10, 1), w)
+    for at in (slice(0, 640), slice(T - 640, T)):
+        assert torch.equal(h[at], h1) and torch.equal(rstd[at], rstd1)
+    del h
+    p = moe.moe_post_norm(y, x, w, gate=gate, next_weight=w, **kw)
+    p1 = moe.moe_post_norm(some[1].repeat(10, 1), some[0].repeat(10, 1), w, gate=some[2].repeat(10, 1), next_weight=w, **kw)
+    for at in (slice(0, 640), slice(T - 640, T)):
+        assert torch.equal(p.out[at], p1.out) and torch.equal(p.next_h[at], p1.next_h)
+    del p.out, p.next_h
+    d = moe.moe_post_norm_backward(x, y, w, p.rstd, gate=gate, **kw)
+    d1 = moe.moe_post_norm_backward(some[0].repeat(10, 1), some[1].repeat(10, 1), w, p1.rstd, gate=some[2].repeat(10, 1),
+                                    **kw)
+    dx, _ = moe.moe_pre_norm_backward(d.dresidual, x, w, rstd, dresidual=d.dy)
+    dx1, _ = moe.moe_pre_norm_backward(d1.dresidual, some[0].repeat(10, 1), w, rstd1, dresidual=d1.dy)
+    for at in (slice(0, 640), slice(T - 640, T)):
+        for a, b in ((d.dy, d1.dy), (d.dresidual, d1.dresidual), (d.dgate, d1.dgate), (dx, dx1)):
+            assert torch.equal(a[at], b)
