@@ -18,13 +18,16 @@
 // per CTA and summed by a second kernel in a fixed order: no atomics, so the result does not
 // depend on the schedule.
 //
-// Measured (bf16): before and after with the next norm, 4096 x 7168: 66 us for 294 MB (0.65 of a copy; 21
-// and 43 us alone).  Both gradients of 5003 x 2880 with a sigmoid gate: 68 us for 288 MB, two launches of
+// Measured (bf16): before and after with the next norm, 4096 x 7168: 66 us for 352 MB (0.78 of a copy; 21
+// and 43 us alone).  Both gradients of 5003 x 2880 with a sigmoid gate: 69 us for 288 MB, two launches of
 // 4.7 us among them that sum the weights' partials.  One row: 6.7 us on the device.  About 4 us of
 // each launch are its first loads and last stores; the after-norm with a next norm holds its weights and the
 // stored row in registers (111, so 448 threads per SM) and is then bound by the two reductions' latency.
-// Rows of odd widths: 8000 x 4811 before and after with the next norm 102 us, 1.8 times the bytes' time; where
-// the matrices do not lie alike the vectors are joined, bound by instructions: 165 us.
+// Rows of odd widths: 8000 x 4811 before and after with the next norm 102 us, 1.5 times the bytes' time; where
+// the matrices do not lie alike the vectors are joined: 165 us, bound by instructions and, in the instances of 32
+// elements a thread, by spilled registers (3000 x 9001 before, backward: 88 us, 3.7 times the bytes' time).  So
+// are wide rows whose matrices do not fit the ring (2000 x 16384 before, backward, with a residual's gradient: 98
+// us, 2.5 times).
 #pragma once
 
 #include <atomic>
@@ -685,7 +688,8 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
             for (int e = 0; e < NP; ++e) {
                 float2 p = mul2(d.pair(e), mul2(y.pair(e), both(r)));
                 if constexpr (SIGMOID) {
-                    const float2 s = sigmoid_as<T>(gt.pair(e));
+                    const float2 v = gt.pair(e), x = make_float2(exp_minus<T>(v.x), exp_minus<T>(v.y));
+                    const float2 s = make_float2(sigmoid_of<T>(x.x), sigmoid_of<T>(x.y));
                     if constexpr (KEEP) kept[i * NP + e] = s;
                     p = mul2(p, s);
                 } else if constexpr (FULL) {
@@ -714,8 +718,9 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_backward_kernel(const 
                 const float2 n = mul2(y.pair(e), both(r));
                 float2 dw = mul2(d.pair(e), w.v[e]);
                 if constexpr (SIGMOID) {
-                    const float2 v = gt.pair(e), x = make_float2(exp_minus<T>(v.x), exp_minus<T>(v.y));
-                    float2 s;
+                    float2 v = gt.pair(e), s;
+                    if constexpr (!KEEP) asm volatile("" : "+f"(v.x), "+f"(v.y));   // again, not kept in (spilled) registers
+                    const float2 x = make_float2(exp_minus<T>(v.x), exp_minus<T>(v.y));
                     if constexpr (KEEP) s = kept[i * NP + e];
                     else s = make_float2(sigmoid_of<T>(x.x), sigmoid_of<T>(x.y));
                     const float2 slope = make_float2(slope_of(x.x, s.x), slope_of(x.y, s.y));
@@ -757,8 +762,8 @@ constexpr int kRingMostDepth = 4;
 // At most: vectors are 8 or 4 elements.
 inline int ring_weight_bytes(int H, bool shift) { return shift ? ring_vectors<true>(H, 8) * 32 : H * 4; }
 
-// What an instance remembers per device: that its shared-memory limit is set, and the CTAs per SM by
-// the warps of a CTA.
+// What an instance remembers: the devices on which its shared-memory limit is set, and the CTAs per SM by the
+// warps of a CTA (the same on every device that the library runs on).
 struct NormInstance {
     std::atomic<uint64_t> limit{0};
     std::atomic<int> occupancy[kNormThreads / 32 + 1] = {};
@@ -863,12 +868,15 @@ inline bool alike(const NormArgs& a, int gate, int es) {
 
 // Where the rows come from, by their alignment (wide: 16-byte addresses and strides), number and width:
 //   fewer rows than twice the SMs: registers, 16 elements per thread where the row then fits a CTA's
-//     threads (more threads on each row)
+//     threads (more threads on each row).  (bf16 rows of 7168, after with the next norm: 303 of them 7.5 us, 7.9
+//     from the ring; 608 of them 12.0 and 11.1.  Rows of 2048: 1024 of them 7.0 and 7.3, 2048 of them 10.5 either way.)
 //   else wide rows, and others whose matrices lie alike (not few: 8 CTAs need rows): the ring, 32 elements per thread (8000 bf16 rows
 //     of 4811 before and after with the next norm: 102 against 165 us from registers); registers where
 //     the weights and two rows do not fit a CTA's shared memory
 //   else registers, 16 elements per thread up to 4096 columns, else 32 (8000 rows of 4811: 212 and 165 us;
 //     of 1569: 57 and 67)
+// The register instances of 32 elements do not fit 128 registers with two or three matrices: the compiler spills
+// 100 to 1400 bytes of them a thread (the others at most 32).
 template <class T>
 cudaError_t launch_norm_type(const NormArgs& a, int which, int gate, bool wide, int sms, cudaStream_t stream,
                              int* ctas) {
