@@ -31,12 +31,12 @@
 // the stage in which an expert ends is finished by a warp of each CTA that zeroes the rows past the
 // end, for both operands, so that nothing a neighbour holds (a NaN, say) reaches the sum.
 //
-// Measured: 131072 rows of bf16 over 128 skewed experts, K 2048, N 1536 with SiLU: 520 us at full clocks (1586
-// TFLOP/s, tensor pipe 79% busy), 600 us in a long loop, where the power limit lowers them (cuBLAS's dense
-// product falls from 2030 to 1720 TFLOP/s the same way).  Bound by the operands' way from L2 into the SMs:
-// the loads alone take 465 us (15.5 TB/s), without the epilogue 475 us.  Weights' gradient of the
-// same rows 562 us (637 us in a loop).  Decode, 64 rows over 128 experts: 54 us for 321 MB (0.88 of a copy); rows'
-// gradient of 1024 rows, 8 experts of 14336 x 4096: 166 us (0.95 of a copy).
+// Measured: 131072 rows of bf16 over 128 skewed experts, K 2048, N 1536 with SiLU: 526 us in short loops (1568
+// TFLOP/s, tensor pipe 79% busy), 600 us in a long one, where the power limit lowers the clocks (a library
+// product of 8192^3 falls from 1904 to 1710 TFLOP/s the same way).  The rows' gradient of the same batch 540 us, through
+// SiLU (2048 to 768 columns) 342 us, the weights' gradient 566 us (638 us in a long loop).  Decode, 64 rows over 128
+// experts: 54 us for 321 MB (0.88 of a copy); rows' gradient of 1024 rows, 8 experts of 14336 x 4096: 165 us
+// (0.95 of a copy).
 #include <type_traits>
 
 #include "train.cuh"
