@@ -231,7 +231,8 @@ int moe_post_norm_backward(const void* dout, int64_t lddout, const void* y, int6
     if (!p) return MOE_ERR_INVALID_ARG;
     int gate = 0, rc = check_norm(T, H, dtype, p->weight_dtype);
     if (rc != MOE_OK || (rc = check_gate(p, T, H, &gate)) != MOE_OK) return rc;
-    if (lddout < H || ldy < H || !p->weight || !dweight || (dgate && p->gate_kind == MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
+    if (lddout < H || ldy < H || !p->weight || !dweight || (dgate && p->gate_kind == MOE_GATE_NONE))
+        return MOE_ERR_INVALID_ARG;
     const size_t es = dtype_bytes(dtype), ws = dtype_bytes(p->weight_dtype);
     if (T > 0 && (!dout || !y || !rstd || !dy)) return MOE_ERR_INVALID_ARG;
     const size_t gs = gate == kGateChannel ? 4 : es;   // a channel gate's gradient is fp32

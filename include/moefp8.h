@@ -621,8 +621,9 @@ int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* a, int64_t l
  *   out[i] = grads[i] * min(1, max_norm / (total + eps))
  * grads, out, numel, dtype: host arrays of n (device addresses, elements, MOE_DTYPE_*); out[i] ==
  * grads[i] clips in place.  A result that overlaps another result or gradient (a tensor given twice, in
- * place) is refused with MOE_ERR_INVALID_ARG.  total_norm: device fp32.  A NaN total makes every gradient NaN, as the formula does.  Nothing is read after the call returns but the
- * tensors.  workspace: device scratch of moe_clip_grads_workspace_size(n) bytes, 8-byte aligned. */
+ * place) is refused with MOE_ERR_INVALID_ARG.  total_norm: device fp32.  A NaN total makes every gradient
+ * NaN, as the formula does.  Nothing is read after the call returns but the tensors.  workspace: device
+ * scratch of moe_clip_grads_workspace_size(n) bytes, 8-byte aligned. */
 #define MOE_NORM_L2 0
 #define MOE_NORM_INF 1
 size_t moe_clip_grads_workspace_size(int n);
