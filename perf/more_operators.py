@@ -129,6 +129,11 @@ def work(case):
 
 
 # --------------------------------------------------------------------------------- 4-bit numbers
+def _power(e):
+    """2^e of whole numbers, in 64 bits, exact."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _e2m1(a):
     """Nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even code) to magnitudes."""
     step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0)).to(a.dtype)
@@ -138,7 +143,7 @@ def _e2m1(a):
 def _e4m3(a):
     """Nearest e4m3 number to magnitudes, as the values (saturating at 448)."""
     _, p = torch.frexp(a)
-    step = torch.ldexp(torch.ones_like(a), p.clamp(min=-5) - 4)   # 2^-9 below 2^-6
+    step = _power(p.clamp(min=-5) - 4).to(a.dtype)   # 2^-9 below 2^-6
     return (torch.round(a / step) * step).clamp(max=448.0)
 
 
@@ -151,7 +156,7 @@ def _quantise(x, form):
     if form == "mxfp4":
         m, p = torch.frexp(top)          # top = m 2^p, m in [1/2, 1): 2^(p-3) holds up to 6/8 2^p
         e = torch.where(top > 0, p - 3 + (m > 0.75), torch.full_like(p, -127)).clamp(-127, 127)
-        scale, row = torch.ldexp(torch.ones_like(top, dtype=torch.float64), e), None
+        scale, row = _power(e), None
         div = scale.to(g.dtype)
     else:
         row = (top.amax(1) / 2688).float()
@@ -212,7 +217,7 @@ def _weights(g, E, N, K, form, gate_up):
             s = _e4m3(top / (6 * total[e])).clamp(min=2.0 ** -9)
             d = s * total[e]
         else:
-            d = s = torch.exp2(torch.ceil(torch.log2(top / 6)))
+            d = s = _power(torch.ceil(torch.log2(top / 6))).float()
         q = w.div_(d[:, :, None])
         codes[e] = _codes(_e2m1(q.abs()).copysign(q).reshape(N, K))
         scales[e] = _scale_bytes(s, form)
@@ -221,7 +226,7 @@ def _weights(g, E, N, K, form, gate_up):
 
 def _scale_values(b, form, dtype):
     if form == "mxfp4":
-        return torch.ldexp(torch.ones(b.shape, dtype=dtype, device=b.device), b.int() - 127)
+        return _power(b.int() - 127).to(dtype)
     return b.view(torch.float8_e4m3fn).to(dtype)
 
 
@@ -483,7 +488,7 @@ def _exact_quant(x, form):
     v = x.double().reshape(R, K // G, G)
     top = v.abs().amax(2, keepdim=True)
     if form == "mxfp4":
-        d = torch.exp2(torch.arange(-127, 128, device="cuda").double())      # the first scale that holds the largest
+        d = _power(torch.arange(-127, 128, device="cuda"))      # the first scale that holds the largest
         d = d[torch.searchsorted(d, (top / 6).contiguous()).clamp(max=254)]
     else:
         row = (top.amax(1, keepdim=True) / 2688).float().double()
