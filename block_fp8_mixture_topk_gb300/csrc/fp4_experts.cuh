@@ -1,0 +1,487 @@
+// The experts' products on 4-bit rows and weights, over rows sorted by expert, with fp32 accumulation:
+//
+//   product            c[r] = a[r] @ w[e]^T                a [rows, K], w [E, N, K], c [rows, N]
+//   ... SiLU(gate)*up  h[r] = silu(c[r, :N/2]) * c[r, N/2:]
+// where expert e owns rows [offsets[e], offsets[e+1]) and a and w stand for codes and scales (fp4.cuh); the scale
+// of a row and of an expert (nvfp4) multiply the fp32 sum.
+//
+// One persistent kernel on clusters of two CTAs, one CTA per SM, built like the 16-bit products.  An item is a
+// tile of 256 output columns (the weights, 128 lanes of tensor memory in each CTA) by up to 224 rows (N of the MMA,
+// in steps of 32, half of them loaded by each CTA), so an expert's last tile costs its rows.  One thread of CTA 0
+// issues tcgen05.mma.cta_group::2 of kind mxf4 (a scale per 32) or mxf4nvf4 (per 16), K = 64 a step; a stage is a
+// block of 256 K, four steps: 30 KB of codes and 3 or 6 KB of scales into an SM for 448 cycles of its tensor pipe.
+//
+// Tensor memory: two accumulators of 224 columns leave 64 for scales (with 256 rows nothing would be left, and one
+// accumulator alone would stop the tensor pipe while it is read).  A slot of scales is two words of the weights'
+// 128 rows and of the item's rows, 24 columns; the two slots are filled in turn by tcgen05.cp, issued by the MMA
+// thread ahead of the MMAs that read them: the two run in the order in which one thread issues them.
+//
+// The rows' scales lie in tiles of 224 rows that start with the expert (fp4.cuh), so an item reads whole tiles; both
+// CTAs need the scales of all its rows.
+#pragma once
+
+#include "fp4.cuh"
+#include "pair.cuh"
+
+namespace mfp8 {
+namespace {
+
+constexpr int F_N = kFp4Rows;
+constexpr int F_A = 128 * 128;                      // bytes of the weights' codes of a stage in one CTA
+constexpr int F_B = F_N / 2 * 128;                  // of the rows'
+constexpr int F_EPI_WARPS = 8, F_FIRST_EPI = 4;     // warps 0: TMA, 1: MMA, 2: tile table
+constexpr int F_THREADS = (F_FIRST_EPI + F_EPI_WARPS) * 32;
+constexpr uint32_t F_TMEM = 512;
+constexpr int F_GROUP = 4;                          // row tiles visited together
+constexpr int F_SLOT = 24;                          // columns of a slot of scales: 2 words of 128 and of 256 rows
+__host__ __device__ constexpr int f_stages(int fmt) { return fmt == MOE_FP4_MXFP4 ? 6 : 5; }
+__host__ __device__ constexpr int f_scales(int fmt) { return 3 * fp4_words(fmt) * 512; }   // bytes of a stage
+__host__ __device__ constexpr int f_stage(int fmt) { return F_A + F_B + f_scales(fmt); }
+
+struct FCtl {
+    uint64_t full[6];           // (CTA 0) both CTAs' operands of the stage are in place
+    uint64_t empty[6];          // the stage's MMAs completed
+    uint64_t tfull[2];          // the accumulators are complete
+    uint64_t tempty[2];         // (CTA 0) both CTAs' epilogue warps moved them out
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int half_bad[2];
+    int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
+    int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each expert
+};
+__host__ __device__ constexpr size_t f_smem(int fmt) {
+    return 1024 + static_cast<size_t>(f_stages(fmt)) * f_stage(fmt) + 2 * X_STAGED + sizeof(FCtl);
+}
+static_assert(f_smem(MOE_FP4_MXFP4) <= 232448 && f_smem(MOE_FP4_NVFP4) <= 232448, "more shared memory than a CTA has");
+static_assert(2 * (256 + F_SLOT) > static_cast<int>(F_TMEM) && F_N + F_SLOT <= 256, "an accumulator and a slot to each half");
+
+// One output tile: rows [r0, r0 + nrow) of column tile n of expert e, the m-th of its row tiles.
+struct FItem {
+    int e, n, m, r0, nrow;
+};
+
+__device__ __forceinline__ FItem f_item(const Fp4Args& a, const FCtl* ctl, int64_t w, int NT) {
+    // the expert whose tiles hold tile w / NT; within it F_GROUP row tiles by all column tiles, row tiles
+    // fastest, so that the items under way at one time share rows and weights in L2
+    FItem t;
+    const int g = static_cast<int>(w / NT);
+    int lo = 0, hi = a.E - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (ctl->tile0[mid] <= g) lo = mid;
+        else hi = mid - 1;
+    }
+    const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo];
+    int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
+    const int grp = local / (F_GROUP * NT);
+    local -= grp * F_GROUP * NT;
+    const int gm = mt - grp * F_GROUP < F_GROUP ? mt - grp * F_GROUP : F_GROUP;
+    const int m = grp * F_GROUP + local % gm;
+    const int cnt = ctl->row0[lo + 1] - ctl->row0[lo];
+    t.e = __shfl_sync(0xffffffffu, lo, 0);
+    t.n = __shfl_sync(0xffffffffu, local / gm, 0);
+    t.m = __shfl_sync(0xffffffffu, m, 0);
+    t.r0 = __shfl_sync(0xffffffffu, ctl->row0[lo] + m * F_N, 0);
+    t.nrow = __shfl_sync(0xffffffffu, cnt - m * F_N < F_N ? cnt - m * F_N : F_N, 0);
+    return t;
+}
+__device__ __forceinline__ int f_rows_mma(int nrow) { return (nrow + 31) / 32 * 32; }
+
+// Instruction descriptor: e2m1 operands, both K-major, M = 256; sf: the first byte of the scales' words (2 of them
+// per row and step with mxfp4, all 4 with nvfp4).
+template <int FMT>
+__device__ __forceinline__ uint32_t f_idesc(int n, int sf) {
+    return (static_cast<uint32_t>(sf) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           ((FMT == MOE_FP4_MXFP4 ? 1u : 0u) << 23) | (2u << 27) | (static_cast<uint32_t>(sf) << 29);
+}
+// D (256 x N over both CTAs) (+)= (A * scales) * (B * scales)^T, K = 64; issued by one thread of CTA 0.
+template <int FMT>
+__device__ __forceinline__ void f_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                      uint32_t accumulate) {
+    if constexpr (FMT == MOE_FP4_MXFP4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+// Each CTA's 512-byte tile at this shared-memory address into 4 columns of its own tensor memory.
+__device__ __forceinline__ void f_copy_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+template <class T, int FMT, bool SILU>
+__global__ void __launch_bounds__(F_THREADS, 1)
+    fp4_expert_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmSA,
+                      const __grid_constant__ CUtensorMap tmSB, const Fp4Args a) {
+    constexpr int STAGES = f_stages(FMT), W = fp4_words(FMT);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    uint8_t* smA = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);   // [STAGES][F_A]
+    uint8_t* smB = smA + STAGES * F_A;                                      // [STAGES][F_B]
+    uint8_t* smS = smB + STAGES * F_B;                                      // [STAGES][weights W, rows 2 W][512]
+    uint8_t* smE = smS + STAGES * f_scales(FMT);                            // [2][X_STAGED]
+    FCtl* ctl = reinterpret_cast<FCtl*>(smE + 2 * X_STAGED);
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_rank());
+    const int OC = SILU ? a.N / 2 : a.N;                        // output columns
+    const int NT = SILU ? (OC + 127) / 128 : (OC + 255) / 256;
+    const int KB = fp4_blocks(a.K);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_addr(&ctl->full[s]), 1);
+            mbar_init(smem_addr(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&ctl->tfull[b]), 1);
+            mbar_init(smem_addr(&ctl->tempty[b]), 2 * F_EPI_WARPS);
+        }
+        mbar_init(smem_addr(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        ctl->half_bad[0] = ctl->half_bad[1] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
+        tma_prefetch_map(&tmSA);
+        tma_prefetch_map(&tmSB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_addr(&ctl->tmem_base), F_TMEM);
+        tmem_relinquish_pair();
+    }
+    grid_dependency_wait();
+    // the experts' rows, offsets out of range or order repaired and reported, as in the 16-bit products
+    int bad = 0;
+    for (int e = threadIdx.x; e <= a.E; e += F_THREADS) {
+        if (!a.offsets) {
+            ctl->row0[e] = e == 0 ? 0 : static_cast<int>(a.rows);
+            continue;
+        }
+        const int64_t o = a.offsets[e], prev = e > 0 ? a.offsets[e - 1] : 0;
+        bad |= o < 0 || o > a.rows || prev > o || (e == 0 && o != 0);
+        ctl->row0[e] = static_cast<int>(e == 0 || o < 0 ? 0 : o > a.rows ? a.rows : o);
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            status_set(a.status, MOE_STATUS_BAD_COUNT);
+            for (int e = 1; e <= a.E; ++e)
+                if (ctl->row0[e] < ctl->row0[e - 1]) ctl->row0[e] = ctl->row0[e - 1];
+        }
+        __syncthreads();
+    }
+    if (warp == 2) {
+        int carry = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int cnt = e < a.E ? ctl->row0[e + 1] - ctl->row0[e] : 0;
+            const int own = (cnt + F_N - 1) / F_N;
+            int v = own;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, s);
+                if (lane >= s) v += u;
+            }
+            if (e < a.E) ctl->tile0[e] = carry + v - own;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) ctl->tile0[a.E] = carry;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();   // both CTAs' barriers are initialised before any arrival from the other
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    const int64_t total = static_cast<int64_t>(ctl->tile0[a.E]) * NT;
+    const int64_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true;
+        const uint32_t smA0 = smem_addr(smA), smB0 = smem_addr(smB), smS0 = smem_addr(smS);
+        const uint32_t full = smem_addr(&ctl->full[0]), full0 = cluster_map(full, 0);
+        const int w_tiles = SILU ? (OC + 63) / 64 : (a.N + 127) / 128;   // of the weights' scales, an expert
+        for (int64_t w = cluster; w < total && ok; w += clusters) {
+            const FItem t = f_item(a, ctl, w, NT);
+            const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's output columns
+            const int nn = f_rows_mma(t.nrow);
+            const int32_t r0 = t.r0 + rank * (nn / 2);
+            const int small = nn <= 64 ? nn / 32 : 0;   // few rows: in boxes of 16, only as many as the MMAs read
+            const int halves = nn > 128 ? 2 : 1;        // of the rows' scales
+            const uint32_t bytes = F_A + (small ? small * 2048 : F_B) + (1 + halves) * W * 512;
+            // 512-byte tiles of scales; a tile of weights past the last is not multiplied into anything stored
+            const int wt = 2 * t.n + rank;
+            int32_t sa = static_cast<int32_t>((static_cast<int64_t>(t.e) * w_tiles + (wt < w_tiles ? wt : w_tiles - 1)) * KB * W);
+            int32_t sb = static_cast<int32_t>((static_cast<int64_t>(ctl->row0[t.e] / F_N) + t.e + t.m) * KB * 2 * W);
+            for (int kb = 0; kb < KB; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->empty[stage]), phase ^ 1u, abort_flag, a.status));
+                if (!ok) break;
+                if (elect_lane()) {
+                    const uint32_t bar = full0 + stage * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(full + stage * 8, 2 * bytes);
+                    const uint32_t da = smA0 + stage * F_A, db = smB0 + stage * F_B, ds = smS0 + stage * f_scales(FMT);
+                    if (SILU) tma_load_5d_pair(da, &tmA, kb * 128, 0, 0, c0 / 16, t.e, bar);   // 16 of gate, 16 of up in turn
+                    else tma_load_3d_pair(da, &tmA, kb * 128, c0, t.e, bar);
+                    if (small == 0) tma_load_2d_pair(db, &tmB, kb * 128, r0, bar);
+                    for (int i = 0; i < small; ++i) tma_load_2d_pair(db + i * 2048, &tmB16, kb * 128, r0 + i * 16, bar);
+                    tma_load_3d_pair(ds, &tmSA, 0, 0, sa, bar);
+                    for (int h = 0; h < halves; ++h) tma_load_3d_pair(ds + (1 + h) * W * 512, &tmSB, 0, 0, sb + h * W, bar);
+                }
+                __syncwarp();
+                sa += W;
+                sb += 2 * W;
+                ++issued;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // after an abort CTA 0 lets the loads of the stages it armed land, both CTAs' bytes; CTA 1, which
+        // cannot see its loads' completion, waits for CTA 0 at the closing cluster barrier
+        if (!ok && rank == 0 && lane == 0) {
+            for (int s = 0; s < STAGES; ++s) {
+                const uint32_t n_s = (issued + STAGES - 1 - s) / STAGES;
+                if (n_s > 0) mbar_wait<true>(smem_addr(&ctl->full[s]), (n_s - 1) & 1u, nullptr, a.status);
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ------------------------------------------------------------ MMA (CTA 0)
+            const uint64_t ad0 = smem_desc_k128_sw128(smem_addr(smA)), bd0 = smem_desc_k128_sw128(smem_addr(smB));
+            const uint64_t sd0 = smem_desc_sf_tile(smem_addr(smS));
+            int stage = 0;
+            uint32_t phase = 0, buf = 0, bphase = 0, slot = 0;
+            bool ok = true;
+            for (int64_t w = cluster; w < total && ok; w += clusters) {
+                const FItem t = f_item(a, ctl, w, NT);
+                ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + buf * 256;
+                const int nn = f_rows_mma(t.nrow);
+                const uint32_t idesc = f_idesc<FMT>(nn, 0);
+                for (int kb = 0; kb < KB; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->full[stage]), phase, abort_flag, a.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ad = ad0 + stage * (F_A >> 4), bd = bd0 + stage * (F_B >> 4);
+                    const uint64_t sd = sd0 + stage * (f_scales(FMT) >> 4);
+                    const int left = a.K - kb * kFp4Block;
+                    const int steps = left >= kFp4Block ? 4 : (left + 63) / 64;
+                    if (elect_lane()) {
+                        constexpr int PER = FMT == MOE_FP4_MXFP4 ? 4 : 2;   // steps of a slot
+#pragma unroll
+                        for (int k0 = 0; k0 < 4; k0 += PER) {
+                            if (k0 < steps) {
+                                const uint32_t sfa = tmem + (((slot + k0 / PER) & 1u) ? 256 : 0) + F_N, sfb = sfa + 8;
+                                const int word = k0 / PER * 2;
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    f_copy_scales(sfa + j * 4, sd + (word + j) * 32);
+                                    f_copy_scales(sfb + j * 8, sd + (W + word + j) * 32);
+                                    if (nn > 128) f_copy_scales(sfb + j * 8 + 4, sd + (2 * W + word + j) * 32);
+                                }
+#pragma unroll
+                                for (int k = k0; k < k0 + PER; ++k) {
+                                    const int j = FMT == MOE_FP4_MXFP4 ? k >> 1 : k - k0;
+                                    const uint32_t id = idesc | (FMT == MOE_FP4_MXFP4 && (k & 1) ? (2u << 4) | (2u << 29) : 0u);
+                                    if (k < steps)
+                                        f_mma<FMT>(d, ad + k * 2, bd + k * 2, id, sfa + j * 4, sfb + j * 8, (kb | k) > 0 ? 1u : 0u);
+                                }
+                            }
+                        }
+                        mma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
+                        if (kb + 1 == KB) mma_commit_pair(smem_addr(&ctl->tfull[buf]), 3);
+                    }
+                    __syncwarp();
+                    slot ^= FMT == MOE_FP4_MXFP4 || steps <= 2 ? 1u : 0u;   // (a stage of nvfp4 takes two)
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                buf ^= 1u;
+                if (buf == 0) bphase ^= 1u;
+            }
+            // every MMA complete before the CTAs can leave (they read both CTAs' shared memory)
+            if (elect_lane()) {
+                mma_commit_pair(smem_addr(&ctl->drain), 1);
+                mbar_wait(smem_addr(&ctl->drain), 0, nullptr, a.status);
+            }
+        }
+    } else if (warp >= F_FIRST_EPI) {
+        // ---------------------------------------------------------------- epilogue
+        const int g = (warp - F_FIRST_EPI) >> 2;
+        const int sp = warp & 3;                   // tensor-memory lane quarter
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+        T* out = static_cast<T*>(a.out);
+        const Block block = {smE + g * X_STAGED, 1 + g, sp * 32 + lane};
+        uint32_t buf = 0, bphase = 0;
+        bool ok = true;
+        const uint32_t tempty0 = cluster_map(smem_addr(&ctl->tempty[0]), 0), tempty1 = cluster_map(smem_addr(&ctl->tempty[1]), 0);
+        for (int64_t w = cluster; w < total; w += clusters) {
+            const FItem t = f_item(a, ctl, w, NT);
+            const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's columns
+            const int col = sp * 32 + lane;
+            const int blocks = (t.nrow + 31) / 32;
+            float wg = 1.0f;
+            if constexpr (FMT == MOE_FP4_NVFP4) wg = __ldg(a.w_global + t.e);
+            ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
+            if (!half_ok(ok, block, &ctl->half_bad[g])) break;
+            tc_fence_after();
+            for (int blk = g; blk < blocks; blk += 2) {
+                float v[32];
+                const int64_t r0 = static_cast<int64_t>(t.r0) + blk * 32;
+                const int nrow = t.nrow - blk * 32;
+                float rs = 0.0f;
+                if constexpr (FMT == MOE_FP4_NVFP4) rs = lane < nrow ? __ldg(a.row_scale + r0 + lane) * wg : 0.0f;
+                tmem_ld32(lane_base + buf * 256 + blk * 32, v);
+                if constexpr (FMT == MOE_FP4_NVFP4) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, rs, i);
+                }
+                if constexpr (SILU) {
+                    // lanes: 16 gate columns, then the up columns of the same; hc: the column of h.  A gate lane
+                    // gives the up lane beside it its rows 16 .. 31 for that lane's up of rows 0 .. 15: each
+                    // then holds 16 rows of one column of h
+                    const bool up = (lane & 16) != 0;
+                    const int hc = sp * 16 + (lane & 15), first = up ? 16 : 0;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[16 + i], 16);
+                        const float gate = up ? o : v[i], u = up ? v[16 + i] : o;
+                        block.put<T>(first + i, hc, __fdividef(gate, 1.0f + __expf(-gate)) * u);
+                    }
+                    block.sync();
+                    block.each_piece<8>([&](int, int r, int q, uint8_t* p) {
+                        if (r < nrow && c0 + q * 8 < OC)
+                            *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) = *reinterpret_cast<const uint4*>(p);
+                    });
+                    block.sync();
+                } else if constexpr (sizeof(T) == 4) {
+                    // 16 rows of 128 columns at a time
+                    constexpr int PITCH = 512 + 16;
+                    static_assert(16 * PITCH <= X_STAGED, "a staged block");
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            *reinterpret_cast<float*>(block.stage + i * PITCH + col * 4) = v[part * 16 + i];
+                        block.sync();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = i * 128 + block.et, r = k >> 5, q = k & 31;
+                            if (part * 16 + r < nrow && c0 + q * 4 < OC)
+                                *reinterpret_cast<uint4*>(out + (r0 + part * 16 + r) * OC + c0 + q * 4) =
+                                    *reinterpret_cast<const uint4*>(block.stage + r * PITCH + q * 16);
+                        }
+                        block.sync();
+                    }
+                } else {
+                    block.store<T>(v, col, out + r0 * OC, OC, nrow, c0, OC);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(buf ? tempty1 : tempty0);
+            buf ^= 1u;
+            if (buf == 0) bphase ^= 1u;
+        }
+        if (ok) {   // rows of no expert: zero
+            constexpr int PER = 16 / static_cast<int>(sizeof(T));
+            const int64_t first = ctl->row0[a.E], n = (a.rows - first) * OC / PER;
+            const int64_t step = static_cast<int64_t>(gridDim.x) * (F_EPI_WARPS * 32);
+            for (int64_t i = static_cast<int64_t>(blockIdx.x) * (F_EPI_WARPS * 32) + threadIdx.x - F_FIRST_EPI * 32; i < n; i += step)
+                reinterpret_cast<uint4*>(out + first * OC)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();   // no CTA leaves while the other's MMAs, loads or arrivals may still reach it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, F_TMEM);
+}
+
+void f_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int fmt, unsigned clusters, cudaStream_t stream) {
+    *cfg = {};
+    cfg->gridDim = dim3(2 * clusters);
+    cfg->blockDim = dim3(F_THREADS);
+    cfg->dynamicSmemBytes = f_smem(fmt);
+    cfg->stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+}
+
+template <int FMT>
+struct Fp4Launch {
+    static int clusters;   // of two CTAs resident at once (the same for every instance: one CTA per SM)
+    template <class T, bool SILU>
+    static cudaError_t one(const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t most_items, cudaStream_t stream) {
+        if (clusters < 1) return cudaErrorNotSupported;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        f_config(&cfg, attr, FMT, static_cast<unsigned>(most_items < clusters ? most_items : clusters), stream);
+        return cudaLaunchKernelEx(&cfg, fp4_expert_kernel<T, FMT, SILU>, tm[0], tm[1], tm[2], tm[3], tm[4], a);
+    }
+    static cudaError_t launch(int dtype, bool silu, const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t items,
+                              cudaStream_t s) {
+        if (silu) return dtype == MOE_DTYPE_BF16 ? one<__nv_bfloat16, true>(a, tm, items, s) : one<__half, true>(a, tm, items, s);
+        return dtype == MOE_DTYPE_BF16   ? one<__nv_bfloat16, false>(a, tm, items, s)
+               : dtype == MOE_DTYPE_FP16 ? one<__half, false>(a, tm, items, s)
+                                         : one<float, false>(a, tm, items, s);
+    }
+    template <class T, bool SILU>
+    static cudaError_t smem() {
+        return cudaFuncSetAttribute(fp4_expert_kernel<T, FMT, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(f_smem(FMT)));
+    }
+    static cudaError_t init() {
+        cudaError_t e = smem<__nv_bfloat16, true>();
+        if (e == cudaSuccess) e = smem<__half, true>();
+        if (e == cudaSuccess) e = smem<__nv_bfloat16, false>();
+        if (e == cudaSuccess) e = smem<__half, false>();
+        if (e == cudaSuccess) e = smem<float, false>();
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        f_config(&cfg, attr, FMT, 1, nullptr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, fp4_expert_kernel<__nv_bfloat16, FMT, false>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        clusters = n;
+        return cudaSuccess;
+    }
+};
+template <int FMT>
+int Fp4Launch<FMT>::clusters = 0;
+
+}  // namespace
+
+}  // namespace mfp8

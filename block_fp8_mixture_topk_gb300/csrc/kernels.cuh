@@ -223,6 +223,8 @@ cudaError_t launch_decode_mlp(const DecodeMlpArgs& args, int num_sms, cudaStream
 // tokens.cu, experts.cu, clip.cu: once-per-device set-up
 cudaError_t tokens_init_device();
 cudaError_t experts_init_device();
+// fp4.cu
+cudaError_t fp4_init_device();
 cudaError_t clip_init_device();
 
 // api.cu: once-per-device set-up; on MOE_OK, *status = the device status word's address

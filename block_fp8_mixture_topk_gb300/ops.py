@@ -143,6 +143,13 @@ def lib():
                 "moe_expert_gemm_wgrad": ([P, I64, P, I64, I, P, I64, I, I, I, P, P], I),
                 "moe_clip_grads_workspace_size": ([I], SZ),
                 "moe_clip_grads": ([P, P, P, P, I, I, F, F, P, P, SZ, P], I),
+                "moe_fp4_row_scale_bytes": ([I, I64, I, I], SZ),
+                "moe_fp4_weight_scale_bytes": ([I, I, I, I], SZ),
+                "moe_fp4_quant": ([P, I64, I, I, P, I, I64, I, P, P, P, P], I),
+                "moe_fp4_dequant": ([P, P, P, I, P, I, I64, I, I, P, P], I),
+                "moe_mxfp4_quant_weight": ([P, I, I, I, I, P, P, P], I),
+                "moe_fp4_pack_scales": ([P, I, I, I, I, I, P, P], I),
+                "moe_fp4_expert_gemm": ([P, P, P, I, P, P, P, P, I64, I, I, I, I, I, P, P], I),
                 "moe_get_device_status": ([P, I], I),
                 "moe_selftest_bounded_wait": ([I, P], I),
                 "moe_error_string": ([I], ctypes.c_char_p),
@@ -973,6 +980,173 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
                                      dw.data_ptr(), stream)
     _check("moe_expert_gemm_wgrad", rc)
     return dw
+
+
+# ---- 4-bit rows and weights (C ABI section "4-bit rows and weights") -------------------------
+
+FP4_FORMAT = {"mxfp4": 0, "nvfp4": 1}
+_FP4_GROUP = {"mxfp4": 32, "nvfp4": 16}
+
+
+def _fp4_format(fmt):
+    if fmt not in FP4_FORMAT:
+        raise ValueError(f"format must be one of {list(FP4_FORMAT)}, got {fmt!r}")
+    return FP4_FORMAT[fmt]
+
+
+@dataclasses.dataclass
+class Fp4Rows:
+    """Rows in 4 bits (moe_fp4_quant)."""
+    codes: torch.Tensor                   # uint8 [rows, K/2], two e2m1 codes to a byte, the first in the low half
+    scales: torch.Tensor                  # uint8, the groups' scales in the products' tiles
+    row_scale: torch.Tensor | None        # nvfp4: fp32 [rows]
+    format: str                           # "mxfp4" or "nvfp4"
+    expert_offsets: torch.Tensor | None   # int32 [E+1] of rows sorted by expert; None: one weight for all rows
+
+
+def _fp4_offsets(offsets):
+    """Number of experts (0: None) of a valid expert_offsets."""
+    if offsets is None:
+        return 0
+    _cuda(offsets, torch.int32, "expert_offsets")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"expert_offsets must be [E+1], got {list(offsets.shape)}")
+    return offsets.shape[0] - 1
+
+
+def moe_fp4_quant(x, format="mxfp4", expert_offsets=None) -> Fp4Rows:
+    """Rows x [rows, K] (bf16, fp16 or fp32) in 4 bits: "mxfp4" (e2m1 codes, 32 along K to a power-of-two scale) or
+    "nvfp4" (16 to an e4m3 scale, and an fp32 scale per row).  expert_offsets: the rows are sorted by expert
+    (moe_dispatch), for the products of that many experts.  K a multiple of 32, at most 32768."""
+    code, ld = _rows(x, "x")
+    fmt = _fp4_format(format)
+    E = _fp4_offsets(expert_offsets)
+    n, K = x.shape
+    L = lib()
+    stream = _training_stream("moe_fp4_quant", "x expert_offsets", x, expert_offsets)
+    codes = _matrix(n, K // 2, torch.uint8)
+    scales = _vector(L.moe_fp4_row_scale_bytes(fmt, n, E, K), torch.uint8)
+    row_scale = _vector(n, torch.float32) if fmt else None
+    rc = L.moe_fp4_quant(x.data_ptr(), ld, code, fmt, None if E == 0 else expert_offsets.data_ptr(), E, n, K,
+                         codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt else None, stream)
+    _check("moe_fp4_quant", rc)
+    return Fp4Rows(codes, scales, row_scale, format, expert_offsets)
+
+
+def _fp4_rows(rows):
+    """(format code, number of experts, rows, K) of an Fp4Rows whose parts fit together."""
+    fmt = _fp4_format(rows.format)
+    E = _fp4_offsets(rows.expert_offsets)
+    _cuda(rows.codes, torch.uint8, "rows.codes")
+    if rows.codes.dim() != 2:
+        raise ValueError(f"rows.codes must be a matrix, got {list(rows.codes.shape)}")
+    n, K = rows.codes.shape[0], 2 * rows.codes.shape[1]
+    if n > _INT_MAX or K > _INT_MAX:
+        raise _too_large("rows.codes")
+    _dense(rows.scales, "rows.scales", torch.uint8, (lib().moe_fp4_row_scale_bytes(fmt, n, E, K),))
+    if fmt:
+        if rows.row_scale is None:
+            raise ValueError("nvfp4 rows need a row_scale")
+        _dense(rows.row_scale, "rows.row_scale", torch.float32, (n,))
+    elif rows.row_scale is not None:
+        raise ValueError("mxfp4 rows have no row_scale")
+    return fmt, E, n, K
+
+
+def _or_none(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_fp4_dequant(rows: Fp4Rows, dtype=torch.bfloat16):
+    """The numbers that 4-bit rows stand for, [rows, K] in dtype (bf16, fp16 or fp32)."""
+    fmt, E, n, K = _fp4_rows(rows)
+    if dtype not in DTYPE:
+        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
+    stream = _stream("codes scales row_scale expert_offsets", rows.codes, rows.scales, rows.row_scale, rows.expert_offsets)
+    out = _matrix(n, K, dtype)
+    rc = lib().moe_fp4_dequant(rows.codes.data_ptr(), rows.scales.data_ptr(), _or_none(rows.row_scale) if n else None, fmt,
+                               _or_none(rows.expert_offsets), E, n, K, DTYPE[dtype], out.data_ptr(), stream)
+    _check("moe_fp4_dequant", rc)
+    return out
+
+
+def moe_mxfp4_quant_weight(w):
+    """MXFP4 quantisation of expert weights [E, N, K] (bf16, fp16 or fp32): returns (codes uint8 [E, N, K/2], two e2m1 per
+    byte, element 2i in the low half; UE8M0 scale bytes uint8 [E, N, K/32]) (load-time)."""
+    code = _typed(w, "w")
+    if w.dim() != 3 or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [E, N, K], got {list(w.shape)}")
+    E, N, K = w.shape
+    if max(E, N, K) > _INT_MAX:
+        raise _too_large("w")
+    q = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+    s = torch.empty(E, N, K // 32, dtype=torch.uint8, device=w.device)
+    _check("moe_mxfp4_quant_weight", lib().moe_mxfp4_quant_weight(_ptr(w), code, E, N, K, _ptr(q), _ptr(s), _stream("w", w)))
+    return q, s
+
+
+def moe_fp4_pack_scales(scales, format="mxfp4", gate_up=False):
+    """Scale bytes of 4-bit weights [E, N, K/32] (mxfp4, UE8M0) or [E, N, K/16] (nvfp4, e4m3; moe_nvfp4_quant_weight's)
+    into the tiles that the 4-bit products read (load-time).  gate_up: of a w13 (gate rows, then up rows) for
+    moe_fp4_expert_gemm_silu_mul."""
+    fmt = _fp4_format(format)
+    scales = _codes(_cuda(scales, None, "scales"))
+    if scales.dim() != 3:
+        raise ValueError(f"scales must be [E, N, K/{_FP4_GROUP[format]}], got {list(scales.shape)}")
+    E, N, C = scales.shape
+    K = C * _FP4_GROUP[format]
+    if max(E, N, K) > _INT_MAX:
+        raise _too_large("scales")
+    words = 2 * (1 + fmt)
+    out = torch.empty(E, (N + 127) // 128, (K + 255) // 256, words * 512, dtype=torch.uint8, device=scales.device)
+    _check("moe_fp4_pack_scales", lib().moe_fp4_pack_scales(_ptr(scales), fmt, E, N, K, int(bool(gate_up)), _ptr(out),
+                                                            _stream("scales", scales)))
+    return out
+
+
+def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, silu):
+    fmt, E, n, K = _fp4_rows(rows)
+    _cuda(w, torch.uint8, "w")
+    if w.dim() != 3 or 2 * w.shape[2] != K or w.shape[0] != max(E, 1):
+        raise ValueError(f"w must be [{max(E, 1)}, N, {K // 2}] for these rows, got {list(w.shape)}")
+    N = w.shape[1]
+    if N > _INT_MAX:
+        raise _too_large("w")
+    if dtype not in DTYPE or (silu and dtype == torch.float32):
+        raise TypeError(f"dtype must be bfloat16{', float16 or float32' if not silu else ' or float16'}, got {dtype}")
+    _cuda(w_scales, torch.uint8, "w_scales")
+    if w_scales.numel() != lib().moe_fp4_weight_scale_bytes(fmt, max(E, 1), N, K):
+        raise ValueError("w_scales must be moe_fp4_pack_scales of w's scales in the rows' format")
+    if (w_global is None) != (fmt == 0):
+        raise ValueError("w_global is needed with nvfp4, and only there")
+    if fmt:
+        _dense(w_global, "w_global", torch.float32, (max(E, 1),))
+    stream = _stream("rows.codes rows.scales rows.row_scale rows.expert_offsets w w_scales w_global", rows.codes, rows.scales,
+                     rows.row_scale, rows.expert_offsets, w, w_scales, w_global)
+    out = _matrix(n, N // 2 if silu else N, dtype)
+    rc = lib().moe_fp4_expert_gemm(rows.codes.data_ptr(), rows.scales.data_ptr(), _or_none(rows.row_scale) if n else None, fmt,
+                                   w.data_ptr(), w_scales.data_ptr(), _or_none(w_global), _or_none(rows.expert_offsets), n,
+                                   max(E, 1), N, K, int(silu), DTYPE[dtype], out.data_ptr(), stream)
+    _check("moe_fp4_expert_gemm", rc)
+    return out
+
+
+def moe_fp4_expert_gemm(rows: Fp4Rows, w, w_scales, w_global=None, dtype=torch.bfloat16):
+    """The experts' product on 4-bit rows (moe_fp4_quant) and weights: out[r] = rows[r] @ w[e]^T, [rows, N] in dtype (bf16,
+    fp16 or fp32).  w: codes uint8 [E, N, K/2]; w_scales: their scales packed (moe_fp4_pack_scales); w_global fp32 [E] with
+    nvfp4.  Rows of no expert are zero.  Rows without expert_offsets: E = 1, one weight for all."""
+    return _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, False)
+
+
+def moe_fp4_expert_gemm_silu_mul(rows: Fp4Rows, w, w_scales, w_global=None, dtype=torch.bfloat16):
+    """The first product with its activation: h [rows, N/2] = silu(gate) * up in dtype (bf16 or fp16).  w [E, N, K/2]: gate
+    rows, then up rows; w_scales packed with gate_up=True."""
+    return _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, True)
+
+
+def moe_fp4_expert_gemm_silu_mul_quant(rows: Fp4Rows, w, w_scales, w_global=None) -> Fp4Rows:
+    """The same with h rounded to bf16 and in 4 bits again (the rows' format), for the second product."""
+    return moe_fp4_quant(moe_fp4_expert_gemm_silu_mul(rows, w, w_scales, w_global), rows.format, rows.expert_offsets)
 
 
 def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):

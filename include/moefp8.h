@@ -616,6 +616,50 @@ int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* a, int64_t l
                           const int32_t* expert_offsets, int64_t num_rows, int E, int N, int K, void* dw,
                           void* stream);
 
+/* ---- 4-bit rows and weights (microscaled floating point) -----------------------------------
+ * e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte along K, the first in the low half, with a
+ * scale for each group along K ("MXFP4", "NVFP4": page "Quantization and MoE Optimizations", section MXFP4; the formats
+ * of page "vllm.model_executor.layers.quantization.online.nvfp4"):
+ *   MOE_FP4_MXFP4  32 to a UE8M0 scale s = 2^(byte - 127), the smallest with max|x| <= 6 s; x ~ code * s
+ *   MOE_FP4_NVFP4  16 to an e4m3 scale b = e4m3(max|x| / (6 r)), and an fp32 r for each row (rows: max|x of the
+ *                  row| / 2688) or expert (weights: moe_nvfp4_quant_weight's global scale); x ~ code * b * r
+ * Scales and codes are the nearest (ties to even) to the real quotients.  A group (mxfp4) or row (nvfp4) with an
+ * infinity or NaN stands for NaN.  K is a multiple of 32, at most 32768 for rows.
+ *
+ * The products take scales in tiles (512 bytes: 32 lines of 16, line l the words of rows l, l + 32, l + 64, l + 96, a word
+ * four consecutive groups; W = 2 tiles (mxfp4) or 4 (nvfp4) for 128 rows by 256 columns; bytes past K are 0):
+ *   weights  [E][ceil(N/128)][ceil(K/256)][W][512]; with gate_up (rows gate, then up; N % 32 == 0) of the rows in the
+ *            order 16 gate, 16 up of the same columns, and so on: for the SiLU product
+ *   rows     [tiles of 224 rows][ceil(K/256)][2][W][512]; row r of expert e, whose rows begin at o_e, in tile
+ *            o_e / 224 + e + (r - o_e) / 224, and rows of no expert as those of an expert E. */
+#define MOE_FP4_MXFP4 0
+#define MOE_FP4_NVFP4 1
+/* Bytes of the rows' scales (E = 0: rows that are not sorted by expert) and of the weights'; 0 for sizes that the calls
+ * refuse. */
+size_t moe_fp4_row_scale_bytes(int fmt, int64_t num_rows, int E, int K);
+size_t moe_fp4_weight_scale_bytes(int fmt, int E, int N, int K);
+/* Rows x [num_rows, K] of row stride ldx (bf16, fp16 or fp32, any element's address) in 4 bits.  expert_offsets int32
+ * [E+1]: the rows are sorted by expert (moe_dispatch), for the products of E experts; NULL with E = 0: one weight for
+ * all rows.  codes [num_rows, K/2], scales moe_fp4_row_scale_bytes (both 16-byte aligned; the scales of no row are left
+ * as they are), row_scale fp32 [num_rows] (nvfp4; else NULL). */
+int moe_fp4_quant(const void* x, int64_t ldx, int dtype, int fmt, const int32_t* expert_offsets, int E, int64_t num_rows,
+                  int K, uint8_t* codes, uint8_t* scales, float* row_scale, void* stream);
+/* The numbers that such rows stand for, in fp32 and rounded to out's type: out [num_rows, K], 16-byte aligned. */
+int moe_fp4_dequant(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt,
+                    const int32_t* expert_offsets, int E, int64_t num_rows, int K, int dtype, void* out, void* stream);
+/* Load time: weights w [E, N, K] (bf16, fp16 or fp32, dense, 16-byte aligned) in MXFP4, codes [E, N, K/2] and scale bytes
+ * [E, N, K/32]; and scale bytes [E, N, K/32 or K/16] (also moe_nvfp4_quant_weight's or a checkpoint's) into tiles. */
+int moe_mxfp4_quant_weight(const void* w, int dtype, int E, int N, int K, uint8_t* codes, uint8_t* scales, void* stream);
+int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate_up, uint8_t* out, void* stream);
+/* The experts' products of such rows and weights on the tensor cores, fp32 accumulation (epilogues, offsets and rows of no
+ * expert as moe_expert_gemm's; expert_offsets NULL with E = 1: all rows):
+ *   MOE_EXPERT_STORE    out [num_rows, N] in dtype (bf16, fp16 or fp32), N a multiple of 8
+ *   MOE_EXPERT_SILU_MUL out [num_rows, N/2] in dtype (bf16 or fp16), N a multiple of 32, w_scales packed with gate_up
+ * w_codes [E, N, K/2]; w_global fp32 [E] and row_scale with nvfp4, else NULL.  All arrays 16-byte aligned. */
+int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt, const uint8_t* w_codes,
+                        const uint8_t* w_scales, const float* w_global, const int32_t* expert_offsets, int64_t num_rows,
+                        int E, int N, int K, int epilogue, int dtype, void* out, void* stream);
+
 /* Global norm of n gradient tensors and their clipping:
  *   total = sqrt(sum of squares) (MOE_NORM_L2) or the largest magnitude (MOE_NORM_INF) over all,
  *   out[i] = grads[i] * min(1, max_norm / (total + eps))
