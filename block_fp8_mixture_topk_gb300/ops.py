@@ -143,6 +143,10 @@ def lib():
                 "moe_expert_gemm_wgrad": ([P, I64, P, I64, I, P, I64, I, I, I, P, P], I),
                 "moe_clip_grads_workspace_size": ([I], SZ),
                 "moe_clip_grads": ([P, P, P, P, I, I, F, F, P, P, SZ, P], I),
+                "moe_router_workspace_size": ([I, I], SZ),
+                "moe_router": ([P, I64, I, I, I, I, P, P, P, P, P, P, P, P, SZ, P], I),
+                "moe_router_backward": ([P, I64, I, I, I, I, P, P, P, P, P, F, F, P, P], I),
+                "moe_router_update_bias": ([P, P, I, F, P], I),
                 "moe_fp4_row_scale_bytes": ([I, I64, I, I], SZ),
                 "moe_fp4_weight_scale_bytes": ([I, I, I, I], SZ),
                 "moe_fp4_quant": ([P, I64, I, I, P, I, I64, I, P, P, P, P], I),
@@ -982,6 +986,125 @@ def moe_expert_gemm_wgrad(dc, a, expert_offsets):
     return dw
 
 
+def _or_none(t):
+    return None if t is None else t.data_ptr()
+
+
+# ---- the router in its training form (C ABI section "training") ------------------------------
+
+GROUP_SCORE = {"top2": 0, "max": 1}
+
+
+class _RouterParams(ctypes.Structure):
+    _fields_ = [("scoring", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("routed_scaling", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
+@dataclasses.dataclass
+class Router:
+    """The experts of each token (moe_router); the last four with losses=True, z_loss with softmax."""
+    ids: torch.Tensor                          # int32 [T, topk], -1 where no expert is left
+    weights: torch.Tensor                      # fp32 [T, topk]
+    counts: torch.Tensor | None = None         # int32 [E], tokens of each expert
+    tokens: torch.Tensor | None = None         # int32 [], tokens that chose an expert
+    balance_loss: torch.Tensor | None = None   # fp32 []
+    z_loss: torch.Tensor | None = None         # fp32 []
+
+
+def _router_params(E, routing, renormalize, group_score):
+    r = routing or RoutingParams()
+    if r.scoring not in SCORING:
+        raise ValueError(f"scoring must be one of {list(SCORING)}, got {r.scoring!r}")
+    if group_score not in GROUP_SCORE:
+        raise ValueError(f"group_score must be one of {list(GROUP_SCORE)}, got {group_score!r}")
+    if r.bias is not None:
+        _dense(r.bias, "bias", torch.float32, (E,))
+    return _RouterParams(SCORING[r.scoring], r.n_group, r.topk_group, GROUP_SCORE[group_score], int(bool(renormalize)),
+                         r.routed_scaling, _or_none(r.bias))
+
+
+def moe_router(logits, topk, renormalize=True, routing: RoutingParams | None = None, group_score="top2", valid=None,
+               losses=False) -> Router:
+    """The router in its training form, for logits [T, E] (bf16, fp16 or fp32): softmax or sigmoid scores, a selection bias
+    and groups with either (routing; group_score "top2": a group's value is the sum of its two largest keys, "max":
+    its largest), the topk experts of each token with their weights.  valid: bool or uint8 [T], false for padded tokens, which
+    get ids -1.  losses: also the experts' loads, the balance loss and (softmax) the z loss, as include/moefp8.h
+    defines them."""
+    code, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    prm = _router_params(E, routing, renormalize, group_score)
+    if valid is not None:
+        if valid.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"valid must be bool or uint8, got {valid.dtype}")
+        _dense(valid, "valid", valid.dtype, (T,))
+    if not 0 < topk <= _INT_MAX:
+        raise ValueError(f"topk must be positive, got {topk}")
+    bias = routing.bias if routing else None
+    stream = _training_stream("moe_router", "logits bias valid", logits, bias, valid)
+    L = lib()
+    r = Router(_matrix(T, topk, torch.int32), _matrix(T, topk, torch.float32))
+    counts = tokens = both = ws = None
+    wsb = 0
+    if losses:
+        counts, tokens, both = _vector(E, torch.int32), _empty_strided((), (), torch.int32), _vector(2, torch.float32)
+        wsb = L.moe_router_workspace_size(T, E)
+        ws = _vector(wsb, torch.uint8)
+        r.counts, r.tokens, r.balance_loss = counts, tokens, both[0]
+        r.z_loss = both[1] if prm.scoring == 0 else None
+    rc = L.moe_router(logits.data_ptr(), ld, code, T, E, topk, ctypes.byref(prm), _or_none(valid), r.ids.data_ptr(),
+                      r.weights.data_ptr(), _or_none(counts), _or_none(tokens), _or_none(both), _or_none(ws), wsb, stream)
+    _check("moe_router", rc)
+    return r
+
+
+def moe_router_backward(logits, router: Router, dweights, renormalize=True, routing: RoutingParams | None = None,
+                        balance_coef=0.0, z_coef=0.0):
+    """Gradient of the logits, [T, E] in their type, for dweights fp32 [T, topk]: of sum(dweights * weights) +
+    balance_coef * balance_loss + z_coef * z_loss (z_coef: softmax), the choice and the loads taken as constants.
+    router: moe_router's result (with losses=True where a coefficient is not 0)."""
+    code, ld = _rows(logits, "logits")
+    T, E = logits.shape
+    prm = _router_params(E, routing, renormalize, "top2")
+    prm.n_group = 1   # the choice is made
+    ids = router.ids
+    _cuda(ids, torch.int32, "router.ids")
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"router.ids must be [{T}, topk], got {list(ids.shape)}")
+    k = ids.shape[1]
+    _dense(dweights, "dweights", torch.float32, (T, k))
+    counts = tokens = None
+    if balance_coef != 0.0 or z_coef != 0.0:
+        if router.counts is None or router.tokens is None:
+            raise ValueError("balance_coef and z_coef need a router of losses=True")
+        counts, tokens = router.counts, router.tokens
+        _dense(counts, "router.counts", torch.int32, (E,))
+        _dense(tokens, "router.tokens", torch.int32, ())
+    if z_coef != 0.0 and prm.scoring != 0:
+        raise ValueError("z_coef goes with softmax scores")
+    stream = _training_stream("moe_router_backward", "logits router.ids dweights router.counts router.tokens", logits, ids,
+                              dweights, counts, tokens)
+    out = _matrix(T, E, logits.dtype)
+    rc = lib().moe_router_backward(logits.data_ptr(), ld, code, T, E, k, ctypes.byref(prm), ids.data_ptr(),
+                                   dweights.data_ptr(), _or_none(counts), _or_none(tokens), balance_coef, z_coef,
+                                   out.data_ptr(), stream)
+    _check("moe_router_backward", rc)
+    return out
+
+
+def moe_router_update_bias(bias, counts, rate):
+    """The balancing bias fp32 [E] after a step, in place: += rate for experts whose count (moe_router's counts, or
+    sums of them) is below the mean, -= rate above."""
+    _cuda(bias, torch.float32, "bias")
+    if bias.dim() != 1:
+        raise ValueError(f"bias must be [E], got {list(bias.shape)}")
+    _dense(counts, "counts", torch.int32, tuple(bias.shape))
+    stream = _stream("bias counts", bias, counts)
+    _check("moe_router_update_bias", lib().moe_router_update_bias(bias.data_ptr(), counts.data_ptr(), bias.shape[0],
+                                                                  float(rate), stream))
+    torch.autograd.graph.increment_version([bias])
+
+
 # ---- 4-bit rows and weights (C ABI section "4-bit rows and weights") -------------------------
 
 FP4_FORMAT = {"mxfp4": 0, "nvfp4": 1}
@@ -1051,10 +1174,6 @@ def _fp4_rows(rows):
     elif rows.row_scale is not None:
         raise ValueError("mxfp4 rows have no row_scale")
     return fmt, E, n, K
-
-
-def _or_none(t):
-    return None if t is None else t.data_ptr()
 
 
 def moe_fp4_dequant(rows: Fp4Rows, dtype=torch.bfloat16):

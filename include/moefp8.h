@@ -52,6 +52,7 @@ extern "C" {
 #define MOE_STATUS_BAD_EXPERT_ID 0x2u     /* a routed id was outside [0, E); pair dropped */
 #define MOE_STATUS_BAD_COUNT 0x4u         /* a masked-layout count or an expert's row offset was out of range; clamped */
 #define MOE_STATUS_BAD_SCALE 0x8u         /* a scale packed as UE8M0 was not a positive power of two */
+#define MOE_STATUS_BAD_LOGIT 0x10u        /* moe_router: a logit was NaN or +infinity; counted as -infinity */
 
 /* Limits of this implementation. */
 #define MOE_MAX_EXPERTS 1024
@@ -615,6 +616,50 @@ int moe_expert_gemm_dgrad(const void* dc, int64_t lddc, int dtype, const void* w
 int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* a, int64_t lda, int dtype,
                           const int32_t* expert_offsets, int64_t num_rows, int E, int N, int K, void* dw,
                           void* stream);
+
+/* The router in its training form: logits of any of the types, a bias and groups with either scoring, a mask for padded
+ * tokens, the experts' loads and the losses that keep them even, and the gradient of the logits.  (moe_route_topk, which the
+ * layer's forward runs, takes fp32 logits, bias and groups with sigmoid only.)
+ *   score    s = softmax(l) or sigmoid(l); key = s + bias, or the order of the logits where bias is NULL
+ *   groups   (n_group > 1) E / n_group consecutive experts; the topk_group groups whose value, the sum of the two
+ *            largest keys or the largest (MOE_GROUP_*), is largest stay (ties: lower group)
+ *   choice   the topk largest keys (ties: lower expert), as the real numbers are ordered; a logit of -infinity is never
+ *            chosen, and NaN and +infinity count as that (MOE_STATUS_BAD_LOGIT); slots without an expert hold id -1, weight 0
+ *   weights  routed_scaling * s, divided by the sum of the chosen s with renormalize
+ * logits [T, E] with row stride ld; bias fp32 [E] or NULL; valid: bytes [T], 0 = a padded token (all ids -1), or NULL;
+ * ids int32 [T, topk], weights fp32 [T, topk], descending keys (moe_dispatch drops the -1).
+ * counts int32 [E], tokens int32 [1], losses fp32 [2], all three or none (NULL): the tokens of each expert, n = the tokens
+ * that chose an expert, and
+ *   losses[0] = sum_e (E * counts[e] / (topk * n)) * mean_t(P[t, e]),  P = s / sum_e(s)   (balance)
+ *   losses[1] = mean_t(logsumexp(l[t])^2)   (softmax; 0 with sigmoid)
+ * over those n (0 where n = 0).  workspace (with counts): device scratch of moe_router_workspace_size(T, E) bytes, 4-byte
+ * aligned.  Errors: UNSUPPORTED_SHAPE (E > 1024, topk > min(E, 32), E % n_group, n_group > 32, topk over the experts of
+ * topk_group groups). */
+#define MOE_GROUP_TOP2 0
+#define MOE_GROUP_MAX 1
+typedef struct moe_router_params {
+    int32_t scoring;        /* MOE_SCORING_* */
+    int32_t n_group;        /* 1 = ungrouped */
+    int32_t topk_group;
+    int32_t group_score;    /* MOE_GROUP_* */
+    int32_t renormalize;
+    float routed_scaling;
+    const float* bias;      /* device fp32 [E] or NULL; not part of the weights, no gradient */
+} moe_router_params;
+size_t moe_router_workspace_size(int T, int E);
+int moe_router(const void* logits, int64_t ld, int dtype, int T, int E, int topk, const moe_router_params* params,
+               const uint8_t* valid, int32_t* ids, float* weights, int32_t* counts, int32_t* tokens, float* losses,
+               void* workspace, size_t workspace_bytes, void* stream);
+/* The gradient of the logits, dlogits [T, E] dense in their type, for dweights fp32 [T, topk] and the losses'
+ * coefficients: of sum(dweights * weights) + balance_coef * losses[0] + z_coef * losses[1] (z_coef: softmax), the choice and
+ * counts taken as constants.  ids (distinct in a token), counts, tokens: moe_router's (counts with balance_coef, tokens with
+ * either, else NULL); a token without ids has gradient zero.  Of params, scoring, renormalize and routed_scaling count.
+ * An id >= E is dropped and sets MOE_STATUS_BAD_EXPERT_ID. */
+int moe_router_backward(const void* logits, int64_t ld, int dtype, int T, int E, int topk, const moe_router_params* params,
+                        const int32_t* ids, const float* dweights, const int32_t* counts, const int32_t* tokens,
+                        float balance_coef, float z_coef, void* dlogits, void* stream);
+/* The balancing bias after a step: bias[e] += rate where counts[e] is below the mean of counts [E], -= rate where above. */
+int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate, void* stream);
 
 /* ---- 4-bit rows and weights (microscaled floating point) -----------------------------------
  * e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte along K, the first in the low half, with a
