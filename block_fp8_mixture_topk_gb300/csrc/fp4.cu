@@ -4,86 +4,43 @@
 //   mxfp4  scale = the smallest power of two s with max|x| <= 6 s, code = e2m1(x / s): x / s is exact
 //   nvfp4  r = fp32(max|x of the row| / 2688), b = e4m3(max|x of the group| / (6 r)), code = e2m1(x / (b r)): the
 //          quotients are taken in fp32 a little too large and a little too small; where the two round differently,
-//          a comparison with the border itself, exact in fp64, decides
+//          a comparison with the border itself, its product exact in two fp32 parts, decides (with 16-bit rows a few
+//          per cent of the groups: their quotients are often nearly a border; in fp64 the kernel took 5 times as long)
 // An infinity or NaN makes its group (mxfp4: scale NaN) or row (nvfp4: row scale NaN) NaN.
 //
-// Memory is the bound: a row's vectors of eight elements are loaded once, all of them before the first is used,
-// and stay in registers (32 to 1024 threads to a row, up to four vectors each); the codes go out as whole words, the
-// scales as words of four groups put together across lanes.
+// Memory is the bound: a thread loads its two vectors of 16 elements whole (32 bytes at a time) before it uses the first,
+// so a group is one lane's or two lanes'; they stay in registers for the row's maximum (32 to 1024 threads to a row).
+// The codes go out as eight bytes a vector, the scales as words of four groups put together across lanes.
 #include "fp4.cuh"
 
 namespace mfp8 {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kVecs = 4;   // vectors of 8 elements a thread
+constexpr int kQuantVecs = 2;   // vectors of 16 elements a thread
 
-// 8 elements from p (16-byte addresses unless !ALIGNED).
-template <class T, bool ALIGNED>
-struct Vec8 {
-    static constexpr int kRaw = sizeof(T) == 4 ? 2 : 1;
-    uint4 raw[kRaw];
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (ALIGNED) {
-#pragma unroll
-            for (int i = 0; i < kRaw; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        } else {
-            T* e = reinterpret_cast<T*>(raw);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = p[i];
-        }
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < kRaw; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const T*>(raw)[i]); }
-    // bits of the largest magnitude: they order as the magnitudes do, infinity and NaN above
-    __device__ __forceinline__ uint32_t top() const {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(get(i)) & 0x7fffffffu);
-        return m;
-    }
-};
-
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
-        : "=r"(r)
-        : "f"(hi), "f"(lo));
-    return r;
+// Whether a >= 0 is rounded up from code c past the border m r to the next: m has few bits, the product's two parts are
+// exact (r not below kLeastRow), ties go to the even code.
+__device__ __forceinline__ bool past_border(float a, float m, float r, uint32_t c) {
+    const float p = m * r, rest = fmaf(m, r, -p);
+    return a > p || (a == p && (rest < 0.0f || (rest == 0.0f && (c & 1u))));
 }
-// codes of x[i] * f, one word
-template <class V>
-__device__ __forceinline__ uint32_t e2m1_word(const V& x, float f) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w |= e2m1_pair(x.get(2 * i) * f, x.get(2 * i + 1) * f) << (8 * i);
-    return w;
+// Border between e2m1 codes c and c + 1.
+__device__ __forceinline__ float e2m1_border(uint32_t c) {
+    return 0.25f * static_cast<float>(static_cast<uint32_t>(0x00140e0a07050301ull >> (8 * c)) & 0xffu);
 }
 
-// e2m1(x / d) by the borders between the codes: d has at most 28 bits and a border 3, so the products are exact.
-__device__ __forceinline__ uint32_t e2m1_exact(float x, double d) {
+// Row scales below kLeastRow, in fp64: e2m1(x / d), e4m3(x / (6 r)) by the borders between codes.
+__device__ __noinline__ uint32_t e2m1_tiny(float x, double d) {
     const double a = fabs(static_cast<double>(x));
-    const float border[7] = {0.25f, 0.75f, 1.25f, 1.75f, 2.5f, 3.5f, 5.0f};
     uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < 7; ++i) {
-        const double t = border[i] * d;
+    for (uint32_t i = 0; i < 7; ++i) {
+        const double t = e2m1_border(i) * d;
         c += a > t || (a == t && (i & 1)) ? 1u : 0u;
     }
     return c | (__float_as_uint(x) >> 31 << 3);
 }
-template <class V>
-__device__ __noinline__ uint32_t e2m1_word_exact(V x, double d) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w |= e2m1_exact(x.get(i), d) << (4 * i);
-    return w;
-}
-// e4m3(x / (6 r)) for x >= 0, r > 0, likewise: the border to the next number has 5 bits.
-__device__ __noinline__ uint32_t e4m3_exact(float x, float r) {
+__device__ __noinline__ uint32_t e4m3_tiny(float x, float r) {
     const double d = 6.0 * static_cast<double>(r);
     const uint32_t near = e4m3x2(static_cast<float>(fmin(static_cast<double>(x) / d, 448.0)), 0.0f) & 0x7fu;
     uint32_t c = near > 0 ? near - 1 : 0;
@@ -105,86 +62,102 @@ struct QuantArgs {
     uint8_t* tiles;
     uint8_t* plain;
     float* row_scale;
+    int align;                 // bytes of which every row's address is a multiple: 32, 16 or less
+    int warps;                 // of a row
 };
 
 constexpr float kSlack = 0x1p-21f;       // over the error of a quotient or product of a few fp32 operations
-constexpr float kLeastRow = 0x1p-100f;   // row scales below: fp64 throughout
+constexpr float kLeastRow = 0x1p-100f;
 
-template <class T, int FMT, bool ALIGNED>
-__global__ void __launch_bounds__(1024) fp4_quant_kernel(const QuantArgs a, int tpr) {
+// A group's scale byte and its part's codes, nvfp4 (rs > 0).
+template <class T>
+__device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top, float rs, uint2* codes) {
+    const float g = __uint_as_float(top);
+    *codes = make_uint2(0, 0);
+    if (rs < kLeastRow) {
+        const uint32_t s = e4m3_tiny(g, rs);
+        if (s > 0) {
+            const double d = static_cast<double>(e4m3_number(s)) * static_cast<double>(rs);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                codes->x |= e2m1_tiny(x.get(i), d) << (4 * i);
+                codes->y |= e2m1_tiny(x.get(8 + i), d) << (4 * i);
+            }
+        }
+        return s;
+    }
+    const float t = __fdividef(g, 6.0f * rs);
+    const uint32_t two = e4m3x2(t * (1.0f - kSlack), t * (1.0f + kSlack));
+    uint32_t s = two & 0xffu;
+    if (s != two >> 8) s += past_border(g, 3.0f * (e4m3_number(s) + e4m3_number(s + 1)), rs, s) ? 1u : 0u;
+    if (s == 0) return 0;
+    const float b = e4m3_number(s), f = __fdividef(1.0f, b * rs);
+    uint2 lo = e2m1_words(x, f * (1.0f - kSlack));
+    const uint2 hi = e2m1_words(x, f * (1.0f + kSlack));
+    if (lo.x != hi.x || lo.y != hi.y) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            uint32_t& w = i < 8 ? lo.x : lo.y;
+            const uint32_t c = w >> (4 * (i & 7)) & 7u;
+            if (((w ^ (i < 8 ? hi.x : hi.y)) >> (4 * (i & 7)) & 0xfu) && past_border(fabsf(x.get(i)), e2m1_border(c) * b, rs, c))
+                w += 1u << (4 * (i & 7));
+        }
+    }
+    *codes = lo;
+    return s;
+}
+
+template <class T, int FMT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) fp4_quant_kernel(const QuantArgs a) {
     grid_dependency_wait();
-    constexpr int G = fp4_group(FMT), LANES = G / 8, W = fp4_words(FMT);   // lanes of a group
+    constexpr int G = fp4_group(FMT), LANES = G / 16, W = fp4_words(FMT);   // lanes of a group
     __shared__ uint32_t s_top[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int at = threadIdx.x % tpr;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int own = warp / a.warps, tpr = a.warps * 32;     // the block's row
+    const int at = threadIdx.x - own * tpr;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / a.warps) + own;
     const bool live = r < a.rows;
-    const int KB = fp4_blocks(a.K), vecs = a.K / 8;
+    const int KB = fp4_blocks(a.K), vecs = a.K / 16;
     const T* row = static_cast<const T*>(a.x) + r * a.ld;
-    Vec8<T, ALIGNED> x[kVecs];
+    Vec16<T> x[kQuantVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < kQuantVecs; ++i) {
         const int v = at + i * tpr;
-        if (live && v < vecs) x[i].load(row + v * 8);
+        if (live && v < vecs) x[i].load(row + v * 16, a.align);
         else x[i].zero();
     }
-    uint32_t top[kVecs];
+    Fp4Place place = {0, 0};
+    if (a.tiles && live) place = fp4_place(a.offsets, a.E, r);
+    uint32_t top[kQuantVecs];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < kQuantVecs; ++i) {
         top[i] = x[i].top();
-#pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) top[i] = max(top[i], __shfl_xor_sync(kAll, top[i], o));
+        if (LANES == 2) top[i] = max(top[i], __shfl_xor_sync(kAll, top[i], 1));
     }
     float rs = 1.0f;
     if constexpr (FMT == MOE_FP4_NVFP4) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) m = max(m, top[i]);
-        m = __reduce_max_sync(kAll, m);
-        if (tpr > 32) {
+        uint32_t m = __reduce_max_sync(kAll, max(top[0], top[1]));
+        if (a.warps > 1) {
             if (lane == 0) s_top[warp] = m;
             __syncthreads();
-            const int first = warp / (tpr / 32) * (tpr / 32);
-            m = __reduce_max_sync(kAll, lane < tpr / 32 ? s_top[first + lane] : 0u);
+            m = __reduce_max_sync(kAll, lane < a.warps ? s_top[own * a.warps + lane] : 0u);
         }
         rs = m < 0x7f800000u ? __fdiv_rn(__uint_as_float(m), 2688.0f) : __int_as_float(0x7fffffff);
         if (live && at == 0) a.row_scale[r] = rs;
     }
-    if (!live) return;   // (whole warps: tpr is a multiple of 32)
-    Fp4Place place = {0, 0};
-    if (a.tiles) place = fp4_place(a.offsets, a.E, r);
-    uint8_t* tile = a.tiles + (place.tile * KB * 2 + (place.in >> 7)) * (W * 512);
-    uint32_t* codes = reinterpret_cast<uint32_t*>(a.codes + r * (a.K / 2));
+    if (!live) return;   // (whole warps)
+    uint8_t* tile = fp4_scale_row(a.tiles, place.tile, place.in, KB, W);
+    uint2* codes = reinterpret_cast<uint2*>(a.codes + r * (a.K / 2));
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < kQuantVecs; ++i) {
         const int v = at + i * tpr;
-        if (v >= KB * 32) break;   // (whole warps)
-        uint32_t s, w;
+        if ((v & ~31) >= KB * 16) break;   // (whole warps)
+        uint32_t s = 0;
+        uint2 w = make_uint2(0, 0);
         if constexpr (FMT == MOE_FP4_MXFP4) {
-            const uint32_t e = top[i] >> 23;
-            const int byte = static_cast<int>(e) - ((top[i] & 0x7fffffu) > 0x400000u ? 1 : 2);
-            s = e == 255 ? 255u : static_cast<uint32_t>(max(byte, 0));
-            w = e == 255 ? 0u : e2m1_word(x[i], __uint_as_float((254u - s) << 23));   // 2^-(s - 127)
-        } else {
-            s = 0;
-            w = 0;
-            if (rs > 0.0f) {   // not zero and not NaN
-                const float g = __uint_as_float(top[i]);
-                bool exact = rs < kLeastRow;
-                if (!exact) {
-                    const float t = __fdividef(g, 6.0f * rs);
-                    s = e4m3x2(t * (1.0f - kSlack), t * (1.0f + kSlack));
-                    exact = (s & 0x7fu) != (s >> 8);
-                    s &= 0x7fu;
-                }
-                if (exact) s = e4m3_exact(g, rs);
-                if (s > 0) {
-                    const float b = e4m3_number(s), f = __fdividef(1.0f, b * rs);
-                    w = e2m1_word(x[i], f * (1.0f + kSlack));
-                    if (rs < kLeastRow || w != e2m1_word(x[i], f * (1.0f - kSlack)))
-                        w = e2m1_word_exact(x[i], static_cast<double>(b) * static_cast<double>(rs));
-                }
-            }
+            s = mxfp4_group(x[i], top[i], &w);
+        } else if (rs > 0.0f) {   // not zero and not NaN
+            s = nvfp4_group(x[i], top[i], rs, &w);
         }
         if (v < vecs) codes[v] = w;
         else s = 0;   // columns past K: a scale that is a number
@@ -193,15 +166,16 @@ __global__ void __launch_bounds__(1024) fp4_quant_kernel(const QuantArgs a, int 
             uint32_t word = s << (8 * (c & 3));
 #pragma unroll
             for (int o = LANES; o < 4 * LANES; o <<= 1) word |= __shfl_xor_sync(kAll, word, o);
-            const int kb = v >> 5;
-            if (lane % (4 * LANES) == 0)
-                *reinterpret_cast<uint32_t*>(tile + static_cast<int64_t>(kb) * (2 * W * 512) +
-                                             fp4_word(place.in & 127, (c >> 2) % W)) = word;
+            const int kb = v >> 4;
+            if (lane % (4 * LANES) == 0 && kb < KB)
+                *reinterpret_cast<uint32_t*>(tile + static_cast<int64_t>(kb) * (2 * W * 512) + (c >> 2) % W * 512) = word;
         } else if (lane % LANES == 0 && v < vecs) {
             a.plain[r * (a.K / G) + c] = static_cast<uint8_t>(s);
         }
     }
 }
+
+constexpr int kVecs = 4;   // vectors of 8 elements a thread, of the values' kernel
 
 struct DequantArgs {
     const uint8_t* codes;
@@ -304,16 +278,21 @@ RowPlan row_plan(int64_t rows, int K) {
 }
 
 template <class T, int FMT>
-cudaError_t quant_type(const QuantArgs& a, bool on16, cudaStream_t stream) {
-    const RowPlan p = row_plan(a.rows, a.K);
-    return on16 ? launch_pdl(fp4_quant_kernel<T, FMT, true>, dim3(p.blocks), dim3(p.threads), 0, stream, a, p.tpr)
-                : launch_pdl(fp4_quant_kernel<T, FMT, false>, dim3(p.blocks), dim3(p.threads), 0, stream, a, p.tpr);
+cudaError_t quant_type(QuantArgs a, cudaStream_t stream) {
+    const uintptr_t bits = address(a.x) | (a.rows > 1 ? static_cast<uintptr_t>(a.ld) * sizeof(T) : 0);
+    a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+    const int all = fp4_blocks(a.K) * 16;                                       // vectors of a row
+    a.warps = (all + 32 * kQuantVecs - 1) / (32 * kQuantVecs);
+    const int per = a.warps < 8 ? 8 / a.warps : 1;                              // rows of a block of up to 256 threads
+    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(32 * a.warps * per);
+    return a.warps <= 8 ? launch_pdl(fp4_quant_kernel<T, FMT, 256>, grid, block, 0, stream, a)
+                        : launch_pdl(fp4_quant_kernel<T, FMT, 1024>, grid, block, 0, stream, a);
 }
 template <int FMT>
-cudaError_t quant_format(int dtype, const QuantArgs& a, bool on16, cudaStream_t stream) {
-    return dtype == MOE_DTYPE_BF16   ? quant_type<__nv_bfloat16, FMT>(a, on16, stream)
-           : dtype == MOE_DTYPE_FP16 ? quant_type<__half, FMT>(a, on16, stream)
-                                     : quant_type<float, FMT>(a, on16, stream);
+cudaError_t quant_format(int dtype, const QuantArgs& a, cudaStream_t stream) {
+    return dtype == MOE_DTYPE_BF16   ? quant_type<__nv_bfloat16, FMT>(a, stream)
+           : dtype == MOE_DTYPE_FP16 ? quant_type<__half, FMT>(a, stream)
+                                     : quant_type<float, FMT>(a, stream);
 }
 template <int FMT>
 cudaError_t dequant_format(int dtype, const DequantArgs& a, cudaStream_t stream) {
@@ -398,11 +377,10 @@ int moe_fp4_quant(const void* x, int64_t ldx, int dtype, int fmt, const int32_t*
         return MOE_ERR_INVALID_ARG;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
-    const QuantArgs a = {x, ldx, num_rows, K, E, expert_offsets, codes, scales, nullptr, row_scale};
-    const bool on16 = address(x) % 16 == 0 && (num_rows == 1 || ldx * dtype_bytes(dtype) % 16 == 0);
+    const QuantArgs a = {x, ldx, num_rows, K, E, expert_offsets, codes, scales, nullptr, row_scale, 0, 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(fmt == MOE_FP4_MXFP4 ? quant_format<MOE_FP4_MXFP4>(dtype, a, on16, s)
-                                            : quant_format<MOE_FP4_NVFP4>(dtype, a, on16, s));
+    return cuda_status(fmt == MOE_FP4_MXFP4 ? quant_format<MOE_FP4_MXFP4>(dtype, a, s)
+                                            : quant_format<MOE_FP4_NVFP4>(dtype, a, s));
 }
 
 int moe_fp4_dequant(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt,
@@ -430,8 +408,8 @@ int moe_mxfp4_quant_weight(const void* w, int dtype, int E, int N, int K, uint8_
     if (!w || !codes || !scales || address(w) % 16 || address(codes) % 16) return MOE_ERR_INVALID_ARG;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
-    const QuantArgs a = {w, K, rows, K, 0, nullptr, codes, nullptr, scales, nullptr};
-    return cuda_status(quant_format<MOE_FP4_MXFP4>(dtype, a, true, static_cast<cudaStream_t>(stream)));
+    const QuantArgs a = {w, K, rows, K, 0, nullptr, codes, nullptr, scales, nullptr, 0, 0};
+    return cuda_status(quant_format<MOE_FP4_MXFP4>(dtype, a, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate_up, uint8_t* out, void* stream) {
@@ -450,20 +428,22 @@ int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate
 
 int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt, const uint8_t* w_codes,
                         const uint8_t* w_scales, const float* w_global, const int32_t* expert_offsets, int64_t num_rows,
-                        int E, int N, int K, int epilogue, int dtype, void* out, void* stream) {
-    const bool silu = epilogue == MOE_EXPERT_SILU_MUL;
+                        int E, int N, int K, int epilogue, int dtype, void* out, uint8_t* out_scales, void* stream) {
+    const bool quant = epilogue == MOE_EXPERT_SILU_MUL_QUANT, silu = epilogue == MOE_EXPERT_SILU_MUL || quant;
     if (!silu && epilogue != MOE_EXPERT_STORE) return MOE_ERR_INVALID_ARG;
+    if (quant && (fmt != MOE_FP4_MXFP4 || dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARG;
     int rc = check_rows(fmt, dtype, expert_offsets, expert_offsets ? E : 0, num_rows, K);
     if (rc != MOE_OK) return rc;
     if (E < 1 || N < 1 || (!expert_offsets && E != 1) || (silu && dtype == MOE_DTYPE_FP32)) return MOE_ERR_INVALID_ARG;
-    if (N % (silu ? 32 : 8) != 0 || N >= (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (N % (quant ? 64 : silu ? 32 : 8) != 0 || N >= (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
     const bool nv = fmt == MOE_FP4_NVFP4;
     if (!w_codes || !w_scales || (w_global != nullptr) != nv || (row_scale != nullptr) != (nv && num_rows > 0))
         return MOE_ERR_INVALID_ARG;
     if (address(w_codes) % 16 || address(w_scales) % 16 || address(w_global) % 4 || address(row_scale) % 4)
         return MOE_ERR_INVALID_ARG;
     if (num_rows == 0) return MOE_OK;
-    if (!codes || !scales || !out || address(codes) % 16 || address(scales) % 16 || address(out) % 16)
+    if (!codes || !scales || !out || address(codes) % 16 || address(scales) % 16 || address(out) % 16 ||
+        (out_scales != nullptr) != quant || address(out_scales) % 16)
         return MOE_ERR_INVALID_ARG;
     const size_t scale_bytes = moe_fp4_row_scale_bytes(fmt, num_rows, expert_offsets ? E : 0, K);
     const size_t w_scale_bytes = moe_fp4_weight_scale_bytes(fmt, E, N, K);
@@ -473,12 +453,12 @@ int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float
     CUtensorMap tm[5];
     if (fp4_maps(tm, codes, scales, scale_bytes, fmt, w_codes, w_scales, w_scale_bytes, num_rows, E, N, K, silu) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const Fp4Args a = {expert_offsets, E, num_rows, N, K, row_scale, w_global, out, status};
+    const Fp4Args a = {expert_offsets, E, num_rows, N, K, row_scale, w_global, out, out_scales, status};
     const int64_t row_tiles = num_rows / kFp4Rows + (num_rows < E ? num_rows : E) + 1;
     const int64_t items = row_tiles * (silu ? (N / 2 + 127) / 128 : (N + 255) / 256);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(nv ? fp4_experts_launch<MOE_FP4_NVFP4>(dtype, silu, a, tm, items, s)
-                          : fp4_experts_launch<MOE_FP4_MXFP4>(dtype, silu, a, tm, items, s));
+    return cuda_status(nv ? fp4_experts_launch<MOE_FP4_NVFP4>(dtype, epilogue, a, tm, items, s)
+                          : fp4_experts_launch<MOE_FP4_MXFP4>(dtype, epilogue, a, tm, items, s));
 }
 
 }  // extern "C"

@@ -14,6 +14,8 @@
 //           than floor(o/224) + n/224.)  Rows of no expert follow as an expert E.
 #pragma once
 
+#include <type_traits>
+
 #include "train.cuh"
 
 namespace mfp8 {
@@ -28,6 +30,12 @@ __host__ __device__ __forceinline__ int fp4_blocks(int K) { return (K + kFp4Bloc
 
 // Byte of the first scale of word j of row `in` (0 .. 127) in 128 rows' tiles of one K block.
 __host__ __device__ __forceinline__ int fp4_word(int in, int j) { return j * 512 + (in & 31) * 16 + (in >> 5) * 4; }
+
+// Tile of an expert's first rows, which begin at row o; the scales' bytes of row `in` of a tile (word 0 of K block 0).
+__host__ __device__ __forceinline__ int64_t fp4_tile(int64_t o, int e) { return o / kFp4Rows + e; }
+__device__ __forceinline__ uint8_t* fp4_scale_row(uint8_t* tiles, int64_t tile, int in, int blocks, int words) {
+    return tiles + (tile * blocks * 2 + (in >> 7)) * (words * 512) + fp4_word(in & 127, 0);
+}
 
 // The tile and the place in it of row r, found by a whole warp: e is the last expert whose rows begin at or before
 // r, o where they begin.  Offsets out of order or range count as the running maximum of the clamped ones, from 0,
@@ -69,6 +77,97 @@ __device__ __forceinline__ float ue8m0_number(uint32_t byte) {   // 255 is NaN
     return byte == 255 ? __int_as_float(0x7fffffff) : byte ? __uint_as_float(byte << 23) : __uint_as_float(1u << 22);
 }
 
+// 16 elements.
+template <class T>
+struct Vec16 {
+    static constexpr int kWords = 4 * static_cast<int>(sizeof(T));
+    uint32_t w[kWords];
+    // from a row at 32-byte addresses, 16-byte ones or any
+    __device__ __forceinline__ void load(const T* p, int align) {
+        if (align == 32) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 8)
+                asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                               "=r"(w[i + 6]), "=r"(w[i + 7])
+                             : "l"(reinterpret_cast<const uint32_t*>(p) + i));
+        } else if (align == 16) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+                w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+            }
+        } else if constexpr (sizeof(T) == 2) {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = e[2 * i] | static_cast<uint32_t>(e[2 * i + 1]) << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    // elements 2 i and 2 i + 1
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else return __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    }
+    __device__ __forceinline__ float get(int i) const { return (i & 1) ? pair(i / 2).y : pair(i / 2).x; }
+    // fp32 bits of the largest magnitude: they order as the magnitudes do, infinity and NaN above
+    __device__ __forceinline__ uint32_t top() const {
+        if constexpr (sizeof(T) == 4) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+            uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) m = __vmaxs2(m, w[i] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
+            return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+        }
+    }
+};
+
+// Codes of x * f, two words.
+template <class V>
+__device__ __forceinline__ uint2 e2m1_words(const V& x, float f) {
+    uint32_t r[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float2 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul2(x.pair(4 * h + i), both(f));
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};\n\t}"
+            : "=r"(r[h])
+            : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
+    }
+    return make_uint2(r[0], r[1]);
+}
+
+// A group's UE8M0 byte and its part's codes, for the fp32 bits of its largest magnitude: the smallest power of two
+// that takes it to 6 or below; 255 (NaN) where it is not finite.
+template <class T>
+__device__ __forceinline__ uint32_t mxfp4_group(const Vec16<T>& x, uint32_t top, uint2* codes) {
+    const uint32_t e = top >> 23;
+    *codes = make_uint2(0, 0);
+    if (e == 255) return 255u;
+    const int byte = static_cast<int>(e) - ((top & 0x7fffffu) > 0x400000u ? 1 : 2);
+    const uint32_t s = static_cast<uint32_t>(max(byte, 0));
+    *codes = e2m1_words(x, __uint_as_float((254u - s) << 23));   // times 2^-(s - 127), exact
+    return s;
+}
+
 // fp4_mxfp4.cu, fp4_nvfp4.cu: the products, a format to a translation unit.  tm: weights' codes, rows' codes in boxes
 // of kFp4Rows / 2 and of 16 rows, weights' scales, rows' scales.
 struct Fp4Args {
@@ -79,12 +178,14 @@ struct Fp4Args {
     const float* row_scale;    // nvfp4
     const float* w_global;     // nvfp4, [E]
     void* out;
+    uint8_t* out_scales;       // kFp4SiluQuant
     uint32_t* status;
 };
+enum Fp4Mode { kFp4Store = MOE_EXPERT_STORE, kFp4Silu = MOE_EXPERT_SILU_MUL, kFp4SiluQuant = MOE_EXPERT_SILU_MUL_QUANT };
 template <int FMT>
 cudaError_t fp4_experts_init();
 template <int FMT>
-cudaError_t fp4_experts_launch(int dtype, bool silu, const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t most_items,
+cudaError_t fp4_experts_launch(int dtype, int mode, const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t most_items,
                                cudaStream_t stream);
 
 }  // namespace mfp8

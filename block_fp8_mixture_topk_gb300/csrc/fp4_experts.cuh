@@ -34,13 +34,13 @@ constexpr int F_THREADS = (F_FIRST_EPI + F_EPI_WARPS) * 32;
 constexpr uint32_t F_TMEM = 512;
 constexpr int F_GROUP = 4;                          // row tiles visited together
 constexpr int F_SLOT = 24;                          // columns of a slot of scales: 2 words of 128 and of 256 rows
-__host__ __device__ constexpr int f_stages(int fmt) { return fmt == MOE_FP4_MXFP4 ? 6 : 5; }
+constexpr int F_STAGES = 5;
 __host__ __device__ constexpr int f_scales(int fmt) { return 3 * fp4_words(fmt) * 512; }   // bytes of a stage
 __host__ __device__ constexpr int f_stage(int fmt) { return F_A + F_B + f_scales(fmt); }
 
 struct FCtl {
-    uint64_t full[6];           // (CTA 0) both CTAs' operands of the stage are in place
-    uint64_t empty[6];          // the stage's MMAs completed
+    uint64_t full[F_STAGES];    // (CTA 0) both CTAs' operands of the stage are in place
+    uint64_t empty[F_STAGES];   // the stage's MMAs completed
     uint64_t tfull[2];          // the accumulators are complete
     uint64_t tempty[2];         // (CTA 0) both CTAs' epilogue warps moved them out
     uint64_t drain;
@@ -51,7 +51,7 @@ struct FCtl {
     int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each expert
 };
 __host__ __device__ constexpr size_t f_smem(int fmt) {
-    return 1024 + static_cast<size_t>(f_stages(fmt)) * f_stage(fmt) + 2 * X_STAGED + sizeof(FCtl);
+    return 1024 + static_cast<size_t>(F_STAGES) * f_stage(fmt) + 4 * X_STAGED + sizeof(FCtl);
 }
 static_assert(f_smem(MOE_FP4_MXFP4) <= 232448 && f_smem(MOE_FP4_NVFP4) <= 232448, "more shared memory than a CTA has");
 static_assert(2 * (256 + F_SLOT) > static_cast<int>(F_TMEM) && F_N + F_SLOT <= 256, "an accumulator and a slot to each half");
@@ -117,19 +117,63 @@ __device__ __forceinline__ void f_copy_scales(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
-template <class T, int FMT, bool SILU>
+// A block of 32 rows in the warp's 32 tensor-memory lanes (output columns), as fragments of 16 lanes by 8 rows: element
+// 4 q + i of v[h] is lane 16 h + 8 (i / 2) + t / 4, row 8 q + 2 (t % 4) + i % 2 of thread t.  The values are there after
+// f_wait_block, which names them so that nothing reads them earlier.
+__device__ __forceinline__ void f_load_block(uint32_t taddr, float (&v)[2][16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+            "[%16];"
+            : "=f"(v[h][0]), "=f"(v[h][1]), "=f"(v[h][2]), "=f"(v[h][3]), "=f"(v[h][4]), "=f"(v[h][5]), "=f"(v[h][6]),
+              "=f"(v[h][7]), "=f"(v[h][8]), "=f"(v[h][9]), "=f"(v[h][10]), "=f"(v[h][11]), "=f"(v[h][12]), "=f"(v[h][13]),
+              "=f"(v[h][14]), "=f"(v[h][15])
+            : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16))
+            : "memory");
+}
+__device__ __forceinline__ void f_wait_block(float (&v)[2][16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0][0]), "+f"(v[0][1]), "+f"(v[0][2]), "+f"(v[0][3]), "+f"(v[0][4]), "+f"(v[0][5]), "+f"(v[0][6]),
+                   "+f"(v[0][7]), "+f"(v[0][8]), "+f"(v[0][9]), "+f"(v[0][10]), "+f"(v[0][11]), "+f"(v[0][12]),
+                   "+f"(v[0][13]), "+f"(v[0][14]), "+f"(v[0][15])
+                 :
+                 : "memory");
+    asm volatile(""
+                 : "+f"(v[1][0]), "+f"(v[1][1]), "+f"(v[1][2]), "+f"(v[1][3]), "+f"(v[1][4]), "+f"(v[1][5]), "+f"(v[1][6]),
+                   "+f"(v[1][7]), "+f"(v[1][8]), "+f"(v[1][9]), "+f"(v[1][10]), "+f"(v[1][11]), "+f"(v[1][12]),
+                   "+f"(v[1][13]), "+f"(v[1][14]), "+f"(v[1][15])
+                 :
+                 : "memory");
+}
+// Four 8 x 8 fragments of 16-bit values stored transposed, 16 bytes a row; lane t gives the address of row t % 8 of t / 8.
+__device__ __forceinline__ void f_store_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) return bf16x2(lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float silu_mul(float gate, float up) { return __fdividef(gate, 1.0f + __expf(-gate)) * up; }
+
+template <class T, int FMT, int MODE>
 __global__ void __launch_bounds__(F_THREADS, 1)
     fp4_expert_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmSA,
                       const __grid_constant__ CUtensorMap tmSB, const Fp4Args a) {
-    constexpr int STAGES = f_stages(FMT), W = fp4_words(FMT);
+    constexpr int STAGES = F_STAGES, W = fp4_words(FMT);
+    constexpr bool SILU = MODE != kFp4Store;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t* smA = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);   // [STAGES][F_A]
     uint8_t* smB = smA + STAGES * F_A;                                      // [STAGES][F_B]
     uint8_t* smS = smB + STAGES * F_B;                                      // [STAGES][weights W, rows 2 W][512]
-    uint8_t* smE = smS + STAGES * f_scales(FMT);                            // [2][X_STAGED]
-    FCtl* ctl = reinterpret_cast<FCtl*>(smE + 2 * X_STAGED);
+    uint8_t* smE = smS + STAGES * f_scales(FMT);                            // [2 halves][2][X_STAGED]
+    FCtl* ctl = reinterpret_cast<FCtl*>(smE + 4 * X_STAGED);
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
@@ -327,74 +371,150 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         }
     } else if (warp >= F_FIRST_EPI) {
         // ---------------------------------------------------------------- epilogue
+        // The four warps of a half take blocks of 32 rows in turn with the other half's: the accumulators' lanes are output
+        // columns, so a block is stored transposed into shared memory (16-bit results: 8 x 8 at a time by stmatrix) and
+        // leaves by whole rows; two buffers, so that one barrier a block is enough.
         const int g = (warp - F_FIRST_EPI) >> 2;
         const int sp = warp & 3;                   // tensor-memory lane quarter
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
         T* out = static_cast<T*>(a.out);
-        const Block block = {smE + g * X_STAGED, 1 + g, sp * 32 + lane};
-        uint32_t buf = 0, bphase = 0;
+        uint8_t* const stage0 = smE + g * (2 * X_STAGED);
+        const Block block = {stage0, 1 + g, sp * 32 + lane};
+        uint32_t buf = 0, bphase = 0, side = 0;
         bool ok = true;
         const uint32_t tempty0 = cluster_map(smem_addr(&ctl->tempty[0]), 0), tempty1 = cluster_map(smem_addr(&ctl->tempty[1]), 0);
         for (int64_t w = cluster; w < total; w += clusters) {
             const FItem t = f_item(a, ctl, w, NT);
             const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's columns
-            const int col = sp * 32 + lane;
             const int blocks = (t.nrow + 31) / 32;
-            float wg = 1.0f;
-            if constexpr (FMT == MOE_FP4_NVFP4) wg = __ldg(a.w_global + t.e);
+            float wg = 1.0f, rs = 0.0f;
+            const auto row_scale = [&](int blk) {   // of the lane's row, times the expert's
+                const int r = blk * 32 + lane;
+                return r < t.nrow ? __ldg(a.row_scale + t.r0 + r) * wg : 0.0f;
+            };
+            if constexpr (FMT == MOE_FP4_NVFP4) {
+                wg = __ldg(a.w_global + t.e);
+                if (g < blocks) rs = row_scale(g);
+            }
             ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
             if (!half_ok(ok, block, &ctl->half_bad[g])) break;
             tc_fence_after();
-            for (int blk = g; blk < blocks; blk += 2) {
-                float v[32];
-                const int64_t r0 = static_cast<int64_t>(t.r0) + blk * 32;
-                const int nrow = t.nrow - blk * 32;
-                float rs = 0.0f;
-                if constexpr (FMT == MOE_FP4_NVFP4) rs = lane < nrow ? __ldg(a.row_scale + r0 + lane) * wg : 0.0f;
-                tmem_ld32(lane_base + buf * 256 + blk * 32, v);
-                if constexpr (FMT == MOE_FP4_NVFP4) {
+            const uint32_t acc = lane_base + buf * 256;
+            if constexpr (sizeof(T) == 4) {
+                const int col = sp * 32 + lane;
+                for (int blk = g; blk < blocks; blk += 2) {
+                    float v[32];
+                    const int64_t r0 = static_cast<int64_t>(t.r0) + blk * 32;
+                    const int nrow = t.nrow - blk * 32;
+                    tmem_ld32(acc + blk * 32, v);
+                    if constexpr (FMT == MOE_FP4_NVFP4) {
+                        if (blk != g) rs = row_scale(blk);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, rs, i);
-                }
-                if constexpr (SILU) {
-                    // lanes: 16 gate columns, then the up columns of the same; hc: the column of h.  A gate lane
-                    // gives the up lane beside it its rows 16 .. 31 for that lane's up of rows 0 .. 15: each
-                    // then holds 16 rows of one column of h
-                    const bool up = (lane & 16) != 0;
-                    const int hc = sp * 16 + (lane & 15), first = up ? 16 : 0;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float o = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[16 + i], 16);
-                        const float gate = up ? o : v[i], u = up ? v[16 + i] : o;
-                        block.put<T>(first + i, hc, __fdividef(gate, 1.0f + __expf(-gate)) * u);
+                        for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, rs, i);
                     }
-                    block.sync();
-                    block.each_piece<8>([&](int, int r, int q, uint8_t* p) {
-                        if (r < nrow && c0 + q * 8 < OC)
-                            *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) = *reinterpret_cast<const uint4*>(p);
-                    });
-                    block.sync();
-                } else if constexpr (sizeof(T) == 4) {
                     // 16 rows of 128 columns at a time
                     constexpr int PITCH = 512 + 16;
                     static_assert(16 * PITCH <= X_STAGED, "a staged block");
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
+                        uint8_t* stage = stage0 + part * X_STAGED;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            *reinterpret_cast<float*>(block.stage + i * PITCH + col * 4) = v[part * 16 + i];
+                        for (int i = 0; i < 16; ++i) *reinterpret_cast<float*>(stage + i * PITCH + col * 4) = v[part * 16 + i];
                         block.sync();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int k = i * 128 + block.et, r = k >> 5, q = k & 31;
                             if (part * 16 + r < nrow && c0 + q * 4 < OC)
                                 *reinterpret_cast<uint4*>(out + (r0 + part * 16 + r) * OC + c0 + q * 4) =
-                                    *reinterpret_cast<const uint4*>(block.stage + r * PITCH + q * 16);
+                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
                         }
-                        block.sync();
                     }
-                } else {
-                    block.store<T>(v, col, out + r0 * OC, OC, nrow, c0, OC);
+                }
+            } else {
+                float v[2][16];
+                if (g < blocks) f_load_block(acc + g * 32, v);
+                for (int blk = g; blk < blocks; blk += 2) {
+                    f_wait_block(v);
+                    if constexpr (FMT == MOE_FP4_NVFP4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float s0 = __shfl_sync(0xffffffffu, rs, 8 * q + 2 * (lane & 3));
+                            const float s1 = __shfl_sync(0xffffffffu, rs, 8 * q + 2 * (lane & 3) + 1);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                v[h][4 * q] *= s0, v[h][4 * q + 2] *= s0;
+                                v[h][4 * q + 1] *= s1, v[h][4 * q + 3] *= s1;
+                            }
+                        }
+                        if (blk + 2 < blocks) rs = row_scale(blk + 2);
+                    }
+                    uint8_t* stage = stage0 + side * X_STAGED;
+                    side ^= 1u;
+                    constexpr int PITCH = SILU ? 128 + 16 : X_PITCH;
+                    if constexpr (SILU) {   // lanes 0 .. 15 gate, 16 .. 31 the up of the same columns
+                        const uint32_t to = smem_addr(stage) + ((lane >> 4) * 8 + (lane & 7)) * PITCH + sp * 32 + ((lane >> 3) & 1) * 16;
+#pragma unroll
+                        for (int q = 0; q < 4; q += 2) {
+                            uint32_t p[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                p[i] = pack2<T>(silu_mul(v[0][4 * q + 2 * i], v[1][4 * q + 2 * i]),
+                                                silu_mul(v[0][4 * q + 2 * i + 1], v[1][4 * q + 2 * i + 1]));
+                            f_store_turned(to + q * 8 * PITCH, p[0], p[1], p[2], p[3]);
+                        }
+                    } else {
+                        const uint32_t to = smem_addr(stage) + (lane & 7) * PITCH + sp * 64 + (lane >> 3) * 16;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            f_store_turned(to + q * 8 * PITCH, pack2<T>(v[0][4 * q], v[0][4 * q + 1]),
+                                           pack2<T>(v[0][4 * q + 2], v[0][4 * q + 3]), pack2<T>(v[1][4 * q], v[1][4 * q + 1]),
+                                           pack2<T>(v[1][4 * q + 2], v[1][4 * q + 3]));
+                    }
+                    if (blk + 2 < blocks) f_load_block(acc + (blk + 2) * 32, v);
+                    block.sync();
+                    const int64_t r0 = static_cast<int64_t>(t.r0) + blk * 32;
+                    const int nrow = t.nrow - blk * 32;
+                    if constexpr (MODE == kFp4SiluQuant) {
+                        // a thread 16 of a row's 64 columns, two threads a group
+                        const int r = block.et >> 2, part = block.et & 3, c = c0 + part * 16;
+                        Vec16<T> x;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 u = *reinterpret_cast<const uint4*>(stage + r * PITCH + part * 32 + i * 16);
+                            x.w[4 * i] = u.x, x.w[4 * i + 1] = u.y, x.w[4 * i + 2] = u.z, x.w[4 * i + 3] = u.w;
+                        }
+                        uint32_t top = x.top();
+                        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        uint2 codes;
+                        const uint32_t s = mxfp4_group(x, top, &codes);
+                        if (r < nrow) {
+                            const int in = blk * 32 + r, group = c >> 5;
+                            if (c < OC) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + (r0 + r) * (OC / 2) + c / 2) = codes;
+                            uint8_t* tile = fp4_scale_row(a.out_scales, fp4_tile(ctl->row0[t.e], t.e) + t.m, in, fp4_blocks(OC), 2);
+                            if ((part & 1) == 0)
+                                tile[(group >> 3) * 2048 + ((group >> 2) & 1) * 512 + (group & 3)] =
+                                    static_cast<uint8_t>(c < OC ? s : 0u);
+                            // the K block's other 128 columns, where no item has them
+                            if (t.n == NT - 1 && (NT & 1) && rank == 1 && part == 0)
+                                *reinterpret_cast<uint32_t*>(tile + (group >> 3) * 2048 + 512) = 0u;
+                        }
+                    } else if constexpr (SILU) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int k = i * 128 + block.et, r = k >> 3, q = k & 7;
+                            if (r < nrow && c0 + q * 8 < OC)
+                                *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) =
+                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = i * 128 + block.et, r = k >> 4, q = k & 15;
+                            if (r < nrow && c0 + q * 8 < OC)
+                                *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) =
+                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
+                        }
+                    }
                 }
             }
             tc_fence_before();
@@ -404,11 +524,22 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             if (buf == 0) bphase ^= 1u;
         }
         if (ok) {   // rows of no expert: zero
-            constexpr int PER = 16 / static_cast<int>(sizeof(T));
-            const int64_t first = ctl->row0[a.E], n = (a.rows - first) * OC / PER;
+            const int64_t first = ctl->row0[a.E], left = a.rows - first;
+            const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (F_EPI_WARPS * 32) + threadIdx.x - F_FIRST_EPI * 32;
             const int64_t step = static_cast<int64_t>(gridDim.x) * (F_EPI_WARPS * 32);
-            for (int64_t i = static_cast<int64_t>(blockIdx.x) * (F_EPI_WARPS * 32) + threadIdx.x - F_FIRST_EPI * 32; i < n; i += step)
-                reinterpret_cast<uint4*>(out + first * OC)[i] = make_uint4(0, 0, 0, 0);
+            const int64_t row_bytes = MODE == kFp4SiluQuant ? OC / 2 : static_cast<int64_t>(OC) * static_cast<int64_t>(sizeof(T));
+            uint4* zero = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + first * row_bytes);
+            for (int64_t i = i0; i < left * row_bytes / 16; i += step) zero[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (MODE == kFp4SiluQuant) {   // their scales: those of an expert E
+                const int words = fp4_blocks(OC) * 2;
+                for (int64_t i = i0; i < left * words; i += step) {
+                    const int64_t r = i / words;
+                    const int j = static_cast<int>(i - r * words), m = static_cast<int>(r / F_N);
+                    uint8_t* tile = fp4_scale_row(a.out_scales, fp4_tile(first, a.E) + m, static_cast<int>(r - static_cast<int64_t>(m) * F_N),
+                                                  words / 2, 2);
+                    *reinterpret_cast<uint32_t*>(tile + (j >> 1) * 2048 + (j & 1) * 512) = 0u;
+                }
+            }
         }
     }
 
@@ -439,39 +570,44 @@ void f_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int fmt, unsig
 template <int FMT>
 struct Fp4Launch {
     static int clusters;   // of two CTAs resident at once (the same for every instance: one CTA per SM)
-    template <class T, bool SILU>
+    template <class T, int MODE>
     static cudaError_t one(const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t most_items, cudaStream_t stream) {
         if (clusters < 1) return cudaErrorNotSupported;
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         f_config(&cfg, attr, FMT, static_cast<unsigned>(most_items < clusters ? most_items : clusters), stream);
-        return cudaLaunchKernelEx(&cfg, fp4_expert_kernel<T, FMT, SILU>, tm[0], tm[1], tm[2], tm[3], tm[4], a);
+        return cudaLaunchKernelEx(&cfg, fp4_expert_kernel<T, FMT, MODE>, tm[0], tm[1], tm[2], tm[3], tm[4], a);
     }
-    static cudaError_t launch(int dtype, bool silu, const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t items,
+    static cudaError_t launch(int dtype, int mode, const Fp4Args& a, const CUtensorMap (&tm)[5], int64_t items,
                               cudaStream_t s) {
-        if (silu) return dtype == MOE_DTYPE_BF16 ? one<__nv_bfloat16, true>(a, tm, items, s) : one<__half, true>(a, tm, items, s);
-        return dtype == MOE_DTYPE_BF16   ? one<__nv_bfloat16, false>(a, tm, items, s)
-               : dtype == MOE_DTYPE_FP16 ? one<__half, false>(a, tm, items, s)
-                                         : one<float, false>(a, tm, items, s);
+        if constexpr (FMT == MOE_FP4_MXFP4)
+            if (mode == kFp4SiluQuant) return one<__nv_bfloat16, kFp4SiluQuant>(a, tm, items, s);
+        if (mode == kFp4Silu)
+            return dtype == MOE_DTYPE_BF16 ? one<__nv_bfloat16, kFp4Silu>(a, tm, items, s) : one<__half, kFp4Silu>(a, tm, items, s);
+        return dtype == MOE_DTYPE_BF16   ? one<__nv_bfloat16, kFp4Store>(a, tm, items, s)
+               : dtype == MOE_DTYPE_FP16 ? one<__half, kFp4Store>(a, tm, items, s)
+                                         : one<float, kFp4Store>(a, tm, items, s);
     }
-    template <class T, bool SILU>
+    template <class T, int MODE>
     static cudaError_t smem() {
-        return cudaFuncSetAttribute(fp4_expert_kernel<T, FMT, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fp4_expert_kernel<T, FMT, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(f_smem(FMT)));
     }
     static cudaError_t init() {
-        cudaError_t e = smem<__nv_bfloat16, true>();
-        if (e == cudaSuccess) e = smem<__half, true>();
-        if (e == cudaSuccess) e = smem<__nv_bfloat16, false>();
-        if (e == cudaSuccess) e = smem<__half, false>();
-        if (e == cudaSuccess) e = smem<float, false>();
+        cudaError_t e = smem<__nv_bfloat16, kFp4Silu>();
+        if constexpr (FMT == MOE_FP4_MXFP4)
+            if (e == cudaSuccess) e = smem<__nv_bfloat16, kFp4SiluQuant>();
+        if (e == cudaSuccess) e = smem<__half, kFp4Silu>();
+        if (e == cudaSuccess) e = smem<__nv_bfloat16, kFp4Store>();
+        if (e == cudaSuccess) e = smem<__half, kFp4Store>();
+        if (e == cudaSuccess) e = smem<float, kFp4Store>();
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         f_config(&cfg, attr, FMT, 1, nullptr);
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fp4_expert_kernel<__nv_bfloat16, FMT, false>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, fp4_expert_kernel<__nv_bfloat16, FMT, kFp4Store>, &cfg) != cudaSuccess) {
             (void)cudaGetLastError();
             n = 0;
         }

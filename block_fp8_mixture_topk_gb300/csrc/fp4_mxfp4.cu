@@ -7,8 +7,8 @@ cudaError_t fp4_experts_init<MOE_FP4_MXFP4>() {
     return Fp4Launch<MOE_FP4_MXFP4>::init();
 }
 template <>
-cudaError_t fp4_experts_launch<MOE_FP4_MXFP4>(int dtype, bool silu, const Fp4Args& a, const CUtensorMap (&tm)[5],
+cudaError_t fp4_experts_launch<MOE_FP4_MXFP4>(int dtype, int mode, const Fp4Args& a, const CUtensorMap (&tm)[5],
                                               int64_t most_items, cudaStream_t stream) {
-    return Fp4Launch<MOE_FP4_MXFP4>::launch(dtype, silu, a, tm, most_items, stream);
+    return Fp4Launch<MOE_FP4_MXFP4>::launch(dtype, mode, a, tm, most_items, stream);
 }
 }  // namespace mfp8

@@ -153,7 +153,7 @@ def lib():
                 "moe_fp4_dequant": ([P, P, P, I, P, I, I64, I, I, P, P], I),
                 "moe_mxfp4_quant_weight": ([P, I, I, I, I, P, P, P], I),
                 "moe_fp4_pack_scales": ([P, I, I, I, I, I, P, P], I),
-                "moe_fp4_expert_gemm": ([P, P, P, I, P, P, P, P, I64, I, I, I, I, I, P, P], I),
+                "moe_fp4_expert_gemm": ([P, P, P, I, P, P, P, P, I64, I, I, I, I, I, P, P, P], I),
                 "moe_get_device_status": ([P, I], I),
                 "moe_selftest_bounded_wait": ([I, P], I),
                 "moe_error_string": ([I], ctypes.c_char_p),
@@ -1223,7 +1223,7 @@ def moe_fp4_pack_scales(scales, format="mxfp4", gate_up=False):
     return out
 
 
-def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, silu):
+def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, epilogue):
     fmt, E, n, K = _fp4_rows(rows)
     _cuda(w, torch.uint8, "w")
     if w.dim() != 3 or 2 * w.shape[2] != K or w.shape[0] != max(E, 1):
@@ -1231,10 +1231,11 @@ def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, silu):
     N = w.shape[1]
     if N > _INT_MAX:
         raise _too_large("w")
-    if dtype not in DTYPE or (silu and dtype == torch.float32):
-        raise TypeError(f"dtype must be bfloat16{', float16 or float32' if not silu else ' or float16'}, got {dtype}")
+    if dtype not in DTYPE or (epilogue and dtype == torch.float32):
+        raise TypeError(f"dtype must be bfloat16{' or float16' if epilogue else ', float16 or float32'}, got {dtype}")
     _cuda(w_scales, torch.uint8, "w_scales")
-    if w_scales.numel() != lib().moe_fp4_weight_scale_bytes(fmt, max(E, 1), N, K):
+    L = lib()
+    if w_scales.numel() != L.moe_fp4_weight_scale_bytes(fmt, max(E, 1), N, K):
         raise ValueError("w_scales must be moe_fp4_pack_scales of w's scales in the rows' format")
     if (w_global is None) != (fmt == 0):
         raise ValueError("w_global is needed with nvfp4, and only there")
@@ -1242,30 +1243,39 @@ def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, silu):
         _dense(w_global, "w_global", torch.float32, (max(E, 1),))
     stream = _stream("rows.codes rows.scales rows.row_scale rows.expert_offsets w w_scales w_global", rows.codes, rows.scales,
                      rows.row_scale, rows.expert_offsets, w, w_scales, w_global)
-    out = _matrix(n, N // 2 if silu else N, dtype)
-    rc = lib().moe_fp4_expert_gemm(rows.codes.data_ptr(), rows.scales.data_ptr(), _or_none(rows.row_scale) if n else None, fmt,
-                                   w.data_ptr(), w_scales.data_ptr(), _or_none(w_global), _or_none(rows.expert_offsets), n,
-                                   max(E, 1), N, K, int(silu), DTYPE[dtype], out.data_ptr(), stream)
+    out_scales = None
+    if epilogue == 2:
+        out = _matrix(n, N // 4, torch.uint8)
+        out_scales = _vector(L.moe_fp4_row_scale_bytes(fmt, n, E, N // 2), torch.uint8)
+    else:
+        out = _matrix(n, N // 2 if epilogue else N, dtype)
+    rc = L.moe_fp4_expert_gemm(rows.codes.data_ptr(), rows.scales.data_ptr(), _or_none(rows.row_scale) if n else None, fmt,
+                               w.data_ptr(), w_scales.data_ptr(), _or_none(w_global), _or_none(rows.expert_offsets), n,
+                               max(E, 1), N, K, epilogue, DTYPE[dtype], out.data_ptr(), _or_none(out_scales), stream)
     _check("moe_fp4_expert_gemm", rc)
-    return out
+    return out if out_scales is None else Fp4Rows(out, out_scales, None, rows.format, rows.expert_offsets)
 
 
 def moe_fp4_expert_gemm(rows: Fp4Rows, w, w_scales, w_global=None, dtype=torch.bfloat16):
     """The experts' product on 4-bit rows (moe_fp4_quant) and weights: out[r] = rows[r] @ w[e]^T, [rows, N] in dtype (bf16,
     fp16 or fp32).  w: codes uint8 [E, N, K/2]; w_scales: their scales packed (moe_fp4_pack_scales); w_global fp32 [E] with
     nvfp4.  Rows of no expert are zero.  Rows without expert_offsets: E = 1, one weight for all."""
-    return _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, False)
+    return _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, 0)
 
 
 def moe_fp4_expert_gemm_silu_mul(rows: Fp4Rows, w, w_scales, w_global=None, dtype=torch.bfloat16):
     """The first product with its activation: h [rows, N/2] = silu(gate) * up in dtype (bf16 or fp16).  w [E, N, K/2]: gate
     rows, then up rows; w_scales packed with gate_up=True."""
-    return _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, True)
+    return _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, 1)
 
 
 def moe_fp4_expert_gemm_silu_mul_quant(rows: Fp4Rows, w, w_scales, w_global=None) -> Fp4Rows:
-    """The same with h rounded to bf16 and in 4 bits again (the rows' format), for the second product."""
-    return moe_fp4_quant(moe_fp4_expert_gemm_silu_mul(rows, w, w_scales, w_global), rows.format, rows.expert_offsets)
+    """The same with h rounded to bf16 and in 4 bits again (the rows' format), for the second product.  N a multiple of 64."""
+    if w.dim() == 3 and w.shape[1] % 64:
+        raise ValueError(f"w must have a multiple of 64 rows, got {w.shape[1]}")
+    if rows.format == "mxfp4":
+        return _fp4_expert_gemm(rows, w, w_scales, w_global, torch.bfloat16, 2)
+    return moe_fp4_quant(_fp4_expert_gemm(rows, w, w_scales, w_global, torch.bfloat16, 1), rows.format, rows.expert_offsets)
 
 
 def moe_clip_grads(grads, max_norm, norm_type=2.0, eps=1e-6, out=None):

@@ -700,10 +700,14 @@ int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate
  * expert as moe_expert_gemm's; expert_offsets NULL with E = 1: all rows):
  *   MOE_EXPERT_STORE    out [num_rows, N] in dtype (bf16, fp16 or fp32), N a multiple of 8
  *   MOE_EXPERT_SILU_MUL out [num_rows, N/2] in dtype (bf16 or fp16), N a multiple of 32, w_scales packed with gate_up
+ *   MOE_EXPERT_SILU_MUL_QUANT (mxfp4; dtype bf16) the same rounded to bf16 and quantised as moe_fp4_quant does, for the
+ *            second product: out the codes [num_rows, N/4], out_scales moe_fp4_row_scale_bytes(fmt, num_rows, E, N/2) bytes
+ *            (else NULL), N a multiple of 64.  (A row scale of nvfp4 needs the whole row: moe_fp4_quant after SILU_MUL.)
  * w_codes [E, N, K/2]; w_global fp32 [E] and row_scale with nvfp4, else NULL.  All arrays 16-byte aligned. */
+#define MOE_EXPERT_SILU_MUL_QUANT 2
 int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt, const uint8_t* w_codes,
                         const uint8_t* w_scales, const float* w_global, const int32_t* expert_offsets, int64_t num_rows,
-                        int E, int N, int K, int epilogue, int dtype, void* out, void* stream);
+                        int E, int N, int K, int epilogue, int dtype, void* out, uint8_t* out_scales, void* stream);
 
 /* Global norm of n gradient tensors and their clipping:
  *   total = sqrt(sum of squares) (MOE_NORM_L2) or the largest magnitude (MOE_NORM_INF) over all,
