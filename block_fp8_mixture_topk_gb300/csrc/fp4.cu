@@ -334,10 +334,11 @@ cudaError_t fp4_maps(CUtensorMap (&tm)[5], const uint8_t* codes, const uint8_t* 
     for (int i = 0; i < 2 && e == cudaSuccess; ++i) e = encode_u8_map_nd(&tm[1 + i], codes, 2, dims, strides, boxes[i], true);
     // scales as rows of 512-byte tiles
     const uint64_t s_strides[2] = {256, 512};
-    const uint32_t s_box[3] = {256, 2, static_cast<uint32_t>(fp4_words(fmt))};
+    const uint32_t a_box[3] = {256, 2, static_cast<uint32_t>(fp4_words(fmt))};
+    const uint32_t b_box[3] = {256, 2, 2 * static_cast<uint32_t>(fp4_words(fmt))};
     const uint64_t a_dims[3] = {256, 2, w_scale_bytes / 512}, b_dims[3] = {256, 2, scale_bytes / 512};
-    if (e == cudaSuccess) e = encode_u8_map_nd(&tm[3], w_scales, 3, a_dims, s_strides, s_box, false);
-    if (e == cudaSuccess) e = encode_u8_map_nd(&tm[4], scales, 3, b_dims, s_strides, s_box, false);
+    if (e == cudaSuccess) e = encode_u8_map_nd(&tm[3], w_scales, 3, a_dims, s_strides, a_box, false);
+    if (e == cudaSuccess) e = encode_u8_map_nd(&tm[4], scales, 3, b_dims, s_strides, b_box, false);
     return e;
 }
 
@@ -448,14 +449,15 @@ int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float
     const size_t scale_bytes = moe_fp4_row_scale_bytes(fmt, num_rows, expert_offsets ? E : 0, K);
     const size_t w_scale_bytes = moe_fp4_weight_scale_bytes(fmt, E, N, K);
     if (scale_bytes / 512 >= (size_t(1) << 31) || w_scale_bytes / 512 >= (size_t(1) << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int64_t row_tiles = num_rows / kFp4Rows + (num_rows < E ? num_rows : E) + 1;
+    const int64_t items = row_tiles * (silu ? (N / 2 + 127) / 128 : (N + 255) / 256);
+    if (items >= int64_t(1) << 31) return MOE_ERR_UNSUPPORTED_SHAPE;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     CUtensorMap tm[5];
     if (fp4_maps(tm, codes, scales, scale_bytes, fmt, w_codes, w_scales, w_scale_bytes, num_rows, E, N, K, silu) != cudaSuccess)
         return MOE_ERR_CUDA;
     const Fp4Args a = {expert_offsets, E, num_rows, N, K, row_scale, w_global, out, out_scales, status};
-    const int64_t row_tiles = num_rows / kFp4Rows + (num_rows < E ? num_rows : E) + 1;
-    const int64_t items = row_tiles * (silu ? (N / 2 + 127) / 128 : (N + 255) / 256);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(nv ? fp4_experts_launch<MOE_FP4_NVFP4>(dtype, epilogue, a, tm, items, s)
                           : fp4_experts_launch<MOE_FP4_MXFP4>(dtype, epilogue, a, tm, items, s));

@@ -34,13 +34,20 @@ constexpr int F_THREADS = (F_FIRST_EPI + F_EPI_WARPS) * 32;
 constexpr uint32_t F_TMEM = 512;
 constexpr int F_GROUP = 4;                          // row tiles visited together
 constexpr int F_SLOT = 24;                          // columns of a slot of scales: 2 words of 128 and of 256 rows
-constexpr int F_STAGES = 5;
+constexpr int F_STAGED = 2048;                      // bytes of staged results a warp
+constexpr int F_ITEMS = 128;                        // a cluster's first items, in a table
+__host__ __device__ constexpr int f_stages(int fmt) { return fmt == MOE_FP4_MXFP4 ? 6 : 5; }
 __host__ __device__ constexpr int f_scales(int fmt) { return 3 * fp4_words(fmt) * 512; }   // bytes of a stage
 __host__ __device__ constexpr int f_stage(int fmt) { return F_A + F_B + f_scales(fmt); }
 
+// One output tile: rows [r0, r0 + nrow) of column tile n of expert e, the m-th of its row tiles.
+struct FItem {
+    int e, n, m, r0, nrow;
+};
+
 struct FCtl {
-    uint64_t full[F_STAGES];    // (CTA 0) both CTAs' operands of the stage are in place
-    uint64_t empty[F_STAGES];   // the stage's MMAs completed
+    uint64_t full[6];       // (CTA 0) both CTAs' operands of the stage are in place
+    uint64_t empty[6];   // the stage's MMAs completed
     uint64_t tfull[2];          // the accumulators are complete
     uint64_t tempty[2];         // (CTA 0) both CTAs' epilogue warps moved them out
     uint64_t drain;
@@ -49,21 +56,17 @@ struct FCtl {
     int half_bad[2];
     int row0[MOE_MAX_EXPERTS + 1];    // first row of each expert, checked against the rows
     int tile0[MOE_MAX_EXPERTS + 1];   // first row tile of each expert
+    FItem item[F_ITEMS];              // the cluster's first
 };
 __host__ __device__ constexpr size_t f_smem(int fmt) {
-    return 1024 + static_cast<size_t>(F_STAGES) * f_stage(fmt) + 4 * X_STAGED + sizeof(FCtl);
+    return 1024 + static_cast<size_t>(f_stages(fmt)) * f_stage(fmt) + F_EPI_WARPS * F_STAGED + sizeof(FCtl);
 }
 static_assert(f_smem(MOE_FP4_MXFP4) <= 232448 && f_smem(MOE_FP4_NVFP4) <= 232448, "more shared memory than a CTA has");
 static_assert(2 * (256 + F_SLOT) > static_cast<int>(F_TMEM) && F_N + F_SLOT <= 256, "an accumulator and a slot to each half");
 
-// One output tile: rows [r0, r0 + nrow) of column tile n of expert e, the m-th of its row tiles.
-struct FItem {
-    int e, n, m, r0, nrow;
-};
-
-__device__ __forceinline__ FItem f_item(const Fp4Args& a, const FCtl* ctl, int64_t w, int NT) {
-    // the expert whose tiles hold tile w / NT; within it F_GROUP row tiles by all column tiles, row tiles
-    // fastest, so that the items under way at one time share rows and weights in L2
+// Item w of the launch: the expert whose tiles hold tile w / NT; within it F_GROUP row tiles by all column tiles, row
+// tiles fastest, so that the items under way at one time share rows and weights in L2.
+__device__ __forceinline__ FItem f_item_at(const Fp4Args& a, const FCtl* ctl, uint32_t w, uint32_t NT) {
     FItem t;
     const int g = static_cast<int>(w / NT);
     int lo = 0, hi = a.E - 1;
@@ -73,18 +76,30 @@ __device__ __forceinline__ FItem f_item(const Fp4Args& a, const FCtl* ctl, int64
         else hi = mid - 1;
     }
     const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo];
-    int local = static_cast<int>(w - static_cast<int64_t>(ctl->tile0[lo]) * NT);
-    const int grp = local / (F_GROUP * NT);
+    uint32_t local = w - static_cast<uint32_t>(ctl->tile0[lo]) * NT;
+    const uint32_t grp = local / (F_GROUP * NT);
     local -= grp * F_GROUP * NT;
-    const int gm = mt - grp * F_GROUP < F_GROUP ? mt - grp * F_GROUP : F_GROUP;
-    const int m = grp * F_GROUP + local % gm;
-    const int cnt = ctl->row0[lo + 1] - ctl->row0[lo];
-    t.e = __shfl_sync(0xffffffffu, lo, 0);
-    t.n = __shfl_sync(0xffffffffu, local / gm, 0);
-    t.m = __shfl_sync(0xffffffffu, m, 0);
-    t.r0 = __shfl_sync(0xffffffffu, ctl->row0[lo] + m * F_N, 0);
-    t.nrow = __shfl_sync(0xffffffffu, cnt - m * F_N < F_N ? cnt - m * F_N : F_N, 0);
+    const int left = mt - static_cast<int>(grp) * F_GROUP;
+    const uint32_t gm = left < F_GROUP ? left : F_GROUP;
+    t.n = static_cast<int>(local / gm);
+    t.m = static_cast<int>(grp * F_GROUP + local - t.n * gm);
+    t.e = lo;
+    t.r0 = ctl->row0[lo] + t.m * F_N;
+    const int rows = ctl->row0[lo + 1] - t.r0;
+    t.nrow = rows < F_N ? rows : F_N;
     return t;
+}
+// The k-th item of this cluster, from the table or (a long launch) worked out; the same values in every lane, which the
+// compiler knows.  (Worked out by every role, an item took each of them 520 cycles, a quarter of a short one.)
+__device__ __forceinline__ FItem f_item(const Fp4Args& a, const FCtl* ctl, uint32_t k, uint32_t w, uint32_t NT) {
+    const FItem t = k < F_ITEMS ? ctl->item[k] : f_item_at(a, ctl, w, NT);
+    FItem u;
+    u.e = __shfl_sync(0xffffffffu, t.e, 0);
+    u.n = __shfl_sync(0xffffffffu, t.n, 0);
+    u.m = __shfl_sync(0xffffffffu, t.m, 0);
+    u.r0 = __shfl_sync(0xffffffffu, t.r0, 0);
+    u.nrow = __shfl_sync(0xffffffffu, t.nrow, 0);
+    return u;
 }
 __device__ __forceinline__ int f_rows_mma(int nrow) { return (nrow + 31) / 32 * 32; }
 
@@ -165,15 +180,15 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     fp4_expert_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmSA,
                       const __grid_constant__ CUtensorMap tmSB, const Fp4Args a) {
-    constexpr int STAGES = F_STAGES, W = fp4_words(FMT);
+    constexpr int STAGES = f_stages(FMT), W = fp4_words(FMT);
     constexpr bool SILU = MODE != kFp4Store;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t* smA = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);   // [STAGES][F_A]
     uint8_t* smB = smA + STAGES * F_A;                                      // [STAGES][F_B]
     uint8_t* smS = smB + STAGES * F_B;                                      // [STAGES][weights W, rows 2 W][512]
-    uint8_t* smE = smS + STAGES * f_scales(FMT);                            // [2 halves][2][X_STAGED]
-    FCtl* ctl = reinterpret_cast<FCtl*>(smE + 4 * X_STAGED);
+    uint8_t* smE = smS + STAGES * f_scales(FMT);                            // [F_EPI_WARPS][F_STAGED]
+    FCtl* ctl = reinterpret_cast<FCtl*>(smE + F_EPI_WARPS * F_STAGED);
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
@@ -244,12 +259,15 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    const uint32_t total = static_cast<uint32_t>(ctl->tile0[a.E]) * NT;   // (below 2^31: checked with the sizes)
+    const uint32_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    if (threadIdx.x < F_ITEMS && cluster + threadIdx.x * clusters < total)
+        ctl->item[threadIdx.x] = f_item_at(a, ctl, cluster + threadIdx.x * clusters, NT);
+    __syncthreads();
     cluster_barrier();   // both CTAs' barriers are initialised before any arrival from the other
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort_flag = &ctl->abort_flag;
-    const int64_t total = static_cast<int64_t>(ctl->tile0[a.E]) * NT;
-    const int64_t cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA (both CTAs)
@@ -259,14 +277,14 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         const uint32_t smA0 = smem_addr(smA), smB0 = smem_addr(smB), smS0 = smem_addr(smS);
         const uint32_t full = smem_addr(&ctl->full[0]), full0 = cluster_map(full, 0);
         const int w_tiles = SILU ? (OC + 63) / 64 : (a.N + 127) / 128;   // of the weights' scales, an expert
-        for (int64_t w = cluster; w < total && ok; w += clusters) {
-            const FItem t = f_item(a, ctl, w, NT);
+        uint32_t k = 0;
+        for (uint32_t w = cluster; w < total && ok; w += clusters, ++k) {
+            const FItem t = f_item(a, ctl, k, w, NT);
             const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's output columns
             const int nn = f_rows_mma(t.nrow);
             const int32_t r0 = t.r0 + rank * (nn / 2);
             const int small = nn <= 64 ? nn / 32 : 0;   // few rows: in boxes of 16, only as many as the MMAs read
-            const int halves = nn > 128 ? 2 : 1;        // of the rows' scales
-            const uint32_t bytes = F_A + (small ? small * 2048 : F_B) + (1 + halves) * W * 512;
+            const uint32_t bytes = F_A + (small ? small * 2048 : F_B) + f_scales(FMT);
             // 512-byte tiles of scales; a tile of weights past the last is not multiplied into anything stored
             const int wt = 2 * t.n + rank;
             int32_t sa = static_cast<int32_t>((static_cast<int64_t>(t.e) * w_tiles + (wt < w_tiles ? wt : w_tiles - 1)) * KB * W);
@@ -283,7 +301,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     if (small == 0) tma_load_2d_pair(db, &tmB, kb * 128, r0, bar);
                     for (int i = 0; i < small; ++i) tma_load_2d_pair(db + i * 2048, &tmB16, kb * 128, r0 + i * 16, bar);
                     tma_load_3d_pair(ds, &tmSA, 0, 0, sa, bar);
-                    for (int h = 0; h < halves; ++h) tma_load_3d_pair(ds + (1 + h) * W * 512, &tmSB, 0, 0, sb + h * W, bar);
+                    tma_load_3d_pair(ds + W * 512, &tmSB, 0, 0, sb, bar);
                 }
                 __syncwarp();
                 sa += W;
@@ -311,8 +329,9 @@ __global__ void __launch_bounds__(F_THREADS, 1)
             int stage = 0;
             uint32_t phase = 0, buf = 0, bphase = 0, slot = 0;
             bool ok = true;
-            for (int64_t w = cluster; w < total && ok; w += clusters) {
-                const FItem t = f_item(a, ctl, w, NT);
+            uint32_t k = 0;
+            for (uint32_t w = cluster; w < total && ok; w += clusters, ++k) {
+                const FItem t = f_item(a, ctl, k, w, NT);
                 ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tempty[buf]), bphase ^ 1u, abort_flag, a.status));
                 if (!ok) break;
                 tc_fence_after();
@@ -371,20 +390,25 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         }
     } else if (warp >= F_FIRST_EPI) {
         // ---------------------------------------------------------------- epilogue
-        // The four warps of a half take blocks of 32 rows in turn with the other half's: the accumulators' lanes are output
-        // columns, so a block is stored transposed into shared memory (16-bit results: 8 x 8 at a time by stmatrix) and
-        // leaves by whole rows; two buffers, so that one barrier a block is enough.
+        // The four warps of a half hold the CTA's 128 columns; the halves take blocks of 32 rows in turn.  Lanes are output
+        // columns: 16-bit results go into shared memory transposed (8 x 8 at a time by stmatrix) and leave by rows.
+        //   store         each warp by itself, 64 bytes (fp32: 128) of a row: no barrier in the loop (with one, and whole
+        //                 rows of 256 bytes, warps stood at it half of the time)
+        //   SiLU          the half together, 128 bytes of a row (a warp has 32), from two buffers in turn: one barrier a block
+        // Rows are staged without padding, their 16-byte pieces exchanged by row so that no bank is hit twice.
         const int g = (warp - F_FIRST_EPI) >> 2;
         const int sp = warp & 3;                   // tensor-memory lane quarter
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
         T* out = static_cast<T*>(a.out);
-        uint8_t* const stage0 = smE + g * (2 * X_STAGED);
-        const Block block = {stage0, 1 + g, sp * 32 + lane};
+        uint8_t* const half_stage = smE + g * (4 * F_STAGED);
+        uint8_t* const warp_stage = half_stage + sp * F_STAGED;
+        const Block block = {half_stage, 1 + g, sp * 32 + lane};   // (for its barrier)
         uint32_t buf = 0, bphase = 0, side = 0;
         bool ok = true;
         const uint32_t tempty0 = cluster_map(smem_addr(&ctl->tempty[0]), 0), tempty1 = cluster_map(smem_addr(&ctl->tempty[1]), 0);
-        for (int64_t w = cluster; w < total; w += clusters) {
-            const FItem t = f_item(a, ctl, w, NT);
+        uint32_t k = 0;
+        for (uint32_t w = cluster; w < total; w += clusters, ++k) {
+            const FItem t = f_item(a, ctl, k, w, NT);
             const int c0 = t.n * (SILU ? 128 : 256) + rank * (SILU ? 64 : 128);   // this CTA's columns
             const int blocks = (t.nrow + 31) / 32;
             float wg = 1.0f, rs = 0.0f;
@@ -397,37 +421,32 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                 if (g < blocks) rs = row_scale(g);
             }
             ok = __all_sync(0xffffffffu, mbar_wait<true>(smem_addr(&ctl->tfull[buf]), bphase, abort_flag, a.status));
-            if (!half_ok(ok, block, &ctl->half_bad[g])) break;
+            if (SILU ? !half_ok(ok, block, &ctl->half_bad[g]) : !ok) break;
             tc_fence_after();
             const uint32_t acc = lane_base + buf * 256;
             if constexpr (sizeof(T) == 4) {
-                const int col = sp * 32 + lane;
                 for (int blk = g; blk < blocks; blk += 2) {
                     float v[32];
-                    const int64_t r0 = static_cast<int64_t>(t.r0) + blk * 32;
-                    const int nrow = t.nrow - blk * 32;
                     tmem_ld32(acc + blk * 32, v);
                     if constexpr (FMT == MOE_FP4_NVFP4) {
                         if (blk != g) rs = row_scale(blk);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, rs, i);
                     }
-                    // 16 rows of 128 columns at a time
-                    constexpr int PITCH = 512 + 16;
-                    static_assert(16 * PITCH <= X_STAGED, "a staged block");
+                    const int c = c0 + sp * 32 + (lane & 7) * 4;
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        uint8_t* stage = stage0 + part * X_STAGED;
+                    for (int part = 0; part < 2; ++part) {   // 16 rows of 32 columns at a time
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) *reinterpret_cast<float*>(stage + i * PITCH + col * 4) = v[part * 16 + i];
-                        block.sync();
+                        for (int i = 0; i < 16; ++i) *reinterpret_cast<float*>(warp_stage + i * 128 + lane * 4) = v[part * 16 + i];
+                        __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int k = i * 128 + block.et, r = k >> 5, q = k & 31;
-                            if (part * 16 + r < nrow && c0 + q * 4 < OC)
-                                *reinterpret_cast<uint4*>(out + (r0 + part * 16 + r) * OC + c0 + q * 4) =
-                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
+                            const int q = i * 4 + (lane >> 3), r = blk * 32 + part * 16 + q;
+                            const uint4 u = *reinterpret_cast<const uint4*>(warp_stage + q * 128 + (lane & 7) * 16);
+                            if (r < t.nrow && c < OC)
+                                *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(t.r0) + r) * OC + c) = u;
                         }
+                        __syncwarp();
                     }
                 }
             } else {
@@ -448,11 +467,13 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                         }
                         if (blk + 2 < blocks) rs = row_scale(blk + 2);
                     }
-                    uint8_t* stage = stage0 + side * X_STAGED;
+                    // row r at r * PITCH, its piece p at p ^ swap(r)
+                    constexpr int PITCH = SILU ? 128 : 64;
+                    uint8_t* stage = SILU ? half_stage + side * (2 * F_STAGED) : warp_stage;
                     side ^= 1u;
-                    constexpr int PITCH = SILU ? 128 + 16 : X_PITCH;
                     if constexpr (SILU) {   // lanes 0 .. 15 gate, 16 .. 31 the up of the same columns
-                        const uint32_t to = smem_addr(stage) + ((lane >> 4) * 8 + (lane & 7)) * PITCH + sp * 32 + ((lane >> 3) & 1) * 16;
+                        const int r = (lane >> 4) * 8 + (lane & 7);
+                        const uint32_t to = smem_addr(stage) + r * PITCH + (((sp * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4);
 #pragma unroll
                         for (int q = 0; q < 4; q += 2) {
                             uint32_t p[4];
@@ -463,7 +484,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                             f_store_turned(to + q * 8 * PITCH, p[0], p[1], p[2], p[3]);
                         }
                     } else {
-                        const uint32_t to = smem_addr(stage) + (lane & 7) * PITCH + sp * 64 + (lane >> 3) * 16;
+                        const int r = lane & 7;
+                        const uint32_t to = smem_addr(stage) + r * PITCH + (((lane >> 3) ^ (r >> 1)) << 4);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             f_store_turned(to + q * 8 * PITCH, pack2<T>(v[0][4 * q], v[0][4 * q + 1]),
@@ -471,7 +493,8 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                                            pack2<T>(v[1][4 * q + 2], v[1][4 * q + 3]));
                     }
                     if (blk + 2 < blocks) f_load_block(acc + (blk + 2) * 32, v);
-                    block.sync();
+                    if (SILU) block.sync();
+                    else __syncwarp();
                     const int64_t r0 = static_cast<int64_t>(t.r0) + blk * 32;
                     const int nrow = t.nrow - blk * 32;
                     if constexpr (MODE == kFp4SiluQuant) {
@@ -480,7 +503,7 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                         Vec16<T> x;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint4 u = *reinterpret_cast<const uint4*>(stage + r * PITCH + part * 32 + i * 16);
+                            const uint4 u = *reinterpret_cast<const uint4*>(stage + r * PITCH + (((part * 2 + i) ^ (r & 7)) << 4));
                             x.w[4 * i] = u.x, x.w[4 * i + 1] = u.y, x.w[4 * i + 2] = u.z, x.w[4 * i + 3] = u.w;
                         }
                         uint32_t top = x.top();
@@ -504,16 +527,17 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                             const int k = i * 128 + block.et, r = k >> 3, q = k & 7;
                             if (r < nrow && c0 + q * 8 < OC)
                                 *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) =
-                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
+                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + ((q ^ (r & 7)) << 4));
                         }
                     } else {
+                        const int c = c0 + sp * 32 + (lane & 3) * 8;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int k = i * 128 + block.et, r = k >> 4, q = k & 15;
-                            if (r < nrow && c0 + q * 8 < OC)
-                                *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c0 + q * 8) =
-                                    *reinterpret_cast<const uint4*>(stage + r * PITCH + q * 16);
+                            const int r = i * 8 + (lane >> 2);
+                            const uint4 u = *reinterpret_cast<const uint4*>(stage + r * PITCH + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                            if (r < nrow && c < OC) *reinterpret_cast<uint4*>(out + (r0 + r) * OC + c) = u;
                         }
+                        __syncwarp();   // before the next block is staged
                     }
                 }
             }
