@@ -4,7 +4,7 @@
 namespace mfp8 {
 namespace {
 
-constexpr int kFinalCtas = 8, kFinalThreads = 512;
+constexpr int kFinalCtas = 8, kFinalThreads = 1024;
 
 // The blocks' sums: expert chunk by CTA of one cluster (a thread adds every (threads / chunk)-th block, those sums in order),
 // whose shares of the balance loss the first CTA adds up.
@@ -35,6 +35,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
     float s = 0.0f;
     int c = 0;
     if (r < rows && e < E)
+#pragma unroll 4
         for (int b = r; b < blocks; b += rows) {
             s += share[static_cast<int64_t>(b) * E + e];
             c += count[static_cast<int64_t>(b) * E + e];
@@ -95,14 +96,8 @@ __global__ void __launch_bounds__(1024) router_bias_kernel(float* bias, const in
     if (e < E && mine != sum) bias[e] += mine < sum ? rate : -rate;
 }
 
-// Blocks of a launch: enough for every token, and with loads few enough to add up.  (A block's eight warps hold E / 32
-// registers of each of five arrays; four blocks to an SM are resident at E <= 256.)
-constexpr int kStatBlocks = kPlanSms * 2;
-int router_blocks(int T) { return (T + kRouterWarps - 1) / kRouterWarps; }
-int router_stat_blocks(int T) {
-    const int b = router_blocks(T);
-    return b < kStatBlocks ? b : kStatBlocks;
-}
+// Blocks of a launch: one to an SM, or to a token.
+int router_blocks(int T) { return T < kPlanSms ? T : kPlanSms; }
 
 int check_router(int dtype, int64_t ld, int T, int E, int k, const moe_router_params* p) {
     if (!p || !known_dtype(dtype) || T < 0 || E < 1 || k < 1) return MOE_ERR_INVALID_ARG;
@@ -126,7 +121,7 @@ extern "C" {
 
 size_t moe_router_workspace_size(int T, int E) {
     if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS) return 0;
-    return static_cast<size_t>(router_stat_blocks(T)) * (2 * static_cast<size_t>(E) + 2) * 4;
+    return static_cast<size_t>(router_blocks(T)) * (2 * static_cast<size_t>(E) + 2) * 4;
 }
 
 int moe_router(const void* logits, int64_t ld, int dtype, int T, int E, int topk, const moe_router_params* p,
@@ -147,7 +142,7 @@ int moe_router(const void* logits, int64_t ld, int dtype, int T, int E, int topk
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int blocks = stats ? router_stat_blocks(T) : router_blocks(T);
+    const int blocks = router_blocks(T);
     RouterArgs a = {};
     a.logits = logits, a.ld = ld, a.T = T, a.E = E, a.k = topk;
     a.sigmoid = p->scoring == MOE_SCORING_SIGMOID, a.groups = p->n_group, a.kept = p->topk_group;
@@ -191,11 +186,10 @@ int moe_router_backward(const void* logits, int64_t ld, int dtype, int T, int E,
     a.sigmoid = p->scoring == MOE_SCORING_SIGMOID, a.renorm = p->renormalize != 0, a.scaling = p->routed_scaling;
     a.ids = ids, a.dweights = dweights, a.counts = counts, a.live = tokens, a.balance = balance_coef, a.z = z_coef;
     a.dlogits = dlogits, a.status = status;
-    const int most = kPlanSms * 8, blocks = router_blocks(T) < most ? router_blocks(T) : most;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(dtype == MOE_DTYPE_BF16   ? router_backward<__nv_bfloat16>(a, blocks, s)
-                       : dtype == MOE_DTYPE_FP16 ? router_backward<__half>(a, blocks, s)
-                                                 : router_backward<float>(a, blocks, s));
+    return cuda_status(dtype == MOE_DTYPE_BF16   ? router_backward<__nv_bfloat16>(a, s)
+                       : dtype == MOE_DTYPE_FP16 ? router_backward<__half>(a, s)
+                                                 : router_backward<float>(a, s));
 }
 
 int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate, void* stream) {

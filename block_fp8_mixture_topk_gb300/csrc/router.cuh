@@ -15,10 +15,11 @@
 // The choice is that of the real numbers: keys are formed in fp32, and where two of them that a decision compares are
 // closer than their error (and not of the same logit and bias) the token's choice is repeated on fp64 keys.
 //
-// Lane i holds experts i V .. i V + V - 1 in registers (V = 1 to 32, E <= 32 V), the next token's logits are under way while
-// one is chosen for.  A round of the top-k is a maximum over a lane's keys, one over the warp (as ordered integers) and
-// a ballot.  Loads and score sums stay in registers over a warp's tokens, are added across a block's warps in
-// order, and a last small launch adds the blocks' sums: no atomics, the same result every time.
+// Lane i holds experts i V .. i V + V - 1 in registers (V = 1 to 32, E <= 32 V).  A round of the top-k is a maximum over a
+// lane's keys, one over the warp (as ordered integers) and a ballot.  A token is one long chain of such steps, so the
+// bound is how many of them an SM has under way and the instructions of a token: everything that a warp keeps across tokens but its score sums lies in
+// shared memory, so that 32 warps of 64 registers fit (V <= 8).  Score sums stay in registers over a warp's tokens and
+// are added across warps, then blocks (a last small launch) in a fixed order; the loads are integers.
 #pragma once
 
 #include <type_traits>
@@ -27,7 +28,8 @@
 
 namespace mfp8 {
 
-constexpr int kRouterWarps = 8;      // tokens under way in a block
+constexpr int router_warps(int V) { return V <= 4 ? 32 : V == 8 ? 24 : 256 / V; }   // of a block, one block to an SM
+constexpr int kBackwardWarps = 8;
 
 struct RouterArgs {
     const void* logits;
@@ -68,9 +70,15 @@ struct RouterBackwardArgs {
 template <class T>
 cudaError_t router_forward(const RouterArgs& a, int blocks, cudaStream_t stream);
 template <class T>
-cudaError_t router_backward(const RouterBackwardArgs& a, int blocks, cudaStream_t stream);
+cudaError_t router_backward(const RouterBackwardArgs& a, cudaStream_t stream);
 
 #ifdef MOE_ROUTER_KERNELS
+// Rows that can be loaded V elements at a time: E a multiple of V, addresses of the vectors (16 bytes at most).
+template <class T>
+bool router_vectors(const void* p, int64_t ld, int E, int V) {
+    const int64_t bytes = V * static_cast<int64_t>(sizeof(T)) < 16 ? V * static_cast<int64_t>(sizeof(T)) : 16;
+    return E % V == 0 && address(p) % bytes == 0 && ld * static_cast<int64_t>(sizeof(T)) % bytes == 0;
+}
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
@@ -81,19 +89,27 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
+// Sum over the first k lanes (the others hold 0), the same in every lane.
+__device__ __forceinline__ float chosen_sum(float v, int k) {
+    if (k > 8) {
+        v += __shfl_xor_sync(kAll, v, 16);
+        v += __shfl_xor_sync(kAll, v, 8);
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return __shfl_sync(kAll, v, 0);
 }
-// fp32 as integers of the same order, both zeros alike; 0 stands for no candidate.
+// fp32 as integers of the same order, both zeros alike.
 __device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+    const int b = __float_as_int(v + 0.0f);
+    return static_cast<uint32_t>(b ^ ((b >> 31) | INT32_MIN));
 }
 __device__ __forceinline__ float of_ordered(uint32_t u) {
     return __uint_as_float(u >> 31 ? u ^ 0x80000000u : ~u);
 }
+
+// (No NaN.)
+__device__ __forceinline__ float warp_max(float v) { return of_ordered(__reduce_max_sync(kAll, ordered(v))); }
 
 // V logits from p on, those past `count` kNone.
 template <class T, int V>
@@ -133,16 +149,17 @@ struct Logits {
     }
 };
 
-// A lane's logits; one that is not finite counts as -inf (true in *odd unless it is -inf).
+// A lane's logits; NaN and +inf count as -inf (true in *odd).
 template <class T, int V>
 __device__ __forceinline__ void finite_logits(const Logits<T, V>& raw, int count, float (&l)[V], bool* odd) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const float x = v < count ? to_f32(raw.e[v]) : kNone;
-        l[v] = fabsf(x) < INFINITY ? x : kNone;
-        *odd |= !(fabsf(x) < INFINITY) && x != kNone;
+        l[v] = x < INFINITY ? x : kNone;
+        *odd |= !(x < INFINITY);
     }
 }
+constexpr uint32_t kLeastKey = 0x00800000u;   // of a finite number; -inf is below
 
 // Accurate where it vanishes, too.
 __device__ __forceinline__ float sigmoid32(float l) {
@@ -150,104 +167,151 @@ __device__ __forceinline__ float sigmoid32(float l) {
     return __fdividef(l < 0.0f ? e : 1.0f, 1.0f + e);
 }
 
-// The choice on fp64 keys.  Returns on lane j < k the j-th expert or -1.
-template <int V>
-__device__ __noinline__ int choose_exact(const float* l, const RouterArgs& a, int first, int count) {
+// The choice on fp64 keys, compared as ordered integers (fp64 instructions are a 64th of the others' rate here).  Returns on
+// lane j < k the j-th expert or -1.
+__device__ __forceinline__ uint64_t ordered(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return b ^ (b >> 63 ? ~uint64_t(0) : uint64_t(1) << 63);
+}
+__device__ __forceinline__ double of_ordered(uint64_t u) {
+    return __longlong_as_double(static_cast<long long>(u >> 63 ? u ^ (uint64_t(1) << 63) : ~u));
+}
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max(v, static_cast<uint64_t>(__shfl_xor_sync(kAll, static_cast<unsigned long long>(v), o)));
+    return v;
+}
+template <int V, bool SIGMOID>
+__device__ __noinline__ int choose_exact(const float* l, float m, const RouterArgs& a, int first, int lanes) {
     const int lane = threadIdx.x & 31;
-    double key[V];
-    double m = kNone;
-    for (int v = 0; v < V; ++v) m = fmax(m, static_cast<double>(l[v]));
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
-    double z = 0.0;
+    uint64_t key[V];   // 0: not to be chosen
+    double s[V], z = 1.0;
+#pragma unroll
     for (int v = 0; v < V; ++v) {
         const double x = l[v];
-        key[v] = l[v] == kNone ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m);
-        z += key[v];
+        s[v] = l[v] == kNone ? 0.0 : SIGMOID ? exp(-x) : exp(x - m);
     }
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
-    if (a.sigmoid) z = 1.0;
-    for (int v = 0; v < V; ++v)
-        key[v] = l[v] == kNone ? static_cast<double>(kNone) : key[v] / z + (a.bias ? static_cast<double>(a.bias[first + v]) : 0.0);
+    if (!SIGMOID) {
+        z = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) z += s[v];
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const double b = a.bias && first + v < a.E ? static_cast<double>(a.bias[first + v]) : 0.0;
+        key[v] = l[v] == kNone ? 0u : ordered((SIGMOID ? 1.0 / (1.0 + s[v]) : s[v] / z) + b);
+    }
     if (a.groups > 1) {
         const int G = a.E / a.groups;
-        double mine = kNone;   // lane g: value of group g
-        for (int g = 0; g < a.groups; ++g) {
-            double t1 = kNone, t2 = kNone;
-            for (int v = 0; v < V; ++v)
-                if (v < count && (first + v) / G == g) {
-                    t2 = fmax(t2, fmin(t1, key[v]));
-                    t1 = fmax(t1, key[v]);
-                }
-            for (int o = 16; o > 0; o >>= 1) {
-                const double u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
-                t2 = fmax(fmin(t1, u1), fmax(t2, u2));
-                t1 = fmax(t1, u1);
+        const auto join = [](uint64_t& t1, uint64_t& t2, uint64_t u1, uint64_t u2) {
+            t2 = max(min(t1, u1), max(t2, u2));
+            t1 = max(t1, u1);
+        };
+        const auto across = [&](uint64_t& t1, uint64_t& t2, int steps) {   // steps: lanes of a group
+            for (int o = 1; o < steps; o <<= 1) {
+                const uint64_t u1 = __shfl_xor_sync(kAll, static_cast<unsigned long long>(t1), o);
+                const uint64_t u2 = __shfl_xor_sync(kAll, static_cast<unsigned long long>(t2), o);
+                join(t1, t2, u1, u2);
             }
-            if (a.top2 && t2 > kNone) t1 += t2;
-            if (lane == g) mine = t1;
+            return a.top2 && t2 > 0 ? ordered(of_ordered(t1) + of_ordered(t2)) : t1;
+        };
+        uint64_t mine = 0;   // a group's value, in its lanes or in lane g
+        if (lanes > 0) {
+            uint64_t t1 = 0, t2 = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) join(t1, t2, key[v], 0);
+            mine = across(t1, t2, lanes);
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                uint64_t t1 = 0, t2 = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (first + v >= g * G && first + v < g * G + G) join(t1, t2, key[v], 0);
+                const uint64_t value = across(t1, t2, 32);
+                if (lane == g) mine = value;
+            }
         }
+        const int apart = lanes > 0 ? lanes : 1, own = lane / apart;
         int place = 0;
         for (int g = 0; g < a.groups; ++g) {
-            const double o = __shfl_sync(kAll, mine, g);
-            place += o > mine || (o == mine && g < lane);
+            const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(mine), g * apart);
+            place += o > mine || (o == mine && g < own);
         }
-        const uint32_t stay = __ballot_sync(kAll, lane < a.groups && place < a.kept);
-        for (int v = 0; v < V; ++v)
-            if (v < count && !((stay >> ((first + v) / G)) & 1u)) key[v] = kNone;
+        const uint32_t stay = __ballot_sync(kAll, own < a.groups && place < a.kept);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = lanes > 0 ? lane : (first + v) / G;
+            if (!((stay >> (g & 31)) & 1u)) key[v] = 0;
+        }
     }
     int id = -1;
     for (int j = 0; j < a.k; ++j) {
-        double best = kNone;
+        uint64_t best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = max(best, key[v]);
+        const uint64_t top = warp_max(best);
+        if (top == 0) break;
         int at = 0;
-        for (int v = 0; v < V; ++v)
-            if (key[v] > best) best = key[v], at = v;
-        double top = best;
-        for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAll, top, o));
-        if (top == kNone) break;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+            if (key[v] == top) at = v;
         const int src = __ffs(static_cast<int>(__ballot_sync(kAll, best == top))) - 1;
         const int e = __shfl_sync(kAll, first + at, src);
-        if (lane == src) key[at] = kNone;
+        if (lane == src) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v == at) key[v] = 0;
+        }
         if (lane == j) id = e;
     }
     return id;
 }
 
-template <class T, int V, bool STATS>
-__global__ void __launch_bounds__(kRouterWarps * 32) router_kernel(const RouterArgs a) {
+template <class T, int V, bool STATS, bool SIGMOID>
+__global__ void __launch_bounds__(router_warps(V) * 32, 1) router_kernel(const RouterArgs a) {
     grid_dependency_wait();
-    extern __shared__ float s_share[];   // STATS: [E] sums, [E] counts, z, live
+    // bias [32 V], loads [32 V] (STATS), at the end score sums [warps][32 V] in place of them
+    extern __shared__ float s_mem[];
+    float* s_bias = s_mem;
+    int* s_loads = reinterpret_cast<int*>(s_mem + 32 * V);
+    constexpr int WARPS = router_warps(V);
+    __shared__ uint2 s_nears[WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1u;
+    uint2* const s_near = s_nears[warp];
     const int first = lane * V, count = min(max(a.E - first, 0), V);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRouterWarps;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS;
     const T* logits = static_cast<const T*>(a.logits);
-    float b[V];
     float b_most = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        b[v] = a.bias && v < count ? __ldg(a.bias + first + v) : 0.0f;
-        b_most = fmaxf(b_most, fabsf(b[v]));
+    for (int e = threadIdx.x; e < 32 * V; e += WARPS * 32) {
+        const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.0f;
+        s_bias[e] = b;
+        if constexpr (STATS) s_loads[e] = 0;
     }
-    if (a.bias) b_most = warp_max(b_most);
+    __syncthreads();
+    if (a.bias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, fabsf(s_bias[first + v]));
+        b_most = warp_max(b_most);
+    }
     const bool scored = a.bias || (a.groups > 1 && a.top2);   // keys are needed as numbers, not only their order
     const int G = a.E / a.groups;
     // groups of whole lanes, a power of two of them: by shuffles among them; other groups one after the other
     const int lanes = G % V == 0 && ((G / V) & (G / V - 1)) == 0 ? G / V : 0;
     float share[V];
-    int loads[V];
     float z_sum = 0.0f;
     int live = 0;
     if constexpr (STATS) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) share[v] = 0.0f, loads[v] = 0;
+        for (int v = 0; v < V; ++v) share[v] = 0.0f;
     }
     bool odd = false;
 
-    int64_t t = static_cast<int64_t>(blockIdx.x) * kRouterWarps + warp;
-    Logits<T, V> raw, next;
-    if (t < a.T) next.load(logits + t * a.ld + first, count, a.vector);
-    for (; t < a.T; t += step) {
-        raw = next;
-        if (t + step < a.T) next.load(logits + (t + step) * a.ld + first, count, a.vector);
+    // a block's tokens are one in gridDim.x: few tokens spread over the SMs
+    for (int64_t t = blockIdx.x + static_cast<int64_t>(warp) * gridDim.x; t < a.T; t += step) {
+        Logits<T, V> raw;
+        raw.load(logits + t * a.ld + first, count, a.vector);
         const bool wanted = !a.valid || a.valid[t] != 0;
         float l[V];
         bool any = false;
@@ -261,42 +325,50 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_kernel(const RouterA
         float w = 0.0f;
         if (m > kNone) {   // some expert can be chosen
             float s[V], z = 1.0f;
-            if (scored || STATS || (!a.sigmoid && !a.renorm)) {
+            if (scored || STATS || !SIGMOID) {   // (exp(-inf) = 0: an expert that cannot be chosen has score 0)
                 z = 0.0f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    s[v] = l[v] == kNone ? 0.0f : a.sigmoid ? sigmoid32(l[v]) : expf(l[v] - m);
+                    if (SIGMOID) {
+                        const float e = __expf(-fabsf(l[v]));
+                        s[v] = __fdividef(l[v] < 0.0f ? e : 1.0f, 1.0f + e);
+                    } else {
+                        s[v] = __expf(l[v] - m);
+                    }
                     z += s[v];
                 }
                 z = warp_sum(z);
             }
             const float per = __fdividef(1.0f, z);
-            // keys, as ordered integers
+            // More than the error of a difference of keys is `slack` and kRel of the larger: a score is off by 2^-22.4 of itself
+            // (the quotient, a sum) and by its exponential: 2^-22 and 1.44 * 2^-24 of the exponent d, that is by less
+            // than 2^-23.5 (sigmoid: s (1 - s) <= 1/4, s (1 - s) d < 0.23) or 2^-24 of the largest score (softmax: d
+            // e^-d < 0.37) and 2^-22 of itself; softmax scores share a factor off by 2^-18 at most (38 roundings, and
+            // 1.44 * 2^-24 of the entropy), which counts by the difference of the scores, at most 2 b_most over the keys'.
+            constexpr float kRel = 0x1p-20f;
+            const float slack = (SIGMOID ? 0x1p-20f : 0x1p-17f) * b_most + (SIGMOID ? 0x1p-22f : 0x1p-22f * per);
+            // keys as numbers and as ordered integers
+            float x[V];
             uint32_t key[V];
-            // more than the error of a difference of keys, less 2^-19 of the keys: a score is off by 2^-20 of itself (two
-            // ulp of expf and of the quotient; with softmax also of the distance to the largest logit, which
-            // is at most 2^-24 of the largest score) and, with softmax, by a factor that all share (37 roundings)
-            const float slack = 0x1p-17f * b_most + (a.sigmoid ? 0.0f : 0x1p-22f * per);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float x = a.bias ? (a.sigmoid ? s[v] : s[v] * per) + b[v] : l[v];
-                key[v] = l[v] == kNone ? 0u : ordered(x);
+            for (int v = 0; v < V; ++v) x[v] = l[v];
+            if (scored) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[v] = l[v] > kNone ? (SIGMOID ? s[v] : s[v] * per) + s_bias[first + v] : kNone;
             }
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = ordered(a.bias ? x[v] : l[v]);
             bool close = false;
             if (a.groups > 1) {
                 // a group's value; for groups of whole lanes in its lanes, else in lane g
-                float mine = kNone;
-                const auto number = [&](int v) {
-                    return l[v] == kNone ? kNone : scored ? (a.sigmoid ? s[v] : s[v] * per) + b[v] : l[v];
-                };
+                float mine = kNone, t1 = kNone, t2 = kNone;
                 const auto join = [](float& t1, float& t2, float u1, float u2) {
                     t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
                     t1 = fmaxf(t1, u1);
                 };
                 if (lanes > 0) {
-                    float t1 = kNone, t2 = kNone;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) join(t1, t2, number(v), kNone);
+                    for (int v = 0; v < V; ++v) join(t1, t2, x[v], kNone);
                     for (int o = 1; o < lanes; o <<= 1) {
                         const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
                         join(t1, t2, u1, u2);
@@ -304,10 +376,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_kernel(const RouterA
                     mine = a.top2 && t2 > kNone ? t1 + t2 : t1;
                 } else {
                     for (int g = 0; g < a.groups; ++g) {
-                        float t1 = kNone, t2 = kNone;
+                        t1 = t2 = kNone;
 #pragma unroll
                         for (int v = 0; v < V; ++v)
-                            if (v < count && (first + v) / G == g) join(t1, t2, number(v), kNone);
+                            if (v < count && (first + v) / G == g) join(t1, t2, x[v], kNone);
                         for (int o = 16; o > 0; o >>= 1) {
                             const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
                             join(t1, t2, u1, u2);
@@ -325,7 +397,52 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_kernel(const RouterA
                 if (scored && a.kept < a.groups) {
                     const float last = warp_max(real && place == a.kept - 1 ? mine : kNone);
                     const float out = warp_max(real && place == a.kept ? mine : kNone);
-                    close = out > kNone && last - out <= 4.0f * slack + 0x1p-18f * fmaxf(fabsf(last), fabsf(out));
+                    const float limit = 4.0f * slack + 2.0f * kRel * fmaxf(fabsf(last), fabsf(out));
+                    close = out > kNone && last - out <= limit;
+                    if (SIGMOID && lanes > 0 && close) {
+                        // the groups at the border by the fp64 keys of their two best (and what may be), a lane each
+                        const bool border = real && (fabsf(mine - last) <= limit || fabsf(mine - out) <= limit);
+                        const float best = a.top2 && t2 > kNone ? t2 : t1, low = best - (slack + kRel * fabsf(best));
+                        int found = 0;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            const bool in = border && x[v] >= low;
+                            const uint32_t all = __ballot_sync(kAll, in);
+                            const int at = found + __popc(all & below);
+                            if (in && at < 32) s_near[at] = make_uint2(first + v, own);
+                            found += __popc(all);
+                        }
+                        __syncwarp();
+                        if (found <= 32) {
+                            uint64_t wide = 0;
+                            uint32_t group = 0xffffffffu;
+                            if (lane < found) {
+                                const uint32_t e = s_near[lane].x;
+                                group = s_near[lane].y;
+                                const double x64 = to_f32(logits[t * a.ld + e]);
+                                wide = ordered(1.0 / (1.0 + exp(-x64)) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0));
+                            }
+                            uint64_t u1 = 0, u2 = 0;
+                            for (int i = 0; i < found; ++i) {
+                                const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(wide), i);
+                                if (__shfl_sync(kAll, group, i) == static_cast<uint32_t>(own)) {
+                                    u2 = max(min(u1, o), u2);
+                                    u1 = max(u1, o);
+                                }
+                            }
+                            const uint64_t value = a.top2 && u2 > 0 ? ordered(of_ordered(u1) + of_ordered(u2)) : u1;
+                            const uint32_t borders = __ballot_sync(kAll, border);
+                            place = 0;
+                            for (int g = 0; g < a.groups; ++g) {
+                                const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(value), g * apart);
+                                const float of = __shfl_sync(kAll, mine, g * apart);
+                                const bool both = border && ((borders >> (g * apart)) & 1u);
+                                place += both ? o > value || (o == value && g < own) : of > mine || (of == mine && g < own);
+                            }
+                            close = false;
+                        }
+                        __syncwarp();
+                    }
                 }
                 const uint32_t stay = __ballot_sync(kAll, real && place < a.kept);
 #pragma unroll
@@ -334,293 +451,408 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_kernel(const RouterA
                     if (v >= count || !((stay >> (g & 31)) & 1u)) key[v] = 0u;
                 }
             }
-            // the k largest (and, with keys in fp32, one more to see how near it is)
-            uint32_t taken = 0;
-            float before = 0.0f;
-            int before_id = -1;
-            const int rounds = a.bias ? a.k + 1 : a.k;
-            for (int j = 0; j < rounds; ++j) {
-                uint32_t most = key[0];
+            // the k largest (and, with keys in fp32, one more to see how near it is).  Keys from the (k + 1)-th largest of the
+            // lanes' largest on hold them all and are hardly more: lane i takes the i-th of these and counts the ones ahead.
+            // More than 32 of them (many equal keys, or k near the number of lanes): round by round.
+            const int need = a.bias ? a.k + 1 : a.k;
+            uint32_t most = key[0], least = 1u;
 #pragma unroll
-                for (int v = 1; v < V; ++v) most = max(most, key[v]);
-                const uint32_t top = __reduce_max_sync(kAll, most);
-                if (top == 0u) break;
-                const int src = __ffs(static_cast<int>(__ballot_sync(kAll, most == top))) - 1;
-                int at = 0;
+            for (int v = 1; v < V; ++v) most = max(most, key[v]);
+            for (int j = 0; j < need; ++j) {
+                least = __reduce_max_sync(kAll, most);
+                if (least < kLeastKey) break;
+                if (most == least) most = 0u;
+            }
+            least = max(least, kLeastKey);
+            // (keys in fp32: all that may be among them)
+            if (a.bias && least > kLeastKey) {
+                const float low = of_ordered(least);
+                least = max(ordered(low - (slack + kRel * fabsf(low))), kLeastKey);
+            }
+            int slot[V], found = 0;
 #pragma unroll
-                for (int v = V - 1; v >= 0; --v)
-                    if (key[v] == top) at = v;
-                const int e = __shfl_sync(kAll, first + at, src);
+            for (int v = 0; v < V; ++v) {
+                const uint32_t in = __ballot_sync(kAll, key[v] >= least);
+                slot[v] = key[v] >= least ? found + __popc(in & below) : 32;
+                found += __popc(in);
+            }
+            if (found <= 32) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (slot[v] < 32) s_near[slot[v]] = make_uint2(key[v], first + v);
+                __syncwarp();
+                const uint2 mine = lane < found ? s_near[lane] : make_uint2(0u, 0u);
+                int place = 0;
+                for (int i = 0; i < found; ++i) {
+                    const uint2 o = s_near[i];
+                    place += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+                }
+                __syncwarp();
+                if (lane < found) s_near[place] = mine;
+                __syncwarp();
                 if (a.bias) {
-                    const float now = of_ordered(top);
-                    if (j > 0 && before - now <= slack + 0x1p-19f * fmaxf(fabsf(before), fabsf(now)))
-                        close |= to_f32(logits[t * a.ld + e]) != to_f32(logits[t * a.ld + before_id]) ||
-                                 a.bias[e] != a.bias[before_id];
-                    before = now;
-                    before_id = e;
+                    bool near = false;
+                    if (lane < a.k && lane + 1 < found) {
+                        const uint2 u = s_near[lane], n = s_near[lane + 1];
+                        const float before = of_ordered(u.x), now = of_ordered(n.x);
+                        if (before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)))
+                            near = to_f32(logits[t * a.ld + u.y]) != to_f32(logits[t * a.ld + n.y]) || a.bias[u.y] != a.bias[n.y];
+                    }
+                    if (__any_sync(kAll, near)) {   // their order by fp64 keys, a lane each
+                        double all = 1.0;
+                        if (!SIGMOID) {
+                            all = 0.0;
+                            for (int v = 0; v < V; ++v) all += exp(static_cast<double>(l[v]) - m);
+                            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
+                        }
+                        uint64_t wide = 0;
+                        if (lane < found) {
+                            const double x64 = to_f32(logits[t * a.ld + mine.y]);
+                            const double s64 = SIGMOID ? 1.0 / (1.0 + exp(-x64)) : exp(x64 - m) / all;
+                            wide = ordered(s64 + static_cast<double>(a.bias[mine.y]));
+                        }
+                        place = 0;
+                        for (int i = 0; i < found; ++i) {
+                            const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(wide), i);
+                            const uint32_t oe = __shfl_sync(kAll, mine.y, i);
+                            place += o > wide || (o == wide && oe < mine.y);
+                        }
+                        __syncwarp();
+                        if (lane < found) s_near[place] = mine;
+                        __syncwarp();
+                    }
                 }
-                if (j >= a.k) break;
-                if (lane == src) {
+                if (lane < a.k && lane < found) id = static_cast<int>(s_near[lane].y);
+                __syncwarp();
+            } else {
+                float before = 0.0f;
+                int before_id = -1;
+                for (int j = 0; j < need; ++j) {
+                    most = key[0];
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (v == at) key[v] = 0u;
-                    taken |= 1u << at;
+                    for (int v = 1; v < V; ++v) most = max(most, key[v]);
+                    const uint32_t top = __reduce_max_sync(kAll, most);
+                    if (top < kLeastKey) break;
+                    const int src = __ffs(static_cast<int>(__ballot_sync(kAll, most == top))) - 1;
+                    int at = 0;
+#pragma unroll
+                    for (int v = V - 1; v >= 0; --v)
+                        if (key[v] == top) at = v;
+                    const int e = __shfl_sync(kAll, first + at, src);
+                    if (a.bias) {
+                        const float now = of_ordered(top);
+                        if (j > 0 && before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)))
+                            close |= to_f32(logits[t * a.ld + e]) != to_f32(logits[t * a.ld + before_id]) ||
+                                     a.bias[e] != a.bias[before_id];
+                        before = now;
+                        before_id = e;
+                    }
+                    if (j >= a.k) break;
+                    if (lane == src) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            if (v == at) key[v] = 0u;
+                    }
+                    if (lane == j) id = e;
                 }
-                if (lane == j) id = e;
             }
             if (close) {   // (the same in every lane)
                 float copy[V];   // (so that l itself stays in registers)
 #pragma unroll
                 for (int v = 0; v < V; ++v) copy[v] = l[v];
-                id = choose_exact<V>(copy, a, first, count);
-                taken = 0;
-                for (int j = 0; j < a.k; ++j) {
-                    const int e = __shfl_sync(kAll, id, j);
-                    if (e >= first && e < first + V) taken |= 1u << (e - first);
-                }
+                id = choose_exact<V, SIGMOID>(copy, m, a, first, lanes);
             }
             // weights, on lane j
             const bool chose = id >= 0;
-            const float x = chose ? to_f32(logits[t * a.ld + id]) : kNone;
-            if (a.renorm) {
-                if (a.sigmoid) {
-                    w = chose ? sigmoid32(x) : 0.0f;
-                    const float sum = warp_sum(w), most = warp_max(x);
+            const float own = chose ? to_f32(logits[t * a.ld + id]) : kNone;
+            if (SIGMOID) {
+                w = sigmoid32(own);
+                if (a.renorm) {
+                    const float sum = chosen_sum(w, a.k);
                     if (sum > 1e-30f) {
                         w = __fdividef(w, sum);
                     } else {   // all far below: s ~ exp(l)
-                        w = chose ? expf(x - most) : 0.0f;
-                        w /= warp_sum(w);
+                        w = expf(own - warp_max(own));
+                        w /= chosen_sum(w, a.k);
                     }
-                } else {
-                    const float most = warp_max(x);
-                    w = chose ? expf(x - most) : 0.0f;
-                    w = __fdividef(w, warp_sum(w));
                 }
+            } else if (a.renorm) {
+                w = expf(own - warp_max(own));
+                w = __fdividef(w, chosen_sum(w, a.k));
             } else {
-                w = !chose ? 0.0f : a.sigmoid ? sigmoid32(x) : expf(x - m) * per;
+                w = expf(own - m) * per;
             }
             if constexpr (STATS) {
                 const float by = __fdividef(1.0f, fmaxf(z, 1e-37f));
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    share[v] = fmaf(s[v], by, share[v]);
-                    loads[v] += static_cast<int>((taken >> v) & 1u);
-                }
-                const float lse = a.sigmoid ? 0.0f : m + logf(z);
+                for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], by, share[v]);
+                if (chose) atomicAdd(s_loads + id, 1);   // (whole numbers: in any order)
+                const float lse = SIGMOID ? 0.0f : m + logf(z);
                 z_sum = fmaf(lse, lse, z_sum);
                 ++live;
             }
         }
         if (lane < a.k) {
             a.ids[t * a.k + lane] = id;
-            a.weights[t * a.k + lane] = w * a.scaling;
+            a.weights[t * a.k + lane] = id >= 0 ? w * a.scaling : 0.0f;
         }
     }
     if (odd) status_set(a.status, MOE_STATUS_BAD_LOGIT);
     if constexpr (STATS) {
-        int* s_loads = reinterpret_cast<int*>(s_share + a.E);
-        float* s_z = s_share + 2 * a.E;
-        int* s_live = reinterpret_cast<int*>(s_z + 1);
-        for (int i = 0; i < kRouterWarps; ++i) {
-            if (warp == i) {
+        __shared__ float s_z[WARPS];
+        __shared__ int s_live[WARPS];
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += WARPS * 32) a.part_count[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_loads[e];
+        if (lane == 0) s_z[warp] = z_sum, s_live[warp] = live;
+        __syncthreads();
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v < count) {
-                        s_share[first + v] = share[v] + (i ? s_share[first + v] : 0.0f);
-                        s_loads[first + v] = loads[v] + (i ? s_loads[first + v] : 0);
-                    }
-                if (lane == 0) {
-                    *s_z = z_sum + (i ? *s_z : 0.0f);
-                    *s_live = live + (i ? *s_live : 0);
-                }
-            }
-            __syncthreads();
-        }
-        for (int e = threadIdx.x; e < a.E; e += kRouterWarps * 32) {
-            a.part_share[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_share[e];
-            a.part_count[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_loads[e];
+        for (int v = 0; v < V; ++v) s_mem[warp * (32 * V) + first + v] = share[v];
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += WARPS * 32) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < WARPS; ++i) sum += s_mem[i * (32 * V) + e];
+            a.part_share[static_cast<int64_t>(blockIdx.x) * a.E + e] = sum;
         }
         if (threadIdx.x == 0) {
-            a.part_z[blockIdx.x] = *s_z;
-            a.part_live[blockIdx.x] = *s_live;
+            float z = 0.0f;
+            int n = 0;
+            for (int i = 0; i < WARPS; ++i) z += s_z[i], n += s_live[i];
+            a.part_z[blockIdx.x] = z;
+            a.part_live[blockIdx.x] = n;
         }
     }
 }
 
-template <class T, int V>
-__global__ void __launch_bounds__(kRouterWarps * 32) router_backward_kernel(const RouterBackwardArgs a) {
+// The gradient: L lanes to a token, V experts to a lane (a warp has 32 / L tokens under way, its sums take log2 L steps).
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+template <class T, int V, int L, bool SIGMOID>
+__global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 3 : 1) router_backward_kernel(const RouterBackwardArgs a) {
     grid_dependency_wait();
-    extern __shared__ float s_rows[];   // [warps][32 V]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = lane * V, count = min(max(a.E - first, 0), V);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRouterWarps;
+    // the loads' factors h [L V], rows of chosen gradients [tokens][L V]; expert e at e % V * L + e / V
+    extern __shared__ float s_mem[];
+    constexpr int TOKENS = kBackwardWarps * 32 / L;
+    const int lane = threadIdx.x & 31, sub = lane % L, slot = threadIdx.x / L;
+    const int first = sub * V, count = min(max(a.E - first, 0), V);
     const T* logits = static_cast<const T*>(a.logits);
-    float* row = s_rows + warp * (32 * V);
+    float* row = s_mem + (slot + 1) * (L * V);
     const bool shares = a.balance != 0.0f;
-    const bool dense = shares || a.z != 0.0f || (!a.sigmoid && !a.renorm);   // every logit has a gradient
-    float h[V];
+    const bool dense = shares || a.z != 0.0f || (!SIGMOID && !a.renorm);   // every logit has a gradient
+    // the first token's logits are under way while the loads' factors are made
+    const int64_t step = static_cast<int64_t>(gridDim.x) * TOKENS;
+    int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
+    Logits<T, V> raw;
+    raw.load(logits + (t0 + slot) * a.ld + first, dense && t0 + slot < a.T ? count : 0, a.vector);
     float z_by = 0.0f;
     if (shares || a.z != 0.0f) {
         const float n = fmaxf(static_cast<float>(*a.live), 1.0f);
         z_by = 2.0f * a.z / n;
         const float by = a.balance * static_cast<float>(a.E) / (static_cast<float>(a.k) * n) / n;
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = shares && v < count ? by * static_cast<float>(a.counts[first + v]) : 0.0f;
+        for (int e = threadIdx.x; e < L * V; e += kBackwardWarps * 32)
+            s_mem[e % V * L + e / V] = shares && e < a.E ? by * static_cast<float>(a.counts[e]) : 0.0f;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) row[v * 32 + lane] = 0.0f;
+    for (int v = 0; v < V; ++v) row[v * L + sub] = 0.0f;
+    __syncthreads();
     bool bad = false;
 
-    int64_t t = static_cast<int64_t>(blockIdx.x) * kRouterWarps + warp;
-    Logits<T, V> raw, next;
-    int next_id = -1;
-    float next_dw = 0.0f;
-    const auto fetch = [&](int64_t u) {
-        if (u >= a.T) return;
-        next.load(logits + u * a.ld + first, dense ? count : 0, a.vector);
-        if (lane < a.k) {
-            next_id = __ldg(a.ids + u * a.k + lane);
-            next_dw = __ldg(a.dweights + u * a.k + lane);
+    for (; t0 < a.T; t0 += step) {   // (the same for a whole block)
+        const int64_t t = t0 + slot;
+        const bool real = t < a.T;
+        const int32_t* ids = a.ids + t * a.k;
+        // a chosen expert j of this lane: its id (else -1)
+        const auto chosen = [&](int j) { return real && j < a.k ? __ldg(ids + j) : -1; };
+        const int id0 = chosen(sub);
+        bool any = id0 >= 0 && id0 < a.E;
+        for (int j = sub + L; j < a.k; j += L) {
+            const int id = chosen(j);
+            any |= id >= 0 && id < a.E;
         }
-    };
-    fetch(t);
-    for (; t < a.T; t += step) {
-        raw = next;
-        int id = lane < a.k ? next_id : -1;
-        const float dw = next_dw;
-        fetch(t + step);
-        if (id >= a.E) bad = true, id = -1;
-        const bool chose = id >= 0;
-        Logits<T, V> out;
-        if (__any_sync(kAll, chose)) {
-            const float x = chose ? to_f32(logits[t * a.ld + id]) : kNone;
-            const float g = chose ? a.scaling * dw : 0.0f;
-            float l[V], s[V], m = 0.0f, z = 1.0f;
-            if (dense) {
-                bool odd = false;
-                finite_logits(raw, count, l, &odd);
+        const bool some = lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;   // the token has an expert
+        float s[V], m = 0.0f, z = 1.0f;   // s: the score (softmax: times z); 0 of an expert that cannot be chosen
+        float e[V];                       // sigmoid: exp(-|l|), negative where l is
+        if (dense) {
+            float l[V];
+            bool odd = false;
+            finite_logits(raw, real && some ? count : 0, l, &odd);
+            if (!SIGMOID) {
                 m = l[0];
 #pragma unroll
                 for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-                m = warp_max(m);
-                z = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s[v] = l[v] == kNone ? 0.0f : a.sigmoid ? sigmoid32(l[v]) : expf(l[v] - m);
-                    z += s[v];
-                }
-                z = warp_sum(z);
+                m = lanes_max<L>(m);
+                m = m > kNone ? m : 0.0f;
             }
-            const float per = __fdividef(1.0f, fmaxf(z, 1e-37f));
-            // the chosen experts' part, on lane j
-            float d = 0.0f, sum_g = 0.0f;
-            if (a.renorm) {
-                float q;
-                if (a.sigmoid) {
-                    q = chose ? sigmoid32(x) : 0.0f;
-                    const float sum = warp_sum(q), most = warp_max(x);
-                    if (sum > 1e-30f) {
-                        q = __fdividef(q, sum);
-                    } else {
-                        q = chose ? expf(x - most) : 0.0f;
-                        q /= warp_sum(q);
-                    }
-                } else {
-                    const float most = warp_max(x);
-                    q = chose ? expf(x - most) : 0.0f;
-                    q = __fdividef(q, warp_sum(q));
-                }
-                d = q * (g - warp_sum(q * g));
-                if (a.sigmoid) d *= sigmoid32(-x);
-            } else if (a.sigmoid) {
-                d = g * sigmoid32(x) * sigmoid32(-x);
-            } else {
-                const float p = chose ? expf(x - m) * per : 0.0f;
-                d = p * g;
-                sum_g = warp_sum(p * g);
-            }
-            if (chose) row[id % V * 32 + id / V] = d;
-            __syncwarp();
-            float mean_h = 0.0f;
-            if (shares) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) mean_h = fmaf(s[v], h[v], mean_h);
-                mean_h = warp_sum(mean_h) * per;
-            }
-            const float z_part = a.z != 0.0f ? z_by * (m + logf(z)) : 0.0f;
+            z = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float r = row[v * 32 + lane];
-                if (dense && v < count) {
-                    const float p = s[v] * per;
-                    if (shares) r += p * (h[v] - mean_h) * (a.sigmoid ? sigmoid32(-l[v]) : 1.0f);
-                    if (!a.sigmoid) r += p * (z_part - sum_g);
+                if (SIGMOID) {
+                    const float p = __expf(-fabsf(l[v]));
+                    s[v] = __fdividef(l[v] < 0.0f ? p : 1.0f, 1.0f + p);
+                    e[v] = l[v] < 0.0f ? -p : p;
+                } else {
+                    s[v] = __expf(l[v] - m);
                 }
-                out.e[v] = from_f32<T>(r);
+                z += s[v];
             }
-            __syncwarp();
-            if (chose) row[id % V * 32 + id / V] = 0.0f;
-            __syncwarp();
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) out.e[v] = from_f32<T>(0.0f);
+            z = lanes_sum<L>(z);
         }
-        out.store(static_cast<T*>(a.dlogits) + t * a.E + first, count, a.vector_out);
+        if (t + step < a.T) raw.load(logits + (t + step) * a.ld + first, dense ? count : 0, a.vector);
+        const float per = __fdividef(1.0f, fmaxf(z, 1e-37f));
+        // the chosen experts' part: sums over them, then each one's gradient (a lane has one, or every L-th)
+        const auto part = [&](int id, float dw, float* q, float* g, float* phi) {
+            const bool chose = id >= 0 && id < a.E;
+            const float x = chose ? to_f32(logits[t * a.ld + id]) : kNone;
+            *g = chose ? a.scaling * dw : 0.0f;
+            *q = !chose ? 0.0f : SIGMOID ? sigmoid32(x) : a.renorm ? x : expf(x - m) * per;
+            *phi = SIGMOID && chose ? sigmoid32(-x) : 1.0f;
+            return x;
+        };
+        const auto dweight = [&](int j) { return real && j < a.k ? __ldg(a.dweights + t * a.k + j) : 0.0f; };
+        float q0, g0, phi0;
+        const float x0 = part(id0, dweight(sub), &q0, &g0, &phi0);
+        bad |= id0 >= a.E;
+        float most = x0, sum = 0.0f, sum_g = 0.0f;
+        bool tiny = false;   // sigmoid scores that vanish: s ~ exp(l)
+        if (a.renorm) {
+            float all = q0;
+            for (int j = sub + L; j < a.k; j += L) {
+                float q, g, phi;
+                most = fmaxf(most, part(chosen(j), 0.0f, &q, &g, &phi));
+                all += q;
+            }
+            most = lanes_max<L>(most);
+            if (SIGMOID) sum = lanes_sum<L>(all);
+            tiny = SIGMOID && !(sum > 1e-30f);
+            const bool logs = !SIGMOID || tiny;
+            if (__any_sync(kAll, logs)) {   // (the warp's tokens together: the sum below is over lanes)
+                all = x0 > kNone ? expf(x0 - most) : 0.0f;
+                if (logs) q0 = all;
+                for (int j = sub + L; j < a.k; j += L) {
+                    float q, g, phi;
+                    const float x = part(chosen(j), 0.0f, &q, &g, &phi);
+                    all += x > kNone ? expf(x - most) : 0.0f;
+                }
+                const float other = lanes_sum<L>(all);
+                if (logs) sum = other;
+            }
+        }
+        const float by = a.renorm ? 1.0f / fmaxf(sum, 1e-37f) : 1.0f;
+        q0 *= by;
+        // (of a further choice j: q as q0, in the same way)
+        const auto again = [&](int j, float* q, float* g, float* phi) {
+            const int id = chosen(j);
+            bad |= id >= a.E;
+            const float x = part(id, dweight(j), q, g, phi);
+            if (a.renorm && (!SIGMOID || tiny)) *q = x > kNone ? expf(x - most) : 0.0f;
+            *q *= by;
+            return id >= 0 && id < a.E ? id : -1;
+        };
+        sum_g = q0 * g0;
+        for (int j = sub + L; j < a.k; j += L) {
+            float q, g, phi;
+            again(j, &q, &g, &phi);
+            sum_g = fmaf(q, g, sum_g);
+        }
+        sum_g = lanes_sum<L>(sum_g);
+        const float inner = a.renorm ? sum_g : 0.0f;
+        if (any && id0 >= 0 && id0 < a.E) row[id0 % V * L + id0 / V] = phi0 * q0 * (g0 - inner);
+        for (int j = sub + L; j < a.k; j += L) {
+            float q, g, phi;
+            const int id = again(j, &q, &g, &phi);
+            if (id >= 0) row[id % V * L + id / V] = phi * q * (g - inner);
+        }
+        __syncwarp();
+        float mean_h = 0.0f;
+        if (shares) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) mean_h = fmaf(s[v], s_mem[v * L + sub], mean_h);
+            mean_h = lanes_sum<L>(mean_h) * per;
+        }
+        // of every softmax logit: the z loss, and the chosen sum where it is not renormalised
+        const float each = SIGMOID || !some ? 0.0f : (a.z != 0.0f ? z_by * (m + logf(z)) : 0.0f) - (a.renorm ? 0.0f : sum_g);
+        Logits<T, V> out;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float r = row[v * L + sub];
+            if (dense) {
+                const float p = s[v] * per;
+                float by_p = each;
+                // 1 - s, with its digits where s is near 1
+                if (shares) by_p += (s_mem[v * L + sub] - mean_h) * (!SIGMOID ? 1.0f : e[v] > 0.0f ? e[v] * s[v] : 1.0f - s[v]);
+                r = fmaf(p, by_p, r);
+            }
+            out.e[v] = from_f32<T>(r);
+        }
+        __syncwarp();
+        if (id0 >= 0 && id0 < a.E) row[id0 % V * L + id0 / V] = 0.0f;
+        for (int j = sub + L; j < a.k; j += L) {
+            const int id = chosen(j);
+            if (id >= 0 && id < a.E) row[id % V * L + id / V] = 0.0f;
+        }
+        __syncwarp();
+        if (real) out.store(static_cast<T*>(a.dlogits) + t * a.E + first, count, a.vector_out);
     }
     if (bad) status_set(a.status, MOE_STATUS_BAD_EXPERT_ID);
 }
 
-template <class T, int V>
-cudaError_t forward_v(const RouterArgs& a, int blocks, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(blocks)), block(kRouterWarps * 32);
-    if (!a.part_share) return launch_pdl(router_kernel<T, V, false>, grid, block, 0, stream, a);
-    return launch_pdl(router_kernel<T, V, true>, grid, block, (2 * static_cast<size_t>(a.E) + 2) * 4, stream, a);
+template <class T, int V, bool SIGMOID>
+cudaError_t forward_v(RouterArgs a, int blocks, cudaStream_t stream) {
+    a.vector = router_vectors<T>(a.logits, a.ld, a.E, V);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(router_warps(V) * 32);
+    if (!a.part_share) return launch_pdl(router_kernel<T, V, false, SIGMOID>, grid, block, 32 * V * sizeof(float), stream, a);
+    return launch_pdl(router_kernel<T, V, true, SIGMOID>, grid, block,
+                      static_cast<size_t>(router_warps(V)) * 32 * V * sizeof(float), stream, a);
 }
-template <class T, int V>
-cudaError_t backward_v(const RouterBackwardArgs& a, int blocks, cudaStream_t stream) {
-    return launch_pdl(router_backward_kernel<T, V>, dim3(static_cast<unsigned>(blocks)), dim3(kRouterWarps * 32),
-                      static_cast<size_t>(kRouterWarps) * 32 * V * 4, stream, a);
+template <class T, bool SIGMOID>
+cudaError_t forward_scoring(const RouterArgs& a, int blocks, cudaStream_t stream) {
+    if (a.E <= 32) return forward_v<T, 1, SIGMOID>(a, blocks, stream);
+    if (a.E <= 128) return forward_v<T, 4, SIGMOID>(a, blocks, stream);
+    if (a.E <= 256) return forward_v<T, 8, SIGMOID>(a, blocks, stream);
+    if (a.E <= 512) return forward_v<T, 16, SIGMOID>(a, blocks, stream);
+    return forward_v<T, 32, SIGMOID>(a, blocks, stream);
+}
+
+template <class T, int V, int L, bool SIGMOID>
+cudaError_t backward_v(RouterBackwardArgs a, cudaStream_t stream) {
+    a.vector = router_vectors<T>(a.logits, a.ld, a.E, V);
+    a.vector_out = router_vectors<T>(a.dlogits, a.E, a.E, V);
+    constexpr int TOKENS = kBackwardWarps * 32 / L;
+    const int64_t blocks = (static_cast<int64_t>(a.T) + TOKENS - 1) / TOKENS, most = kPlanSms * 8;
+    return launch_pdl(router_backward_kernel<T, V, L, SIGMOID>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                      dim3(kBackwardWarps * 32), static_cast<size_t>(TOKENS + 1) * L * V * sizeof(float), stream, a);
+}
+// 8 lanes to a token up to 128 experts, 16 up to 256.
+template <class T, bool SIGMOID>
+cudaError_t backward_scoring(const RouterBackwardArgs& a, cudaStream_t stream) {
+    if (a.E <= 16) return backward_v<T, 2, 8, SIGMOID>(a, stream);
+    if (a.E <= 64) return backward_v<T, 8, 8, SIGMOID>(a, stream);
+    if (a.E <= 128) return backward_v<T, 16, 8, SIGMOID>(a, stream);
+    if (a.E <= 256) return backward_v<T, 16, 16, SIGMOID>(a, stream);
+    if (a.E <= 512) return backward_v<T, 16, 32, SIGMOID>(a, stream);
+    return backward_v<T, 32, 32, SIGMOID>(a, stream);
 }
 
 }  // namespace
 
-// Rows that can be loaded V elements at a time: E a multiple of V, addresses of the vectors (16 bytes at most).
 template <class T>
-bool router_vectors(const void* p, int64_t ld, int E, int V) {
-    const int64_t bytes = V * static_cast<int64_t>(sizeof(T)) < 16 ? V * static_cast<int64_t>(sizeof(T)) : 16;
-    return E % V == 0 && address(p) % bytes == 0 && ld * static_cast<int64_t>(sizeof(T)) % bytes == 0;
-}
-inline int router_v(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
-
-template <class T>
-cudaError_t router_forward(const RouterArgs& args, int blocks, cudaStream_t stream) {
-    RouterArgs a = args;
-    const int V = router_v(a.E);
-    a.vector = router_vectors<T>(a.logits, a.ld, a.E, V);
-    switch (V) {
-        case 1: return forward_v<T, 1>(a, blocks, stream);
-        case 2: return forward_v<T, 2>(a, blocks, stream);
-        case 4: return forward_v<T, 4>(a, blocks, stream);
-        case 8: return forward_v<T, 8>(a, blocks, stream);
-        case 16: return forward_v<T, 16>(a, blocks, stream);
-        default: return forward_v<T, 32>(a, blocks, stream);
-    }
+cudaError_t router_forward(const RouterArgs& a, int blocks, cudaStream_t stream) {
+    return a.sigmoid ? forward_scoring<T, true>(a, blocks, stream) : forward_scoring<T, false>(a, blocks, stream);
 }
 template <class T>
-cudaError_t router_backward(const RouterBackwardArgs& args, int blocks, cudaStream_t stream) {
-    RouterBackwardArgs a = args;
-    const int V = router_v(a.E);
-    a.vector = router_vectors<T>(a.logits, a.ld, a.E, V);
-    a.vector_out = router_vectors<T>(a.dlogits, a.E, a.E, V);
-    switch (V) {
-        case 1: return backward_v<T, 1>(a, blocks, stream);
-        case 2: return backward_v<T, 2>(a, blocks, stream);
-        case 4: return backward_v<T, 4>(a, blocks, stream);
-        case 8: return backward_v<T, 8>(a, blocks, stream);
-        case 16: return backward_v<T, 16>(a, blocks, stream);
-        default: return backward_v<T, 32>(a, blocks, stream);
-    }
+cudaError_t router_backward(const RouterBackwardArgs& a, cudaStream_t stream) {
+    return a.sigmoid ? backward_scoring<T, true>(a, stream) : backward_scoring<T, false>(a, stream);
 }
 #endif  // MOE_ROUTER_KERNELS
 

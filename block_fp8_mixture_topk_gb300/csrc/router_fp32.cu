@@ -4,5 +4,5 @@
 
 namespace mfp8 {
 template cudaError_t router_forward<float>(const RouterArgs&, int, cudaStream_t);
-template cudaError_t router_backward<float>(const RouterBackwardArgs&, int, cudaStream_t);
+template cudaError_t router_backward<float>(const RouterBackwardArgs&, cudaStream_t);
 }  // namespace mfp8
