@@ -11,6 +11,7 @@ import ctypes
 import dataclasses
 import os
 import threading
+import typing
 import warnings
 
 import torch
@@ -1117,24 +1118,42 @@ def _fp4_format(fmt):
     return FP4_FORMAT[fmt]
 
 
-@dataclasses.dataclass
-class Fp4Rows:
+class Fp4Rows(typing.NamedTuple):
     """Rows in 4 bits (moe_fp4_quant)."""
     codes: torch.Tensor                   # uint8 [rows, K/2], two e2m1 codes to a byte, the first in the low half
     scales: torch.Tensor                  # uint8, the groups' scales in the products' tiles
     row_scale: torch.Tensor | None        # nvfp4: fp32 [rows]
     format: str                           # "mxfp4" or "nvfp4"
     expert_offsets: torch.Tensor | None   # int32 [E+1] of rows sorted by expert; None: one weight for all rows
+    made: tuple = ()                      # of a result of these functions: its sizes and tensors (checked once)
 
 
 def _fp4_offsets(offsets):
     """Number of experts (0: None) of a valid expert_offsets."""
     if offsets is None:
         return 0
-    _cuda(offsets, torch.int32, "expert_offsets")
-    if offsets.dim() != 1 or offsets.shape[0] < 2:
+    if offsets.dtype is not torch.int32 or not offsets.is_cuda or offsets.dim() != 1 or not offsets.is_contiguous():
+        _cuda(offsets, torch.int32, "expert_offsets")
         raise ValueError(f"expert_offsets must be [E+1], got {list(offsets.shape)}")
-    return offsets.shape[0] - 1
+    E = offsets.shape[0] - 1
+    if E < 1:
+        raise ValueError(f"expert_offsets must be [E+1], got {list(offsets.shape)}")
+    return E
+
+
+_FP4_ROWS, _FP4_MAX_COLS = 224, 32768
+
+
+def _fp4_row_scale_bytes(fmt, n, E, K):
+    """moe_fp4_row_scale_bytes, without the call (which counts in a step of one token)."""
+    if K % 32 or not 0 < K <= _FP4_MAX_COLS or E > 1024 or n >= 2 ** 31 - _FP4_ROWS:
+        return 0
+    return (n // _FP4_ROWS + E + 1) * ((K + 255) // 256) * (2048 << fmt)
+
+
+def _fp4_weight_scale_bytes(fmt, E, N, K):
+    """moe_fp4_weight_scale_bytes, likewise."""
+    return E * ((N + 127) // 128) * ((K + 255) // 256) * (1024 << fmt)
 
 
 def moe_fp4_quant(x, format="mxfp4", expert_offsets=None) -> Fp4Rows:
@@ -1145,33 +1164,37 @@ def moe_fp4_quant(x, format="mxfp4", expert_offsets=None) -> Fp4Rows:
     fmt = _fp4_format(format)
     E = _fp4_offsets(expert_offsets)
     n, K = x.shape
-    L = lib()
     stream = _training_stream("moe_fp4_quant", "x expert_offsets", x, expert_offsets)
     codes = _matrix(n, K // 2, torch.uint8)
-    scales = _vector(L.moe_fp4_row_scale_bytes(fmt, n, E, K), torch.uint8)
+    scales = _vector(_fp4_row_scale_bytes(fmt, n, E, K), torch.uint8)
     row_scale = _vector(n, torch.float32) if fmt else None
-    rc = L.moe_fp4_quant(x.data_ptr(), ld, code, fmt, None if E == 0 else expert_offsets.data_ptr(), E, n, K,
-                         codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt else None, stream)
-    _check("moe_fp4_quant", rc)
-    return Fp4Rows(codes, scales, row_scale, format, expert_offsets)
+    rc = lib().moe_fp4_quant(x.data_ptr(), ld, code, fmt, expert_offsets.data_ptr() if E else None, E, n, K,
+                             codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt else None, stream)
+    if rc:
+        _check("moe_fp4_quant", rc)
+    return Fp4Rows(codes, scales, row_scale, format, expert_offsets,
+                   (fmt, E, n, K, codes, scales, row_scale, expert_offsets, format))
 
 
 def _fp4_rows(rows):
     """(format code, number of experts, rows, K) of an Fp4Rows whose parts fit together."""
-    fmt = _fp4_format(rows.format)
-    E = _fp4_offsets(rows.expert_offsets)
-    _cuda(rows.codes, torch.uint8, "rows.codes")
-    if rows.codes.dim() != 2:
-        raise ValueError(f"rows.codes must be a matrix, got {list(rows.codes.shape)}")
-    n, K = rows.codes.shape[0], 2 * rows.codes.shape[1]
+    codes, scales, row_scale, format, offsets, made = rows
+    if made and made[4] is codes and made[5] is scales and made[6] is row_scale and made[7] is offsets and made[8] is format:
+        return made[:4]
+    fmt = _fp4_format(format)
+    E = _fp4_offsets(offsets)
+    _cuda(codes, torch.uint8, "rows.codes")
+    if codes.dim() != 2:
+        raise ValueError(f"rows.codes must be a matrix, got {list(codes.shape)}")
+    n, K = codes.shape[0], 2 * codes.shape[1]
     if n > _INT_MAX or K > _INT_MAX:
         raise _too_large("rows.codes")
-    _dense(rows.scales, "rows.scales", torch.uint8, (lib().moe_fp4_row_scale_bytes(fmt, n, E, K),))
+    _dense(scales, "rows.scales", torch.uint8, (_fp4_row_scale_bytes(fmt, n, E, K),))
     if fmt:
-        if rows.row_scale is None:
+        if row_scale is None:
             raise ValueError("nvfp4 rows need a row_scale")
-        _dense(rows.row_scale, "rows.row_scale", torch.float32, (n,))
-    elif rows.row_scale is not None:
+        _dense(row_scale, "rows.row_scale", torch.float32, (n,))
+    elif row_scale is not None:
         raise ValueError("mxfp4 rows have no row_scale")
     return fmt, E, n, K
 
@@ -1181,11 +1204,13 @@ def moe_fp4_dequant(rows: Fp4Rows, dtype=torch.bfloat16):
     fmt, E, n, K = _fp4_rows(rows)
     if dtype not in DTYPE:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    stream = _stream("codes scales row_scale expert_offsets", rows.codes, rows.scales, rows.row_scale, rows.expert_offsets)
+    codes, scales, row_scale, _, offsets, _ = rows
+    stream = _stream("codes scales row_scale expert_offsets", codes, scales, row_scale, offsets)
     out = _matrix(n, K, dtype)
-    rc = lib().moe_fp4_dequant(rows.codes.data_ptr(), rows.scales.data_ptr(), _or_none(rows.row_scale) if n else None, fmt,
-                               _or_none(rows.expert_offsets), E, n, K, DTYPE[dtype], out.data_ptr(), stream)
-    _check("moe_fp4_dequant", rc)
+    rc = lib().moe_fp4_dequant(codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt and n else None, fmt,
+                               offsets.data_ptr() if E else None, E, n, K, DTYPE[dtype], out.data_ptr(), stream)
+    if rc:
+        _check("moe_fp4_dequant", rc)
     return out
 
 
@@ -1223,37 +1248,49 @@ def moe_fp4_pack_scales(scales, format="mxfp4", gate_up=False):
     return out
 
 
-def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, epilogue):
-    fmt, E, n, K = _fp4_rows(rows)
+def _fp4_weights(fmt, E, K, w, w_scales, w_global):
+    """Rows N of each expert's weights, which fit rows of E experts and K columns (the checks that failed, with their words)."""
     _cuda(w, torch.uint8, "w")
-    if w.dim() != 3 or 2 * w.shape[2] != K or w.shape[0] != max(E, 1):
-        raise ValueError(f"w must be [{max(E, 1)}, N, {K // 2}] for these rows, got {list(w.shape)}")
+    if w.dim() != 3 or 2 * w.shape[2] != K or w.shape[0] != E:
+        raise ValueError(f"w must be [{E}, N, {K // 2}] for these rows, got {list(w.shape)}")
     N = w.shape[1]
     if N > _INT_MAX:
         raise _too_large("w")
-    if dtype not in DTYPE or (epilogue and dtype == torch.float32):
-        raise TypeError(f"dtype must be bfloat16{' or float16' if epilogue else ', float16 or float32'}, got {dtype}")
     _cuda(w_scales, torch.uint8, "w_scales")
-    L = lib()
-    if w_scales.numel() != L.moe_fp4_weight_scale_bytes(fmt, max(E, 1), N, K):
+    if w_scales.numel() != _fp4_weight_scale_bytes(fmt, E, N, K):
         raise ValueError("w_scales must be moe_fp4_pack_scales of w's scales in the rows' format")
     if (w_global is None) != (fmt == 0):
         raise ValueError("w_global is needed with nvfp4, and only there")
     if fmt:
-        _dense(w_global, "w_global", torch.float32, (max(E, 1),))
-    stream = _stream("rows.codes rows.scales rows.row_scale rows.expert_offsets w w_scales w_global", rows.codes, rows.scales,
-                     rows.row_scale, rows.expert_offsets, w, w_scales, w_global)
+        _dense(w_global, "w_global", torch.float32, (E,))
+    return N
+
+
+def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, epilogue):
+    fmt, E, n, K = _fp4_rows(rows)
+    codes, scales, row_scale, format, offsets, _ = rows
+    experts = E or 1
+    N = _fp4_weights(fmt, experts, K, w, w_scales, w_global)
+    code = DTYPE.get(dtype)
+    if code is None or (epilogue and code == 2):
+        raise TypeError(f"dtype must be bfloat16{' or float16' if epilogue else ', float16 or float32'}, got {dtype}")
+    stream = _stream("rows.codes rows.scales rows.row_scale rows.expert_offsets w w_scales w_global", codes, scales, row_scale,
+                     offsets, w, w_scales, w_global)
     out_scales = None
     if epilogue == 2:
         out = _matrix(n, N // 4, torch.uint8)
-        out_scales = _vector(L.moe_fp4_row_scale_bytes(fmt, n, E, N // 2), torch.uint8)
+        out_scales = _vector(_fp4_row_scale_bytes(fmt, n, E, N // 2), torch.uint8)
     else:
         out = _matrix(n, N // 2 if epilogue else N, dtype)
-    rc = L.moe_fp4_expert_gemm(rows.codes.data_ptr(), rows.scales.data_ptr(), _or_none(rows.row_scale) if n else None, fmt,
-                               w.data_ptr(), w_scales.data_ptr(), _or_none(w_global), _or_none(rows.expert_offsets), n,
-                               max(E, 1), N, K, epilogue, DTYPE[dtype], out.data_ptr(), _or_none(out_scales), stream)
-    _check("moe_fp4_expert_gemm", rc)
-    return out if out_scales is None else Fp4Rows(out, out_scales, None, rows.format, rows.expert_offsets)
+    rc = lib().moe_fp4_expert_gemm(codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt and n else None, fmt,
+                                   w.data_ptr(), w_scales.data_ptr(), w_global.data_ptr() if fmt else None,
+                                   offsets.data_ptr() if E else None, n, experts, N, K, epilogue, code, out.data_ptr(),
+                                   None if out_scales is None else out_scales.data_ptr(), stream)
+    if rc:
+        _check("moe_fp4_expert_gemm", rc)
+    if out_scales is None:
+        return out
+    return Fp4Rows(out, out_scales, None, format, offsets, (fmt, E, n, N // 2, out, out_scales, None, offsets, format))
 
 
 def moe_fp4_expert_gemm(rows: Fp4Rows, w, w_scales, w_global=None, dtype=torch.bfloat16):
