@@ -4,8 +4,8 @@
 //   mxfp4  scale = the smallest power of two s with max|x| <= 6 s, code = e2m1(x / s): x / s is exact
 //   nvfp4  r = fp32(max|x of the row| / 2688), b = e4m3(max|x of the group| / (6 r)), code = e2m1(x / (b r)): the
 //          quotients are taken in fp32 a little too large and a little too small; where the two round differently,
-//          a comparison with the border itself, its product exact in two fp32 parts, decides (with 16-bit rows a few
-//          per cent of the groups: their quotients are often nearly a border; in fp64 the kernel took 5 times as long)
+//          a comparison with the border itself, its product exact in two fp32 parts, decides; 16-bit rows, whose quotients
+//          are often nearly a border, need neither (border_side)
 // An infinity or NaN makes its group (mxfp4: scale NaN) or row (nvfp4: row scale NaN) NaN.
 //
 // Memory is the bound: a thread loads its two vectors of 16 elements whole (32 bytes at a time) before it uses the first,
@@ -69,11 +69,28 @@ struct QuantArgs {
 constexpr float kSlack = 0x1p-21f;       // over the error of a quotient or product of a few fp32 operations
 constexpr float kLeastRow = 0x1p-100f;
 
-// A group's scale byte and its part's codes, nvfp4 (rs > 0).
+// Rows of 16 bits need no borders.  With the largest magnitude m, r is m / 2688 rounded, and a quotient by the exact m / 2688 is
+// g * 448 / m or x * 2688 / (b m): of numbers of 11, 4 and few bits, so it is a border or away from it by 2^-16 of itself or
+// more, and the rounding of r only decides on which side of a border that it would meet a quotient lies: below where r
+// is too large.  A factor of 1 -+ 2^-20 takes it there in spite of the arithmetic's 2^-21.  0 where r is exact: those
+// rows meet borders, and are decided as 32-bit ones.
 template <class T>
-__device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top, float rs, uint2* codes) {
+__device__ __forceinline__ float border_side(float m, float rs) {
+    if (sizeof(T) == 4) return 0.0f;
+    const float over = fmaf(rs, 2688.0f, -m);
+    return over > 0.0f ? 1.0f - 0x1p-20f : over < 0.0f ? 1.0f + 0x1p-20f : 0.0f;
+}
+
+// A group's scale byte and its part's codes, nvfp4 (rs > 0; side: border_side).
+template <class T>
+__device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top, float rs, float side, uint2* codes) {
     const float g = __uint_as_float(top);
     *codes = make_uint2(0, 0);
+    if (sizeof(T) == 2 && side != 0.0f && rs >= kLeastRow) {
+        const uint32_t s = e4m3x2(__fdividef(g, 6.0f * rs) * side, 0.0f) & 0xffu;
+        if (s > 0) *codes = e2m1_words(x, __fdividef(1.0f, e4m3_number(s) * rs) * side);
+        return s;
+    }
     if (rs < kLeastRow) {
         const uint32_t s = e4m3_tiny(g, rs);
         if (s > 0) {
@@ -107,8 +124,14 @@ __device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top,
     return s;
 }
 
+// Blocks to an SM: with rows of 16 bits 1536 threads (40 registers), 98 KB of rows under way.
+template <class T>
+constexpr int quant_blocks(int threads) {
+    return (sizeof(T) == 2 && threads < 1024 ? 1536 : 1024) / threads;
+}
+
 template <class T, int FMT, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) fp4_quant_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_kernel(const QuantArgs a) {
     grid_dependency_wait();
     constexpr int G = fp4_group(FMT), LANES = G / 16, W = fp4_words(FMT);   // lanes of a group
     __shared__ uint32_t s_top[32];
@@ -134,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fp4_quant_kernel(cons
         top[i] = x[i].top();
         if (LANES == 2) top[i] = max(top[i], __shfl_xor_sync(kAll, top[i], 1));
     }
-    float rs = 1.0f;
+    float rs = 1.0f, side = 0.0f;
     if constexpr (FMT == MOE_FP4_NVFP4) {
         uint32_t m = __reduce_max_sync(kAll, max(top[0], top[1]));
         if (a.warps > 1) {
@@ -143,6 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fp4_quant_kernel(cons
             m = __reduce_max_sync(kAll, lane < a.warps ? s_top[own * a.warps + lane] : 0u);
         }
         rs = m < 0x7f800000u ? __fdiv_rn(__uint_as_float(m), 2688.0f) : __int_as_float(0x7fffffff);
+        side = border_side<T>(__uint_as_float(m), rs);
         if (live && at == 0) a.row_scale[r] = rs;
     }
     if (!live) return;   // (whole warps)
@@ -157,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) fp4_quant_kernel(cons
         if constexpr (FMT == MOE_FP4_MXFP4) {
             s = mxfp4_group(x[i], top[i], &w);
         } else if (rs > 0.0f) {   // not zero and not NaN
-            s = nvfp4_group(x[i], top[i], rs, &w);
+            s = nvfp4_group(x[i], top[i], rs, side, &w);
         }
         if (v < vecs) codes[v] = w;
         else s = 0;   // columns past K: a scale that is a number
@@ -185,6 +209,7 @@ struct DequantArgs {
     int64_t rows;
     int K, E;
     void* out;
+    bool align32;              // out is at a 32-byte address
 };
 
 // Values of the codes: code times group scale is exact in fp32, the row's scale and the result's type round.
@@ -226,9 +251,18 @@ __global__ void __launch_bounds__(1024) fp4_dequant_kernel(const DequantArgs a, 
             e[2 * j] = from_f32<T>(FMT == MOE_FP4_NVFP4 ? f.x * scale * rs : f.x * scale);
             e[2 * j + 1] = from_f32<T>(FMT == MOE_FP4_NVFP4 ? f.y * scale * rs : f.y * scale);
         }
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(out + v * 8) = *reinterpret_cast<const uint4*>(e);
+        } else {   // 32 bytes at once (rows at 16-byte addresses: K is a multiple of 32, out of 16 bytes)
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(e);
+            if (a.align32)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + v * 8), "r"(u[0]), "r"(u[1]),
+                             "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                             : "memory");
+            else
 #pragma unroll
-        for (int j = 0; j < static_cast<int>(sizeof(e)) / 16; ++j)
-            reinterpret_cast<uint4*>(out + v * 8)[j] = reinterpret_cast<const uint4*>(e)[j];
+                for (int j = 0; j < 2; ++j) reinterpret_cast<uint4*>(out + v * 8)[j] = reinterpret_cast<const uint4*>(e)[j];
+        }
     }
 }
 
@@ -285,8 +319,9 @@ cudaError_t quant_type(QuantArgs a, cudaStream_t stream) {
     a.warps = (all + 32 * kQuantVecs - 1) / (32 * kQuantVecs);
     const int per = a.warps < 8 ? 8 / a.warps : 1;                              // rows of a block of up to 256 threads
     const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(32 * a.warps * per);
-    return a.warps <= 8 ? launch_pdl(fp4_quant_kernel<T, FMT, 256>, grid, block, 0, stream, a)
-                        : launch_pdl(fp4_quant_kernel<T, FMT, 1024>, grid, block, 0, stream, a);
+    if (a.warps <= 8) return launch_pdl(fp4_quant_kernel<T, FMT, 256>, grid, block, 0, stream, a);
+    return a.warps <= 16 ? launch_pdl(fp4_quant_kernel<T, FMT, 512>, grid, block, 0, stream, a)
+                         : launch_pdl(fp4_quant_kernel<T, FMT, 1024>, grid, block, 0, stream, a);
 }
 template <int FMT>
 cudaError_t quant_format(int dtype, const QuantArgs& a, cudaStream_t stream) {
@@ -395,7 +430,7 @@ int moe_fp4_dequant(const uint8_t* codes, const uint8_t* scales, const float* ro
         return MOE_ERR_INVALID_ARG;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status)) != MOE_OK) return rc;
-    const DequantArgs a = {codes, scales, row_scale, expert_offsets, num_rows, K, E, out};
+    const DequantArgs a = {codes, scales, row_scale, expert_offsets, num_rows, K, E, out, address(out) % 32 == 0};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(fmt == MOE_FP4_MXFP4 ? dequant_format<MOE_FP4_MXFP4>(dtype, a, s)
                                             : dequant_format<MOE_FP4_NVFP4>(dtype, a, s));
