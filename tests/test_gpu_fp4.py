@@ -246,6 +246,11 @@ CASES = [  # rows per expert, rows of no expert, N, K
     ([1, 0] * 512, 1, 32, 32),
     ([513, 1500, 0, 40, 1025], 9, 352, 544),
     ([448, 449, 2000, 97], 0, 800, 2080),
+    # many items: two row tiles to one
+    ([5000, 0, 449, 20000, 300, 224, 1], 5, 4096, 64),
+    ([5000, 0, 449, 20000, 300, 448, 1], 5, 4096, 512),
+    ([5000, 0, 449, 20000, 300, 224, 1], 0, 4096, 544),
+    ([17, 25000, 0, 673, 240], 3, 4128, 1312),
 ]
 
 
@@ -350,12 +355,13 @@ def test_captured_and_on_another_stream():
     assert torch.equal(out, step())
 
 
-def test_results_repeat():
+@pytest.mark.parametrize("counts, N", [([300, 5, 700], 512), ([9000, 5, 18000], 4096)])
+def test_results_repeat(counts, N):
     g = gen(17)
-    off = offsets_of([300, 5, 700])
+    off = offsets_of(counts)
     for fmt in FORMATS:
-        q, tiles, glob, _ = make_weights(g, 3, 512, 1024, fmt)
-        rows = moe.moe_fp4_quant(spread(g, 1005, 1024, torch.bfloat16), fmt, off)
+        q, tiles, glob, _ = make_weights(g, 3, N, 1024, fmt)
+        rows = moe.moe_fp4_quant(spread(g, sum(counts), 1024, torch.bfloat16), fmt, off)
         want = moe.moe_fp4_expert_gemm(rows, q, tiles, glob)
         for _ in range(20):
             assert torch.equal(moe.moe_fp4_expert_gemm(rows, q, tiles, glob), want)
