@@ -82,10 +82,10 @@ template <class T>
 cudaError_t router_backward(const RouterBackwardArgs& a, cudaStream_t stream);
 
 #ifdef MOE_ROUTER_KERNELS
-// Rows that can be loaded V elements at a time: E a multiple of V, addresses of the vectors (16 bytes at most).
+// Rows that can be loaded V elements at a time: E a multiple of V, addresses of the vectors (32 bytes at most).
 template <class T>
 bool router_vectors(const void* p, int64_t ld, int E, int V) {
-    const int64_t bytes = V * static_cast<int64_t>(sizeof(T)) < 16 ? V * static_cast<int64_t>(sizeof(T)) : 16;
+    const int64_t size = V * static_cast<int64_t>(sizeof(T)), bytes = size < 32 ? size : 32;
     return E % V == 0 && address(p) % bytes == 0 && ld * static_cast<int64_t>(sizeof(T)) % bytes == 0;
 }
 namespace {
@@ -120,7 +120,7 @@ __device__ __forceinline__ float of_ordered(uint32_t u) {
 // (No NaN.)
 __device__ __forceinline__ float warp_max(float v) { return of_ordered(__reduce_max_sync(kAll, ordered(v))); }
 
-// V logits from p on, those past `count` kNone.
+// V logits from p on, those past `count` -inf (vector: count is 0 or V).
 template <class T, int V>
 struct Logits {
     static constexpr int kBytes = V * static_cast<int>(sizeof(T));
@@ -129,24 +129,40 @@ struct Logits {
                  typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
     union {
         Word w[kWords];
+        uint32_t u[kBytes >= 4 ? kBytes / 4 : 1];
         T e[V];
     };
     __device__ __forceinline__ Logits() {}
     __device__ __forceinline__ void load(const T* p, int count, bool vector) {
-        if (vector) {
-            if (count > 0) {
+        if (vector && count > 0) {
+            if constexpr (kBytes % 32 == 0) {   // whole sectors
+#pragma unroll
+                for (int i = 0; i < kBytes / 4; i += 8)
+                    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                                 : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3]), "=r"(u[i + 4]), "=r"(u[i + 5]),
+                                   "=r"(u[i + 6]), "=r"(u[i + 7])
+                                 : "l"(reinterpret_cast<const uint32_t*>(p) + i));
+            } else {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const Word*>(p) + i);
             }
         } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < count) e[v] = p[v];
+            for (int v = 0; v < V; ++v) e[v] = v < count ? p[v] : from_f32<T>(-INFINITY);
         }
     }
     __device__ __forceinline__ void store(T* p, int count, bool vector) const {
         if (vector) {
-            if (count > 0) {
+            if (count <= 0) return;
+            if constexpr (kBytes % 32 == 0) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 4; i += 8)
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                     reinterpret_cast<uint32_t*>(p) + i),
+                                 "r"(u[i]), "r"(u[i + 1]), "r"(u[i + 2]), "r"(u[i + 3]), "r"(u[i + 4]), "r"(u[i + 5]),
+                                 "r"(u[i + 6]), "r"(u[i + 7])
+                                 : "memory");
+            } else {
 #pragma unroll
                 for (int i = 0; i < kWords; ++i) reinterpret_cast<Word*>(p)[i] = w[i];
             }
@@ -160,10 +176,10 @@ struct Logits {
 
 // A lane's logits; NaN and +inf count as -inf (true in *odd).
 template <class T, int V>
-__device__ __forceinline__ void finite_logits(const Logits<T, V>& raw, int count, float (&l)[V], bool* odd) {
+__device__ __forceinline__ void finite_logits(const Logits<T, V>& raw, float (&l)[V], bool* odd) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const float x = v < count ? to_f32(raw.e[v]) : kNone;
+        const float x = to_f32(raw.e[v]);
         l[v] = x < INFINITY ? x : kNone;
         *odd |= !(x < INFINITY);
     }
@@ -542,7 +558,7 @@ __device__ __noinline__ void route_token(const RouterArgs& a, int64_t t, int lan
     raw.load(logits + seat.first, seat.count, false);
     float l[V], none[V], lse;
     bool odd = false;
-    finite_logits(raw, seat.count, l, &odd);
+    finite_logits(raw, l, &odd);
     float m = l[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
@@ -661,10 +677,10 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
         const bool real = t < a.T;
         const T* row = logits + t * a.ld;
         Logits<T, V> raw;
-        raw.load(row + first, real ? count : 0, a.vector);
         const bool wanted = real && (!a.valid || a.valid[t] != 0);
+        raw.load(row + first, wanted ? count : 0, a.vector);
         float l[V], s[V];
-        finite_logits(raw, wanted ? count : 0, l, &odd);
+        finite_logits(raw, l, &odd);
         float m = l[0];
 #pragma unroll
         for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
@@ -901,10 +917,10 @@ __global__ void __launch_bounds__(router_warps(V, 32) * 32, 1) router_warp_kerne
     for (int64_t t = blockIdx.x + static_cast<int64_t>(warp) * gridDim.x; t < a.T; t += step) {
         const T* row = logits + t * a.ld;
         Logits<T, V> raw;
-        raw.load(row + seat.first, seat.count, a.vector);
         const bool wanted = !a.valid || a.valid[t] != 0;
+        raw.load(row + seat.first, wanted ? seat.count : 0, a.vector);
         float l[V];
-        finite_logits(raw, wanted ? seat.count : 0, l, &odd);
+        finite_logits(raw, l, &odd);
         float m = l[0];
 #pragma unroll
         for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
@@ -926,32 +942,34 @@ __global__ void __launch_bounds__(router_warps(V, 32) * 32, 1) router_warp_kerne
 
 // The gradient: L lanes to a token, V experts to a lane (a warp has 32 / L tokens under way, its sums take log2 L steps).
 template <class T, int V, int L, bool SIGMOID>
-__global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 3 : 1) router_backward_kernel(const RouterBackwardArgs a) {
+__global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 4 : 2) router_backward_kernel(const RouterBackwardArgs a) {
     grid_dependency_wait();
-    // the loads' factors h [L V], rows of chosen gradients [tokens][L V]; expert e at e % V * L + e / V
+    // the loads' factors h, rows of chosen gradients [tokens]; expert e of one at e % V * P + e / V (P odd: neighbours and a
+    // lane's own fall into different banks)
+    constexpr int P = L + 1;
     extern __shared__ float s_mem[];
     constexpr int TOKENS = kBackwardWarps * 32 / L;
     const int lane = threadIdx.x & 31, sub = lane % L, slot = threadIdx.x / L;
     const int first = sub * V, count = min(max(a.E - first, 0), V);
     const T* logits = static_cast<const T*>(a.logits);
-    float* row = s_mem + (slot + 1) * (L * V);
+    float* row = s_mem + (slot + 1) * (P * V);
     const bool shares = a.balance != 0.0f;
     const bool dense = shares || a.z != 0.0f || (!SIGMOID && !a.renorm);   // every logit has a gradient
     // the first token's logits are under way while the loads' factors are made
     const int64_t step = static_cast<int64_t>(gridDim.x) * TOKENS;
     int64_t t0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
     Logits<T, V> raw;
-    raw.load(logits + (t0 + slot) * a.ld + first, dense && t0 + slot < a.T ? count : 0, a.vector);
+    if (a.vector) raw.load(logits + (t0 + slot) * a.ld + first, dense && t0 + slot < a.T ? count : 0, true);
     float z_by = 0.0f;
     if (shares || a.z != 0.0f) {
         const float n = fmaxf(static_cast<float>(*a.live), 1.0f);
         z_by = 2.0f * a.z / n;
         const float by = a.balance * static_cast<float>(a.E) / (static_cast<float>(a.k) * n) / n;
         for (int e = threadIdx.x; e < L * V; e += kBackwardWarps * 32)
-            s_mem[e % V * L + e / V] = shares && e < a.E ? by * static_cast<float>(a.counts[e]) : 0.0f;
+            s_mem[e % V * P + e / V] = shares && e < a.E ? by * static_cast<float>(a.counts[e]) : 0.0f;
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) row[v * L + sub] = 0.0f;
+    for (int v = 0; v < V; ++v) row[v * P + sub] = 0.0f;
     __syncthreads();
     bool bad = false;
 
@@ -968,35 +986,52 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 3 : 1) router_b
             any |= id >= 0 && id < a.E;
         }
         const bool some = lanes_max<L>(any ? 1.0f : 0.0f) > 0.0f;   // the token has an expert
-        float s[V], m = 0.0f, z = 1.0f;   // s: the score (softmax: times z); 0 of an expert that cannot be chosen
-        float e[V];                       // sigmoid: exp(-|l|), negative where l is
+        // of each expert c: softmax the score times z, sigmoid the score times 1 - score, which is e / (1 + e)^2 with e = exp(-|l|);
+        // 0 of an expert that cannot be chosen
+        float c[V], m = 0.0f, z = 1.0f, mean_h = 0.0f;
         if (dense) {
-            float l[V];
             bool odd = false;
-            finite_logits(raw, real && some ? count : 0, l, &odd);
-            if (!SIGMOID) {
-                m = l[0];
+            if (a.vector) {
+                finite_logits(raw, c, &odd);
+            } else {   // by neighbouring lanes, through the token's row
+                if (real)
+                    for (int e = sub; e < a.E; e += L) row[e % V * P + e / V] = to_f32(logits[t * a.ld + e]);
+                __syncwarp();
 #pragma unroll
-                for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+                for (int v = 0; v < V; ++v) {
+                    const float x = real && v < count ? row[v * P + sub] : kNone;
+                    c[v] = x < INFINITY ? x : kNone;
+                    row[v * P + sub] = 0.0f;
+                }
+                __syncwarp();
+            }
+            if (!SIGMOID) {
+                m = c[0];
+#pragma unroll
+                for (int v = 1; v < V; ++v) m = fmaxf(m, c[v]);
                 m = lanes_max<L>(m);
                 m = m > kNone ? m : 0.0f;
             }
             z = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                float score;
                 if (SIGMOID) {
-                    const float p = __expf(-fabsf(l[v]));
-                    s[v] = __fdividef(l[v] < 0.0f ? p : 1.0f, 1.0f + p);
-                    e[v] = l[v] < 0.0f ? -p : p;
+                    const float e = __expf(-fabsf(c[v])), r = __fdividef(1.0f, 1.0f + e), er = e * r;
+                    score = c[v] < 0.0f ? er : r;
+                    c[v] = er * r;
                 } else {
-                    s[v] = __expf(l[v] - m);
+                    score = c[v] = __expf(c[v] - m);
                 }
-                z += s[v];
+                z += score;
+                if (shares) mean_h = fmaf(score, s_mem[v * P + sub], mean_h);
             }
             z = lanes_sum<L>(z);
+            if (shares) mean_h = lanes_sum<L>(mean_h);
         }
-        if (t + step < a.T) raw.load(logits + (t + step) * a.ld + first, dense ? count : 0, a.vector);
-        const float per = __fdividef(1.0f, fmaxf(z, 1e-37f));
+        if (a.vector && t + step < a.T) raw.load(logits + (t + step) * a.ld + first, dense ? count : 0, true);
+        const float per = some ? __fdividef(1.0f, fmaxf(z, 1e-37f)) : 0.0f;
+        mean_h *= per;
         // the chosen experts' part: sums over them, then each one's gradient (a lane has one, or every L-th)
         const auto part = [&](int id, float dw, float* q, float* g, float* phi) {
             const bool chose = id >= 0 && id < a.E;
@@ -1054,42 +1089,42 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 3 : 1) router_b
         }
         sum_g = lanes_sum<L>(sum_g);
         const float inner = a.renorm ? sum_g : 0.0f;
-        if (any && id0 >= 0 && id0 < a.E) row[id0 % V * L + id0 / V] = phi0 * q0 * (g0 - inner);
+        if (any && id0 >= 0 && id0 < a.E) row[id0 % V * P + id0 / V] = phi0 * q0 * (g0 - inner);
         for (int j = sub + L; j < a.k; j += L) {
             float q, g, phi;
             const int id = again(j, &q, &g, &phi);
-            if (id >= 0) row[id % V * L + id / V] = phi * q * (g - inner);
+            if (id >= 0) row[id % V * P + id / V] = phi * q * (g - inner);
         }
         __syncwarp();
-        float mean_h = 0.0f;
-        if (shares) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) mean_h = fmaf(s[v], s_mem[v * L + sub], mean_h);
-            mean_h = lanes_sum<L>(mean_h) * per;
-        }
         // of every softmax logit: the z loss, and the chosen sum where it is not renormalised
         const float each = SIGMOID || !some ? 0.0f : (a.z != 0.0f ? z_by * (m + logf(z)) : 0.0f) - (a.renorm ? 0.0f : sum_g);
-        Logits<T, V> out;
+        T* to = static_cast<T*>(a.dlogits) + t * a.E;
+        const auto gradient = [&](int v) {
+            const float r = row[v * P + sub];
+            return dense ? fmaf(c[v] * per, shares ? s_mem[v * P + sub] - mean_h + each : each, r) : r;
+        };
+        if (a.vector_out) {
+            Logits<T, V> out;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float r = row[v * L + sub];
-            if (dense) {
-                const float p = s[v] * per;
-                float by_p = each;
-                // 1 - s, with its digits where s is near 1
-                if (shares) by_p += (s_mem[v * L + sub] - mean_h) * (!SIGMOID ? 1.0f : e[v] > 0.0f ? e[v] * s[v] : 1.0f - s[v]);
-                r = fmaf(p, by_p, r);
+            for (int v = 0; v < V; ++v) out.e[v] = from_f32<T>(gradient(v));
+            __syncwarp();
+            if (id0 >= 0 && id0 < a.E) row[id0 % V * P + id0 / V] = 0.0f;
+            for (int j = sub + L; j < a.k; j += L) {
+                const int id = chosen(j);
+                if (id >= 0 && id < a.E) row[id % V * P + id / V] = 0.0f;
             }
-            out.e[v] = from_f32<T>(r);
+            if (real) out.store(to + first, count, true);
+        } else {   // rows of odd sizes: by neighbouring lanes (element by element from each lane's own, they took twice as long)
+#pragma unroll
+            for (int v = 0; v < V; ++v) row[v * P + sub] = gradient(v);
+            __syncwarp();
+            if (real)
+                for (int e = sub; e < a.E; e += L) to[e] = from_f32<T>(row[e % V * P + e / V]);
+            __syncwarp();
+#pragma unroll
+            for (int v = 0; v < V; ++v) row[v * P + sub] = 0.0f;
         }
         __syncwarp();
-        if (id0 >= 0 && id0 < a.E) row[id0 % V * L + id0 / V] = 0.0f;
-        for (int j = sub + L; j < a.k; j += L) {
-            const int id = chosen(j);
-            if (id >= 0 && id < a.E) row[id % V * L + id / V] = 0.0f;
-        }
-        __syncwarp();
-        if (real) out.store(static_cast<T*>(a.dlogits) + t * a.E + first, count, a.vector_out);
     }
     if (bad) status_set(a.status, MOE_STATUS_BAD_EXPERT_ID);
 }
@@ -1138,7 +1173,7 @@ cudaError_t backward_v(RouterBackwardArgs a, cudaStream_t stream) {
     constexpr int TOKENS = kBackwardWarps * 32 / L;
     const int64_t blocks = (static_cast<int64_t>(a.T) + TOKENS - 1) / TOKENS, most = kPlanSms * 8;
     return launch_pdl(router_backward_kernel<T, V, L, SIGMOID>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                      dim3(kBackwardWarps * 32), static_cast<size_t>(TOKENS + 1) * L * V * sizeof(float), stream, a);
+                      dim3(kBackwardWarps * 32), static_cast<size_t>(TOKENS + 1) * (L + 1) * V * sizeof(float), stream, a);
 }
 // 8 lanes to a token up to 128 experts, 16 up to 256.
 template <class T, bool SIGMOID>
