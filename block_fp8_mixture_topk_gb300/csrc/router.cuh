@@ -206,6 +206,39 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     for (int o = 16; o > 0; o >>= 1) v = max(v, static_cast<uint64_t>(__shfl_xor_sync(kAll, static_cast<unsigned long long>(v), o)));
     return v;
 }
+// exp(x) in fp64 for x <= 0, to a few 2^-53 of itself: x = n ln2 / 32 + r, 2^(n / 32) from a table and exp(r) by its series
+// (|r| < 0.011: the sixth power's term is the last above 2^-55; a table-driven exponential after Tang, ACM TOMS 15, 1989).
+// A third of the fp64 instructions of exp(), which has more to take care of.  Below 2^-1000: 0.
+__device__ const double kPowers[32] = {
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
+__device__ __forceinline__ double exp64(double x) {
+    const double magic = 0x1.8p52;
+    const double t = fma(x, 0x1.71547652b82fep+5, magic), n = t - magic;
+    const int k = __double2loint(t);
+    double r = fma(n, -0x1.62e42fee00000p-6, x);   // the first part of ln2 / 32 has 32 bits: exact
+    r = fma(n, -0x1.a39ef35793c76p-38, r);
+    double p = fma(r, 1.0 / 720.0, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p * r, r, r);
+    const double power = kPowers[k & 31], value = fma(power, p, power);
+    const int up = k >> 5;
+    return x < -693.0 ? 0.0 : __hiloint2double(__double2hiint(value) + up * (1 << 20), __double2loint(value));
+}
+
+__device__ __forceinline__ double sigmoid64(double x) {
+    const double e = exp64(-fabs(x));
+    return (x < 0.0 ? e : 1.0) / (1.0 + e);
+}
+
 template <int V, bool SIGMOID>
 __device__ __noinline__ int choose_exact(const float* l, float m, const RouterArgs& a, int first, int count, int lanes) {
     const int lane = threadIdx.x & 31;
@@ -214,7 +247,7 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const double x = l[v];
-        s[v] = l[v] == kNone ? 0.0 : SIGMOID ? exp(-x) : exp(x - m);
+        s[v] = l[v] == kNone ? 0.0 : exp64(SIGMOID ? -fabs(x) : x - m);
     }
     if (!SIGMOID) {
         z = 0.0;
@@ -225,7 +258,7 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const double b = a.bias && v < count ? static_cast<double>(a.bias[first + v]) : 0.0;
-        key[v] = l[v] == kNone ? 0u : ordered((SIGMOID ? 1.0 / (1.0 + s[v]) : s[v] / z) + b);
+        key[v] = l[v] == kNone ? 0u : ordered((SIGMOID ? (l[v] < 0.0f ? s[v] : 1.0) / (1.0 + s[v]) : s[v] / z) + b);
     }
     if (a.groups > 1) {
         uint64_t t1 = 0, t2 = 0;
@@ -385,7 +418,7 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                         const uint32_t e = s_near[lane].x;
                         group = s_near[lane].y;
                         const double x64 = to_f32(logits[e]);
-                        wide = ordered(1.0 / (1.0 + exp(-x64)) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0));
+                        wide = ordered(sigmoid64(x64) + (a.bias ? static_cast<double>(a.bias[e]) : 0.0));
                     }
                     uint64_t u1 = 0, u2 = 0;
                     for (int i = 0; i < found; ++i) {
@@ -462,13 +495,14 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                 double all = 1.0;
                 if (!SIGMOID) {
                     all = 0.0;
-                    for (int v = 0; v < V; ++v) all += exp(static_cast<double>(l[v]) - m);
+                    #pragma unroll
+                    for (int v = 0; v < V; ++v) all += l[v] > kNone ? exp64(static_cast<double>(l[v]) - m) : 0.0;
                     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
                 }
                 uint64_t wide = 0;
                 if (lane < found) {
                     const double x64 = to_f32(logits[mine.y]);
-                    const double s64 = SIGMOID ? 1.0 / (1.0 + exp(-x64)) : exp(x64 - m) / all;
+                    const double s64 = SIGMOID ? sigmoid64(x64) : exp64(x64 - m) / all;
                     wide = ordered(s64 + static_cast<double>(a.bias[mine.y]));
                 }
                 place = 0;
