@@ -258,7 +258,9 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const double b = a.bias && v < count ? static_cast<double>(a.bias[first + v]) : 0.0;
-        key[v] = l[v] == kNone ? 0u : ordered((SIGMOID ? (l[v] < 0.0f ? s[v] : 1.0) / (1.0 + s[v]) : s[v] / z) + b);
+        key[v] = l[v] == kNone || b == static_cast<double>(kNone)
+                     ? 0u
+                     : ordered((SIGMOID ? (l[v] < 0.0f ? s[v] : 1.0) / (1.0 + s[v]) : s[v] / z) + b);
     }
     if (a.groups > 1) {
         uint64_t t1 = 0, t2 = 0;
@@ -627,6 +629,8 @@ constexpr size_t router_smem(bool stats) {
     return 2 * slots + (near > sums ? near : sums);
 }
 
+// (A bias of -inf masks its expert.)
+__device__ __forceinline__ float finite_magnitude(float b) { return fabsf(b) < INFINITY ? fabsf(b) : 0.0f; }
 // Bias by slot, loads at zero.
 template <int V, int WARPS, bool STATS>
 __device__ __forceinline__ void router_start(const RouterArgs& a, float* s_bias, int* s_loads) {
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
     float b_most = 0.0f;
     if (a.bias) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, fabsf(s_bias[sub * V + v]));
+        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, finite_magnitude(s_bias[sub * V + v]));
         b_most = lanes_max<L>(b_most);
     }
     const bool scored = a.bias || (a.groups > 1 && a.top2);   // keys are needed as numbers, not only their order
@@ -939,7 +943,7 @@ __global__ void __launch_bounds__(router_warps(V, 32) * 32, 1) router_warp_kerne
     float b_most = 0.0f;
     if (a.bias) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, fabsf(s_bias[lane * V + v]));
+        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, finite_magnitude(s_bias[lane * V + v]));
         b_most = warp_max(b_most);
     }
     float share[V], z_sum = 0.0f;

@@ -380,6 +380,48 @@ def test_offsets_out_of_order_are_reported():
         assert torch.equal(got, moe.moe_fp4_expert_gemm(moe.moe_fp4_quant(x, fmt, good), q, tiles, glob))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_launches_and_large_results(fmt):
+    """More items than a cluster's table holds, results past 2^31 elements: columns and the last rows as in small calls."""
+    g = gen(20)
+    n, N, K = 66000, 32768, 64
+    x = spread(g, n, K, torch.bfloat16)
+    q, tiles, glob, _ = make_weights(g, 1, N, K, fmt)
+    out = moe.moe_fp4_expert_gemm(moe.moe_fp4_quant(x, fmt), q, tiles, glob)
+    assert out.numel() > 2 ** 31
+    cut = q[:, :4096].contiguous(), tiles[:, :32].contiguous()
+    assert torch.equal(out[:, :4096], moe.moe_fp4_expert_gemm(moe.moe_fp4_quant(x, fmt), *cut, glob))
+    tail = moe.moe_fp4_expert_gemm(moe.moe_fp4_quant(x[-300:].clone(), fmt), q, tiles, glob)
+    assert torch.equal(out[-300:], tail)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_past_2_31_elements(fmt):
+    n, K = 70000, 32768
+    x = torch.empty(n, K, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    off = torch.tensor([0, 100, 69000, n], dtype=torch.int32, device="cuda")
+    rows = moe.moe_fp4_quant(x, fmt, off)
+    tail = moe.moe_fp4_quant(x[-300:].clone(), fmt)
+    assert torch.equal(rows.codes[-300:], tail.codes)
+    assert torch.equal(moe.moe_fp4_dequant(rows)[-300:], moe.moe_fp4_dequant(tail))
+
+
+def test_borders_of_16_bit_rows():
+    """Every largest magnitude of a bf16 row with every number below it, and many of fp16's: quotients that nvfp4's borders meet."""
+    for dtype, bits in ((torch.bfloat16, 7), (torch.float16, 10)):
+        for start in range(0, 2 ** bits, 1 if bits == 7 else 13):
+            top = 1 + start / 2 ** bits
+            below = (1 + torch.arange(2 ** bits, dtype=torch.float64) / 2 ** bits)[None] * 2.0 ** -torch.arange(0, 8)[:, None]
+            v = below.reshape(-1)
+            v = v[v <= top]
+            v = torch.cat([v, torch.zeros(-len(v) % 64)])[:32768]
+            x = torch.stack([v, v.flip(0)])
+            x = torch.cat([x, torch.zeros(2, 64)], 1)[:, :32768 - 64] if x.shape[1] > 32768 - 64 else torch.cat([x, torch.zeros(2, 64)], 1)
+            x[:, -1] = top
+            x = x.to(dtype).cuda()
+            same(moe.moe_fp4_dequant(moe.moe_fp4_quant(x, "nvfp4"), torch.float32), quantise64(x, "nvfp4"), f"{dtype} {top}")
+
+
 def test_half_step_of_a_product_of_ones():
     """Products of numbers that 4 bits hold exactly are exact."""
     x = torch.ones(40, 512, dtype=torch.bfloat16, device="cuda")

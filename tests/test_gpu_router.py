@@ -344,3 +344,57 @@ def test_agrees_with_the_layers_router():
         r = moe.moe_router(x, k, True, rp)
         assert torch.equal(ids, r.ids)
         assert ((w - r.weights).abs() <= w * 60 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [40, 6000])
+def test_bias_masks_experts(T, scoring):
+    """A bias of -inf takes its expert out of the choice and of its group's value, not out of the shares."""
+    g = gen(12)
+    for E, groups, kept in ((64, 1, 1), (64, 8, 3), (60, 6, 2)):
+        l = torch.randn(T, E, generator=g)
+        bias = torch.randint(-40, 41, (E,), generator=g) * 0.001
+        gone = torch.zeros(E, dtype=torch.bool)
+        gone[::3] = True
+        c = Case(T, E, 4, scoring, "given", groups, kept)
+        ref = reference(c, torch.where(gone, -math.inf, l), bias, None)
+        r = moe.moe_router(l.cuda(), 4, routing=routing(c, torch.where(gone, -math.inf, bias).cuda()), losses=True)
+        # (softmax keys shift with the masked experts' share of the sum: compare where the reference has it too)
+        if scoring == "sigmoid":
+            assert torch.equal(r.ids.cpu().long(), ref["ids"])
+        assert not gone[r.ids.cpu().long()].any()
+        ref = reference(dataclasses.replace(c, groups=1), l, torch.where(gone, -1e30, bias), None)
+        if groups == 1:
+            assert torch.equal(r.ids.cpu().long(), ref["ids"])
+
+
+def test_many_tokens():
+    """Logits past 2^31 elements: the last tokens come out as they do alone."""
+    T, E = 8_500_000, 256
+    x = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    tail = x[-500:].clone()
+    rp = moe.RoutingParams("sigmoid", n_group=8, topk_group=4)
+    r = moe.moe_router(x, 8, routing=rp, losses=True)
+    one = moe.moe_router(tail, 8, routing=rp)
+    assert torch.equal(r.ids[-500:], one.ids) and torch.equal(r.weights[-500:], one.weights)
+    assert int(r.tokens) == T and int(r.counts.long().sum()) == 8 * T
+    dw = torch.ones(T, 8, device="cuda")
+    dw[:, ::2] = 0.5
+    d = moe.moe_router_backward(x, r, dw, routing=rp)
+    assert torch.equal(d[-500:], moe.moe_router_backward(tail, one, dw[-500:].contiguous(), routing=rp))
+
+
+@pytest.mark.parametrize("E", [24, 56, 100, 128])
+def test_many_and_few_tokens_agree(E):
+    """Four tokens to a warp and one choose and weigh alike, and gather the same loads."""
+    for scoring, bias in (("softmax", False), ("sigmoid", True)):
+        g = gen(13)
+        x = torch.randn(9000, E, generator=g).bfloat16().cuda()
+        rp = moe.RoutingParams(scoring, bias=(torch.randint(-40, 41, (E,), generator=g) * 0.001).cuda() if bias else None)
+        valid = (torch.rand(9000, generator=g) > 0.1).cuda()
+        r = moe.moe_router(x, 6, routing=rp, valid=valid, losses=True)
+        parts = [moe.moe_router(x[i:i + 3000], 6, routing=rp, valid=valid[i:i + 3000], losses=True) for i in range(0, 9000, 3000)]
+        assert torch.equal(r.ids, torch.cat([p.ids for p in parts]))
+        assert torch.equal(r.counts, sum(p.counts for p in parts)) and int(r.tokens) == sum(int(p.tokens) for p in parts)
+        w = torch.cat([p.weights for p in parts])
+        assert ((r.weights - w).abs() <= 30 * 2.0 ** -24 * w).all()   # sums of the same terms in another order
