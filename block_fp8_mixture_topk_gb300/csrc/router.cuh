@@ -631,6 +631,14 @@ constexpr size_t router_smem(bool stats) {
 
 // (A bias of -inf masks its expert.)
 __device__ __forceinline__ float finite_magnitude(float b) { return fabsf(b) < INFINITY ? fabsf(b) : 0.0f; }
+// Whether a token (the lanes of `lanes` from base on) has a logit above -inf whose bias is, too.
+template <int V>
+__device__ __forceinline__ bool some_unmasked(const float (&l)[V], const float* bias, int base, uint32_t lanes) {
+    bool able = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) able |= l[v] > kNone && bias[v] > kNone;
+    return ((__ballot_sync(kAll, able) >> base) & lanes) != 0u;
+}
 // Bias by slot, loads at zero.
 template <int V, int WARPS, bool STATS>
 __device__ __forceinline__ void router_start(const RouterArgs& a, float* s_bias, int* s_loads) {
@@ -691,10 +699,15 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
     const T* logits = static_cast<const T*>(a.logits);
     router_start<V, WARPS, STATS>(a, s_bias, s_loads);
     float b_most = 0.0f;
+    bool masks = false;   // a bias of -inf
     if (a.bias) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, finite_magnitude(s_bias[sub * V + v]));
+        for (int v = 0; v < V; ++v) {
+            b_most = fmaxf(b_most, finite_magnitude(s_bias[sub * V + v]));
+            masks |= s_bias[sub * V + v] == kNone;
+        }
         b_most = lanes_max<L>(b_most);
+        masks = __any_sync(kAll, masks);
     }
     const bool scored = a.bias || (a.groups > 1 && a.top2);   // keys are needed as numbers, not only their order
     const int need = a.bias ? a.k + 1 : a.k;
@@ -723,8 +736,9 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
 #pragma unroll
         for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
         m = lanes_max<L>(m);
-        const bool alive = m > kNone;   // some expert can be chosen
+        bool alive = m > kNone;   // some expert can be chosen
         m = alive ? m : 0.0f;
+        if (masks) alive = some_unmasked<V>(l, s_bias + sub * V, base, (1u << L) - 1u);
         float per = 1.0f;
         if (scored || STATS || !SIGMOID) {
             float z = 0.0f;
@@ -737,7 +751,7 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
             per = __fdividef(1.0f, fmaxf(z, 1e-37f));
             if constexpr (STATS) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], per, share[v]);
+                for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], alive ? per : 0.0f, share[v]);
                 const float lse = SIGMOID || !alive ? 0.0f : m + logf(z);
                 if (sub == 0) {
                     z_sum = fmaf(lse, lse, z_sum);
@@ -941,10 +955,15 @@ __global__ void __launch_bounds__(router_warps(V, 32) * 32, 1) router_warp_kerne
     const T* logits = static_cast<const T*>(a.logits);
     router_start<V, WARPS, STATS>(a, s_bias, s_loads);
     float b_most = 0.0f;
+    bool masks = false;   // a bias of -inf
     if (a.bias) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) b_most = fmaxf(b_most, finite_magnitude(s_bias[lane * V + v]));
+        for (int v = 0; v < V; ++v) {
+            b_most = fmaxf(b_most, finite_magnitude(s_bias[lane * V + v]));
+            masks |= s_bias[lane * V + v] == kNone;
+        }
         b_most = warp_max(b_most);
+        masks = __any_sync(kAll, masks);
     }
     float share[V], z_sum = 0.0f;
     int live = 0;
@@ -963,7 +982,9 @@ __global__ void __launch_bounds__(router_warps(V, 32) * 32, 1) router_warp_kerne
 #pragma unroll
         for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
         m = warp_max(m);
-        if (m > kNone) {   // some expert can be chosen
+        bool alive = m > kNone;   // some expert can be chosen
+        if (masks) alive = some_unmasked<V>(l, s_bias + lane * V, 0, kAll);
+        if (alive) {
             float lse = 0.0f;
             route_warp<T, V, SIGMOID, STATS>(a, row, t, seat, l, m, b_most, s_bias, STATS ? s_loads : nullptr, near, share, &lse);
             z_sum = fmaf(lse, lse, z_sum);

@@ -626,8 +626,9 @@ int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* a, int64_t l
  *   choice   the topk largest keys (ties: lower expert), as the real numbers are ordered; a logit of -infinity is never
  *            chosen, and NaN and +infinity count as that (MOE_STATUS_BAD_LOGIT); slots without an expert hold id -1, weight 0
  *   weights  routed_scaling * s, divided by the sum of the chosen s with renormalize
- * logits [T, E] with row stride ld; bias fp32 [E] (finite, or -infinity: the expert is never chosen) or NULL; valid: bytes [T], 0 = a padded token (all ids -1), or NULL;
- * ids int32 [T, topk], weights fp32 [T, topk], descending keys (moe_dispatch drops the -1).
+ * logits [T, E] with row stride ld; bias fp32 [E] (finite, or -infinity: the expert is never chosen) or NULL; valid: bytes [T],
+ * 0 = a padded token (all ids -1), or NULL; ids int32 [T, topk], weights fp32 [T, topk], descending keys (moe_dispatch drops
+ * the -1).
  * counts int32 [E], tokens int32 [1], losses fp32 [2], all three or none (NULL): the tokens of each expert, n = the tokens
  * that chose an expert, and
  *   losses[0] = sum_e (E * counts[e] / (topk * n)) * mean_t(P[t, e]),  P = s / sum_e(s)   (balance)
@@ -692,8 +693,9 @@ int moe_fp4_quant(const void* x, int64_t ldx, int dtype, int fmt, const int32_t*
 /* The numbers that such rows stand for, in fp32 and rounded to out's type: out [num_rows, K], 16-byte aligned. */
 int moe_fp4_dequant(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt,
                     const int32_t* expert_offsets, int E, int64_t num_rows, int K, int dtype, void* out, void* stream);
-/* Load time: weights w [E, N, K] (bf16, fp16 or fp32, dense, 16-byte aligned; K at most 32768) in MXFP4, codes [E, N, K/2] and scale bytes
- * [E, N, K/32]; and scale bytes [E, N, K/32 or K/16] (also moe_nvfp4_quant_weight's or a checkpoint's) into tiles. */
+/* Load time: weights w [E, N, K] (bf16, fp16 or fp32, dense, 16-byte aligned; K at most 32768) in MXFP4, codes [E, N, K/2]
+ * and scale bytes [E, N, K/32]; and scale bytes [E, N, K/32 or K/16] (also moe_nvfp4_quant_weight's or a checkpoint's) into
+ * tiles. */
 int moe_mxfp4_quant_weight(const void* w, int dtype, int E, int N, int K, uint8_t* codes, uint8_t* scales, void* stream);
 int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate_up, uint8_t* out, void* stream);
 /* The experts' products of such rows and weights on the tensor cores, fp32 accumulation (epilogues, offsets and rows of no

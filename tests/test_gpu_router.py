@@ -368,6 +368,33 @@ def test_bias_masks_experts(T, scoring):
             assert torch.equal(r.ids.cpu().long(), ref["ids"])
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E", [(300, 64), (6000, 64), (6000, 200)])
+def test_tokens_of_masked_experts_only(T, E, scoring):
+    """A token whose logits above -inf are all of masked experts chooses none: it is not counted, has no share in the losses and
+    no gradient."""
+    g = gen(14)
+    l = torch.randn(T, E, generator=g)
+    bias = torch.zeros(E)
+    bias[E // 2:] = -math.inf
+    none = torch.rand(T, generator=g) < 0.2
+    l[none, :E // 2] = -math.inf
+    rp = moe.RoutingParams(scoring, bias=bias.cuda())
+    r = moe.moe_router(l.cuda(), 4, routing=rp, losses=True)
+    rest = moe.moe_router(l[~none].cuda(), 4, routing=rp, losses=True)
+    assert (r.ids.cpu()[none] == -1).all() and (r.weights.cpu()[none] == 0).all()
+    assert torch.equal(r.ids.cpu()[~none], rest.ids.cpu()) and torch.equal(r.counts, rest.counts)
+    assert int(r.tokens) == int(rest.tokens) == int((~none).sum())
+    # sums of at most T positive terms in another order
+    tol = 2 * T * 2.0 ** -24
+    assert abs(float(r.balance_loss) - float(rest.balance_loss)) <= tol * float(rest.balance_loss)
+    if scoring == "softmax":
+        assert abs(float(r.z_loss) - float(rest.z_loss)) <= tol * float(rest.z_loss)
+    dl = moe.moe_router_backward(l.cuda(), r, torch.ones_like(r.weights), routing=rp, balance_coef=0.1,
+                                 z_coef=0.1 if scoring == "softmax" else 0.0)
+    assert (dl.cpu()[none] == 0).all() and torch.isfinite(dl).all()
+
+
 def test_many_tokens():
     """Logits past 2^31 elements: the last tokens come out as they do alone."""
     T, E = 8_500_000, 256
