@@ -1125,7 +1125,6 @@ class Fp4Rows(typing.NamedTuple):
     row_scale: torch.Tensor | None        # nvfp4: fp32 [rows]
     format: str                           # "mxfp4" or "nvfp4"
     expert_offsets: torch.Tensor | None   # int32 [E+1] of rows sorted by expert; None: one weight for all rows
-    made: tuple = ()                      # of a result of these functions: its sizes and tensors (checked once)
 
 
 def _fp4_offsets(offsets):
@@ -1172,21 +1171,19 @@ def moe_fp4_quant(x, format="mxfp4", expert_offsets=None) -> Fp4Rows:
                              codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt else None, stream)
     if rc:
         _check("moe_fp4_quant", rc)
-    return Fp4Rows(codes, scales, row_scale, format, expert_offsets,
-                   (fmt, E, n, K, codes, scales, row_scale, expert_offsets, format))
+    return Fp4Rows(codes, scales, row_scale, format, expert_offsets)
 
 
 def _fp4_rows(rows):
     """(format code, number of experts, rows, K) of an Fp4Rows whose parts fit together."""
-    codes, scales, row_scale, format, offsets, made = rows
-    if made and made[4] is codes and made[5] is scales and made[6] is row_scale and made[7] is offsets and made[8] is format:
-        return made[:4]
+    codes, scales, row_scale, format, offsets = rows
     fmt = _fp4_format(format)
     E = _fp4_offsets(offsets)
     _cuda(codes, torch.uint8, "rows.codes")
     if codes.dim() != 2:
         raise ValueError(f"rows.codes must be a matrix, got {list(codes.shape)}")
-    n, K = codes.shape[0], 2 * codes.shape[1]
+    n, K = codes.shape
+    K *= 2
     if n > _INT_MAX or K > _INT_MAX:
         raise _too_large("rows.codes")
     _dense(scales, "rows.scales", torch.uint8, (_fp4_row_scale_bytes(fmt, n, E, K),))
@@ -1204,7 +1201,7 @@ def moe_fp4_dequant(rows: Fp4Rows, dtype=torch.bfloat16):
     fmt, E, n, K = _fp4_rows(rows)
     if dtype not in DTYPE:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    codes, scales, row_scale, _, offsets, _ = rows
+    codes, scales, row_scale, _, offsets = rows
     stream = _stream("codes scales row_scale expert_offsets", codes, scales, row_scale, offsets)
     out = _matrix(n, K, dtype)
     rc = lib().moe_fp4_dequant(codes.data_ptr(), scales.data_ptr(), row_scale.data_ptr() if fmt and n else None, fmt,
@@ -1268,7 +1265,7 @@ def _fp4_weights(fmt, E, K, w, w_scales, w_global):
 
 def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, epilogue):
     fmt, E, n, K = _fp4_rows(rows)
-    codes, scales, row_scale, format, offsets, _ = rows
+    codes, scales, row_scale, format, offsets = rows
     experts = E or 1
     N = _fp4_weights(fmt, experts, K, w, w_scales, w_global)
     code = DTYPE.get(dtype)
@@ -1290,7 +1287,7 @@ def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, epilogue):
         _check("moe_fp4_expert_gemm", rc)
     if out_scales is None:
         return out
-    return Fp4Rows(out, out_scales, None, format, offsets, (fmt, E, n, N // 2, out, out_scales, None, offsets, format))
+    return Fp4Rows(out, out_scales, None, format, offsets)
 
 
 def moe_fp4_expert_gemm(rows: Fp4Rows, w, w_scales, w_global=None, dtype=torch.bfloat16):

@@ -431,3 +431,18 @@ def test_half_step_of_a_product_of_ones():
         check(got, (moe.moe_fp4_dequant(moe.moe_fp4_quant(x, fmt), torch.float32).double() @ w[0].T), w[0].abs().sum(1)[None].expand(40, 40),
               steps(512), "ones")
     assert half_step(torch.float32) == 2.0 ** -24
+
+
+def test_rows_are_checked_at_each_call():
+    """Rows of which a tensor was given other memory are refused, those that these functions made as well."""
+    rows = moe.moe_fp4_quant(torch.ones(300, 512, dtype=torch.bfloat16, device="cuda"), "nvfp4")
+    moe.moe_fp4_dequant(rows)
+    for name, other in (("codes", rows.codes[:200].clone()), ("scales", rows.scales[:512].clone()),
+                        ("row_scale", rows.row_scale[:10].clone())):
+        part = getattr(rows, name)
+        kept = part.data
+        part.data = other
+        with pytest.raises(ValueError):
+            moe.moe_fp4_dequant(rows)
+        part.data = kept
+    moe.moe_fp4_dequant(rows)
