@@ -81,13 +81,13 @@ __device__ __forceinline__ float border_side(float m, float rs) {
     return over > 0.0f ? 1.0f - 0x1p-20f : over < 0.0f ? 1.0f + 0x1p-20f : 0.0f;
 }
 
-// A group's scale byte and its part's codes, nvfp4 (rs > 0; side: border_side).
+// A group's scale byte and its part's codes, nvfp4 (rs > 0; side: border_side; by: 1 / (6 rs)).
 template <class T>
-__device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top, float rs, float side, uint2* codes) {
+__device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top, float rs, float side, float by, uint2* codes) {
     const float g = __uint_as_float(top);
     *codes = make_uint2(0, 0);
     if (sizeof(T) == 2 && side != 0.0f && rs >= kLeastRow) {
-        const uint32_t s = e4m3x2(__fdividef(g, 6.0f * rs) * side, 0.0f) & 0xffu;
+        const uint32_t s = e4m3x2(g * (by * side), 0.0f) & 0xffu;
         if (s > 0) *codes = e2m1_words(x, __fdividef(1.0f, e4m3_number(s) * rs) * side);
         return s;
     }
@@ -103,7 +103,7 @@ __device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top,
         }
         return s;
     }
-    const float t = __fdividef(g, 6.0f * rs);
+    const float t = g * by;
     const uint32_t two = e4m3x2(t * (1.0f - kSlack), t * (1.0f + kSlack));
     uint32_t s = two & 0xffu;
     if (s != two >> 8) s += past_border(g, 3.0f * (e4m3_number(s) + e4m3_number(s + 1)), rs, s) ? 1u : 0u;
@@ -135,12 +135,11 @@ __global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_k
     grid_dependency_wait();
     constexpr int G = fp4_group(FMT), LANES = G / 16, W = fp4_words(FMT);   // lanes of a group
     __shared__ uint32_t s_top[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int own = warp / a.warps, tpr = a.warps * 32;     // the block's row
-    const int at = threadIdx.x - own * tpr;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / a.warps) + own;
-    const bool live = r < a.rows;
-    const int KB = fp4_blocks(a.K), vecs = a.K / 16;
+    const int at = threadIdx.x, own = threadIdx.y, tpr = blockDim.x;   // the thread of a row, the block's row
+    const int lane = at & 31;
+    const uint32_t row_of = blockIdx.x * blockDim.y + own;
+    const bool live = row_of < static_cast<uint32_t>(a.rows);
+    const int r = static_cast<int>(row_of), KB = fp4_blocks(a.K), vecs = a.K / 16;
     const T* row = static_cast<const T*>(a.x) + r * a.ld;
     Vec16<T> x[kQuantVecs];
 #pragma unroll
@@ -157,21 +156,22 @@ __global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_k
         top[i] = x[i].top();
         if (LANES == 2) top[i] = max(top[i], __shfl_xor_sync(kAll, top[i], 1));
     }
-    float rs = 1.0f, side = 0.0f;
+    float rs = 1.0f, side = 0.0f, by = 0.0f;
     if constexpr (FMT == MOE_FP4_NVFP4) {
         uint32_t m = __reduce_max_sync(kAll, max(top[0], top[1]));
         if (a.warps > 1) {
-            if (lane == 0) s_top[warp] = m;
+            if (lane == 0) s_top[own * a.warps + (at >> 5)] = m;
             __syncthreads();
             m = __reduce_max_sync(kAll, lane < a.warps ? s_top[own * a.warps + lane] : 0u);
         }
         rs = m < 0x7f800000u ? __fdiv_rn(__uint_as_float(m), 2688.0f) : __int_as_float(0x7fffffff);
         side = border_side<T>(__uint_as_float(m), rs);
+        by = __fdividef(1.0f, 6.0f * rs);
         if (live && at == 0) a.row_scale[r] = rs;
     }
     if (!live) return;   // (whole warps)
     uint8_t* tile = fp4_scale_row(a.tiles, place.tile, place.in, KB, W);
-    uint2* codes = reinterpret_cast<uint2*>(a.codes + r * (a.K / 2));
+    uint2* codes = reinterpret_cast<uint2*>(a.codes + static_cast<int64_t>(r) * (a.K / 2));
 #pragma unroll
     for (int i = 0; i < kQuantVecs; ++i) {
         const int v = at + i * tpr;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_k
         if constexpr (FMT == MOE_FP4_MXFP4) {
             s = mxfp4_group(x[i], top[i], &w);
         } else if (rs > 0.0f) {   // not zero and not NaN
-            s = nvfp4_group(x[i], top[i], rs, side, &w);
+            s = nvfp4_group(x[i], top[i], rs, side, by, &w);
         }
         if (v < vecs) codes[v] = w;
         else s = 0;   // columns past K: a scale that is a number
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_k
             if (lane % (4 * LANES) == 0 && kb < KB)
                 *reinterpret_cast<uint32_t*>(tile + static_cast<int64_t>(kb) * (2 * W * 512) + (c >> 2) % W * 512) = word;
         } else if (lane % LANES == 0 && v < vecs) {
-            a.plain[r * (a.K / G) + c] = static_cast<uint8_t>(s);
+            a.plain[static_cast<int64_t>(r) * (a.K / G) + c] = static_cast<uint8_t>(s);
         }
     }
 }
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(1024) fp4_dequant_kernel(const DequantArgs a, 
     const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
     if (r >= a.rows) return;   // (whole warps)
     const int KB = fp4_blocks(a.K), vecs = a.K / 8;
-    const Fp4Place place = fp4_place(a.offsets, a.E, r);
+    const Fp4Place place = fp4_place(a.offsets, a.E, static_cast<int>(r));
     const uint8_t* tile = a.tiles + (place.tile * KB * 2 + (place.in >> 7)) * (W * 512);
     const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.codes + r * (a.K / 2));
     const float rs = FMT == MOE_FP4_NVFP4 ? a.row_scale[r] : 1.0f;
@@ -318,7 +318,7 @@ cudaError_t quant_type(QuantArgs a, cudaStream_t stream) {
     const int all = fp4_blocks(a.K) * 16;                                       // vectors of a row
     a.warps = (all + 32 * kQuantVecs - 1) / (32 * kQuantVecs);
     const int per = a.warps < 8 ? 8 / a.warps : 1;                              // rows of a block of up to 256 threads
-    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(32 * a.warps * per);
+    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(32 * a.warps, per);
     if (a.warps <= 8) return launch_pdl(fp4_quant_kernel<T, FMT, 256>, grid, block, 0, stream, a);
     return a.warps <= 16 ? launch_pdl(fp4_quant_kernel<T, FMT, 512>, grid, block, 0, stream, a)
                          : launch_pdl(fp4_quant_kernel<T, FMT, 1024>, grid, block, 0, stream, a);

@@ -44,8 +44,8 @@ struct Fp4Place {
     int64_t tile;
     int in;
 };
-__device__ __forceinline__ Fp4Place fp4_place(const int32_t* offsets, int E, int64_t r) {
-    int64_t e = 0, o = 0;
+__device__ __forceinline__ Fp4Place fp4_place(const int32_t* offsets, int E, int r) {
+    int e = 0, o = 0;
     if (offsets) {
         const int lane = threadIdx.x & 31;
         int most = 0;
@@ -63,8 +63,8 @@ __device__ __forceinline__ Fp4Place fp4_place(const int32_t* offsets, int E, int
         }
         o = most;
     }
-    const int64_t m = (r - o) / kFp4Rows;
-    return {o / kFp4Rows + e + m, static_cast<int>(r - o - m * kFp4Rows)};
+    const uint32_t past = static_cast<uint32_t>(r - o), m = past / kFp4Rows;
+    return {static_cast<int64_t>(static_cast<uint32_t>(o) / kFp4Rows + e + m), static_cast<int>(past - m * kFp4Rows)};
 }
 
 // e4m3 number of a byte without its sign.
@@ -75,6 +75,18 @@ __device__ __forceinline__ float e4m3_number(uint32_t code) {
 }
 __device__ __forceinline__ float ue8m0_number(uint32_t byte) {   // 255 is NaN
     return byte == 255 ? __int_as_float(0x7fffffff) : byte ? __uint_as_float(byte << 23) : __uint_as_float(1u << 22);
+}
+
+// The larger magnitudes of two pairs of elements, NaN above all.
+template <class T>
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                             __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    const __half2 m = __hmax2_nan(__habs2(*reinterpret_cast<const __half2*>(&a)), __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // 16 elements.
@@ -126,10 +138,10 @@ struct Vec16 {
             for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
             return m;
         } else {
-            uint32_t m = w[0] & 0x7fff7fffu;
+            uint32_t m = abs_max2<T>(w[0], w[1]);
 #pragma unroll
-            for (int i = 1; i < kWords; ++i) m = __vmaxs2(m, w[i] & 0x7fff7fffu);
-            m = max(m & 0xffffu, m >> 16);
+            for (int i = 2; i < kWords; ++i) m = abs_max2<T>(m, w[i]);
+            m = max(m & 0x7fffu, m >> 16 & 0x7fffu);
             if constexpr (std::is_same<T, __nv_bfloat16>::value) return m << 16;
             return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
         }
