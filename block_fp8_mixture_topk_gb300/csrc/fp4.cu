@@ -8,16 +8,21 @@
 //          are often nearly a border, need neither (border_side)
 // An infinity or NaN makes its group (mxfp4: scale NaN) or row (nvfp4: row scale NaN) NaN.
 //
-// Memory is the bound: a thread loads its two vectors of 16 elements whole (32 bytes at a time) before it uses the first,
+// Memory is the bound: a thread loads its vectors of 16 elements whole (32 bytes at a time) before it uses the first,
 // so a group is one lane's or two lanes'; they stay in registers for the row's maximum (32 to 1024 threads to a row).
 // The codes go out as eight bytes a vector, the scales as words of four groups put together across lanes.
+//
+// Measured (GB300; rows read, codes and scales written): mxfp4 131072 x 2048 bf16 98 us, 6.9 TB/s; 4096 x 32768 53 us, 6.4 TB/s;
+// 5003 x 2880 fp32 8.7 us.  nvfp4 116 us, 5.9 TB/s; 65 us, 5.3 TB/s; 10.2 us: its row's maximum is a barrier, and its quotients make
+// 200 instructions of 16 elements, three of four issue slots.  So a row takes small blocks (64 threads in place of 256: 121 ->
+// 116 us), and a long row four vectors a thread in place of two (32768 columns: 84 -> 65 us, mxfp4 68 -> 53; 7168: 31 and 32).
+// Values back: 131072 x 2048 100 us, 6.8 TB/s.
 #include "fp4.cuh"
 
 namespace mfp8 {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kQuantVecs = 2;   // vectors of 16 elements a thread
 
 // Whether a >= 0 is rounded up from code c past the border m r to the next: m has few bits, the product's two parts are
 // exact (r not below kLeastRow), ties go to the even code.
@@ -124,14 +129,14 @@ __device__ __forceinline__ uint32_t nvfp4_group(const Vec16<T>& x, uint32_t top,
     return s;
 }
 
-// Blocks to an SM: with rows of 16 bits 1536 threads (40 registers), 98 KB of rows under way.
-template <class T>
+// Blocks to an SM: with two vectors of 16-bit elements a thread 1536 threads (40 registers), 98 KB of rows under way, else 1024.
+template <class T, int VECS>
 constexpr int quant_blocks(int threads) {
-    return (sizeof(T) == 2 && threads < 1024 ? 1536 : 1024) / threads;
+    return (sizeof(T) == 2 && VECS == 2 ? 1536 : 1024) / threads;
 }
 
-template <class T, int FMT, int THREADS>
-__global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_kernel(const QuantArgs a) {
+template <class T, int FMT, int THREADS, int VECS>
+__global__ void __launch_bounds__(THREADS, quant_blocks<T, VECS>(THREADS)) fp4_quant_kernel(const QuantArgs a) {
     grid_dependency_wait();
     constexpr int G = fp4_group(FMT), LANES = G / 16, W = fp4_words(FMT);   // lanes of a group
     __shared__ uint32_t s_top[32];
@@ -141,24 +146,27 @@ __global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_k
     const bool live = row_of < static_cast<uint32_t>(a.rows);
     const int r = static_cast<int>(row_of), KB = fp4_blocks(a.K), vecs = a.K / 16;
     const T* row = static_cast<const T*>(a.x) + r * a.ld;
-    Vec16<T> x[kQuantVecs];
+    Vec16<T> x[VECS];
 #pragma unroll
-    for (int i = 0; i < kQuantVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
         const int v = at + i * tpr;
         if (live && v < vecs) x[i].load(row + v * 16, a.align);
         else x[i].zero();
     }
     Fp4Place place = {0, 0};
     if (a.tiles && live) place = fp4_place(a.offsets, a.E, r);
-    uint32_t top[kQuantVecs];
+    uint32_t top[VECS];
 #pragma unroll
-    for (int i = 0; i < kQuantVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
         top[i] = x[i].top();
         if (LANES == 2) top[i] = max(top[i], __shfl_xor_sync(kAll, top[i], 1));
     }
+    uint32_t most = top[0];
+#pragma unroll
+    for (int i = 1; i < VECS; ++i) most = max(most, top[i]);
     float rs = 1.0f, side = 0.0f, by = 0.0f;
     if constexpr (FMT == MOE_FP4_NVFP4) {
-        uint32_t m = __reduce_max_sync(kAll, max(top[0], top[1]));
+        uint32_t m = __reduce_max_sync(kAll, most);
         if (a.warps > 1) {
             if (lane == 0) s_top[own * a.warps + (at >> 5)] = m;
             __syncthreads();
@@ -173,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, quant_blocks<T>(THREADS)) fp4_quant_k
     uint8_t* tile = fp4_scale_row(a.tiles, place.tile, place.in, KB, W);
     uint2* codes = reinterpret_cast<uint2*>(a.codes + static_cast<int64_t>(r) * (a.K / 2));
 #pragma unroll
-    for (int i = 0; i < kQuantVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
         const int v = at + i * tpr;
         if ((v & ~31) >= KB * 16) break;   // (whole warps)
         uint32_t s = 0;
@@ -214,12 +222,13 @@ struct DequantArgs {
 
 // Values of the codes: code times group scale is exact in fp32, the row's scale and the result's type round.
 template <class T, int FMT>
-__global__ void __launch_bounds__(1024) fp4_dequant_kernel(const DequantArgs a, int tpr) {
+__global__ void __launch_bounds__(1024) fp4_dequant_kernel(const DequantArgs a) {
     grid_dependency_wait();
     constexpr int LANES = fp4_group(FMT) / 8, W = fp4_words(FMT);
-    const int at = threadIdx.x % tpr;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
-    if (r >= a.rows) return;   // (whole warps)
+    const int at = threadIdx.x, tpr = blockDim.x;
+    const uint32_t row_of = blockIdx.x * blockDim.y + threadIdx.y;
+    if (row_of >= static_cast<uint32_t>(a.rows)) return;   // (whole warps)
+    const int64_t r = row_of;
     const int KB = fp4_blocks(a.K), vecs = a.K / 8;
     const Fp4Place place = fp4_place(a.offsets, a.E, static_cast<int>(r));
     const uint8_t* tile = a.tiles + (place.tile * KB * 2 + (place.in >> 7)) * (W * 512);
@@ -298,30 +307,19 @@ __global__ void __launch_bounds__(256) fp4_pack_kernel(const uint8_t* s, int64_t
     }
 }
 
-// Threads of a row: as few warps as hold it in kVecs vectors each, and rows to a block of 256 threads or more.
-struct RowPlan {
-    int tpr, threads;
-    unsigned blocks;
-};
-RowPlan row_plan(int64_t rows, int K) {
-    const int vecs = fp4_blocks(K) * 32;
-    int tpr = 32;
-    while (tpr * kVecs < vecs) tpr <<= 1;
-    const int threads = tpr > 256 ? tpr : 256, per = threads / tpr;
-    return {tpr, threads, static_cast<unsigned>((rows + per - 1) / per)};
-}
-
 template <class T, int FMT>
 cudaError_t quant_type(QuantArgs a, cudaStream_t stream) {
     const uintptr_t bits = address(a.x) | (a.rows > 1 ? static_cast<uintptr_t>(a.ld) * sizeof(T) : 0);
     a.align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
     const int all = fp4_blocks(a.K) * 16;                                       // vectors of a row
-    a.warps = (all + 32 * kQuantVecs - 1) / (32 * kQuantVecs);
-    const int per = a.warps < 8 ? 8 / a.warps : 1;                              // rows of a block of up to 256 threads
-    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(32 * a.warps, per);
-    if (a.warps <= 8) return launch_pdl(fp4_quant_kernel<T, FMT, 256>, grid, block, 0, stream, a);
-    return a.warps <= 16 ? launch_pdl(fp4_quant_kernel<T, FMT, 512>, grid, block, 0, stream, a)
-                         : launch_pdl(fp4_quant_kernel<T, FMT, 1024>, grid, block, 0, stream, a);
+    const auto launch = [&](auto kernel, int vecs) {
+        a.warps = (all + 32 * vecs - 1) / (32 * vecs);
+        const int most = FMT == MOE_FP4_NVFP4 ? 2 : 8, per = a.warps < most ? most / a.warps : 1;   // rows of a block
+        return launch_pdl(kernel, dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(32 * a.warps, per), 0, stream, a);
+    };
+    if (all <= 8 * 64) return launch(fp4_quant_kernel<T, FMT, 256, 2>, 2);
+    if constexpr (sizeof(T) == 2) return launch(fp4_quant_kernel<T, FMT, 512, 4>, 4);
+    else return all <= 16 * 64 ? launch(fp4_quant_kernel<T, FMT, 512, 2>, 2) : launch(fp4_quant_kernel<T, FMT, 1024, 2>, 2);
 }
 template <int FMT>
 cudaError_t quant_format(int dtype, const QuantArgs& a, cudaStream_t stream) {
@@ -331,11 +329,12 @@ cudaError_t quant_format(int dtype, const QuantArgs& a, cudaStream_t stream) {
 }
 template <int FMT>
 cudaError_t dequant_format(int dtype, const DequantArgs& a, cudaStream_t stream) {
-    const RowPlan p = row_plan(a.rows, a.K);
-    const dim3 grid(p.blocks), block(p.threads);
-    return dtype == MOE_DTYPE_BF16   ? launch_pdl(fp4_dequant_kernel<__nv_bfloat16, FMT>, grid, block, 0, stream, a, p.tpr)
-           : dtype == MOE_DTYPE_FP16 ? launch_pdl(fp4_dequant_kernel<__half, FMT>, grid, block, 0, stream, a, p.tpr)
-                                     : launch_pdl(fp4_dequant_kernel<float, FMT>, grid, block, 0, stream, a, p.tpr);
+    // as few warps as hold a row, kVecs vectors a thread; blocks of up to 256 threads or one row
+    const int warps = (a.K / 8 + 32 * kVecs - 1) / (32 * kVecs), per = warps < 8 ? 8 / warps : 1;
+    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(32 * warps, per);
+    return dtype == MOE_DTYPE_BF16   ? launch_pdl(fp4_dequant_kernel<__nv_bfloat16, FMT>, grid, block, 0, stream, a)
+           : dtype == MOE_DTYPE_FP16 ? launch_pdl(fp4_dequant_kernel<__half, FMT>, grid, block, 0, stream, a)
+                                     : launch_pdl(fp4_dequant_kernel<float, FMT>, grid, block, 0, stream, a);
 }
 
 bool known_format(int fmt) { return fmt == MOE_FP4_MXFP4 || fmt == MOE_FP4_NVFP4; }
