@@ -25,6 +25,13 @@
 // token: everything that a warp keeps across tokens but its score sums lies in shared memory, and 24 or 32 warps of 80 or 64
 // registers fit.  Score sums are added across warps, then blocks (a last small launch) in a fixed order; the loads are
 // integers.
+//
+// Measured (GB300; choice alone, with loads and losses, gradient, gradient with the losses'), us:
+//   58368 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 experts    59, 66, 18, 33   (the bytes: 9, 9, 9, 18)
+//   58368 x 128 bf16, softmax, 8 experts                         19, 26, 8, 14    (2.8, 2.8, 2.8, 4.5)
+//   152 x 256 as the first                                       4, 9, 2.4, 3.7   (launches)
+// The choice issues an instruction in 54% of the cycles with 24 warps to an SM and waits for shuffles and shared memory in
+// between; DRAM is below 20%.
 #pragma once
 
 #include <type_traits>

@@ -446,3 +446,13 @@ def test_rows_are_checked_at_each_call():
             moe.moe_fp4_dequant(rows)
         part.data = kept
     moe.moe_fp4_dequant(rows)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids_of)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [2080, 8192, 8224, 9216, 16416, 20000, 32736])
+def test_long_rows(K, fmt, dtype):
+    """Rows of every share of a block's threads."""
+    x = spread(gen(22), 5, K, dtype)
+    rows = moe.moe_fp4_quant(x.cuda(), fmt)
+    assert torch.equal(moe.moe_fp4_dequant(rows, torch.float32).cpu(), quantise64(x, fmt).float())
