@@ -48,20 +48,21 @@ __device__ __forceinline__ Fp4Place fp4_place(const int32_t* offsets, int E, int
     int e = 0, o = 0;
     if (offsets) {
         const int lane = threadIdx.x & 31;
-        int most = 0;
+        int most = 0;   // of the lane's offsets up to r
         e = E;
         for (int i0 = 1; i0 <= E; i0 += 32) {
             const int i = i0 + lane;
             const int32_t v = i <= E ? __ldg(offsets + i) : 0;
             const uint32_t past = __ballot_sync(0xffffffffu, v > r);
-            const int first = past ? __ffs(static_cast<int>(past)) - 1 : 32;
-            most = max(most, __reduce_max_sync(0xffffffffu, lane < first ? max(v, 0) : 0));
             if (past) {
+                const int first = __ffs(static_cast<int>(past)) - 1;
+                if (lane < first) most = max(most, v);
                 e = i0 + first - 1;
                 break;
             }
+            most = max(most, v);
         }
-        o = most;
+        o = __reduce_max_sync(0xffffffffu, most);
     }
     const uint32_t past = static_cast<uint32_t>(r - o), m = past / kFp4Rows;
     return {static_cast<int64_t>(static_cast<uint32_t>(o) / kFp4Rows + e + m), static_cast<int>(past - m * kFp4Rows)};
