@@ -14,7 +14,7 @@
 //
 // Measured (GB300; rows read, codes and scales written): mxfp4 131072 x 2048 bf16 98 us, 6.9 TB/s; 4096 x 32768 53 us, 6.4 TB/s;
 // 5003 x 2880 fp32 8.7 us.  nvfp4 116 us, 5.9 TB/s; 65 us, 5.3 TB/s; 10.2 us: its row's maximum is a barrier, and its quotients make
-// 200 instructions of 16 elements, three of four issue slots.  So a row takes small blocks (64 threads in place of 256: 121 ->
+// 200 instructions of 16 elements, 2.7 of 4 issue slots.  So a row takes small blocks (64 threads in place of 256: 121 ->
 // 116 us), and a long row four vectors a thread in place of two (32768 columns: 84 -> 65 us, mxfp4 68 -> 53; 7168: 31 and 32).
 // Values back: 131072 x 2048 100 us, 6.8 TB/s.
 #include "fp4.cuh"
