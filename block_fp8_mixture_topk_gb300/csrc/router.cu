@@ -11,6 +11,7 @@ constexpr int kFinalCtas = 8, kFinalThreads = 1024;
 __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThreads)
     router_loads_kernel(const float* share, const int32_t* count, const float* z, const int32_t* live, int blocks, int E, int k,
                         int32_t* counts, int32_t* tokens, float* losses) {
+    cluster_arrive();   // this CTA runs
     grid_dependency_wait();
     __shared__ float s_share[kFinalThreads], s_part[kFinalCtas];
     __shared__ int s_count[kFinalThreads];
@@ -55,6 +56,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
     __syncthreads();
     s_share[threadIdx.x] = part;
     __syncthreads();
+    cluster_wait();     // every CTA runs: the first one's shared memory can be written
     if (threadIdx.x < 32) {   // chunk <= 128: four to a lane
         float v = 0.0f;
         for (int i = lane; i < chunk; i += 32) v += s_share[i];
@@ -65,6 +67,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
             asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
         }
     }
+    __syncwarp();
     cluster_barrier();
     if (rank == 0 && threadIdx.x == 0) {
         int tokens_all = 0;
