@@ -81,22 +81,30 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
     }
 }
 
-// bias[e] += rate * sign(mean(counts) - counts[e])
+// bias[e] += rate * sign(mean(counts) - counts[e]), over the experts that a bias of -inf does not mask: counted among them, the
+// masked ones' empty loads would put the mean below what the others share evenly, and each step would push all of those down.
 __global__ void __launch_bounds__(1024) router_bias_kernel(float* bias, const int32_t* counts, int E, float rate) {
     grid_dependency_wait();
-    __shared__ unsigned long long s_sum[32];
+    __shared__ long long s_sum[32];
+    __shared__ int s_able[32];
     const int e = threadIdx.x, lane = e & 31;
-    const int32_t c = e < E ? counts[e] : 0;
+    const float b = e < E ? bias[e] : -INFINITY;
+    const bool able = b > -INFINITY;
+    const int32_t c = able ? counts[e] : 0;
     long long sum = c;
+    int n = able ? 1 : 0;
+    const auto add = [&] {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_sum[e >> 5] = static_cast<unsigned long long>(sum);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        n = __reduce_add_sync(0xffffffffu, n);
+    };
+    add();
+    if (lane == 0) s_sum[e >> 5] = sum, s_able[e >> 5] = n;
     __syncthreads();
-    sum = static_cast<long long>(s_sum[lane]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const long long mine = static_cast<long long>(c) * E;
-    if (e < E && mine != sum) bias[e] += mine < sum ? rate : -rate;
+    sum = s_sum[lane], n = s_able[lane];
+    add();
+    const long long mine = static_cast<long long>(c) * n;
+    if (able && mine != sum) bias[e] = b + (mine < sum ? rate : -rate);
 }
 
 // Blocks of a launch: one to an SM, or to a token.

@@ -1095,7 +1095,7 @@ def moe_router_backward(logits, router: Router, dweights, renormalize=True, rout
 
 def moe_router_update_bias(bias, counts, rate):
     """The balancing bias fp32 [E] after a step, in place: += rate for experts whose count (moe_router's counts, or
-    sums of them) is below the mean, -= rate above."""
+    sums of them) is below the mean, -= rate above.  Experts masked by a bias of -inf stay so, and are left out of the mean."""
     _cuda(bias, torch.float32, "bias")
     if bias.dim() != 1:
         raise ValueError(f"bias must be [E], got {list(bias.shape)}")

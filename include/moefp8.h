@@ -659,7 +659,8 @@ int moe_router(const void* logits, int64_t ld, int dtype, int T, int E, int topk
 int moe_router_backward(const void* logits, int64_t ld, int dtype, int T, int E, int topk, const moe_router_params* params,
                         const int32_t* ids, const float* dweights, const int32_t* counts, const int32_t* tokens,
                         float balance_coef, float z_coef, void* dlogits, void* stream);
-/* The balancing bias after a step: bias[e] += rate where counts[e] is below the mean of counts [E], -= rate where above. */
+/* The balancing bias after a step: bias[e] += rate where counts[e] is below the mean count, -= rate where above.  Experts that a
+ * bias of -infinity masks stay masked, and the mean is that of the others. */
 int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate, void* stream);
 
 /* ---- 4-bit rows and weights (microscaled floating point) -----------------------------------

