@@ -493,9 +493,11 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
         if (lane < found) s_near[place] = mine;
         __syncwarp();
         if (a.bias) {
+            // each key of the first k with the one before it, and all others with the k-th: the next may be of the same logit
+            // and bias as the k-th, and a nearer one behind it
             bool near = false;
-            if (lane < a.k && lane + 1 < found) {
-                const uint2 u = s_near[lane], n = s_near[lane + 1];
+            if (lane > 0 && lane < found) {
+                const uint2 u = s_near[min(lane, a.k) - 1], n = s_near[lane];
                 const float before = of_ordered(u.x), now = of_ordered(n.x);
                 if (before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)))
                     near = to_f32(logits[u.y]) != to_f32(logits[n.y]) || a.bias[u.y] != a.bias[n.y];
@@ -542,6 +544,18 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
             for (int v = V - 1; v >= 0; --v)
                 if (key[v] == top) at = v;
             const int e = __shfl_sync(kAll, first + at, src);
+            if (a.bias && j == a.k) {   // all that are left with the k-th
+                const float x = to_f32(logits[before_id]), b = a.bias[before_id];
+                bool near = false;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float now = of_ordered(key[v]);
+                    near |= key[v] >= kLeastKey && before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)) &&
+                            (l[v] != x || s_bias[lane * V + v] != b);
+                }
+                close |= __any_sync(kAll, near);
+                break;
+            }
             if (a.bias) {
                 const float now = of_ordered(top);
                 if (j > 0 && before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)))
@@ -549,7 +563,6 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                 before = now;
                 before_id = e;
             }
-            if (j >= a.k) break;
             if (lane == src) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -887,8 +900,14 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
                 if (a.bias && j + 1 < n) {
                     const uint2 o = sorted[j + 1];
                     const float before = of_ordered(u.x), now = of_ordered(o.x);
-                    if (before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)))
+                    if (before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now))) {
                         close |= x[i] != to_f32(row[o.y]) || s_bias[u.y / G * per_group + u.y % G] != s_bias[o.y / G * per_group + o.y % G];
+                        // the k-th and the next are alike: one behind them may be as near
+                        if (j + 1 == a.k && j + 2 < n) {
+                            const float third = j + 2 < kSorted ? of_ordered(sorted[j + 2].x) : before;
+                            close |= before - third <= slack + kRel * fmaxf(fabsf(before), fabsf(third));
+                        }
+                    }
                 }
             }
         }

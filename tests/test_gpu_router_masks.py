@@ -47,3 +47,42 @@ def test_bias_update_keeps_an_even_load_of_the_unmasked():
     assert bias[1] > 0 and bias[3] < 0 and (bias[5::2] == 0).all()
     r = moe.moe_router(torch.randn(300, E, generator=g).cuda(), 4, routing=moe.RoutingParams("sigmoid", bias=bias), losses=True)
     assert (r.counts[::2] == 0).all()
+
+
+# ---------------------------------------------------------------------------- keys nearer than fp32 tells
+def score64(l, scoring):
+    l = l.double()
+    return torch.softmax(l, 1) if scoring == "softmax" else torch.sigmoid(l)
+
+
+def choice64(l, bias, scoring, k):
+    """The k largest fp64 keys, ties to the lower expert."""
+    return (score64(l, scoring) + bias.double()).sort(dim=1, descending=True, stable=True).indices[:, :k]
+
+
+@pytest.mark.parametrize("T", [300, 6000])
+@pytest.mark.parametrize("copies", [2, 3, 20, 40])
+@pytest.mark.parametrize("above", [0, 3, 7])
+def test_a_near_key_behind_equal_ones(above, copies, T):
+    """At the border of the choice lie experts of one logit and one bias, and behind them one whose key is as near as fp32 tells, of
+    another logit and bias: it is chosen where its real key is larger."""
+    g, E = gen(2), 64
+    for last in (True, False):
+        bias = torch.full((E,), -3.0)
+        order = torch.randperm(E, generator=g)
+        alike = order[:copies].sort().values
+        other = E - 1 if last else 0
+        alike = alike[alike != other]
+        bias[alike], bias[other] = 0.125, 0.375
+        top = torch.tensor([e for e in order.tolist() if e != other and e not in alike.tolist()][:above], dtype=torch.long)
+        bias[top] = 4.0
+        l = torch.randn(T, E, generator=g)
+        x = 0.5 + torch.rand(T, generator=g)
+        s = torch.sigmoid(x.double())
+        l[:, alike] = x[:, None]
+        want = s + 0.125 - 0.375
+        l[:, other] = torch.log(want / (1 - want)).float()   # the same key but for the rounding of its logit: 2^-26 or so
+        for k in (above + 1, above + 2):
+            ref = choice64(l, bias, "sigmoid", k)
+            r = moe.moe_router(l.cuda(), k, routing=moe.RoutingParams("sigmoid", bias=bias.cuda()))
+            assert torch.equal(r.ids.cpu().long(), ref), (last, k)
