@@ -12,8 +12,10 @@
 //   renormalised  dl_j = phi_j q_j (g_j - sum q g);   else  softmax: dl_e = s_e (g_e - sum s g), sigmoid: dl_j = phi_j s_j g_j
 //   balance a     dl_e += phi_e P_e (h_e - sum P h), h_e = a E counts_e / (k n^2);   z b  dl_e += 2 b lse s_e / n
 //
-// The choice is that of the real numbers: keys are formed in fp32, and where two of them that a decision compares are
-// closer than their error (and not of the same logit and bias) the token's choice is repeated on fp64 keys.
+// The choice is that of fp64 keys: they are formed in fp32, and where two of them that a decision compares are closer than their
+// error (and not of the same logit and bias) the token's choice is repeated in fp64.  Keys that are equal there are ordered by
+// their logits and then their biases, groups by their scores without the bias and what these leave to 1: where a score is lost in
+// the bias, or is 1 to fp64's last bit (sigmoid from 37 on), that is the order of the real numbers if the biases are the same.
 //
 // Lanes hold V experts each in registers.  Where a token's experts fit eight lanes and there are many tokens, a warp takes four
 // at a time, so that most instructions work for four tokens; else a token has a warp.  The lanes are dealt to the groups, a
@@ -246,6 +248,44 @@ __device__ __forceinline__ double sigmoid64(double x) {
     return (x < 0.0 ? e : 1.0) / (1.0 + e);
 }
 
+// Orders equal fp64 keys: the larger logit first, then the larger bias.
+__device__ __forceinline__ uint64_t tie_key(float l, float b) { return static_cast<uint64_t>(ordered(l)) << 32 | ordered(b); }
+
+// The places of groups of which some have equal fp64 values (t1, t2: a group's two largest keys): by the scores of the experts whose
+// keys these are, and then by what the scores leave to 1.  (Rare: bf16 logits that meet, scores that vanish or reach 1.)
+template <int V, bool SIGMOID>
+__device__ __noinline__ int tied_place(const float* l, const uint64_t* key, float m, const RouterArgs& a, int first, int lanes,
+                                       uint64_t mine) {
+    const int own = (threadIdx.x & 31) / lanes;
+    uint64_t t1 = 0, t2 = 0, p1 = 0, p2 = 0;   // the two largest keys and their tie_key
+    const auto join = [&](uint64_t t, uint64_t p) {
+        const bool top = t > t1 || (t == t1 && p > p1);
+        if (top || t > t2 || (t == t2 && p > p2)) t2 = top ? t1 : t, p2 = top ? p1 : p;
+        if (top) t1 = t, p1 = p;
+    };
+    for (int v = 0; v < V; ++v)
+        if (key[v] != 0) join(key[v], tie_key(l[v], a.bias ? a.bias[first + v] : 0.0f));
+    for (int o = 1; o < lanes; o <<= 1) {
+        const uint64_t u1 = __shfl_xor_sync(kAll, static_cast<unsigned long long>(t1), o), u2 = __shfl_xor_sync(kAll, static_cast<unsigned long long>(t2), o);
+        const uint64_t q1 = __shfl_xor_sync(kAll, static_cast<unsigned long long>(p1), o), q2 = __shfl_xor_sync(kAll, static_cast<unsigned long long>(p2), o);
+        join(u1, q1);
+        join(u2, q2);
+    }
+    const double x1 = of_ordered(static_cast<uint32_t>(p1 >> 32)), x2 = of_ordered(static_cast<uint32_t>(p2 >> 32));
+    const bool one = t1 != 0, two = a.top2 && t2 != 0;
+    const auto score = [&](double x) { return SIGMOID ? sigmoid64(x) : exp64(x - m); };
+    const uint64_t sum = ordered((one ? score(x1) : 0.0) + (two ? score(x2) : 0.0));
+    const uint64_t rest = SIGMOID ? ~ordered((one ? sigmoid64(-x1) : 0.0) + (two ? sigmoid64(-x2) : 0.0)) : 0;
+    int place = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(mine), g * lanes);
+        const uint64_t os = __shfl_sync(kAll, static_cast<unsigned long long>(sum), g * lanes);
+        const uint64_t orest = __shfl_sync(kAll, static_cast<unsigned long long>(rest), g * lanes);
+        place += o != mine ? o > mine : os != sum ? os > sum : orest != rest ? orest > rest : g < own;
+    }
+    return place;
+}
+
 template <int V, bool SIGMOID>
 __device__ __noinline__ int choose_exact(const float* l, float m, const RouterArgs& a, int first, int count, int lanes) {
     const int lane = threadIdx.x & 31;
@@ -285,9 +325,17 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
         const uint64_t mine = a.top2 && t2 > 0 ? ordered(of_ordered(t1) + of_ordered(t2)) : t1;
         const int own = lane / lanes;
         int place = 0;
+        bool tied = false;
         for (int g = 0; g < a.groups; ++g) {
             const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(mine), g * lanes);
             place += o > mine || (o == mine && g < own);
+            tied |= o == mine && g != own && own < a.groups;
+        }
+        if (__any_sync(kAll, tied)) {
+            uint64_t copy[V];   // (so that the keys stay in registers)
+#pragma unroll
+            for (int v = 0; v < V; ++v) copy[v] = key[v];
+            place = tied_place<V, SIGMOID>(l, copy, m, a, first, lanes, mine);
         }
         if (own >= a.groups || place >= a.kept) {
 #pragma unroll
@@ -301,11 +349,27 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
         for (int v = 1; v < V; ++v) best = max(best, key[v]);
         const uint64_t top = warp_max(best);
         if (top == 0) break;
-        int at = 0;
+        int at = 0, equal = 0;
 #pragma unroll
-        for (int v = V - 1; v >= 0; --v)
+        for (int v = V - 1; v >= 0; --v) {
             if (key[v] == top) at = v;
-        const int src = __ffs(static_cast<int>(__ballot_sync(kAll, best == top))) - 1;
+            equal += key[v] == top ? 1 : 0;
+        }
+        bool has = best == top;
+        if (__reduce_add_sync(kAll, equal) > 1) {
+            uint64_t tie = 0;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) {
+                if (key[v] == top) {
+                    const uint64_t p = tie_key(l[v], a.bias ? a.bias[first + v] : 0.0f);
+                    if (p >= tie) at = v;
+                    tie = max(tie, p);
+                }
+            }
+            const uint64_t first_of = warp_max(tie);
+            has = has && tie == first_of;
+        }
+        const int src = __ffs(static_cast<int>(__ballot_sync(kAll, has))) - 1;
         const int e = __shfl_sync(kAll, first + at, src);
         if (lane == src) {
 #pragma unroll
@@ -439,14 +503,16 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                     }
                     const uint64_t value = a.top2 && u2 > 0 ? ordered(of_ordered(u1) + of_ordered(u2)) : u1;
                     const uint32_t borders = __ballot_sync(kAll, border);
+                    bool tied = false;   // (equal in fp64, too)
                     place = 0;
                     for (int g = 0; g < a.groups; ++g) {
                         const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(value), g * lanes);
                         const float of = __shfl_sync(kAll, mine, g * lanes);
                         const bool both = border && ((borders >> (g * lanes)) & 1u);
                         place += both ? o > value || (o == value && g < own) : of > mine || (of == mine && g < own);
+                        tied |= both && o == value && g != own;
                     }
-                    close = false;
+                    close = __any_sync(kAll, tied);
                 }
                 __syncwarp();
             }
@@ -510,17 +576,20 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                     for (int v = 0; v < V; ++v) all += l[v] > kNone ? exp64(static_cast<double>(l[v]) - m) : 0.0;
                     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
                 }
-                uint64_t wide = 0;
+                uint64_t wide = 0, tie = 0;
                 if (lane < found) {
-                    const double x64 = to_f32(logits[mine.y]);
+                    const float x = to_f32(logits[mine.y]), b = a.bias[mine.y];
+                    const double x64 = x;
                     const double s64 = SIGMOID ? sigmoid64(x64) : exp64(x64 - m) / all;
-                    wide = ordered(s64 + static_cast<double>(a.bias[mine.y]));
+                    wide = ordered(s64 + static_cast<double>(b));
+                    tie = tie_key(x, b);
                 }
                 place = 0;
                 for (int i = 0; i < found; ++i) {
                     const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(wide), i);
+                    const uint64_t ot = __shfl_sync(kAll, static_cast<unsigned long long>(tie), i);
                     const uint32_t oe = __shfl_sync(kAll, mine.y, i);
-                    place += o > wide || (o == wide && oe < mine.y);
+                    place += o != wide ? o > wide : ot != tie ? ot > tie : oe < mine.y;
                 }
                 __syncwarp();
                 if (lane < found) s_near[place] = mine;

@@ -623,8 +623,11 @@ int moe_expert_gemm_wgrad(const void* dc, int64_t lddc, const void* a, int64_t l
  *   score    s = softmax(l) or sigmoid(l); key = s + bias, or the order of the logits where bias is NULL
  *   groups   (n_group > 1) E / n_group consecutive experts; the topk_group groups whose value, the sum of the two
  *            largest keys or the largest (MOE_GROUP_*), is largest stay (ties: lower group)
- *   choice   the topk largest keys (ties: lower expert), as the real numbers are ordered; a logit of -infinity is never
- *            chosen, and NaN and +infinity count as that (MOE_STATUS_BAD_LOGIT); slots without an expert hold id -1, weight 0
+ *   choice   the topk largest keys (ties: lower expert); a logit of -infinity is never chosen, and NaN and +infinity count
+ *            as that (MOE_STATUS_BAD_LOGIT); slots without an expert hold id -1, weight 0
+ *   order    keys and groups' values are compared as fp64 numbers (scores below 2^-1000 of a token's largest count as 0).  Keys
+ *            equal there go by their logit, then their bias; groups by the sum of the scores, then by how little these leave to 1
+ *            (sigmoid): with one bias for all experts, or none, the order of the real numbers
  *   weights  routed_scaling * s, divided by the sum of the chosen s with renormalize
  * logits [T, E] with row stride ld; bias fp32 [E] (finite, or -infinity: the expert is never chosen) or NULL; valid: bytes [T],
  * 0 = a padded token (all ids -1), or NULL; ids int32 [T, topk], weights fp32 [T, topk], descending keys (moe_dispatch drops

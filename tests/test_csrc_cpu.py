@@ -43,5 +43,34 @@ def test_cluster_barriers_are_whole():
         assert steps == ["arrive", "wait"] * (len(steps) // 2), name
 
 
+EXCHANGE = re.compile(r"\b(?:warp_max|warp_sum|lanes_max<\w+>|lanes_sum<\w+>|chosen_sum|__shfl\w*_sync|__any_sync|__all_sync|__ballot_sync|"
+                      r"__reduce_\w+_sync|__syncwarp|__syncthreads\w*|half_ok)\(")
+
+
+def test_no_exchange_behind_a_short_circuit():
+    """What a whole warp or block has to enter does not stand behind &&, || or ?:, which lets some of its threads past it (a
+    constant's, in capitals, is the same for all)."""
+    def statements(text):
+        """Pieces between braces and the semicolons outside of parentheses; headers of if, for and while by themselves."""
+        depth, start = 0, 0
+        for i, c in enumerate(text):
+            depth += {"(": 1, ")": -1}.get(c, 0)
+            header = c == ")" and depth == 0 and re.match(r"\s*(?:else\s+)?(?:if(?:\s+constexpr)?|for|while)\s*\(", text[start:i])
+            if header or (c in ";{}" and depth == 0) or c in "{}":
+                yield text[start:i + 1]
+                start = i + 1
+                depth = 0 if c in "{}" else depth
+
+    seen = 0
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu*"))):
+        text = re.sub(r"//[^\n]*|#[^\n]*", "", open(path).read())
+        for part in statements(text):
+            for m in EXCHANGE.finditer(part):
+                seen += 1
+                before = re.sub(r"\b[A-Z][A-Z0-9_]* \?", "", part[:m.start()])
+                assert not re.search(r"&&|\|\||\?", before), f"{os.path.basename(path)}: {' '.join(part.split())}"
+    assert seen > 100
+
+
 if __name__ == "__main__":
     pytest.main([__file__])

@@ -86,3 +86,66 @@ def test_a_near_key_behind_equal_ones(above, copies, T):
             ref = choice64(l, bias, "sigmoid", k)
             r = moe.moe_router(l.cuda(), k, routing=moe.RoutingParams("sigmoid", bias=bias.cuda()))
             assert torch.equal(r.ids.cpu().long(), ref), (last, k)
+
+
+# ------------------------------------------------------------------------- keys that are equal in fp64
+def routes(T):
+    """Sizes that reach the warp-a-token and the four-tokens-a-warp kernel."""
+    return ((300, 64), (T, 64), (T, 128), (T, 256))
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("value", [0.0, 0.375, -2.0])
+def test_one_bias_for_all_orders_as_the_logits(scoring, value):
+    """Scores that are 1 to fp64's last bit, that vanish in it or in the bias: with one bias for all the choice is the logits'."""
+    g = gen(3)
+    for T, E in routes(6000):
+        l = torch.randn(T, E, generator=g)
+        l[::4] *= 100.0          # sigmoid: 1 and 0; softmax: below 2^-1000 of the largest
+        l[1::4] += 45.0          # sigmoid: 1 - 1e-19
+        l[2::4] -= 60.0          # sigmoid: 1e-26, lost in the bias
+        bias = torch.full((E,), value)
+        ref = l.sort(dim=1, descending=True, stable=True).indices[:, :6]
+        for b in (bias.cuda(), None):
+            r = moe.moe_router(l.cuda(), 6, routing=moe.RoutingParams(scoring, bias=b))
+            assert torch.equal(r.ids.cpu().long(), ref), (T, E, b is None)
+    for pair in ([40.0, 41.0], [-200.0, -199.0], [0.0, 1e-30]):
+        r = moe.moe_router(torch.tensor([pair]).cuda(), 1, routing=moe.RoutingParams(scoring, bias=torch.full((2,), value).cuda()))
+        assert r.ids.item() == 1
+
+
+@pytest.mark.parametrize("score", ["max", "top2"])
+@pytest.mark.parametrize("value", [None, 0.0, 0.375])
+def test_groups_of_scores_that_are_one(value, score):
+    """Sigmoid scores from 37 on: a group's value is what its scores leave to 1, the smaller the better."""
+    g = gen(4)
+    for T, E in routes(6000):
+        G, kept = 8, 3
+        l = 38.0 + 20.0 * torch.rand(T, E, generator=g)
+        bias = None if value is None else torch.full((E,), value).cuda()
+        by = l.reshape(T, G, -1)
+        top = by.sort(dim=2, descending=True).values[:, :, :1 if score == "max" else 2]
+        rest = torch.exp(-top.double()).sum(2)   # 1 - sigmoid(l), to 1e-16 of itself
+        order = rest.sort(dim=1, stable=True).indices[:, :kept]
+        keep = torch.zeros(T, G, dtype=torch.bool).scatter_(1, order, True)
+        ref = by.masked_fill(~keep[:, :, None], -math.inf).reshape(T, E).sort(dim=1, descending=True, stable=True).indices[:, :4]
+        r = moe.moe_router(l.cuda(), 4, routing=moe.RoutingParams("sigmoid", n_group=G, topk_group=kept, bias=bias), group_score=score)
+        assert torch.equal(r.ids.cpu().long(), ref), (T, E)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_scores_the_bias_swallows(scoring):
+    """Scores of 1e-26 and less beside a bias of 1: the groups' order is that of the scores' sums."""
+    g = gen(5)
+    for T, E in routes(6000):
+        G, kept = 8, 3
+        l = -60.0 - 20.0 * torch.rand(T, E, generator=g)
+        if scoring == "softmax":
+            l[:, 0] = 0.0        # the largest score is 1, and its group the first
+        by = l.reshape(T, G, -1)
+        total = torch.exp(by.sort(dim=2, descending=True).values[:, :, :2].double()).sum(2)
+        order = total.sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        keep = torch.zeros(T, G, dtype=torch.bool).scatter_(1, order, True)
+        ref = by.masked_fill(~keep[:, :, None], -math.inf).reshape(T, E).sort(dim=1, descending=True, stable=True).indices[:, :4]
+        r = moe.moe_router(l.cuda(), 4, routing=moe.RoutingParams(scoring, n_group=G, topk_group=kept, bias=torch.ones(E).cuda()))
+        assert torch.equal(r.ids.cpu().long(), ref), (T, E)
