@@ -399,6 +399,10 @@ __device__ __forceinline__ float score32(float l, float m) {
     return __fdividef(l < 0.0f ? e : 1.0f, 1.0f + e);
 }
 
+// A sum of sigmoid scores below which they vanish (e^-69): there s is e^l to fp32's last bit, and shares are formed as e^(l - m), the
+// largest logit's being 1, which no underflow reaches.
+constexpr float kVanished = 1e-30f;
+
 // The lane's place among 32 that take a token: its group, its first expert and how many it has.
 struct Seat {
     int lanes, own, first, count;   // lanes: of a group
@@ -429,8 +433,17 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
         z = warp_sum(z);
         per = __fdividef(1.0f, fmaxf(z, 1e-37f));
         if constexpr (STATS) {
+            if (SIGMOID && z < kVanished) {   // (the same in every lane)
+                float u[V], sum = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], per, share[v]);
+                for (int v = 0; v < V; ++v) sum += u[v] = __expf(l[v] - m);
+                sum = warp_sum(sum);
+#pragma unroll
+                for (int v = 0; v < V; ++v) share[v] += __fdividef(u[v], sum);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], per, share[v]);
+            }
             *lse = SIGMOID ? 0.0f : m + logf(z);
         }
     }
@@ -839,8 +852,17 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
             z = lanes_sum<L>(z);
             per = __fdividef(1.0f, fmaxf(z, 1e-37f));
             if constexpr (STATS) {
+                const bool gone = SIGMOID && alive && z < kVanished;   // (the same in a token's lanes)
 #pragma unroll
-                for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], alive ? per : 0.0f, share[v]);
+                for (int v = 0; v < V; ++v) share[v] = fmaf(s[v], alive && !gone ? per : 0.0f, share[v]);
+                if (SIGMOID && __any_sync(kAll, gone)) {
+                    float u[V], sum = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum += u[v] = __expf(l[v] - m);
+                    sum = lanes_sum<L>(sum);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) share[v] += gone ? __fdividef(u[v], sum) : 0.0f;
+                }
                 const float lse = SIGMOID || !alive ? 0.0f : m + logf(z);
                 if (sub == 0) {
                     z_sum = fmaf(lse, lse, z_sum);
@@ -1182,6 +1204,33 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 4 : 2) router_b
             }
             z = lanes_sum<L>(z);
             if (shares) mean_h = lanes_sum<L>(mean_h);
+            if (SIGMOID && shares) {
+                const bool gone = some && z < kVanished;   // (the same in a token's lanes)
+                if (__any_sync(kAll, gone)) {   // the logits once more
+                    float u[V], top = kNone, all = 0.0f, h = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float x = gone && v < count ? to_f32(logits[t * a.ld + first + v]) : kNone;
+                        u[v] = x < INFINITY ? x : kNone;
+                        top = fmaxf(top, u[v]);
+                    }
+                    top = lanes_max<L>(top);
+                    top = top > kNone ? top : 0.0f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        u[v] = __expf(u[v] - top);
+                        all += u[v];
+                        h = fmaf(u[v], s_mem[v * P + sub], h);
+                    }
+                    all = lanes_sum<L>(all);
+                    h = lanes_sum<L>(h);
+                    if (gone) {
+                        z = all, mean_h = h;
+#pragma unroll
+                        for (int v = 0; v < V; ++v) c[v] = u[v];   // (1 - s is 1)
+                    }
+                }
+            }
         }
         if (a.vector && t + step < a.T) raw.load(logits + (t + step) * a.ld + first, dense ? count : 0, true);
         const float per = some ? __fdividef(1.0f, fmaxf(z, 1e-37f)) : 0.0f;

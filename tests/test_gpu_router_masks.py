@@ -149,3 +149,55 @@ def test_groups_whose_scores_the_bias_swallows(scoring):
         ref = by.masked_fill(~keep[:, :, None], -math.inf).reshape(T, E).sort(dim=1, descending=True, stable=True).indices[:, :4]
         r = moe.moe_router(l.cuda(), 4, routing=moe.RoutingParams(scoring, n_group=G, topk_group=kept, bias=torch.ones(E).cuda()))
         assert torch.equal(r.ids.cpu().long(), ref), (T, E)
+
+
+# -------------------------------------------------------------------------------- scores that vanish
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("T,E", [(40, 64), (6000, 64), (6000, 100), (300, 250), (300, 1000)])
+def test_tokens_whose_sigmoid_scores_vanish(T, E, dtype):
+    """Their shares, the balance loss and its gradient are those of the formulas, whose scores are e^l there."""
+    g = gen(6)
+    l = torch.randn(T, E, generator=g) * 2
+    l[::2] -= 75.0 + 400.0 * torch.rand(len(l[::2]), 1, generator=g)    # from 1e-33 to far below fp32's range
+    l[1::6] -= 66.0                                                     # about where the shares change their form
+    l[2, ::3], l[4, 1:], l[6] = -math.inf, -math.inf, -math.inf
+    l = l.to(dtype)
+    valid = torch.rand(T, generator=g) < 0.9
+    valid[:8] = True
+    dw = torch.randn(T, 4, generator=g)
+    coef = 0.7 * T
+    # in 64 bits, through logarithms
+    x = l.double().requires_grad_()
+    none = x.detach() == -math.inf
+    live = valid & ~none.all(1)
+    n = int(live.sum())
+    safe = torch.where(live[:, None], torch.where(none, -1e5, x), 0.0)
+    log = torch.nn.functional.logsigmoid(safe)
+    share = torch.softmax(log, 1) * live[:, None]
+    ids = torch.where(none, -math.inf, x.detach()).sort(dim=1, descending=True, stable=True).indices[:, :4]
+    real = live[:, None] & ~none.gather(1, ids)
+    counts = torch.bincount(ids[real], minlength=E)
+    f = counts.double() * E / (4 * n)
+    balance = (f * share.sum(0)).sum() / n
+    w = torch.softmax(torch.where(real, log.gather(1, ids), torch.where(real.any(1, keepdim=True), -math.inf, 0.0)), 1) * real
+    grad = torch.autograd.grad((w * dw.double()).sum() + coef * balance, x)[0].nan_to_num(0.0).detach()
+    w, balance, share = w.detach(), balance.detach(), share.detach()
+
+    r = moe.moe_router(l.cuda(), 4, routing=moe.RoutingParams("sigmoid"), valid=valid.cuda(), losses=True)
+    assert torch.equal(r.ids.cpu().long(), torch.where(real, ids, -1))
+    assert torch.equal(r.counts.cpu().long(), counts) and int(r.tokens) == n
+    # fp32 half-steps: an exponential of a difference of up to 20 (the rest are below 2^-24 of the largest) 4 and 20, its sum 2 and
+    # as many as a lane has experts, the quotient 4, twice; the sums over tokens
+    u = 2 * (30 + E // 8) * 2.0 ** -24
+    check_to = lambda got, want, size: ((got.double().cpu() - want).abs() <= size).all()  # noqa: E731
+    assert check_to(r.weights, w, u * w + 1e-37)
+    assert check_to(r.balance_loss, balance, (u + (T / 2432 + 80) * 2.0 ** -24) * balance)
+    got = moe.moe_router_backward(l.cuda(), r, dw.cuda(), routing=moe.RoutingParams("sigmoid"), balance_coef=coef)
+    h = coef * f / n
+    size = share * (h + (share * h).sum(1, keepdim=True))
+    inner = (w * dw.double().abs()).sum(1, keepdim=True)
+    size = size.scatter_add(1, ids, torch.where(real, w * (dw.double().abs() + inner), 0.0))
+    assert check_to(got, grad, torch.finfo(dtype).eps / 2 * grad.abs() + 4 * u * size + 1e-37)
+    # what it was before: nothing of those tokens in the loss
+    vanished = live & (l.double().max(1).values < -100)
+    assert vanished.any() and abs(float(share[vanished].sum()) - int(vanished.sum())) < 1e-6
