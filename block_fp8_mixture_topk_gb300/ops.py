@@ -1229,7 +1229,8 @@ def moe_mxfp4_quant_weight(w):
 def moe_fp4_pack_scales(scales, format="mxfp4", gate_up=False):
     """Scale bytes of 4-bit weights [E, N, K/32] (mxfp4, UE8M0) or [E, N, K/16] (nvfp4, e4m3; moe_nvfp4_quant_weight's)
     into the tiles that the 4-bit products read (load-time).  gate_up: of a w13 (gate rows, then up rows) for
-    moe_fp4_expert_gemm_silu_mul."""
+    moe_fp4_expert_gemm_silu_mul and _silu_mul_quant, in another order of the same size: the result notes which, and products of
+    the other kind refuse it (a copy, a part of it or scales laid out elsewhere carry no note, and are taken as right)."""
     fmt = _fp4_format(format)
     scales = _codes(_cuda(scales, None, "scales"))
     if scales.dim() != 3:
@@ -1242,6 +1243,7 @@ def moe_fp4_pack_scales(scales, format="mxfp4", gate_up=False):
     out = torch.empty(E, (N + 127) // 128, (K + 255) // 256, words * 512, dtype=torch.uint8, device=scales.device)
     _check("moe_fp4_pack_scales", lib().moe_fp4_pack_scales(_ptr(scales), fmt, E, N, K, int(bool(gate_up)), _ptr(out),
                                                             _stream("scales", scales)))
+    out.fp4_gate_up = bool(gate_up)
     return out
 
 
@@ -1271,6 +1273,8 @@ def _fp4_expert_gemm(rows, w, w_scales, w_global, dtype, epilogue):
     code = DTYPE.get(dtype)
     if code is None or (epilogue and code == 2):
         raise TypeError(f"dtype must be bfloat16{' or float16' if epilogue else ', float16 or float32'}, got {dtype}")
+    if getattr(w_scales, "fp4_gate_up", epilogue != 0) != (epilogue != 0):
+        raise ValueError(f"w_scales must be packed with gate_up={epilogue != 0} for this product")
     stream = _stream("rows.codes rows.scales rows.row_scale rows.expert_offsets w w_scales w_global", codes, scales, row_scale,
                      offsets, w, w_scales, w_global)
     out_scales = None

@@ -679,7 +679,8 @@ int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate
  * The products take scales in tiles (512 bytes: 32 lines of 16, line l the words of rows l, l + 32, l + 64, l + 96, a word
  * four consecutive groups; W = 2 tiles (mxfp4) or 4 (nvfp4) for 128 rows by 256 columns; bytes past K are 0):
  *   weights  [E][ceil(N/128)][ceil(K/256)][W][512]; with gate_up (rows gate, then up; N % 32 == 0) of the rows in the
- *            order 16 gate, 16 up of the same columns, and so on: for the SiLU product
+ *            order 16 gate, 16 up of the same columns, and so on: for the SiLU products, which take no others (both kinds have
+ *            one size, so the library cannot tell; the Python binding notes the kind on the tensors that it packs)
  *   rows     [tiles of 224 rows][ceil(K/256)][2][W][512]; row r of expert e, whose rows begin at o_e, in tile
  *            o_e / 224 + e + (r - o_e) / 224, and rows of no expert as those of an expert E. */
 #define MOE_FP4_MXFP4 0
