@@ -397,8 +397,11 @@ size_t moe_fp4_row_scale_bytes(int fmt, int64_t num_rows, int E, int K) {
 }
 
 size_t moe_fp4_weight_scale_bytes(int fmt, int E, int N, int K) {
-    if (!known_format(fmt) || E < 1 || N < 1 || K < 1 || K % 32 != 0) return 0;
-    return static_cast<size_t>(E) * ((static_cast<size_t>(N) + 127) / 128) * fp4_blocks(K) * fp4_words(fmt) * 512;
+    if (!known_format(fmt) || E < 1 || E > MOE_MAX_EXPERTS || N < 1 || N % 8 != 0 || N >= kFp4MaxOut || K < 1 || K % 32 != 0 ||
+        K > kFp4MaxCols)
+        return 0;
+    const size_t tiles = static_cast<size_t>(E) * ((static_cast<size_t>(N) + 127) / 128) * fp4_blocks(K) * fp4_words(fmt);
+    return tiles < (size_t(1) << 31) ? tiles * 512 : 0;
 }
 
 int moe_fp4_quant(const void* x, int64_t ldx, int dtype, int fmt, const int32_t* expert_offsets, int E, int64_t num_rows,
@@ -449,7 +452,7 @@ int moe_mxfp4_quant_weight(const void* w, int dtype, int E, int N, int K, uint8_
 
 int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate_up, uint8_t* out, void* stream) {
     if (!known_format(fmt) || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-    if (K % 32 != 0 || (gate_up && N % 32 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (moe_fp4_weight_scale_bytes(fmt, E, N, K) == 0 || (gate_up && N % 32 != 0)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!s || !out || address(out) % 16) return MOE_ERR_INVALID_ARG;
     int rc;
     uint32_t* status = nullptr;
@@ -470,7 +473,7 @@ int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float
     int rc = check_rows(fmt, dtype, expert_offsets, expert_offsets ? E : 0, num_rows, K);
     if (rc != MOE_OK) return rc;
     if (E < 1 || N < 1 || (!expert_offsets && E != 1) || (silu && dtype == MOE_DTYPE_FP32)) return MOE_ERR_INVALID_ARG;
-    if (N % (quant ? 64 : silu ? 32 : 8) != 0 || N >= (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (N % (quant ? 64 : silu ? 32 : 8) != 0 || N >= kFp4MaxOut) return MOE_ERR_UNSUPPORTED_SHAPE;
     const bool nv = fmt == MOE_FP4_NVFP4;
     if (!w_codes || !w_scales || (w_global != nullptr) != nv || (row_scale != nullptr) != (nv && num_rows > 0))
         return MOE_ERR_INVALID_ARG;
@@ -482,7 +485,7 @@ int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float
         return MOE_ERR_INVALID_ARG;
     const size_t scale_bytes = moe_fp4_row_scale_bytes(fmt, num_rows, expert_offsets ? E : 0, K);
     const size_t w_scale_bytes = moe_fp4_weight_scale_bytes(fmt, E, N, K);
-    if (scale_bytes / 512 >= (size_t(1) << 31) || w_scale_bytes / 512 >= (size_t(1) << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (scale_bytes / 512 >= (size_t(1) << 31) || w_scale_bytes == 0) return MOE_ERR_UNSUPPORTED_SHAPE;
     const int64_t row_tiles = num_rows / kFp4Rows + (num_rows < E ? num_rows : E) + 1;
     const int64_t items = row_tiles * (silu ? (N / 2 + 127) / 128 : (N + 255) / 256);
     if (items >= int64_t(1) << 31) return MOE_ERR_UNSUPPORTED_SHAPE;

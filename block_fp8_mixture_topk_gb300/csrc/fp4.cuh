@@ -23,6 +23,7 @@ namespace mfp8 {
 constexpr int kFp4Rows = 224;      // rows of an item of the products, and of a tile of their scales
 constexpr int kFp4Block = 256;     // columns of a K block
 constexpr int kFp4MaxCols = 32768;
+constexpr int kFp4MaxOut = 1 << 24;   // output columns of a product are fewer
 
 __host__ __device__ constexpr int fp4_group(int fmt) { return fmt == MOE_FP4_MXFP4 ? 32 : 16; }
 __host__ __device__ constexpr int fp4_words(int fmt) { return fmt == MOE_FP4_MXFP4 ? 2 : 4; }

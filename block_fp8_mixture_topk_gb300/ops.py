@@ -1152,6 +1152,8 @@ def _fp4_row_scale_bytes(fmt, n, E, K):
 
 def _fp4_weight_scale_bytes(fmt, E, N, K):
     """moe_fp4_weight_scale_bytes, likewise."""
+    if K % 32 or not 0 < K <= _FP4_MAX_COLS or E > 1024 or N % 8 or not 0 < N < 2 ** 24:
+        return 0
     return E * ((N + 127) // 128) * ((K + 255) // 256) * (1024 << fmt)
 
 
@@ -1256,7 +1258,8 @@ def _fp4_weights(fmt, E, K, w, w_scales, w_global):
     if N > _INT_MAX:
         raise _too_large("w")
     _cuda(w_scales, torch.uint8, "w_scales")
-    if w_scales.numel() != _fp4_weight_scale_bytes(fmt, E, N, K):
+    size = _fp4_weight_scale_bytes(fmt, E, N, K)   # (0: the library refuses the product)
+    if size and w_scales.numel() != size:
         raise ValueError("w_scales must be moe_fp4_pack_scales of w's scales in the rows' format")
     if (w_global is None) != (fmt == 0):
         raise ValueError("w_global is needed with nvfp4, and only there")

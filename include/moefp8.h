@@ -686,7 +686,8 @@ int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate
 #define MOE_FP4_MXFP4 0
 #define MOE_FP4_NVFP4 1
 /* Bytes of the rows' scales (E = 0: rows that are not sorted by expert) and of the weights'; 0 for sizes that the calls
- * refuse. */
+ * refuse (weights: those of the packing and of every product: E > 1024, K no multiple of 32 or past 32768, N no multiple of 8 or
+ * 2^24 and more). */
 size_t moe_fp4_row_scale_bytes(int fmt, int64_t num_rows, int E, int K);
 size_t moe_fp4_weight_scale_bytes(int fmt, int E, int N, int K);
 /* Rows x [num_rows, K] of row stride ldx (bf16, fp16 or fp32, any element's address) in 4 bits.  expert_offsets int32
