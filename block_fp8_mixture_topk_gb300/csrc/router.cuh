@@ -1206,29 +1206,26 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, V <= 16 ? 4 : 2) router_b
             if (shares) mean_h = lanes_sum<L>(mean_h);
             if (SIGMOID && shares) {
                 const bool gone = some && z < kVanished;   // (the same in a token's lanes)
-                if (__any_sync(kAll, gone)) {   // the logits once more
-                    float u[V], top = kNone, all = 0.0f, h = 0.0f;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
+                if (__any_sync(kAll, gone)) {   // the logits once more, twice: kept, they would cost registers in every token
+                    const auto logit = [&](int v) {
                         const float x = gone && v < count ? to_f32(logits[t * a.ld + first + v]) : kNone;
-                        u[v] = x < INFINITY ? x : kNone;
-                        top = fmaxf(top, u[v]);
-                    }
+                        return x < INFINITY ? x : kNone;
+                    };
+                    float top = kNone, all = 0.0f, h = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) top = fmaxf(top, logit(v));
                     top = lanes_max<L>(top);
                     top = top > kNone ? top : 0.0f;
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        u[v] = __expf(u[v] - top);
-                        all += u[v];
-                        h = fmaf(u[v], s_mem[v * P + sub], h);
+                        const float u = __expf(logit(v) - top);
+                        all += u;
+                        h = fmaf(u, s_mem[v * P + sub], h);
+                        c[v] = gone ? u : c[v];   // (1 - s is 1)
                     }
                     all = lanes_sum<L>(all);
                     h = lanes_sum<L>(h);
-                    if (gone) {
-                        z = all, mean_h = h;
-#pragma unroll
-                        for (int v = 0; v < V; ++v) c[v] = u[v];   // (1 - s is 1)
-                    }
+                    z = gone ? all : z, mean_h = gone ? h : mean_h;
                 }
             }
         }
