@@ -381,15 +381,17 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
     return id;
 }
 
-// More than the error of a difference of keys is slack() and kRel of the larger.  A score is off by 2^-22.4 of itself (the
+// More than the error of a difference of keys is key_slack() and kRel of the larger.  A score is off by 2^-22.4 of itself (the
 // quotient, a sum) and by its exponential: 2^-22 and 1.44 * 2^-24 of the exponent d, that is by less than 2^-23.5 (sigmoid:
-// s (1 - s) <= 1/4, s (1 - s) d < 0.23) or 2^-24 of the largest score (softmax: d e^-d < 0.37) and 2^-22 of itself; softmax
-// scores share a factor off by 2^-18 at most (38 roundings, and 1.44 * 2^-24 of the entropy), which counts by the difference
-// of the scores, at most 2 b_most over the keys'.
+// s (1 - s) <= 1/4, s (1 - s) d < 0.23) or 2^-24 of the largest score (softmax: d e^-d < 0.37) and 2^-22 of itself; a score is at most
+// the key and b_most, so kRel and 2^-20 b_most cover what goes by the score.  Softmax scores share a factor, the sum's: in units of
+// 2^-24 its V + 4 additions (V experts a lane, five exchanges), its exponentials' 4 and 1.44 of the entropy (10 at most), and its
+// reciprocal's 4.  That counts by the difference of the scores, at most 2 b_most over the keys'.
 constexpr float kRel = 0x1p-20f;
-template <bool SIGMOID>
+template <int V, bool SIGMOID>
 __device__ __forceinline__ float key_slack(float b_most, float per) {
-    return (SIGMOID ? 0x1p-20f : 0x1p-17f) * b_most + (SIGMOID ? 0x1p-22f : 0x1p-22f * per);
+    constexpr float kShared = 2 * (V + 22) * 0x1p-24f;
+    return (SIGMOID ? 0x1p-20f : 0x1p-20f + kShared) * b_most + (SIGMOID ? 0x1p-22f : 0x1p-22f * per);
 }
 // Scores from logits (softmax: times z, m the largest logit); exp(-inf) = 0: one that cannot be chosen has score 0.
 template <bool SIGMOID>
@@ -447,7 +449,7 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
             *lse = SIGMOID ? 0.0f : m + logf(z);
         }
     }
-    const float slack = key_slack<SIGMOID>(b_most, per);
+    const float slack = key_slack<V, SIGMOID>(b_most, per);
     uint32_t key[V];
     if (scored) {   // s: keys as numbers
 #pragma unroll
@@ -870,7 +872,7 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
                 }
             }
         }
-        const float slack = key_slack<SIGMOID>(b_most, per);
+        const float slack = key_slack<V, SIGMOID>(b_most, per);
         // keys as numbers (s, where they are needed) and as ordered integers
         uint32_t key[V];
         if (scored) {
