@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_fp8_mixture_topk_gb300 as moe
+import test_gpu_router as base
 from train_testutil import gen
 
 pytestmark = pytest.mark.gpu
@@ -201,3 +202,91 @@ def test_tokens_whose_sigmoid_scores_vanish(T, E, dtype):
     # what it was before: nothing of those tokens in the loss
     vanished = live & (l.double().max(1).values < -100)
     assert vanished.any() and abs(float(share[vanished].sum()) - int(vanished.sum())) < 1e-6
+
+
+# ------------------------------------------------------ tokens that four to a warp leave to the whole warp
+SHARED = [base.Case(6000, E, k, scoring, bias, groups, kept, score, renorm, 1.5, dtype, padding)
+          for E, k, scoring, bias, groups, kept, score, renorm, dtype, padding in (
+    (64, 15, "softmax", "steps", 1, 1, "top2", True, torch.float32, 0.1),
+    (64, 16, "softmax", "", 1, 1, "top2", False, torch.bfloat16, 0.0),
+    (64, 16, "sigmoid", "steps", 1, 1, "top2", True, torch.float32, 0.2),
+    (64, 17, "sigmoid", "", 1, 1, "top2", True, torch.float16, 0.0),
+    (64, 32, "softmax", "steps", 1, 1, "top2", False, torch.float32, 0.3),
+    (64, 15, "sigmoid", "large", 8, 4, "top2", True, torch.float32, 0.0),
+    (64, 16, "softmax", "zero", 8, 3, "max", True, torch.float32, 0.1),
+    (128, 15, "sigmoid", "steps", 8, 2, "top2", False, torch.bfloat16, 0.0),
+    (128, 16, "sigmoid", "steps", 4, 2, "max", True, torch.float32, 0.1),
+    (128, 17, "softmax", "", 2, 1, "top2", True, torch.float32, 0.0),
+    (128, 32, "sigmoid", "large", 8, 3, "top2", True, torch.float32, 0.1),
+    (100, 32, "softmax", "", 5, 4, "top2", False, torch.float16, 0.5))]
+
+
+@pytest.mark.parametrize("c", SHARED, ids=str)
+def test_many_choices_of_many_tokens(c):
+    base.test_choice_weights_and_loads(c)
+
+
+@pytest.mark.parametrize("c", SHARED[::3], ids=str)
+def test_gradient_of_many_choices(c):
+    base.test_gradient(c, True)
+
+
+@pytest.mark.parametrize("groups,kept", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_keys_closer_than_their_fp32_error_of_many_tokens(scoring, groups, kept):
+    g = gen(7)
+    for E in (64, 128):
+        l = torch.randn(1, E, generator=g) + torch.randn(6000, E, generator=g) * 1e-7
+        s = score64(l[:1], scoring)[0]
+        bias = (1.0 - s).float()
+        c = base.Case(6000, E, 8, scoring, "given", groups, kept)
+        r = moe.moe_router(l.cuda(), 8, routing=base.routing(c, bias.cuda()))
+        assert torch.equal(r.ids.cpu().long(), base.reference(c, l, bias, None)["ids"])
+
+
+@pytest.mark.parametrize("T", [5, 6000])
+def test_all_equal_keys_of_many_tokens(T):
+    for scoring in ("softmax", "sigmoid"):
+        for bias in (None, torch.full((64,), 0.25, device="cuda")):
+            for dtype in (torch.float32, torch.bfloat16):
+                x = torch.zeros(T, 64, dtype=dtype, device="cuda")
+                for groups, kept, k in ((1, 1, 6), (8, 2, 10), (1, 1, 32)):
+                    rp = moe.RoutingParams(scoring, n_group=groups, topk_group=kept, bias=bias)
+                    r = moe.moe_router(x, k, routing=rp, losses=True)
+                    assert torch.equal(r.ids.cpu(), torch.arange(k, dtype=torch.int32).expand(T, k))
+                    assert torch.allclose(r.weights, torch.full_like(r.weights, 1 / k), rtol=1e-6)
+                    assert r.counts.tolist() == [T] * k + [0] * (64 - k)
+
+
+@pytest.mark.parametrize("score", ["top2", "max"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [40, 6000])
+def test_masked_experts_in_groups_keep_their_shares(T, scoring, score):
+    """A bias of -inf takes an expert out of the choice and its group's value; the scores of the others are the same as before, and
+    it keeps its share in the balance loss."""
+    g = gen(8)
+    for E, groups, kept in ((64, 8, 3), (60, 6, 2), (128, 4, 2)):
+        l = torch.randn(T, E, generator=g)
+        bias = torch.randint(-40, 41, (E,), generator=g) * 0.001
+        gone = torch.zeros(E, dtype=torch.bool)
+        gone[::3] = True
+        gone[:E // groups - 1] = True        # all but one of the first group
+        gone[-(E // groups):] = True         # all of the last
+        bias[gone] = -math.inf
+        s = score64(l, scoring)
+        key = s + bias.double()
+        top = key.reshape(T, groups, -1).sort(dim=2, descending=True).values[:, :, :1 if score == "max" else 2]
+        none = (top == -math.inf).all(2)
+        value = torch.where(top == -math.inf, 0.0, top).sum(2).masked_fill(none, -math.inf)
+        order = value.sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        keep = torch.zeros(T, groups, dtype=torch.bool).scatter_(1, order, True).repeat_interleave(E // groups, 1)
+        best = key.masked_fill(~keep, -math.inf).sort(dim=1, descending=True, stable=True)
+        ids = torch.where(best.values > -math.inf, best.indices, -1)[:, :4]
+        rp = moe.RoutingParams(scoring, n_group=groups, topk_group=kept, bias=bias.cuda())
+        r = moe.moe_router(l.cuda(), 4, routing=rp, group_score=score, losses=True)
+        assert torch.equal(r.ids.cpu().long(), ids)
+        counts = torch.bincount(ids[ids >= 0], minlength=E)
+        assert torch.equal(r.counts.cpu().long(), counts) and int(r.tokens) == T
+        want = (counts.double() * E / (4 * T) * (s / s.sum(1, keepdim=True)).mean(0)).sum()
+        # a score and its sum: 4 half-steps each, the argument's rounding (|l| < 8), the lane's and the tokens' sums
+        assert abs(float(r.balance_loss) - float(want)) <= (40 + E // 8 + T / 2432 + 80) * 2.0 ** -24 * float(want)

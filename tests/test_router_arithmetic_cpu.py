@@ -53,3 +53,55 @@ def test_slack_of_keys_covers_their_error(tmp_path):
         assert float(soft) >= 2 * b * shared + own * b, V
         assert float(sigm) >= own * b + 2 * 2.0 ** -23.5, V
         assert rel >= own
+
+
+@pytest.fixture(scope="module")
+def exponential(tmp_path_factory):
+    """Largest errors, in 2^-53 of the value, of exp64 and of sigmoid64 over ranges of the argument, and what is not in order."""
+    main = r"""
+    uint64_t state = 1;
+    const auto uniform = [&] {   // of [0, 1)
+        state = state * 6364136223846793005ull + 1442695040888963407ull;
+        return (double)(state >> 11) * 0x1p-53;
+    };
+    const auto off = [](double got, long double want) { return (double)(fabsl((long double)got - want) / want * 0x1p53L); };
+    for (double range : {1e-12, 1e-6, 0.005, 0.0108304, 0.022, 1.0, 40.0, 693.0}) {
+        double e = 0, s = 0, t = 0;
+        for (int i = 0; i < 200000; ++i) {
+            const double x = -range * uniform();
+            e = fmax(e, off(exp64(x), expl((long double)x)));
+            s = fmax(s, off(sigmoid64(x), expl((long double)x) / (1.0L + expl((long double)x))));
+            t = fmax(t, off(sigmoid64(-x), 1.0L / (1.0L + expl((long double)x))));
+        }
+        printf("%g %g %g %g ", range, e, s, t);
+    }
+    // next to the table's borders, and fp32 neighbours in order
+    double e = 0;
+    int wrong = 0;
+    for (int i = 0; i < 2000; ++i) {
+        const float c = -(float)((i + 0.5) * 0.6931471805599453 / 32);
+        float x = c;
+        for (int j = 0; j < 50; ++j) x = nextafterf(x, 0.0f);
+        double before = exp64(x);
+        for (int j = 0; j < 100; ++j) {
+            x = nextafterf(x, -1e9f);
+            const double v = exp64(x);
+            wrong += v > before;
+            before = v;
+            e = fmax(e, off(v, expl((long double)x)));
+        }
+    }
+    printf("border %g %d %d", e, wrong, exp64(0.0) == 1.0 && exp64(-694.0) == 0.0 && exp64(-INFINITY) == 0.0);
+"""
+    return run(tmp_path_factory.mktemp("exp"), [("__device__ const double kPowers[32]", "// Orders equal fp64 keys")], main)
+
+
+def test_exponential_of_near_keys(exponential):
+    """exp64: a table entry and the last step round once each (2 of 2^-53 together), the argument's reduction, the series and its end
+    are below 2^-7 of that; a score adds its sum's and its quotient's rounding.  The test's own 2^-63 counts little."""
+    at = exponential.index("border")
+    for r, e, s, t in zip(*[iter(exponential[:at])] * 4):
+        assert float(e) <= 2.25, f"exp64 within {r}: {e}"
+        assert float(s) <= 4.5 and float(t) <= 4.5, f"sigmoid64 within {r}: {s}, {t}"
+    assert float(exponential[at + 1]) <= 2.25
+    assert exponential[at + 2:] == ["0", "1"]   # neighbours in order; the ends
