@@ -75,10 +75,11 @@ constexpr float kSlack = 0x1p-21f;       // over the error of a quotient or prod
 constexpr float kLeastRow = 0x1p-100f;
 
 // Rows of 16 bits need no borders.  With the largest magnitude m, r is m / 2688 rounded, and a quotient by the exact m / 2688 is
-// g * 448 / m or x * 2688 / (b m): of numbers of 11, 4 and few bits, so it is a border or away from it by 2^-16 of itself or
-// more, and the rounding of r only decides on which side of a border that it would meet a quotient lies: below where r
-// is too large.  A factor of 1 -+ 2^-20 takes it there in spite of the arithmetic's 2^-21.  0 where r is exact: those
-// rows meet borders, and are decided as 32-bit ones.
+// g * 448 / m or x * 2688 / (b m).  Against a border h that is 21 x (16 bits of an fp16 row) against h b m (3, 4 and 11 bits; scales: 7 g
+// against 5 and 11 bits), whole numbers up to a power of two: equal, or apart by 1 or more in at most 65 * 2047 of the smaller
+// unit (x = 1584, m = 2047, b = 13, h = 5), 2^-17.02 of the quotient (of a bf16 row 2^-13.9).  The rounding of r (2^-24) only decides on
+// which side of a border that it would meet a quotient lies: below where r is too large.  A factor of 1 -+ 2^-20 takes it there in
+// spite of the arithmetic's 2^-21.  0 where r is exact: those rows meet borders, and are decided as 32-bit ones.
 template <class T>
 __device__ __forceinline__ float border_side(float m, float rs) {
     if (sizeof(T) == 4) return 0.0f;

@@ -670,7 +670,9 @@ int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate
  * e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte along K, the first in the low half, with a
  * scale for each group along K ("MXFP4", "NVFP4": page "Quantization and MoE Optimizations", section MXFP4; the formats
  * of page "vllm.model_executor.layers.quantization.online.nvfp4"):
- *   MOE_FP4_MXFP4  32 to a UE8M0 scale s = 2^(byte - 127), the smallest with max|x| <= 6 s; x ~ code * s
+ *   MOE_FP4_MXFP4  32 to a UE8M0 scale s = 2^(byte - 127), the smallest with max|x| <= 6 s, so that nothing saturates (the
+ *                  conversion in the OCP microscaling text takes s = 2^(floor(log2 max|x|) - 2), half of it where max|x| is
+ *                  over 1.5 times its power of two, and saturates what is over 6 s); x ~ code * s
  *   MOE_FP4_NVFP4  16 to an e4m3 scale b = e4m3(max|x| / (6 r)), and an fp32 r for each row (rows: max|x of the
  *                  row| / 2688) or expert (weights: moe_nvfp4_quant_weight's global scale); x ~ code * b * r
  * Scales and codes are the nearest (ties to even) to the real quotients.  A group (mxfp4) or row (nvfp4) with an
@@ -711,7 +713,8 @@ int moe_fp4_pack_scales(const uint8_t* s, int fmt, int E, int N, int K, int gate
  *   MOE_EXPERT_SILU_MUL_QUANT (mxfp4; dtype bf16) the same rounded to bf16 and quantised as moe_fp4_quant does, for the
  *            second product: out the codes [num_rows, N/4], out_scales moe_fp4_row_scale_bytes(fmt, num_rows, E, N/2) bytes
  *            (else NULL), N a multiple of 64.  (A row scale of nvfp4 needs the whole row: moe_fp4_quant after SILU_MUL.)
- * w_codes [E, N, K/2]; w_global fp32 [E] and row_scale with nvfp4, else NULL.  All arrays 16-byte aligned. */
+ * w_codes [E, N, K/2]; w_global fp32 [E] and row_scale with nvfp4, else NULL; a row's scale times its expert's is one fp32
+ * factor of the row's sums, 0 or a normal number (with largest values x and w: 1e-31 < x * w < 1e45).  All arrays 16-byte aligned. */
 #define MOE_EXPERT_SILU_MUL_QUANT 2
 int moe_fp4_expert_gemm(const uint8_t* codes, const uint8_t* scales, const float* row_scale, int fmt, const uint8_t* w_codes,
                         const uint8_t* w_scales, const float* w_global, const int32_t* expert_offsets, int64_t num_rows,
