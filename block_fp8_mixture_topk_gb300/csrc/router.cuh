@@ -401,6 +401,10 @@ __device__ __forceinline__ float score32(float l, float m) {
     return __fdividef(l < 0.0f ? e : 1.0f, 1.0f + e);
 }
 
+// A group's value, of finite keys: held finite, so that it is not taken for that of a group without experts, nor two that overflow for
+// far apart (equal or near, they are compared in fp64).
+__device__ __forceinline__ float within_fp32(float v) { return fminf(fmaxf(v, -0x1.fffffep127f), 0x1.fffffep127f); }
+
 // A sum of sigmoid scores below which they vanish (e^-69): there s is e^l to fp32's last bit, and shares are formed as e^(l - m), the
 // largest logit's being 1, which no underflow reaches.
 constexpr float kVanished = 1e-30f;
@@ -473,7 +477,7 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
             const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
             join(u1, u2);
         }
-        const float mine = a.top2 && t2 > kNone ? t1 + t2 : t1;
+        const float mine = a.top2 && t2 > kNone ? within_fp32(t1 + t2) : t1;
         const bool real = own < a.groups;
         int place = 0;
         for (int g = 0; g < a.groups; ++g) {
@@ -905,7 +909,7 @@ __global__ void __launch_bounds__(router_warps(V, L) * 32, 1) router_kernel(cons
                 const float u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
                 join(u1, u2);
             }
-            const float mine = a.top2 && t2 > kNone ? t1 + t2 : t1;
+            const float mine = a.top2 && t2 > kNone ? within_fp32(t1 + t2) : t1;
             int place = 0;
             for (int g = 0; g < a.groups; ++g) {
                 const float o = __shfl_sync(kAll, mine, base + g * a.lanes);

@@ -290,3 +290,25 @@ def test_masked_experts_in_groups_keep_their_shares(T, scoring, score):
         want = (counts.double() * E / (4 * T) * (s / s.sum(1, keepdim=True)).mean(0)).sum()
         # a score and its sum: 4 half-steps each, the argument's rounding (|l| < 8), the lane's and the tokens' sums
         assert abs(float(r.balance_loss) - float(want)) <= (40 + E // 8 + T / 2432 + 80) * 2.0 ** -24 * float(want)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_whose_values_pass_fp32(scoring, sign):
+    """Sums of two keys with finite biases near fp32's largest number: the larger sum, and at equal ones the scores' sum."""
+    g = gen(9)
+    for T, E in routes(6000):
+        G, kept, size = 8, 3, E // 8
+        l = torch.randn(T, E, generator=g)
+        level = torch.tensor([3.0, 2.0, 3.0, 2.5, 3.0, 2.0, 3.0, 3.0]) * sign * 1e38
+        bias = level.repeat_interleave(size)
+        s = score64(l, scoring).reshape(T, G, size).sort(dim=2, descending=True).values[:, :, :2].sum(2)
+        # by the level, then the scores (a group's own two best keys are equal in fp64: by their logits, so by their scores)
+        rank = torch.unique(level, sorted=True, return_inverse=True)[1]
+        order = (rank.double() * 10 + s).sort(dim=1, descending=True, stable=True).indices[:, :kept]
+        keep = torch.zeros(T, G, dtype=torch.bool).scatter_(1, order, True).repeat_interleave(size, 1)
+        key = (rank.double().repeat_interleave(size) * 1000 + l.double()).masked_fill(~keep, -math.inf)
+        ids = key.sort(dim=1, descending=True, stable=True).indices[:, :4]
+        rp = moe.RoutingParams(scoring, n_group=G, topk_group=kept, bias=bias.cuda())
+        r = moe.moe_router(l.cuda(), 4, routing=rp)
+        assert torch.equal(r.ids.cpu().long(), ids), (T, E)
