@@ -251,18 +251,32 @@ __device__ __forceinline__ double sigmoid64(double x) {
 // Orders equal fp64 keys: the larger logit first, then the larger bias.
 __device__ __forceinline__ uint64_t tie_key(float l, float b) { return static_cast<uint64_t>(ordered(l)) << 32 | ordered(b); }
 
-// The places of groups of which some have equal fp64 values (t1, t2: a group's two largest keys): by the scores of the experts whose
-// keys these are, and then by what the scores leave to 1.  (Rare: bf16 logits that meet, scores that vanish or reach 1.)
+// A key t and its tie_key p among the two largest so far.
+__device__ __forceinline__ void two_best(uint64_t t, uint64_t p, uint64_t& t1, uint64_t& p1, uint64_t& t2, uint64_t& p2) {
+    const bool top = t > t1 || (t == t1 && p > p1);
+    if (top || t > t2 || (t == t2 && p > p2)) t2 = top ? t1 : t, p2 = top ? p1 : p;
+    if (top) t1 = t, p1 = p;
+}
+// Whether the last group that stays and the first that does not have the same value, *meet (by a whole warp; of the lanes that
+// are `real`, each place is one group's).
+__device__ __forceinline__ bool border_ties(uint64_t value, int place, int kept, bool real, uint64_t* meet) {
+    const uint32_t last = __ballot_sync(kAll, real && place == kept - 1);
+    const uint32_t out = __ballot_sync(kAll, real && place == kept);
+    if (last == 0u || out == 0u) return false;   // (the same in every lane)
+    *meet = __shfl_sync(kAll, static_cast<unsigned long long>(value), __ffs(static_cast<int>(last)) - 1);
+    const uint64_t next = __shfl_sync(kAll, static_cast<unsigned long long>(value), __ffs(static_cast<int>(out)) - 1);
+    return *meet == next && next != 0;
+}
+
+// The places of groups of which some at the border have the same fp64 value, meet: as they are, if it is by the same logits and
+// biases (16-bit logits often meet), else by the scores of their two best experts, and then by what these leave to 1 (scores that vanish
+// or reach 1).
 template <int V, bool SIGMOID>
 __device__ __noinline__ int tied_place(const float* l, const uint64_t* key, float m, const RouterArgs& a, int first, int lanes,
-                                       uint64_t mine) {
+                                       uint64_t mine, uint64_t meet, int place) {
     const int own = (threadIdx.x & 31) / lanes;
     uint64_t t1 = 0, t2 = 0, p1 = 0, p2 = 0;   // the two largest keys and their tie_key
-    const auto join = [&](uint64_t t, uint64_t p) {
-        const bool top = t > t1 || (t == t1 && p > p1);
-        if (top || t > t2 || (t == t2 && p > p2)) t2 = top ? t1 : t, p2 = top ? p1 : p;
-        if (top) t1 = t, p1 = p;
-    };
+    const auto join = [&](uint64_t t, uint64_t p) { two_best(t, p, t1, p1, t2, p2); };
     for (int v = 0; v < V; ++v)
         if (key[v] != 0) join(key[v], tie_key(l[v], a.bias ? a.bias[first + v] : 0.0f));
     for (int o = 1; o < lanes; o <<= 1) {
@@ -271,12 +285,17 @@ __device__ __noinline__ int tied_place(const float* l, const uint64_t* key, floa
         join(u1, q1);
         join(u2, q2);
     }
+    if (!a.top2) t2 = p2 = 0;
+    const bool equal = own < a.groups && mine == meet;
+    const int src = __ffs(static_cast<int>(__ballot_sync(kAll, equal))) - 1;
+    const uint64_t r1 = __shfl_sync(kAll, static_cast<unsigned long long>(p1), src), r2 = __shfl_sync(kAll, static_cast<unsigned long long>(p2), src);
+    if (!__any_sync(kAll, equal && (p1 != r1 || p2 != r2))) return place;
     const double x1 = of_ordered(static_cast<uint32_t>(p1 >> 32)), x2 = of_ordered(static_cast<uint32_t>(p2 >> 32));
-    const bool one = t1 != 0, two = a.top2 && t2 != 0;
+    const bool one = t1 != 0, two = t2 != 0;
     const auto score = [&](double x) { return SIGMOID ? sigmoid64(x) : exp64(x - m); };
     const uint64_t sum = ordered((one ? score(x1) : 0.0) + (two ? score(x2) : 0.0));
     const uint64_t rest = SIGMOID ? ~ordered((one ? sigmoid64(-x1) : 0.0) + (two ? sigmoid64(-x2) : 0.0)) : 0;
-    int place = 0;
+    place = 0;
     for (int g = 0; g < a.groups; ++g) {
         const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(mine), g * lanes);
         const uint64_t os = __shfl_sync(kAll, static_cast<unsigned long long>(sum), g * lanes);
@@ -325,17 +344,16 @@ __device__ __noinline__ int choose_exact(const float* l, float m, const RouterAr
         const uint64_t mine = a.top2 && t2 > 0 ? ordered(of_ordered(t1) + of_ordered(t2)) : t1;
         const int own = lane / lanes;
         int place = 0;
-        bool tied = false;
         for (int g = 0; g < a.groups; ++g) {
             const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(mine), g * lanes);
             place += o > mine || (o == mine && g < own);
-            tied |= o == mine && g != own && own < a.groups;
         }
-        if (__any_sync(kAll, tied)) {
+        uint64_t meet = 0;
+        if (border_ties(mine, place, a.kept, own < a.groups, &meet)) {
             uint64_t copy[V];   // (so that the keys stay in registers)
 #pragma unroll
             for (int v = 0; v < V; ++v) copy[v] = key[v];
-            place = tied_place<V, SIGMOID>(l, copy, m, a, first, lanes, mine);
+            place = tied_place<V, SIGMOID>(l, copy, m, a, first, lanes, mine, meet, place);
         }
         if (own >= a.groups || place >= a.kept) {
 #pragma unroll
@@ -418,6 +436,17 @@ struct Seat {
         count = own < a.groups ? min(max(G - inside, 0), V) : 0;
     }
 };
+
+// Whether one of a lane's keys that are left (kNone: taken) is near the k-th largest, last, and of another logit or bias.
+template <int V>
+__device__ __noinline__ bool left_near(const float* keys, const float* l, const float* bias, float last, float l_last, float b_last,
+                                       float slack) {
+    bool near = false;
+    for (int v = 0; v < V; ++v)
+        near |= keys[v] > kNone && last - keys[v] <= slack + kRel * fmaxf(fabsf(last), fabsf(keys[v])) &&
+                (l[v] != l_last || bias[v] != b_last);
+    return near;
+}
 
 // The choice and the weights of token t by a whole warp, for its logits l, the largest m (some expert can be chosen).  s_bias:
 // by slot; loads: null, or to be counted into; STATS: the shares are added to share, *lse is set.
@@ -522,16 +551,34 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                     }
                     const uint64_t value = a.top2 && u2 > 0 ? ordered(of_ordered(u1) + of_ordered(u2)) : u1;
                     const uint32_t borders = __ballot_sync(kAll, border);
-                    bool tied = false;   // (equal in fp64, too)
                     place = 0;
                     for (int g = 0; g < a.groups; ++g) {
                         const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(value), g * lanes);
                         const float of = __shfl_sync(kAll, mine, g * lanes);
                         const bool both = border && ((borders >> (g * lanes)) & 1u);
                         place += both ? o > value || (o == value && g < own) : of > mine || (of == mine && g < own);
-                        tied |= both && o == value && g != own;
                     }
-                    close = __any_sync(kAll, tied);
+                    close = false;
+                    uint64_t meet = 0;
+                    if (border_ties(value, place, a.kept, border, &meet)) {
+                        // equal in fp64, too: alike, if it is by the same logits and biases, else decided by those
+                        uint64_t tie = 0, t1 = 0, t2 = 0, p1 = 0, p2 = 0;
+                        if (lane < found) {
+                            const uint32_t e = s_near[lane].x;
+                            tie = tie_key(to_f32(logits[e]), a.bias ? a.bias[e] : 0.0f);
+                        }
+                        for (int i = 0; i < found; ++i) {
+                            const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(wide), i);
+                            const uint64_t ot = __shfl_sync(kAll, static_cast<unsigned long long>(tie), i);
+                            if (__shfl_sync(kAll, group, i) == static_cast<uint32_t>(own)) two_best(o, ot, t1, p1, t2, p2);
+                        }
+                        const bool equal = border && value == meet;
+                        if (!a.top2) p2 = 0;
+                        const int src = __ffs(static_cast<int>(__ballot_sync(kAll, equal))) - 1;
+                        const uint64_t q1 = __shfl_sync(kAll, static_cast<unsigned long long>(p1), src);
+                        const uint64_t q2 = __shfl_sync(kAll, static_cast<unsigned long long>(p2), src);
+                        close = __any_sync(kAll, equal && (p1 != q1 || p2 != q2));
+                    }
                 }
                 __syncwarp();
             }
@@ -595,20 +642,31 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
                     for (int v = 0; v < V; ++v) all += l[v] > kNone ? exp64(static_cast<double>(l[v]) - m) : 0.0;
                     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
                 }
-                uint64_t wide = 0, tie = 0;
+                uint64_t wide = 0;
+                float x = 0.0f, b = 0.0f;
                 if (lane < found) {
-                    const float x = to_f32(logits[mine.y]), b = a.bias[mine.y];
+                    x = to_f32(logits[mine.y]), b = a.bias[mine.y];
                     const double x64 = x;
                     const double s64 = SIGMOID ? sigmoid64(x64) : exp64(x64 - m) / all;
                     wide = ordered(s64 + static_cast<double>(b));
-                    tie = tie_key(x, b);
                 }
+                bool tied = false;   // (equal in fp64, too)
                 place = 0;
                 for (int i = 0; i < found; ++i) {
                     const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(wide), i);
-                    const uint64_t ot = __shfl_sync(kAll, static_cast<unsigned long long>(tie), i);
                     const uint32_t oe = __shfl_sync(kAll, mine.y, i);
-                    place += o != wide ? o > wide : ot != tie ? ot > tie : oe < mine.y;
+                    place += o > wide || (o == wide && oe < mine.y);
+                    tied |= o == wide && i != lane;
+                }
+                if (__any_sync(kAll, tied)) {
+                    const uint64_t tie = tie_key(x, b);
+                    place = 0;
+                    for (int i = 0; i < found; ++i) {
+                        const uint64_t o = __shfl_sync(kAll, static_cast<unsigned long long>(wide), i);
+                        const uint64_t ot = __shfl_sync(kAll, static_cast<unsigned long long>(tie), i);
+                        const uint32_t oe = __shfl_sync(kAll, mine.y, i);
+                        place += o != wide ? o > wide : ot != tie ? ot > tie : oe < mine.y;
+                    }
                 }
                 __syncwarp();
                 if (lane < found) s_near[place] = mine;
@@ -632,16 +690,15 @@ __device__ __forceinline__ void route_warp(const RouterArgs& a, const T* logits,
             for (int v = V - 1; v >= 0; --v)
                 if (key[v] == top) at = v;
             const int e = __shfl_sync(kAll, first + at, src);
-            if (a.bias && j == a.k) {   // all that are left with the k-th
-                const float x = to_f32(logits[before_id]), b = a.bias[before_id];
-                bool near = false;
+            if (a.bias && j == a.k) {
+                const float now = of_ordered(top);
+                if (before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now))) {   // (the same in every lane)
+                    float keys[V], logit[V];   // (copies, so that the registers stay those of the loop above)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const float now = of_ordered(key[v]);
-                    near |= key[v] >= kLeastKey && before - now <= slack + kRel * fmaxf(fabsf(before), fabsf(now)) &&
-                            (l[v] != x || s_bias[lane * V + v] != b);
+                    for (int v = 0; v < V; ++v) keys[v] = key[v] >= kLeastKey ? of_ordered(key[v]) : kNone, logit[v] = l[v];
+                    const bool near = left_near<V>(keys, logit, s_bias + lane * V, before, to_f32(logits[before_id]), a.bias[before_id], slack);
+                    close |= __any_sync(kAll, near);
                 }
-                close |= __any_sync(kAll, near);
                 break;
             }
             if (a.bias) {
