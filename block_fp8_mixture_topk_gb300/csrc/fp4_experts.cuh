@@ -20,11 +20,13 @@
 // CTAs need the scales of all its rows.
 //
 // Measured (GB300; the tensor cores' 4-bit rate taken as four times a measured 16-bit 1941 TFLOP/s):
-//   8192 rows of 8 experts, nvfp4, 4096 -> 2 x 14336 with SiLU 302 us, 6370 TFLOP/s, 0.82; 14336 -> 4096 150 us, 0.82.  A
-//   stage's 33 or 36 KB come into an SM at about 64 bytes a cycle, 520 or 560 cycles for 448 of its tensor pipe: the bound.
+//   8192 rows of 8 experts, nvfp4, 4096 -> 2 x 14336 with SiLU 302-312 us, 6370 TFLOP/s, 0.82 (359 under the power cap, at 1380 MHz);
+//   14336 -> 4096 150 us, 0.82, fp32 results 160.  A stage's 33 or 36 KB come into an SM at 63 bytes a cycle (counted: 70 of the cycles
+//   with work), 520 or 560 cycles for 448 of its tensor pipe: the bound.
 //   131072 rows of 128 skewed experts, mxfp4, 2048 -> 2 x 768 with requantisation 145 us, 0.73 (eight K blocks an item: the
 //   start and the end of an item show); 768 -> 2048 121 us, 5.7 TB/s: the results' stores.
-//   One token's 8 rows, 2048 -> 2 x 768 10 us, 768 -> 2048 8 us: a launch, and one stage's way after the other.
+//   131072 even rows, 768 -> 2048, nvfp4: bf16 results 179 us, fp32 245 (4.8 TB/s).
+//   One token's 8 rows, 2048 -> 2 x 768 7 us, 768 -> 2048 6 us: a launch, and one stage's way after the other.
 // Weights fetched into L2 ahead of the stages were slower (5003 rows, 2048 -> 7168: 28 -> 31 us: the copies' issue is
 // what is short); two row tiles of an item on the same weights, too (302 -> 355 us: the epilogue no longer hidden).
 #pragma once
@@ -182,6 +184,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+// (The result is rounded to 16 bits: 9.8e-6 of the values elsewhere than the exact h's, 7.1e-6 with expf and a full division, which took
+// 239 us in place of 129 at 131072 x 2048 -> 2 x 768.)
 __device__ __forceinline__ float silu_mul(float gate, float up) { return __fdividef(gate, 1.0f + __expf(-gate)) * up; }
 
 template <class T, int FMT, int MODE>

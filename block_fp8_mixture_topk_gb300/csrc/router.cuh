@@ -411,7 +411,10 @@ __device__ __forceinline__ float key_slack(float b_most, float per) {
     constexpr float kShared = 2 * (V + 22) * 0x1p-24f;
     return (SIGMOID ? 0x1p-20f : 0x1p-20f + kShared) * b_most + (SIGMOID ? 0x1p-22f : 0x1p-22f * per);
 }
-// Scores from logits (softmax: times z, m the largest logit); exp(-inf) = 0: one that cannot be chosen has score 0.
+// Scores from logits (softmax: times z, m the largest logit); exp(-inf) = 0: one that cannot be chosen has score 0.  __expf and
+// __fdividef are off by 2 ulp each and by |x| 2^-24 of the exponent, in place of expf's and the division's 1 and 1/2.  It is within the
+// slack, and what is summed of them is as near to 64 bits: shares' gradient 2.4e-7 in the 2-norm with either at 16384 x 256 sigmoid,
+// 9.2e-8 and 8.9e-8 at 65536 x 128 softmax, the choice 20.3 and 23.0, 21.5 and 22.6 us.
 template <bool SIGMOID>
 __device__ __forceinline__ float score32(float l, float m) {
     if (!SIGMOID) return __expf(l - m);
